@@ -312,6 +312,135 @@ im2win_status im2win_conv_fused_noalloc(const void *x, const void *filt, void *o
                                         int64_t H_f, int64_t W_f, int64_t s_h, int64_t s_w,
                                         int dtype, void *stream);
 
+/*
+ * The residual block around a convolution
+ * ---------------------------------------
+ * What follows a convolution in a channels-last block works on rows: x[R][C] is
+ * any channels-last tensor with its positions flattened (R = N*H*W) or a list of
+ * feature vectors. Three operators, with their gradients: a gated feed-forward
+ * over the channels, the norms before and after a block with its gate and
+ * residual scale, and the clipping of a list of gradients by their global norm.
+ * Layouts are dense and row-major; dtype, alignment, streams, workspaces and
+ * errors are as above, except where a call says otherwise. Sums, statistics and
+ * accumulators are fp32; each output is rounded once to the dtype. Every call
+ * gives the same bits each time it is made on the same inputs.
+ */
+typedef enum {
+    IM2WIN_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+    IM2WIN_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
+    IM2WIN_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+    IM2WIN_ACT_RELU = 3,      /* max(g, 0); its derivative at 0 is 0 */
+    IM2WIN_ACT_SIGMOID = 4    /* 1 / (1 + exp(-g)) */
+} im2win_act;
+
+/* Which buffer of the gated feed-forward a size is asked for. */
+typedef enum {
+    IM2WIN_FFN_FORWARD = 0,  /* workspace of im2win_gated_ffn without `saved` */
+    IM2WIN_FFN_TRAIN = 1,    /* workspace of im2win_gated_ffn with `saved` */
+    IM2WIN_FFN_BACKWARD = 2, /* workspace of im2win_gated_ffn_backward */
+    IM2WIN_FFN_SAVED = 3     /* the buffer `saved` itself */
+} im2win_ffn_buffer;
+
+/* Bytes of one of these buffers for R rows, C channels and F hidden channels,
+ * written to *bytes (a HOST pointer). Pure host arithmetic. R may be 0; C and F
+ * must be >= 1 and every product of two of them at most 2^40, and R, C and F
+ * each at most 2^31 - 1 (else IM2WIN_ERR_UNSUPPORTED). */
+im2win_status im2win_gated_ffn_size(int buffer, int64_t R, int64_t C, int64_t F, int dtype, size_t *bytes);
+
+/*
+ * Gated feed-forward block:
+ *   g = x w_gate^T, u = x w_up^T, h = act(g) * u, y = h w_down^T,
+ * x[R][C], w_gate[F][C], w_up[F][C], w_down[C][F], y[R][C]. F16/BF16 run on the
+ * tensor cores (few rows: on the CUDA cores, bound by reading the weights), with
+ * g and u in fp32 and h rounded to the dtype between the two products (an |h|
+ * beyond the dtype's range becomes infinite there); F32 runs on the CUDA cores.
+ * `saved` (NULL for inference) receives what im2win_gated_ffn_backward needs;
+ * its contents are opaque. ws begins with the 256-byte status block that
+ * im2win_device_status reads.
+ */
+im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, void *y,
+                               void *saved, void *ws, size_t ws_bytes, int64_t R, int64_t C, int64_t F, int act,
+                               int dtype, void *stream);
+
+/*
+ * Gradients of im2win_gated_ffn at the same x, weights and act, from dy[R][C] and
+ * the `saved` buffer of that forward call:
+ *   dh = dy w_down, dg = dh * u * act'(g), du = dh * act(g),
+ *   dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x, dw_down = dy^T h.
+ * dg and du are rounded to the dtype between the products. dx, or the three dw
+ * together, may be NULL and are then not computed. With R = 0 the dw are zero.
+ */
+im2win_status im2win_gated_ffn_backward(const void *dy, const void *x, const void *w_gate, const void *w_up,
+                                        const void *w_down, const void *saved, void *dx, void *dw_gate, void *dw_up,
+                                        void *dw_down, void *ws, size_t ws_bytes, int64_t R, int64_t C, int64_t F,
+                                        int act, int dtype, void *stream);
+
+typedef enum {
+    IM2WIN_NORM_NONE = 0,  /* v */
+    IM2WIN_NORM_RMS = 1,   /* v / sqrt(mean(v^2) + eps) * w */
+    IM2WIN_NORM_LAYER = 2  /* (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * w + b */
+} im2win_norm;
+
+/*
+ * The seam between two residual blocks: the norm after a block's branch y, its
+ * gate and residual scale, and the norm before the next block, in one pass:
+ *   r = res_scale * x + gate[row / rows_per_gate] * post(y),   n = pre(r),
+ * x, y, r, n are [R][C]; res_scale, w_*, b_* are [C]; gate is
+ * [ceil(R / rows_per_gate)][C] (rows_per_gate = H*W gates each image's channels,
+ * >= R gates every row alike, 1 gives each row its own). All have the call's
+ * dtype. n is computed from r before r is rounded. NULL means absent: y (then
+ * r = res_scale * x; post, gate, w_post and b_post must be absent too), gate,
+ * res_scale, w_* (1), b_* (0; only a LAYER norm may have one), r (not written).
+ * n must be given exactly when pre is not IM2WIN_NORM_NONE; a w or b of an absent norm
+ * is an error, and so is a call with neither r nor n. The outputs may be the inputs x or y
+ * themselves (r = x updates the residual in place) but must not overlap them
+ * otherwise. Needs no workspace. C is at most 2^20.
+ */
+im2win_status im2win_residual_norm(const void *x, const void *y, const void *gate, int64_t rows_per_gate,
+                                   const void *res_scale, int post, const void *w_post, const void *b_post, int pre,
+                                   const void *w_pre, const void *b_pre, double eps, void *r, void *n, int64_t R,
+                                   int64_t C, int dtype, void *stream);
+
+/* Workspace of im2win_residual_norm_backward in bytes (host arithmetic only). */
+im2win_status im2win_residual_norm_backward_size(int64_t R, int64_t C, int64_t rows_per_gate, int dtype, size_t *bytes);
+
+/*
+ * Gradients of im2win_residual_norm from dr and dn (either may be NULL: zero;
+ * dn must be NULL where pre is absent). Each of dx, dy, dgate, dres_scale,
+ * dw_post, db_post, dw_pre, db_pre may be NULL (not computed); one of an absent
+ * input is an error. Everything is recomputed from x and y; sums over rows are
+ * joined in a fixed order. With R = 0 the sums are zero. No output may overlap an
+ * input.
+ */
+im2win_status im2win_residual_norm_backward(const void *dr, const void *dn, const void *x, const void *y,
+                                            const void *gate, int64_t rows_per_gate, const void *res_scale, int post,
+                                            const void *w_post, const void *b_post, int pre, const void *w_pre,
+                                            const void *b_pre, double eps, void *dx, void *dy, void *dgate,
+                                            void *dres_scale, void *dw_post, void *db_post, void *dw_pre,
+                                            void *db_pre, void *ws, size_t ws_bytes, int64_t R, int64_t C, int dtype,
+                                            void *stream);
+
+/* Workspace of im2win_clip_grad_norm in bytes for `count` tensors of sizes[i]
+ * elements (a HOST array; host arithmetic only). */
+im2win_status im2win_clip_grad_norm_size(const int64_t *sizes, int64_t count, size_t *bytes);
+
+/*
+ * Global norm of `count` gradients and their clipping:
+ *   *norm = sqrt(sum over all elements of grads[i][j]^2),
+ *   outs[i][j] = grads[i][j] * min(1, max_norm / (*norm + eps)).
+ * grads, outs, sizes and dtypes are HOST arrays (read before the call returns)
+ * of device pointers, element counts (>= 0) and im2win_dtype codes; norm is a
+ * device float. outs[i] may be grads[i] (in place) and must not overlap any
+ * other tensor; outs = NULL computes the norm alone. Gradients need only their
+ * element's alignment (views into a flat buffer), the other pointers 16 bytes
+ * (norm: 4). A NaN among the gradients makes the norm and every output NaN, an
+ * infinity makes the factor 0, as the formula gives. Squares are summed in
+ * fp32 within at most 8192 elements and in fp64 across them.
+ */
+im2win_status im2win_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *sizes,
+                                    const int *dtypes, int64_t count, double max_norm, double eps, float *norm,
+                                    void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

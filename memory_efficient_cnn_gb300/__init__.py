@@ -18,3 +18,9 @@ from ._binding import (  # noqa: F401
     NCHW, NHWC, conv_ex, conv_fused_ex, im2win_conv_ex, im2win_conv_fused_ex, im2win_transform_ex,
     im2win_workspace_size_ex, out_hw_pd, transform_ex,
     KERNEL_EXPAND, KERNEL_F32, KERNEL_TAP, PlanInfo, im2win_plan)
+from .block import (  # noqa: F401,E402
+    ACTS, FFN_BACKWARD, FFN_FORWARD, FFN_SAVED, FFN_TRAIN, NORMS,
+    clip_grad_norm, gated_ffn, gated_ffn_backward, gated_ffn_train, grad_norm, im2win_clip_grad_norm,
+    im2win_clip_grad_norm_size, im2win_gated_ffn, im2win_gated_ffn_backward, im2win_gated_ffn_size,
+    im2win_residual_norm, im2win_residual_norm_backward, im2win_residual_norm_backward_size, residual_norm,
+    residual_norm_backward)

@@ -26,7 +26,9 @@ EXPORTS = ("im2win_workspace_size", "im2win_transform", "im2win_conv", "im2win_c
            "im2win_status_string", "im2win_device_status", "im2win_conv_fused_noalloc",
            "im2win_transform_nhwc", "im2win_conv_nhwc", "im2win_conv_fused_nhwc",
            "im2win_workspace_size_ex", "im2win_transform_ex", "im2win_conv_ex", "im2win_conv_fused_ex",
-           "im2win_plan")
+           "im2win_plan", "im2win_gated_ffn_size", "im2win_gated_ffn", "im2win_gated_ffn_backward",
+           "im2win_residual_norm", "im2win_residual_norm_backward_size", "im2win_residual_norm_backward",
+           "im2win_clip_grad_norm_size", "im2win_clip_grad_norm")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 KERNEL_F32, KERNEL_TAP, KERNEL_EXPAND = 0, 1, 2
 
@@ -82,12 +84,19 @@ def lib() -> ctypes.CDLL:
             L.im2win_conv_ex.argtypes = [vp, vp, vp, vp, sz] + shp + pd + [vp]
             L.im2win_conv_fused_ex.argtypes = [vp, vp, vp, vp, sz] + shp + pd + [vp]
             L.im2win_plan.argtypes = [ctypes.c_int] + shp + pd + [ctypes.c_int, ctypes.POINTER(PlanInfo)]
-            for f in ("im2win_workspace_size", "im2win_transform", "im2win_conv",
-                      "im2win_conv_fused", "im2win_device_status", "im2win_conv_fused_noalloc",
-                      "im2win_transform_nhwc", "im2win_conv_nhwc", "im2win_conv_fused_nhwc",
-                      "im2win_workspace_size_ex", "im2win_transform_ex", "im2win_conv_ex",
-                      "im2win_conv_fused_ex", "im2win_plan"):
-                getattr(L, f).restype = ctypes.c_int
+            ci, f64 = ctypes.c_int, ctypes.c_double
+            L.im2win_gated_ffn_size.argtypes = [ci, i64, i64, i64, ci, ctypes.POINTER(sz)]
+            L.im2win_gated_ffn.argtypes = [vp] * 7 + [sz, i64, i64, i64, ci, ci, vp]
+            L.im2win_gated_ffn_backward.argtypes = [vp] * 11 + [sz, i64, i64, i64, ci, ci, vp]
+            block = [vp, vp, vp, i64, vp, ci, vp, vp, ci, vp, vp, f64]  # x ... eps of a residual norm
+            L.im2win_residual_norm.argtypes = block + [vp, vp, i64, i64, ci, vp]
+            L.im2win_residual_norm_backward_size.argtypes = [i64, i64, i64, ci, ctypes.POINTER(sz)]
+            L.im2win_residual_norm_backward.argtypes = [vp, vp] + block + [vp] * 9 + [sz, i64, i64, ci, vp]
+            L.im2win_clip_grad_norm_size.argtypes = [vp, i64, ctypes.POINTER(sz)]
+            L.im2win_clip_grad_norm.argtypes = [vp, vp, vp, vp, i64, f64, f64, vp, vp, sz, vp]
+            for f in EXPORTS:
+                if f != "im2win_status_string":
+                    getattr(L, f).restype = ci
             _lib = L
     return _lib
 
