@@ -343,8 +343,8 @@ typedef enum {
 
 /* Bytes of one of these buffers for R rows, C channels and F hidden channels,
  * written to *bytes (a HOST pointer). Pure host arithmetic. R may be 0; C and F
- * must be >= 1 and every product of two of them at most 2^40, and R, C and F
- * each at most 2^31 - 1 (else IM2WIN_ERR_UNSUPPORTED). */
+ * must be >= 1, every product of two of them at most 2^40, and R, C and F each
+ * at most 2^31 - 1024 (else IM2WIN_ERR_UNSUPPORTED). */
 im2win_status im2win_gated_ffn_size(int buffer, int64_t R, int64_t C, int64_t F, int dtype, size_t *bytes);
 
 /*

@@ -94,7 +94,8 @@ __device__ __forceinline__ void act_both(float g, float &a, float &d) {
     }
 }
 
-// Calls f.template operator()<ACT>() through an integral constant for a run-time code.
+// Calls f with an integral constant of a run-time activation code; false for an
+// unknown one.
 template <int V>
 struct IntC {
     static constexpr int value = V;
@@ -108,6 +109,18 @@ inline bool with_act(int act, Fn f) {
         case IM2WIN_ACT_RELU: f(IntC<IM2WIN_ACT_RELU>()); return true;
         case IM2WIN_ACT_SIGMOID: f(IntC<IM2WIN_ACT_SIGMOID>()); return true;
         default: return false;
+    }
+}
+
+// The same on the device.
+template <typename Fn>
+__device__ __forceinline__ void with_act_device(int act, Fn f) {
+    switch (act) {
+        case IM2WIN_ACT_SILU: f(IntC<IM2WIN_ACT_SILU>()); break;
+        case IM2WIN_ACT_GELU: f(IntC<IM2WIN_ACT_GELU>()); break;
+        case IM2WIN_ACT_GELU_TANH: f(IntC<IM2WIN_ACT_GELU_TANH>()); break;
+        case IM2WIN_ACT_RELU: f(IntC<IM2WIN_ACT_RELU>()); break;
+        default: f(IntC<IM2WIN_ACT_SIGMOID>()); break;
     }
 }
 

@@ -1,0 +1,56 @@
+// Copies of dense 16-bit matrices whose width is no multiple of 8 to rows of a
+// whole number of 16-byte vectors, which the tensor-core products' copies need.
+#include "gated_ffn.cuh"
+#include "tc_ptx.cuh"
+
+namespace im2win {
+namespace ffn {
+namespace {
+
+struct List {
+    Repitch m[5];
+    int64_t first[6];  // first vector of each matrix, then their total
+    int count;
+};
+
+// One 16-byte output vector per thread, eight 2-byte loads (a row's start has
+// any alignment); elements past a row's end are written as zero.
+__global__ void __launch_bounds__(256) repitch(const __grid_constant__ List l) {
+    tc::allow_dependents();
+    tc::grid_dependency_wait();
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= l.first[l.count]) return;
+    int i = 0;
+    while (i + 1 < l.count && id >= l.first[i + 1]) ++i;
+    const Repitch m = l.m[i];
+    const int vecs = (m.cols + 7) / 8;
+    const int64_t row = (id - l.first[i]) / vecs;
+    const int c = (int)(id - l.first[i] - row * vecs) * 8;
+    const uint16_t *src = static_cast<const uint16_t *>(m.src) + row * m.cols + c;
+    uint32_t v[4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t x = c + e < m.cols ? src[e] : 0u;
+        v[e / 2] = e % 2 ? v[e / 2] | (x << 16) : x;
+    }
+    reinterpret_cast<uint4 *>(m.dst)[row * vecs + c / 8] = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+}  // namespace
+
+cudaError_t launch_repitch(const Repitch *list, int count, cudaStream_t st) {
+    List l;
+    l.count = count;
+    l.first[0] = 0;
+    for (int i = 0; i < count; ++i) {
+        l.m[i] = list[i];
+        l.first[i + 1] = l.first[i] + (int64_t)list[i].rows * ((list[i].cols + 7) / 8);
+    }
+    const int64_t blocks = (l.first[count] + 255) / 256;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    repitch<<<(unsigned)blocks, 256, 0, st>>>(l);
+    return cudaGetLastError();
+}
+
+}  // namespace ffn
+}  // namespace im2win

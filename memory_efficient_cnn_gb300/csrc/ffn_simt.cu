@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(THREADS) simt_product(Product p, int tiles_n) 
             const int m = m0 + tm + i, n = n0 + tn + j;
             if (m >= p.M || n >= p.N) continue;
             T *out = static_cast<T *>(p.out) + (int64_t)m * p.ldo + n;
-            const int64_t at = (int64_t)m * p.N + n;
+            const int64_t at = kept_index(m, n, p.N);
             if (EPI == EPI_STORE) {
                 *out = from_f32<T>(acc[0][i][j]);
             } else if (EPI == EPI_GATED) {

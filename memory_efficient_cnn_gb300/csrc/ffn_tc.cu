@@ -1,0 +1,668 @@
+// Products of the gated feed-forward on the tensor cores (fp16/bf16 operands,
+// fp32 accumulators in tensor memory).
+//
+// One persistent warp-specialised kernel computes D = A B^T tile by tile: one
+// thread issues TMA copies of 64 steps of K into a ring of shared-memory stages,
+// one issues tcgen05.mma on them, eight warps turn finished accumulators into
+// outputs while the next tile accumulates in the other half of tensor memory.
+// Operands may be stored with K or with the output index innermost (the backward
+// products read every matrix as it lies): both are 128-byte-swizzled layouts
+// that the copies write and the MMA reads.
+//
+// Two tile shapes: pairs of CTAs (cta_group::2) share 256 x 256 tiles, each
+// staging half of A and half of B (64 bytes of shared memory fill per clock and
+// SM at the MMA's full rate: a single CTA's 128 x 128 tile needs twice that);
+// single CTAs with 128 x 128 tiles serve outputs of few tiles. With fewer tiles
+// than SMs, or a last wave that would leave most idle, the K steps of all tiles
+// are dealt out evenly ("streamed"): a CTA takes a contiguous run of steps,
+// which may begin and end inside a tile, and writes fp32 partial tiles, which a
+// second kernel adds in the order of K.
+#include <algorithm>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "gated_ffn.cuh"
+#include "tc_ptx.cuh"
+
+namespace im2win {
+namespace ffn {
+namespace {
+
+using namespace im2win::tc;
+
+constexpr int BK = 64;           // K steps of one stage: 128 bytes
+constexpr int ROWS = 128;        // rows of A a CTA stages (its TMEM lanes)
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
+
+template <int CG, int BN>
+struct Tile {
+    static constexpr int M = ROWS * CG;
+    static constexpr int B_ROWS = BN / CG;  // rows of B a CTA stages
+    static constexpr int A_BYTES = ROWS * BK * 2, B_BYTES = B_ROWS * BK * 2;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = 6;
+    static constexpr int SMEM = STAGE * STAGES + 1024 + 256;  // + alignment + barriers
+};
+
+struct TcParams {
+    CUtensorMap a[2], b[2];
+    int M, N, KB;              // KB: blocks of 64 K steps of one segment
+    int segs;                  // 2: the K blocks of a[1], b[1] follow those of a[0], b[0]
+    int batch;                 // 2: a second product a[1], b[1] -> out2 of the same shape
+    int tiles_m, tiles_n, tiles;
+    int a_rows;                // rows of A's copies (fewer than ROWS when M is)
+    int bf16, act;
+    void *out, *out2;
+    float *g, *u;
+    int64_t ldo;
+    int vec;                   // 16-byte output stores
+    float *part;               // streamed: partial tiles
+    int64_t part_ld, part_step;  // row pitch and distance between contributions, in floats
+    int clear_status;
+    uint32_t *status;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address in the cluster's shared memory of `addr` in CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    if (CG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    if (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+            : "memory");
+    else
+        mma_f16(d, a, b, idesc, accumulate);
+}
+// One arrival on `bar` of each CTA of the tile once the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (CG == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        mma_commit(bar);
+}
+template <int CG>
+__device__ __forceinline__ void alloc_tmem(uint32_t slot, uint32_t cols) {
+    if (CG == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(slot, cols);
+        tmem_relinquish();
+    }
+}
+template <int CG>
+__device__ __forceinline__ void free_tmem(uint32_t addr, uint32_t cols) {
+    if (CG == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        tmem_dealloc(addr, cols);
+}
+
+// One run of K blocks of one tile.
+struct Work {
+    int z, tm, tn;  // batch, tile row, tile column
+    int k0, k1;     // K blocks, over all segments
+    int slot;       // streamed: the run's place among the tile's
+};
+
+// The K blocks of a streamed launch are dealt to `units` CTA groups: unit i takes
+// blocks [i * total / units, (i + 1) * total / units).
+__host__ __device__ inline int64_t stream_begin(int64_t total, int units, int i) { return total * i / units; }
+// The unit that holds block b.
+__host__ __device__ inline int stream_unit(int64_t total, int units, int64_t b) {
+    int i = (int)(b * units / total);
+    while (i + 1 < units && stream_begin(total, units, i + 1) <= b) ++i;
+    while (i > 0 && stream_begin(total, units, i) > b) --i;
+    return i;
+}
+
+// Walks a CTA group's work.
+struct Walk {
+    int KT, tiles, tiles_m, tiles_n, per_z, units, unit, streamed;
+    int64_t at, end;  // streamed: K blocks; else: tiles
+    __device__ Walk(const TcParams &p, int unit_, int units_) {
+        KT = p.KB * p.segs;
+        tiles = p.tiles, tiles_m = p.tiles_m, tiles_n = p.tiles_n, per_z = tiles_m * tiles_n;
+        units = units_, unit = unit_, streamed = p.part != nullptr;
+        at = streamed ? stream_begin((int64_t)tiles * KT, units, unit) : unit;
+        end = streamed ? stream_begin((int64_t)tiles * KT, units, unit + 1) : tiles;
+    }
+    __device__ bool next(Work &w) {
+        if (at >= end) return false;
+        int t;
+        if (streamed) {
+            t = (int)(at / KT);
+            w.k0 = (int)(at - (int64_t)t * KT);
+            w.k1 = (int)min((int64_t)KT, w.k0 + end - at);
+            w.slot = unit - stream_unit((int64_t)tiles * KT, units, (int64_t)t * KT);
+            at += w.k1 - w.k0;
+        } else {
+            t = (int)at;
+            w.k0 = 0, w.k1 = KT, w.slot = 0;
+            at += units;
+        }
+        w.z = t / per_z;
+        t -= w.z * per_z;
+        // bands of 8 tile rows, column by column, so that tiles in flight share operands in L2
+        const int band = t / (8 * tiles_n), r = t - band * 8 * tiles_n;
+        const int rows = min(8, tiles_m - band * 8);
+        w.tn = r / rows;
+        w.tm = band * 8 + r - w.tn * rows;
+        return true;
+    }
+};
+
+// 32 consecutive outputs of one row from fp32, guarded by `n` valid ones.
+__device__ __forceinline__ void store_row32(uint16_t *dst, const float (&v)[32], int n, bool vec, int bf16) {
+    if (vec && n >= 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 q;
+            q.x = pack2(v[8 * i], v[8 * i + 1], bf16);
+            q.y = pack2(v[8 * i + 2], v[8 * i + 3], bf16);
+            q.z = pack2(v[8 * i + 4], v[8 * i + 5], bf16);
+            q.w = pack2(v[8 * i + 6], v[8 * i + 7], bf16);
+            reinterpret_cast<uint4 *>(dst)[i] = q;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) dst[i] = cvt16(v[i], bf16);
+    }
+}
+
+// h = act(g) * u of 32 elements; the activation is chosen once for all of them.
+__device__ __forceinline__ void gate32(int act, const float (&g)[32], const float (&u)[32], float (&h)[32]) {
+    auto each = [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) h[i] = act_value<decltype(a)::value>(g[i]) * u[i];
+    };
+    with_act_device(act, each);
+}
+// dh and g, u -> dg, du (in g and u).
+template <int N>
+__device__ __forceinline__ void dgate_n(int act, const float (&dh)[N], float (&g)[N], float (&u)[N]) {
+    auto each = [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float v, d;
+            act_both<decltype(a)::value>(g[i], v, d);
+            g[i] = dh[i] * u[i] * d;
+            u[i] = dh[i] * v;
+        }
+    };
+    with_act_device(act, each);
+}
+
+__device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    tmem_ld32(taddr, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Accumulator columns [c, c + 32) (GATED: of the gate half) of row m, output columns from n.
+template <int BN, int EPI>
+__device__ __forceinline__ void epilogue32(const TcParams &p, uint32_t taddr, int c, int m, int n, uint16_t *out) {
+    float v[32];
+    load32(taddr + c, v);
+    const int left = m < p.M ? p.N - n : 0;
+    if (EPI == EPI_STORE) {
+        if (left > 0) store_row32(out + (int64_t)m * p.ldo + n, v, left, p.vec, p.bf16);
+    } else if (EPI == EPI_GATED) {
+        float u[32], h[32];
+        load32(taddr + BN / 2 + c, u);
+        if (left <= 0) return;
+        gate32(p.act, v, u, h);
+        store_row32(out + (int64_t)m * p.ldo + n, h, left, p.vec, p.bf16);
+        if (p.g) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (4 * i >= left) break;
+                const int64_t at = kept_index(m, n + 4 * i, p.N);
+                *reinterpret_cast<float4 *>(p.g + at) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                *reinterpret_cast<float4 *>(p.u + at) = make_float4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+            }
+        }
+    } else {
+        if (left <= 0) return;
+        float g[32], u[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t at = kept_index(m, n + 4 * i, p.N);
+            const bool in = 4 * i < left;
+            const float4 a = in ? *reinterpret_cast<const float4 *>(p.g + at) : make_float4(0, 0, 0, 0);
+            const float4 b = in ? *reinterpret_cast<const float4 *>(p.u + at) : make_float4(0, 0, 0, 0);
+            g[4 * i] = a.x, g[4 * i + 1] = a.y, g[4 * i + 2] = a.z, g[4 * i + 3] = a.w;
+            u[4 * i] = b.x, u[4 * i + 1] = b.y, u[4 * i + 2] = b.z, u[4 * i + 3] = b.w;
+        }
+        dgate_n<32>(p.act, v, g, u);
+        store_row32(out + (int64_t)m * p.ldo + n, g, left, p.vec, p.bf16);
+        store_row32(static_cast<uint16_t *>(p.out2) + (int64_t)m * p.ldo + n, u, left, p.vec, p.bf16);
+    }
+}
+
+enum Site : uint32_t { SITE_STAGE_FULL = 32, SITE_STAGE_EMPTY, SITE_ACC_FULL, SITE_ACC_EMPTY };
+
+template <int CG, int BN, bool AK, bool BKM, int EPI>
+__global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__ TcParams p) {
+    using T = Tile<CG, BN>;
+    extern __shared__ unsigned char dyn[];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+    __shared__ alignas(8) uint64_t bars[2 * T::STAGES + 4];
+    const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * T::STAGES;
+    const uint32_t acc_full = empty + 8 * T::STAGES, acc_empty = acc_full + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const int unit = blockIdx.x / CG, units = gridDim.x / CG;
+    const Ctl ctl{&abort_flag, p.status};
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < T::STAGES; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, CG * EPI_WARPS);
+        }
+        fence_mbar_init();
+    }
+    allow_dependents();
+    grid_dependency_wait();
+    // (after the wait: an earlier kernel on this SM may still have held tensor memory)
+    if (warp == 2) alloc_tmem<CG>(smem_u32(&tmem_slot), 2 * BN);
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    // (a wait of this launch gives up two seconds from now at the earliest, after this store)
+    if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
+
+    if (warp == 0 && lane == 0) {
+        // ---- copies
+        Walk walk(p, unit, units);
+        Work w;
+        int s = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        constexpr int b_box = EPI == EPI_GATED && CG == 1 ? BN / 2 : T::B_ROWS;
+        const uint32_t a_bytes = AK ? p.a_rows * BK * 2 : (p.a_rows + 63) / 64 * 64 * BK * 2;
+        const uint32_t bytes = CG * (a_bytes + T::B_BYTES);
+        while (ok && walk.next(w)) {
+            const int m0 = w.tm * T::M + (int)rank * ROWS;
+            for (int kb = w.k0; kb < w.k1; ++kb) {
+                if (!(ok = bar_wait(empty + 8 * s, phase ^ 1, ctl, SITE_STAGE_EMPTY))) break;
+                const uint32_t sa = base + s * T::STAGE, sb = sa + T::A_BYTES;
+                const uint32_t bar = CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
+                if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
+                const int seg = kb >= p.KB ? 1 : 0, k = (kb - seg * p.KB) * BK;
+                const CUtensorMap *ma = &p.a[seg | w.z], *mb = &p.b[seg | w.z];
+                if (AK) {
+                    tma_2d<CG>(sa, ma, k, m0, bar);
+                } else {
+                    for (int i = 0; i < p.a_rows; i += 64) tma_2d<CG>(sa + i * BK * 2, ma, m0 + i, k, bar);
+                }
+                if (EPI == EPI_GATED) {  // gate rows, then up rows of the same hidden channels
+                    const int n0 = w.tn * (BN / 2);
+                    if (CG == 2) {
+                        tma_2d<CG>(sb, &p.b[rank], k, n0, bar);
+                    } else {
+                        tma_2d<CG>(sb, &p.b[0], k, n0, bar);
+                        tma_2d<CG>(sb + b_box * BK * 2, &p.b[1], k, n0, bar);
+                    }
+                } else {
+                    const int n0 = w.tn * BN + (int)rank * T::B_ROWS;
+                    if (BKM) {
+                        tma_2d<CG>(sb, mb, k, n0, bar);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < T::B_ROWS; i += 64) tma_2d<CG>(sb + i * BK * 2, mb, n0 + i, k, bar);
+                    }
+                }
+                if (++s == T::STAGES) s = 0, phase ^= 1;
+            }
+        }
+        if (!ok) {  // copies in flight land within microseconds; give them two milliseconds
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---- MMAs
+        Walk walk(p, unit, units);
+        Work w;
+        int s = 0, n_tile = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t idesc = make_idesc(p.bf16 != 0, T::M, BN) | (AK ? 0u : 1u << 15) | (BKM ? 0u : 1u << 16);
+        // K-major: 8-row groups 1024 bytes apart, a K step of 16 is 32 bytes further in the
+        // swizzled row. Else: blocks of 64 output indexes BK * 128 bytes apart, groups of 8
+        // K rows 1024 bytes apart, a K step is two groups.
+        const uint64_t da = smem_desc(base, AK ? 16u : BK * 128u, 1024u) | (2ull << 61);
+        const uint64_t db = smem_desc(base + T::A_BYTES, BKM ? 16u : BK * 128u, 1024u) | (2ull << 61);
+        constexpr uint32_t step_a = (AK ? 32u : 2048u) >> 4, step_b = (BKM ? 32u : 2048u) >> 4;
+        while (ok && walk.next(w)) {
+            const int buf = n_tile & 1;
+            if (!(ok = bar_wait(acc_empty + 8 * buf, ((n_tile >> 1) & 1) ^ 1, ctl, SITE_ACC_EMPTY))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + buf * BN;
+            for (int kb = w.k0; kb < w.k1; ++kb) {
+                if (!(ok = bar_wait(full + 8 * s, phase, ctl, SITE_STAGE_FULL))) break;
+                tc_fence_after();
+                const uint64_t off = (uint64_t)(s * T::STAGE) >> 4;
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k)
+                    mma<CG>(d, da + off + k * step_a, db + off + k * step_b, idesc, kb > w.k0 || k > 0);
+                commit<CG>(empty + 8 * s);
+                if (++s == T::STAGES) s = 0, phase ^= 1;
+            }
+            if (ok) commit<CG>(acc_full + 8 * buf);
+            ++n_tile;
+        }
+        if (!ok) {
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
+        }
+    } else if (warp >= 4) {
+        // ---- outputs
+        Walk walk(p, unit, units);
+        Work w;
+        int n_tile = 0;
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;  // output columns of a tile
+        constexpr int BEGIN_STEP = BN / 2;                    // accumulator columns of half the warps
+        const uint32_t empty_bar0 = CG == 2 ? map_rank(acc_empty, 0) : acc_empty;
+        while (walk.next(w)) {
+            const int buf = n_tile & 1;
+            if (!warp_bar_wait(acc_full + 8 * buf, (n_tile >> 1) & 1, ctl, SITE_ACC_FULL)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + buf * BN + ((uint32_t)(q * 32) << 16);
+            const int row0 = w.tm * T::M + (int)rank * ROWS + q * 32, m = row0 + lane;
+            if (row0 < p.M) {
+                if (p.part) {
+                    float *dst = p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
+#pragma unroll
+                    for (int c = half * BEGIN_STEP; c < (half + 1) * BEGIN_STEP; c += 32) {
+                        float v[32];
+                        load32(taddr + c, v);
+                        if (m < p.M) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                reinterpret_cast<float4 *>(dst + c)[i] =
+                                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        }
+                    }
+                } else {
+                    uint16_t *out = static_cast<uint16_t *>(w.z ? p.out2 : p.out);
+#pragma unroll
+                    for (int c = half * (COLS / 2); c < (half + 1) * (COLS / 2); c += 32) {
+                        const int n = w.tn * COLS + c;
+                        if (n < p.N) epilogue32<BN, EPI>(p, taddr, c, m, n, out);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) arrive_cluster(empty_bar0 + 8 * buf);
+                else mbar_arrive(acc_empty + 8 * buf);
+            }
+            ++n_tile;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync();
+    tc_fence_after();
+    if (warp == 2) free_tmem<CG>(tmem, 2 * BN);
+}
+
+// Adds the partial tiles of a streamed launch and finishes the outputs: one
+// thread for four consecutive output columns.
+template <int BN, int EPI>
+__global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams p, int tile_m, int units) {
+    allow_dependents();
+    grid_dependency_wait();
+    constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;
+    const int quads = (p.N + 3) / 4;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= (int64_t)p.batch * p.M * quads) return;
+    const int n = (int)(id % quads) * 4;
+    const int64_t zm = id / quads;
+    const int z = (int)(zm / p.M), m = (int)(zm - (int64_t)z * p.M);
+    const int tm = m / tile_m, tn = n / COLS;
+    // the tile's index in the order of Walk, and the units that hold its first and last block
+    const int band = tm / 8, rows = min(8, p.tiles_m - band * 8);
+    const int t = z * p.tiles_m * p.tiles_n + band * 8 * p.tiles_n + tn * rows + (tm - band * 8);
+    const int KT = p.KB * p.segs;
+    const int64_t total = (int64_t)p.tiles * KT;
+    const int count = stream_unit(total, units, (int64_t)(t + 1) * KT - 1) - stream_unit(total, units, (int64_t)t * KT) + 1;
+    const float *src = p.part + zm * p.part_ld + (int64_t)tn * BN + (n - tn * COLS);
+    float v[4] = {}, u[4] = {};
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) {
+        const float4 a = *reinterpret_cast<const float4 *>(src + j * p.part_step);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        if (EPI == EPI_GATED) {
+            const float4 b = *reinterpret_cast<const float4 *>(src + j * p.part_step + BN / 2);
+            u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
+        }
+    }
+    const int left = min(4, p.N - n);
+    const int64_t at = (int64_t)m * p.ldo + n;
+    uint16_t *out = static_cast<uint16_t *>(z ? p.out2 : p.out) + at;
+    auto put = [&](uint16_t *dst, const float (&r)[4]) {
+        if (p.vec && left == 4) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(r[0], r[1], p.bf16), pack2(r[2], r[3], p.bf16));
+        } else {
+            for (int i = 0; i < left; ++i) dst[i] = cvt16(r[i], p.bf16);
+        }
+    };
+    if (EPI == EPI_STORE) {
+        put(out, v);
+    } else if (EPI == EPI_GATED) {
+        if (p.g) {
+            *reinterpret_cast<float4 *>(p.g + kept_index(m, n, p.N)) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(p.u + kept_index(m, n, p.N)) = make_float4(u[0], u[1], u[2], u[3]);
+        }
+        float h[4];
+        with_act_device(p.act, [&](auto a) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = act_value<decltype(a)::value>(v[i]) * u[i];
+        });
+        put(out, h);
+    } else {
+        const float4 ga = *reinterpret_cast<const float4 *>(p.g + kept_index(m, n, p.N));
+        const float4 ua = *reinterpret_cast<const float4 *>(p.u + kept_index(m, n, p.N));
+        float g[4] = {ga.x, ga.y, ga.z, ga.w}, uu[4] = {ua.x, ua.y, ua.z, ua.w};
+        dgate_n<4>(p.act, v, g, uu);
+        put(out, g);
+        put(static_cast<uint16_t *>(p.out2) + at, uu);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+// An operand of I output indexes and K steps, copied `rows` output indexes (K
+// innermost) or 64 (else) at a time.
+bool encode(CUtensorMap &map, const Operand &o, int I, int K, int rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)(o.k_major ? K : I), (cuuint64_t)(o.k_major ? I : K)};
+    const cuuint64_t strides[1] = {(cuuint64_t)o.ld * 2};
+    const cuuint32_t box[2] = {64u, o.k_major ? (cuuint32_t)rows : (cuuint32_t)BK};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(o.p), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename K, typename... A>
+cudaError_t launch_with(K kernel, int grid, int block, size_t smem, int cluster, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int CG, int BN, bool AK, bool BKM, int EPI>
+cudaError_t launch_shape(const TcParams &p, const TcPlan &pl, cudaStream_t st) {
+    using T = Tile<CG, BN>;
+    auto kernel = tc_product<CG, BN, AK, BKM, EPI>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    if (e != cudaSuccess) return e;
+    e = launch_with(kernel, pl.units * CG, THREADS, T::SMEM, CG, st, p);
+    if (e != cudaSuccess || !p.part) return e;
+    const int64_t quads = (int64_t)p.batch * p.M * ((p.N + 3) / 4);
+    return launch_with(tc_join<BN, EPI>, (int)((quads + 255) / 256), 256, 0, 1, st, p, T::M, pl.units);
+}
+
+template <int CG, int BN>
+cudaError_t launch_tile(const TcParams &p, const TcPlan &pl, const Product &d, cudaStream_t st) {
+    if (d.epi == EPI_GATED) return launch_shape<CG, BN, true, true, EPI_GATED>(p, pl, st);
+    if (d.epi == EPI_DGATED) return launch_shape<CG, BN, true, false, EPI_DGATED>(p, pl, st);
+    if (!d.a0.k_major) return launch_shape<CG, BN, false, false, EPI_STORE>(p, pl, st);
+    if (d.b0.k_major) return launch_shape<CG, BN, true, true, EPI_STORE>(p, pl, st);
+    return launch_shape<CG, BN, true, false, EPI_STORE>(p, pl, st);
+}
+
+}  // namespace
+
+// SMs the work is cut for. A constant, so that sizes and results depend on the
+// shape alone.
+constexpr int SMS = 152;
+
+TcPlan plan_tc(const Product &d) {
+    const int KT = (d.K + BK - 1) / BK * (d.epi != EPI_GATED && d.a1.p && !d.batch ? 2 : 1);
+    const int z = d.batch ? 2 : 1;
+    TcPlan best;
+    double best_cost = 0;
+    for (int v = 0; v < 4; ++v) {
+        TcPlan pl;
+        pl.cg = v < 2 ? 2 : 1;
+        pl.bn = pl.cg == 2 ? 256 : 128;
+        pl.streamed = (v & 1) != 0;
+        const int tm = ROWS * pl.cg, cols = d.epi == EPI_GATED ? pl.bn / 2 : pl.bn;
+        pl.tiles_m = (d.M + tm - 1) / tm;
+        pl.tiles_n = (d.N + cols - 1) / cols;
+        const int64_t tiles = (int64_t)z * pl.tiles_m * pl.tiles_n, total = tiles * KT;
+        if (tiles > 0x3fffffff || total > 0x3fffffffll) continue;  // (streamed indexes stay in 32 bits)
+        const int most = SMS / pl.cg;
+        // clocks: a K block takes 512 in either shape (the pair's MMAs; the single CTA's
+        // shared-memory fill), a tile's start and end about 1500, a second launch 4000, and
+        // partial sums are written and read at about 3000 bytes a clock
+        double cost;
+        if (!pl.streamed) {
+            pl.units = (int)std::min<int64_t>(most, tiles);
+            cost = (double)((tiles + pl.units - 1) / pl.units) * KT * 512 + 1500;
+        } else {
+            pl.units = (int)std::min<int64_t>(most, std::max<int64_t>(1, total / 4));  // 4 blocks at least
+            if (tiles > 8 * pl.units || tiles % pl.units == 0) continue;  // (nearly) even without it
+            int64_t slots = 1;
+            for (int64_t t = 0; t < tiles; ++t)
+                slots = std::max<int64_t>(slots, stream_unit(total, pl.units, (t + 1) * KT - 1) -
+                                                     stream_unit(total, pl.units, t * KT) + 1);
+            pl.slots = (int)slots;
+            pl.part_ld = (int64_t)pl.tiles_n * pl.bn;
+            pl.part_step = (int64_t)z * d.M * pl.part_ld;
+            pl.part_bytes = (size_t)(slots * pl.part_step) * 4;
+            const double moved = (double)(tiles + pl.units) * std::min(tm, d.M) * pl.bn * 8;
+            cost = (double)((total + pl.units - 1) / pl.units) * 512 + 3000 + 4000 + moved / 3000;
+        }
+        if (best.units == 0 || cost < best_cost) best = pl, best_cost = cost;
+    }
+    return best;
+}
+
+cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool clear_status, void *part, cudaStream_t st) {
+    const TcPlan pl = plan_tc(d);
+    if (pl.units == 0) return cudaErrorInvalidValue;
+    TcParams p = {};
+    p.M = d.M; p.N = d.N; p.KB = (d.K + BK - 1) / BK;
+    const bool two = d.a1.p != nullptr;
+    p.segs = d.epi != EPI_GATED && two && !d.batch ? 2 : 1;
+    p.batch = d.batch ? 2 : 1;
+    p.tiles_m = pl.tiles_m; p.tiles_n = pl.tiles_n; p.tiles = p.batch * pl.tiles_m * pl.tiles_n;
+    p.a_rows = std::min(ROWS, (d.M + 7) / 8 * 8);
+    const int b_box = d.epi == EPI_GATED && pl.cg == 1 ? pl.bn / 2 : pl.bn / pl.cg;
+    if (!encode(p.a[0], d.a0, d.M, d.K, p.a_rows) || !encode(p.b[0], d.b0, d.N, d.K, b_box)) return cudaErrorInvalidValue;
+    if (two && !encode(p.a[1], d.a1, d.M, d.K, p.a_rows)) return cudaErrorInvalidValue;
+    if (d.b1.p && !encode(p.b[1], d.b1, d.N, d.K, b_box)) return cudaErrorInvalidValue;
+    p.bf16 = bf16; p.act = d.act;
+    p.out = d.out; p.out2 = d.out2; p.g = d.g; p.u = d.u; p.ldo = d.ldo;
+    p.vec = d.ldo % 8 == 0;
+    if (pl.streamed) {
+        p.part = static_cast<float *>(part);
+        p.part_ld = pl.part_ld;
+        p.part_step = pl.part_step;
+    }
+    p.status = status;
+    p.clear_status = clear_status;
+    return pl.cg == 2 ? launch_tile<2, 256>(p, pl, d, st) : launch_tile<1, 128>(p, pl, d, st);
+}
+
+}  // namespace ffn
+}  // namespace im2win

@@ -1,4 +1,7 @@
 // Gated feed-forward block: argument checks, buffers and the sequence of products.
+#include <algorithm>
+#include <initializer_list>
+
 #include "gated_ffn.cuh"
 
 using namespace im2win;
@@ -8,7 +11,7 @@ namespace {
 
 im2win_status check_dims(int64_t R, int64_t C, int64_t F, int dtype) {
     if (R < 0 || C < 1 || F < 1 || elem_size(dtype) == 0) return IM2WIN_ERR_INVALID_ARG;
-    const int64_t most = 0x7fffffff, area = int64_t(1) << 40;
+    const int64_t most = 0x7fffffff - 1023, area = int64_t(1) << 40;
     if (R > most || C > most || F > most || R * C > area || R * F > area || C * F > area) return IM2WIN_ERR_UNSUPPORTED;
     return IM2WIN_OK;
 }
@@ -24,44 +27,176 @@ struct Parts {
     }
 };
 
-// saved: h, then g and u in fp32.
+// A call's problem. 16-bit types run on the tensor cores, whose copies need row
+// pitches that are multiples of 16 bytes: own buffers have such a pitch, and
+// matrices of the caller whose width is no multiple of 8 are first copied to one.
+struct Problem {
+    int R, C, F, dtype, esz, act;
+    bool tc;
+    int64_t Cp, Fp;  // pitches of rows of C and F elements
+    Problem(int64_t R_, int64_t C_, int64_t F_, int act_, int dtype_)
+        : R((int)R_), C((int)C_), F((int)F_), dtype(dtype_), esz(elem_size(dtype_)), act(act_),
+          tc(dtype_ != IM2WIN_F32), Cp(tc ? (C_ + 7) / 8 * 8 : C_), Fp(tc ? (F_ + 7) / 8 * 8 : F_) {}
+
+    size_t rows_c(int64_t rows) const { return (size_t)(rows * Cp) * esz; }
+    size_t rows_f(int64_t rows) const { return (size_t)(rows * Fp) * esz; }
+
+    Product gated(const void *x, const void *wg, const void *wu, void *h, float *g, float *u) const {
+        Product p;
+        p.M = R; p.N = F; p.K = C;
+        p.a0 = {x, Cp, true}; p.b0 = {wg, Cp, true}; p.b1 = {wu, Cp, true};
+        p.epi = EPI_GATED; p.act = act;
+        p.out = h; p.ldo = Fp; p.g = g; p.u = u;
+        return p;
+    }
+    Product down(const void *h, const void *wd, void *y) const {
+        Product p;
+        p.M = R; p.N = C; p.K = F;
+        p.a0 = {h, Fp, true}; p.b0 = {wd, Fp, true};
+        p.out = y; p.ldo = C;
+        return p;
+    }
+    Product dgated(const void *dy, const void *wd, const float *g, const float *u, void *dg, void *du) const {
+        Product p;
+        p.M = R; p.N = F; p.K = C;
+        p.a0 = {dy, Cp, true}; p.b0 = {wd, Fp, false};
+        p.epi = EPI_DGATED; p.act = act;
+        p.out = dg; p.out2 = du; p.ldo = Fp;
+        p.g = const_cast<float *>(g); p.u = const_cast<float *>(u);
+        return p;
+    }
+    Product dx(const void *dg, const void *du, const void *wg, const void *wu, void *out) const {
+        Product p;
+        p.M = R; p.N = C; p.K = F;
+        p.a0 = {dg, Fp, true}; p.b0 = {wg, Cp, false};
+        p.a1 = {du, Fp, true}; p.b1 = {wu, Cp, false};
+        p.out = out; p.ldo = C;
+        return p;
+    }
+    Product dw_in(const void *dg, const void *du, const void *x, void *dwg, void *dwu) const {
+        Product p;
+        p.M = F; p.N = C; p.K = R;
+        p.a0 = {dg, Fp, false}; p.a1 = {du, Fp, false};
+        p.b0 = p.b1 = {x, Cp, false};
+        p.batch = true;
+        p.out = dwg; p.out2 = dwu; p.ldo = C;
+        return p;
+    }
+    Product dw_down(const void *dy, const void *h, void *out) const {
+        Product p;
+        p.M = C; p.N = F; p.K = R;
+        p.a0 = {dy, Cp, false}; p.b0 = {h, Fp, false};
+        p.out = out; p.ldo = F;
+        return p;
+    }
+};
+
+// saved: h, then g and u in fp32 (kept_index). They stay in fp32 because dg and
+// du, made of them, are rounded once more on their own.
 struct SavedParts {
     size_t h, g, u, bytes;
-    SavedParts(int64_t R, int64_t F, int esz) {
+    explicit SavedParts(const Problem &q) {
         Parts p(0);
-        h = p.add((size_t)(R * F) * esz);
-        g = p.add((size_t)(R * F) * 4);
-        u = p.add((size_t)(R * F) * 4);
+        h = p.add(q.rows_f(q.R));
+        g = p.add(kept_elems(q.R, q.F) * 4);
+        u = p.add(kept_elems(q.R, q.F) * 4);
         bytes = p.end;
     }
 };
 
+const void *const kSome = reinterpret_cast<const void *>(16);  // a present operand, where only sizes matter
+void *const kSomeOut = reinterpret_cast<void *>(16);
+
 struct ForwardParts {
-    size_t h, bytes;
-    ForwardParts(int64_t R, int64_t F, int esz, bool saved) {
+    size_t h, x, wg, wu, wd, part, bytes;
+    ForwardParts(const Problem &q, bool saved) {
         Parts p(kStatusBytes);
-        h = p.end;
-        if (!saved) p.add((size_t)(R * F) * esz);
+        h = p.add(saved ? 0 : q.rows_f(q.R));
+        const bool pad_c = q.Cp != q.C, pad_f = q.Fp != q.F;
+        x = p.add(pad_c ? q.rows_c(q.R) : 0);
+        wg = p.add(pad_c ? q.rows_c(q.F) : 0);
+        wu = p.add(pad_c ? q.rows_c(q.F) : 0);
+        wd = p.add(pad_f ? q.rows_f(q.C) : 0);
+        part = p.end;
+        if (q.tc && q.R > 0)
+            p.add(std::max(plan_tc(q.gated(kSome, kSome, kSome, kSomeOut, nullptr, nullptr)).part_bytes,
+                           plan_tc(q.down(kSome, kSome, kSomeOut)).part_bytes));
         bytes = p.end;
     }
 };
 
 struct BackwardParts {
-    size_t dg, du, bytes;
-    BackwardParts(int64_t R, int64_t F, int esz) {
+    size_t dg, du, x, dy, wg, wu, wd, part, bytes;
+    explicit BackwardParts(const Problem &q) {
         Parts p(kStatusBytes);
-        dg = p.add((size_t)(R * F) * esz);
-        du = p.add((size_t)(R * F) * esz);
+        dg = p.add(q.rows_f(q.R));
+        du = p.add(q.rows_f(q.R));
+        const bool pad_c = q.Cp != q.C, pad_f = q.Fp != q.F;
+        x = p.add(pad_c ? q.rows_c(q.R) : 0);
+        dy = p.add(pad_c ? q.rows_c(q.R) : 0);
+        wg = p.add(pad_c ? q.rows_c(q.F) : 0);
+        wu = p.add(pad_c ? q.rows_c(q.F) : 0);
+        wd = p.add(pad_f ? q.rows_f(q.C) : 0);
+        part = p.end;
+        if (q.tc && q.R > 0) {
+            size_t most = 0;
+            for (const Product &d : {q.dgated(kSome, kSome, nullptr, nullptr, kSomeOut, kSomeOut),
+                                     q.dx(kSome, kSome, kSome, kSome, kSomeOut),
+                                     q.dw_in(kSome, kSome, kSome, kSomeOut, kSomeOut), q.dw_down(kSome, kSome, kSomeOut)})
+                most = std::max(most, plan_tc(d).part_bytes);
+            p.add(most);
+        }
         bytes = p.end;
     }
 };
 
 unsigned char *at(void *base, size_t off) { return static_cast<unsigned char *>(base) + off; }
 const unsigned char *at(const void *base, size_t off) { return static_cast<const unsigned char *>(base) + off; }
+float *floats(void *base, size_t off) { return reinterpret_cast<float *>(at(base, off)); }
+const float *floats(const void *base, size_t off) { return reinterpret_cast<const float *>(at(base, off)); }
 
 bool known_act(int act) {
     return with_act(act, [](auto) {});
 }
+
+// The launches of one call, up to the first that fails.
+struct Sequence {
+    const Problem &q;
+    void *ws;
+    void *part;
+    cudaStream_t st;
+    cudaError_t e = cudaSuccess;
+    bool cleared = false;
+    Repitch copies[5];
+    int n_copies = 0;
+
+    // The matrix itself, or its copy at `to` with a pitch of whole vectors.
+    const void *pitched(const void *src, int rows, int cols, size_t to) {
+        if (!q.tc || cols % 8 == 0) return src;
+        copies[n_copies++] = {src, at(ws, to), rows, cols};
+        return at(ws, to);
+    }
+    void copy_pitched() {
+        if (n_copies && e == cudaSuccess) e = launch_repitch(copies, n_copies, st);
+    }
+    void run(const Product &p) {
+        if (e != cudaSuccess) return;
+        if (q.tc) {
+            e = launch_tc(p, q.dtype == IM2WIN_BF16, static_cast<uint32_t *>(ws), !cleared, part, st);
+        } else {
+            if (!cleared) e = cudaMemsetAsync(ws, 0, kStatusBytes, st);
+            Product one = p;
+            one.batch = false;
+            if (p.batch) one.a1 = one.b1 = Operand();
+            if (e == cudaSuccess) e = launch_simt(one, q.dtype, st);
+            if (p.batch && e == cudaSuccess) {
+                one.a0 = p.a1, one.b0 = p.b1, one.out = p.out2;
+                e = launch_simt(one, q.dtype, st);
+            }
+        }
+        cleared = true;
+    }
+};
 
 }  // namespace
 
@@ -71,12 +206,12 @@ im2win_status im2win_gated_ffn_size(int buffer, int64_t R, int64_t C, int64_t F,
     if (!bytes) return IM2WIN_ERR_INVALID_ARG;
     const im2win_status s = check_dims(R, C, F, dtype);
     if (s != IM2WIN_OK) return s;
-    const int esz = elem_size(dtype);
+    const Problem q(R, C, F, 0, dtype);
     switch (buffer) {
-        case IM2WIN_FFN_FORWARD: *bytes = ForwardParts(R, F, esz, false).bytes; return IM2WIN_OK;
-        case IM2WIN_FFN_TRAIN: *bytes = ForwardParts(R, F, esz, true).bytes; return IM2WIN_OK;
-        case IM2WIN_FFN_BACKWARD: *bytes = BackwardParts(R, F, esz).bytes; return IM2WIN_OK;
-        case IM2WIN_FFN_SAVED: *bytes = SavedParts(R, F, esz).bytes; return IM2WIN_OK;
+        case IM2WIN_FFN_FORWARD: *bytes = ForwardParts(q, false).bytes; return IM2WIN_OK;
+        case IM2WIN_FFN_TRAIN: *bytes = ForwardParts(q, true).bytes; return IM2WIN_OK;
+        case IM2WIN_FFN_BACKWARD: *bytes = BackwardParts(q).bytes; return IM2WIN_OK;
+        case IM2WIN_FFN_SAVED: *bytes = SavedParts(q).bytes; return IM2WIN_OK;
         default: return IM2WIN_ERR_INVALID_ARG;
     }
 }
@@ -91,33 +226,20 @@ im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_
     if (!x || !w_gate || !w_up || !w_down || !y) return IM2WIN_ERR_INVALID_ARG;
     for (const void *p : {x, w_gate, w_up, w_down, (const void *)y, (const void *)saved, (const void *)ws})
         if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
-    const int esz = elem_size(dtype);
-    const ForwardParts parts(R, F, esz, saved != nullptr);
+    const Problem q(R, C, F, act, dtype);
+    const ForwardParts parts(q, saved != nullptr);
     if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const SavedParts kept(R, F, esz);
+    const SavedParts kept(q);
     void *h = saved ? at(saved, kept.h) : at(ws, parts.h);
-
-    cudaError_t e = cudaMemsetAsync(ws, 0, kStatusBytes, st);
-    Product p1;
-    p1.M = (int)R; p1.N = (int)F; p1.K = (int)C;
-    p1.a0 = {x, C, true};
-    p1.b0 = {w_gate, C, true};
-    p1.b1 = {w_up, C, true};
-    p1.epi = EPI_GATED; p1.act = act;
-    p1.out = h; p1.ldo = F;
-    if (saved) {
-        p1.g = reinterpret_cast<float *>(at(saved, kept.g));
-        p1.u = reinterpret_cast<float *>(at(saved, kept.u));
-    }
-    if (e == cudaSuccess) e = launch_simt(p1, dtype, st);
-    Product p2;
-    p2.M = (int)R; p2.N = (int)C; p2.K = (int)F;
-    p2.a0 = {h, F, true};
-    p2.b0 = {w_down, F, true};
-    p2.out = y; p2.ldo = C;
-    if (e == cudaSuccess) e = launch_simt(p2, dtype, st);
-    return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+    Sequence seq{q, ws, at(ws, parts.part), static_cast<cudaStream_t>(stream)};
+    x = seq.pitched(x, q.R, q.C, parts.x);
+    w_gate = seq.pitched(w_gate, q.F, q.C, parts.wg);
+    w_up = seq.pitched(w_up, q.F, q.C, parts.wu);
+    w_down = seq.pitched(w_down, q.C, q.F, parts.wd);
+    seq.copy_pitched();
+    seq.run(q.gated(x, w_gate, w_up, h, saved ? floats(saved, kept.g) : nullptr, saved ? floats(saved, kept.u) : nullptr));
+    seq.run(q.down(h, w_down, y));
+    return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
 }
 
 im2win_status im2win_gated_ffn_backward(const void *dy, const void *x, const void *w_gate, const void *w_up,
@@ -133,57 +255,35 @@ im2win_status im2win_gated_ffn_backward(const void *dy, const void *x, const voi
     for (const void *p : {dy, x, w_gate, w_up, w_down, saved, (const void *)dx, (const void *)dw_gate,
                           (const void *)dw_up, (const void *)dw_down, (const void *)ws})
         if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
-    const int esz = elem_size(dtype);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
     if (R == 0) {  // sums over no rows
+        cudaError_t e = cudaSuccess;
         for (void *w : {dw_gate, dw_up, dw_down})
-            if (w && e == cudaSuccess) e = cudaMemsetAsync(w, 0, (size_t)(C * F) * esz, st);
+            if (w && e == cudaSuccess) e = cudaMemsetAsync(w, 0, (size_t)(C * F) * elem_size(dtype), st);
         return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
     }
     if (!dx && !want_dw) return IM2WIN_OK;
-    const BackwardParts parts(R, F, esz);
+    const Problem q(R, C, F, act, dtype);
+    const BackwardParts parts(q);
     if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
-    const SavedParts kept(R, F, esz);
+    const SavedParts kept(q);
     void *dg = at(ws, parts.dg), *du = at(ws, parts.du);
-
-    e = cudaMemsetAsync(ws, 0, kStatusBytes, st);
-    Product p;
-    p.M = (int)R; p.N = (int)F; p.K = (int)C;
-    p.a0 = {dy, C, true};
-    p.b0 = {w_down, F, false};
-    p.epi = EPI_DGATED; p.act = act;
-    p.out = dg; p.out2 = du; p.ldo = F;
-    p.g = reinterpret_cast<float *>(const_cast<unsigned char *>(at(saved, kept.g)));
-    p.u = reinterpret_cast<float *>(const_cast<unsigned char *>(at(saved, kept.u)));
-    if (e == cudaSuccess) e = launch_simt(p, dtype, st);
-    if (dx && e == cudaSuccess) {
-        Product q;
-        q.M = (int)R; q.N = (int)C; q.K = (int)F;
-        q.a0 = {dg, F, true};
-        q.b0 = {w_gate, C, false};
-        q.a1 = {du, F, true};
-        q.b1 = {w_up, C, false};
-        q.out = dx; q.ldo = C;
-        e = launch_simt(q, dtype, st);
+    Sequence seq{q, ws, at(ws, parts.part), st};
+    dy = seq.pitched(dy, q.R, q.C, parts.dy);
+    w_down = seq.pitched(w_down, q.C, q.F, parts.wd);
+    if (dx) {
+        w_gate = seq.pitched(w_gate, q.F, q.C, parts.wg);
+        w_up = seq.pitched(w_up, q.F, q.C, parts.wu);
     }
+    if (want_dw) x = seq.pitched(x, q.R, q.C, parts.x);
+    seq.copy_pitched();
+    seq.run(q.dgated(dy, w_down, floats(saved, kept.g), floats(saved, kept.u), dg, du));
+    if (dx) seq.run(q.dx(dg, du, w_gate, w_up, dx));
     if (want_dw) {
-        Product q;
-        q.M = (int)F; q.N = (int)C; q.K = (int)R;
-        q.b0 = {x, C, false};
-        q.ldo = C;
-        for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
-            q.a0 = {i ? du : dg, F, false};
-            q.out = i ? dw_up : dw_gate;
-            e = launch_simt(q, dtype, st);
-        }
-        q.M = (int)C; q.N = (int)F;
-        q.a0 = {dy, C, false};
-        q.b0 = {at(saved, kept.h), F, false};
-        q.out = dw_down; q.ldo = F;
-        if (e == cudaSuccess) e = launch_simt(q, dtype, st);
+        seq.run(q.dw_in(dg, du, x, dw_gate, dw_up));
+        seq.run(q.dw_down(dy, at(saved, kept.h), dw_down));
     }
-    return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+    return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
 }
 
 }  // extern "C"

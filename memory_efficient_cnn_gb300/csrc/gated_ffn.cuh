@@ -33,18 +33,49 @@ enum Epilogue {
     EPI_DGATED = 2  // d = dh: out = dg, out2 = du, from the kept g, u
 };
 
-// D[M][N] = A0 B0^T (+ A1 B1^T); EPI_GATED: g = A0 B0^T, u = A0 B1^T.
+// The kept g and u lie in blocks of 32 rows by 4 columns, rows outermost in a
+// block: a warp whose lanes hold one row each moves 512 contiguous bytes.
+__host__ __device__ inline int64_t kept_index(int m, int n, int N) {
+    return ((int64_t)(m / 32) * ((N + 3) / 4) + n / 4) * 128 + (m % 32) * 4 + n % 4;
+}
+inline size_t kept_elems(int64_t M, int64_t N) { return (size_t)((M + 31) / 32 * 32) * (size_t)((N + 3) / 4 * 4); }
+
+// D[M][N] = A0 B0^T (+ A1 B1^T); EPI_GATED: g = A0 B0^T, u = A0 B1^T; batch: out =
+// A0 B0^T and out2 = A1 B1^T.
 struct Product {
     int M = 0, N = 0, K = 0;
     Operand a0, b0, a1, b1;
     int epi = EPI_STORE;
     int act = 0;
+    bool batch = false;
     void *out = nullptr, *out2 = nullptr;
-    float *g = nullptr, *u = nullptr;  // [M][N]: written (EPI_GATED, may be null) or read (EPI_DGATED)
+    float *g = nullptr, *u = nullptr;  // kept_index(): written (EPI_GATED, may be null) or read (EPI_DGATED)
     int64_t ldo = 0;                   // row pitch of out and out2 in elements
 };
 
+// CUDA cores: any type, shape and alignment (no batch).
 cudaError_t launch_simt(const Product &p, int dtype, cudaStream_t st);
+
+// Tensor cores: fp16/bf16; operands 16-byte aligned with pitches that are multiples
+// of 8 elements. A product takes part_bytes of scratch. status: the workspace's
+// status block, cleared first where asked.
+struct TcPlan {
+    int cg = 0, bn = 0;       // CTAs and columns of a tile
+    bool streamed = false;    // K blocks dealt out evenly, partial tiles joined
+    int tiles_m = 0, tiles_n = 0, units = 0, slots = 0;
+    int64_t part_ld = 0, part_step = 0;
+    size_t part_bytes = 0;
+};
+TcPlan plan_tc(const Product &p);
+cudaError_t launch_tc(const Product &p, bool bf16, uint32_t *status, bool clear_status, void *part, cudaStream_t st);
+
+// Copies of dense matrices to a pitch that is a multiple of 8 elements (16-bit types).
+struct Repitch {
+    const void *src;
+    void *dst;
+    int rows, cols;
+};
+cudaError_t launch_repitch(const Repitch *list, int count, cudaStream_t st);  // count <= 5
 
 }  // namespace ffn
 }  // namespace im2win
