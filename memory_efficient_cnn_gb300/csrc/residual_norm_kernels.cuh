@@ -1,0 +1,705 @@
+// The norms around a residual block with its gate and residual scale:
+//   r = res_scale * x + gate * post(y),  n = pre(r),  and the gradients.
+//
+// With m, i the mean (0 for RMS) and inverse deviation of a row v, its normed
+// row is hat = (v - m) i and post(v) = hat * w + b; for a gradient d of post(v),
+//   e = d * w,  dv = i (e - [mean(e)] - hat * mean(e * hat)),
+// the bracket for LAYER only. dt = dr + pre'(dn) is the gradient of r.
+#pragma once
+
+#include "residual_norm.cuh"
+
+namespace im2win {
+namespace rnorm {
+
+namespace {
+
+constexpr int ROW_THREADS = 256;
+
+// Sum over the block, the same for every thread and in a fixed order.
+__device__ __forceinline__ float block_sum(float v, float *s) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ROW_THREADS / 32; ++i) t += s[i];
+    __syncthreads();
+    return t;
+}
+
+template <typename T>
+__device__ __forceinline__ float load_or(const void *p, int64_t i, float absent) {
+    return p ? to_f32(static_cast<const T *>(p)[i]) : absent;
+}
+
+// Mean and inverse deviation of f(c), c < C, for a norm kind.
+template <typename Fn>
+__device__ __forceinline__ void row_moments(int kind, int64_t C, float eps, float *s, Fn f, float &m, float &i) {
+    m = 0.0f, i = 1.0f;
+    if (kind == IM2WIN_NORM_NONE) return;
+    float a = 0.0f;
+    if (kind == IM2WIN_NORM_LAYER) {
+        for (int64_t c = threadIdx.x; c < C; c += ROW_THREADS) a += f(c);
+        m = block_sum(a, s) / (float)C;
+        a = 0.0f;
+    }
+    for (int64_t c = threadIdx.x; c < C; c += ROW_THREADS) {
+        const float d = f(c) - m;
+        a = fmaf(d, d, a);
+    }
+    i = 1.0f / sqrtf(block_sum(a, s) / (float)C + eps);
+}
+
+// One row of r in fp32, element by element.
+template <typename T>
+struct RowOf {
+    const NormArgs &p;
+    int64_t row, gate_row;
+    float my, iy;
+    __device__ RowOf(const NormArgs &p_, int64_t row_) : p(p_), row(row_), gate_row(row_ / p_.per_gate), my(0), iy(1) {}
+    __device__ float x(int64_t c) const { return to_f32(static_cast<const T *>(p.x)[row * p.C + c]); }
+    __device__ float y(int64_t c) const { return to_f32(static_cast<const T *>(p.y)[row * p.C + c]); }
+    __device__ float yhat(int64_t c) const { return (y(c) - my) * iy; }
+    __device__ float post(int64_t c) const {
+        return fmaf(yhat(c), load_or<T>(p.w_post, c, 1.0f), load_or<T>(p.b_post, c, 0.0f));
+    }
+    __device__ float gate(int64_t c) const { return load_or<T>(p.gate, gate_row * p.C + c, 1.0f); }
+    __device__ float r(int64_t c) const {
+        const float kept = x(c) * load_or<T>(p.res_scale, c, 1.0f);
+        return p.y ? fmaf(gate(c), post(c), kept) : kept;
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(ROW_THREADS) norm_forward(NormArgs p) {
+    __shared__ float s[ROW_THREADS / 32];
+    RowOf<T> row(p, blockIdx.x);
+    if (p.y) row_moments(p.post, p.C, p.eps, s, [&](int64_t c) { return row.y(c); }, row.my, row.iy);
+    float mr, ir;
+    row_moments(p.pre, p.C, p.eps, s, [&](int64_t c) { return row.r(c); }, mr, ir);
+    for (int64_t c = threadIdx.x; c < p.C; c += ROW_THREADS) {
+        const float r = row.r(c);
+        if (p.r) static_cast<T *>(p.r)[row.row * p.C + c] = from_f32<T>(r);
+        if (p.n)
+            static_cast<T *>(p.n)[row.row * p.C + c] =
+                from_f32<T>(fmaf((r - mr) * ir, load_or<T>(p.w_pre, c, 1.0f), load_or<T>(p.b_pre, c, 0.0f)));
+    }
+}
+
+// dt of one element of a row whose statistics are known.
+template <typename T>
+__device__ __forceinline__ float total_grad(const NormArgs &p, const RowOf<T> &row, const RowStats &st, int64_t c) {
+    float dt = load_or<T>(p.dr, p.dr ? row.row * p.C + c : 0, 0.0f);
+    if (p.dn) {
+        const float e = to_f32(static_cast<const T *>(p.dn)[row.row * p.C + c]) * load_or<T>(p.w_pre, c, 1.0f);
+        dt += st.ir * (e - st.e1 - (row.r(c) - st.mr) * st.ir * st.e2);
+    }
+    return dt;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(ROW_THREADS) norm_backward_rows(NormArgs p) {
+    __shared__ float s[ROW_THREADS / 32];
+    RowOf<T> row(p, blockIdx.x);
+    RowStats st = {};
+    if (p.y) row_moments(p.post, p.C, p.eps, s, [&](int64_t c) { return row.y(c); }, row.my, row.iy);
+    st.my = row.my, st.iy = row.iy;
+    if (p.dn) {
+        row_moments(p.pre, p.C, p.eps, s, [&](int64_t c) { return row.r(c); }, st.mr, st.ir);
+        float a = 0.0f, b = 0.0f;
+        for (int64_t c = threadIdx.x; c < p.C; c += ROW_THREADS) {
+            const float e = to_f32(static_cast<const T *>(p.dn)[row.row * p.C + c]) * load_or<T>(p.w_pre, c, 1.0f);
+            a += e;
+            b = fmaf(e, (row.r(c) - st.mr) * st.ir, b);
+        }
+        if (p.pre == IM2WIN_NORM_LAYER) st.e1 = block_sum(a, s) / (float)p.C;
+        st.e2 = block_sum(b, s) / (float)p.C;
+    }
+    if (threadIdx.x == 0) reinterpret_cast<RowStats *>(p.stats)[row.row] = st;
+    float e1 = 0.0f, e2 = 0.0f;  // of post
+    if (p.dy && p.post != IM2WIN_NORM_NONE) {
+        float a = 0.0f, b = 0.0f;
+        for (int64_t c = threadIdx.x; c < p.C; c += ROW_THREADS) {
+            const float e = total_grad(p, row, st, c) * row.gate(c) * load_or<T>(p.w_post, c, 1.0f);
+            a += e;
+            b = fmaf(e, row.yhat(c), b);
+        }
+        if (p.post == IM2WIN_NORM_LAYER) e1 = block_sum(a, s) / (float)p.C;
+        e2 = block_sum(b, s) / (float)p.C;
+    }
+    for (int64_t c = threadIdx.x; c < p.C; c += ROW_THREADS) {
+        const float dt = total_grad(p, row, st, c);
+        if (p.dx) static_cast<T *>(p.dx)[row.row * p.C + c] = from_f32<T>(dt * load_or<T>(p.res_scale, c, 1.0f));
+        if (p.dy) {
+            const float e = dt * row.gate(c);
+            static_cast<T *>(p.dy)[row.row * p.C + c] = from_f32<T>(
+                p.post == IM2WIN_NORM_NONE
+                    ? e
+                    : st.iy * (e * load_or<T>(p.w_post, c, 1.0f) - e1 - row.yhat(c) * e2));
+        }
+    }
+}
+
+// ---- sums over rows
+
+constexpr int SUM_COLS = 32, SUM_LANES = 8;
+
+// Block (column block, task): 32 columns, 8 rows at a time.
+template <typename T>
+__global__ void __launch_bounds__(SUM_COLS * SUM_LANES)
+    norm_column_sums(NormArgs p, SumPlan plan, int64_t col_blocks, float *part, T *dgate) {
+    __shared__ float s[SUMS][SUM_LANES][SUM_COLS];
+    const int64_t task = blockIdx.x / col_blocks, c = (int64_t)(blockIdx.x % col_blocks) * SUM_COLS + threadIdx.x % SUM_COLS;
+    const int lane = threadIdx.x / SUM_COLS;
+    const bool in = c < p.C;
+    float acc[SUMS] = {};
+    auto join = [&](int q) {  // the column's sum over the lanes, in the first lane
+        s[q][lane][threadIdx.x % SUM_COLS] = acc[q];
+        acc[q] = 0.0f;
+        __syncthreads();
+        float t = 0.0f;
+        if (lane == 0)
+            for (int l = 0; l < SUM_LANES; ++l) t += s[q][l][threadIdx.x];
+        __syncthreads();
+        return t;
+    };
+    const int64_t g0 = plan.group_splits > 1 ? task / plan.group_splits : task * plan.groups_per_task;
+    const int64_t g1 = min(plan.groups, g0 + plan.groups_per_task);
+    for (int64_t g = g0; g < g1; ++g) {
+        const int64_t first = g * p.per_gate + (plan.group_splits > 1 ? (task % plan.group_splits) * plan.span : 0);
+        const int64_t last = min(min(p.R, (g + 1) * p.per_gate), plan.group_splits > 1 ? first + plan.span : p.R);
+        for (int64_t r = first + lane; in && r < last; r += SUM_LANES) {
+            RowOf<T> row(p, r);
+            const RowStats st = reinterpret_cast<const RowStats *>(p.stats)[r];
+            row.my = st.my, row.iy = st.iy;
+            const float dt = total_grad(p, row, st, c);
+            acc[SUM_RES] = fmaf(row.x(c), dt, acc[SUM_RES]);
+            if (p.y) {
+                acc[SUM_GATE] = fmaf(row.post(c), dt, acc[SUM_GATE]);
+                const float dp = dt * row.gate(c);
+                acc[SUM_W_POST] = fmaf(dp, row.yhat(c), acc[SUM_W_POST]);
+                acc[SUM_B_POST] += dp;
+            }
+            if (p.dn) {
+                const float d = to_f32(static_cast<const T *>(p.dn)[r * p.C + c]);
+                acc[SUM_W_PRE] = fmaf(d, (row.r(c) - st.mr) * st.ir, acc[SUM_W_PRE]);
+                acc[SUM_B_PRE] += d;
+            }
+        }
+        if (dgate && plan.group_splits == 1) {
+            const float t = join(SUM_GATE);
+            if (lane == 0 && in) dgate[g * p.C + c] = from_f32<T>(t);
+        }
+    }
+    for (int q = 0; q < SUMS; ++q) {
+        const float t = join(q);
+        if (lane == 0 && in) part[(q * plan.tasks + task) * p.C + c] = t;
+    }
+}
+
+// out[j][c] = sum of the `per` partial rows of j, in their order.
+template <typename T>
+__global__ void __launch_bounds__(256) join_partials(const float *part, int64_t per, int64_t total, int64_t C, T *out) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    const float *src = part + (i / C) * per * C + i % C;
+    float t = 0.0f;
+    for (int64_t k = 0; k < per; ++k) t += src[k * C];
+    out[i] = from_f32<T>(t);
+}
+
+// ---- rows in registers
+//
+// A row of at most TPR * EPT elements is held by TPR neighbouring threads, EPT
+// fp32 values each, so that every input is read from memory once and the row's
+// statistics are reductions over registers (two passes for LAYER: the second
+// moment is taken about the mean). Thread t holds vectors t, t + TPR, ... of V
+// elements: 16-byte vectors where C allows, else 4-byte ones, else elements.
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+    T v[V];
+};
+
+template <typename T, int V, int EPT, int TPR>
+struct Row {
+    static constexpr int VPT = EPT / V;
+    using P = Pack<T, V>;
+    static __device__ __forceinline__ int first(int j, int t) { return (j * TPR + t) * V; }
+    // `absent` where p is null; columns past C read as `outside`
+    static __device__ __forceinline__ void load(P (&d)[VPT], const void *p, int64_t at, int C, int t, float absent,
+                                                float outside = 0.0f) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = first(j, t);
+            if (p && c < C) {
+                d[j] = *reinterpret_cast<const P *>(static_cast<const T *>(p) + at + c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[j].v[i] = from_f32<T>(c < C ? absent : outside);
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t at, int C, int t, const float (&v)[EPT]) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = first(j, t);
+            if (c >= C) continue;
+            P d;
+#pragma unroll
+            for (int i = 0; i < V; ++i) d.v[i] = from_f32<T>(v[j * V + i]);
+            *reinterpret_cast<P *>(static_cast<T *>(p) + at + c) = d;
+        }
+    }
+    static __device__ __forceinline__ float get(const P (&d)[VPT], int e) { return to_f32(d[e / V].v[e % V]); }
+    static __device__ __forceinline__ bool inside(int e, int C, int t) { return first(e / V, t) < C; }
+};
+
+// Sums over the TPR threads of a row, the same bits in every one of them. Rows of
+// more than a warp join their warps' sums through shared memory, in two buffers
+// in turn: a buffer is written again only after the barrier of the reduction
+// between, which every thread reaches after reading it.
+template <int TPR, int THREADS>
+struct RowReduce {
+    static constexpr int WARPS = TPR > 32 ? TPR / 32 : 1;
+    float2 (*buf)[THREADS / 32];  // [2][THREADS / 32]
+    int phase = 0;
+    __device__ explicit RowReduce(float2 (*b)[THREADS / 32]) : buf(b) {}
+    __device__ __forceinline__ float2 sum2(float a, float b) {
+#pragma unroll
+        for (int o = (TPR > 32 ? 32 : TPR) / 2; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        if (TPR > 32) {
+            const int slot = threadIdx.x / TPR, warp = threadIdx.x >> 5;
+            if ((threadIdx.x & 31) == 0) buf[phase][warp] = make_float2(a, b);
+            if (TPR == THREADS) __syncthreads();
+            else asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(TPR) : "memory");
+            a = b = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                const float2 v = buf[phase][slot * WARPS + w];
+                a += v.x, b += v.y;
+            }
+            phase ^= 1;
+        }
+        return make_float2(a, b);
+    }
+    __device__ __forceinline__ float sum(float a) { return sum2(a, 0.0f).x; }
+};
+
+// v -> its normed values; m and i as in row_moments.
+template <typename R, int EPT, typename Red>
+__device__ __forceinline__ void norm_values(int kind, float (&v)[EPT], int C, float inv_c, float eps, int t, Red &red,
+                                            float &i) {
+    i = 1.0f;
+    if (kind == IM2WIN_NORM_NONE) return;
+    float a = 0.0f;
+    if (kind == IM2WIN_NORM_LAYER) {
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) a += v[e];
+        const float m = red.sum(a) * inv_c;
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) v[e] = R::inside(e, C, t) ? v[e] - m : 0.0f;
+        a = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) a = fmaf(v[e], v[e], a);
+    i = 1.0f / sqrtf(red.sum(a) * inv_c + eps);
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) v[e] *= i;
+}
+
+// One row a TPR threads, rows dealt out to the grid in turn. Bound by memory: two
+// rows read and two written; the parameters come from L1.
+template <typename T, int V, int EPT, int TPR, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_forward_rows(const __grid_constant__ NormArgs p) {
+    using R = Row<T, V, EPT, TPR>;
+    __shared__ float2 buf[2][THREADS / 32];
+    RowReduce<TPR, THREADS> red(buf);
+    constexpr int RPB = THREADS / TPR;
+    const int t = threadIdx.x % TPR, C = (int)p.C;
+    const float inv_c = 1.0f / (float)C;
+    // every thread of a block makes the same number of rounds (the reductions' barriers)
+    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.R; row0 += (int64_t)gridDim.x * RPB) {
+        const int64_t row = row0 + threadIdx.x / TPR;
+        const bool live = row < p.R;
+        const int width = live ? C : 0;
+        const int64_t at = row * C;
+        typename R::P px[R::VPT], py[R::VPT], pg[R::VPT], ps[R::VPT], w[R::VPT], b[R::VPT];
+        R::load(px, p.x, at, width, t, 0.0f);
+        R::load(py, p.y, at, width, t, 0.0f);
+        R::load(ps, p.res_scale, 0, C, t, 1.0f);
+        R::load(pg, p.gate, live && p.gate ? row / p.per_gate * C : 0, C, t, 1.0f);
+        R::load(w, p.w_post, 0, C, t, 1.0f);
+        R::load(b, p.b_post, 0, C, t, 0.0f);
+        float r[EPT], i;
+        if (p.y) {
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) r[e] = R::get(py, e);
+            norm_values<R>(p.post, r, C, inv_c, p.eps, t, red, i);
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) r[e] = R::get(pg, e) * fmaf(r[e], R::get(w, e), R::get(b, e));
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) r[e] = 0.0f;
+        }
+        R::load(w, p.w_pre, 0, C, t, 1.0f);
+        R::load(b, p.b_pre, 0, C, t, 0.0f);
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) r[e] = R::inside(e, C, t) ? fmaf(R::get(px, e), R::get(ps, e), r[e]) : 0.0f;
+        if (p.r) R::store(p.r, at, width, t, r);
+        if (p.n) {
+            norm_values<R>(p.pre, r, C, inv_c, p.eps, t, red, i);
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) r[e] = fmaf(r[e], R::get(w, e), R::get(b, e));
+            R::store(p.n, at, width, t, r);
+        }
+    }
+}
+
+// ---- the backward pass in one reading of its inputs
+//
+// A block walks rows and keeps the sums over them in registers, a thread for its
+// own columns. Within a gate group dw_post, db_post and dgate all follow from
+//   A = sum dt * yhat,  B = sum dt:   dgate = w A + b B,  dw_post += gate A,  db_post += gate B,
+// so five sums are enough: A, B, sum x dt, sum dn rhat and sum dn. Two ways of
+// cutting the rows:
+//  long groups   block k takes rows [R k / blocks, R (k+1) / blocks), its row slots
+//                in turn; at the end of a group and of its rows it joins its slots'
+//                A and B into segment k + g (unique along the staircase of blocks and
+//                groups), which the joining kernel weighs with the group's gate;
+//  short groups  a row slot takes whole groups, writes their dgate and adds the
+//                weighed A and B to its sums in shared memory.
+
+template <typename T, int V, int EPT, int TPR, int THREADS, bool SHORT>
+__global__ void __launch_bounds__(THREADS, 1)
+    norm_backward_fused(const __grid_constant__ NormArgs p, const __grid_constant__ BackPlan plan, float *part, float *seg,
+                        T *dgate) {
+    using R = Row<T, V, EPT, TPR>;
+    constexpr int RPB = THREADS / TPR;
+    extern __shared__ float dyn[];  // SHORT: A and B weighed, [2][RPB][TPR * EPT]; then [RPB][TPR * EPT] to join slots
+    __shared__ float2 buf[2][THREADS / 32];
+    RowReduce<TPR, THREADS> red(buf);
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR, C = (int)p.C;
+    const float inv_c = 1.0f / (float)C;
+    constexpr int W = TPR * EPT;  // columns a slot holds
+    float *fold = dyn + (size_t)slot * W, *join = dyn + (SHORT ? 2 * RPB * W : 0);
+    float acc[BACK_SUMS][EPT];
+#pragma unroll
+    for (int q = 0; q < BACK_SUMS; ++q)
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) acc[q][e] = 0.0f;
+    if (SHORT) {
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) fold[e * TPR + t] = fold[RPB * W + e * TPR + t] = 0.0f;
+    }
+
+    // Rows [first, last) of group g, every `step`-th; `rounds` is the same for all slots.
+    auto rows = [&](int64_t g, int64_t first, int64_t last, int64_t step, int64_t rounds, typename R::P(&pg)[R::VPT]) {
+        typename R::P px[R::VPT], py[R::VPT], pr[R::VPT], pn[R::VPT], w[R::VPT], b[R::VPT];
+        auto fetch = [&](int64_t row) {
+            const int width = row < last ? C : 0;
+            R::load(px, p.x, row * C, width, t, 0.0f);
+            R::load(py, p.y, row * C, width, t, 0.0f);
+            R::load(pr, p.dr, row * C, width, t, 0.0f);
+            R::load(pn, p.dn, row * C, width, t, 0.0f);
+        };
+        R::load(pg, p.gate, p.gate ? g * C : 0, C, t, 1.0f);
+        fetch(first);
+        for (int64_t k = 0; k < rounds; ++k) {
+            const int64_t row = first + k * step;
+            const int width = row < last ? C : 0;
+            const float eps = row < last ? p.eps : 1.0f;  // (a slot without a row: zeros throughout)
+            float yh[EPT], rh[EPT], d[EPT], iy = 1.0f, ir = 1.0f;
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) yh[e] = R::get(py, e);
+            if (p.y) norm_values<R>(p.post, yh, C, inv_c, eps, t, red, iy);
+            R::load(w, p.res_scale, 0, C, t, 1.0f);
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                d[e] = R::get(pr, e);
+                rh[e] = R::get(px, e) * R::get(w, e);
+            }
+            if (p.dn) {
+                if (p.y) {
+                    R::load(w, p.w_post, 0, C, t, 1.0f);
+                    R::load(b, p.b_post, 0, C, t, 0.0f);
+#pragma unroll
+                    for (int e = 0; e < EPT; ++e)
+                        rh[e] = R::inside(e, width, t) ? fmaf(R::get(pg, e), fmaf(yh[e], R::get(w, e), R::get(b, e)), rh[e]) : 0.0f;
+                }
+                norm_values<R>(p.pre, rh, C, inv_c, eps, t, red, ir);
+                R::load(w, p.w_pre, 0, C, t, 1.0f);
+                float e1 = 0.0f, e2 = 0.0f;
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) {
+                    const float n = R::get(pn, e), f = n * R::get(w, e);
+                    e1 += f;
+                    e2 = fmaf(f, rh[e], e2);
+                    acc[BACK_W_PRE][e] = fmaf(n, rh[e], acc[BACK_W_PRE][e]);
+                    acc[BACK_B_PRE][e] += n;
+                }
+                const float2 m = red.sum2(e1, e2);
+                e1 = p.pre == IM2WIN_NORM_LAYER ? m.x * inv_c : 0.0f;
+                e2 = m.y * inv_c;
+#pragma unroll
+                for (int e = 0; e < EPT; ++e)
+                    d[e] = fmaf(ir, R::get(pn, e) * R::get(w, e) - e1 - rh[e] * e2, d[e]);
+            }
+            // d is dt from here on (its columns past C meet only zeros: x, yh; and are not stored)
+            R::load(w, p.res_scale, 0, C, t, 1.0f);
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                if (!R::inside(e, width, t)) d[e] = 0.0f;
+                acc[BACK_RES][e] = fmaf(R::get(px, e), d[e], acc[BACK_RES][e]);
+                acc[BACK_A][e] = fmaf(d[e], yh[e], acc[BACK_A][e]);
+                acc[BACK_B][e] += d[e];
+                rh[e] = d[e] * R::get(w, e);
+            }
+            if (k + 1 < rounds) fetch(row + step);  // in flight through the last reduction and the stores
+            if (p.dx) R::store(p.dx, row * C, width, t, rh);
+            if (p.dy) {
+                R::load(w, p.w_post, 0, C, t, 1.0f);
+                float f1 = 0.0f, f2 = 0.0f;
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) {
+                    d[e] *= R::get(pg, e) * R::get(w, e);
+                    f1 += d[e];
+                    f2 = fmaf(d[e], yh[e], f2);
+                }
+                if (p.post != IM2WIN_NORM_NONE) {
+                    const float2 m = red.sum2(f1, f2);
+                    f1 = p.post == IM2WIN_NORM_LAYER ? m.x * inv_c : 0.0f;
+                    f2 = m.y * inv_c;
+#pragma unroll
+                    for (int e = 0; e < EPT; ++e) d[e] = iy * (d[e] - f1 - yh[e] * f2);
+                }
+                R::store(p.dy, row * C, width, t, d);
+            }
+        }
+    };
+    // Adds one sum over the block's slots, in their order, into dst (and clears it).
+    auto join_slots = [&](int q, float *dst) {
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+            join[slot * W + R::first(e / V, t) + e % V] = acc[q][e];
+            acc[q][e] = 0.0f;
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < C; c += THREADS) {
+            float v = 0.0f;
+#pragma unroll 8
+            for (int i = 0; i < RPB; ++i) v += join[i * W + c];
+            dst[c] = v;
+        }
+        __syncthreads();
+    };
+
+    typename R::P pg[R::VPT];
+    if (SHORT) {
+        // slot s of all takes groups s, s + slots, ...
+        const int64_t slots = (int64_t)gridDim.x * RPB;
+        for (int64_t g0 = (int64_t)blockIdx.x * RPB; g0 < plan.groups; g0 += slots) {
+            const int64_t g = g0 + slot, first = g * p.per_gate;
+            const int64_t last = g < plan.groups ? min(p.R, first + p.per_gate) : first;
+            rows(g < plan.groups ? g : 0, first, last, 1, p.per_gate, pg);
+            if (!p.y) continue;
+            typename R::P w[R::VPT], b[R::VPT];
+            R::load(w, p.w_post, 0, C, t, 1.0f);
+            R::load(b, p.b_post, 0, C, t, 0.0f);
+            float d[EPT];
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                d[e] = fmaf(R::get(w, e), acc[BACK_A][e], R::get(b, e) * acc[BACK_B][e]);
+                fold[e * TPR + t] += R::get(pg, e) * acc[BACK_A][e];
+                fold[RPB * W + e * TPR + t] += R::get(pg, e) * acc[BACK_B][e];
+                acc[BACK_A][e] = acc[BACK_B][e] = 0.0f;
+            }
+            if (dgate && g < plan.groups) R::store(dgate, g * C, C, t, d);
+        }
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) acc[BACK_A][e] = fold[e * TPR + t], acc[BACK_B][e] = fold[RPB * W + e * TPR + t];
+        for (int q = 0; q < BACK_SUMS; ++q) join_slots(q, part + ((int64_t)q * gridDim.x + blockIdx.x) * C);
+    } else {
+        const int64_t begin = p.R * blockIdx.x / gridDim.x, end = p.R * (blockIdx.x + 1) / gridDim.x;
+        for (int64_t at = begin; at < end;) {
+            const int64_t g = at / p.per_gate, last = min(end, (g + 1) * p.per_gate);
+            rows(g, at + slot, last, RPB, (last - at + RPB - 1) / RPB, pg);
+            if (p.y) {
+                float *dst = seg + (blockIdx.x + g) * 2 * C;
+                join_slots(BACK_A, dst);
+                join_slots(BACK_B, dst + C);
+            }
+            at = last;
+        }
+        for (int q = 0; q < BACK_A; ++q) join_slots(q, part + ((int64_t)q * gridDim.x + blockIdx.x) * C);
+    }
+}
+
+// Joins the fused pass's partial sums: 32 columns a block, its 32 warps over
+// slices of the partials, then the warps' in order. blockIdx.y: 0 dres_scale,
+// 1 dw_pre, 2 db_pre, 3 dw_post, 4 db_post, 5.. dgate of group y - 5 (long groups).
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_join(const __grid_constant__ NormArgs p, const __grid_constant__ BackPlan plan,
+                                                  const float *part, const float *seg, JoinOuts o) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t C = p.C, c = (int64_t)blockIdx.x * 32 + lane;
+    const bool in = c < C;
+    const int what = blockIdx.y < BACK_SUMS ? (int)blockIdx.y : BACK_SUMS;
+    T *out = static_cast<T *>(what < BACK_SUMS ? o.out[what] : o.dgate);
+    if (!out) return;
+    auto over_warps = [&](float v) {
+        s[warp][lane] = v;
+        __syncthreads();
+        v = 0.0f;
+        if (warp == 0)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v += s[i][lane];
+        __syncthreads();
+        return v;
+    };
+    // block k's rows, and so its groups, as the fused pass cut them
+    auto first_row = [&](int64_t k) { return p.R * k / plan.blocks; };
+    if (what < BACK_SUMS && (what < BACK_A || plan.short_groups)) {
+        float v = 0.0f;
+        if (in)
+#pragma unroll 4
+            for (int64_t k = warp; k < plan.blocks; k += 32) v += part[((int64_t)what * plan.blocks + k) * C + c];
+        v = over_warps(v);
+        if (warp == 0 && in) out[c] = from_f32<T>(v);
+    } else if (what < BACK_SUMS) {
+        float v = 0.0f;
+        if (in)
+            for (int64_t k = warp; k < plan.blocks; k += 32) {
+                const int64_t begin = first_row(k), end = first_row(k + 1);
+                if (begin >= end) continue;
+                for (int64_t g = begin / p.per_gate; g <= (end - 1) / p.per_gate; ++g)
+                    v = fmaf(load_or<T>(p.gate, p.gate ? g * C + c : 0, 1.0f), seg[(k + g) * 2 * C + (what == BACK_B ? C : 0) + c], v);
+            }
+        v = over_warps(v);
+        if (warp == 0 && in) out[c] = from_f32<T>(v);
+    } else {
+        // groups blockIdx.y - 5, + gridDim.y - 5, ...: the blocks whose rows meet the group's
+        for (int64_t g = blockIdx.y - BACK_SUMS; g < plan.groups; g += gridDim.y - BACK_SUMS) {
+            const int64_t lo = g * p.per_gate, hi = min(p.R, lo + p.per_gate);
+            int64_t k0 = lo * plan.blocks / p.R;
+            while (k0 > 0 && first_row(k0) > lo) --k0;
+            while (first_row(k0 + 1) <= lo) ++k0;
+            float a = 0.0f, b = 0.0f;
+            if (in)
+                for (int64_t k = k0 + warp; k < plan.blocks && first_row(k) < hi; k += 32) {
+                    if (first_row(k) >= first_row(k + 1)) continue;
+                    a += seg[(k + g) * 2 * C + c];
+                    b += seg[(k + g) * 2 * C + C + c];
+                }
+            a = over_warps(a), b = over_warps(b);
+            if (warp == 0 && in)
+                out[g * C + c] = from_f32<T>(fmaf(load_or<T>(p.w_post, c, 1.0f), a, load_or<T>(p.b_post, c, 0.0f) * b));
+        }
+    }
+}
+
+template <typename T, int V, int TPR>
+cudaError_t launch_fused(const NormArgs &p, const BackPlan &plan, float *part, float *seg, T *dgate, cudaStream_t st) {
+    constexpr int EPT = 8, THREADS = FUSED_THREADS;
+    const size_t smem = (size_t)(plan.short_groups ? 3 : 1) * THREADS * EPT * 4;
+    auto kernel = plan.short_groups ? norm_backward_fused<T, V, EPT, TPR, THREADS, true>
+                                    : norm_backward_fused<T, V, EPT, TPR, THREADS, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<plan.blocks, THREADS, smem, st>>>(p, plan, part, seg, dgate);
+    return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t launch_fused_tpr(const NormArgs &p, const BackPlan &plan, float *part, float *seg, T *dgate, cudaStream_t st) {
+    switch (plan.tpr) {
+        case 8: return launch_fused<T, V, 8>(p, plan, part, seg, dgate, st);
+        case 16: return launch_fused<T, V, 16>(p, plan, part, seg, dgate, st);
+        case 32: return launch_fused<T, V, 32>(p, plan, part, seg, dgate, st);
+        case 64: return launch_fused<T, V, 64>(p, plan, part, seg, dgate, st);
+        case 128: return launch_fused<T, V, 128>(p, plan, part, seg, dgate, st);
+        case 256: return launch_fused<T, V, 256>(p, plan, part, seg, dgate, st);
+        default: return launch_fused<T, V, 512>(p, plan, part, seg, dgate, st);
+    }
+}
+
+// Elements of the widest vector that rows of C elements allow; calls f with it.
+template <typename T, typename Fn>
+inline cudaError_t with_vector(int64_t C, Fn f) {
+    constexpr int wide = 16 / (int)sizeof(T), mid = 4 / (int)sizeof(T);
+    return C % wide == 0 ? f(IntC<wide>()) : C % mid == 0 ? f(IntC<mid>()) : f(IntC<1>());
+}
+
+template <typename T, int V, int TPR>
+cudaError_t launch_rows(const NormArgs &p, cudaStream_t st) {
+    constexpr int THREADS = TPR > 256 ? TPR : 256;
+    const int64_t blocks = (p.R + THREADS / TPR - 1) / (THREADS / TPR);
+    norm_forward_rows<T, V, 8, TPR, THREADS><<<(unsigned)std::min<int64_t>(blocks, SMS * 2048 / THREADS), THREADS, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t launch_forward(const NormArgs &p, cudaStream_t st) {
+    if (p.C <= 32) return launch_rows<T, V, 4>(p, st);
+    if (p.C <= 128) return launch_rows<T, V, 16>(p, st);
+    if (p.C <= 256) return launch_rows<T, V, 32>(p, st);
+    if (p.C <= 512) return launch_rows<T, V, 64>(p, st);
+    if (p.C <= 1024) return launch_rows<T, V, 128>(p, st);
+    if (p.C <= 2048) return launch_rows<T, V, 256>(p, st);
+    if (p.C <= 4096) return launch_rows<T, V, 512>(p, st);
+    return launch_rows<T, V, 1024>(p, st);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_norm_forward(const NormArgs &p, cudaStream_t st) {
+    if (p.C <= 8 * 1024) return with_vector<T>(p.C, [&](auto v) { return launch_forward<T, decltype(v)::value>(p, st); });
+    norm_forward<T><<<(unsigned)p.R, ROW_THREADS, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_norm_backward(const NormArgs &args, const ColumnGrads &g, void *ws, cudaStream_t st) {
+    NormArgs p = args;
+    const BackwardParts parts(p.R, p.C, p.per_gate);
+    unsigned char *base = static_cast<unsigned char *>(ws);
+    p.stats = reinterpret_cast<float *>(base + parts.stats);
+    float *part = reinterpret_cast<float *>(base + parts.part), *seg = reinterpret_cast<float *>(base + parts.seg);
+    T *dgate = static_cast<T *>(g.dgate);
+    const BackPlan fused = plan_back(p.R, p.C, p.per_gate);
+    if (fused.blocks) {
+        const cudaError_t e = with_vector<T>(
+            p.C, [&](auto v) { return launch_fused_tpr<T, decltype(v)::value>(p, fused, part, seg, dgate, st); });
+        if (!g.any() || e != cudaSuccess) return e;
+        const JoinOuts o = {{g.dres_scale, g.dw_pre, g.db_pre, g.dw_post, g.db_post}, fused.short_groups ? nullptr : g.dgate};
+        const dim3 grid((unsigned)((p.C + 31) / 32),
+                        BACK_SUMS + (o.dgate ? (unsigned)std::min<int64_t>(fused.groups, 1024) : 0));
+        norm_join<T><<<grid, 1024, 0, st>>>(p, fused, part, seg, o);
+        return cudaGetLastError();
+    }
+    const SumPlan plan = plan_sums(p.R, p.per_gate);
+    const int64_t col_blocks = (p.C + SUM_COLS - 1) / SUM_COLS;
+    norm_backward_rows<T><<<(unsigned)p.R, ROW_THREADS, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (!g.any() || e != cudaSuccess) return e;
+    norm_column_sums<T><<<(unsigned)(plan.tasks * col_blocks), SUM_COLS * SUM_LANES, 0, st>>>(p, plan, col_blocks, part, dgate);
+    void *outs[SUMS] = {g.dres_scale, g.dw_post, g.db_post, g.dw_pre, g.db_pre, plan.group_splits > 1 ? g.dgate : nullptr};
+    for (int q = 0; q < SUMS; ++q) {
+        if (!outs[q]) continue;
+        const int64_t total = q == SUM_GATE ? plan.groups * p.C : p.C;
+        join_partials<T><<<(unsigned)((total + 255) / 256), 256, 0, st>>>(
+            part + q * plan.tasks * p.C, q == SUM_GATE ? plan.group_splits : plan.tasks, total, p.C,
+            static_cast<T *>(outs[q]));
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace rnorm
+}  // namespace im2win
