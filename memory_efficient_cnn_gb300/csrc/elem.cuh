@@ -34,12 +34,14 @@ __device__ __forceinline__ bf16_t from_f32<bf16_t>(float v) {
     return __float2bfloat16_rn(v);
 }
 
-// The elements of one aligned 16-byte vector.
-template <typename T>
-struct alignas(16) Vec16 {
-    static constexpr int N = 16 / (int)sizeof(T);
-    T v[N];
+// V elements moved as one aligned word.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+    static constexpr int N = V;
+    T v[V];
 };
+template <typename T>
+using Vec16 = Vec<T, 16 / (int)sizeof(T)>;
 
 // Calls f with a null pointer of the C++ type of dtype code `dtype`; false for
 // an unknown code.

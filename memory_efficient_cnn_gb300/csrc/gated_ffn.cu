@@ -38,6 +38,8 @@ struct Problem {
         : R((int)R_), C((int)C_), F((int)F_), dtype(dtype_), esz(elem_size(dtype_)), act(act_),
           tc(dtype_ != IM2WIN_F32), Cp(tc ? (C_ + 7) / 8 * 8 : C_), Fp(tc ? (F_ + 7) / 8 * 8 : F_) {}
 
+    // the forward pass of few rows has kernels of its own
+    bool few() const { return R <= few_rows(dtype); }
     size_t rows_c(int64_t rows) const { return (size_t)(rows * Cp) * esz; }
     size_t rows_f(int64_t rows) const { return (size_t)(rows * Fp) * esz; }
 
@@ -108,10 +110,16 @@ const void *const kSome = reinterpret_cast<const void *>(16);  // a present oper
 void *const kSomeOut = reinterpret_cast<void *>(16);
 
 struct ForwardParts {
-    size_t h, x, wg, wu, wd, part, bytes;
+    size_t h, h_lo, x, wg, wu, wd, part, bytes;
     ForwardParts(const Problem &q, bool saved) {
         Parts p(kStatusBytes);
         h = p.add(saved ? 0 : q.rows_f(q.R));
+        h_lo = x = wg = wu = wd = part = p.end;
+        if (q.few()) {
+            p.add(q.tc ? q.rows_f(q.R) : 0);
+            bytes = p.end;
+            return;
+        }
         const bool pad_c = q.Cp != q.C, pad_f = q.Fp != q.F;
         x = p.add(pad_c ? q.rows_c(q.R) : 0);
         wg = p.add(pad_c ? q.rows_c(q.F) : 0);
@@ -231,13 +239,20 @@ im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_
     if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
     const SavedParts kept(q);
     void *h = saved ? at(saved, kept.h) : at(ws, parts.h);
-    Sequence seq{q, ws, at(ws, parts.part), static_cast<cudaStream_t>(stream)};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    float *g = saved ? floats(saved, kept.g) : nullptr, *u = saved ? floats(saved, kept.u) : nullptr;
+    if (q.few()) {
+        const Few f = {q.R, q.C, q.F, act, x, w_gate, w_up, w_down, y, h, at(ws, parts.h_lo), q.Fp, g, u,
+                       static_cast<uint32_t *>(ws)};
+        return launch_few(f, dtype, st) == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+    }
+    Sequence seq{q, ws, at(ws, parts.part), st};
     x = seq.pitched(x, q.R, q.C, parts.x);
     w_gate = seq.pitched(w_gate, q.F, q.C, parts.wg);
     w_up = seq.pitched(w_up, q.F, q.C, parts.wu);
     w_down = seq.pitched(w_down, q.C, q.F, parts.wd);
     seq.copy_pitched();
-    seq.run(q.gated(x, w_gate, w_up, h, saved ? floats(saved, kept.g) : nullptr, saved ? floats(saved, kept.u) : nullptr));
+    seq.run(q.gated(x, w_gate, w_up, h, g, u));
     seq.run(q.down(h, w_down, y));
     return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
 }

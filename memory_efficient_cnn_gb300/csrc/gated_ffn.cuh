@@ -69,6 +69,20 @@ struct TcPlan {
 TcPlan plan_tc(const Product &p);
 cudaError_t launch_tc(const Product &p, bool bf16, uint32_t *status, bool clear_status, void *part, cudaStream_t st);
 
+// The forward pass of few rows (R <= few_rows(dtype)), from dense matrices of any
+// alignment that their type allows; h and its remainder h_lo (16-bit types) have
+// rows of ldh elements, a multiple of 8 there.
+struct Few {
+    int R, C, F, act;
+    const void *x, *w_gate, *w_up, *w_down;
+    void *y, *h, *h_lo;
+    int64_t ldh;
+    float *g, *u;
+    uint32_t *status;
+};
+int few_rows(int dtype);
+cudaError_t launch_few(const Few &f, int dtype, cudaStream_t st);
+
 // Copies of dense matrices to a pitch that is a multiple of 8 elements (16-bit types).
 struct Repitch {
     const void *src;

@@ -218,15 +218,10 @@ __global__ void __launch_bounds__(256) join_partials(const float *part, int64_t 
 // moment is taken about the mean). Thread t holds vectors t, t + TPR, ... of V
 // elements: 16-byte vectors where C allows, else 4-byte ones, else elements.
 
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-    T v[V];
-};
-
 template <typename T, int V, int EPT, int TPR>
 struct Row {
     static constexpr int VPT = EPT / V;
-    using P = Pack<T, V>;
+    using P = Vec<T, V>;
     static __device__ __forceinline__ int first(int j, int t) { return (j * TPR + t) * V; }
     // `absent` where p is null; columns past C read as `outside`
     static __device__ __forceinline__ void load(P (&d)[VPT], const void *p, int64_t at, int C, int t, float absent,
