@@ -8,11 +8,11 @@ allocate through torch, and nothing is computed here.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from . import _binding as _b
-from ._binding import _check, _cuda, _dtype_code, _same_device, _stream, lib
+from ._binding import _check, _cuda, _dtype_code, _same_device, lib
 
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
@@ -28,6 +28,23 @@ def _code(table, name, what):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _stream(device: int):
+    """The current stream of a device, as an integer (a call costs a tenth of building a Stream object)."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _alike(dtype, device: int, *ts) -> bool:
+    """Whether every tensor is contiguous, of one dtype and on one CUDA device. The
+    calls test this first and look for what is wrong only where it fails: a small
+    call costs less on the GPU than a full set of checks on the host."""
+    if device < 0:
+        return False
+    for t in ts:
+        if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+            return False
+    return True
 
 
 def _bytes(t):
@@ -50,6 +67,7 @@ def _empty(nbytes, device):
 
 
 # ---------------------------------------------------------------- gated feed-forward
+@functools.lru_cache(maxsize=4096)
 def im2win_gated_ffn_size(buffer: int, R, C, F, dtype: int) -> int:
     out = ctypes.c_size_t(0)
     _check("im2win_gated_ffn_size", lib().im2win_gated_ffn_size(buffer, R, C, F, dtype, ctypes.byref(out)))
@@ -62,83 +80,106 @@ def _ffn_shapes(fn, x, w_gate, w_up, w_down):
     if x.dim() < 1 or w_gate.dim() != 2:
         raise ValueError(f"{fn}: x must be [..., C] and w_gate [F, C]")
     C, F = x.shape[-1], w_gate.shape[0]
-    _shape(fn, "w_gate", w_gate, (F, C))
-    _shape(fn, "w_up", w_up, (F, C))
-    _shape(fn, "w_down", w_down, (C, F))
-    if C < 1 or F < 1:
-        raise ValueError(f"{fn}: C and F must be at least 1")
-    _same_dtype(fn, x, w_gate, w_up, w_down)
-    _same_device(fn, x, w_gate, w_up, w_down)
-    _cuda(x, w_gate, w_up, w_down)
+    if not (C >= 1 and F >= 1 and w_gate.shape == w_up.shape == (F, C) and w_down.shape == (C, F)
+            and _alike(x.dtype, x.get_device(), x, w_gate, w_up, w_down)):
+        _shape(fn, "w_gate", w_gate, (F, C))
+        _shape(fn, "w_up", w_up, (F, C))
+        _shape(fn, "w_down", w_down, (C, F))
+        if C < 1 or F < 1:
+            raise ValueError(f"{fn}: C and F must be at least 1")
+        _same_dtype(fn, x, w_gate, w_up, w_down)
+        _same_device(fn, x, w_gate, w_up, w_down)
+        _cuda(x, w_gate, w_up, w_down)
     return x.numel() // C, C, F
+
+
+def _ffn(fn, dims, x, w_gate, w_up, w_down, y, saved, ws, act):
+    """The call itself, on checked tensors."""
+    _check(fn, lib().im2win_gated_ffn(
+        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), y.data_ptr(), _ptr(saved), ws.data_ptr(),
+        _bytes(ws), *dims, _code(ACTS, act, "act"), _dtype_code(x), _stream(x.get_device())))
+
+
+def _ffn_outputs(fn, dims, x, y, saved, ws):
+    if not (y.shape == x.shape and _alike(x.dtype, x.get_device(), y)):
+        _shape(fn, "y", y, x.shape)
+        _same_dtype(fn, x, y)
+    others = [y, ws] if saved is None else [y, ws, saved]
+    _same_device(fn, x, *others)
+    _cuda(*others)
+    if saved is not None and _bytes(saved) < im2win_gated_ffn_size(FFN_SAVED, *dims, _dtype_code(x)):
+        raise ValueError(f"{fn}: saved is too small")
 
 
 def im2win_gated_ffn(x, w_gate, w_up, w_down, y, saved, ws, act: str = "silu") -> None:
     """y = (act(x w_gate^T) * (x w_up^T)) w_down^T; saved None: inference."""
     fn = "im2win_gated_ffn"
-    R, C, F = _ffn_shapes(fn, x, w_gate, w_up, w_down)
-    _shape(fn, "y", y, x.shape)
-    _same_dtype(fn, x, y)
-    _same_device(fn, x, y, ws, *([] if saved is None else [saved]))
-    _cuda(y, ws, *([] if saved is None else [saved]))
-    code = _dtype_code(x)
-    if saved is not None and _bytes(saved) < im2win_gated_ffn_size(FFN_SAVED, R, C, F, code):
+    dims = _ffn_shapes(fn, x, w_gate, w_up, w_down)
+    _ffn_outputs(fn, dims, x, y, saved, ws)
+    _ffn(fn, dims, x, w_gate, w_up, w_down, y, saved, ws, act)
+
+
+def _ffn_backward(fn, dims, dy, x, w_gate, w_up, w_down, saved, dx, dw_gate, dw_up, dw_down, ws, act):
+    _check(fn, lib().im2win_gated_ffn_backward(
+        dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), saved.data_ptr(), _ptr(dx),
+        _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), ws.data_ptr(), _bytes(ws), *dims, _code(ACTS, act, "act"),
+        _dtype_code(x), _stream(x.get_device())))
+
+
+def _ffn_backward_inputs(fn, dims, dy, x, saved, ws):
+    _shape(fn, "dy", dy, x.shape)
+    _same_dtype(fn, x, dy)
+    _same_device(fn, x, dy, saved, ws)
+    _cuda(dy, saved, ws)
+    if _bytes(saved) < im2win_gated_ffn_size(FFN_SAVED, *dims, _dtype_code(x)):
         raise ValueError(f"{fn}: saved is too small")
-    _check(fn, lib().im2win_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(y), _ptr(saved), _ptr(ws),
-                                      _bytes(ws), R, C, F, _code(ACTS, act, "act"), code, _stream(x)))
 
 
 def im2win_gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, dx, dw_gate, dw_up, dw_down, ws,
                               act: str = "silu") -> None:
     """Gradients of im2win_gated_ffn; dx, or the three dw, may be None."""
     fn = "im2win_gated_ffn_backward"
-    R, C, F = _ffn_shapes(fn, x, w_gate, w_up, w_down)
-    _shape(fn, "dy", dy, x.shape)
-    outs = [t for t in (dx, dw_gate, dw_up, dw_down) if t is not None]
+    dims = _ffn_shapes(fn, x, w_gate, w_up, w_down)
+    _ffn_backward_inputs(fn, dims, dy, x, saved, ws)
     for name, t, like in (("dx", dx, x), ("dw_gate", dw_gate, w_gate), ("dw_up", dw_up, w_up), ("dw_down", dw_down, w_down)):
         if t is not None:
             _shape(fn, name, t, like.shape)
-    _same_dtype(fn, x, dy, *outs)
-    _same_device(fn, x, dy, saved, ws, *outs)
-    _cuda(dy, saved, ws, *outs)
-    code = _dtype_code(x)
-    if _bytes(saved) < im2win_gated_ffn_size(FFN_SAVED, R, C, F, code):
-        raise ValueError(f"{fn}: saved is too small")
-    _check(fn, lib().im2win_gated_ffn_backward(
-        _ptr(dy), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(saved), _ptr(dx), _ptr(dw_gate), _ptr(dw_up),
-        _ptr(dw_down), _ptr(ws), _bytes(ws), R, C, F, _code(ACTS, act, "act"), code, _stream(x)))
+            _same_dtype(fn, x, t)
+            _same_device(fn, x, t)
+            _cuda(t)
+    _ffn_backward(fn, dims, dy, x, w_gate, w_up, w_down, saved, dx, dw_gate, dw_up, dw_down, ws, act)
 
 
-def _ffn_buffer(buffer, x, w_gate):
-    C = x.shape[-1]
-    return _empty(im2win_gated_ffn_size(buffer, x.numel() // max(C, 1), C, w_gate.shape[0], _dtype_code(x)), x.device)
+def _ffn_buffer(buffer, dims, x):
+    return _empty(im2win_gated_ffn_size(buffer, *dims, _dtype_code(x)), x.device)
+
+
+def _ffn_forward(fn, x, w_gate, w_up, w_down, act, ws, out, saved, train):
+    dims = _ffn_shapes(fn, x, w_gate, w_up, w_down)
+    given = ws is not None or out is not None or saved is not None
+    if ws is None:
+        ws = _ffn_buffer(FFN_TRAIN if train else FFN_FORWARD, dims, x)
+    if saved is None and train:
+        saved = _ffn_buffer(FFN_SAVED, dims, x)
+    if out is None:
+        out = torch.empty_like(x)
+    if given:
+        _ffn_outputs(fn, dims, x, out, saved, ws)
+    _ffn(fn, dims, x, w_gate, w_up, w_down, out, saved, ws, act)
+    return out, saved
 
 
 def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, act: str = "silu",
               ws: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """Gated feed-forward block over the last axis of x[..., C]."""
-    _ffn_shapes("gated_ffn", x, w_gate, w_up, w_down)
-    if ws is None:
-        ws = _ffn_buffer(FFN_FORWARD, x, w_gate)
-    if out is None:
-        out = torch.empty_like(x)
-    im2win_gated_ffn(x, w_gate, w_up, w_down, out, None, ws, act)
-    return out
+    return _ffn_forward("gated_ffn", x, w_gate, w_up, w_down, act, ws, out, None, False)[0]
 
 
 def gated_ffn_train(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                     act: str = "silu", ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
                     saved: torch.Tensor | None = None):
     """gated_ffn() and the buffer its gated_ffn_backward() needs: (y, saved)."""
-    _ffn_shapes("gated_ffn_train", x, w_gate, w_up, w_down)
-    if ws is None:
-        ws = _ffn_buffer(FFN_TRAIN, x, w_gate)
-    if saved is None:
-        saved = _ffn_buffer(FFN_SAVED, x, w_gate)
-    if out is None:
-        out = torch.empty_like(x)
-    im2win_gated_ffn(x, w_gate, w_up, w_down, out, saved, ws, act)
-    return out, saved
+    return _ffn_forward("gated_ffn_train", x, w_gate, w_up, w_down, act, ws, out, saved, True)
 
 
 def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
@@ -146,12 +187,14 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
                        need_dx: bool = True, need_dw: bool = True):
     """(dx, dw_gate, dw_up, dw_down) of gated_ffn_train() at the same arguments;
     None for what is not needed."""
-    _ffn_shapes("gated_ffn_backward", x, w_gate, w_up, w_down)
+    fn = "gated_ffn_backward"
+    dims = _ffn_shapes(fn, x, w_gate, w_up, w_down)
     if ws is None:
-        ws = _ffn_buffer(FFN_BACKWARD, x, w_gate)
+        ws = _ffn_buffer(FFN_BACKWARD, dims, x)
+    _ffn_backward_inputs(fn, dims, dy, x, saved, ws)
     dx = torch.empty_like(x) if need_dx else None
     dws = [torch.empty_like(w) if need_dw else None for w in (w_gate, w_up, w_down)]
-    im2win_gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, dx, *dws, ws, act)
+    _ffn_backward(fn, dims, dy, x, w_gate, w_up, w_down, saved, dx, *dws, ws, act)
     return (dx, *dws)
 
 
@@ -159,47 +202,59 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
 _NORM_PARAMS = ("res_scale", "w_post", "b_post", "w_pre", "b_pre")
 
 
-def _norm_check(fn, x, y, gate, rows_per_gate, outs, params):
-    """(R, C, rows a gate) after the checks of a call's tensors; outs are
-    (name, tensor or None, shape)."""
+def _norm_check(fn, x, y, gate, rows_per_gate, rows, params):
+    """(R, C, rows a gate) after the checks of a call's tensors; rows are (name,
+    tensor or None) of x's shape, params the tensors of _NORM_PARAMS."""
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"{fn}: x must be [..., C]")
-    C = x.shape[-1]
+    shape = x.shape
+    C = shape[-1]
     R = x.numel() // C
-    if y is not None:
-        _shape(fn, "y", y, x.shape)
-    if gate is not None:
-        if rows_per_gate is None:
-            rows_per_gate = max(R, 1)
-        if rows_per_gate < 1:
-            raise ValueError(f"{fn}: rows_per_gate must be at least 1")
-        _shape(fn, "gate", gate, (-(-R // rows_per_gate), C))
-    else:
+    if gate is None or rows_per_gate is None:
         rows_per_gate = max(R, 1)
+    elif rows_per_gate < 1:
+        raise ValueError(f"{fn}: rows_per_gate must be at least 1")
+    if y is not None:
+        rows = (("y", y), *rows)
+    given = [t for _, t in rows if t is not None]
+    for t in given:
+        if t.shape != shape:
+            for name, v in rows:
+                if v is not None:
+                    _shape(fn, name, v, shape)
+    if gate is not None:
+        _shape(fn, "gate", gate, (-(-R // rows_per_gate), C))
+        given.append(gate)
     for name, t in zip(_NORM_PARAMS, params):
         if t is not None:
             _shape(fn, name, t, (C,))
-    for name, t, want in outs:
-        if t is not None:
-            _shape(fn, name, t, want)
-    given = [t for t in (x, y, gate, *params, *(t for _, t, _ in outs)) if t is not None]
-    _same_dtype(fn, *given)
-    _same_device(fn, *given)
-    _cuda(*given)
+            given.append(t)
+    if not _alike(x.dtype, x.get_device(), x, *given):
+        _same_dtype(fn, x, *given)
+        _same_device(fn, x, *given)
+        _cuda(x, *given)
     return R, C, rows_per_gate
+
+
+def _norm_args(dims, x, y, gate, res_scale, post, w_post, b_post, pre, w_pre, b_pre, eps):
+    return (x.data_ptr(), _ptr(y), _ptr(gate), dims[2], _ptr(res_scale), _code(NORMS, post, "post"), _ptr(w_post),
+            _ptr(b_post), _code(NORMS, pre, "pre"), _ptr(w_pre), _ptr(b_pre), eps)
+
+
+def _norm(fn, dims, args, x, r, n):
+    _check(fn, lib().im2win_residual_norm(*args, _ptr(r), _ptr(n), dims[0], dims[1], _dtype_code(x),
+                                          _stream(x.get_device())))
 
 
 def im2win_residual_norm(x, y, gate, rows_per_gate, res_scale, post, w_post, b_post, pre, w_pre, b_pre, eps, r,
                          n) -> None:
     """r = res_scale * x + gate * post(y), n = pre(r); None: absent."""
     fn = "im2win_residual_norm"
-    R, C, per = _norm_check(fn, x, y, gate, rows_per_gate, (("r", r, x.shape), ("n", n, x.shape)),
-                            (res_scale, w_post, b_post, w_pre, b_pre))
-    _check(fn, lib().im2win_residual_norm(
-        _ptr(x), _ptr(y), _ptr(gate), per, _ptr(res_scale), _code(NORMS, post, "post"), _ptr(w_post), _ptr(b_post),
-        _code(NORMS, pre, "pre"), _ptr(w_pre), _ptr(b_pre), eps, _ptr(r), _ptr(n), R, C, _dtype_code(x), _stream(x)))
+    dims = _norm_check(fn, x, y, gate, rows_per_gate, (("r", r), ("n", n)), (res_scale, w_post, b_post, w_pre, b_pre))
+    _norm(fn, dims, _norm_args(dims, x, y, gate, res_scale, post, w_post, b_post, pre, w_pre, b_pre, eps), x, r, n)
 
 
+@functools.lru_cache(maxsize=4096)
 def im2win_residual_norm_backward_size(R, C, rows_per_gate, dtype: int) -> int:
     out = ctypes.c_size_t(0)
     _check("im2win_residual_norm_backward_size",
@@ -207,23 +262,32 @@ def im2win_residual_norm_backward_size(R, C, rows_per_gate, dtype: int) -> int:
     return out.value
 
 
+def _norm_backward(fn, dims, args, dr, dn, x, grads, ws):
+    _check(fn, lib().im2win_residual_norm_backward(
+        _ptr(dr), _ptr(dn), *args, *[_ptr(t) for t in grads], ws.data_ptr(), _bytes(ws), dims[0], dims[1],
+        _dtype_code(x), _stream(x.get_device())))
+
+
 def im2win_residual_norm_backward(dr, dn, x, y, gate, rows_per_gate, res_scale, post, w_post, b_post, pre, w_pre,
                                   b_pre, eps, dx, dy, dgate, dres_scale, dw_post, db_post, dw_pre, db_pre, ws) -> None:
     """Gradients of im2win_residual_norm; None: an absent input, or a gradient not computed."""
     fn = "im2win_residual_norm_backward"
-    outs = [("dr", dr, x.shape), ("dn", dn, x.shape), ("dx", dx, x.shape), ("dy", dy, x.shape)]
-    if dgate is not None and gate is not None:
-        outs.append(("dgate", dgate, gate.shape))
-    outs += [(name, t, x.shape[-1:]) for name, t in (("dres_scale", dres_scale), ("dw_post", dw_post),
-                                                     ("db_post", db_post), ("dw_pre", dw_pre), ("db_pre", db_pre))]
-    R, C, per = _norm_check(fn, x, y, gate, rows_per_gate, outs, (res_scale, w_post, b_post, w_pre, b_pre))
+    dims = _norm_check(fn, x, y, gate, rows_per_gate, (("dr", dr), ("dn", dn), ("dx", dx), ("dy", dy)),
+                       (res_scale, w_post, b_post, w_pre, b_pre))
+    grads = (dx, dy, dgate, dres_scale, dw_post, db_post, dw_pre, db_pre)
+    for name, t, want in (("dgate", dgate, None if gate is None else gate.shape), ("dres_scale", dres_scale, dims[1:2]),
+                          ("dw_post", dw_post, dims[1:2]), ("db_post", db_post, dims[1:2]),
+                          ("dw_pre", dw_pre, dims[1:2]), ("db_pre", db_pre, dims[1:2])):
+        if t is not None:
+            if want is not None:
+                _shape(fn, name, t, want)
+            _same_dtype(fn, x, t)
+            _same_device(fn, x, t)
+            _cuda(t)
     _same_device(fn, x, ws)
     _cuda(ws)
-    _check(fn, lib().im2win_residual_norm_backward(
-        _ptr(dr), _ptr(dn), _ptr(x), _ptr(y), _ptr(gate), per, _ptr(res_scale), _code(NORMS, post, "post"),
-        _ptr(w_post), _ptr(b_post), _code(NORMS, pre, "pre"), _ptr(w_pre), _ptr(b_pre), eps, _ptr(dx), _ptr(dy),
-        _ptr(dgate), _ptr(dres_scale), _ptr(dw_post), _ptr(db_post), _ptr(dw_pre), _ptr(db_pre), _ptr(ws), _bytes(ws),
-        R, C, _dtype_code(x), _stream(x)))
+    _norm_backward(fn, dims, _norm_args(dims, x, y, gate, res_scale, post, w_post, b_post, pre, w_pre, b_pre, eps), dr,
+                   dn, x, grads, ws)
 
 
 def residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post: str = "none", w_post=None, b_post=None,
@@ -232,9 +296,11 @@ def residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post: str =
     """(r, n) of r = res_scale * x + gate * post(y), n = pre(r) over the last
     axis; n is None where pre is "none". gate[i] belongs to rows_per_gate
     consecutive rows (None: all rows). y None: r = res_scale * x."""
+    fn = "residual_norm"
+    dims = _norm_check(fn, x, y, gate, rows_per_gate, (), (res_scale, w_post, b_post, w_pre, b_pre))
     r = torch.empty_like(x)
     n = torch.empty_like(x) if pre != "none" else None
-    im2win_residual_norm(x, y, gate, rows_per_gate, res_scale, post, w_post, b_post, pre, w_pre, b_pre, eps, r, n)
+    _norm(fn, dims, _norm_args(dims, x, y, gate, res_scale, post, w_post, b_post, pre, w_pre, b_pre, eps), x, r, n)
     return r, n
 
 
@@ -245,15 +311,17 @@ def residual_norm_backward(dr, dn, x: torch.Tensor, y: torch.Tensor | None = Non
     """Gradients of residual_norm() at the same arguments, as a dict of dx, dy,
     dgate, dres_scale, dw_post, db_post, dw_pre, db_pre (None for an absent input)."""
     fn = "residual_norm_backward"
-    R, C, per = _norm_check(fn, x, y, gate, rows_per_gate, (("dr", dr, x.shape), ("dn", dn, x.shape)),
-                            (res_scale, w_post, b_post, w_pre, b_pre))
+    dims = _norm_check(fn, x, y, gate, rows_per_gate, (("dr", dr), ("dn", dn)), (res_scale, w_post, b_post, w_pre, b_pre))
     if ws is None:
-        ws = _empty(im2win_residual_norm_backward_size(R, C, per, _dtype_code(x)), x.device)
+        ws = _empty(im2win_residual_norm_backward_size(*dims, _dtype_code(x)), x.device)
+    else:
+        _same_device(fn, x, ws)
+        _cuda(ws)
     like = dict(dx=x, dy=y, dgate=gate, dres_scale=res_scale, dw_post=w_post, db_post=b_post, dw_pre=w_pre,
                 db_pre=b_pre)
     out = {k: None if v is None else torch.empty_like(v) for k, v in like.items()}
-    im2win_residual_norm_backward(dr, dn, x, y, gate, rows_per_gate, res_scale, post, w_post, b_post, pre, w_pre,
-                                  b_pre, eps, *out.values(), ws)
+    _norm_backward(fn, dims, _norm_args(dims, x, y, gate, res_scale, post, w_post, b_post, pre, w_pre, b_pre, eps), dr,
+                   dn, x, out.values(), ws)
     return out
 
 
@@ -265,37 +333,60 @@ def im2win_clip_grad_norm_size(sizes) -> int:
     return out.value
 
 
+def _clip_check(fn, grads, outs, device: int):
+    """The gradients' dtype codes after the checks of the lists."""
+    given = grads
+    if outs is not None and outs is not grads:
+        if len(outs) != len(grads):
+            raise ValueError(f"{fn}: {len(outs)} outputs for {len(grads)} gradients")
+        if [t.shape for t in outs] != [t.shape for t in grads] or [t.dtype for t in outs] != [t.dtype for t in grads]:
+            for i, (g, o) in enumerate(zip(grads, outs)):
+                _shape(fn, f"outs[{i}]", o, g.shape)
+                _same_dtype(fn, g, o)
+        given = grads + outs
+    if device < 0 or not all([t.get_device() == device and t.is_contiguous() for t in given]):
+        _cuda(*given)
+        _same_device(fn, *given)
+        raise ValueError(f"{fn}: every tensor must be on one device")
+    return [_dtype_code(t) for t in grads]
+
+
+def _clip(fn, grads, outs, sizes, codes, max_norm, eps, norm, ws):
+    k = len(grads)
+    pointers, counts, types = ctypes.c_void_p * k, ctypes.c_int64 * k, ctypes.c_int * k
+    at = pointers(*[t.data_ptr() for t in grads])
+    to = None if outs is None else at if outs is grads else pointers(*[t.data_ptr() for t in outs])
+    _check(fn, lib().im2win_clip_grad_norm(at, to, counts(*sizes), types(*codes), k, max_norm, eps, norm.data_ptr(),
+                                           ws.data_ptr(), _bytes(ws), _stream(norm.get_device())))
+
+
 def im2win_clip_grad_norm(grads, outs, max_norm: float, eps: float, norm, ws) -> None:
     """*norm = the gradients' global 2-norm; outs[i] = grads[i] * min(1, max_norm / (norm + eps)); outs None: the
     norm alone."""
     fn = "im2win_clip_grad_norm"
     grads = list(grads)
     outs = None if outs is None else list(outs)
-    if outs is not None:
-        if len(outs) != len(grads):
-            raise ValueError(f"{fn}: {len(outs)} outputs for {len(grads)} gradients")
-        for i, (g, o) in enumerate(zip(grads, outs)):
-            if o is not g:
-                _shape(fn, f"outs[{i}]", o, g.shape)
-                _same_dtype(fn, g, o)
     if norm.dtype != torch.float32 or norm.numel() != 1:
         raise ValueError(f"{fn}: norm must be one float32")
-    given = grads + (outs or [])
-    _same_device(fn, norm, ws, *given)
-    _cuda(norm, ws, *given)
-    k = len(grads)
-    vps, i64s, ints = ctypes.c_void_p * k, ctypes.c_int64 * k, ctypes.c_int * k
-    _check(fn, lib().im2win_clip_grad_norm(
-        vps(*[g.data_ptr() for g in grads]), None if outs is None else vps(*[o.data_ptr() for o in outs]),
-        i64s(*[g.numel() for g in grads]), ints(*[_dtype_code(g) for g in grads]), k, max_norm, eps, _ptr(norm), _ptr(ws),
-        _bytes(ws), _stream(norm)))
+    _same_device(fn, norm, ws)
+    _cuda(norm, ws)
+    codes = _clip_check(fn, grads, outs, norm.get_device())
+    _clip(fn, grads, outs, [t.numel() for t in grads], codes, max_norm, eps, norm, ws)
 
 
-def _clip(grads, outs, max_norm, eps, ws, device):
+def _clip_lists(fn, grads, outs, max_norm, eps, ws):
+    if not grads:
+        raise ValueError(f"{fn}: no gradients")
+    codes = _clip_check(fn, grads, outs, grads[0].get_device())
+    sizes = [t.numel() for t in grads]
+    device = grads[0].device
     if ws is None:
-        ws = _empty(im2win_clip_grad_norm_size([g.numel() for g in grads]), device)
+        ws = _empty(im2win_clip_grad_norm_size(sizes), device)
+    else:
+        _same_device(fn, grads[0], ws)
+        _cuda(ws)
     norm = torch.empty((), dtype=torch.float32, device=device)
-    im2win_clip_grad_norm(grads, outs, max_norm, eps, norm, ws)
+    _clip(fn, grads, outs, sizes, codes, max_norm, eps, norm, ws)
     return norm
 
 
@@ -303,14 +394,9 @@ def clip_grad_norm(grads, max_norm: float, outs=None, eps: float = 1e-6, ws: tor
     """Scale the gradients by min(1, max_norm / (norm + eps)), in place or into
     `outs`, and return their global 2-norm (a float32 scalar on the device)."""
     grads = list(grads)
-    if not grads:
-        raise ValueError("clip_grad_norm: no gradients")
-    return _clip(grads, grads if outs is None else list(outs), max_norm, eps, ws, grads[0].device)
+    return _clip_lists("clip_grad_norm", grads, grads if outs is None else list(outs), max_norm, eps, ws)
 
 
 def grad_norm(grads, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Global 2-norm of the gradients (a float32 scalar on the device)."""
-    grads = list(grads)
-    if not grads:
-        raise ValueError("grad_norm: no gradients")
-    return _clip(grads, None, 0.0, 0.0, ws, grads[0].device)
+    return _clip_lists("grad_norm", list(grads), None, 0.0, 0.0, ws)

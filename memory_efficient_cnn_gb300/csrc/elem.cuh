@@ -58,40 +58,85 @@ inline bool with_dtype(int dtype, Fn f) {
 inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // ---- activations of the gated feed-forward, and their derivatives at g
+//
+// FAST is for results that are rounded to 16 bits: exponentials and quotients by
+// the hardware's approximations (about 1e-6 off, a five-hundredth of fp16's
+// rounding), and the normal distribution's tail by the polynomial below. With
+// them the epilogues of the products no longer cost more than the products:
+// gelu over 200704 x 512 hidden values took 221 us with erff and expf.
 
-__device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
+template <bool FAST>
+__device__ __forceinline__ float exp_f32(float v) {
+    return FAST ? __expf(v) : expf(v);
+}
+template <bool FAST>
+__device__ __forceinline__ float recip_f32(float v) {
+    return FAST ? __fdividef(1.0f, v) : 1.0f / v;
+}
+template <bool FAST>
+__device__ __forceinline__ float sigmoid_f32(float g) {
+    return recip_f32<FAST>(1.0f + exp_f32<FAST>(-g));
+}
 
-template <int ACT>
+// The standard normal distribution at g, and its density.
+// FAST: erfc(z) = t P(t) exp(-z^2), t = 1 / (1 + 0.38 z), the form of Hastings'
+// rational approximations (Abramowitz and Stegun, 7.1.23 to 7.1.28), with a P of
+// degree 6 fitted here by minimax least squares over 0 <= z <= 12: relative error
+// at most 1.04e-6, also in the tail.
+template <bool FAST>
+__device__ __forceinline__ float normal_cdf(float g, float &density) {
+    const float e = exp_f32<FAST>(-0.5f * g * g);
+    density = e * 0.39894228040143268f;
+    if (!FAST) return 0.5f * erfcf(-0.70710678118654752f * g);
+    const float t = recip_f32<FAST>(fmaf(0.38f * 0.70710678118654752f, fabsf(g), 1.0f));
+    float q = -0.12541769670848360f;
+    q = fmaf(q, t, 0.33603686314665066f);
+    q = fmaf(q, t, -0.06991412938979578f);
+    q = fmaf(q, t, 0.24783511846747405f);
+    q = fmaf(q, t, 0.18059404117089478f);
+    q = fmaf(q, t, 0.21657745820323432f);
+    q = fmaf(q, t, 0.21428731011020574f);
+    const float tail = 0.5f * q * t * e;
+    return g < 0.0f ? tail : 1.0f - tail;
+}
+
+// Twice the argument of gelu_tanh's tanh: (1 + tanh z) / 2 is the sigmoid of 2 z.
+__device__ __forceinline__ float gelu_tanh_arg(float g) { return 1.5957691216057307f * (g + 0.044715f * g * g * g); }
+
+template <int ACT, bool FAST>
 __device__ __forceinline__ float act_value(float g) {
-    if (ACT == IM2WIN_ACT_SILU) return g * sigmoid_f32(g);
-    if (ACT == IM2WIN_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
-    if (ACT == IM2WIN_ACT_GELU_TANH)
-        return 0.5f * g * (1.0f + tanhf(0.79788456080286536f * (g + 0.044715f * g * g * g)));
+    if (ACT == IM2WIN_ACT_SILU) return g * sigmoid_f32<FAST>(g);
+    if (ACT == IM2WIN_ACT_GELU) {
+        float density;
+        return g * normal_cdf<FAST>(g, density);
+    }
+    if (ACT == IM2WIN_ACT_GELU_TANH) return g * sigmoid_f32<FAST>(gelu_tanh_arg(g));
     if (ACT == IM2WIN_ACT_RELU) return g > 0.0f ? g : (g != g ? g : 0.0f);
-    return sigmoid_f32(g);
+    return sigmoid_f32<FAST>(g);
 }
 
 // a = act(g), d = act'(g)
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ void act_both(float g, float &a, float &d) {
     if (ACT == IM2WIN_ACT_SILU) {
-        const float p = sigmoid_f32(g);
+        const float p = sigmoid_f32<FAST>(g);
         a = g * p;
-        d = p + a * (1.0f - p);
+        d = fmaf(a, 1.0f - p, p);
     } else if (ACT == IM2WIN_ACT_GELU) {
-        const float cdf = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
-        a = g * cdf;
-        d = cdf + g * expf(-0.5f * g * g) * 0.39894228040143268f;
+        float density;
+        const float p = normal_cdf<FAST>(g, density);
+        a = g * p;
+        d = fmaf(g, density, p);
     } else if (ACT == IM2WIN_ACT_GELU_TANH) {
-        const float t = tanhf(0.79788456080286536f * (g + 0.044715f * g * g * g));
-        a = 0.5f * g * (1.0f + t);
-        d = 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * 0.79788456080286536f *
-                                      (1.0f + 0.134145f * fminf(g * g, 1e38f));  // (bounded: 0 times it stays 0)
+        const float p = sigmoid_f32<FAST>(gelu_tanh_arg(g));
+        a = g * p;
+        // (g^2 is bounded, so that 0 times it stays 0)
+        d = fmaf(a * (1.0f - p), 1.5957691216057307f * fmaf(0.134145f, fminf(g * g, 1e38f), 1.0f), p);
     } else if (ACT == IM2WIN_ACT_RELU) {
-        a = act_value<IM2WIN_ACT_RELU>(g);
+        a = act_value<IM2WIN_ACT_RELU, FAST>(g);
         d = g > 0.0f ? 1.0f : 0.0f;
     } else {
-        a = sigmoid_f32(g);
+        a = sigmoid_f32<FAST>(g);
         d = a * (1.0f - a);
     }
 }

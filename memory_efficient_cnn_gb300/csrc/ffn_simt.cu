@@ -69,11 +69,11 @@ __global__ void __launch_bounds__(THREADS) simt_product(Product p, int tiles_n) 
                 *out = from_f32<T>(acc[0][i][j]);
             } else if (EPI == EPI_GATED) {
                 const float g = acc[0][i][j], u = acc[NB - 1][i][j];
-                *out = from_f32<T>(act_value<ACT>(g) * u);
+                *out = from_f32<T>(act_value<ACT, sizeof(T) == 2>(g) * u);
                 if (p.g) p.g[at] = g, p.u[at] = u;
             } else {
                 float a, d;
-                act_both<ACT>(p.g[at], a, d);
+                act_both<ACT, sizeof(T) == 2>(p.g[at], a, d);
                 *out = from_f32<T>(acc[0][i][j] * p.u[at] * d);
                 static_cast<T *>(p.out2)[(int64_t)m * p.ldo + n] = from_f32<T>(acc[0][i][j] * a);
             }

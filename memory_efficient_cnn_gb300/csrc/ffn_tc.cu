@@ -213,7 +213,7 @@ __device__ __forceinline__ void store_row32(uint16_t *dst, const float (&v)[32],
 __device__ __forceinline__ void gate32(int act, const float (&g)[32], const float (&u)[32], float (&h)[32]) {
     auto each = [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) h[i] = act_value<decltype(a)::value>(g[i]) * u[i];
+        for (int i = 0; i < 32; ++i) h[i] = act_value<decltype(a)::value, true>(g[i]) * u[i];
     };
     with_act_device(act, each);
 }
@@ -224,7 +224,7 @@ __device__ __forceinline__ void dgate_n(int act, const float (&dh)[N], float (&g
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float v, d;
-            act_both<decltype(a)::value>(g[i], v, d);
+            act_both<decltype(a)::value, true>(g[i], v, d);
             g[i] = dh[i] * u[i] * d;
             u[i] = dh[i] * v;
         }
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams 
         float h[4];
         with_act_device(p.act, [&](auto a) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = act_value<decltype(a)::value>(v[i]) * u[i];
+            for (int i = 0; i < 4; ++i) h[i] = act_value<decltype(a)::value, true>(v[i]) * u[i];
         });
         put(out, h);
     } else {
@@ -621,10 +621,8 @@ TcPlan plan_tc(const Product &d) {
         } else {
             pl.units = (int)std::min<int64_t>(most, std::max<int64_t>(1, total / 4));  // 4 blocks at least
             if (tiles > 8 * pl.units || tiles % pl.units == 0) continue;  // (nearly) even without it
-            int64_t slots = 1;
-            for (int64_t t = 0; t < tiles; ++t)
-                slots = std::max<int64_t>(slots, stream_unit(total, pl.units, (t + 1) * KT - 1) -
-                                                     stream_unit(total, pl.units, t * KT) + 1);
+            // a tile meets at most this many runs of at least floor(total / units) blocks
+            const int64_t slots = (KT - 1) / (total / pl.units) + 2;
             pl.slots = (int)slots;
             pl.part_ld = (int64_t)pl.tiles_n * pl.bn;
             pl.part_step = (int64_t)z * d.M * pl.part_ld;
