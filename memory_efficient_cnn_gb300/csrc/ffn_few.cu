@@ -149,7 +149,11 @@ __global__ void __launch_bounds__(THREADS) few_mma(const __grid_constant__ FewPa
         T *out = static_cast<T *>(p.out) + (int64_t)m * p.ldo + n;
         if (GATED) {
             float h = 0.0f;
-            with_act_device(p.act, [&](auto a) { h = act_value<decltype(a)::value, true>(v[0]) * v[NW - 1]; });
+            with_act_device(p.act, [&](auto a) {
+                float unused;
+                split(act_value2<decltype(a)::value>(f2(v[0])), h, unused);
+            });
+            h *= v[NW - 1];
             const T hi = from_f32<T>(h);
             const float rest = h - to_f32(hi);
             *out = hi;  // (the remainder of an infinite rounding is none)
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(THREADS) few_fma(const __grid_constant__ FewPa
     float *out = static_cast<float *>(p.out) + (int64_t)m * p.ldo + n;
     if (GATED) {
         float h = 0.0f;
-        with_act_device(p.act, [&](auto a) { h = act_value<decltype(a)::value, false>(v[0]) * v[NW - 1]; });
+        with_act_device(p.act, [&](auto a) { h = act_value<decltype(a)::value>(v[0]) * v[NW - 1]; });
         *out = h;
         if (p.g) p.g[kept_index(m, n, p.N)] = v[0], p.u[kept_index(m, n, p.N)] = v[NW - 1];
     } else {

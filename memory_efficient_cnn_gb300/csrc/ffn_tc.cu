@@ -3,7 +3,7 @@
 //
 // One persistent warp-specialised kernel computes D = A B^T tile by tile: one
 // thread issues TMA copies of 64 steps of K into a ring of shared-memory stages,
-// one issues tcgen05.mma on them, eight warps turn finished accumulators into
+// one issues tcgen05.mma on them, sixteen warps turn finished accumulators into
 // outputs while the next tile accumulates in the other half of tensor memory.
 // Operands may be stored with K or with the output index innermost (the backward
 // products read every matrix as it lies): both are 128-byte-swizzled layouts
@@ -33,7 +33,7 @@ using namespace im2win::tc;
 
 constexpr int BK = 64;           // K steps of one stage: 128 bytes
 constexpr int ROWS = 128;        // rows of A a CTA stages (its TMEM lanes)
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16;
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 
 template <int CG, int BN>
@@ -78,8 +78,8 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+__device__ __forceinline__ void arrive_relaxed(uint32_t addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
@@ -190,95 +190,97 @@ struct Walk {
     }
 };
 
-// 32 consecutive outputs of one row from fp32, guarded by `n` valid ones.
-__device__ __forceinline__ void store_row32(uint16_t *dst, const float (&v)[32], int n, bool vec, int bf16) {
-    if (vec && n >= 32) {
+// N consecutive outputs of one row from fp32, `n` of them valid.
+template <int N>
+__device__ __forceinline__ void store_row(uint16_t *dst, const F2 (&v)[N / 2], int n, bool vec, int bf16) {
+    uint32_t w[N / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint4 q;
-            q.x = pack2(v[8 * i], v[8 * i + 1], bf16);
-            q.y = pack2(v[8 * i + 2], v[8 * i + 3], bf16);
-            q.z = pack2(v[8 * i + 4], v[8 * i + 5], bf16);
-            q.w = pack2(v[8 * i + 6], v[8 * i + 7], bf16);
-            reinterpret_cast<uint4 *>(dst)[i] = q;
-        }
+    for (int i = 0; i < N / 2; ++i) {
+        float lo, hi;
+        split(v[i], lo, hi);
+        w[i] = pack2(lo, hi, bf16);
+    }
+    if (vec && n >= N) {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) dst[i] = cvt16(v[i], bf16);
+        for (int i = 0; i < N; ++i)
+            if (i < n) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
     }
 }
 
-// h = act(g) * u of 32 elements; the activation is chosen once for all of them.
-__device__ __forceinline__ void gate32(int act, const float (&g)[32], const float (&u)[32], float (&h)[32]) {
-    auto each = [&](auto a) {
+// g -> h = act(g) * u; the activation is chosen once for all N values.
+template <int N>
+__device__ __forceinline__ void gate_values(int act, F2 (&g)[N / 2], const F2 (&u)[N / 2]) {
+    with_act_device(act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) h[i] = act_value<decltype(a)::value, true>(g[i]) * u[i];
-    };
-    with_act_device(act, each);
+        for (int i = 0; i < N / 2; ++i) g[i] = mul2(act_value2<decltype(a)::value>(g[i]), u[i]);
+    });
 }
 // dh and g, u -> dg, du (in g and u).
 template <int N>
-__device__ __forceinline__ void dgate_n(int act, const float (&dh)[N], float (&g)[N], float (&u)[N]) {
-    auto each = [&](auto a) {
+__device__ __forceinline__ void dgate_values(int act, const F2 (&dh)[N / 2], F2 (&g)[N / 2], F2 (&u)[N / 2]) {
+    with_act_device(act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float v, d;
-            act_both<decltype(a)::value, true>(g[i], v, d);
-            g[i] = dh[i] * u[i] * d;
-            u[i] = dh[i] * v;
+        for (int i = 0; i < N / 2; ++i) {
+            F2 v, d;
+            act_both2<decltype(a)::value>(g[i], v, d);
+            g[i] = mul2(mul2(dh[i], u[i]), d);
+            u[i] = mul2(dh[i], v);
         }
-    };
-    with_act_device(act, each);
+    });
 }
 
-__device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    tmem_ld32(taddr, r);
-    tmem_wait_ld();
+// Kept values of N columns of row m, `n` of them valid, to and from pairs.
+template <int N>
+__device__ __forceinline__ void keep(float *kept, int64_t at, const F2 (&v)[N / 2], int n) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < N / 4; ++i)
+        if (4 * i < n) *reinterpret_cast<ulonglong2 *>(kept + at + i * 128) = make_ulonglong2(v[2 * i].v, v[2 * i + 1].v);
 }
-
-// Accumulator columns [c, c + 32) (GATED: of the gate half) of row m, output columns from n.
-template <int BN, int EPI>
-__device__ __forceinline__ void epilogue32(const TcParams &p, uint32_t taddr, int c, int m, int n, uint16_t *out) {
-    float v[32];
-    load32(taddr + c, v);
-    const int left = m < p.M ? p.N - n : 0;
-    if (EPI == EPI_STORE) {
-        if (left > 0) store_row32(out + (int64_t)m * p.ldo + n, v, left, p.vec, p.bf16);
-    } else if (EPI == EPI_GATED) {
-        float u[32], h[32];
-        load32(taddr + BN / 2 + c, u);
-        if (left <= 0) return;
-        gate32(p.act, v, u, h);
-        store_row32(out + (int64_t)m * p.ldo + n, h, left, p.vec, p.bf16);
-        if (p.g) {
+template <int N>
+__device__ __forceinline__ void kept_values(const float *kept, int64_t at, F2 (&v)[N / 2], int n) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (4 * i >= left) break;
-                const int64_t at = kept_index(m, n + 4 * i, p.N);
-                *reinterpret_cast<float4 *>(p.g + at) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                *reinterpret_cast<float4 *>(p.u + at) = make_float4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
-            }
-        }
-    } else {
-        if (left <= 0) return;
-        float g[32], u[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t at = kept_index(m, n + 4 * i, p.N);
-            const bool in = 4 * i < left;
-            const float4 a = in ? *reinterpret_cast<const float4 *>(p.g + at) : make_float4(0, 0, 0, 0);
-            const float4 b = in ? *reinterpret_cast<const float4 *>(p.u + at) : make_float4(0, 0, 0, 0);
-            g[4 * i] = a.x, g[4 * i + 1] = a.y, g[4 * i + 2] = a.z, g[4 * i + 3] = a.w;
-            u[4 * i] = b.x, u[4 * i + 1] = b.y, u[4 * i + 2] = b.z, u[4 * i + 3] = b.w;
-        }
-        dgate_n<32>(p.act, v, g, u);
-        store_row32(out + (int64_t)m * p.ldo + n, g, left, p.vec, p.bf16);
-        store_row32(static_cast<uint16_t *>(p.out2) + (int64_t)m * p.ldo + n, u, left, p.vec, p.bf16);
+    for (int i = 0; i < N / 4; ++i) {
+        const ulonglong2 q =
+            4 * i < n ? *reinterpret_cast<const ulonglong2 *>(kept + at + i * 128) : make_ulonglong2(0, 0);
+        v[2 * i].v = q.x, v[2 * i + 1].v = q.y;
     }
+}
+
+constexpr int CHUNK = 16;  // accumulator columns a warp turns into outputs at a time
+
+__device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[CHUNK]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void pairs_of(const uint32_t (&r)[CHUNK], F2 (&v)[CHUNK / 2]) {
+#pragma unroll
+    for (int i = 0; i < CHUNK / 2; ++i) v[i] = f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+
+// Outputs of a chunk of row m from its accumulator values v (and u), columns from n.
+template <int EPI>
+__device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[CHUNK / 2], F2 (&u)[CHUNK / 2], int m, int n,
+                                             uint16_t *out) {
+    const int left = m < p.M ? p.N - n : 0;
+    if (left <= 0) return;
+    const int64_t at = (int64_t)m * p.ldo + n;
+    if (EPI == EPI_GATED) {
+        if (p.g) {
+            keep<CHUNK>(p.g, kept_index(m, n, p.N), v, left);
+            keep<CHUNK>(p.u, kept_index(m, n, p.N), u, left);
+        }
+        gate_values<CHUNK>(p.act, v, u);
+    } else if (EPI == EPI_DGATED) {
+        F2 g[CHUNK / 2];
+        kept_values<CHUNK>(p.g, kept_index(m, n, p.N), g, left);
+        kept_values<CHUNK>(p.u, kept_index(m, n, p.N), u, left);
+        dgate_values<CHUNK>(p.act, v, g, u);
+        store_row<CHUNK>(out + at, g, left, p.vec, p.bf16);
+        store_row<CHUNK>(static_cast<uint16_t *>(p.out2) + at, u, left, p.vec, p.bf16);
+        return;
+    }
+    store_row<CHUNK>(out + at, v, left, p.vec, p.bf16);
 }
 
 enum Site : uint32_t { SITE_STAGE_FULL = 32, SITE_STAGE_EMPTY, SITE_ACC_FULL, SITE_ACC_EMPTY };
@@ -407,48 +409,58 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
             while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
         }
     } else if (warp >= 4) {
-        // ---- outputs
+        // ---- outputs: a warp for 32 rows and a share of the columns
         Walk walk(p, unit, units);
         Work w;
         int n_tile = 0;
-        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int q = warp & 3, share = (warp - 4) >> 2;
+        constexpr int SHARES = EPI_WARPS / 4;
         constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;  // output columns of a tile
-        constexpr int BEGIN_STEP = BN / 2;                    // accumulator columns of half the warps
         const uint32_t empty_bar0 = CG == 2 ? map_rank(acc_empty, 0) : acc_empty;
         while (walk.next(w)) {
             const int buf = n_tile & 1;
             if (!warp_bar_wait(acc_full + 8 * buf, (n_tile >> 1) & 1, ctl, SITE_ACC_FULL)) break;
             tc_fence_after();
             const uint32_t taddr = tmem + buf * BN + ((uint32_t)(q * 32) << 16);
-            const int row0 = w.tm * T::M + (int)rank * ROWS + q * 32, m = row0 + lane;
-            if (row0 < p.M) {
-                if (p.part) {
-                    float *dst = p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
+            const int m = w.tm * T::M + (int)rank * ROWS + q * 32 + lane;
+            // Once the warp's last accumulator column is in registers the MMAs may have the
+            // buffer; the arrival orders no memory but the loads, which are done, so it need not
+            // wait for the stores under way.
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_relaxed(empty_bar0 + 8 * buf);
+            };
+            if (p.part) {
+                constexpr int SPAN = BN / SHARES;
+                float *dst = p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
+#pragma unroll 1
+                for (int c = share * SPAN; c < (share + 1) * SPAN; c += CHUNK) {
+                    uint32_t r[CHUNK];
+                    load_chunk(taddr + c, r);
+                    tmem_wait_ld();
+                    if (c + CHUNK == (share + 1) * SPAN) release();
+                    if (m < p.M) {
 #pragma unroll
-                    for (int c = half * BEGIN_STEP; c < (half + 1) * BEGIN_STEP; c += 32) {
-                        float v[32];
-                        load32(taddr + c, v);
-                        if (m < p.M) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                reinterpret_cast<float4 *>(dst + c)[i] =
-                                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        }
-                    }
-                } else {
-                    uint16_t *out = static_cast<uint16_t *>(w.z ? p.out2 : p.out);
-#pragma unroll
-                    for (int c = half * (COLS / 2); c < (half + 1) * (COLS / 2); c += 32) {
-                        const int n = w.tn * COLS + c;
-                        if (n < p.N) epilogue32<BN, EPI>(p, taddr, c, m, n, out);
+                        for (int i = 0; i < CHUNK / 4; ++i)
+                            reinterpret_cast<uint4 *>(dst + c)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
                     }
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2) arrive_cluster(empty_bar0 + 8 * buf);
-                else mbar_arrive(acc_empty + 8 * buf);
+            } else {
+                constexpr int SPAN = COLS / SHARES;
+                uint16_t *out = static_cast<uint16_t *>(w.z ? p.out2 : p.out);
+#pragma unroll 1
+                for (int c = share * SPAN; c < (share + 1) * SPAN; c += CHUNK) {
+                    uint32_t r[CHUNK], ru[CHUNK];
+                    load_chunk(taddr + c, r);
+                    if (EPI == EPI_GATED) load_chunk(taddr + BN / 2 + c, ru);
+                    tmem_wait_ld();
+                    if (c + CHUNK == (share + 1) * SPAN) release();
+                    F2 v[CHUNK / 2], u[CHUNK / 2];
+                    pairs_of(r, v);
+                    if (EPI == EPI_GATED) pairs_of(ru, u);
+                    finish_chunk<EPI>(p, v, u, m, w.tn * COLS + c, out);
+                }
             }
             ++n_tile;
         }
@@ -481,47 +493,46 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams 
     const int64_t total = (int64_t)p.tiles * KT;
     const int count = stream_unit(total, units, (int64_t)(t + 1) * KT - 1) - stream_unit(total, units, (int64_t)t * KT) + 1;
     const float *src = p.part + zm * p.part_ld + (int64_t)tn * BN + (n - tn * COLS);
-    float v[4] = {}, u[4] = {};
+    F2 v[2] = {f2(0.0f), f2(0.0f)}, u[2] = {f2(0.0f), f2(0.0f)};
+    auto add = [](F2(&sum)[2], const float *from) {
+        const float4 a = *reinterpret_cast<const float4 *>(from);
+        sum[0] = add2(sum[0], f2(a.x, a.y)), sum[1] = add2(sum[1], f2(a.z, a.w));
+    };
 #pragma unroll 4
     for (int j = 0; j < count; ++j) {
-        const float4 a = *reinterpret_cast<const float4 *>(src + j * p.part_step);
-        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-        if (EPI == EPI_GATED) {
-            const float4 b = *reinterpret_cast<const float4 *>(src + j * p.part_step + BN / 2);
-            u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
-        }
+        add(v, src + j * p.part_step);
+        if (EPI == EPI_GATED) add(u, src + j * p.part_step + BN / 2);
     }
     const int left = min(4, p.N - n);
     const int64_t at = (int64_t)m * p.ldo + n;
     uint16_t *out = static_cast<uint16_t *>(z ? p.out2 : p.out) + at;
-    auto put = [&](uint16_t *dst, const float (&r)[4]) {
+    auto put = [&](uint16_t *dst, const F2(&r)[2]) {
+        float a, b, c, d;
+        split(r[0], a, b);
+        split(r[1], c, d);
+        const uint32_t lo = pack2(a, b, p.bf16), hi = pack2(c, d, p.bf16);
         if (p.vec && left == 4) {
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(r[0], r[1], p.bf16), pack2(r[2], r[3], p.bf16));
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
         } else {
-            for (int i = 0; i < left; ++i) dst[i] = cvt16(r[i], p.bf16);
+            for (int i = 0; i < left; ++i) dst[i] = (uint16_t)((i < 2 ? lo : hi) >> (16 * (i & 1)));
         }
     };
-    if (EPI == EPI_STORE) {
-        put(out, v);
-    } else if (EPI == EPI_GATED) {
+    if (EPI == EPI_GATED) {
         if (p.g) {
-            *reinterpret_cast<float4 *>(p.g + kept_index(m, n, p.N)) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(p.u + kept_index(m, n, p.N)) = make_float4(u[0], u[1], u[2], u[3]);
+            keep<4>(p.g, kept_index(m, n, p.N), v, left);
+            keep<4>(p.u, kept_index(m, n, p.N), u, left);
         }
-        float h[4];
-        with_act_device(p.act, [&](auto a) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = act_value<decltype(a)::value, true>(v[i]) * u[i];
-        });
-        put(out, h);
-    } else {
-        const float4 ga = *reinterpret_cast<const float4 *>(p.g + kept_index(m, n, p.N));
-        const float4 ua = *reinterpret_cast<const float4 *>(p.u + kept_index(m, n, p.N));
-        float g[4] = {ga.x, ga.y, ga.z, ga.w}, uu[4] = {ua.x, ua.y, ua.z, ua.w};
-        dgate_n<4>(p.act, v, g, uu);
+        gate_values<4>(p.act, v, u);
+    } else if (EPI == EPI_DGATED) {
+        F2 g[2];
+        kept_values<4>(p.g, kept_index(m, n, p.N), g, left);
+        kept_values<4>(p.u, kept_index(m, n, p.N), u, left);
+        dgate_values<4>(p.act, v, g, u);
         put(out, g);
-        put(static_cast<uint16_t *>(p.out2) + at, uu);
+        put(static_cast<uint16_t *>(p.out2) + at, u);
+        return;
     }
+    put(out, v);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {

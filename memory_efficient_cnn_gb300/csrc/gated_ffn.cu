@@ -196,10 +196,10 @@ struct Sequence {
             Product one = p;
             one.batch = false;
             if (p.batch) one.a1 = one.b1 = Operand();
-            if (e == cudaSuccess) e = launch_simt(one, q.dtype, st);
+            if (e == cudaSuccess) e = launch_simt(one, st);
             if (p.batch && e == cudaSuccess) {
                 one.a0 = p.a1, one.b0 = p.b1, one.out = p.out2;
-                e = launch_simt(one, q.dtype, st);
+                e = launch_simt(one, st);
             }
         }
         cleared = true;

@@ -53,8 +53,8 @@ struct Product {
     int64_t ldo = 0;                   // row pitch of out and out2 in elements
 };
 
-// CUDA cores: any type, shape and alignment (no batch).
-cudaError_t launch_simt(const Product &p, int dtype, cudaStream_t st);
+// CUDA cores, fp32 (no batch).
+cudaError_t launch_simt(const Product &p, cudaStream_t st);
 
 // Tensor cores: fp16/bf16; operands 16-byte aligned with pitches that are multiples
 // of 8 elements. A product takes part_bytes of scratch. status: the workspace's
