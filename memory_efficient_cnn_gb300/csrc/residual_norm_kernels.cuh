@@ -217,39 +217,126 @@ __global__ void __launch_bounds__(256) join_partials(const float *part, int64_t 
 // statistics are reductions over registers (two passes for LAYER: the second
 // moment is taken about the mean). Thread t holds vectors t, t + TPR, ... of V
 // elements: 16-byte vectors where C allows, else 4-byte ones, else elements.
+// Arithmetic is on pairs of values (F2).
+
+template <typename T>
+__device__ __forceinline__ void to_pair(F2 v, T &lo, T &hi) {
+    float a, b;
+    split(v, a, b);
+    lo = from_f32<T>(a), hi = from_f32<T>(b);
+}
 
 template <typename T, int V, int EPT, int TPR>
 struct Row {
-    static constexpr int VPT = EPT / V;
+    static constexpr int VPT = EPT / V, PAIRS = EPT / 2;
+    using E = T;
     using P = Vec<T, V>;
+    struct Packed {
+        P v[VPT];
+    };
     static __device__ __forceinline__ int first(int j, int t) { return (j * TPR + t) * V; }
-    // `absent` where p is null; columns past C read as `outside`
-    static __device__ __forceinline__ void load(P (&d)[VPT], const void *p, int64_t at, int C, int t, float absent,
-                                                float outside = 0.0f) {
+    static __device__ __forceinline__ bool inside(int e, int C, int t) { return first(e / V, t) < C; }
+    // Columns past C (0 for a row that is not there) read as zero.
+    static __device__ __forceinline__ void load(Packed &d, const void *p, int64_t at, int C, int t) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = first(j, t);
-            if (p && c < C) {
-                d[j] = *reinterpret_cast<const P *>(static_cast<const T *>(p) + at + c);
+            if (c < C) {
+                d.v[j] = *reinterpret_cast<const P *>(static_cast<const T *>(p) + at + c);
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) d[j].v[i] = from_f32<T>(c < C ? absent : outside);
+                for (int i = 0; i < V; ++i) d.v[j].v[i] = from_f32<T>(0.0f);
             }
         }
     }
-    static __device__ __forceinline__ void store(void *p, int64_t at, int C, int t, const float (&v)[EPT]) {
+    static __device__ __forceinline__ void store(void *p, int64_t at, int C, int t, const F2 (&v)[PAIRS]) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = first(j, t);
+            T e[V > 1 ? V : 2];
+            if (V > 1) {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) to_pair<T>(v[j * V / 2 + i], e[2 * i], e[2 * i + 1]);
+            } else {
+                to_pair<T>(v[j / 2], e[0], e[1]);
+                e[0] = e[j % 2];
+            }
             if (c >= C) continue;
             P d;
 #pragma unroll
-            for (int i = 0; i < V; ++i) d.v[i] = from_f32<T>(v[j * V + i]);
+            for (int i = 0; i < V; ++i) d.v[i] = e[i];
             *reinterpret_cast<P *>(static_cast<T *>(p) + at + c) = d;
         }
     }
-    static __device__ __forceinline__ float get(const P (&d)[VPT], int e) { return to_f32(d[e / V].v[e % V]); }
-    static __device__ __forceinline__ bool inside(int e, int C, int t) { return first(e / V, t) < C; }
+    static __device__ __forceinline__ float get(const Packed &d, int e) { return to_f32(d.v[e / V].v[e % V]); }
+    static __device__ __forceinline__ F2 pair(const Packed &d, int i) { return f2(get(d, 2 * i), get(d, 2 * i + 1)); }
+    static __device__ __forceinline__ void clear_outside(F2 (&v)[PAIRS], int C, int t) {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            float a, b;
+            split(v[i], a, b);
+            v[i] = f2(inside(2 * i, C, t) ? a : 0.0f, inside(2 * i + 1, C, t) ? b : 0.0f);
+        }
+    }
+};
+
+// The rows a thread will need, copied ahead into its own part of shared memory
+// (no barrier: nobody else reads it), or loaded when asked for where a vector is
+// too short for such copies.
+template <typename R, int ARRAYS, int DEPTH, int THREADS>
+struct Ahead {
+    static constexpr bool ASYNC = sizeof(typename R::P) >= 4;
+    static constexpr int BYTES = ASYNC ? DEPTH * ARRAYS * THREADS * (int)sizeof(typename R::Packed) : 0;
+    unsigned char *base;
+    int stage = 0;  // of the next row to be read
+    __device__ explicit Ahead(void *smem) : base(static_cast<unsigned char *>(smem)) {}
+    // vectors of one stage and array: [VPT][THREADS], so that a warp's are consecutive
+    __device__ __forceinline__ unsigned char *at(int s, int a, int j) {
+        return base + ((size_t)((s * ARRAYS + a) * R::VPT + j) * THREADS + threadIdx.x) * sizeof(typename R::P);
+    }
+    // Starts the copies of a row (C = 0: zeros) into the stage `ahead` rows on; not
+    // `wanted`: of none, as after the last row, whose stage may get other copies next.
+    __device__ __forceinline__ void copy(int ahead, bool wanted, const void *const (&p)[ARRAYS], int64_t row_at, int C,
+                                         int t) {
+        if (!ASYNC) return;
+        int s = stage + ahead;
+        if (s >= DEPTH) s -= DEPTH;
+#pragma unroll
+        for (int a = 0; a < ARRAYS; ++a) {
+            if (!p[a] || !wanted) continue;
+#pragma unroll
+            for (int j = 0; j < R::VPT; ++j) {
+                const int c = R::first(j, t), bytes = c < C ? (int)sizeof(typename R::P) : 0;
+                copy_vector(at(s, a, j), static_cast<const typename R::E *>(p[a]) + (bytes ? row_at + c : 0), bytes);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    static __device__ __forceinline__ void copy_vector(void *dst, const void *src, int bytes) {
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+        if (sizeof(typename R::P) == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+        else if (sizeof(typename R::P) == 8)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+    }
+    // Waits until at most `later` rows started after this one are still on their way.
+    template <int LATER>
+    __device__ __forceinline__ void wait() {
+        if (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
+    }
+    __device__ __forceinline__ void read(typename R::Packed &d, int a, const void *p, int64_t row_at, int C, int t) {
+        if (ASYNC) {
+#pragma unroll
+            for (int j = 0; j < R::VPT; ++j) d.v[j] = *reinterpret_cast<const typename R::P *>(at(stage, a, j));
+        } else {
+            R::load(d, p, row_at, C, t);
+        }
+    }
+    __device__ __forceinline__ void next() {
+        if (++stage == DEPTH) stage = 0;
+    }
 };
 
 // Sums over the TPR threads of a row, the same bits in every one of them. Rows of
@@ -258,99 +345,172 @@ struct Row {
 // between, which every thread reaches after reading it.
 template <int TPR, int THREADS>
 struct RowReduce {
-    static constexpr int WARPS = TPR > 32 ? TPR / 32 : 1;
-    float2 (*buf)[THREADS / 32];  // [2][THREADS / 32]
+    static constexpr int LANES = TPR > 32 ? 32 : TPR, WARPS = TPR > 32 ? TPR / 32 : 1;
+    float (*buf)[2][THREADS / 32];  // [2][2][THREADS / 32]
     int phase = 0;
-    __device__ explicit RowReduce(float2 (*b)[THREADS / 32]) : buf(b) {}
-    __device__ __forceinline__ float2 sum2(float a, float b) {
+    __device__ explicit RowReduce(float (*b)[2][THREADS / 32]) : buf(b) {}
+    __device__ __forceinline__ void barrier() {
+        if (TPR == THREADS) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.x / TPR + 1), "r"(TPR) : "memory");
+    }
+    __device__ __forceinline__ float sum(float a) {
 #pragma unroll
-        for (int o = (TPR > 32 ? 32 : TPR) / 2; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
+        for (int o = LANES / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
         if (TPR > 32) {
-            const int slot = threadIdx.x / TPR, warp = threadIdx.x >> 5;
-            if ((threadIdx.x & 31) == 0) buf[phase][warp] = make_float2(a, b);
-            if (TPR == THREADS) __syncthreads();
-            else asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(TPR) : "memory");
-            a = b = 0.0f;
+            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = threadIdx.x / TPR * WARPS;
+            if (lane == 0) buf[phase][0][warp] = a;
+            barrier();
+            a = buf[phase][0][w0 + lane % WARPS];
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float2 v = buf[phase][slot * WARPS + w];
-                a += v.x, b += v.y;
-            }
+            for (int o = WARPS / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
             phase ^= 1;
         }
+        return a;
+    }
+    // Two sums: the lower half of the lanes goes on with a, the upper with b.
+    __device__ __forceinline__ float2 sum2(float a, float b) {
+        const int lane = threadIdx.x & 31;
+        const bool up = (lane & (LANES / 2)) != 0;
+        float v = up ? b : a;
+        v += __shfl_xor_sync(0xffffffffu, up ? a : b, LANES / 2);
+#pragma unroll
+        for (int o = LANES / 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        const int row0 = lane & ~(LANES - 1);
+        if (TPR <= 32)
+            return make_float2(__shfl_sync(0xffffffffu, v, row0), __shfl_sync(0xffffffffu, v, row0 + LANES / 2));
+        const int warp = threadIdx.x >> 5, w0 = threadIdx.x / TPR * WARPS;
+        if ((lane & 15) == 0) buf[phase][lane >> 4][warp] = v;
+        barrier();
+        if (WARPS <= 16) {
+            v = buf[phase][lane / WARPS & 1][w0 + lane % WARPS];
+#pragma unroll
+            for (int o = WARPS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            a = __shfl_sync(0xffffffffu, v, 0), b = __shfl_sync(0xffffffffu, v, WARPS);
+        } else {
+            a = buf[phase][0][lane], b = buf[phase][1][lane];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+                b += __shfl_xor_sync(0xffffffffu, b, o);
+            }
+        }
+        phase ^= 1;
         return make_float2(a, b);
     }
-    __device__ __forceinline__ float sum(float a) { return sum2(a, 0.0f).x; }
 };
 
-// v -> its normed values; m and i as in row_moments.
-template <typename R, int EPT, typename Red>
-__device__ __forceinline__ void norm_values(int kind, float (&v)[EPT], int C, float inv_c, float eps, int t, Red &red,
-                                            float &i) {
-    i = 1.0f;
-    if (kind == IM2WIN_NORM_NONE) return;
-    float a = 0.0f;
-    if (kind == IM2WIN_NORM_LAYER) {
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) a += v[e];
-        const float m = red.sum(a) * inv_c;
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) v[e] = R::inside(e, C, t) ? v[e] - m : 0.0f;
-        a = 0.0f;
-    }
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) a = fmaf(v[e], v[e], a);
-    i = 1.0f / sqrtf(red.sum(a) * inv_c + eps);
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) v[e] *= i;
+__device__ __forceinline__ float total2(F2 v) {
+    float a, b;
+    split(v, a, b);
+    return a + b;
 }
 
-// One row a TPR threads, rows dealt out to the grid in turn. Bound by memory: two
-// rows read and two written; the parameters come from L1.
+// v -> its normed values, zero past C; i is the inverse deviation.
+template <typename R, typename Red>
+__device__ __forceinline__ void norm_values(int kind, F2 (&v)[R::PAIRS], int C, bool full, float inv_c, float eps, int t,
+                                            Red &red, float &i) {
+    i = 1.0f;
+    if (kind == IM2WIN_NORM_NONE) return;
+    F2 a = f2(0.0f);
+    if (kind == IM2WIN_NORM_LAYER) {
+#pragma unroll
+        for (int e = 0; e < R::PAIRS; ++e) a = add2(a, v[e]);
+        const F2 m = f2(-red.sum(total2(a)) * inv_c);
+#pragma unroll
+        for (int e = 0; e < R::PAIRS; ++e) v[e] = add2(v[e], m);
+        if (!full) R::clear_outside(v, C, t);
+        a = f2(0.0f);
+    }
+#pragma unroll
+    for (int e = 0; e < R::PAIRS; ++e) a = fma2(v[e], v[e], a);
+    i = 1.0f / sqrtf(red.sum(total2(a)) * inv_c + eps);
+    const F2 ii = f2(i);
+#pragma unroll
+    for (int e = 0; e < R::PAIRS; ++e) v[e] = mul2(v[e], ii);
+}
+
+// One row a TPR threads; a block takes a run of rows, its row slots in turn.
+// Bound by memory (two rows read, two written): the parameters stay in registers
+// as they are stored, the next rows are on their way while one is worked on.
 template <typename T, int V, int EPT, int TPR, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_forward_rows(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1024 / THREADS)
+    norm_forward_rows(const __grid_constant__ NormArgs p, const __grid_constant__ FastDiv per_gate) {
     using R = Row<T, V, EPT, TPR>;
-    __shared__ float2 buf[2][THREADS / 32];
+    constexpr int RPB = THREADS / TPR, DEPTH = 3;
+    using A = Ahead<R, 2, DEPTH, THREADS>;
+    extern __shared__ uint4 dyn[];
+    __shared__ float buf[2][2][THREADS / 32];
     RowReduce<TPR, THREADS> red(buf);
-    constexpr int RPB = THREADS / TPR;
-    const int t = threadIdx.x % TPR, C = (int)p.C;
+    A ahead(dyn);
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR, C = (int)p.C;
+    const bool full = C == TPR * EPT;
     const float inv_c = 1.0f / (float)C;
-    // every thread of a block makes the same number of rounds (the reductions' barriers)
-    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.R; row0 += (int64_t)gridDim.x * RPB) {
-        const int64_t row = row0 + threadIdx.x / TPR;
-        const bool live = row < p.R;
-        const int width = live ? C : 0;
-        const int64_t at = row * C;
-        typename R::P px[R::VPT], py[R::VPT], pg[R::VPT], ps[R::VPT], w[R::VPT], b[R::VPT];
-        R::load(px, p.x, at, width, t, 0.0f);
-        R::load(py, p.y, at, width, t, 0.0f);
-        R::load(ps, p.res_scale, 0, C, t, 1.0f);
-        R::load(pg, p.gate, live && p.gate ? row / p.per_gate * C : 0, C, t, 1.0f);
-        R::load(w, p.w_post, 0, C, t, 1.0f);
-        R::load(b, p.b_post, 0, C, t, 0.0f);
-        float r[EPT], i;
+    const int64_t begin = p.R * blockIdx.x / gridDim.x, end = p.R * (blockIdx.x + 1) / gridDim.x;
+    const int rounds = (int)((end - begin + RPB - 1) / RPB);
+    const void *const rows[2] = {p.x, p.y};
+    typename R::Packed ps, wq, bq, wp, bp;
+    auto start = [&](int k, int into) {
+        const int64_t row = begin + (int64_t)k * RPB + slot;
+        ahead.copy(into, k < rounds, rows, row * C, row < end ? C : 0, t);
+    };
+#pragma unroll
+    for (int k = 0; k < DEPTH - 1; ++k) start(k, k);
+    if (p.res_scale) R::load(ps, p.res_scale, 0, C, t);
+    if (p.w_post) R::load(wq, p.w_post, 0, C, t);
+    if (p.b_post) R::load(bq, p.b_post, 0, C, t);
+    if (p.w_pre) R::load(wp, p.w_pre, 0, C, t);
+    if (p.b_pre) R::load(bp, p.b_pre, 0, C, t);
+#pragma unroll 1
+    for (int k = 0; k < rounds; ++k) {
+        const int64_t row = begin + (int64_t)k * RPB + slot, at = row * C;
+        const int width = row < end ? C : 0;
+        start(k + DEPTH - 1, DEPTH - 1);
+        ahead.template wait<DEPTH - 1>();
+        typename R::Packed pg, d;
+        F2 r[R::PAIRS];
+        float i;
         if (p.y) {
+            if (p.gate) R::load(pg, p.gate, (int64_t)fdiv((uint32_t)row, per_gate) * C, width, t);
+            ahead.read(d, 1, p.y, at, width, t);
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) r[e] = R::get(py, e);
-            norm_values<R>(p.post, r, C, inv_c, p.eps, t, red, i);
+            for (int e = 0; e < R::PAIRS; ++e) r[e] = R::pair(d, e);
+            norm_values<R>(p.post, r, C, full, inv_c, p.eps, t, red, i);
+            if (p.w_post) {
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) r[e] = R::get(pg, e) * fmaf(r[e], R::get(w, e), R::get(b, e));
+                for (int e = 0; e < R::PAIRS; ++e) r[e] = mul2(r[e], R::pair(wq, e));
+            }
+            if (p.b_post) {
+#pragma unroll
+                for (int e = 0; e < R::PAIRS; ++e) r[e] = add2(r[e], R::pair(bq, e));
+            }
+            if (p.gate) {
+#pragma unroll
+                for (int e = 0; e < R::PAIRS; ++e) r[e] = mul2(r[e], R::pair(pg, e));
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) r[e] = 0.0f;
+            for (int e = 0; e < R::PAIRS; ++e) r[e] = f2(0.0f);
         }
-        R::load(w, p.w_pre, 0, C, t, 1.0f);
-        R::load(b, p.b_pre, 0, C, t, 0.0f);
+        ahead.read(d, 0, p.x, at, width, t);
+        ahead.next();
+        if (p.res_scale) {
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) r[e] = R::inside(e, C, t) ? fmaf(R::get(px, e), R::get(ps, e), r[e]) : 0.0f;
+            for (int e = 0; e < R::PAIRS; ++e) r[e] = fma2(R::pair(d, e), R::pair(ps, e), r[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < R::PAIRS; ++e) r[e] = add2(R::pair(d, e), r[e]);
+        }
         if (p.r) R::store(p.r, at, width, t, r);
         if (p.n) {
-            norm_values<R>(p.pre, r, C, inv_c, p.eps, t, red, i);
+            norm_values<R>(p.pre, r, C, full, inv_c, p.eps, t, red, i);
+            if (p.w_pre) {
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) r[e] = fmaf(r[e], R::get(w, e), R::get(b, e));
+                for (int e = 0; e < R::PAIRS; ++e) r[e] = mul2(r[e], R::pair(wp, e));
+            }
+            if (p.b_pre) {
+#pragma unroll
+                for (int e = 0; e < R::PAIRS; ++e) r[e] = add2(r[e], R::pair(bp, e));
+            }
             R::store(p.n, at, width, t, r);
         }
     }
@@ -361,129 +521,210 @@ __global__ void __launch_bounds__(THREADS) norm_forward_rows(const __grid_consta
 // A block walks rows and keeps the sums over them in registers, a thread for its
 // own columns. Within a gate group dw_post, db_post and dgate all follow from
 //   A = sum dt * yhat,  B = sum dt:   dgate = w A + b B,  dw_post += gate A,  db_post += gate B,
-// so five sums are enough: A, B, sum x dt, sum dn rhat and sum dn. Two ways of
-// cutting the rows:
+// so five sums are enough: A, B, sum x dt, sum dn rhat and sum dn (B and the last
+// only where there is a bias). Two ways of cutting the rows:
 //  long groups   block k takes rows [R k / blocks, R (k+1) / blocks), its row slots
 //                in turn; at the end of a group and of its rows it joins its slots'
 //                A and B into segment k + g (unique along the staircase of blocks and
 //                groups), which the joining kernel weighs with the group's gate;
 //  short groups  a row slot takes whole groups, writes their dgate and adds the
 //                weighed A and B to its sums in shared memory.
+template <typename R, int THREADS>
+using BackAhead = Ahead<R, 4, sizeof(typename R::Packed) <= 16 ? 3 : 2, THREADS>;
 
 template <typename T, int V, int EPT, int TPR, int THREADS, bool SHORT>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_backward_fused(const __grid_constant__ NormArgs p, const __grid_constant__ BackPlan plan, float *part, float *seg,
                         T *dgate) {
     using R = Row<T, V, EPT, TPR>;
-    constexpr int RPB = THREADS / TPR;
-    extern __shared__ float dyn[];  // SHORT: A and B weighed, [2][RPB][TPR * EPT]; then [RPB][TPR * EPT] to join slots
-    __shared__ float2 buf[2][THREADS / 32];
-    RowReduce<TPR, THREADS> red(buf);
-    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR, C = (int)p.C;
-    const float inv_c = 1.0f / (float)C;
+    using A = BackAhead<R, THREADS>;
+    constexpr int RPB = THREADS / TPR, DEPTH = sizeof(typename R::Packed) <= 16 ? 3 : 2;
     constexpr int W = TPR * EPT;  // columns a slot holds
-    float *fold = dyn + (size_t)slot * W, *join = dyn + (SHORT ? 2 * RPB * W : 0);
-    float acc[BACK_SUMS][EPT];
+    // rows on their way; SHORT: A and B weighed, [2][RPB][W]; then [RPB][W] to join slots
+    extern __shared__ uint4 dyn[];
+    float *sums = reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(dyn) + A::BYTES);
+    __shared__ float buf[2][2][THREADS / 32];
+    RowReduce<TPR, THREADS> red(buf);
+    A ahead(dyn);
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR, C = (int)p.C;
+    const bool full = C == W;
+    const float inv_c = 1.0f / (float)C;
+    float *fold = sums + (size_t)slot * W, *join = sums + (SHORT ? 2 * RPB * W : 0);
+    const void *const inputs[4] = {p.x, p.y, p.dr, p.dn};
+    F2 acc[BACK_SUMS][R::PAIRS];
 #pragma unroll
     for (int q = 0; q < BACK_SUMS; ++q)
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) acc[q][e] = 0.0f;
+        for (int e = 0; e < R::PAIRS; ++e) acc[q][e] = f2(0.0f);
     if (SHORT) {
 #pragma unroll
         for (int e = 0; e < EPT; ++e) fold[e * TPR + t] = fold[RPB * W + e * TPR + t] = 0.0f;
     }
 
-    // Rows [first, last) of group g, every `step`-th; `rounds` is the same for all slots.
-    auto rows = [&](int64_t g, int64_t first, int64_t last, int64_t step, int64_t rounds, typename R::P(&pg)[R::VPT]) {
-        typename R::P px[R::VPT], py[R::VPT], pr[R::VPT], pn[R::VPT], w[R::VPT], b[R::VPT];
-        auto fetch = [&](int64_t row) {
-            const int width = row < last ? C : 0;
-            R::load(px, p.x, row * C, width, t, 0.0f);
-            R::load(py, p.y, row * C, width, t, 0.0f);
-            R::load(pr, p.dr, row * C, width, t, 0.0f);
-            R::load(pn, p.dn, row * C, width, t, 0.0f);
+    // Rows first, first + step, ... before last, of group g; `rounds` is the same for all slots.
+    auto rows = [&](int64_t g, int64_t first, int64_t last, int step, int rounds, typename R::Packed &pg) {
+        auto start = [&](int k, int into) {
+            const int64_t row = first + (int64_t)k * step;
+            ahead.copy(into, k < rounds, inputs, row * C, row < last ? C : 0, t);
         };
-        R::load(pg, p.gate, p.gate ? g * C : 0, C, t, 1.0f);
-        fetch(first);
-        for (int64_t k = 0; k < rounds; ++k) {
-            const int64_t row = first + k * step;
+#pragma unroll
+        for (int k = 0; k < DEPTH - 1; ++k) start(k, k);
+        if (p.gate) R::load(pg, p.gate, g * C, C, t);
+#pragma unroll 1
+        for (int k = 0; k < rounds; ++k) {
+            const int64_t row = first + (int64_t)k * step, at = row * C;
             const int width = row < last ? C : 0;
             const float eps = row < last ? p.eps : 1.0f;  // (a slot without a row: zeros throughout)
-            float yh[EPT], rh[EPT], d[EPT], iy = 1.0f, ir = 1.0f;
+            start(k + DEPTH - 1, DEPTH - 1);
+            ahead.template wait<DEPTH - 1>();
+            F2 yh[R::PAIRS], rh[R::PAIRS], d[R::PAIRS];
+            float iy = 1.0f, ir = 1.0f;
+            typename R::Packed v, w;
+            ahead.read(v, 0, p.x, at, width, t);
+            if (p.res_scale) {
+                R::load(w, p.res_scale, 0, C, t);
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) yh[e] = R::get(py, e);
-            if (p.y) norm_values<R>(p.post, yh, C, inv_c, eps, t, red, iy);
-            R::load(w, p.res_scale, 0, C, t, 1.0f);
+                for (int e = 0; e < R::PAIRS; ++e) rh[e] = mul2(R::pair(v, e), R::pair(w, e));
+            } else {
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                d[e] = R::get(pr, e);
-                rh[e] = R::get(px, e) * R::get(w, e);
+                for (int e = 0; e < R::PAIRS; ++e) rh[e] = R::pair(v, e);
+            }
+            if (p.y) {
+                ahead.read(v, 1, p.y, at, width, t);
+#pragma unroll
+                for (int e = 0; e < R::PAIRS; ++e) yh[e] = R::pair(v, e);
+                norm_values<R>(p.post, yh, C, full, inv_c, eps, t, red, iy);
+                if (p.dn) {
+#pragma unroll
+                    for (int e = 0; e < R::PAIRS; ++e) d[e] = yh[e];
+                    if (p.w_post) {
+                        R::load(w, p.w_post, 0, C, t);
+#pragma unroll
+                        for (int e = 0; e < R::PAIRS; ++e) d[e] = mul2(d[e], R::pair(w, e));
+                    }
+                    if (p.b_post) {
+                        R::load(w, p.b_post, 0, width, t);
+#pragma unroll
+                        for (int e = 0; e < R::PAIRS; ++e) d[e] = add2(d[e], R::pair(w, e));
+                    }
+                    if (p.gate) {
+#pragma unroll
+                        for (int e = 0; e < R::PAIRS; ++e) d[e] = mul2(d[e], R::pair(pg, e));
+                    }
+#pragma unroll
+                    for (int e = 0; e < R::PAIRS; ++e) rh[e] = add2(rh[e], d[e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < R::PAIRS; ++e) yh[e] = f2(0.0f);
+            }
+            if (p.dr) {
+                ahead.read(v, 2, p.dr, at, width, t);
+#pragma unroll
+                for (int e = 0; e < R::PAIRS; ++e) d[e] = R::pair(v, e);
+            } else {
+#pragma unroll
+                for (int e = 0; e < R::PAIRS; ++e) d[e] = f2(0.0f);
             }
             if (p.dn) {
-                if (p.y) {
-                    R::load(w, p.w_post, 0, C, t, 1.0f);
-                    R::load(b, p.b_post, 0, C, t, 0.0f);
+                norm_values<R>(p.pre, rh, C, full, inv_c, eps, t, red, ir);
+                ahead.read(v, 3, p.dn, at, width, t);
+                F2 n[R::PAIRS], e1 = f2(0.0f), e2 = f2(0.0f);
 #pragma unroll
-                    for (int e = 0; e < EPT; ++e)
-                        rh[e] = R::inside(e, width, t) ? fmaf(R::get(pg, e), fmaf(yh[e], R::get(w, e), R::get(b, e)), rh[e]) : 0.0f;
+                for (int e = 0; e < R::PAIRS; ++e) {
+                    n[e] = R::pair(v, e);
+                    acc[BACK_W_PRE][e] = fma2(n[e], rh[e], acc[BACK_W_PRE][e]);
                 }
-                norm_values<R>(p.pre, rh, C, inv_c, eps, t, red, ir);
-                R::load(w, p.w_pre, 0, C, t, 1.0f);
-                float e1 = 0.0f, e2 = 0.0f;
+                if (p.b_pre) {
 #pragma unroll
-                for (int e = 0; e < EPT; ++e) {
-                    const float n = R::get(pn, e), f = n * R::get(w, e);
-                    e1 += f;
-                    e2 = fmaf(f, rh[e], e2);
-                    acc[BACK_W_PRE][e] = fmaf(n, rh[e], acc[BACK_W_PRE][e]);
-                    acc[BACK_B_PRE][e] += n;
+                    for (int e = 0; e < R::PAIRS; ++e) acc[BACK_B_PRE][e] = add2(acc[BACK_B_PRE][e], n[e]);
                 }
-                const float2 m = red.sum2(e1, e2);
-                e1 = p.pre == IM2WIN_NORM_LAYER ? m.x * inv_c : 0.0f;
-                e2 = m.y * inv_c;
+                if (p.w_pre) {
+                    R::load(w, p.w_pre, 0, C, t);
 #pragma unroll
-                for (int e = 0; e < EPT; ++e)
-                    d[e] = fmaf(ir, R::get(pn, e) * R::get(w, e) - e1 - rh[e] * e2, d[e]);
-            }
-            // d is dt from here on (its columns past C meet only zeros: x, yh; and are not stored)
-            R::load(w, p.res_scale, 0, C, t, 1.0f);
+                    for (int e = 0; e < R::PAIRS; ++e) n[e] = mul2(n[e], R::pair(w, e));
+                }
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                if (!R::inside(e, width, t)) d[e] = 0.0f;
-                acc[BACK_RES][e] = fmaf(R::get(px, e), d[e], acc[BACK_RES][e]);
-                acc[BACK_A][e] = fmaf(d[e], yh[e], acc[BACK_A][e]);
-                acc[BACK_B][e] += d[e];
-                rh[e] = d[e] * R::get(w, e);
+                for (int e = 0; e < R::PAIRS; ++e) e2 = fma2(n[e], rh[e], e2);
+                const F2 scale = f2(ir);
+                if (p.pre == IM2WIN_NORM_LAYER) {
+#pragma unroll
+                    for (int e = 0; e < R::PAIRS; ++e) e1 = add2(e1, n[e]);
+                    const float2 m = red.sum2(total2(e1), total2(e2));
+                    e1 = f2(-m.x * inv_c), e2 = f2(-m.y * inv_c);
+#pragma unroll
+                    for (int e = 0; e < R::PAIRS; ++e) d[e] = fma2(fma2(rh[e], e2, add2(n[e], e1)), scale, d[e]);
+                    if (!full) R::clear_outside(d, C, t);
+                } else {
+                    e2 = f2(-red.sum(total2(e2)) * inv_c);
+#pragma unroll
+                    for (int e = 0; e < R::PAIRS; ++e) d[e] = fma2(fma2(rh[e], e2, n[e]), scale, d[e]);
+                }
             }
-            if (k + 1 < rounds) fetch(row + step);  // in flight through the last reduction and the stores
-            if (p.dx) R::store(p.dx, row * C, width, t, rh);
+            // d is dt, zero past C and in a slot without a row
+            ahead.read(v, 0, p.x, at, width, t);
+            ahead.next();
+#pragma unroll
+            for (int e = 0; e < R::PAIRS; ++e) {
+                acc[BACK_RES][e] = fma2(R::pair(v, e), d[e], acc[BACK_RES][e]);
+                acc[BACK_A][e] = fma2(d[e], yh[e], acc[BACK_A][e]);
+            }
+            if (p.b_post) {
+#pragma unroll
+                for (int e = 0; e < R::PAIRS; ++e) acc[BACK_B][e] = add2(acc[BACK_B][e], d[e]);
+            }
+            if (p.dx) {
+                if (p.res_scale) {
+                    R::load(w, p.res_scale, 0, C, t);
+#pragma unroll
+                    for (int e = 0; e < R::PAIRS; ++e) rh[e] = mul2(d[e], R::pair(w, e));
+                    R::store(p.dx, at, width, t, rh);
+                } else {
+                    R::store(p.dx, at, width, t, d);
+                }
+            }
             if (p.dy) {
-                R::load(w, p.w_post, 0, C, t, 1.0f);
-                float f1 = 0.0f, f2 = 0.0f;
+                if (p.gate) {
 #pragma unroll
-                for (int e = 0; e < EPT; ++e) {
-                    d[e] *= R::get(pg, e) * R::get(w, e);
-                    f1 += d[e];
-                    f2 = fmaf(d[e], yh[e], f2);
+                    for (int e = 0; e < R::PAIRS; ++e) d[e] = mul2(d[e], R::pair(pg, e));
+                }
+                if (p.w_post) {
+                    R::load(w, p.w_post, 0, C, t);
+#pragma unroll
+                    for (int e = 0; e < R::PAIRS; ++e) d[e] = mul2(d[e], R::pair(w, e));
                 }
                 if (p.post != IM2WIN_NORM_NONE) {
-                    const float2 m = red.sum2(f1, f2);
-                    f1 = p.post == IM2WIN_NORM_LAYER ? m.x * inv_c : 0.0f;
-                    f2 = m.y * inv_c;
+                    F2 f1 = f2(0.0f), s2 = f2(0.0f);
 #pragma unroll
-                    for (int e = 0; e < EPT; ++e) d[e] = iy * (d[e] - f1 - yh[e] * f2);
+                    for (int e = 0; e < R::PAIRS; ++e) s2 = fma2(d[e], yh[e], s2);
+                    if (p.post == IM2WIN_NORM_LAYER) {
+#pragma unroll
+                        for (int e = 0; e < R::PAIRS; ++e) f1 = add2(f1, d[e]);
+                        const float2 m = red.sum2(total2(f1), total2(s2));
+                        f1 = f2(-m.x * inv_c), s2 = f2(-m.y * inv_c);
+#pragma unroll
+                        for (int e = 0; e < R::PAIRS; ++e) d[e] = add2(d[e], f1);
+                    } else {
+                        s2 = f2(-red.sum(total2(s2)) * inv_c);
+                    }
+                    const F2 scale = f2(iy);
+#pragma unroll
+                    for (int e = 0; e < R::PAIRS; ++e) d[e] = mul2(fma2(yh[e], s2, d[e]), scale);
                 }
-                R::store(p.dy, row * C, width, t, d);
+                R::store(p.dy, at, width, t, d);
             }
         }
     };
     // Adds one sum over the block's slots, in their order, into dst (and clears it).
-    auto join_slots = [&](int q, float *dst) {
+    auto join_slots = [&](F2(&sum)[R::PAIRS], float *dst) {
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            join[slot * W + R::first(e / V, t) + e % V] = acc[q][e];
-            acc[q][e] = 0.0f;
+            float a, b;
+            split(sum[e / 2], a, b);
+            join[slot * W + R::first(e / V, t) + e % V] = e % 2 ? b : a;
         }
+#pragma unroll
+        for (int e = 0; e < R::PAIRS; ++e) sum[e] = f2(0.0f);
         __syncthreads();
         for (int c = threadIdx.x; c < C; c += THREADS) {
             float v = 0.0f;
@@ -493,46 +734,58 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncthreads();
     };
+    auto put_part = [&](int q, F2(&sum)[R::PAIRS]) { join_slots(sum, part + ((int64_t)q * gridDim.x + blockIdx.x) * C); };
 
-    typename R::P pg[R::VPT];
+    typename R::Packed pg;
     if (SHORT) {
         // slot s of all takes groups s, s + slots, ...
         const int64_t slots = (int64_t)gridDim.x * RPB;
         for (int64_t g0 = (int64_t)blockIdx.x * RPB; g0 < plan.groups; g0 += slots) {
             const int64_t g = g0 + slot, first = g * p.per_gate;
             const int64_t last = g < plan.groups ? min(p.R, first + p.per_gate) : first;
-            rows(g < plan.groups ? g : 0, first, last, 1, p.per_gate, pg);
+            rows(g < plan.groups ? g : 0, first, last, 1, (int)p.per_gate, pg);
             if (!p.y) continue;
-            typename R::P w[R::VPT], b[R::VPT];
-            R::load(w, p.w_post, 0, C, t, 1.0f);
-            R::load(b, p.b_post, 0, C, t, 0.0f);
-            float d[EPT];
+            typename R::Packed w, b;
+            if (p.w_post) R::load(w, p.w_post, 0, C, t);
+            if (p.b_post) R::load(b, p.b_post, 0, C, t);
+            F2 d[R::PAIRS];
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                d[e] = fmaf(R::get(w, e), acc[BACK_A][e], R::get(b, e) * acc[BACK_B][e]);
-                fold[e * TPR + t] += R::get(pg, e) * acc[BACK_A][e];
-                fold[RPB * W + e * TPR + t] += R::get(pg, e) * acc[BACK_B][e];
-                acc[BACK_A][e] = acc[BACK_B][e] = 0.0f;
+            for (int e = 0; e < R::PAIRS; ++e) {
+                const F2 gate = p.gate ? R::pair(pg, e) : f2(1.0f);
+                d[e] = p.w_post ? mul2(R::pair(w, e), acc[BACK_A][e]) : acc[BACK_A][e];
+                if (p.b_post) d[e] = fma2(R::pair(b, e), acc[BACK_B][e], d[e]);
+                float a0, a1, b0, b1;
+                split(mul2(gate, acc[BACK_A][e]), a0, a1);
+                split(mul2(gate, acc[BACK_B][e]), b0, b1);
+                fold[2 * e * TPR + t] += a0, fold[(2 * e + 1) * TPR + t] += a1;
+                fold[RPB * W + 2 * e * TPR + t] += b0, fold[RPB * W + (2 * e + 1) * TPR + t] += b1;
+                acc[BACK_A][e] = acc[BACK_B][e] = f2(0.0f);
             }
             if (dgate && g < plan.groups) R::store(dgate, g * C, C, t, d);
         }
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) acc[BACK_A][e] = fold[e * TPR + t], acc[BACK_B][e] = fold[RPB * W + e * TPR + t];
-        for (int q = 0; q < BACK_SUMS; ++q) join_slots(q, part + ((int64_t)q * gridDim.x + blockIdx.x) * C);
+        for (int e = 0; e < R::PAIRS; ++e) {
+            acc[BACK_A][e] = f2(fold[2 * e * TPR + t], fold[(2 * e + 1) * TPR + t]);
+            acc[BACK_B][e] = f2(fold[RPB * W + 2 * e * TPR + t], fold[RPB * W + (2 * e + 1) * TPR + t]);
+        }
+        put_part(BACK_A, acc[BACK_A]);
+        put_part(BACK_B, acc[BACK_B]);
     } else {
         const int64_t begin = p.R * blockIdx.x / gridDim.x, end = p.R * (blockIdx.x + 1) / gridDim.x;
         for (int64_t at = begin; at < end;) {
             const int64_t g = at / p.per_gate, last = min(end, (g + 1) * p.per_gate);
-            rows(g, at + slot, last, RPB, (last - at + RPB - 1) / RPB, pg);
+            rows(g, at + slot, last, RPB, (int)((last - at + RPB - 1) / RPB), pg);
             if (p.y) {
                 float *dst = seg + (blockIdx.x + g) * 2 * C;
-                join_slots(BACK_A, dst);
-                join_slots(BACK_B, dst + C);
+                join_slots(acc[BACK_A], dst);
+                join_slots(acc[BACK_B], dst + C);
             }
             at = last;
         }
-        for (int q = 0; q < BACK_A; ++q) join_slots(q, part + ((int64_t)q * gridDim.x + blockIdx.x) * C);
     }
+    put_part(BACK_RES, acc[BACK_RES]);
+    put_part(BACK_W_PRE, acc[BACK_W_PRE]);
+    put_part(BACK_B_PRE, acc[BACK_B_PRE]);
 }
 
 // Joins the fused pass's partial sums: 32 columns a block, its 32 warps over
@@ -602,7 +855,7 @@ __global__ void __launch_bounds__(1024) norm_join(const __grid_constant__ NormAr
 template <typename T, int V, int TPR>
 cudaError_t launch_fused(const NormArgs &p, const BackPlan &plan, float *part, float *seg, T *dgate, cudaStream_t st) {
     constexpr int EPT = 8, THREADS = FUSED_THREADS;
-    const size_t smem = (size_t)(plan.short_groups ? 3 : 1) * THREADS * EPT * 4;
+    const size_t smem = BackAhead<Row<T, V, EPT, TPR>, THREADS>::BYTES + (size_t)(plan.short_groups ? 3 : 1) * THREADS * EPT * 4;
     auto kernel = plan.short_groups ? norm_backward_fused<T, V, EPT, TPR, THREADS, true>
                                     : norm_backward_fused<T, V, EPT, TPR, THREADS, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -633,9 +886,16 @@ inline cudaError_t with_vector(int64_t C, Fn f) {
 
 template <typename T, int V, int TPR>
 cudaError_t launch_rows(const NormArgs &p, cudaStream_t st) {
-    constexpr int THREADS = TPR > 256 ? TPR : 256;
-    const int64_t blocks = (p.R + THREADS / TPR - 1) / (THREADS / TPR);
-    norm_forward_rows<T, V, 8, TPR, THREADS><<<(unsigned)std::min<int64_t>(blocks, SMS * 2048 / THREADS), THREADS, 0, st>>>(p);
+    constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
+    auto kernel = norm_forward_rows<T, V, 8, TPR, THREADS>;
+    constexpr int smem = Ahead<Row<T, V, 8, TPR>, 2, 3, THREADS>::BYTES;
+    if (smem > 32 * 1024) {  // (48 KB with the static part need no leave)
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t blocks = (p.R + RPB - 1) / RPB;
+    const FastDiv per = make_fastdiv((uint32_t)std::min(p.per_gate, p.R));
+    kernel<<<(unsigned)std::min<int64_t>(blocks, SMS * 1024 / THREADS), THREADS, smem, st>>>(p, per);
     return cudaGetLastError();
 }
 
