@@ -219,11 +219,18 @@ __global__ void __launch_bounds__(256) join_partials(const float *part, int64_t 
 // elements: 16-byte vectors where C allows, else 4-byte ones, else elements.
 // Arithmetic is on pairs of values (F2).
 
-template <typename T>
-__device__ __forceinline__ void to_pair(F2 v, T &lo, T &hi) {
+__device__ __forceinline__ void to_pair(F2 v, float &lo, float &hi) { split(v, lo, hi); }
+__device__ __forceinline__ void to_pair(F2 v, f16_t &lo, f16_t &hi) {
     float a, b;
     split(v, a, b);
-    lo = from_f32<T>(a), hi = from_f32<T>(b);
+    const __half2 r = __floats2half2_rn(a, b);
+    lo = __low2half(r), hi = __high2half(r);
+}
+__device__ __forceinline__ void to_pair(F2 v, bf16_t &lo, bf16_t &hi) {
+    float a, b;
+    split(v, a, b);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    lo = __low2bfloat16(r), hi = __high2bfloat16(r);
 }
 
 template <typename T, int V, int EPT, int TPR>
@@ -256,9 +263,9 @@ struct Row {
             T e[V > 1 ? V : 2];
             if (V > 1) {
 #pragma unroll
-                for (int i = 0; i < V / 2; ++i) to_pair<T>(v[j * V / 2 + i], e[2 * i], e[2 * i + 1]);
+                for (int i = 0; i < V / 2; ++i) to_pair(v[j * V / 2 + i], e[2 * i], e[2 * i + 1]);
             } else {
-                to_pair<T>(v[j / 2], e[0], e[1]);
+                to_pair(v[j / 2], e[0], e[1]);
                 e[0] = e[j % 2];
             }
             if (c >= C) continue;
@@ -338,6 +345,43 @@ struct Ahead {
         if (++stage == DEPTH) stage = 0;
     }
 };
+
+// Parameters of C elements in shared memory, as they are stored: a thread's part
+// of array i is one conflict-free access at a fixed address (the block's threads
+// fill it together; the caller's barrier follows). Types of 4 bytes, whose copies
+// would not fit beside the rows', read them through L1.
+template <typename R, int ARRAYS, int TPR>
+struct Params {
+    static constexpr bool SHARED = sizeof(typename R::E) == 2;
+    static constexpr int BYTES = SHARED ? ARRAYS * TPR * (int)sizeof(typename R::Packed) : 0;
+    unsigned char *base;
+    const void *const *from;
+    int C, t;
+    __device__ Params(void *smem, const void *const *from_, int C_, int t_)
+        : base(static_cast<unsigned char *>(smem)), from(from_), C(C_), t(t_) {
+        if (!SHARED || threadIdx.x >= TPR) return;
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i) {
+            if (!from[i]) continue;
+            typename R::Packed d;
+            R::load(d, from[i], 0, C, t);
+#pragma unroll
+            for (int j = 0; j < R::VPT; ++j) at(i, j) = d.v[j];
+        }
+    }
+    __device__ __forceinline__ typename R::P &at(int i, int j) {
+        return reinterpret_cast<typename R::P *>(base)[(i * R::VPT + j) * TPR + t];
+    }
+    __device__ __forceinline__ void read(typename R::Packed &d, int i) {
+        if (SHARED) {
+#pragma unroll
+            for (int j = 0; j < R::VPT; ++j) d.v[j] = at(i, j);
+        } else {
+            R::load(d, from[i], 0, C, t);
+        }
+    }
+};
+enum Param { PAR_SCALE, PAR_W_POST, PAR_B_POST, PAR_W_PRE, PAR_B_PRE, PARAMS };
 
 // Sums over the TPR threads of a row, the same bits in every one of them. Rows of
 // more than a warp join their warps' sums through shared memory, in two buffers
@@ -423,17 +467,17 @@ __device__ __forceinline__ void norm_values(int kind, F2 (&v)[R::PAIRS], int C, 
     }
 #pragma unroll
     for (int e = 0; e < R::PAIRS; ++e) a = fma2(v[e], v[e], a);
-    i = 1.0f / sqrtf(red.sum(total2(a)) * inv_c + eps);
+    i = rsqrtf(red.sum(total2(a)) * inv_c + eps);  // (2 ulp at most; a division and a root took 40 instructions)
     const F2 ii = f2(i);
 #pragma unroll
     for (int e = 0; e < R::PAIRS; ++e) v[e] = mul2(v[e], ii);
 }
 
 // One row a TPR threads; a block takes a run of rows, its row slots in turn.
-// Bound by memory (two rows read, two written): the parameters stay in registers
-// as they are stored, the next rows are on their way while one is worked on.
+// Bound by memory (two rows read, two written): the parameters stay in shared
+// memory as they are stored, the next rows are on their way while one is worked on.
 template <typename T, int V, int EPT, int TPR, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1024 / THREADS)
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2)
     norm_forward_rows(const __grid_constant__ NormArgs p, const __grid_constant__ FastDiv per_gate) {
     using R = Row<T, V, EPT, TPR>;
     constexpr int RPB = THREADS / TPR, DEPTH = 3;
@@ -448,40 +492,40 @@ __global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1024 / THREADS)
     const int64_t begin = p.R * blockIdx.x / gridDim.x, end = p.R * (blockIdx.x + 1) / gridDim.x;
     const int rounds = (int)((end - begin + RPB - 1) / RPB);
     const void *const rows[2] = {p.x, p.y};
-    typename R::Packed ps, wq, bq, wp, bp;
+    const void *const given[PARAMS] = {p.res_scale, p.w_post, p.b_post, p.w_pre, p.b_pre};
     auto start = [&](int k, int into) {
         const int64_t row = begin + (int64_t)k * RPB + slot;
         ahead.copy(into, k < rounds, rows, row * C, row < end ? C : 0, t);
     };
 #pragma unroll
     for (int k = 0; k < DEPTH - 1; ++k) start(k, k);
-    if (p.res_scale) R::load(ps, p.res_scale, 0, C, t);
-    if (p.w_post) R::load(wq, p.w_post, 0, C, t);
-    if (p.b_post) R::load(bq, p.b_post, 0, C, t);
-    if (p.w_pre) R::load(wp, p.w_pre, 0, C, t);
-    if (p.b_pre) R::load(bp, p.b_pre, 0, C, t);
+    Params<R, PARAMS, TPR> par(reinterpret_cast<unsigned char *>(dyn) + A::BYTES, given, C, t);
+    __syncthreads();
 #pragma unroll 1
     for (int k = 0; k < rounds; ++k) {
         const int64_t row = begin + (int64_t)k * RPB + slot, at = row * C;
         const int width = row < end ? C : 0;
         start(k + DEPTH - 1, DEPTH - 1);
         ahead.template wait<DEPTH - 1>();
-        typename R::Packed pg, d;
+        typename R::Packed d, w;
         F2 r[R::PAIRS];
         float i;
         if (p.y) {
+            typename R::Packed pg;
             if (p.gate) R::load(pg, p.gate, (int64_t)fdiv((uint32_t)row, per_gate) * C, width, t);
             ahead.read(d, 1, p.y, at, width, t);
 #pragma unroll
             for (int e = 0; e < R::PAIRS; ++e) r[e] = R::pair(d, e);
             norm_values<R>(p.post, r, C, full, inv_c, p.eps, t, red, i);
             if (p.w_post) {
+                par.read(w, PAR_W_POST);
 #pragma unroll
-                for (int e = 0; e < R::PAIRS; ++e) r[e] = mul2(r[e], R::pair(wq, e));
+                for (int e = 0; e < R::PAIRS; ++e) r[e] = mul2(r[e], R::pair(w, e));
             }
             if (p.b_post) {
+                par.read(w, PAR_B_POST);
 #pragma unroll
-                for (int e = 0; e < R::PAIRS; ++e) r[e] = add2(r[e], R::pair(bq, e));
+                for (int e = 0; e < R::PAIRS; ++e) r[e] = add2(r[e], R::pair(w, e));
             }
             if (p.gate) {
 #pragma unroll
@@ -494,8 +538,9 @@ __global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1024 / THREADS)
         ahead.read(d, 0, p.x, at, width, t);
         ahead.next();
         if (p.res_scale) {
+            par.read(w, PAR_SCALE);
 #pragma unroll
-            for (int e = 0; e < R::PAIRS; ++e) r[e] = fma2(R::pair(d, e), R::pair(ps, e), r[e]);
+            for (int e = 0; e < R::PAIRS; ++e) r[e] = fma2(R::pair(d, e), R::pair(w, e), r[e]);
         } else {
 #pragma unroll
             for (int e = 0; e < R::PAIRS; ++e) r[e] = add2(R::pair(d, e), r[e]);
@@ -504,12 +549,14 @@ __global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1024 / THREADS)
         if (p.n) {
             norm_values<R>(p.pre, r, C, full, inv_c, p.eps, t, red, i);
             if (p.w_pre) {
+                par.read(w, PAR_W_PRE);
 #pragma unroll
-                for (int e = 0; e < R::PAIRS; ++e) r[e] = mul2(r[e], R::pair(wp, e));
+                for (int e = 0; e < R::PAIRS; ++e) r[e] = mul2(r[e], R::pair(w, e));
             }
             if (p.b_pre) {
+                par.read(w, PAR_B_PRE);
 #pragma unroll
-                for (int e = 0; e < R::PAIRS; ++e) r[e] = add2(r[e], R::pair(bp, e));
+                for (int e = 0; e < R::PAIRS; ++e) r[e] = add2(r[e], R::pair(w, e));
             }
             R::store(p.n, at, width, t, r);
         }
@@ -526,11 +573,15 @@ __global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1024 / THREADS)
 //  long groups   block k takes rows [R k / blocks, R (k+1) / blocks), its row slots
 //                in turn; at the end of a group and of its rows it joins its slots'
 //                A and B into segment k + g (unique along the staircase of blocks and
-//                groups), which the joining kernel weighs with the group's gate;
+//                groups) for dgate, and weighed with the gate into its sums;
 //  short groups  a row slot takes whole groups, writes their dgate and adds the
 //                weighed A and B to its sums in shared memory.
 template <typename R, int THREADS>
 using BackAhead = Ahead<R, 4, sizeof(typename R::Packed) <= 16 ? 3 : 2, THREADS>;
+// Shared memory of the rows on their way, which also joins slots: THREADS * EPT floats.
+template <typename R, int THREADS>
+constexpr int BACK_ROWS_BYTES = BackAhead<R, THREADS>::BYTES > THREADS * R::PAIRS * 8 ? BackAhead<R, THREADS>::BYTES
+                                                                                  : THREADS * R::PAIRS * 8;
 
 template <typename T, int V, int EPT, int TPR, int THREADS, bool SHORT>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -540,17 +591,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     using A = BackAhead<R, THREADS>;
     constexpr int RPB = THREADS / TPR, DEPTH = sizeof(typename R::Packed) <= 16 ? 3 : 2;
     constexpr int W = TPR * EPT;  // columns a slot holds
-    // rows on their way; SHORT: A and B weighed, [2][RPB][W]; then [RPB][W] to join slots
+    // rows on their way, between groups [RPB][W] to join slots; parameters; SHORT: A and B weighed, [2][RPB][W]
     extern __shared__ uint4 dyn[];
-    float *sums = reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(dyn) + A::BYTES);
+    unsigned char *par_at = reinterpret_cast<unsigned char *>(dyn) + BACK_ROWS_BYTES<R, THREADS>;
+    float *sums = reinterpret_cast<float *>(par_at + Params<R, PARAMS, TPR>::BYTES);
     __shared__ float buf[2][2][THREADS / 32];
     RowReduce<TPR, THREADS> red(buf);
     A ahead(dyn);
     const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR, C = (int)p.C;
     const bool full = C == W;
     const float inv_c = 1.0f / (float)C;
-    float *fold = sums + (size_t)slot * W, *join = sums + (SHORT ? 2 * RPB * W : 0);
+    float *fold = sums + (size_t)slot * W, *join = reinterpret_cast<float *>(dyn);
     const void *const inputs[4] = {p.x, p.y, p.dr, p.dn};
+    const void *const given[PARAMS] = {p.res_scale, p.w_post, p.b_post, p.w_pre, p.b_pre};
+    Params<R, PARAMS, TPR> par(par_at, given, C, t);
+    __syncthreads();
     F2 acc[BACK_SUMS][R::PAIRS];
 #pragma unroll
     for (int q = 0; q < BACK_SUMS; ++q)
@@ -582,7 +637,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             typename R::Packed v, w;
             ahead.read(v, 0, p.x, at, width, t);
             if (p.res_scale) {
-                R::load(w, p.res_scale, 0, C, t);
+                par.read(w, PAR_SCALE);
 #pragma unroll
                 for (int e = 0; e < R::PAIRS; ++e) rh[e] = mul2(R::pair(v, e), R::pair(w, e));
             } else {
@@ -598,12 +653,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < R::PAIRS; ++e) d[e] = yh[e];
                     if (p.w_post) {
-                        R::load(w, p.w_post, 0, C, t);
+                        par.read(w, PAR_W_POST);
 #pragma unroll
                         for (int e = 0; e < R::PAIRS; ++e) d[e] = mul2(d[e], R::pair(w, e));
                     }
                     if (p.b_post) {
-                        R::load(w, p.b_post, 0, width, t);
+                        par.read(w, PAR_B_POST);
 #pragma unroll
                         for (int e = 0; e < R::PAIRS; ++e) d[e] = add2(d[e], R::pair(w, e));
                     }
@@ -640,7 +695,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int e = 0; e < R::PAIRS; ++e) acc[BACK_B_PRE][e] = add2(acc[BACK_B_PRE][e], n[e]);
                 }
                 if (p.w_pre) {
-                    R::load(w, p.w_pre, 0, C, t);
+                    par.read(w, PAR_W_PRE);
 #pragma unroll
                     for (int e = 0; e < R::PAIRS; ++e) n[e] = mul2(n[e], R::pair(w, e));
                 }
@@ -675,7 +730,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (p.dx) {
                 if (p.res_scale) {
-                    R::load(w, p.res_scale, 0, C, t);
+                    par.read(w, PAR_SCALE);
 #pragma unroll
                     for (int e = 0; e < R::PAIRS; ++e) rh[e] = mul2(d[e], R::pair(w, e));
                     R::store(p.dx, at, width, t, rh);
@@ -689,7 +744,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int e = 0; e < R::PAIRS; ++e) d[e] = mul2(d[e], R::pair(pg, e));
                 }
                 if (p.w_post) {
-                    R::load(w, p.w_post, 0, C, t);
+                    par.read(w, PAR_W_POST);
 #pragma unroll
                     for (int e = 0; e < R::PAIRS; ++e) d[e] = mul2(d[e], R::pair(w, e));
                 }
@@ -715,8 +770,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
     };
-    // Adds one sum over the block's slots, in their order, into dst (and clears it).
-    auto join_slots = [&](F2(&sum)[R::PAIRS], float *dst) {
+    // Adds one sum over the block's slots, in their order, clears it and hands each column's to put.
+    auto join_slots = [&](F2(&sum)[R::PAIRS], auto put) {
+        __syncthreads();
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             float a, b;
@@ -730,11 +786,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             float v = 0.0f;
 #pragma unroll 8
             for (int i = 0; i < RPB; ++i) v += join[i * W + c];
-            dst[c] = v;
+            put(c, v);
         }
         __syncthreads();
     };
-    auto put_part = [&](int q, F2(&sum)[R::PAIRS]) { join_slots(sum, part + ((int64_t)q * gridDim.x + blockIdx.x) * C); };
+    auto put_part = [&](int q, F2(&sum)[R::PAIRS]) {
+        float *dst = part + ((int64_t)q * gridDim.x + blockIdx.x) * C;
+        join_slots(sum, [&](int c, float v) { dst[c] = v; });
+    };
 
     typename R::Packed pg;
     if (SHORT) {
@@ -776,9 +835,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int64_t g = at / p.per_gate, last = min(end, (g + 1) * p.per_gate);
             rows(g, at + slot, last, RPB, (int)((last - at + RPB - 1) / RPB), pg);
             if (p.y) {
-                float *dst = seg + (blockIdx.x + g) * 2 * C;
-                join_slots(acc[BACK_A], dst);
-                join_slots(acc[BACK_B], dst + C);
+                for (int q = BACK_A; q <= BACK_B; ++q) {
+                    float *dst = seg + ((blockIdx.x + g) * 2 + (q - BACK_A)) * C;
+                    float *weighed = part + ((int64_t)q * gridDim.x + blockIdx.x) * C;
+                    const bool new_sum = at == begin;
+                    auto put = [&](int c, float v) {  // (the same thread for a column every time)
+                        dst[c] = v;
+                        v *= load_or<T>(p.gate, g * C + c, 1.0f);
+                        weighed[c] = new_sum ? v : weighed[c] + v;
+                    };
+                    if (q == BACK_A) join_slots(acc[BACK_A], put);
+                    else join_slots(acc[BACK_B], put);
+                }
             }
             at = last;
         }
@@ -788,74 +856,62 @@ __global__ void __launch_bounds__(THREADS, 1)
     put_part(BACK_B_PRE, acc[BACK_B_PRE]);
 }
 
-// Joins the fused pass's partial sums: 32 columns a block, its 32 warps over
-// slices of the partials, then the warps' in order. blockIdx.y: 0 dres_scale,
-// 1 dw_pre, 2 db_pre, 3 dw_post, 4 db_post, 5.. dgate of group y - 5 (long groups).
+// Joins the fused pass's partial sums: 32 columns a block, its 8 warps over the
+// partials in turn, then the warps' in order. blockIdx.y: 0 dres_scale, 1 dw_pre,
+// 2 db_pre, 3 dw_post, 4 db_post, then dgate of groups y - 5, y - 5 + (gridDim.y - 5), ...
+// (long groups).
 template <typename T>
-__global__ void __launch_bounds__(1024) norm_join(const __grid_constant__ NormArgs p, const __grid_constant__ BackPlan plan,
-                                                  const float *part, const float *seg, JoinOuts o) {
-    __shared__ float s[32][33];
+__global__ void __launch_bounds__(256) norm_join(const __grid_constant__ NormArgs p, const __grid_constant__ BackPlan plan,
+                                                 const float *part, const float *seg, JoinOuts o) {
+    __shared__ float s[2][8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t C = p.C, c = (int64_t)blockIdx.x * 32 + lane;
-    const bool in = c < C;
+    const int64_t C = p.C, c = (int64_t)blockIdx.x * 32 + lane, from = min(c, C - 1);
     const int what = blockIdx.y < BACK_SUMS ? (int)blockIdx.y : BACK_SUMS;
     T *out = static_cast<T *>(what < BACK_SUMS ? o.out[what] : o.dgate);
     if (!out) return;
-    auto over_warps = [&](float v) {
-        s[warp][lane] = v;
+    auto over_warps = [&](float a, float b) {
+        s[0][warp][lane] = a, s[1][warp][lane] = b;
         __syncthreads();
-        v = 0.0f;
-        if (warp == 0)
+        a = b = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v += s[i][lane];
+        for (int i = 0; i < 8; ++i) a += s[0][i][lane], b += s[1][i][lane];
         __syncthreads();
-        return v;
+        return make_float2(a, b);
     };
-    // block k's rows, and so its groups, as the fused pass cut them
-    auto first_row = [&](int64_t k) { return p.R * k / plan.blocks; };
-    if (what < BACK_SUMS && (what < BACK_A || plan.short_groups)) {
+    if (what < BACK_SUMS) {
+        const float *src = part + (int64_t)what * plan.blocks * C + from;
         float v = 0.0f;
-        if (in)
+#pragma unroll 8
+        for (int k = warp; k < plan.blocks; k += 8) v += src[k * C];
+        v = over_warps(v, 0.0f).x;
+        if (warp == 0 && c < C) out[c] = from_f32<T>(v);
+        return;
+    }
+    const int stride = gridDim.y - BACK_SUMS;
+    for (int64_t g = blockIdx.y - BACK_SUMS; g < plan.groups; g += stride) {
+        // the blocks whose rows meet the group's
+        const int64_t lo = g * p.per_gate, hi = min(p.R, lo + p.per_gate);
+        int k0 = (int)(lo * plan.blocks / p.R), k1 = (int)((hi - 1) * plan.blocks / p.R);
+        while (k0 + 1 < plan.blocks && p.R * (k0 + 1) / plan.blocks <= lo) ++k0;
+        while (k1 + 1 < plan.blocks && p.R * (k1 + 1) / plan.blocks < hi) ++k1;
+        float a = 0.0f, b = 0.0f;
+        const float *src = seg + 2 * g * C + from;
 #pragma unroll 4
-            for (int64_t k = warp; k < plan.blocks; k += 32) v += part[((int64_t)what * plan.blocks + k) * C + c];
-        v = over_warps(v);
-        if (warp == 0 && in) out[c] = from_f32<T>(v);
-    } else if (what < BACK_SUMS) {
-        float v = 0.0f;
-        if (in)
-            for (int64_t k = warp; k < plan.blocks; k += 32) {
-                const int64_t begin = first_row(k), end = first_row(k + 1);
-                if (begin >= end) continue;
-                for (int64_t g = begin / p.per_gate; g <= (end - 1) / p.per_gate; ++g)
-                    v = fmaf(load_or<T>(p.gate, p.gate ? g * C + c : 0, 1.0f), seg[(k + g) * 2 * C + (what == BACK_B ? C : 0) + c], v);
-            }
-        v = over_warps(v);
-        if (warp == 0 && in) out[c] = from_f32<T>(v);
-    } else {
-        // groups blockIdx.y - 5, + gridDim.y - 5, ...: the blocks whose rows meet the group's
-        for (int64_t g = blockIdx.y - BACK_SUMS; g < plan.groups; g += gridDim.y - BACK_SUMS) {
-            const int64_t lo = g * p.per_gate, hi = min(p.R, lo + p.per_gate);
-            int64_t k0 = lo * plan.blocks / p.R;
-            while (k0 > 0 && first_row(k0) > lo) --k0;
-            while (first_row(k0 + 1) <= lo) ++k0;
-            float a = 0.0f, b = 0.0f;
-            if (in)
-                for (int64_t k = k0 + warp; k < plan.blocks && first_row(k) < hi; k += 32) {
-                    if (first_row(k) >= first_row(k + 1)) continue;
-                    a += seg[(k + g) * 2 * C + c];
-                    b += seg[(k + g) * 2 * C + C + c];
-                }
-            a = over_warps(a), b = over_warps(b);
-            if (warp == 0 && in)
-                out[g * C + c] = from_f32<T>(fmaf(load_or<T>(p.w_post, c, 1.0f), a, load_or<T>(p.b_post, c, 0.0f) * b));
+        for (int k = k0 + warp; k <= k1; k += 8) {
+            a += src[2 * k * C];
+            b += src[(2 * k + 1) * C];
         }
+        const float2 v = over_warps(a, b);
+        if (warp == 0 && c < C)
+            out[g * C + c] = from_f32<T>(fmaf(load_or<T>(p.w_post, c, 1.0f), v.x, load_or<T>(p.b_post, c, 0.0f) * v.y));
     }
 }
 
 template <typename T, int V, int TPR>
 cudaError_t launch_fused(const NormArgs &p, const BackPlan &plan, float *part, float *seg, T *dgate, cudaStream_t st) {
     constexpr int EPT = 8, THREADS = FUSED_THREADS;
-    const size_t smem = BackAhead<Row<T, V, EPT, TPR>, THREADS>::BYTES + (size_t)(plan.short_groups ? 3 : 1) * THREADS * EPT * 4;
+    using R = Row<T, V, EPT, TPR>;
+    const size_t smem = BACK_ROWS_BYTES<R, THREADS> + Params<R, PARAMS, TPR>::BYTES + (plan.short_groups ? 2 * THREADS * EPT * 4 : 0);
     auto kernel = plan.short_groups ? norm_backward_fused<T, V, EPT, TPR, THREADS, true>
                                     : norm_backward_fused<T, V, EPT, TPR, THREADS, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -884,31 +940,36 @@ inline cudaError_t with_vector(int64_t C, Fn f) {
     return C % wide == 0 ? f(IntC<wide>()) : C % mid == 0 ? f(IntC<mid>()) : f(IntC<1>());
 }
 
+// 32 bytes of a row a thread.
 template <typename T, int V, int TPR>
 cudaError_t launch_rows(const NormArgs &p, cudaStream_t st) {
-    constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
-    auto kernel = norm_forward_rows<T, V, 8, TPR, THREADS>;
-    constexpr int smem = Ahead<Row<T, V, 8, TPR>, 2, 3, THREADS>::BYTES;
+    constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR, EPT = 32 / (int)sizeof(T);
+    using R = Row<T, V, EPT, TPR>;
+    auto kernel = norm_forward_rows<T, V, EPT, TPR, THREADS>;
+    constexpr int smem = Ahead<R, 2, 3, THREADS>::BYTES + Params<R, PARAMS, TPR>::BYTES;
     if (smem > 32 * 1024) {  // (48 KB with the static part need no leave)
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
     const int64_t blocks = (p.R + RPB - 1) / RPB;
     const FastDiv per = make_fastdiv((uint32_t)std::min(p.per_gate, p.R));
-    kernel<<<(unsigned)std::min<int64_t>(blocks, SMS * 1024 / THREADS), THREADS, smem, st>>>(p, per);
+    kernel<<<(unsigned)std::min<int64_t>(blocks, SMS * (THREADS > 256 ? 1 : 2)), THREADS, smem, st>>>(p, per);
     return cudaGetLastError();
 }
 
 template <typename T, int V>
 cudaError_t launch_forward(const NormArgs &p, cudaStream_t st) {
-    if (p.C <= 32) return launch_rows<T, V, 4>(p, st);
-    if (p.C <= 128) return launch_rows<T, V, 16>(p, st);
-    if (p.C <= 256) return launch_rows<T, V, 32>(p, st);
-    if (p.C <= 512) return launch_rows<T, V, 64>(p, st);
-    if (p.C <= 1024) return launch_rows<T, V, 128>(p, st);
-    if (p.C <= 2048) return launch_rows<T, V, 256>(p, st);
-    if (p.C <= 4096) return launch_rows<T, V, 512>(p, st);
-    return launch_rows<T, V, 1024>(p, st);
+    const int64_t threads = (p.C * (int64_t)sizeof(T) + 31) / 32;  // of a row
+    if (threads <= 4) return launch_rows<T, V, 4>(p, st);
+    if (threads <= 8) return launch_rows<T, V, 8>(p, st);
+    if (threads <= 16) return launch_rows<T, V, 16>(p, st);
+    if (threads <= 32) return launch_rows<T, V, 32>(p, st);
+    if (threads <= 64) return launch_rows<T, V, 64>(p, st);
+    if (threads <= 128) return launch_rows<T, V, 128>(p, st);
+    if (threads <= 256) return launch_rows<T, V, 256>(p, st);
+    if constexpr (sizeof(T) == 4)
+        if (threads > 512) return launch_rows<T, V, 1024>(p, st);
+    return launch_rows<T, V, 512>(p, st);
 }
 
 }  // namespace
@@ -936,7 +997,7 @@ cudaError_t launch_norm_backward(const NormArgs &args, const ColumnGrads &g, voi
         const JoinOuts o = {{g.dres_scale, g.dw_pre, g.db_pre, g.dw_post, g.db_post}, fused.short_groups ? nullptr : g.dgate};
         const dim3 grid((unsigned)((p.C + 31) / 32),
                         BACK_SUMS + (o.dgate ? (unsigned)std::min<int64_t>(fused.groups, 1024) : 0));
-        norm_join<T><<<grid, 1024, 0, st>>>(p, fused, part, seg, o);
+        norm_join<T><<<grid, 256, 0, st>>>(p, fused, part, seg, o);
         return cudaGetLastError();
     }
     const SumPlan plan = plan_sums(p.R, p.per_gate);
