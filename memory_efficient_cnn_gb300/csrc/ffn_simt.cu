@@ -1,90 +1,195 @@
-// fp32 products of the gated feed-forward on the CUDA cores: a 64 x 64 tile of D for each block of 256 threads, 4 x 4
-// outputs a thread, 16 steps of K staged in shared memory as fp32.
+// fp32 products of the gated feed-forward on the CUDA cores.
+//
+// A 64 x 64 tile of D (EPI_GATED: 32 columns of g and the same of u) for each
+// block of 256 threads: two groups of 128, each with half of the K blocks and
+// 8 x 4 outputs a thread, so that outputs of as few tiles as there are SMs still
+// have two warps on each scheduler; the groups' sums are added at the end. The
+// operands' elements are copied asynchronously to shared memory with K outermost,
+// three blocks of 16 K steps in flight, from either layout and any alignment.
+// The inner product is on pairs of columns (paired fp32 FMAs: half the issue
+// slots, which leaves room for the shared-memory reads).
 #include "gated_ffn.cuh"
+#include "tc_ptx.cuh"
 
 namespace im2win {
 namespace ffn {
 namespace {
 
-constexpr int BM = 64, BN = 64, BK = 16, THREADS = 256, PAD = 4;
+constexpr int BM = 64, BN = 64, BK = 16, GROUP = 128, GROUPS = 2, THREADS = GROUP * GROUPS, STAGES = 3;
+constexpr int PITCH = BM + 4;                    // floats; 16-byte aligned rows
+constexpr int STAGE = 2 * BK * PITCH;            // floats of A and B
+constexpr int SMEM = GROUPS * STAGES * STAGE * 4;
 
-// Stages rows i0.. (64) and steps k0.. (16) of an operand as s[k][i], zero
-// outside; neighbouring threads read neighbouring elements of the operand.
-template <bool KMAJ>
-__device__ __forceinline__ void stage(float (&s)[BK][BM + PAD], const float *p, int64_t ld, int i0, int k0, int I, int K) {
+__device__ __forceinline__ void copy4(float *dst, const float *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(in ? 4 : 0)
+                 : "memory");
+}
+
+// Starts copying output indexes i0.. (N of them) and K steps k0.. (16) of an operand
+// to s[k][i], zero outside; neighbouring threads copy neighbouring elements.
+template <bool KMAJ, int N>
+__device__ __forceinline__ void stage(float *s, const float *p, int64_t ld, int i0, int k0, int I, int K, int t) {
 #pragma unroll
-    for (int e = threadIdx.x; e < BM * BK; e += THREADS) {
-        const int i = KMAJ ? e / BK : e % BM, k = KMAJ ? e % BK : e / BM;
+    for (int e = 0; e < N * BK / GROUP; ++e) {
+        const int x = e * GROUP + t;
+        const int i = KMAJ ? x / BK : x % N, k = KMAJ ? x % BK : x / N;
         const bool in = i0 + i < I && k0 + k < K;
         const int64_t at = KMAJ ? (int64_t)(i0 + i) * ld + (k0 + k) : (int64_t)(k0 + k) * ld + (i0 + i);
-        s[k][i] = in ? p[at] : 0.0f;
+        copy4(s + k * PITCH + i, in ? p + at : p, in);
     }
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word at `p` in the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ uint64_t load_of_rank(const uint64_t *p, int rank) {
+    uint32_t a;
+    uint64_t v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return v;
+}
+
 template <bool AK, bool BKM, int EPI, int ACT>
-__global__ void __launch_bounds__(THREADS) simt_product(Product p, int tiles_n) {
-    constexpr int NB = EPI == EPI_GATED ? 2 : 1;  // accumulators
-    __shared__ float sa[BK][BM + PAD], sb[NB][BK][BN + PAD];
-    const int m0 = (int)(blockIdx.x / tiles_n) * BM, n0 = (int)(blockIdx.x % tiles_n) * BN;
-    const int tm = (threadIdx.x / 16) * 4, tn = (threadIdx.x % 16) * 4;
-    float acc[NB][4][4] = {};
-    const int segs = EPI != EPI_GATED && p.a1.p ? 2 : 1;
-    for (int seg = 0; seg < segs; ++seg) {
-        const float *a = static_cast<const float *>(seg ? p.a1.p : p.a0.p);
-        const float *b = static_cast<const float *>(seg ? p.b1.p : p.b0.p);
-        for (int k0 = 0; k0 < p.K; k0 += BK) {
-            stage<AK>(sa, a, p.a0.ld, m0, k0, p.M, p.K);
-            stage<BKM>(sb[0], b, p.b0.ld, n0, k0, p.N, p.K);
-            if (NB == 2) stage<BKM>(sb[NB - 1], static_cast<const float *>(p.b1.p), p.b1.ld, n0, k0, p.N, p.K);
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < BK; ++k) {
-                float av[4], bv[NB][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) av[i] = sa[k][tm + i];
-#pragma unroll
-                for (int q = 0; q < NB; ++q)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) bv[q][j] = sb[q][k][tn + j];
-#pragma unroll
-                for (int q = 0; q < NB; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[q][i][j] = fmaf(av[i], bv[q][j], acc[q][i][j]);
+__global__ void __launch_bounds__(THREADS) simt_product(const __grid_constant__ Product p, int tiles_n, int tiles, int share) {
+    extern __shared__ uint4 dyn[];
+    constexpr bool GATED = EPI == EPI_GATED;
+    constexpr int COLS = GATED ? BN / 2 : BN;
+    const int rank = (int)blockIdx.x % share, id = (int)blockIdx.x / share;
+    const int z = p.batch ? id / tiles : 0, tile = id - z * tiles;
+    const int m0 = tile / tiles_n * BM, n0 = tile % tiles_n * COLS;
+    const int group = threadIdx.x / GROUP, t = threadIdx.x % GROUP;
+    float *mine = reinterpret_cast<float *>(dyn) + group * STAGES * STAGE;
+    const int tm = t / 16 * 8, tn = t % 16;
+    // the thread's two pairs of columns, within a stage's row of B
+    const int c0 = GATED ? tn * 2 : tn * 4, c1 = GATED ? COLS + tn * 2 : tn * 4 + 2;
+    const int segs = !GATED && !p.batch && p.a1.p ? 2 : 1;
+    const int KB = (p.K + BK - 1) / BK, total = KB * segs;
+
+    // the group's K blocks: `first`, `first` + step, ...
+    const int first = rank * GROUPS + group, step = GROUPS * share;
+    auto start = [&](int j) {  // the group's j-th
+        const int b = first + j * step;
+        if (b < total) {
+            const int seg = b >= KB ? 1 : 0, k0 = (b - seg * KB) * BK;
+            float *sa = mine + j % STAGES * STAGE, *sb = sa + BK * PITCH;
+            stage<AK, BM>(sa, static_cast<const float *>(seg || z ? p.a1.p : p.a0.p), p.a0.ld, m0, k0, p.M, p.K, t);
+            if (GATED) {
+                stage<BKM, COLS>(sb, static_cast<const float *>(p.b0.p), p.b0.ld, n0, k0, p.N, p.K, t);
+                stage<BKM, COLS>(sb + COLS, static_cast<const float *>(p.b1.p), p.b0.ld, n0, k0, p.N, p.K, t);
+            } else {
+                stage<BKM, BN>(sb, static_cast<const float *>(seg || z ? p.b1.p : p.b0.p), p.b0.ld, n0, k0, p.N, p.K, t);
             }
-            __syncthreads();
         }
-    }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    F2 acc[4][4];  // [pair of rows][column]
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + tm + i, n = n0 + tn + j;
-            if (m >= p.M || n >= p.N) continue;
-            float *out = static_cast<float *>(p.out) + (int64_t)m * p.ldo + n;
-            const int64_t at = kept_index(m, n, p.N);
-            if (EPI == EPI_STORE) {
-                *out = acc[0][i][j];
-            } else if (EPI == EPI_GATED) {
-                const float g = acc[0][i][j], u = acc[NB - 1][i][j];
-                *out = act_value<ACT>(g) * u;
-                if (p.g) p.g[at] = g, p.u[at] = u;
-            } else {
-                float a, d;
-                act_both<ACT>(p.g[at], a, d);
-                *out = acc[0][i][j] * p.u[at] * d;
-                static_cast<float *>(p.out2)[(int64_t)m * p.ldo + n] = acc[0][i][j] * a;
-            }
+        for (int j = 0; j < 4; ++j) acc[i][j] = f2(0.0f);
+    start(0);
+    start(1);
+#pragma unroll 1
+    for (int j = 0; first + j * step < total; ++j) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        // every thread's copies of this block have landed, and every thread is done with the
+        // block before it, whose stage the next copies take
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(GROUP) : "memory");
+        start(j + 2);
+        const float *sa = mine + j % STAGES * STAGE, *sb = sa + BK * PITCH;
+#pragma unroll
+        for (int k = 0; k < BK; ++k) {
+            const ulonglong2 lo = *reinterpret_cast<const ulonglong2 *>(sa + k * PITCH + tm);
+            const ulonglong2 hi = *reinterpret_cast<const ulonglong2 *>(sa + k * PITCH + tm + 4);
+            const float2 b0 = *reinterpret_cast<const float2 *>(sb + k * PITCH + c0);
+            const float2 b1 = *reinterpret_cast<const float2 *>(sb + k * PITCH + c1);
+            const F2 a[4] = {{lo.x}, {lo.y}, {hi.x}, {hi.y}}, b[4] = {f2(b0.x), f2(b0.y), f2(b1.x), f2(b1.y)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) acc[i][n] = fma2(a[i], b[n], acc[i][n]);
         }
+    }
+    // Every group's sums into its block's shared memory, [pair of rows][column][thread]; then
+    // each block of the cluster finishes its part of the row pairs.
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    uint64_t *sum = reinterpret_cast<uint64_t *>(dyn);
+    constexpr int PART = 16 * GROUP;  // of a group
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) sum[group * PART + (i * 4 + n) * GROUP + t] = acc[i][n].v;
+    cluster_sync();
+    const int threads = THREADS * share;  // of the cluster, over 4 row pairs of GROUP threads
+    for (int e = rank * THREADS + (int)threadIdx.x; e < 4 * GROUP; e += threads) {
+        const int i = e / GROUP, t2 = e % GROUP;
+        F2 v[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
+        for (int r = 0; r < share; ++r)
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    F2 x;
+                    x.v = load_of_rank(sum + g * PART + (i * 4 + n) * GROUP + t2, r);
+                    v[n] = add2(v[n], x);
+                }
+        const int tn2 = t2 % 16, m = m0 + t2 / 16 * 8 + 2 * i;
+        float d[2][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) split(v[n], d[0][n], d[1][n]);
+#pragma unroll
+        for (int row = 0; row < 2; ++row)
+#pragma unroll
+            for (int j = 0; j < (GATED ? 2 : 4); ++j) {
+                const int n = n0 + (GATED ? tn2 * 2 : tn2 * 4) + j;
+                if (m + row >= p.M || n >= p.N) continue;
+                float *out = static_cast<float *>(z ? p.out2 : p.out) + (int64_t)(m + row) * p.ldo + n;
+                const int64_t at = kept_index(m + row, n, p.N);
+                if (EPI == EPI_STORE) {
+                    *out = d[row][j];
+                } else if (GATED) {
+                    const float g = d[row][j], u = d[row][2 + j];
+                    *out = act_value<ACT>(g) * u;
+                    if (p.g) p.g[at] = g, p.u[at] = u;
+                } else {
+                    float a, s;
+                    act_both<ACT>(p.g[at], a, s);
+                    *out = d[row][j] * p.u[at] * s;
+                    static_cast<float *>(p.out2)[(int64_t)(m + row) * p.ldo + n] = d[row][j] * a;
+                }
+            }
+    }
+    cluster_sync();  // the others' shared memory is read no more
 }
 
 template <bool AK, bool BKM, int EPI, int ACT>
 cudaError_t launch(const Product &p, cudaStream_t st) {
-    const int64_t tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
-    if (tm * tn > 0x7fffffff) return cudaErrorInvalidValue;
-    simt_product<AK, BKM, EPI, ACT><<<(unsigned)(tm * tn), THREADS, 0, st>>>(p, (int)tn);
-    return cudaGetLastError();
+    constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;
+    const int64_t tm = (p.M + BM - 1) / BM, tn = (p.N + COLS - 1) / COLS, blocks = tm * tn * (p.batch ? 2 : 1);
+    if (blocks > 0x7fffffff / 8) return cudaErrorInvalidValue;
+    auto kernel = simt_product<AK, BKM, EPI, ACT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    // blocks of a tile: as long as all of them are within three to an SM and each has 8 K blocks
+    const int64_t kb = (int64_t)((p.K + BK - 1) / BK) * (EPI != EPI_GATED && !p.batch && p.a1.p ? 2 : 1);
+    int share = 1;
+    while (share < 8 && blocks * share * 2 <= 3 * 152 && kb >= 16 * share) share *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * share));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)share;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, (int)tn, (int)(tm * tn), share);
 }
 
 }  // namespace

@@ -193,14 +193,7 @@ struct Sequence {
             e = launch_tc(p, q.dtype == IM2WIN_BF16, static_cast<uint32_t *>(ws), !cleared, part, st);
         } else {
             if (!cleared) e = cudaMemsetAsync(ws, 0, kStatusBytes, st);
-            Product one = p;
-            one.batch = false;
-            if (p.batch) one.a1 = one.b1 = Operand();
-            if (e == cudaSuccess) e = launch_simt(one, st);
-            if (p.batch && e == cudaSuccess) {
-                one.a0 = p.a1, one.b0 = p.b1, one.out = p.out2;
-                e = launch_simt(one, st);
-            }
+            if (e == cudaSuccess) e = launch_simt(p, st);
         }
         cleared = true;
     }

@@ -53,7 +53,7 @@ struct Product {
     int64_t ldo = 0;                   // row pitch of out and out2 in elements
 };
 
-// CUDA cores, fp32 (no batch).
+// CUDA cores, fp32.
 cudaError_t launch_simt(const Product &p, cudaStream_t st);
 
 // Tensor cores: fp16/bf16; operands 16-byte aligned with pitches that are multiples
