@@ -1,8 +1,8 @@
 // fp32 products of the gated feed-forward on the CUDA cores.
 //
-// A 64 x 64 tile of D (EPI_GATED: 32 columns of g and the same of u) for each
+// A 128 x 64 tile of D (EPI_GATED: 32 columns of g and the same of u) for each
 // block of 256 threads: two groups of 128, each with half of the K blocks and
-// 8 x 4 outputs a thread, so that outputs of as few tiles as there are SMs still
+// 8 x 8 outputs a thread, so that outputs of as few tiles as there are SMs still
 // have two warps on each scheduler; the groups' sums are added at the end. The
 // operands' elements are copied asynchronously to shared memory with K outermost,
 // three blocks of 16 K steps in flight, from either layout and any alignment.
@@ -15,25 +15,42 @@ namespace im2win {
 namespace ffn {
 namespace {
 
-constexpr int BM = 64, BN = 64, BK = 16, GROUP = 128, GROUPS = 2, THREADS = GROUP * GROUPS, STAGES = 3;
-constexpr int PITCH = BM + 4;                    // floats; 16-byte aligned rows
-constexpr int STAGE = 2 * BK * PITCH;            // floats of A and B
+constexpr int BM = 128, BN = 64, BK = 16, GROUP = 128, GROUPS = 2, THREADS = GROUP * GROUPS, STAGES = 3;
+constexpr int PITCH_A = BM + 4, PITCH_B = BN + 4;    // floats; 16-byte aligned rows
+constexpr int STAGE = BK * (PITCH_A + PITCH_B);      // floats
 constexpr int SMEM = GROUPS * STAGES * STAGE * 4;
+static_assert(SMEM >= GROUPS * 32 * GROUP * 8, "the sums at the end take the stages' place");
 
 __device__ __forceinline__ void copy4(float *dst, const float *src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
                  "r"(in ? 4 : 0)
                  : "memory");
 }
+__device__ __forceinline__ void copy16(float *dst, const float *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(bytes)
+                 : "memory");
+}
 
 // Starts copying output indexes i0.. (N of them) and K steps k0.. (16) of an operand
-// to s[k][i], zero outside; neighbouring threads copy neighbouring elements.
-template <bool KMAJ, int N>
+// to s[k][i], zero outside; neighbouring threads copy neighbouring elements, four
+// at a time where the output index is innermost and rows are 16-byte aligned.
+template <bool KMAJ, int N, int PITCH>
 __device__ __forceinline__ void stage(float *s, const float *p, int64_t ld, int i0, int k0, int I, int K, int t) {
+    if (!KMAJ && (ld & 3) == 0) {
+#pragma unroll
+        for (int e = 0; e < N * BK / (4 * GROUP); ++e) {
+            const int x = e * GROUP + t, i = x % (N / 4) * 4, k = x / (N / 4);
+            const int left = k0 + k < K ? min(I - i0 - i, 4) : 0;
+            copy16(s + k * PITCH + i, left > 0 ? p + (int64_t)(k0 + k) * ld + (i0 + i) : p, left > 0 ? 4 * left : 0);
+        }
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < N * BK / GROUP; ++e) {
         const int x = e * GROUP + t;
-        const int i = KMAJ ? x / BK : x % N, k = KMAJ ? x % BK : x / N;
+        // (K innermost: 8 steps of 4 output indexes a warp, whose words fall in 32 banks)
+        const int i = KMAJ ? x / 8 % N : x % N, k = KMAJ ? x % 8 + x / (8 * N) * 8 : x / N;
         const bool in = i0 + i < I && k0 + k < K;
         const int64_t at = KMAJ ? (int64_t)(i0 + i) * ld + (k0 + k) : (int64_t)(k0 + k) * ld + (i0 + i);
         copy4(s + k * PITCH + i, in ? p + at : p, in);
@@ -53,7 +70,7 @@ __device__ __forceinline__ uint64_t load_of_rank(const uint64_t *p, int rank) {
 }
 
 template <bool AK, bool BKM, int EPI, int ACT>
-__global__ void __launch_bounds__(THREADS) simt_product(const __grid_constant__ Product p, int tiles_n, int tiles, int share) {
+__global__ void __launch_bounds__(THREADS, 2) simt_product(const __grid_constant__ Product p, int tiles_n, int tiles, int share) {
     extern __shared__ uint4 dyn[];
     constexpr bool GATED = EPI == EPI_GATED;
     constexpr int COLS = GATED ? BN / 2 : BN;
@@ -62,9 +79,9 @@ __global__ void __launch_bounds__(THREADS) simt_product(const __grid_constant__ 
     const int m0 = tile / tiles_n * BM, n0 = tile % tiles_n * COLS;
     const int group = threadIdx.x / GROUP, t = threadIdx.x % GROUP;
     float *mine = reinterpret_cast<float *>(dyn) + group * STAGES * STAGE;
-    const int tm = t / 16 * 8, tn = t % 16;
-    // the thread's two pairs of columns, within a stage's row of B
-    const int c0 = GATED ? tn * 2 : tn * 4, c1 = GATED ? COLS + tn * 2 : tn * 4 + 2;
+    // the thread's rows r0.., r0 + 64.. and columns c0.., c0 + 32.. (of g and of u), four each:
+    // a warp's reads of a stage are contiguous
+    const int r0 = t / 8 * 4, c0 = t % 8 * 4;
     const int segs = !GATED && !p.batch && p.a1.p ? 2 : 1;
     const int KB = (p.K + BK - 1) / BK, total = KB * segs;
 
@@ -74,22 +91,22 @@ __global__ void __launch_bounds__(THREADS) simt_product(const __grid_constant__ 
         const int b = first + j * step;
         if (b < total) {
             const int seg = b >= KB ? 1 : 0, k0 = (b - seg * KB) * BK;
-            float *sa = mine + j % STAGES * STAGE, *sb = sa + BK * PITCH;
-            stage<AK, BM>(sa, static_cast<const float *>(seg || z ? p.a1.p : p.a0.p), p.a0.ld, m0, k0, p.M, p.K, t);
+            float *sa = mine + j % STAGES * STAGE, *sb = sa + BK * PITCH_A;
+            stage<AK, BM, PITCH_A>(sa, static_cast<const float *>(seg || z ? p.a1.p : p.a0.p), p.a0.ld, m0, k0, p.M, p.K, t);
             if (GATED) {
-                stage<BKM, COLS>(sb, static_cast<const float *>(p.b0.p), p.b0.ld, n0, k0, p.N, p.K, t);
-                stage<BKM, COLS>(sb + COLS, static_cast<const float *>(p.b1.p), p.b0.ld, n0, k0, p.N, p.K, t);
+                stage<BKM, COLS, PITCH_B>(sb, static_cast<const float *>(p.b0.p), p.b0.ld, n0, k0, p.N, p.K, t);
+                stage<BKM, COLS, PITCH_B>(sb + COLS, static_cast<const float *>(p.b1.p), p.b0.ld, n0, k0, p.N, p.K, t);
             } else {
-                stage<BKM, BN>(sb, static_cast<const float *>(seg || z ? p.b1.p : p.b0.p), p.b0.ld, n0, k0, p.N, p.K, t);
+                stage<BKM, BN, PITCH_B>(sb, static_cast<const float *>(seg || z ? p.b1.p : p.b0.p), p.b0.ld, n0, k0, p.N, p.K, t);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    F2 acc[4][4];  // [pair of rows][column]
+    F2 acc[4][8];  // [pair of rows][column]
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f2(0.0f);
+        for (int j = 0; j < 8; ++j) acc[i][j] = f2(0.0f);
     start(0);
     start(1);
 #pragma unroll 1
@@ -99,18 +116,19 @@ __global__ void __launch_bounds__(THREADS) simt_product(const __grid_constant__ 
         // block before it, whose stage the next copies take
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(GROUP) : "memory");
         start(j + 2);
-        const float *sa = mine + j % STAGES * STAGE, *sb = sa + BK * PITCH;
+        const float *sa = mine + j % STAGES * STAGE, *sb = sa + BK * PITCH_A;
 #pragma unroll
         for (int k = 0; k < BK; ++k) {
-            const ulonglong2 lo = *reinterpret_cast<const ulonglong2 *>(sa + k * PITCH + tm);
-            const ulonglong2 hi = *reinterpret_cast<const ulonglong2 *>(sa + k * PITCH + tm + 4);
-            const float2 b0 = *reinterpret_cast<const float2 *>(sb + k * PITCH + c0);
-            const float2 b1 = *reinterpret_cast<const float2 *>(sb + k * PITCH + c1);
-            const F2 a[4] = {{lo.x}, {lo.y}, {hi.x}, {hi.y}}, b[4] = {f2(b0.x), f2(b0.y), f2(b1.x), f2(b1.y)};
+            const ulonglong2 lo = *reinterpret_cast<const ulonglong2 *>(sa + k * PITCH_A + r0);
+            const ulonglong2 hi = *reinterpret_cast<const ulonglong2 *>(sa + k * PITCH_A + r0 + 64);
+            const float4 b0 = *reinterpret_cast<const float4 *>(sb + k * PITCH_B + c0);
+            const float4 b1 = *reinterpret_cast<const float4 *>(sb + k * PITCH_B + c0 + 32);
+            const F2 a[4] = {{lo.x}, {lo.y}, {hi.x}, {hi.y}};
+            const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int n = 0; n < 8; ++n)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) acc[i][n] = fma2(a[i], b[n], acc[i][n]);
+                for (int i = 0; i < 4; ++i) acc[i][n] = fma2(a[i], f2(b[n]), acc[i][n]);
         }
     }
     // Every group's sums into its block's shared memory, [pair of rows][column][thread]; then
@@ -118,50 +136,55 @@ __global__ void __launch_bounds__(THREADS) simt_product(const __grid_constant__ 
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     uint64_t *sum = reinterpret_cast<uint64_t *>(dyn);
-    constexpr int PART = 16 * GROUP;  // of a group
+    constexpr int PART = 32 * GROUP;  // of a group
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) sum[group * PART + (i * 4 + n) * GROUP + t] = acc[i][n].v;
+        for (int n = 0; n < 8; ++n) sum[group * PART + (i * 8 + n) * GROUP + t] = acc[i][n].v;
     cluster_sync();
-    const int threads = THREADS * share;  // of the cluster, over 4 row pairs of GROUP threads
-    for (int e = rank * THREADS + (int)threadIdx.x; e < 4 * GROUP; e += threads) {
-        const int i = e / GROUP, t2 = e % GROUP;
-        F2 v[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
-        for (int r = 0; r < share; ++r)
+    // 4 columns (of g and of u) of a row pair a thread, over all threads of the cluster
+    constexpr int HALVES = GATED ? 1 : 2;
+    for (int e = rank * THREADS + (int)threadIdx.x; e < 4 * HALVES * GROUP; e += THREADS * share) {
+        const int t2 = e % GROUP, i = e / GROUP % 4, half = e / GROUP / 4;
+        F2 v[GATED ? 8 : 4];
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g)
+        for (int n = 0; n < (GATED ? 8 : 4); ++n) {
+            const uint64_t *at = sum + (i * 8 + half * 4 + n) * GROUP + t2;
+            v[n] = f2(0.0f);
+            for (int r = 0; r < share; ++r)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
+                for (int g = 0; g < GROUPS; ++g) {
                     F2 x;
-                    x.v = load_of_rank(sum + g * PART + (i * 4 + n) * GROUP + t2, r);
+                    x.v = load_of_rank(at + g * PART, r);
                     v[n] = add2(v[n], x);
                 }
-        const int tn2 = t2 % 16, m = m0 + t2 / 16 * 8 + 2 * i;
-        float d[2][4];
+        }
+        const int m = m0 + t2 / 8 * 4 + (i & 1) * 2 + (i >> 1) * 64;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) split(v[n], d[0][n], d[1][n]);
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + half * 32 + t2 % 8 * 4 + j;
+            if (n >= p.N) break;
+            float d[2], du[2];
+            split(v[j], d[0], d[1]);
+            if (GATED) split(v[GATED ? 4 + j : j], du[0], du[1]);
 #pragma unroll
-        for (int row = 0; row < 2; ++row)
-#pragma unroll
-            for (int j = 0; j < (GATED ? 2 : 4); ++j) {
-                const int n = n0 + (GATED ? tn2 * 2 : tn2 * 4) + j;
-                if (m + row >= p.M || n >= p.N) continue;
+            for (int row = 0; row < 2; ++row) {
+                if (m + row >= p.M) break;
                 float *out = static_cast<float *>(z ? p.out2 : p.out) + (int64_t)(m + row) * p.ldo + n;
                 const int64_t at = kept_index(m + row, n, p.N);
                 if (EPI == EPI_STORE) {
-                    *out = d[row][j];
+                    *out = d[row];
                 } else if (GATED) {
-                    const float g = d[row][j], u = d[row][2 + j];
-                    *out = act_value<ACT>(g) * u;
-                    if (p.g) p.g[at] = g, p.u[at] = u;
+                    *out = act_value<ACT>(d[row]) * du[row];
+                    if (p.g) p.g[at] = d[row], p.u[at] = du[row];
                 } else {
                     float a, s;
                     act_both<ACT>(p.g[at], a, s);
-                    *out = d[row][j] * p.u[at] * s;
-                    static_cast<float *>(p.out2)[(int64_t)(m + row) * p.ldo + n] = d[row][j] * a;
+                    *out = d[row] * p.u[at] * s;
+                    static_cast<float *>(p.out2)[(int64_t)(m + row) * p.ldo + n] = d[row] * a;
                 }
             }
+        }
     }
     cluster_sync();  // the others' shared memory is read no more
 }
@@ -174,10 +197,16 @@ cudaError_t launch(const Product &p, cudaStream_t st) {
     auto kernel = simt_product<AK, BKM, EPI, ACT>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    // blocks of a tile: as long as all of them are within three to an SM and each has 8 K blocks
+    // Blocks of a tile: an SM's blocks share its FMA rate, so a launch takes as long as the
+    // fullest SM's blocks one after the other, each with its K blocks and about 8 more for its
+    // start and end.
     const int64_t kb = (int64_t)((p.K + BK - 1) / BK) * (EPI != EPI_GATED && !p.batch && p.a1.p ? 2 : 1);
     int share = 1;
-    while (share < 8 && blocks * share * 2 <= 3 * 152 && kb >= 16 * share) share *= 2;
+    int64_t best = 0;
+    for (int s = 1; s <= 8; ++s) {
+        const int64_t cost = (blocks * s + 151) / 152 * (kb / s + 8);
+        if (best == 0 || cost < best) best = cost, share = s;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks * share));
     cfg.blockDim = dim3(THREADS);
