@@ -12,7 +12,7 @@ import functools
 
 import torch
 
-from ._binding import _check, _cuda, _dtype_code, _same_device, lib
+from ._binding import _DTYPE, _check, _cuda, _dtype_code, _same_device, lib
 
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
@@ -328,7 +328,7 @@ def residual_norm_backward(dr, dn, x: torch.Tensor, y: torch.Tensor | None = Non
 # ---------------------------------------------------------------- gradient clipping
 def im2win_clip_grad_norm_size(sizes) -> int:
     out = ctypes.c_size_t(0)
-    arr = (ctypes.c_int64 * len(sizes))(*sizes)
+    arr = sizes if isinstance(sizes, ctypes.Array) else (ctypes.c_int64 * len(sizes))(*sizes)
     _check("im2win_clip_grad_norm_size", lib().im2win_clip_grad_norm_size(arr, len(sizes), ctypes.byref(out)))
     return out.value
 
@@ -348,16 +348,23 @@ def _clip_check(fn, grads, outs, device: int):
         _cuda(*given)
         _same_device(fn, *given)
         raise ValueError(f"{fn}: every tensor must be on one device")
-    return [_dtype_code(t) for t in grads]
+    try:
+        return (ctypes.c_int * len(grads))(*[_DTYPE[t.dtype] for t in grads])
+    except KeyError:
+        return [_dtype_code(t) for t in grads]  # raises
 
 
-def _clip(fn, grads, outs, sizes, codes, max_norm, eps, norm, ws):
+def _counts(grads):
+    return (ctypes.c_int64 * len(grads))(*[t.numel() for t in grads])
+
+
+def _clip(fn, grads, outs, counts, codes, max_norm, eps, norm, ws):
     k = len(grads)
-    pointers, counts, types = ctypes.c_void_p * k, ctypes.c_int64 * k, ctypes.c_int * k
+    pointers = ctypes.c_void_p * k
     at = pointers(*[t.data_ptr() for t in grads])
     to = None if outs is None else at if outs is grads else pointers(*[t.data_ptr() for t in outs])
-    _check(fn, lib().im2win_clip_grad_norm(at, to, counts(*sizes), types(*codes), k, max_norm, eps, norm.data_ptr(),
-                                           ws.data_ptr(), _bytes(ws), _stream(norm.get_device())))
+    _check(fn, lib().im2win_clip_grad_norm(at, to, counts, codes, k, max_norm, eps, norm.data_ptr(), ws.data_ptr(),
+                                           _bytes(ws), _stream(norm.get_device())))
 
 
 def im2win_clip_grad_norm(grads, outs, max_norm: float, eps: float, norm, ws) -> None:
@@ -371,22 +378,22 @@ def im2win_clip_grad_norm(grads, outs, max_norm: float, eps: float, norm, ws) ->
     _same_device(fn, norm, ws)
     _cuda(norm, ws)
     codes = _clip_check(fn, grads, outs, norm.get_device())
-    _clip(fn, grads, outs, [t.numel() for t in grads], codes, max_norm, eps, norm, ws)
+    _clip(fn, grads, outs, _counts(grads), codes, max_norm, eps, norm, ws)
 
 
 def _clip_lists(fn, grads, outs, max_norm, eps, ws):
     if not grads:
         raise ValueError(f"{fn}: no gradients")
     codes = _clip_check(fn, grads, outs, grads[0].get_device())
-    sizes = [t.numel() for t in grads]
+    counts = _counts(grads)
     device = grads[0].device
     if ws is None:
-        ws = _empty(im2win_clip_grad_norm_size(sizes), device)
+        ws = _empty(im2win_clip_grad_norm_size(counts), device)
     else:
         _same_device(fn, grads[0], ws)
         _cuda(ws)
     norm = torch.empty((), dtype=torch.float32, device=device)
-    _clip(fn, grads, outs, sizes, codes, max_norm, eps, norm, ws)
+    _clip(fn, grads, outs, counts, codes, max_norm, eps, norm, ws)
     return norm
 
 
