@@ -39,7 +39,7 @@ struct Problem {
           tc(dtype_ != IM2WIN_F32), Cp(tc ? (C_ + 7) / 8 * 8 : C_), Fp(tc ? (F_ + 7) / 8 * 8 : F_) {}
 
     // the forward pass of few rows has kernels of its own
-    bool few() const { return R <= few_rows(dtype); }
+    bool few() const { return is_few(R, C, F, dtype); }
     size_t rows_c(int64_t rows) const { return (size_t)(rows * Cp) * esz; }
     size_t rows_f(int64_t rows) const { return (size_t)(rows * Fp) * esz; }
 

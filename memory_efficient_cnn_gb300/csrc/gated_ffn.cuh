@@ -69,7 +69,7 @@ struct TcPlan {
 TcPlan plan_tc(const Product &p);
 cudaError_t launch_tc(const Product &p, bool bf16, uint32_t *status, bool clear_status, void *part, cudaStream_t st);
 
-// The forward pass of few rows (R <= few_rows(dtype)), from dense matrices of any
+// The forward pass of few rows (where is_few), from dense matrices of any
 // alignment that their type allows; h and its remainder h_lo (16-bit types) have
 // rows of ldh elements, a multiple of 8 there.
 struct Few {
@@ -80,7 +80,7 @@ struct Few {
     float *g, *u;
     uint32_t *status;
 };
-int few_rows(int dtype);
+bool is_few(int64_t R, int64_t C, int64_t F, int dtype);
 cudaError_t launch_few(const Few &f, int dtype, cudaStream_t st);
 
 // Copies of dense matrices to a pitch that is a multiple of 8 elements (16-bit types).
