@@ -367,7 +367,8 @@ im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_
  * the `saved` buffer of that forward call:
  *   dh = dy w_down, dg = dh * u * act'(g), du = dh * act(g),
  *   dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x, dw_down = dy^T h.
- * dg and du are rounded to the dtype between the products. dx, or the three dw
+ * dg and du are rounded to the dtype between the products (act is checked, but its
+ * values and slopes are in `saved`). dx, or the three dw
  * together, may be NULL and are then not computed. With R = 0 the dw are zero.
  */
 im2win_status im2win_gated_ffn_backward(const void *dy, const void *x, const void *w_gate, const void *w_up,

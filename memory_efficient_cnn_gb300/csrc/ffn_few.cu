@@ -31,7 +31,7 @@ struct FewParams {
     int act;
     void *out, *out_lo;        // h and its remainder, or y
     int64_t ldo;
-    float *g, *u;              // kept in fp32 where not null
+    void *kept;                // act(g) and u act'(g), where not null
     uint32_t *status;          // cleared where not null
 };
 
@@ -207,17 +207,28 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1) few_mma(const __grid
                 for (int k = 0; k < WARPS; ++k) v[i] += red[k * NW * TILE + i * TILE + e];
             T *out = static_cast<T *>(p.out) + (int64_t)m * p.ldo + n;
             if (GATED) {
-                float h = 0.0f;
+                float act = 0.0f, slope = 0.0f, unused;
                 with_act_device(p.act, [&](auto a) {
-                    float unused;
-                    split(act_value2<decltype(a)::value>(f2(v[0])), h, unused);
+                    F2 x, y;
+                    act_both2<decltype(a)::value>(f2(v[0]), x, y);
+                    split(x, act, unused);
+                    split(y, slope, unused);
                 });
-                h *= v[NW - 1];
+                const float h = act * v[NW - 1];
                 const T hi = from_f32<T>(h);
                 const float rest = h - to_f32(hi);
                 *out = hi;  // (the remainder of an infinite rounding is none)
                 static_cast<T *>(p.out_lo)[(int64_t)m * p.ldo + n] = from_f32<T>(isfinite(rest) ? rest : 0.0f);
-                if (p.g) p.g[kept_index(m, n, p.N)] = v[0], p.u[kept_index(m, n, p.N)] = v[NW - 1];
+                if (p.kept) {
+                    unsigned char *at = static_cast<unsigned char *>(p.kept) + kept_block(m, n, p.N);
+                    const float keep[2] = {act, slope * v[NW - 1]};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t bits = __float_as_uint(keep[i]);
+                        *reinterpret_cast<uint16_t *>(at + i * 512 + n % 8 * 2) = (uint16_t)(bits >> 16);
+                        at[1024 + i * 8 + n % 8] = (unsigned char)(bits >> 8);
+                    }
+                }
             } else {
                 *out = from_f32<T>(v[0]);
             }
@@ -279,10 +290,13 @@ __global__ void __launch_bounds__(THREADS) few_fma(const __grid_constant__ FewPa
         for (int k = 0; k < WARPS; ++k) v[i] += red[k][i * NR * ROWS + threadIdx.x];
     float *out = static_cast<float *>(p.out) + (int64_t)m * p.ldo + n;
     if (GATED) {
-        float h = 0.0f;
-        with_act_device(p.act, [&](auto a) { h = act_value<decltype(a)::value>(v[0]) * v[NW - 1]; });
-        *out = h;
-        if (p.g) p.g[kept_index(m, n, p.N)] = v[0], p.u[kept_index(m, n, p.N)] = v[NW - 1];
+        float act = 0.0f, slope = 0.0f;
+        with_act_device(p.act, [&](auto a) { act_both<decltype(a)::value>(v[0], act, slope); });
+        *out = act * v[NW - 1];
+        if (p.kept) {
+            float *at = static_cast<float *>(p.kept) + (int64_t)m * p.N + n;
+            at[0] = act, at[(int64_t)p.R * p.N] = slope * v[NW - 1];
+        }
     } else {
         *out = v[0];
     }
@@ -369,7 +383,7 @@ cudaError_t launch_few(const Few &f, int dtype, cudaStream_t st) {
     p.w0 = f.w_gate; p.w1 = f.w_up;
     p.act = f.act;
     p.out = f.h; p.out_lo = f.h_lo; p.ldo = f.ldh;
-    p.g = f.g; p.u = f.u;
+    p.kept = f.kept;
     p.status = f.status;
     const cudaError_t e = launch_any<true>(p, dtype, st);
     if (e != cudaSuccess) return e;

@@ -171,17 +171,19 @@ __global__ void __launch_bounds__(THREADS, 2) simt_product(const __grid_constant
             for (int row = 0; row < 2; ++row) {
                 if (m + row >= p.M) break;
                 float *out = static_cast<float *>(z ? p.out2 : p.out) + (int64_t)(m + row) * p.ldo + n;
-                const int64_t at = kept_index(m + row, n, p.N);
+                float *a_at = static_cast<float *>(p.kept) +  (int64_t)(m + row) * p.N + n, *b_at = a_at + (int64_t)p.M * p.N;
                 if (EPI == EPI_STORE) {
                     *out = d[row];
                 } else if (GATED) {
-                    *out = act_value<ACT>(d[row]) * du[row];
-                    if (p.g) p.g[at] = d[row], p.u[at] = du[row];
+                    float a = act_value<ACT>(d[row]), s;
+                    *out = a * du[row];
+                    if (p.kept) {
+                        act_both<ACT>(d[row], a, s);
+                        *a_at = a, *b_at = du[row] * s;
+                    }
                 } else {
-                    float a, s;
-                    act_both<ACT>(p.g[at], a, s);
-                    *out = d[row] * p.u[at] * s;
-                    static_cast<float *>(p.out2)[(int64_t)(m + row) * p.ldo + n] = d[row] * a;
+                    *out = d[row] * *b_at;
+                    static_cast<float *>(p.out2)[(int64_t)(m + row) * p.ldo + n] = d[row] * *a_at;
                 }
             }
         }
@@ -228,7 +230,7 @@ cudaError_t launch_simt(const Product &p, cudaStream_t st) {
     if (p.epi == EPI_GATED)
         with_act(p.act, [&](auto a) { e = launch<true, true, EPI_GATED, decltype(a)::value>(p, st); });
     else if (p.epi == EPI_DGATED)
-        with_act(p.act, [&](auto a) { e = launch<true, false, EPI_DGATED, decltype(a)::value>(p, st); });
+        e = launch<true, false, EPI_DGATED, 0>(p, st);
     else if (p.a0.k_major)
         e = p.b0.k_major ? launch<true, true, EPI_STORE, 0>(p, st) : launch<true, false, EPI_STORE, 0>(p, st);
     else

@@ -53,11 +53,12 @@ struct TcParams {
     int batch;                 // 2: a second product a[1], b[1] -> out2 of the same shape
     int tiles_m, tiles_n, tiles;
     int a_rows;                // rows of A's copies (fewer than ROWS when M is)
+    int a_blocks, b_blocks;    // K outermost, whole blocks of 64 output indexes: one copy takes all of a stage's
     int bf16, act;
     void *out, *out2;
-    float *g, *u;
+    unsigned char *kept;
     int64_t ldo;
-    int vec;                   // 16-byte output stores
+    int vec;                   // bytes of output stores: 32, 16, or 2
     float *part;               // streamed: partial tiles
     int64_t part_ld, part_step;  // row pitch and distance between contributions, in floats
     int clear_status;
@@ -71,6 +72,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same without ordering memory (a release would wait for the stores under way).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // Address in the cluster's shared memory of `addr` in CTA `rank`.
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
@@ -94,6 +99,21 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int
             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
             "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    if (CG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
 }
 template <int CG>
@@ -190,97 +210,139 @@ struct Walk {
     }
 };
 
-// N consecutive outputs of one row from fp32, `n` of them valid.
-template <int N>
-__device__ __forceinline__ void store_row(uint16_t *dst, const F2 (&v)[N / 2], int n, bool vec, int bf16) {
-    uint32_t w[N / 2];
+constexpr int CHUNK = 16;  // accumulator columns a warp turns into outputs at a time
+constexpr int PAIRS = CHUNK / 2;
+
+// A chunk of outputs of one row from fp32, `n` of them valid.
+__device__ __forceinline__ void store_row(uint16_t *dst, const F2 (&v)[PAIRS], int n, int vec, int bf16) {
+    uint32_t w[PAIRS];
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
+    for (int i = 0; i < PAIRS; ++i) {
         float lo, hi;
         split(v[i], lo, hi);
         w[i] = pack2(lo, hi, bf16);
     }
-    if (vec && n >= N) {
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i)
-            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    if (vec == 32 && n >= CHUNK) {  // a whole sector in one store
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else if (vec >= 16 && n >= CHUNK) {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < CHUNK; ++i)
             if (i < n) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
     }
 }
 
-// g -> h = act(g) * u; the activation is chosen once for all N values.
-template <int N>
-__device__ __forceinline__ void gate_values(int act, F2 (&g)[N / 2], const F2 (&u)[N / 2]) {
-    with_act_device(act, [&](auto a) {
+// Eight kept values: their upper halves and the bytes after them.
+__device__ __forceinline__ void keep8(const F2 *v, uint4 &hi, uint2 &lo) {
+    uint32_t b[8];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) g[i] = mul2(act_value2<decltype(a)::value>(g[i]), u[i]);
-    });
+    for (int i = 0; i < 4; ++i) {
+        float x, y;
+        split(v[i], x, y);
+        b[2 * i] = __float_as_uint(x), b[2 * i + 1] = __float_as_uint(y);
+    }
+    hi = make_uint4(__byte_perm(b[0], b[1], 0x7632), __byte_perm(b[2], b[3], 0x7632), __byte_perm(b[4], b[5], 0x7632),
+                    __byte_perm(b[6], b[7], 0x7632));
+    lo.x = __byte_perm(__byte_perm(b[0], b[1], 0x0051), __byte_perm(b[2], b[3], 0x0051), 0x5410);
+    lo.y = __byte_perm(__byte_perm(b[4], b[5], 0x0051), __byte_perm(b[6], b[7], 0x0051), 0x5410);
 }
-// dh and g, u -> dg, du (in g and u).
-template <int N>
-__device__ __forceinline__ void dgate_values(int act, const F2 (&dh)[N / 2], F2 (&g)[N / 2], F2 (&u)[N / 2]) {
-    with_act_device(act, [&](auto a) {
+// (The last eight bits, which were not kept, repeat the eight before them.)
+__device__ __forceinline__ void kept8(F2 *v, const uint4 &hi, uint32_t lo0, uint32_t lo1) {
+    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            F2 v, d;
-            act_both2<decltype(a)::value>(g[i], v, d);
-            g[i] = mul2(mul2(dh[i], u[i]), d);
-            u[i] = mul2(dh[i], v);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = i < 2 ? lo0 : lo1;
+        const uint32_t x = __byte_perm(h[i], lo, i & 1 ? 0x1066 : 0x1044), y = __byte_perm(h[i], lo, i & 1 ? 0x3277 : 0x3255);
+        v[i] = f2(__uint_as_float(x), __uint_as_float(y));
+    }
+}
+// 8 columns of a and b of a row, at kept_block().
+__device__ __forceinline__ void keep_columns(unsigned char *at, const F2 *a, const F2 *b) {
+    uint4 ha, hb;
+    uint2 la, lb;
+    keep8(a, ha, la);
+    keep8(b, hb, lb);
+    *reinterpret_cast<uint4 *>(at) = ha;
+    *reinterpret_cast<uint4 *>(at + 512) = hb;
+    *reinterpret_cast<uint4 *>(at + 1024) = make_uint4(la.x, la.y, lb.x, lb.y);
+}
+
+// g, u -> h = act(g) * u in g; N pairs. KEEP: act(g) and u act'(g) too, in a and u.
+// The activation is chosen once for all values.
+template <int N, bool KEEP>
+__device__ __forceinline__ void gate_values(int act, F2 (&g)[N], F2 (&u)[N], F2 (&a)[N]) {
+    with_act_device(act, [&](auto kind) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (KEEP) {
+                F2 d;
+                act_both2<decltype(kind)::value>(g[i], a[i], d);
+                g[i] = mul2(a[i], u[i]);
+                u[i] = mul2(u[i], d);
+            } else {
+                g[i] = mul2(act_value2<decltype(kind)::value>(g[i]), u[i]);
+            }
         }
     });
 }
 
-// Kept values of N columns of row m, `n` of them valid, to and from pairs.
-template <int N>
-__device__ __forceinline__ void keep(float *kept, int64_t at, const F2 (&v)[N / 2], int n) {
+__device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[CHUNK]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void pairs_of(const uint32_t (&r)[CHUNK], F2 (&v)[PAIRS]) {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-        if (4 * i < n) *reinterpret_cast<ulonglong2 *>(kept + at + i * 128) = make_ulonglong2(v[2 * i].v, v[2 * i + 1].v);
+    for (int i = 0; i < PAIRS; ++i) v[i] = f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
-template <int N>
-__device__ __forceinline__ void kept_values(const float *kept, int64_t at, F2 (&v)[N / 2], int n) {
+
+// The kept values of a chunk of row m: three vectors of each 8 columns.
+struct KeptChunk {
+    uint4 v[2][3];
+};
+__device__ __forceinline__ void fetch_kept(const TcParams &p, KeptChunk &k, int m, int n) {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-        const ulonglong2 q =
-            4 * i < n ? *reinterpret_cast<const ulonglong2 *>(kept + at + i * 128) : make_ulonglong2(0, 0);
-        v[2 * i].v = q.x, v[2 * i + 1].v = q.y;
+    for (int i = 0; i < 2; ++i) {
+        if (m >= p.M || n + 8 * i >= p.N) continue;
+        const unsigned char *at = p.kept + kept_block(m, n + 8 * i, p.N);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) k.v[i][j] = *reinterpret_cast<const uint4 *>(at + 512 * j);
     }
 }
 
-constexpr int CHUNK = 16;  // accumulator columns a warp turns into outputs at a time
-
-__device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[CHUNK]) { tmem_ld16(taddr, r); }
-__device__ __forceinline__ void pairs_of(const uint32_t (&r)[CHUNK], F2 (&v)[CHUNK / 2]) {
-#pragma unroll
-    for (int i = 0; i < CHUNK / 2; ++i) v[i] = f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-}
-
-// Outputs of a chunk of row m from its accumulator values v (and u), columns from n.
+// Outputs of a chunk of row m from its accumulator values v (and u, or kept), columns from n.
 template <int EPI>
-__device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[CHUNK / 2], F2 (&u)[CHUNK / 2], int m, int n,
-                                             uint16_t *out) {
+__device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[PAIRS], F2 (&u)[PAIRS], const KeptChunk &k, int m,
+                                             int n, uint16_t *out) {
     const int left = m < p.M ? p.N - n : 0;
     if (left <= 0) return;
     const int64_t at = (int64_t)m * p.ldo + n;
     if (EPI == EPI_GATED) {
-        if (p.g) {
-            keep<CHUNK>(p.g, kept_index(m, n, p.N), v, left);
-            keep<CHUNK>(p.u, kept_index(m, n, p.N), u, left);
+        F2 a[PAIRS];
+        if (p.kept) {
+            gate_values<PAIRS, true>(p.act, v, u, a);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (8 * i < left) keep_columns(p.kept + kept_block(m, n + 8 * i, p.N), a + 4 * i, u + 4 * i);
+        } else {
+            gate_values<PAIRS, false>(p.act, v, u, a);
         }
-        gate_values<CHUNK>(p.act, v, u);
     } else if (EPI == EPI_DGATED) {
-        F2 g[CHUNK / 2];
-        kept_values<CHUNK>(p.g, kept_index(m, n, p.N), g, left);
-        kept_values<CHUNK>(p.u, kept_index(m, n, p.N), u, left);
-        dgate_values<CHUNK>(p.act, v, g, u);
-        store_row<CHUNK>(out + at, g, left, p.vec, p.bf16);
-        store_row<CHUNK>(static_cast<uint16_t *>(p.out2) + at, u, left, p.vec, p.bf16);
-        return;
+        F2 du[PAIRS];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            F2 a[4], b[4];
+            kept8(a, k.v[i][0], k.v[i][2].x, k.v[i][2].y);
+            kept8(b, k.v[i][1], k.v[i][2].z, k.v[i][2].w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                du[4 * i + j] = mul2(v[4 * i + j], a[j]);
+                v[4 * i + j] = mul2(v[4 * i + j], b[j]);
+            }
+        }
+        store_row(static_cast<uint16_t *>(p.out2) + at, du, left, p.vec, p.bf16);
     }
-    store_row<CHUNK>(out + at, v, left, p.vec, p.bf16);
+    store_row(out + at, v, left, p.vec, p.bf16);
 }
 
 enum Site : uint32_t { SITE_STAGE_FULL = 32, SITE_STAGE_EMPTY, SITE_ACC_FULL, SITE_ACC_EMPTY };
@@ -300,6 +362,12 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
     const int unit = blockIdx.x / CG, units = gridDim.x / CG;
     const Ctl ctl{&abort_flag, p.status};
 
+    if (threadIdx.x >= 64 && threadIdx.x < 68) {  // the maps' first use is a microsecond away
+        const int i = threadIdx.x & 1;
+        const bool b = threadIdx.x >= 66;
+        if (i == 0 || p.segs == 2 || p.batch == 2 || (b && EPI == EPI_GATED))
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(b ? &p.b[i] : &p.a[i])) : "memory");
+    }
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < T::STAGES; ++s) {
@@ -345,6 +413,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                 const CUtensorMap *ma = &p.a[seg | w.z], *mb = &p.b[seg | w.z];
                 if (AK) {
                     tma_2d<CG>(sa, ma, k, m0, bar);
+                } else if (p.a_blocks) {
+                    tma_3d<CG>(sa, ma, 0, k, m0 / 64, bar);
                 } else {
                     for (int i = 0; i < p.a_rows; i += 64) tma_2d<CG>(sa + i * BK * 2, ma, m0 + i, k, bar);
                 }
@@ -360,6 +430,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                     const int n0 = w.tn * BN + (int)rank * T::B_ROWS;
                     if (BKM) {
                         tma_2d<CG>(sb, mb, k, n0, bar);
+                    } else if (p.b_blocks) {
+                        tma_3d<CG>(sb, mb, 0, k, n0 / 64, bar);
                     } else {
 #pragma unroll
                         for (int i = 0; i < T::B_ROWS; i += 64) tma_2d<CG>(sb + i * BK * 2, mb, n0 + i, k, bar);
@@ -419,10 +491,14 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
         const uint32_t empty_bar0 = CG == 2 ? map_rank(acc_empty, 0) : acc_empty;
         while (walk.next(w)) {
             const int buf = n_tile & 1;
+            const int m = w.tm * T::M + (int)rank * ROWS + q * 32 + lane;
+            constexpr int SPAN = COLS / SHARES;  // output columns of the warp
+            // what was kept of a chunk is on its way before the chunk's sums are looked at
+            KeptChunk kept;
+            if (EPI == EPI_DGATED && !p.part) fetch_kept(p, kept, m, w.tn * COLS + share * SPAN);
             if (!warp_bar_wait(acc_full + 8 * buf, (n_tile >> 1) & 1, ctl, SITE_ACC_FULL)) break;
             tc_fence_after();
             const uint32_t taddr = tmem + buf * BN + ((uint32_t)(q * 32) << 16);
-            const int m = w.tm * T::M + (int)rank * ROWS + q * 32 + lane;
             // Once the warp's last accumulator column is in registers the MMAs may have the
             // buffer; the arrival orders no memory but the loads, which are done, so it need not
             // wait for the stores under way.
@@ -432,14 +508,14 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                 if (lane == 0) arrive_relaxed(empty_bar0 + 8 * buf);
             };
             if (p.part) {
-                constexpr int SPAN = BN / SHARES;
+                constexpr int PART_SPAN = BN / SHARES;
                 float *dst = p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
 #pragma unroll 1
-                for (int c = share * SPAN; c < (share + 1) * SPAN; c += CHUNK) {
+                for (int c = share * PART_SPAN; c < (share + 1) * PART_SPAN; c += CHUNK) {
                     uint32_t r[CHUNK];
                     load_chunk(taddr + c, r);
                     tmem_wait_ld();
-                    if (c + CHUNK == (share + 1) * SPAN) release();
+                    if (c + CHUNK == (share + 1) * PART_SPAN) release();
                     if (m < p.M) {
 #pragma unroll
                         for (int i = 0; i < CHUNK / 4; ++i)
@@ -447,7 +523,6 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                     }
                 }
             } else {
-                constexpr int SPAN = COLS / SHARES;
                 uint16_t *out = static_cast<uint16_t *>(w.z ? p.out2 : p.out);
 #pragma unroll 1
                 for (int c = share * SPAN; c < (share + 1) * SPAN; c += CHUNK) {
@@ -456,10 +531,12 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                     if (EPI == EPI_GATED) load_chunk(taddr + BN / 2 + c, ru);
                     tmem_wait_ld();
                     if (c + CHUNK == (share + 1) * SPAN) release();
-                    F2 v[CHUNK / 2], u[CHUNK / 2];
+                    F2 v[PAIRS], u[PAIRS];
                     pairs_of(r, v);
                     if (EPI == EPI_GATED) pairs_of(ru, u);
-                    finish_chunk<EPI>(p, v, u, m, w.tn * COLS + c, out);
+                    const KeptChunk now = kept;
+                    if (EPI == EPI_DGATED && c + CHUNK < (share + 1) * SPAN) fetch_kept(p, kept, m, w.tn * COLS + c + CHUNK);
+                    finish_chunk<EPI>(p, v, u, now, m, w.tn * COLS + c, out);
                 }
             }
             ++n_tile;
@@ -467,23 +544,23 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
     }
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync();
+    if (CG == 2) cluster_sync_relaxed();
     tc_fence_after();
     if (warp == 2) free_tmem<CG>(tmem, 2 * BN);
 }
 
 // Adds the partial tiles of a streamed launch and finishes the outputs: one
-// thread for four consecutive output columns.
+// thread for eight consecutive output columns.
 template <int BN, int EPI>
 __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams p, int tile_m, int units) {
     allow_dependents();
     grid_dependency_wait();
     constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;
-    const int quads = (p.N + 3) / 4;
+    const int octets = (p.N + 7) / 8;
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= (int64_t)p.batch * p.M * quads) return;
-    const int n = (int)(id % quads) * 4;
-    const int64_t zm = id / quads;
+    if (id >= (int64_t)p.batch * p.M * octets) return;
+    const int n = (int)(id % octets) * 8;
+    const int64_t zm = id / octets;
     const int z = (int)(zm / p.M), m = (int)(zm - (int64_t)z * p.M);
     const int tm = m / tile_m, tn = n / COLS;
     // the tile's index in the order of Walk, and the units that hold its first and last block
@@ -493,46 +570,61 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams 
     const int64_t total = (int64_t)p.tiles * KT;
     const int count = stream_unit(total, units, (int64_t)(t + 1) * KT - 1) - stream_unit(total, units, (int64_t)t * KT) + 1;
     const float *src = p.part + zm * p.part_ld + (int64_t)tn * BN + (n - tn * COLS);
-    F2 v[2] = {f2(0.0f), f2(0.0f)}, u[2] = {f2(0.0f), f2(0.0f)};
-    auto add = [](F2(&sum)[2], const float *from) {
-        const float4 a = *reinterpret_cast<const float4 *>(from);
-        sum[0] = add2(sum[0], f2(a.x, a.y)), sum[1] = add2(sum[1], f2(a.z, a.w));
+    F2 v[4], u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = u[i] = f2(0.0f);
+    auto add = [](F2(&sum)[4], const float *from) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 a = reinterpret_cast<const float4 *>(from)[i];
+            sum[2 * i] = add2(sum[2 * i], f2(a.x, a.y)), sum[2 * i + 1] = add2(sum[2 * i + 1], f2(a.z, a.w));
+        }
     };
 #pragma unroll 4
     for (int j = 0; j < count; ++j) {
         add(v, src + j * p.part_step);
         if (EPI == EPI_GATED) add(u, src + j * p.part_step + BN / 2);
     }
-    const int left = min(4, p.N - n);
+    const int left = min(8, p.N - n);
     const int64_t at = (int64_t)m * p.ldo + n;
-    uint16_t *out = static_cast<uint16_t *>(z ? p.out2 : p.out) + at;
-    auto put = [&](uint16_t *dst, const F2(&r)[2]) {
-        float a, b, c, d;
-        split(r[0], a, b);
-        split(r[1], c, d);
-        const uint32_t lo = pack2(a, b, p.bf16), hi = pack2(c, d, p.bf16);
-        if (p.vec && left == 4) {
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
+    auto put = [&](uint16_t *dst, const F2(&r)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            split(r[i], a, b);
+            w[i] = pack2(a, b, p.bf16);
+        }
+        if (p.vec >= 16 && left == 8) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
-            for (int i = 0; i < left; ++i) dst[i] = (uint16_t)((i < 2 ? lo : hi) >> (16 * (i & 1)));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
         }
     };
     if (EPI == EPI_GATED) {
-        if (p.g) {
-            keep<4>(p.g, kept_index(m, n, p.N), v, left);
-            keep<4>(p.u, kept_index(m, n, p.N), u, left);
+        F2 a[4];
+        if (p.kept) {
+            gate_values<4, true>(p.act, v, u, a);
+            keep_columns(p.kept + kept_block(m, n, p.N), a, u);
+        } else {
+            gate_values<4, false>(p.act, v, u, a);
         }
-        gate_values<4>(p.act, v, u);
     } else if (EPI == EPI_DGATED) {
-        F2 g[2];
-        kept_values<4>(p.g, kept_index(m, n, p.N), g, left);
-        kept_values<4>(p.u, kept_index(m, n, p.N), u, left);
-        dgate_values<4>(p.act, v, g, u);
-        put(out, g);
-        put(static_cast<uint16_t *>(p.out2) + at, u);
-        return;
+        const uint4 *from = reinterpret_cast<const uint4 *>(p.kept + kept_block(m, n, p.N));
+        const uint4 ha = from[0], hb = from[32], lo = from[64];
+        F2 a[4], b[4];
+        kept8(a, ha, lo.x, lo.y);
+        kept8(b, hb, lo.z, lo.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = mul2(v[i], a[i]);
+            v[i] = mul2(v[i], b[i]);
+        }
+        put(static_cast<uint16_t *>(p.out2) + at, a);
     }
-    put(out, v);
+    put(static_cast<uint16_t *>(z ? p.out2 : p.out) + at, v);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
@@ -547,16 +639,19 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
     return fn;
 }
 
-// An operand of I output indexes and K steps, copied `rows` output indexes (K
-// innermost) or 64 (else) at a time.
-bool encode(CUtensorMap &map, const Operand &o, int I, int K, int rows) {
+// An operand of I output indexes and K steps, copied `rows` output indexes at a
+// time. K innermost: (K, I). Else: (I, K) in blocks of 64 output indexes, or, where
+// I is a number of whole blocks, (64, K, I / 64), which takes several in one copy.
+bool encode(CUtensorMap &map, const Operand &o, int I, int K, int rows, bool blocks) {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
     if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)(o.k_major ? K : I), (cuuint64_t)(o.k_major ? I : K)};
-    const cuuint64_t strides[1] = {(cuuint64_t)o.ld * 2};
-    const cuuint32_t box[2] = {64u, o.k_major ? (cuuint32_t)rows : (cuuint32_t)BK};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(o.p), dims, strides, box, estr,
+    const cuuint64_t pitch = (cuuint64_t)o.ld * 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)(o.k_major ? K : blocks ? 64 : I), (cuuint64_t)(o.k_major ? I : K),
+                                (cuuint64_t)(blocks ? I / 64 : 1)};
+    const cuuint64_t strides[2] = {pitch, 128};
+    const cuuint32_t box[3] = {64u, o.k_major ? (cuuint32_t)rows : (cuuint32_t)BK, (cuuint32_t)(rows / 64)};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, blocks ? 3 : 2, const_cast<void *>(o.p), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -587,8 +682,8 @@ cudaError_t launch_shape(const TcParams &p, const TcPlan &pl, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = launch_with(kernel, pl.units * CG, THREADS, T::SMEM, CG, st, p);
     if (e != cudaSuccess || !p.part) return e;
-    const int64_t quads = (int64_t)p.batch * p.M * ((p.N + 3) / 4);
-    return launch_with(tc_join<BN, EPI>, (int)((quads + 255) / 256), 256, 0, 1, st, p, T::M, pl.units);
+    const int64_t octets = (int64_t)p.batch * p.M * ((p.N + 7) / 8);
+    return launch_with(tc_join<BN, EPI>, (int)((octets + 255) / 256), 256, 0, 1, st, p, T::M, pl.units);
 }
 
 template <int CG, int BN>
@@ -657,12 +752,15 @@ cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool clear_
     p.tiles_m = pl.tiles_m; p.tiles_n = pl.tiles_n; p.tiles = p.batch * pl.tiles_m * pl.tiles_n;
     p.a_rows = std::min(ROWS, (d.M + 7) / 8 * 8);
     const int b_box = d.epi == EPI_GATED && pl.cg == 1 ? pl.bn / 2 : pl.bn / pl.cg;
-    if (!encode(p.a[0], d.a0, d.M, d.K, p.a_rows) || !encode(p.b[0], d.b0, d.N, d.K, b_box)) return cudaErrorInvalidValue;
-    if (two && !encode(p.a[1], d.a1, d.M, d.K, p.a_rows)) return cudaErrorInvalidValue;
-    if (d.b1.p && !encode(p.b[1], d.b1, d.N, d.K, b_box)) return cudaErrorInvalidValue;
+    p.a_blocks = !d.a0.k_major && d.M % 64 == 0;
+    p.b_blocks = !d.b0.k_major && d.N % 64 == 0;
+    if (!encode(p.a[0], d.a0, d.M, d.K, p.a_rows, p.a_blocks) || !encode(p.b[0], d.b0, d.N, d.K, b_box, p.b_blocks))
+        return cudaErrorInvalidValue;
+    if (two && !encode(p.a[1], d.a1, d.M, d.K, p.a_rows, p.a_blocks)) return cudaErrorInvalidValue;
+    if (d.b1.p && !encode(p.b[1], d.b1, d.N, d.K, b_box, p.b_blocks)) return cudaErrorInvalidValue;
     p.bf16 = bf16; p.act = d.act;
-    p.out = d.out; p.out2 = d.out2; p.g = d.g; p.u = d.u; p.ldo = d.ldo;
-    p.vec = d.ldo % 8 == 0;
+    p.out = d.out; p.out2 = d.out2; p.kept = static_cast<unsigned char *>(d.kept); p.ldo = d.ldo;
+    p.vec = d.ldo % 16 == 0 && aligned_to(d.out, 32) && aligned_to(d.out2, 32) ? 32 : d.ldo % 8 == 0 ? 16 : 2;
     if (pl.streamed) {
         p.part = static_cast<float *>(part);
         p.part_ld = pl.part_ld;

@@ -43,12 +43,12 @@ struct Problem {
     size_t rows_c(int64_t rows) const { return (size_t)(rows * Cp) * esz; }
     size_t rows_f(int64_t rows) const { return (size_t)(rows * Fp) * esz; }
 
-    Product gated(const void *x, const void *wg, const void *wu, void *h, float *g, float *u) const {
+    Product gated(const void *x, const void *wg, const void *wu, void *h, void *kept) const {
         Product p;
         p.M = R; p.N = F; p.K = C;
         p.a0 = {x, Cp, true}; p.b0 = {wg, Cp, true}; p.b1 = {wu, Cp, true};
         p.epi = EPI_GATED; p.act = act;
-        p.out = h; p.ldo = Fp; p.g = g; p.u = u;
+        p.out = h; p.ldo = Fp; p.kept = kept;
         return p;
     }
     Product down(const void *h, const void *wd, void *y) const {
@@ -58,13 +58,13 @@ struct Problem {
         p.out = y; p.ldo = C;
         return p;
     }
-    Product dgated(const void *dy, const void *wd, const float *g, const float *u, void *dg, void *du) const {
+    Product dgated(const void *dy, const void *wd, const void *kept, void *dg, void *du) const {
         Product p;
         p.M = R; p.N = F; p.K = C;
         p.a0 = {dy, Cp, true}; p.b0 = {wd, Fp, false};
         p.epi = EPI_DGATED; p.act = act;
         p.out = dg; p.out2 = du; p.ldo = Fp;
-        p.g = const_cast<float *>(g); p.u = const_cast<float *>(u);
+        p.kept = const_cast<void *>(kept);
         return p;
     }
     Product dx(const void *dg, const void *du, const void *wg, const void *wu, void *out) const {
@@ -93,15 +93,13 @@ struct Problem {
     }
 };
 
-// saved: h, then g and u in fp32 (kept_index). They stay in fp32 because dg and
-// du, made of them, are rounded once more on their own.
+// saved: h, then what the backward pass needs of g and u.
 struct SavedParts {
-    size_t h, g, u, bytes;
+    size_t h, kept, bytes;
     explicit SavedParts(const Problem &q) {
         Parts p(0);
         h = p.add(q.rows_f(q.R));
-        g = p.add(kept_elems(q.R, q.F) * 4);
-        u = p.add(kept_elems(q.R, q.F) * 4);
+        kept = p.add(kept_bytes(q.R, q.F, !q.tc));
         bytes = p.end;
     }
 };
@@ -127,7 +125,7 @@ struct ForwardParts {
         wd = p.add(pad_f ? q.rows_f(q.C) : 0);
         part = p.end;
         if (q.tc && q.R > 0)
-            p.add(std::max(plan_tc(q.gated(kSome, kSome, kSome, kSomeOut, nullptr, nullptr)).part_bytes,
+            p.add(std::max(plan_tc(q.gated(kSome, kSome, kSome, kSomeOut, nullptr)).part_bytes,
                            plan_tc(q.down(kSome, kSome, kSomeOut)).part_bytes));
         bytes = p.end;
     }
@@ -148,7 +146,7 @@ struct BackwardParts {
         part = p.end;
         if (q.tc && q.R > 0) {
             size_t most = 0;
-            for (const Product &d : {q.dgated(kSome, kSome, nullptr, nullptr, kSomeOut, kSomeOut),
+            for (const Product &d : {q.dgated(kSome, kSome, nullptr, kSomeOut, kSomeOut),
                                      q.dx(kSome, kSome, kSome, kSome, kSomeOut),
                                      q.dw_in(kSome, kSome, kSome, kSomeOut, kSomeOut), q.dw_down(kSome, kSome, kSomeOut)})
                 most = std::max(most, plan_tc(d).part_bytes);
@@ -160,8 +158,6 @@ struct BackwardParts {
 
 unsigned char *at(void *base, size_t off) { return static_cast<unsigned char *>(base) + off; }
 const unsigned char *at(const void *base, size_t off) { return static_cast<const unsigned char *>(base) + off; }
-float *floats(void *base, size_t off) { return reinterpret_cast<float *>(at(base, off)); }
-const float *floats(const void *base, size_t off) { return reinterpret_cast<const float *>(at(base, off)); }
 
 bool known_act(int act) {
     return with_act(act, [](auto) {});
@@ -230,12 +226,12 @@ im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_
     const Problem q(R, C, F, act, dtype);
     const ForwardParts parts(q, saved != nullptr);
     if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
-    const SavedParts kept(q);
-    void *h = saved ? at(saved, kept.h) : at(ws, parts.h);
+    const SavedParts own(q);
+    void *h = saved ? at(saved, own.h) : at(ws, parts.h);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    float *g = saved ? floats(saved, kept.g) : nullptr, *u = saved ? floats(saved, kept.u) : nullptr;
+    void *kept = saved ? at(saved, own.kept) : nullptr;
     if (q.few()) {
-        const Few f = {q.R, q.C, q.F, act, x, w_gate, w_up, w_down, y, h, at(ws, parts.h_lo), q.Fp, g, u,
+        const Few f = {q.R, q.C, q.F, act, x, w_gate, w_up, w_down, y, h, at(ws, parts.h_lo), q.Fp, kept,
                        static_cast<uint32_t *>(ws)};
         return launch_few(f, dtype, st) == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
     }
@@ -245,7 +241,7 @@ im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_
     w_up = seq.pitched(w_up, q.F, q.C, parts.wu);
     w_down = seq.pitched(w_down, q.C, q.F, parts.wd);
     seq.copy_pitched();
-    seq.run(q.gated(x, w_gate, w_up, h, g, u));
+    seq.run(q.gated(x, w_gate, w_up, h, kept));
     seq.run(q.down(h, w_down, y));
     return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
 }
@@ -274,7 +270,7 @@ im2win_status im2win_gated_ffn_backward(const void *dy, const void *x, const voi
     const Problem q(R, C, F, act, dtype);
     const BackwardParts parts(q);
     if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
-    const SavedParts kept(q);
+    const SavedParts own(q);
     void *dg = at(ws, parts.dg), *du = at(ws, parts.du);
     Sequence seq{q, ws, at(ws, parts.part), st};
     dy = seq.pitched(dy, q.R, q.C, parts.dy);
@@ -285,11 +281,11 @@ im2win_status im2win_gated_ffn_backward(const void *dy, const void *x, const voi
     }
     if (want_dw) x = seq.pitched(x, q.R, q.C, parts.x);
     seq.copy_pitched();
-    seq.run(q.dgated(dy, w_down, floats(saved, kept.g), floats(saved, kept.u), dg, du));
+    seq.run(q.dgated(dy, w_down, at(saved, own.kept), dg, du));
     if (dx) seq.run(q.dx(dg, du, w_gate, w_up, dx));
     if (want_dw) {
         seq.run(q.dw_in(dg, du, x, dw_gate, dw_up));
-        seq.run(q.dw_down(dy, at(saved, kept.h), dw_down));
+        seq.run(q.dw_down(dy, at(saved, own.h), dw_down));
     }
     return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
 }

@@ -29,16 +29,27 @@ struct Operand {
 // What becomes of an accumulated element (m, n).
 enum Epilogue {
     EPI_STORE = 0,  // out[m][n] = d
-    EPI_GATED = 1,  // two accumulators g, u: out[m][n] = act(g) * u; g and u kept in fp32 where asked
-    EPI_DGATED = 2  // d = dh: out = dg, out2 = du, from the kept g, u
+    EPI_GATED = 1,  // two accumulators g, u: out[m][n] = act(g) * u; act(g) and u act'(g) kept where asked
+    EPI_DGATED = 2  // d = dh: out = dg = d * u act'(g), out2 = du = d * act(g), from the kept values
 };
 
-// The kept g and u lie in blocks of 32 rows by 4 columns, rows outermost in a
-// block: a warp whose lanes hold one row each moves 512 contiguous bytes.
-__host__ __device__ inline int64_t kept_index(int m, int n, int N) {
-    return ((int64_t)(m / 32) * ((N + 3) / 4) + n / 4) * 128 + (m % 32) * 4 + n % 4;
+// What a training step keeps of an M x N product: a = act(g) and b = u act'(g).
+//
+// 16-bit types: in 24 bits, the upper ones of their fp32 form. dg and du, made of
+// them, are rounded to 8 or 11 bits on their own, and the 16 kept bits add less
+// than a hundredth to that; 16-bit a and b would have added half. They lie in
+// blocks of 32 rows by 8 columns: 16 bytes a row of a's upper halves, the same of
+// b's, then 16 bytes a row of the next bytes, a's and b's, so that a warp whose
+// lanes hold a row each moves 512 contiguous bytes.
+//
+// fp32: in fp32, row by row, all a before all b.
+constexpr int KEPT_BLOCK = 1536;
+__host__ __device__ inline int64_t kept_block(int m, int n, int N) {
+    return ((int64_t)(m / 32) * ((N + 7) / 8) + n / 8) * KEPT_BLOCK + (m % 32) * 16;
 }
-inline size_t kept_elems(int64_t M, int64_t N) { return (size_t)((M + 31) / 32 * 32) * (size_t)((N + 3) / 4 * 4); }
+inline size_t kept_bytes(int64_t M, int64_t N, bool f32) {
+    return f32 ? (size_t)(M * N) * 8 : (size_t)((M + 31) / 32) * (size_t)((N + 7) / 8) * KEPT_BLOCK;
+}
 
 // D[M][N] = A0 B0^T (+ A1 B1^T); EPI_GATED: g = A0 B0^T, u = A0 B1^T; batch: out =
 // A0 B0^T and out2 = A1 B1^T.
@@ -49,8 +60,8 @@ struct Product {
     int act = 0;
     bool batch = false;
     void *out = nullptr, *out2 = nullptr;
-    float *g = nullptr, *u = nullptr;  // kept_index(): written (EPI_GATED, may be null) or read (EPI_DGATED)
-    int64_t ldo = 0;                   // row pitch of out and out2 in elements
+    void *kept = nullptr;  // written (EPI_GATED, may be null) or read (EPI_DGATED)
+    int64_t ldo = 0;       // row pitch of out and out2 in elements
 };
 
 // CUDA cores, fp32.
@@ -77,7 +88,7 @@ struct Few {
     const void *x, *w_gate, *w_up, *w_down;
     void *y, *h, *h_lo;
     int64_t ldh;
-    float *g, *u;
+    void *kept;
     uint32_t *status;
 };
 bool is_few(int64_t R, int64_t C, int64_t F, int dtype);
