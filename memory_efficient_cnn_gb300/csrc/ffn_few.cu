@@ -32,6 +32,8 @@ struct FewParams {
     void *out, *out_lo;        // h and its remainder, or y
     int64_t ldo;
     void *kept;                // act(g) and u act'(g), where not null
+    uint16_t *planes;          // fp32: h in planes too then
+    int64_t plane_ld;
     uint32_t *status;          // cleared where not null
 };
 
@@ -292,10 +294,14 @@ __global__ void __launch_bounds__(THREADS) few_fma(const __grid_constant__ FewPa
     if (GATED) {
         float act = 0.0f, slope = 0.0f;
         with_act_device(p.act, [&](auto a) { act_both<decltype(a)::value>(v[0], act, slope); });
-        *out = act * v[NW - 1];
+        const float h = act * v[NW - 1];
+        *out = h;
         if (p.kept) {
-            float *at = static_cast<float *>(p.kept) + (int64_t)m * p.N + n;
-            at[0] = act, at[(int64_t)p.R * p.N] = slope * v[NW - 1];
+            float *at = static_cast<float *>(p.kept) + kept_index_f32(m, n, p.N);
+            at[0] = act, at[kept_count_f32(p.R, p.N)] = slope * v[NW - 1];
+            uint16_t *plane = p.planes + (int64_t)m * p.plane_ld + n;
+            const int64_t next = p.R * p.plane_ld;
+            split_f32(h, plane[0], plane[next], plane[2 * next]);
         }
     } else {
         *out = v[0];
@@ -384,6 +390,7 @@ cudaError_t launch_few(const Few &f, int dtype, cudaStream_t st) {
     p.act = f.act;
     p.out = f.h; p.out_lo = f.h_lo; p.ldo = f.ldh;
     p.kept = f.kept;
+    p.planes = f.planes; p.plane_ld = f.plane_ld;
     p.status = f.status;
     const cudaError_t e = launch_any<true>(p, dtype, st);
     if (e != cudaSuccess) return e;

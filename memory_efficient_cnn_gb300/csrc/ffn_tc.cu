@@ -17,24 +17,11 @@
 // are dealt out evenly ("streamed"): a CTA takes a contiguous run of steps,
 // which may begin and end inside a tile, and writes fp32 partial tiles, which a
 // second kernel adds in the order of K.
-#include <algorithm>
-
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "gated_ffn.cuh"
-#include "tc_ptx.cuh"
+#include "ffn_tc.cuh"
 
 namespace im2win {
 namespace ffn {
 namespace {
-
-using namespace im2win::tc;
-
-constexpr int BK = 64;           // K steps of one stage: 128 bytes
-constexpr int ROWS = 128;        // rows of A a CTA stages (its TMEM lanes)
-constexpr int EPI_WARPS = 16;
-constexpr int THREADS = 128 + 32 * EPI_WARPS;
 
 template <int CG, int BN>
 struct Tile {
@@ -64,154 +51,6 @@ struct TcParams {
     int clear_status;
     uint32_t *status;
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The same without ordering memory (a release would wait for the stores under way).
-__device__ __forceinline__ void cluster_sync_relaxed() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-// Address in the cluster's shared memory of `addr` in CTA `rank`.
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void arrive_relaxed(uint32_t addr) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-    if (CG == 2)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-            : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
-    if (CG == 2)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-            : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-    if (CG == 2)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-            : "memory");
-    else
-        mma_f16(d, a, b, idesc, accumulate);
-}
-// One arrival on `bar` of each CTA of the tile once the MMAs issued so far are done.
-template <int CG>
-__device__ __forceinline__ void commit(uint32_t bar) {
-    if (CG == 2)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)3)
-            : "memory");
-    else
-        mma_commit(bar);
-}
-template <int CG>
-__device__ __forceinline__ void alloc_tmem(uint32_t slot, uint32_t cols) {
-    if (CG == 2) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-        tmem_alloc(slot, cols);
-        tmem_relinquish();
-    }
-}
-template <int CG>
-__device__ __forceinline__ void free_tmem(uint32_t addr, uint32_t cols) {
-    if (CG == 2)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
-    else
-        tmem_dealloc(addr, cols);
-}
-
-// One run of K blocks of one tile.
-struct Work {
-    int z, tm, tn;  // batch, tile row, tile column
-    int k0, k1;     // K blocks, over all segments
-    int slot;       // streamed: the run's place among the tile's
-};
-
-// The K blocks of a streamed launch are dealt to `units` CTA groups: unit i takes
-// blocks [i * total / units, (i + 1) * total / units).
-__host__ __device__ inline int64_t stream_begin(int64_t total, int units, int i) { return total * i / units; }
-// The unit that holds block b.
-__host__ __device__ inline int stream_unit(int64_t total, int units, int64_t b) {
-    int i = (int)(b * units / total);
-    while (i + 1 < units && stream_begin(total, units, i + 1) <= b) ++i;
-    while (i > 0 && stream_begin(total, units, i) > b) --i;
-    return i;
-}
-
-// Walks a CTA group's work.
-struct Walk {
-    int KT, tiles, tiles_m, tiles_n, per_z, units, unit, streamed;
-    int64_t at, end;  // streamed: K blocks; else: tiles
-    __device__ Walk(const TcParams &p, int unit_, int units_) {
-        KT = p.KB * p.segs;
-        tiles = p.tiles, tiles_m = p.tiles_m, tiles_n = p.tiles_n, per_z = tiles_m * tiles_n;
-        units = units_, unit = unit_, streamed = p.part != nullptr;
-        at = streamed ? stream_begin((int64_t)tiles * KT, units, unit) : unit;
-        end = streamed ? stream_begin((int64_t)tiles * KT, units, unit + 1) : tiles;
-    }
-    __device__ bool next(Work &w) {
-        if (at >= end) return false;
-        int t;
-        if (streamed) {
-            t = (int)(at / KT);
-            w.k0 = (int)(at - (int64_t)t * KT);
-            w.k1 = (int)min((int64_t)KT, w.k0 + end - at);
-            w.slot = unit - stream_unit((int64_t)tiles * KT, units, (int64_t)t * KT);
-            at += w.k1 - w.k0;
-        } else {
-            t = (int)at;
-            w.k0 = 0, w.k1 = KT, w.slot = 0;
-            at += units;
-        }
-        w.z = t / per_z;
-        t -= w.z * per_z;
-        // bands of 8 tile rows, column by column, so that tiles in flight share operands in L2
-        const int band = t / (8 * tiles_n), r = t - band * 8 * tiles_n;
-        const int rows = min(8, tiles_m - band * 8);
-        w.tn = r / rows;
-        w.tm = band * 8 + r - w.tn * rows;
-        return true;
-    }
-};
-
-constexpr int CHUNK = 16;  // accumulator columns a warp turns into outputs at a time
-constexpr int PAIRS = CHUNK / 2;
 
 // A chunk of outputs of one row from fp32, `n` of them valid.
 __device__ __forceinline__ void store_row(uint16_t *dst, const F2 (&v)[PAIRS], int n, int vec, int bf16) {
@@ -290,12 +129,6 @@ __device__ __forceinline__ void gate_values(int act, F2 (&g)[N], F2 (&u)[N], F2 
     });
 }
 
-__device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[CHUNK]) { tmem_ld16(taddr, r); }
-__device__ __forceinline__ void pairs_of(const uint32_t (&r)[CHUNK], F2 (&v)[PAIRS]) {
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) v[i] = f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-}
-
 // The kept values of a chunk of row m: three vectors of each 8 columns.
 struct KeptChunk {
     uint4 v[2][3];
@@ -344,8 +177,6 @@ __device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[PAIRS], 
     }
     store_row(out + at, v, left, p.vec, p.bf16);
 }
-
-enum Site : uint32_t { SITE_STAGE_FULL = 32, SITE_STAGE_EMPTY, SITE_ACC_FULL, SITE_ACC_EMPTY };
 
 template <int CG, int BN, bool AK, bool BKM, int EPI>
 __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__ TcParams p) {
@@ -440,10 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                 if (++s == T::STAGES) s = 0, phase ^= 1;
             }
         }
-        if (!ok) {  // copies in flight land within microseconds; give them two milliseconds
-            const uint64_t t0 = globaltimer();
-            while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
-        }
+        if (!ok) let_end();
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---- MMAs
         Walk walk(p, unit, units);
@@ -476,10 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
             if (ok) commit<CG>(acc_full + 8 * buf);
             ++n_tile;
         }
-        if (!ok) {
-            const uint64_t t0 = globaltimer();
-            while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
-        }
+        if (!ok) let_end();
     } else if (warp >= 4) {
         // ---- outputs: a warp for 32 rows and a share of the columns
         Walk walk(p, unit, units);
@@ -556,35 +381,11 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams 
     allow_dependents();
     grid_dependency_wait();
     constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;
-    const int octets = (p.N + 7) / 8;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= (int64_t)p.batch * p.M * octets) return;
-    const int n = (int)(id % octets) * 8;
-    const int64_t zm = id / octets;
-    const int z = (int)(zm / p.M), m = (int)(zm - (int64_t)z * p.M);
-    const int tm = m / tile_m, tn = n / COLS;
-    // the tile's index in the order of Walk, and the units that hold its first and last block
-    const int band = tm / 8, rows = min(8, p.tiles_m - band * 8);
-    const int t = z * p.tiles_m * p.tiles_n + band * 8 * p.tiles_n + tn * rows + (tm - band * 8);
-    const int KT = p.KB * p.segs;
-    const int64_t total = (int64_t)p.tiles * KT;
-    const int count = stream_unit(total, units, (int64_t)(t + 1) * KT - 1) - stream_unit(total, units, (int64_t)t * KT) + 1;
-    const float *src = p.part + zm * p.part_ld + (int64_t)tn * BN + (n - tn * COLS);
+    int z, m, n, count;
+    const float *src;
+    if (!join_source<COLS, BN>(p, tile_m, units, z, m, n, count, src)) return;
     F2 v[4], u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = u[i] = f2(0.0f);
-    auto add = [](F2(&sum)[4], const float *from) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 a = reinterpret_cast<const float4 *>(from)[i];
-            sum[2 * i] = add2(sum[2 * i], f2(a.x, a.y)), sum[2 * i + 1] = add2(sum[2 * i + 1], f2(a.z, a.w));
-        }
-    };
-#pragma unroll 4
-    for (int j = 0; j < count; ++j) {
-        add(v, src + j * p.part_step);
-        if (EPI == EPI_GATED) add(u, src + j * p.part_step + BN / 2);
-    }
+    add_partials<EPI == EPI_GATED, BN>(src, p.part_step, count, v, u);
     const int left = min(8, p.N - n);
     const int64_t at = (int64_t)m * p.ldo + n;
     auto put = [&](uint16_t *dst, const F2(&r)[4]) {
@@ -627,53 +428,6 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams 
     put(static_cast<uint16_t *>(z ? p.out2 : p.out) + at, v);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
-}
-
-// An operand of I output indexes and K steps, copied `rows` output indexes at a
-// time. K innermost: (K, I). Else: (I, K) in blocks of 64 output indexes, or, where
-// I is a number of whole blocks, (64, K, I / 64), which takes several in one copy.
-bool encode(CUtensorMap &map, const Operand &o, int I, int K, int rows, bool blocks) {
-    const PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
-    if (!enc) return false;
-    const cuuint64_t pitch = (cuuint64_t)o.ld * 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)(o.k_major ? K : blocks ? 64 : I), (cuuint64_t)(o.k_major ? I : K),
-                                (cuuint64_t)(blocks ? I / 64 : 1)};
-    const cuuint64_t strides[2] = {pitch, 128};
-    const cuuint32_t box[3] = {64u, o.k_major ? (cuuint32_t)rows : (cuuint32_t)BK, (cuuint32_t)(rows / 64)};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, blocks ? 3 : 2, const_cast<void *>(o.p), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <typename K, typename... A>
-cudaError_t launch_with(K kernel, int grid, int block, size_t smem, int cluster, cudaStream_t st, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)cluster;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int CG, int BN, bool AK, bool BKM, int EPI>
 cudaError_t launch_shape(const TcParams &p, const TcPlan &pl, cudaStream_t st) {
     using T = Tile<CG, BN>;
@@ -682,8 +436,7 @@ cudaError_t launch_shape(const TcParams &p, const TcPlan &pl, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = launch_with(kernel, pl.units * CG, THREADS, T::SMEM, CG, st, p);
     if (e != cudaSuccess || !p.part) return e;
-    const int64_t octets = (int64_t)p.batch * p.M * ((p.N + 7) / 8);
-    return launch_with(tc_join<BN, EPI>, (int)((octets + 255) / 256), 256, 0, 1, st, p, T::M, pl.units);
+    return launch_with(tc_join<BN, EPI>, join_blocks(p), 256, 0, 1, st, p, T::M, pl.units);
 }
 
 template <int CG, int BN>
@@ -697,48 +450,11 @@ cudaError_t launch_tile(const TcParams &p, const TcPlan &pl, const Product &d, c
 
 }  // namespace
 
-// SMs the work is cut for. A constant, so that sizes and results depend on the
-// shape alone.
-constexpr int SMS = 152;
-
 TcPlan plan_tc(const Product &d) {
-    const int KT = (d.K + BK - 1) / BK * (d.epi != EPI_GATED && d.a1.p && !d.batch ? 2 : 1);
-    const int z = d.batch ? 2 : 1;
-    TcPlan best;
-    double best_cost = 0;
-    for (int v = 0; v < 4; ++v) {
-        TcPlan pl;
-        pl.cg = v < 2 ? 2 : 1;
-        pl.bn = pl.cg == 2 ? 256 : 128;
-        pl.streamed = (v & 1) != 0;
-        const int tm = ROWS * pl.cg, cols = d.epi == EPI_GATED ? pl.bn / 2 : pl.bn;
-        pl.tiles_m = (d.M + tm - 1) / tm;
-        pl.tiles_n = (d.N + cols - 1) / cols;
-        const int64_t tiles = (int64_t)z * pl.tiles_m * pl.tiles_n, total = tiles * KT;
-        if (tiles > 0x3fffffff || total > 0x3fffffffll) continue;  // (streamed indexes stay in 32 bits)
-        const int most = SMS / pl.cg;
-        // clocks: a K block takes 512 in either shape (the pair's MMAs; the single CTA's
-        // shared-memory fill), a tile's start and end about 1500, a second launch 4000, and
-        // partial sums are written and read at about 3000 bytes a clock
-        double cost;
-        if (!pl.streamed) {
-            pl.units = (int)std::min<int64_t>(most, tiles);
-            cost = (double)((tiles + pl.units - 1) / pl.units) * KT * 512 + 1500;
-        } else {
-            pl.units = (int)std::min<int64_t>(most, std::max<int64_t>(1, total / 4));  // 4 blocks at least
-            if (tiles > 8 * pl.units || tiles % pl.units == 0) continue;  // (nearly) even without it
-            // a tile meets at most this many runs of at least floor(total / units) blocks
-            const int64_t slots = (KT - 1) / (total / pl.units) + 2;
-            pl.slots = (int)slots;
-            pl.part_ld = (int64_t)pl.tiles_n * pl.bn;
-            pl.part_step = (int64_t)z * d.M * pl.part_ld;
-            pl.part_bytes = (size_t)(slots * pl.part_step) * 4;
-            const double moved = (double)(tiles + pl.units) * std::min(tm, d.M) * pl.bn * 8;
-            cost = (double)((total + pl.units - 1) / pl.units) * 512 + 3000 + 4000 + moved / 3000;
-        }
-        if (best.units == 0 || cost < best_cost) best = pl, best_cost = cost;
-    }
-    return best;
+    // clocks: a K block takes 512 in either shape (the pair's MMAs; the single CTA's
+    // shared-memory fill)
+    const TcPlan pair = plan_tiles(d, 2, 256, 512), single = plan_tiles(d, 1, 128, 512);
+    return pair.units == 0 || (single.units != 0 && single.cost < pair.cost) ? single : pair;
 }
 
 cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool clear_status, void *part, cudaStream_t st) {
@@ -754,10 +470,10 @@ cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool clear_
     const int b_box = d.epi == EPI_GATED && pl.cg == 1 ? pl.bn / 2 : pl.bn / pl.cg;
     p.a_blocks = !d.a0.k_major && d.M % 64 == 0;
     p.b_blocks = !d.b0.k_major && d.N % 64 == 0;
-    if (!encode(p.a[0], d.a0, d.M, d.K, p.a_rows, p.a_blocks) || !encode(p.b[0], d.b0, d.N, d.K, b_box, p.b_blocks))
+    if (!encode(p.a[0], d.a0, 0, d.M, d.K, p.a_rows, p.a_blocks) || !encode(p.b[0], d.b0, 0, d.N, d.K, b_box, p.b_blocks))
         return cudaErrorInvalidValue;
-    if (two && !encode(p.a[1], d.a1, d.M, d.K, p.a_rows, p.a_blocks)) return cudaErrorInvalidValue;
-    if (d.b1.p && !encode(p.b[1], d.b1, d.N, d.K, b_box, p.b_blocks)) return cudaErrorInvalidValue;
+    if (two && !encode(p.a[1], d.a1, 0, d.M, d.K, p.a_rows, p.a_blocks)) return cudaErrorInvalidValue;
+    if (d.b1.p && !encode(p.b[1], d.b1, 0, d.N, d.K, b_box, p.b_blocks)) return cudaErrorInvalidValue;
     p.bf16 = bf16; p.act = d.act;
     p.out = d.out; p.out2 = d.out2; p.kept = static_cast<unsigned char *>(d.kept); p.ldo = d.ldo;
     p.vec = d.ldo % 16 == 0 && aligned_to(d.out, 32) && aligned_to(d.out2, 32) ? 32 : d.ldo % 8 == 0 ? 16 : 2;

@@ -27,59 +27,65 @@ struct Parts {
     }
 };
 
-// A call's problem. 16-bit types run on the tensor cores, whose copies need row
-// pitches that are multiples of 16 bytes: own buffers have such a pitch, and
-// matrices of the caller whose width is no multiple of 8 are first copied to one.
+// A call's problem. The tensor cores' copies need row pitches that are multiples
+// of 16 bytes: own buffers have such a pitch, and matrices of the caller whose
+// width is no multiple of 8 are first copied to one. fp32 matrices are always
+// copied, to three bf16 planes, and own ones are such planes.
 struct Problem {
-    int R, C, F, dtype, esz, act;
-    bool tc;
+    int R, C, F, dtype, act;
+    bool f32;
     int64_t Cp, Fp;  // pitches of rows of C and F elements
     Problem(int64_t R_, int64_t C_, int64_t F_, int act_, int dtype_)
-        : R((int)R_), C((int)C_), F((int)F_), dtype(dtype_), esz(elem_size(dtype_)), act(act_),
-          tc(dtype_ != IM2WIN_F32), Cp(tc ? (C_ + 7) / 8 * 8 : C_), Fp(tc ? (F_ + 7) / 8 * 8 : F_) {}
+        : R((int)R_), C((int)C_), F((int)F_), dtype(dtype_), act(act_), f32(dtype_ == IM2WIN_F32),
+          Cp((C_ + 7) / 8 * 8), Fp((F_ + 7) / 8 * 8) {}
 
     // the forward pass of few rows has kernels of its own
     bool few() const { return is_few(R, C, F, dtype); }
-    size_t rows_c(int64_t rows) const { return (size_t)(rows * Cp) * esz; }
-    size_t rows_f(int64_t rows) const { return (size_t)(rows * Fp) * esz; }
+    // own buffers
+    size_t rows_c(int64_t rows) const { return (size_t)(rows * Cp) * (f32 ? 6 : 2); }
+    size_t rows_f(int64_t rows) const { return (size_t)(rows * Fp) * (f32 ? 6 : 2); }
+    bool copies(int64_t cols) const { return f32 || cols % 8 != 0; }
+
+    Operand by_c(const void *p, int64_t rows, bool k_major) const { return {p, Cp, k_major, rows * Cp}; }
+    Operand by_f(const void *p, int64_t rows, bool k_major) const { return {p, Fp, k_major, rows * Fp}; }
 
     Product gated(const void *x, const void *wg, const void *wu, void *h, void *kept) const {
         Product p;
         p.M = R; p.N = F; p.K = C;
-        p.a0 = {x, Cp, true}; p.b0 = {wg, Cp, true}; p.b1 = {wu, Cp, true};
+        p.a0 = by_c(x, R, true); p.b0 = by_c(wg, F, true); p.b1 = by_c(wu, F, true);
         p.epi = EPI_GATED; p.act = act;
-        p.out = h; p.ldo = Fp; p.kept = kept;
+        p.out = h; p.ldo = Fp; p.plane = R * Fp; p.kept = kept;
         return p;
     }
     Product down(const void *h, const void *wd, void *y) const {
         Product p;
         p.M = R; p.N = C; p.K = F;
-        p.a0 = {h, Fp, true}; p.b0 = {wd, Fp, true};
+        p.a0 = by_f(h, R, true); p.b0 = by_f(wd, C, true);
         p.out = y; p.ldo = C;
         return p;
     }
     Product dgated(const void *dy, const void *wd, const void *kept, void *dg, void *du) const {
         Product p;
         p.M = R; p.N = F; p.K = C;
-        p.a0 = {dy, Cp, true}; p.b0 = {wd, Fp, false};
+        p.a0 = by_c(dy, R, true); p.b0 = by_f(wd, C, false);
         p.epi = EPI_DGATED; p.act = act;
-        p.out = dg; p.out2 = du; p.ldo = Fp;
+        p.out = dg; p.out2 = du; p.ldo = Fp; p.plane = R * Fp;
         p.kept = const_cast<void *>(kept);
         return p;
     }
     Product dx(const void *dg, const void *du, const void *wg, const void *wu, void *out) const {
         Product p;
         p.M = R; p.N = C; p.K = F;
-        p.a0 = {dg, Fp, true}; p.b0 = {wg, Cp, false};
-        p.a1 = {du, Fp, true}; p.b1 = {wu, Cp, false};
+        p.a0 = by_f(dg, R, true); p.b0 = by_c(wg, F, false);
+        p.a1 = by_f(du, R, true); p.b1 = by_c(wu, F, false);
         p.out = out; p.ldo = C;
         return p;
     }
     Product dw_in(const void *dg, const void *du, const void *x, void *dwg, void *dwu) const {
         Product p;
         p.M = F; p.N = C; p.K = R;
-        p.a0 = {dg, Fp, false}; p.a1 = {du, Fp, false};
-        p.b0 = p.b1 = {x, Cp, false};
+        p.a0 = by_f(dg, R, false); p.a1 = by_f(du, R, false);
+        p.b0 = p.b1 = by_c(x, R, false);
         p.batch = true;
         p.out = dwg; p.out2 = dwu; p.ldo = C;
         return p;
@@ -87,10 +93,11 @@ struct Problem {
     Product dw_down(const void *dy, const void *h, void *out) const {
         Product p;
         p.M = C; p.N = F; p.K = R;
-        p.a0 = {dy, Cp, false}; p.b0 = {h, Fp, false};
+        p.a0 = by_c(dy, R, false); p.b0 = by_f(h, R, false);
         p.out = out; p.ldo = F;
         return p;
     }
+    TcPlan plan(const Product &p) const { return f32 ? plan_f32(p) : plan_tc(p); }
 };
 
 // saved: h, then what the backward pass needs of g and u.
@@ -99,7 +106,7 @@ struct SavedParts {
     explicit SavedParts(const Problem &q) {
         Parts p(0);
         h = p.add(q.rows_f(q.R));
-        kept = p.add(kept_bytes(q.R, q.F, !q.tc));
+        kept = p.add(kept_bytes(q.R, q.F, q.f32));
         bytes = p.end;
     }
 };
@@ -111,22 +118,21 @@ struct ForwardParts {
     size_t h, h_lo, x, wg, wu, wd, part, bytes;
     ForwardParts(const Problem &q, bool saved) {
         Parts p(kStatusBytes);
-        h = p.add(saved ? 0 : q.rows_f(q.R));
-        h_lo = x = wg = wu = wd = part = p.end;
-        if (q.few()) {
-            p.add(q.tc ? q.rows_f(q.R) : 0);
-            bytes = p.end;
+        if (q.few()) {  // fp32: h as it is; else its rounding (in `saved` if there is one) and the remainder
+            h = p.add(q.f32 ? (size_t)q.R * q.F * 4 : saved ? 0 : q.rows_f(q.R));
+            h_lo = p.add(q.f32 ? 0 : q.rows_f(q.R));
+            x = wg = wu = wd = part = bytes = p.end;
             return;
         }
-        const bool pad_c = q.Cp != q.C, pad_f = q.Fp != q.F;
-        x = p.add(pad_c ? q.rows_c(q.R) : 0);
-        wg = p.add(pad_c ? q.rows_c(q.F) : 0);
-        wu = p.add(pad_c ? q.rows_c(q.F) : 0);
-        wd = p.add(pad_f ? q.rows_f(q.C) : 0);
+        h = h_lo = p.add(saved ? 0 : q.rows_f(q.R));
+        x = p.add(q.copies(q.C) ? q.rows_c(q.R) : 0);
+        wg = p.add(q.copies(q.C) ? q.rows_c(q.F) : 0);
+        wu = p.add(q.copies(q.C) ? q.rows_c(q.F) : 0);
+        wd = p.add(q.copies(q.F) ? q.rows_f(q.C) : 0);
         part = p.end;
-        if (q.tc && q.R > 0)
-            p.add(std::max(plan_tc(q.gated(kSome, kSome, kSome, kSomeOut, nullptr)).part_bytes,
-                           plan_tc(q.down(kSome, kSome, kSomeOut)).part_bytes));
+        if (q.R > 0)
+            p.add(std::max(q.plan(q.gated(kSome, kSome, kSome, kSomeOut, nullptr)).part_bytes,
+                           q.plan(q.down(kSome, kSome, kSomeOut)).part_bytes));
         bytes = p.end;
     }
 };
@@ -137,19 +143,18 @@ struct BackwardParts {
         Parts p(kStatusBytes);
         dg = p.add(q.rows_f(q.R));
         du = p.add(q.rows_f(q.R));
-        const bool pad_c = q.Cp != q.C, pad_f = q.Fp != q.F;
-        x = p.add(pad_c ? q.rows_c(q.R) : 0);
-        dy = p.add(pad_c ? q.rows_c(q.R) : 0);
-        wg = p.add(pad_c ? q.rows_c(q.F) : 0);
-        wu = p.add(pad_c ? q.rows_c(q.F) : 0);
-        wd = p.add(pad_f ? q.rows_f(q.C) : 0);
+        x = p.add(q.copies(q.C) ? q.rows_c(q.R) : 0);
+        dy = p.add(q.copies(q.C) ? q.rows_c(q.R) : 0);
+        wg = p.add(q.copies(q.C) ? q.rows_c(q.F) : 0);
+        wu = p.add(q.copies(q.C) ? q.rows_c(q.F) : 0);
+        wd = p.add(q.copies(q.F) ? q.rows_f(q.C) : 0);
         part = p.end;
-        if (q.tc && q.R > 0) {
+        if (q.R > 0) {
             size_t most = 0;
             for (const Product &d : {q.dgated(kSome, kSome, nullptr, kSomeOut, kSomeOut),
                                      q.dx(kSome, kSome, kSome, kSome, kSomeOut),
                                      q.dw_in(kSome, kSome, kSome, kSomeOut, kSomeOut), q.dw_down(kSome, kSome, kSomeOut)})
-                most = std::max(most, plan_tc(d).part_bytes);
+                most = std::max(most, q.plan(d).part_bytes);
             p.add(most);
         }
         bytes = p.end;
@@ -174,23 +179,20 @@ struct Sequence {
     Repitch copies[5];
     int n_copies = 0;
 
-    // The matrix itself, or its copy at `to` with a pitch of whole vectors.
-    const void *pitched(const void *src, int rows, int cols, size_t to) {
-        if (!q.tc || cols % 8 == 0) return src;
+    // The matrix itself, or its copy at `to` that the products can read.
+    const void *readable(const void *src, int rows, int cols, size_t to) {
+        if (!q.copies(cols)) return src;
         copies[n_copies++] = {src, at(ws, to), rows, cols};
         return at(ws, to);
     }
-    void copy_pitched() {
-        if (n_copies && e == cudaSuccess) e = launch_repitch(copies, n_copies, st);
+    void copy() {
+        if (n_copies && e == cudaSuccess) e = launch_repitch(copies, n_copies, q.f32, st);
     }
     void run(const Product &p) {
         if (e != cudaSuccess) return;
-        if (q.tc) {
-            e = launch_tc(p, q.dtype == IM2WIN_BF16, static_cast<uint32_t *>(ws), !cleared, part, st);
-        } else {
-            if (!cleared) e = cudaMemsetAsync(ws, 0, kStatusBytes, st);
-            if (e == cudaSuccess) e = launch_simt(p, st);
-        }
+        uint32_t *status = static_cast<uint32_t *>(ws);
+        e = q.f32 ? launch_f32(p, status, !cleared, part, st)
+                  : launch_tc(p, q.dtype == IM2WIN_BF16, status, !cleared, part, st);
         cleared = true;
     }
 };
@@ -231,16 +233,17 @@ im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     void *kept = saved ? at(saved, own.kept) : nullptr;
     if (q.few()) {
-        const Few f = {q.R, q.C, q.F, act, x, w_gate, w_up, w_down, y, h, at(ws, parts.h_lo), q.Fp, kept,
+        const Few f = {q.R, q.C, q.F, act, x, w_gate, w_up, w_down, y, q.f32 ? at(ws, parts.h) : h,
+                       at(ws, parts.h_lo), q.f32 ? (int64_t)q.F : q.Fp, static_cast<uint16_t *>(h), q.Fp, kept,
                        static_cast<uint32_t *>(ws)};
         return launch_few(f, dtype, st) == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
     }
     Sequence seq{q, ws, at(ws, parts.part), st};
-    x = seq.pitched(x, q.R, q.C, parts.x);
-    w_gate = seq.pitched(w_gate, q.F, q.C, parts.wg);
-    w_up = seq.pitched(w_up, q.F, q.C, parts.wu);
-    w_down = seq.pitched(w_down, q.C, q.F, parts.wd);
-    seq.copy_pitched();
+    x = seq.readable(x, q.R, q.C, parts.x);
+    w_gate = seq.readable(w_gate, q.F, q.C, parts.wg);
+    w_up = seq.readable(w_up, q.F, q.C, parts.wu);
+    w_down = seq.readable(w_down, q.C, q.F, parts.wd);
+    seq.copy();
     seq.run(q.gated(x, w_gate, w_up, h, kept));
     seq.run(q.down(h, w_down, y));
     return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
@@ -273,14 +276,14 @@ im2win_status im2win_gated_ffn_backward(const void *dy, const void *x, const voi
     const SavedParts own(q);
     void *dg = at(ws, parts.dg), *du = at(ws, parts.du);
     Sequence seq{q, ws, at(ws, parts.part), st};
-    dy = seq.pitched(dy, q.R, q.C, parts.dy);
-    w_down = seq.pitched(w_down, q.C, q.F, parts.wd);
+    dy = seq.readable(dy, q.R, q.C, parts.dy);
+    w_down = seq.readable(w_down, q.C, q.F, parts.wd);
     if (dx) {
-        w_gate = seq.pitched(w_gate, q.F, q.C, parts.wg);
-        w_up = seq.pitched(w_up, q.F, q.C, parts.wu);
+        w_gate = seq.readable(w_gate, q.F, q.C, parts.wg);
+        w_up = seq.readable(w_up, q.F, q.C, parts.wu);
     }
-    if (want_dw) x = seq.pitched(x, q.R, q.C, parts.x);
-    seq.copy_pitched();
+    if (want_dw) x = seq.readable(x, q.R, q.C, parts.x);
+    seq.copy();
     seq.run(q.dgated(dy, w_down, at(saved, own.kept), dg, du));
     if (dx) seq.run(q.dx(dg, du, w_gate, w_up, dx));
     if (want_dw) {

@@ -24,6 +24,7 @@ struct Operand {
     const void *p = nullptr;
     int64_t ld = 0;
     bool k_major = true;
+    int64_t plane = 0;  // fp32 in three bf16 planes: elements from one to the next
 };
 
 // What becomes of an accumulated element (m, n).
@@ -42,13 +43,33 @@ enum Epilogue {
 // b's, then 16 bytes a row of the next bytes, a's and b's, so that a warp whose
 // lanes hold a row each moves 512 contiguous bytes.
 //
-// fp32: in fp32, row by row, all a before all b.
+// fp32: in fp32, blocks of 32 rows by 4 columns, 16 bytes a row, all a before all b.
 constexpr int KEPT_BLOCK = 1536;
 __host__ __device__ inline int64_t kept_block(int m, int n, int N) {
     return ((int64_t)(m / 32) * ((N + 7) / 8) + n / 8) * KEPT_BLOCK + (m % 32) * 16;
 }
+__host__ __device__ inline int64_t kept_index_f32(int m, int n, int N) {
+    return ((int64_t)(m / 32) * ((N + 3) / 4) + n / 4) * 128 + (m % 32) * 4 + n % 4;
+}
+__host__ __device__ inline int64_t kept_count_f32(int64_t M, int64_t N) { return (M + 31) / 32 * ((N + 3) / 4) * 128; }
 inline size_t kept_bytes(int64_t M, int64_t N, bool f32) {
-    return f32 ? (size_t)(M * N) * 8 : (size_t)((M + 31) / 32) * (size_t)((N + 7) / 8) * KEPT_BLOCK;
+    return f32 ? (size_t)kept_count_f32(M, N) * 8 : (size_t)((M + 31) / 32) * (size_t)((N + 7) / 8) * KEPT_BLOCK;
+}
+
+// An fp32 value as three bf16 ones: the upper 16 bits (cut, so that they cannot
+// round to infinity), the rest rounded, and what is left rounded: v = h + m + l to
+// 2^-26 of v. Infinities and NaN stand in h alone.
+__device__ __forceinline__ void split_f32(float v, uint16_t &h, uint16_t &m, uint16_t &l) {
+    const uint32_t bits = __float_as_uint(v);
+    if ((bits & 0x7f800000u) == 0x7f800000u) {
+        h = __bfloat16_as_ushort(__float2bfloat16_rn(v)), m = l = 0;
+        return;
+    }
+    const float rest = v - __uint_as_float(bits & 0xffff0000u);
+    const bf16_t mid = __float2bfloat16_rn(rest);
+    h = (uint16_t)(bits >> 16);
+    m = __bfloat16_as_ushort(mid);
+    l = __bfloat16_as_ushort(__float2bfloat16_rn(rest - __bfloat162float(mid)));
 }
 
 // D[M][N] = A0 B0^T (+ A1 B1^T); EPI_GATED: g = A0 B0^T, u = A0 B1^T; batch: out =
@@ -62,10 +83,8 @@ struct Product {
     void *out = nullptr, *out2 = nullptr;
     void *kept = nullptr;  // written (EPI_GATED, may be null) or read (EPI_DGATED)
     int64_t ldo = 0;       // row pitch of out and out2 in elements
+    int64_t plane = 0;     // fp32, GATED and DGATED: elements from one plane of out and out2 to the next
 };
-
-// CUDA cores, fp32.
-cudaError_t launch_simt(const Product &p, cudaStream_t st);
 
 // Tensor cores: fp16/bf16; operands 16-byte aligned with pitches that are multiples
 // of 8 elements. A product takes part_bytes of scratch. status: the workspace's
@@ -76,9 +95,15 @@ struct TcPlan {
     int tiles_m = 0, tiles_n = 0, units = 0, slots = 0;
     int64_t part_ld = 0, part_step = 0;
     size_t part_bytes = 0;
+    double cost = 0;          // estimated clocks
 };
 TcPlan plan_tc(const Product &p);
 cudaError_t launch_tc(const Product &p, bool bf16, uint32_t *status, bool clear_status, void *part, cudaStream_t st);
+
+// The same for fp32, whose operands are three bf16 planes each (h + m + l, see
+// split_f32): GATED and DGATED write such planes, STORE writes fp32.
+TcPlan plan_f32(const Product &p);
+cudaError_t launch_f32(const Product &p, uint32_t *status, bool clear_status, void *part, cudaStream_t st);
 
 // The forward pass of few rows (where is_few), from dense matrices of any
 // alignment that their type allows; h and its remainder h_lo (16-bit types) have
@@ -88,19 +113,22 @@ struct Few {
     const void *x, *w_gate, *w_up, *w_down;
     void *y, *h, *h_lo;
     int64_t ldh;
+    uint16_t *planes;  // fp32, training: h in three planes of R rows of plane_ld elements
+    int64_t plane_ld;
     void *kept;
     uint32_t *status;
 };
 bool is_few(int64_t R, int64_t C, int64_t F, int dtype);
 cudaError_t launch_few(const Few &f, int dtype, cudaStream_t st);
 
-// Copies of dense matrices to a pitch that is a multiple of 8 elements (16-bit types).
+// Copies of dense matrices to a pitch that is a multiple of 8 elements: 16-bit types
+// as they are, fp32 in three bf16 planes.
 struct Repitch {
     const void *src;
     void *dst;
     int rows, cols;
 };
-cudaError_t launch_repitch(const Repitch *list, int count, cudaStream_t st);  // count <= 5
+cudaError_t launch_repitch(const Repitch *list, int count, bool f32, cudaStream_t st);  // count <= 5
 
 }  // namespace ffn
 }  // namespace im2win
