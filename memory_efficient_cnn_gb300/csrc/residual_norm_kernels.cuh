@@ -219,18 +219,25 @@ __global__ void __launch_bounds__(256) join_partials(const float *part, int64_t 
 // elements: 16-byte vectors where C allows, else 4-byte ones, else elements.
 // Arithmetic is on pairs of values (F2).
 
-__device__ __forceinline__ void to_pair(F2 v, float &lo, float &hi) { split(v, lo, hi); }
-__device__ __forceinline__ void to_pair(F2 v, f16_t &lo, f16_t &hi) {
-    float a, b;
-    split(v, a, b);
-    const __half2 r = __floats2half2_rn(a, b);
-    lo = __low2half(r), hi = __high2half(r);
+// Two neighbouring 16-bit values, as they lie in a word, and their fp32 pair.
+__device__ __forceinline__ F2 pair_of_word(uint32_t w, bf16_t) {
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-__device__ __forceinline__ void to_pair(F2 v, bf16_t &lo, bf16_t &hi) {
+__device__ __forceinline__ F2 pair_of_word(uint32_t w, f16_t) {
+    const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return f2(r.x, r.y);
+}
+__device__ __forceinline__ uint32_t word_of_pair(F2 v, bf16_t) {
     float a, b;
     split(v, a, b);
     const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-    lo = __low2bfloat16(r), hi = __high2bfloat16(r);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t word_of_pair(F2 v, f16_t) {
+    float a, b;
+    split(v, a, b);
+    const __half2 r = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 template <typename T, int V, int EPT, int TPR>
@@ -238,6 +245,7 @@ struct Row {
     static constexpr int VPT = EPT / V, PAIRS = EPT / 2;
     using E = T;
     using P = Vec<T, V>;
+    static constexpr bool WORDS = sizeof(T) == 2 && V >= 2;  // pairs of values are words
     struct Packed {
         P v[VPT];
     };
@@ -260,23 +268,28 @@ struct Row {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = first(j, t);
-            T e[V > 1 ? V : 2];
-            if (V > 1) {
-#pragma unroll
-                for (int i = 0; i < V / 2; ++i) to_pair(v[j * V / 2 + i], e[2 * i], e[2 * i + 1]);
-            } else {
-                to_pair(v[j / 2], e[0], e[1]);
-                e[0] = e[j % 2];
-            }
             if (c >= C) continue;
             P d;
+            if constexpr (WORDS) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) d.v[i] = e[i];
+                for (int i = 0; i < V / 2; ++i)
+                    reinterpret_cast<uint32_t *>(&d)[i] = word_of_pair(v[j * V / 2 + i], T());
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float a, b;
+                    split(v[(j * V + i) / 2], a, b);
+                    d.v[i] = from_f32<T>((j * V + i) % 2 ? b : a);
+                }
+            }
             *reinterpret_cast<P *>(static_cast<T *>(p) + at + c) = d;
         }
     }
-    static __device__ __forceinline__ float get(const Packed &d, int e) { return to_f32(d.v[e / V].v[e % V]); }
-    static __device__ __forceinline__ F2 pair(const Packed &d, int i) { return f2(get(d, 2 * i), get(d, 2 * i + 1)); }
+    // Values 2 i and 2 i + 1.
+    static __device__ __forceinline__ F2 pair(const Packed &d, int i) {
+        if constexpr (WORDS) return pair_of_word(reinterpret_cast<const uint32_t *>(&d)[i], T());
+        else return f2(to_f32(d.v[2 * i / V].v[2 * i % V]), to_f32(d.v[(2 * i + 1) / V].v[(2 * i + 1) % V]));
+    }
     static __device__ __forceinline__ void clear_outside(F2 (&v)[PAIRS], int C, int t) {
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
