@@ -65,11 +65,12 @@ enum BackSum { BACK_RES, BACK_W_PRE, BACK_B_PRE, BACK_A, BACK_B, BACK_SUMS };
 constexpr int SMS = 152;  // blocks are cut for this many SMs, so that results depend on the shape alone
 constexpr int FUSED_THREADS = 512;
 
-// The fused pass holds rows of up to 4096 elements (8 a thread).
+// The fused pass holds rows of up to 4096 elements (8 a thread), or 8192 (16 a
+// thread, which leaves no shared memory for short groups).
 inline BackPlan plan_back(int64_t R, int64_t C, int64_t per_gate) {
     BackPlan b;
-    if (R == 0 || C > 8 * FUSED_THREADS) return b;
-    b.ept = 8;
+    if (R == 0 || C > 16 * FUSED_THREADS) return b;
+    b.ept = C > 8 * FUSED_THREADS ? 16 : 8;
     b.threads = FUSED_THREADS;
     b.tpr = 8;
     while (b.tpr * b.ept < C) b.tpr *= 2;
@@ -81,6 +82,7 @@ inline BackPlan plan_back(int64_t R, int64_t C, int64_t per_gate) {
     const int64_t long_rounds = (R + slots - 1) / slots + 2 * (b.groups / b.blocks + 1) + b.groups / b.blocks;
     const int64_t short_rounds = (b.groups + slots - 1) / slots * (per_gate + 1);
     b.short_groups = short_rounds < long_rounds;
+    if (b.short_groups && b.ept == 16) return BackPlan();
     b.segments = b.short_groups ? 0 : b.groups + b.blocks;
     return b;
 }

@@ -589,8 +589,10 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2)
 //                groups) for dgate, and weighed with the gate into its sums;
 //  short groups  a row slot takes whole groups, writes their dgate and adds the
 //                weighed A and B to its sums in shared memory.
+template <typename R>
+constexpr int BACK_DEPTH = sizeof(typename R::Packed) <= 16 ? 3 : sizeof(typename R::Packed) <= 32 ? 2 : 1;
 template <typename R, int THREADS>
-using BackAhead = Ahead<R, 4, sizeof(typename R::Packed) <= 16 ? 3 : 2, THREADS>;
+using BackAhead = Ahead<R, 4, BACK_DEPTH<R>, THREADS>;
 // Shared memory of the rows on their way, which also joins slots: THREADS * EPT floats.
 template <typename R, int THREADS>
 constexpr int BACK_ROWS_BYTES = BackAhead<R, THREADS>::BYTES > THREADS * R::PAIRS * 8 ? BackAhead<R, THREADS>::BYTES
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         T *dgate) {
     using R = Row<T, V, EPT, TPR>;
     using A = BackAhead<R, THREADS>;
-    constexpr int RPB = THREADS / TPR, DEPTH = sizeof(typename R::Packed) <= 16 ? 3 : 2;
+    constexpr int RPB = THREADS / TPR, DEPTH = BACK_DEPTH<R>;
     constexpr int W = TPR * EPT;  // columns a slot holds
     // rows on their way, between groups [RPB][W] to join slots; parameters; SHORT: A and B weighed, [2][RPB][W]
     extern __shared__ uint4 dyn[];
@@ -920,13 +922,12 @@ __global__ void __launch_bounds__(256) norm_join(const __grid_constant__ NormArg
     }
 }
 
-template <typename T, int V, int TPR>
+template <typename T, int V, int EPT, int TPR, bool SHORT>
 cudaError_t launch_fused(const NormArgs &p, const BackPlan &plan, float *part, float *seg, T *dgate, cudaStream_t st) {
-    constexpr int EPT = 8, THREADS = FUSED_THREADS;
+    constexpr int THREADS = FUSED_THREADS;
     using R = Row<T, V, EPT, TPR>;
-    const size_t smem = BACK_ROWS_BYTES<R, THREADS> + Params<R, PARAMS, TPR>::BYTES + (plan.short_groups ? 2 * THREADS * EPT * 4 : 0);
-    auto kernel = plan.short_groups ? norm_backward_fused<T, V, EPT, TPR, THREADS, true>
-                                    : norm_backward_fused<T, V, EPT, TPR, THREADS, false>;
+    const size_t smem = BACK_ROWS_BYTES<R, THREADS> + Params<R, PARAMS, TPR>::BYTES + (SHORT ? 2 * THREADS * EPT * 4 : 0);
+    auto kernel = norm_backward_fused<T, V, EPT, TPR, THREADS, SHORT>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kernel<<<plan.blocks, THREADS, smem, st>>>(p, plan, part, seg, dgate);
@@ -935,14 +936,20 @@ cudaError_t launch_fused(const NormArgs &p, const BackPlan &plan, float *part, f
 
 template <typename T, int V>
 cudaError_t launch_fused_tpr(const NormArgs &p, const BackPlan &plan, float *part, float *seg, T *dgate, cudaStream_t st) {
+    if (plan.ept == 16) return launch_fused<T, V, 16, 512, false>(p, plan, part, seg, dgate, st);
+    auto with = [&](auto tpr) {
+        constexpr int TPR = decltype(tpr)::value;
+        return plan.short_groups ? launch_fused<T, V, 8, TPR, true>(p, plan, part, seg, dgate, st)
+                                 : launch_fused<T, V, 8, TPR, false>(p, plan, part, seg, dgate, st);
+    };
     switch (plan.tpr) {
-        case 8: return launch_fused<T, V, 8>(p, plan, part, seg, dgate, st);
-        case 16: return launch_fused<T, V, 16>(p, plan, part, seg, dgate, st);
-        case 32: return launch_fused<T, V, 32>(p, plan, part, seg, dgate, st);
-        case 64: return launch_fused<T, V, 64>(p, plan, part, seg, dgate, st);
-        case 128: return launch_fused<T, V, 128>(p, plan, part, seg, dgate, st);
-        case 256: return launch_fused<T, V, 256>(p, plan, part, seg, dgate, st);
-        default: return launch_fused<T, V, 512>(p, plan, part, seg, dgate, st);
+        case 8: return with(IntC<8>());
+        case 16: return with(IntC<16>());
+        case 32: return with(IntC<32>());
+        case 64: return with(IntC<64>());
+        case 128: return with(IntC<128>());
+        case 256: return with(IntC<256>());
+        default: return with(IntC<512>());
     }
 }
 
