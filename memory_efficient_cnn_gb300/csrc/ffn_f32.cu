@@ -25,7 +25,8 @@ constexpr int BN = 128;
 constexpr int PLANES = 3;
 constexpr int A_BYTES = ROWS * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
 constexpr int STAGES = 6;
-constexpr int SMEM = STAGE * STAGES + 1024;
+constexpr int STAGED = 32 * 9;  // floats of a warp's staged outputs
+constexpr int SMEM = STAGE * STAGES + 1024 + EPI_WARPS * STAGED * 4;
 constexpr int CHUNK_KB = 4;  // K blocks of one run of the accumulators
 
 struct F32Params {
@@ -43,18 +44,30 @@ struct F32Params {
     uint32_t *status;
 };
 
-// 16 columns of a row in fp32, `n` of them valid.
-__device__ __forceinline__ void store_f32(float *dst, const F2 (&v)[PAIRS], int n, bool vec) {
-    if (vec && n >= CHUNK) {
+// 16 columns of a row of whole 16-byte vectors in fp32, `n` columns from here on (a multiple of 4).
+__device__ __forceinline__ void store_f32(float *dst, const F2 (&v)[PAIRS], int n) {
 #pragma unroll
-        for (int i = 0; i < PAIRS / 2; ++i)
-            reinterpret_cast<ulonglong2 *>(dst)[i] = make_ulonglong2(v[2 * i].v, v[2 * i + 1].v);
-    } else {
+    for (int i = 0; i < PAIRS / 2; ++i)
+        if (4 * i < n) reinterpret_cast<ulonglong2 *>(dst)[i] = make_ulonglong2(v[2 * i].v, v[2 * i + 1].v);
+}
+// A warp's 16 columns of 32 rows into rows of any pitch, through its part of shared memory,
+// so that neighbouring lanes store neighbouring columns. rows, n: valid rows and columns.
+__device__ __forceinline__ void store_f32_staged(float *dst, int64_t ldo, const F2 (&v)[PAIRS], int rows, int n, float *stage) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < CHUNK; ++i) {
+    for (int half = 0; half < 2; ++half) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             float a, b;
-            split(v[i / 2], a, b);
-            if (i < n) dst[i] = i & 1 ? b : a;
+            split(v[half * 4 + i], a, b);
+            stage[lane * 9 + 2 * i] = a, stage[lane * 9 + 2 * i + 1] = b;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+            const int row = it * 4 + lane / 8, c = lane % 8;
+            if (row < rows && half * 8 + c < n) dst[row * ldo + half * 8 + c] = stage[row * 9 + c];
         }
     }
 }
@@ -266,6 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
         const int q = warp & 3, share = (warp - 4) >> 2;
         const int c0 = EPI == EPI_GATED ? share * CHUNK : share * 2 * CHUNK;
         const int c1 = EPI == EPI_GATED ? BN / 2 + share * CHUNK : c0 + CHUNK;
+        float *stage = reinterpret_cast<float *>(dyn + STAGES * STAGE + 1024) + (warp - 4) * STAGED;
         int n_run = 0;
         bool ok = true;
         while (ok && walk.next(w)) {
@@ -300,14 +314,18 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
             if (p.part) {
                 float *dst = p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
                 if (m < p.M) {
-                    store_f32(dst + c0, sum[0], CHUNK, true);
-                    store_f32(dst + c1, sum[1], CHUNK, true);
+                    store_f32(dst + c0, sum[0], CHUNK);
+                    store_f32(dst + c1, sum[1], CHUNK);
                 }
             } else if (EPI == EPI_STORE) {
-                const int n = w.tn * BN + c0;
-                float *out = static_cast<float *>(w.z ? p.out2 : p.out) + (int64_t)m * p.ldo + n;
-                if (m < p.M && n < p.N) store_f32(out, sum[0], p.N - n, p.vec);
-                if (m < p.M && n + CHUNK < p.N) store_f32(out + CHUNK, sum[1], p.N - n - CHUNK, p.vec);
+                float *out = static_cast<float *>(w.z ? p.out2 : p.out);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int n = w.tn * BN + c0 + half * CHUNK;
+                    if (n >= p.N) break;
+                    if (!p.vec) store_f32_staged(out + (int64_t)(m - lane) * p.ldo + n, p.ldo, sum[half], p.M - (m - lane), p.N - n, stage);
+                    else if (m < p.M) store_f32(out + (int64_t)m * p.ldo + n, sum[half], p.N - n);
+                }
             } else if (EPI == EPI_GATED) {
                 finish<EPI, CHUNK>(p, sum[0], sum[1], w.z, m, w.tn * (BN / 2) + c0);
             } else {

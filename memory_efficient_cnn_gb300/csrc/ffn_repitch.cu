@@ -14,8 +14,8 @@ struct List {
     int count;
 };
 
-// One 16-byte output vector per thread, eight 2-byte loads (a row's start has
-// any alignment); elements past a row's end are written as zero.
+// One 16-byte output vector per thread from the widest loads that every row's start
+// allows; elements past a row's end are written as zero.
 __global__ void __launch_bounds__(256) repitch(const __grid_constant__ List l) {
     tc::allow_dependents();
     tc::grid_dependency_wait();
@@ -29,10 +29,15 @@ __global__ void __launch_bounds__(256) repitch(const __grid_constant__ List l) {
     const int c = (int)(id - l.first[i] - row * vecs) * 8;
     const uint16_t *src = static_cast<const uint16_t *>(m.src) + row * m.cols + c;
     uint32_t v[4];
+    if (m.cols % 2 == 0) {  // rows start on 4 bytes
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t x = c + e < m.cols ? src[e] : 0u;
-        v[e / 2] = e % 2 ? v[e / 2] | (x << 16) : x;
+        for (int e = 0; e < 4; ++e) v[e] = c + 2 * e < m.cols ? *reinterpret_cast<const uint32_t *>(src + 2 * e) : 0u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t x = c + e < m.cols ? src[e] : 0u;
+            v[e / 2] = e % 2 ? v[e / 2] | (x << 16) : x;
+        }
     }
     reinterpret_cast<uint4 *>(m.dst)[row * vecs + c / 8] = make_uint4(v[0], v[1], v[2], v[3]);
 }

@@ -23,6 +23,8 @@ namespace im2win {
 namespace ffn {
 namespace {
 
+constexpr int STAGED_WORDS = 32 * (PAIRS + 1);  // a warp's chunk of outputs
+
 template <int CG, int BN>
 struct Tile {
     static constexpr int M = ROWS * CG;
@@ -30,7 +32,7 @@ struct Tile {
     static constexpr int A_BYTES = ROWS * BK * 2, B_BYTES = B_ROWS * BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int STAGES = 6;
-    static constexpr int SMEM = STAGE * STAGES + 1024 + 256;  // + alignment + barriers
+    static constexpr int SMEM = STAGE * STAGES + 1024 + EPI_WARPS * STAGED_WORDS * 4;  // + alignment, staged outputs
 };
 
 struct TcParams {
@@ -52,26 +54,53 @@ struct TcParams {
     uint32_t *status;
 };
 
-// A chunk of outputs of one row from fp32, `n` of them valid.
-__device__ __forceinline__ void store_row(uint16_t *dst, const F2 (&v)[PAIRS], int n, int vec, int bf16) {
-    uint32_t w[PAIRS];
+// A chunk of outputs of one row from fp32, rounded and packed.
+__device__ __forceinline__ void pack_row(const F2 (&v)[PAIRS], uint32_t (&w)[PAIRS], int bf16) {
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
         float lo, hi;
         split(v[i], lo, hi);
         w[i] = pack2(lo, hi, bf16);
     }
+}
+// Into a row of whole 16-byte vectors, `n` columns from here on (a multiple of 8).
+__device__ __forceinline__ void store_row(uint16_t *dst, const F2 (&v)[PAIRS], int n, int vec, int bf16) {
+    uint32_t w[PAIRS];
+    pack_row(v, w, bf16);
     if (vec == 32 && n >= CHUNK) {  // a whole sector in one store
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                      "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                      : "memory");
-    } else if (vec >= 16 && n >= CHUNK) {
-        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (n >= CHUNK) reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+// A warp's chunk of 32 rows into rows of any pitch, through its part of shared memory, so
+// that neighbouring lanes store neighbouring columns (a lane's own row in 2-byte stores took
+// 78 us for 2 x 3326 x 914 outputs). rows, n: valid rows and columns.
+__device__ __forceinline__ void store_rows_staged(uint16_t *dst, int64_t ldo, const F2 (&v)[PAIRS], int rows, int n, int bf16,
+                                                  uint32_t *stage) {
+    const int lane = threadIdx.x & 31;
+    uint32_t w[PAIRS];
+    pack_row(v, w, bf16);
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < CHUNK; ++i)
-            if (i < n) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    for (int i = 0; i < PAIRS; ++i) stage[lane * (PAIRS + 1) + i] = w[i];
+    __syncwarp();
+    if (ldo % 2 == 0) {  // 4-byte stores (rows and the first column are even)
+#pragma unroll
+        for (int it = 0; it < PAIRS; ++it) {
+            const int row = it * 4 + lane / PAIRS, c = lane % PAIRS * 2;
+            if (row < rows && c < n) *reinterpret_cast<uint32_t *>(dst + row * ldo + c) = stage[row * (PAIRS + 1) + c / 2];
+        }
+    } else {
+        const uint16_t *half = reinterpret_cast<const uint16_t *>(stage);
+#pragma unroll
+        for (int it = 0; it < CHUNK; ++it) {
+            const int row = it * 2 + lane / CHUNK, c = lane % CHUNK;
+            if (row < rows && c < n) dst[row * ldo + c] = half[row * 2 * (PAIRS + 1) + c];
+        }
     }
 }
 
@@ -143,13 +172,21 @@ __device__ __forceinline__ void fetch_kept(const TcParams &p, KeptChunk &k, int 
     }
 }
 
-// Outputs of a chunk of row m from its accumulator values v (and u, or kept), columns from n.
+// Outputs of a chunk of rows m0 + lane from their accumulator values v (and u, or kept), columns
+// from n; every lane of the warp is here.
 template <int EPI>
-__device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[PAIRS], F2 (&u)[PAIRS], const KeptChunk &k, int m,
-                                             int n, uint16_t *out) {
-    const int left = m < p.M ? p.N - n : 0;
-    if (left <= 0) return;
+__device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[PAIRS], F2 (&u)[PAIRS], const KeptChunk &k, int m0,
+                                             int n, uint16_t *out, uint32_t *stage) {
+    const int m = m0 + (threadIdx.x & 31);
+    if (n >= p.N) return;
     const int64_t at = (int64_t)m * p.ldo + n;
+    if (EPI == EPI_STORE) {
+        if (p.vec == 2) store_rows_staged(out + (int64_t)m0 * p.ldo + n, p.ldo, v, min(32, p.M - m0), p.N - n, p.bf16, stage);
+        else if (m < p.M) store_row(out + at, v, p.N - n, p.vec, p.bf16);
+        return;
+    }
+    if (m >= p.M) return;
+    const int left = (int)(p.ldo - n);  // own buffers: whole vectors, whose last may pass N
     if (EPI == EPI_GATED) {
         F2 a[PAIRS];
         if (p.kept) {
@@ -160,7 +197,7 @@ __device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[PAIRS], 
         } else {
             gate_values<PAIRS, false>(p.act, v, u, a);
         }
-    } else if (EPI == EPI_DGATED) {
+    } else {
         F2 du[PAIRS];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -314,6 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
         constexpr int SHARES = EPI_WARPS / 4;
         constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;  // output columns of a tile
         const uint32_t empty_bar0 = CG == 2 ? map_rank(acc_empty, 0) : acc_empty;
+        uint32_t *stage = reinterpret_cast<uint32_t *>(dyn + T::STAGES * T::STAGE + 1024) + (warp - 4) * STAGED_WORDS;
         while (walk.next(w)) {
             const int buf = n_tile & 1;
             const int m = w.tm * T::M + (int)rank * ROWS + q * 32 + lane;
@@ -361,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                     if (EPI == EPI_GATED) pairs_of(ru, u);
                     const KeptChunk now = kept;
                     if (EPI == EPI_DGATED && c + CHUNK < (share + 1) * SPAN) fetch_kept(p, kept, m, w.tn * COLS + c + CHUNK);
-                    finish_chunk<EPI>(p, v, u, now, m, w.tn * COLS + c, out);
+                    finish_chunk<EPI>(p, v, u, now, m - lane, w.tn * COLS + c, out, stage);
                 }
             }
             ++n_tile;
