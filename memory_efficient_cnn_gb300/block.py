@@ -127,10 +127,13 @@ def _ffn_backward(fn, dims, dy, x, w_gate, w_up, w_down, saved, dx, dw_gate, dw_
 
 
 def _ffn_backward_inputs(fn, dims, dy, x, saved, ws):
-    _shape(fn, "dy", dy, x.shape)
-    _same_dtype(fn, x, dy)
-    _same_device(fn, x, dy, saved, ws)
-    _cuda(dy, saved, ws)
+    device = x.get_device()
+    if not (dy.shape == x.shape and _alike(x.dtype, device, dy) and saved.get_device() == ws.get_device() == device
+            and saved.is_contiguous() and ws.is_contiguous()):
+        _shape(fn, "dy", dy, x.shape)
+        _same_dtype(fn, x, dy)
+        _same_device(fn, x, dy, saved, ws)
+        _cuda(dy, saved, ws)
     if _bytes(saved) < im2win_gated_ffn_size(FFN_SAVED, *dims, _dtype_code(x)):
         raise ValueError(f"{fn}: saved is too small")
 

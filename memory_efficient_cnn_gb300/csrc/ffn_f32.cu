@@ -26,7 +26,8 @@ constexpr int PLANES = 3;
 constexpr int A_BYTES = ROWS * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
 constexpr int STAGES = 6;
 constexpr int STAGED = 32 * 9;  // floats of a warp's staged outputs
-constexpr int SMEM = STAGE * STAGES + 1024 + EPI_WARPS * STAGED * 4;
+constexpr int SMEM = STAGE * STAGES + 1024;
+constexpr int SMEM_STAGED = SMEM + EPI_WARPS * STAGED * 4;  // (only where needed: it takes from L1)
 constexpr int CHUNK_KB = 4;  // K blocks of one run of the accumulators
 
 struct F32Params {
@@ -373,9 +374,10 @@ __global__ void __launch_bounds__(256) f32_join(const __grid_constant__ F32Param
 template <bool AK, bool BKM, int EPI>
 cudaError_t launch_kind(const F32Params &p, const TcPlan &pl, cudaStream_t st) {
     auto kernel = f32_product<AK, BKM, EPI>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    const int smem = EPI == EPI_STORE && !p.vec && !p.part ? SMEM_STAGED : SMEM;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_STAGED);
     if (e != cudaSuccess) return e;
-    e = launch_with(kernel, pl.units, THREADS, SMEM, 1, st, p);
+    e = launch_with(kernel, pl.units, THREADS, smem, 1, st, p);
     if (e != cudaSuccess || !p.part) return e;
     return launch_with(f32_join<EPI>, join_blocks(p), 256, 0, 1, st, p, pl.units);
 }
