@@ -41,7 +41,7 @@ struct F32Params {
     int vec;  // 16-byte fp32 stores
     float *part;
     int64_t part_ld, part_step;
-    int clear_status;
+    int first;
     uint32_t *status;
 };
 
@@ -179,14 +179,15 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
         }
         fence_mbar_init();
     }
-    allow_dependents();
-    grid_dependency_wait();
+    // (as in the 16-bit kernel; here a call's first launch is the splitting)
     if (warp == 2) alloc_tmem<1>(smem_u32(&tmem_slot), 4 * BN);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    allow_dependents();
+    grid_dependency_wait();
     const uint32_t tmem = tmem_slot;  // buffer i: the sums of h h' at 2 i BN, the others' BN further
-    if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
+    if (p.first && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
 
     Walk walk(p, blockIdx.x, gridDim.x);
     Work w;
@@ -387,7 +388,7 @@ cudaError_t launch_kind(const F32Params &p, const TcPlan &pl, cudaStream_t st) {
 // Clocks of a K block: 24 MMAs of 64, and the smaller tiles' shared-memory reads.
 TcPlan plan_f32(const Product &d) { return plan_tiles(d, 1, BN, 1800); }
 
-cudaError_t launch_f32(const Product &d, uint32_t *status, bool clear_status, void *part, cudaStream_t st) {
+cudaError_t launch_f32(const Product &d, uint32_t *status, bool first, void *part, cudaStream_t st) {
     const TcPlan pl = plan_f32(d);
     if (pl.units == 0) return cudaErrorInvalidValue;
     F32Params p = {};
@@ -417,7 +418,7 @@ cudaError_t launch_f32(const Product &d, uint32_t *status, bool clear_status, vo
         p.part_step = pl.part_step;
     }
     p.status = status;
-    p.clear_status = clear_status;
+    p.first = first;
     if (d.epi == EPI_GATED) return launch_kind<true, true, EPI_GATED>(p, pl, st);
     if (d.epi == EPI_DGATED) return launch_kind<true, false, EPI_DGATED>(p, pl, st);
     if (!d.a0.k_major) return launch_kind<false, false, EPI_STORE>(p, pl, st);

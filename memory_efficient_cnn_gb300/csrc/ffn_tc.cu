@@ -53,7 +53,7 @@ struct TcParams {
     int vec;                   // bytes of output stores: 32, 16, or 2
     float *part;               // streamed: partial tiles
     int64_t part_ld, part_step;  // row pitch and distance between contributions, in floats
-    int clear_status;
+    int first;                 // the call's first launch: clears the status
     uint32_t *status;
 };
 
@@ -251,17 +251,22 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
         }
         fence_mbar_init();
     }
+    // Tensor memory before the wait for the launch before, but for a call's first launch: what ran
+    // before that may still hold some on this SM, and wait for an SM itself.
+    auto setup = [&] {
+        if (warp == 2) alloc_tmem<CG>(smem_u32(&tmem_slot), 2 * BN);
+        tc_fence_before();
+        __syncthreads();
+        if (CG == 2) cluster_sync();
+        tc_fence_after();
+    };
+    if (!p.first) setup();
     allow_dependents();
     grid_dependency_wait();
-    // (after the wait: an earlier kernel on this SM may still have held tensor memory)
-    if (warp == 2) alloc_tmem<CG>(smem_u32(&tmem_slot), 2 * BN);
-    tc_fence_before();
-    __syncthreads();
-    if (CG == 2) cluster_sync();
-    tc_fence_after();
+    if (p.first) setup();
     const uint32_t tmem = tmem_slot;
     // (a wait of this launch gives up two seconds from now at the earliest, after this store)
-    if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
+    if (p.first && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
 
     if (warp == 0 && lane == 0) {
         // ---- copies
@@ -499,7 +504,7 @@ TcPlan plan_tc(const Product &d) {
     return pair.units == 0 || (single.units != 0 && single.cost < pair.cost) ? single : pair;
 }
 
-cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool clear_status, void *part, cudaStream_t st) {
+cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool first, void *part, cudaStream_t st) {
     const TcPlan pl = plan_tc(d);
     if (pl.units == 0) return cudaErrorInvalidValue;
     TcParams p = {};
@@ -525,7 +530,7 @@ cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool clear_
         p.part_step = pl.part_step;
     }
     p.status = status;
-    p.clear_status = clear_status;
+    p.first = first;
     return pl.cg == 2 ? launch_tile<2, 256>(p, pl, d, st) : launch_tile<1, 128>(p, pl, d, st);
 }
 

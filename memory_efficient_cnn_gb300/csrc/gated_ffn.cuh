@@ -88,7 +88,7 @@ struct Product {
 
 // Tensor cores: fp16/bf16; operands 16-byte aligned with pitches that are multiples
 // of 8 elements. A product takes part_bytes of scratch. status: the workspace's
-// status block, cleared first where asked.
+// status block; first: the call's first product, which clears it.
 struct TcPlan {
     int cg = 0, bn = 0;       // CTAs and columns of a tile
     bool streamed = false;    // K blocks dealt out evenly, partial tiles joined
@@ -98,12 +98,12 @@ struct TcPlan {
     double cost = 0;          // estimated clocks
 };
 TcPlan plan_tc(const Product &p);
-cudaError_t launch_tc(const Product &p, bool bf16, uint32_t *status, bool clear_status, void *part, cudaStream_t st);
+cudaError_t launch_tc(const Product &p, bool bf16, uint32_t *status, bool first, void *part, cudaStream_t st);
 
 // The same for fp32, whose operands are three bf16 planes each (h + m + l, see
 // split_f32): GATED and DGATED write such planes, STORE writes fp32.
 TcPlan plan_f32(const Product &p);
-cudaError_t launch_f32(const Product &p, uint32_t *status, bool clear_status, void *part, cudaStream_t st);
+cudaError_t launch_f32(const Product &p, uint32_t *status, bool first, void *part, cudaStream_t st);
 
 // The forward pass of few rows (where is_few), from dense matrices of any
 // alignment that their type allows; h and its remainder h_lo (16-bit types) have
