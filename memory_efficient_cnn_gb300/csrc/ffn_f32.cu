@@ -385,8 +385,8 @@ cudaError_t launch_kind(const F32Params &p, const TcPlan &pl, cudaStream_t st) {
 
 }  // namespace
 
-// Clocks of a K block: 24 MMAs of 64, and the smaller tiles' shared-memory reads.
-TcPlan plan_f32(const Product &d) { return plan_tiles(d, 1, BN, 1800); }
+// A K block is 24 MMAs of 64 clocks.
+TcPlan plan_f32(const Product &d) { return plan_tiles(d, 1, BN, 0.95, d.epi == EPI_STORE ? 1 : 3); }
 
 cudaError_t launch_f32(const Product &d, uint32_t *status, bool first, void *part, cudaStream_t st) {
     const TcPlan pl = plan_f32(d);

@@ -498,9 +498,10 @@ cudaError_t launch_tile(const TcParams &p, const TcPlan &pl, const Product &d, c
 }  // namespace
 
 TcPlan plan_tc(const Product &d) {
-    // clocks: a K block takes 512 in either shape (the pair's MMAs; the single CTA's
-    // shared-memory fill)
-    const TcPlan pair = plan_tiles(d, 2, 256, 512), single = plan_tiles(d, 1, 128, 512);
+    // A K block takes the same time in either shape (the pair's MMAs, four times as many; the
+    // single CTA's shared-memory fill), outputs a little over half of it on the smaller tile.
+    const double epi = d.epi == EPI_DGATED ? 4 : d.epi == EPI_GATED ? (d.kept ? 3 : 2.1) : 1.8;
+    const TcPlan pair = plan_tiles(d, 2, 256, 0.345, epi), single = plan_tiles(d, 1, 128, 0.335, 0.55 * epi + 0.1);
     return pair.units == 0 || (single.units != 0 && single.cost < pair.cost) ? single : pair;
 }
 

@@ -126,11 +126,14 @@ struct Work {
 // The K blocks of a streamed launch are dealt to `units` CTA groups: unit i takes
 // blocks [i * total / units, (i + 1) * total / units).
 __host__ __device__ inline int64_t stream_begin(int64_t total, int units, int i) { return total * i / units; }
-// The unit that holds block b.
+// The unit that holds block b: an estimate in fp32, off by one at most, and no
+// 64-bit division (a joining thread spent microseconds on them). Unit i begins at
+// or before b where total * i < (b + 1) * units.
 __host__ __device__ inline int stream_unit(int64_t total, int units, int64_t b) {
-    int i = (int)(b * units / total);
-    while (i + 1 < units && stream_begin(total, units, i + 1) <= b) ++i;
-    while (i > 0 && stream_begin(total, units, i) > b) --i;
+    int i = (int)((float)b * ((float)units / (float)total));
+    if (i > units - 1) i = units - 1;
+    while (i + 1 < units && total * (i + 1) < (b + 1) * units) ++i;
+    while (i > 0 && total * i >= (b + 1) * units) --i;
     return i;
 }
 
@@ -248,12 +251,12 @@ inline int join_blocks(const P &p) {
 template <int COLS, int BN, typename P>
 __device__ __forceinline__ bool join_source(const P &p, int tile_m, int units, int &z, int &m, int &n, int &count,
                                             const float *&src) {
-    const int octets = (p.N + 7) / 8;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= (int64_t)p.batch * p.M * octets) return false;
-    n = (int)(id % octets) * 8;
-    const int64_t zm = id / octets;
-    z = (int)(zm / p.M), m = (int)(zm - (int64_t)z * p.M);
+    // (few tiles: everything here fits 32 bits)
+    const uint32_t octets = (uint32_t)(p.N + 7) / 8, id = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t zm = id / octets;
+    z = zm >= (uint32_t)p.M ? 1 : 0;
+    if (zm >= (uint32_t)p.batch * (uint32_t)p.M) return false;
+    n = (int)(id - zm * octets) * 8, m = (int)zm - z * p.M;
     const int tm = m / tile_m, tn = n / COLS;
     // the tile's index in the order of Walk, and the units that hold its first and last block
     const int band = tm / 8, rows = min(8, p.tiles_m - band * 8);
@@ -261,7 +264,7 @@ __device__ __forceinline__ bool join_source(const P &p, int tile_m, int units, i
     const int KT = p.KB * p.segs;
     const int64_t total = (int64_t)p.tiles * KT;
     count = stream_unit(total, units, (int64_t)(t + 1) * KT - 1) - stream_unit(total, units, (int64_t)t * KT) + 1;
-    src = p.part + zm * p.part_ld + (int64_t)tn * BN + (n - tn * COLS);
+    src = p.part + (int64_t)zm * p.part_ld + (int64_t)tn * BN + (n - tn * COLS);
     return true;
 }
 // Their sums in the order of K (TWO: of g and u).
@@ -284,8 +287,12 @@ __device__ __forceinline__ void add_partials(const float *src, int64_t step, int
 }
 
 // The plan of a product on tiles of 128 * cg rows and bn columns: plain or streamed,
-// whichever the estimate below has faster. kb_clocks: a K block of one tile.
-inline TcPlan plan_tiles(const Product &d, int cg, int bn, double kb_clocks) {
+// whichever the estimate has faster. In microseconds, as measured over rows of 33
+// to 12544 and blocks of 256 x 640 to 4096 x 10240: a launch takes 4 besides its
+// work; a K block of one tile kb; a tile's outputs epi, which hides behind the next
+// tile's K blocks; partial tiles are written and read at 6 TB/s and joined by a
+// second launch of 4.
+inline TcPlan plan_tiles(const Product &d, int cg, int bn, double kb, double epi) {
     const int KT = (d.K + BK - 1) / BK * (d.epi != EPI_GATED && d.a1.p && !d.batch ? 2 : 1);
     const int z = d.batch ? 2 : 1, tm = ROWS * cg, cols = d.epi == EPI_GATED ? bn / 2 : bn, most = SMS / cg;
     TcPlan pl;
@@ -294,10 +301,9 @@ inline TcPlan plan_tiles(const Product &d, int cg, int bn, double kb_clocks) {
     pl.tiles_n = (d.N + cols - 1) / cols;
     const int64_t tiles = (int64_t)z * pl.tiles_m * pl.tiles_n, total = tiles * KT;
     if (tiles > 0x3fffffff || total > 0x3fffffffll) return pl;  // (streamed indexes stay in 32 bits)
-    // clocks besides: a tile's start and end about 1500, a second launch 4000; partial sums are
-    // written and read at about 3000 bytes a clock
     pl.units = (int)std::min<int64_t>(most, tiles);
-    pl.cost = (double)((tiles + pl.units - 1) / pl.units) * KT * kb_clocks + 1500;
+    const int64_t waves = (tiles + pl.units - 1) / pl.units;
+    pl.cost = 4 + KT * kb + epi + (double)(waves - 1) * std::max(KT * kb, epi);
     TcPlan st = pl;
     st.streamed = true;
     st.units = (int)std::min<int64_t>(most, std::max<int64_t>(1, total / 4));  // 4 blocks at least
@@ -308,7 +314,7 @@ inline TcPlan plan_tiles(const Product &d, int cg, int bn, double kb_clocks) {
     st.part_step = (int64_t)z * d.M * st.part_ld;
     st.part_bytes = (size_t)(st.slots * st.part_step) * 4;
     const double moved = (double)(tiles + st.units) * std::min(tm, d.M) * bn * 8;
-    st.cost = (double)((total + st.units - 1) / st.units) * kb_clocks + 3000 + 4000 + moved / 3000;
+    st.cost = 4 + (double)((total + st.units - 1) / st.units) * kb + bn / 128.0 + 4 + moved / 6e6;
     return st.cost < pl.cost ? st : pl;
 }
 

@@ -131,7 +131,7 @@ struct ForwardParts {
         wd = p.add(q.copies(q.F) ? q.rows_f(q.C) : 0);
         part = p.end;
         if (q.R > 0)
-            p.add(std::max(q.plan(q.gated(kSome, kSome, kSome, kSomeOut, nullptr)).part_bytes,
+            p.add(std::max(q.plan(q.gated(kSome, kSome, kSome, kSomeOut, saved ? kSomeOut : nullptr)).part_bytes,
                            q.plan(q.down(kSome, kSome, kSomeOut)).part_bytes));
         bytes = p.end;
     }

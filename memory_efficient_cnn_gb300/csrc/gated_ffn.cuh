@@ -95,7 +95,7 @@ struct TcPlan {
     int tiles_m = 0, tiles_n = 0, units = 0, slots = 0;
     int64_t part_ld = 0, part_step = 0;
     size_t part_bytes = 0;
-    double cost = 0;          // estimated clocks
+    double cost = 0;          // estimated microseconds
 };
 TcPlan plan_tc(const Product &p);
 cudaError_t launch_tc(const Product &p, bool bf16, uint32_t *status, bool first, void *part, cudaStream_t st);
