@@ -11,7 +11,12 @@
 // remainder of that, two 16-bit numbers, at the cost of a second MMA a step: it
 // keeps 16 bits of bf16's 8 and 22 of fp16's 11.
 //
-// fp32: the same split on the CUDA cores, 4 weight rows a warp.
+// fp32: the same split on the CUDA cores, 4 weight rows a block.
+//
+// Measured with blocks of weights of 4096 x 10240, 252 MB in bf16: 43 us for one row
+// and 47 us for five, 5.9 and 5.4 TB/s; 58 us for sixteen. fp32, 4096 x 8192, 403 MB:
+// 60 us for one row (6.7 TB/s: memory), 69 us for four, 102 us for eight, whose loads
+// of x count for more than the weights'.
 #include <algorithm>
 
 #include "gated_ffn.cuh"
@@ -128,21 +133,21 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1) few_mma(const __grid
     auto row = [&](int n, int i, int h) {
         return static_cast<const uint16_t *>(i ? p.w1 : p.w0) + (int64_t)min(n * 16 + lane / 4 + h * 8, p.N - 1) * p.K;
     };
-    tc::grid_dependency_wait();
-    tc::allow_dependents();
-    if (p.status && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
-
     int next_tile = blockIdx.x, next_k = 0;  // of the copies
-    auto start = [&](int ahead) {
+    auto copy_weights = [&](int ahead, int tile, int k) {
+        const bool in = k < p.K;
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ring.copy(ahead, i * 2 + h, row(tile, i, h) + (in ? k : 0), in);
+    };
+    auto start = [&](int ahead, bool weights) {
         if (!AHEAD) return;
         if (next_tile < tiles) {
             const int k = next_k + k_lane;
             const bool in = k < p.K;
             const int64_t at = in ? k : 0;
-#pragma unroll
-            for (int i = 0; i < NW; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) ring.copy(ahead, i * 2 + h, row(next_tile, i, h) + at, in);
+            if (weights) copy_weights(ahead, next_tile, k);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 // (a row that is not there is not read: one line asked for by every warp costs L2 more
@@ -156,15 +161,29 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1) few_mma(const __grid
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // The second launch begins while the first runs, which has waited for all before it and
+    // writes h alone: the first weights need not wait for it.
+    if (AHEAD && !GATED) {
+        int tile = blockIdx.x, k = 0;
 #pragma unroll
-    for (int s = 0; s < Stages::DEPTH - 1; ++s) start(s);
+        for (int s = 0; s < Stages::DEPTH - 1; ++s) {
+            if (tile < tiles) copy_weights(s, tile, k + k_lane);
+            k += STEP;
+            if (k >= p.K) k = 0, tile += gridDim.x;
+        }
+    }
+    tc::grid_dependency_wait();
+    tc::allow_dependents();
+    if (p.status && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
+#pragma unroll
+    for (int s = 0; s < Stages::DEPTH - 1; ++s) start(s, GATED);
 
 #pragma unroll 1
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         float acc[NW][NT][4] = {};
 #pragma unroll 1
         for (int k0 = 0; k0 < p.K; k0 += STEP) {
-            start(Stages::DEPTH - 1);
+            start(Stages::DEPTH - 1, true);
             if (AHEAD) asm volatile("cp.async.wait_group %0;" ::"n"(Stages::DEPTH - 1) : "memory");
             const int k = k0 + k_lane;
             uint4 a[NW][2];
@@ -239,18 +258,42 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1) few_mma(const __grid
     }
 }
 
-// fp32: NR rows of b, 4 weight rows a block, vectors of V elements.
+// Sums of N values over a warp's lanes. While there are two or more, a lane hands
+// half of them to its partner and goes on with the other half; it ends with those
+// from the returned index on (butterflies of all N: 150 us instead of 132 us for
+// eight rows of 4096 x 8192).
+template <int N, int O, int SIZE>
+__device__ __forceinline__ int fold_lanes(float (&v)[SIZE], int lane) {
+    if constexpr (O == 0) {
+        return 0;
+    } else if constexpr (N == 1) {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], O);
+        return fold_lanes<1, O / 2>(v, lane);
+    } else {
+        const bool upper = (lane & O) != 0;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float keep = upper ? v[i + N / 2] : v[i], give = upper ? v[i] : v[i + N / 2];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, O);
+        }
+        return (upper ? N / 2 : 0) + fold_lanes<N / 2, O / 2>(v, lane);
+    }
+}
+
+// fp32: NR rows of b, 4 weight rows a block, vectors of V elements. From four rows
+// on two blocks an SM, of one step at a time (one block of two steps: 132 us instead
+// of 102 us for eight rows of 4096 x 8192); below, registers for two steps in flight.
 template <int NR, int V, bool GATED>
-__global__ void __launch_bounds__(THREADS) few_fma(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(THREADS, NR >= 4 ? 2 : 1) few_fma(const __grid_constant__ FewParams p) {
     constexpr int NW = GATED ? 2 : 1, ROWS = 4, SUMS = NW * ROWS * NR;
     __shared__ float red[WARPS][SUMS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n0 = blockIdx.x * ROWS;
     using P = Vec<float, V>;
-    float acc[NW][ROWS][NR] = {};
+    float acc[SUMS] = {};  // [NW][NR][ROWS]
     tc::grid_dependency_wait();
     tc::allow_dependents();
     if (p.status && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
-#pragma unroll 2
+#pragma unroll (NR * NW <= 4 ? 2 : 1)
     for (int k = (warp * 32 + lane) * V; k < p.K; k += THREADS * V) {
         P w[NW][ROWS];
 #pragma unroll
@@ -267,20 +310,17 @@ __global__ void __launch_bounds__(THREADS) few_fma(const __grid_constant__ FewPa
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) acc[i][r][m] = fmaf(w[i][r].v[e], x.v[e], acc[i][r][m]);
+                    for (int e = 0; e < V; ++e) {
+                        float &sum = acc[(i * NR + m) * ROWS + r];
+                        sum = fmaf(w[i][r].v[e], x.v[e], sum);
+                    }
         }
     }
+    const int first = fold_lanes<SUMS, 16>(acc, lane);
+    if (SUMS >= 32 || lane % (32 / SUMS) == 0) {
 #pragma unroll
-    for (int i = 0; i < NW; ++i)
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-            for (int m = 0; m < NR; ++m) {
-                float v = acc[i][r][m];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == 0) red[warp][(i * NR + m) * ROWS + r] = v;
-            }
+        for (int i = 0; i < (SUMS + 31) / 32; ++i) red[warp][first + i] = acc[i];
+    }
     __syncthreads();
     if (threadIdx.x >= NR * ROWS) return;
     const int m = threadIdx.x / ROWS, n = n0 + threadIdx.x % ROWS;
@@ -373,10 +413,12 @@ cudaError_t launch_any(const FewParams &p, int dtype, cudaStream_t st) {
 
 }  // namespace
 
-// Where these kernels are the faster ones. Up to 16 rows always. Up to 32 rows of
-// 16-bit types for small weights, where their two launches count for more than the
-// second reading of b: 15 us against 25 us of the tensor-memory products at 32
-// rows of 1024 x 4096, 101 us against 64 us at 4096 x 10240.
+// Where these kernels are the faster ones. 16-bit types: up to 16 rows (1024 x 4096:
+// 13 us against 19 us of the tensor-memory products; 4096 x 10240: 58 us against 57
+// us); up to 32 rows for small weights, where the products' partial sums count for
+// more than the second reading of b here (32 rows of 512 x 1536: 8 us against 14 us;
+// 2048 x 4096: 26 us against 28 us; 2048 x 8192: 46 us against 31 us). fp32: up to 8
+// rows (2048 x 4096: 35 us against 90 us).
 bool is_few(int64_t R, int64_t C, int64_t F, int dtype) {
     if (dtype == IM2WIN_F32) return R <= 8;
     return R <= 16 || (R <= 32 && C * F <= (int64_t(8) << 20));

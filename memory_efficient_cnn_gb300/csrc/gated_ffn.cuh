@@ -14,9 +14,6 @@ namespace ffn {
 //             dx = dg w_gate + du w_up      (M = R, N = C, K = F, twice)
 //             dw_gate = dg^T x, dw_up = du^T x   (M = F, N = C, K = R)
 //             dw_down = dy^T h                   (M = C, N = F, K = R)
-struct Dims {
-    int R, C, F;
-};
 
 // One operand: element (i, k) (i an output row or column, k the summed index) is
 // p[i * ld + k] (k_major) or p[k * ld + i].
