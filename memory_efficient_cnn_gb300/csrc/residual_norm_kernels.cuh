@@ -501,8 +501,10 @@ __device__ __forceinline__ void norm_values(int kind, F2 (&v)[R::PAIRS], int C, 
 }
 
 // One row a TPR threads; a block takes a run of rows, its row slots in turn.
-// Bound by memory (two rows read, two written): the parameters stay in shared
-// memory as they are stored, the next rows are on their way while one is worked on.
+// Two rows read, two written: the parameters stay in shared memory as they are
+// stored, the next rows are on their way while one is worked on. 8192 rows of 4096
+// bf16: 54 us, 5.0 TB/s; 200704 rows of 128 fp16 with two LAYER norms: 46 us, 4.5
+// TB/s, half of the issue slots taken (36 instructions a value).
 template <typename T, int V, int EPT, int TPR, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2)
     norm_forward_rows(const __grid_constant__ NormArgs p, const __grid_constant__ FastDiv per_gate) {
@@ -604,6 +606,9 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2)
 //                groups) for dgate, and weighed with the gate into its sums;
 //  short groups  a row slot takes whole groups, writes their dgate and adds the
 //                weighed A and B to its sums in shared memory.
+// Four rows read, two written. 8192 rows of 4096 bf16, RMS: 118 us; 200704 rows of 128
+// fp16, LAYER: 86 us; instructions bound both (70 a value, half of the issue slots). One
+// block an SM: five sums and a row's values take 123 registers of 128.
 template <typename R>
 constexpr int BACK_DEPTH = sizeof(typename R::Packed) <= 16 ? 3 : sizeof(typename R::Packed) <= 32 ? 2 : 1;
 template <typename R, int THREADS>
