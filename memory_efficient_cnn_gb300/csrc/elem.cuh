@@ -147,32 +147,36 @@ __device__ __forceinline__ F2 recip2(F2 a) {
     });
 }
 
-// The factor of g in act(g) (act(g) itself for sigmoid, the step for relu); e is
-// exp(-g^2 / 2) for gelu.
 // gelu's normal distribution: erfc(z) = t P(t) exp(-z^2), t = 1 / (1 + 0.38 z), the
 // form of Hastings' rational approximations (Abramowitz and Stegun, 7.1.23 to
 // 7.1.28), with a P of degree 6 fitted here by minimax least squares over
 // 0 <= z <= 12: relative error at most 1.04e-6, also in the tail. The
-// coefficients below are halved.
+// coefficients below are halved and negative. This is minus its part beyond size =
+// |g| standard deviations; e is exp(-g^2 / 2).
+__device__ __forceinline__ F2 minus_normal_tail2(F2 g, F2 size, F2 &e) {
+    e = exp2_2(mul2(mul2(g, f2(-0.72134752044448170f)), g));  // -log2(e) / 2
+    const F2 t = recip2(fma2(size, f2(0.38f * 0.70710678118654752f), f2(1.0f)));
+    F2 q = f2(0.062708848354241800f);
+    q = fma2(q, t, f2(-0.16801843157332533f));
+    q = fma2(q, t, f2(0.034957064694897890f));
+    q = fma2(q, t, f2(-0.12391755923373703f));
+    q = fma2(q, t, f2(-0.09029702208545247f));
+    q = fma2(q, t, f2(-0.10828872910161622f));
+    q = fma2(q, t, f2(-0.10714365505117787f));
+    return mul2(mul2(q, t), e);
+}
+
+// The factor of g in act(g) (act(g) itself for sigmoid, the step for relu); e is
+// exp(-g^2 / 2) for gelu.
 template <int ACT>
 __device__ __forceinline__ F2 act_factor2(F2 g, F2 &e) {
     if (ACT == IM2WIN_ACT_GELU) {
-        e = exp2_2(mul2(mul2(g, f2(-0.72134752044448170f)), g));  // -log2(e) / 2
-        const F2 size = each2(g, [](float v) { return fabsf(v); });
-        const F2 t = recip2(fma2(size, f2(0.38f * 0.70710678118654752f), f2(1.0f)));
-        F2 q = f2(-0.062708848354241800f);
-        q = fma2(q, t, f2(0.16801843157332533f));
-        q = fma2(q, t, f2(-0.034957064694897890f));
-        q = fma2(q, t, f2(0.12391755923373703f));
-        q = fma2(q, t, f2(0.09029702208545247f));
-        q = fma2(q, t, f2(0.10828872910161622f));
-        q = fma2(q, t, f2(0.10714365505117787f));
-        const F2 tail = mul2(mul2(q, t), e);  // beyond |g|
+        const F2 tail = minus_normal_tail2(g, each2(g, [](float v) { return fabsf(v); }), e);
         float g0, g1, t0, t1, c0, c1;
         split(g, g0, g1);
         split(tail, t0, t1);
-        split(fma2(tail, f2(-1.0f), f2(1.0f)), c0, c1);
-        return f2(g0 < 0.0f ? t0 : c0, g1 < 0.0f ? t1 : c1);
+        split(add2(tail, f2(1.0f)), c0, c1);
+        return f2(g0 < 0.0f ? -t0 : c0, g1 < 0.0f ? -t1 : c1);
     }
     if (ACT == IM2WIN_ACT_RELU) return each2(g, [](float v) { return v > 0.0f ? 1.0f : 0.0f; });
     F2 arg;
@@ -187,6 +191,11 @@ template <int ACT>
 __device__ __forceinline__ F2 act_value2(F2 g) {
     if (ACT == IM2WIN_ACT_RELU) return each2(g, [](float v) { return v < 0.0f ? 0.0f : v; });
     F2 e;
+    if (ACT == IM2WIN_ACT_GELU) {  // max(g, 0) - |g| tail, which needs no selection (bounded: 0 times it stays 0)
+        const F2 size = each2(g, [](float v) { return fminf(fabsf(v), 1e30f); });
+        const F2 tail = minus_normal_tail2(g, size, e);
+        return fma2(size, tail, each2(g, [](float v) { return fmaxf(v, 0.0f); }));
+    }
     const F2 p = act_factor2<ACT>(g, e);
     return ACT == IM2WIN_ACT_SIGMOID ? p : mul2(g, p);
 }
