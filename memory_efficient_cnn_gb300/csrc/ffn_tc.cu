@@ -28,8 +28,6 @@ namespace im2win {
 namespace ffn {
 namespace {
 
-constexpr int STAGED_WORDS = 32 * (PAIRS + 1);  // a warp's chunk of outputs
-
 template <int CG, int BN>
 struct Tile {
     static constexpr int M = ROWS * CG;
@@ -61,56 +59,6 @@ struct TcParams {
     int first;                 // the call's first launch: clears the status
     uint32_t *status;
 };
-
-// A chunk of outputs of one row from fp32, rounded and packed.
-__device__ __forceinline__ void pack_row(const F2 (&v)[PAIRS], uint32_t (&w)[PAIRS], int bf16) {
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-        float lo, hi;
-        split(v[i], lo, hi);
-        w[i] = pack2(lo, hi, bf16);
-    }
-}
-// Into a row of whole 16-byte vectors, `n` columns from here on (a multiple of 8).
-__device__ __forceinline__ void store_row(uint16_t *dst, const F2 (&v)[PAIRS], int n, int vec, int bf16) {
-    uint32_t w[PAIRS];
-    pack_row(v, w, bf16);
-    if (vec == 32 && n >= CHUNK) {  // a whole sector in one store
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (n >= CHUNK) reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-}
-// A warp's chunk of 32 rows into rows of any pitch, through its part of shared memory, so
-// that neighbouring lanes store neighbouring columns (a lane's own row in 2-byte stores took
-// 78 us for 2 x 3326 x 914 outputs). rows, n: valid rows and columns.
-__device__ __forceinline__ void store_rows_staged(uint16_t *dst, int64_t ldo, const F2 (&v)[PAIRS], int rows, int n, int bf16,
-                                                  uint32_t *stage) {
-    const int lane = threadIdx.x & 31;
-    uint32_t w[PAIRS];
-    pack_row(v, w, bf16);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) stage[lane * (PAIRS + 1) + i] = w[i];
-    __syncwarp();
-    if (ldo % 2 == 0) {  // 4-byte stores (rows and the first column are even)
-#pragma unroll
-        for (int it = 0; it < PAIRS; ++it) {
-            const int row = it * 4 + lane / PAIRS, c = lane % PAIRS * 2;
-            if (row < rows && c < n) *reinterpret_cast<uint32_t *>(dst + row * ldo + c) = stage[row * (PAIRS + 1) + c / 2];
-        }
-    } else {
-        const uint16_t *half = reinterpret_cast<const uint16_t *>(stage);
-#pragma unroll
-        for (int it = 0; it < CHUNK; ++it) {
-            const int row = it * 2 + lane / CHUNK, c = lane % CHUNK;
-            if (row < rows && c < n) dst[row * ldo + c] = half[row * 2 * (PAIRS + 1) + c];
-        }
-    }
-}
 
 // Eight kept values: their upper halves and the bytes after them.
 __device__ __forceinline__ void keep8(const F2 *v, uint4 &hi, uint2 &lo) {
@@ -145,25 +93,6 @@ __device__ __forceinline__ void keep_columns(unsigned char *at, const F2 *a, con
     *reinterpret_cast<uint4 *>(at) = ha;
     *reinterpret_cast<uint4 *>(at + 512) = hb;
     *reinterpret_cast<uint4 *>(at + 1024) = make_uint4(la.x, la.y, lb.x, lb.y);
-}
-
-// g, u -> h = act(g) * u in g; N pairs. KEEP: act(g) and u act'(g) too, in a and u.
-// The activation is chosen once for all values.
-template <int N, bool KEEP>
-__device__ __forceinline__ void gate_values(int act, F2 (&g)[N], F2 (&u)[N], F2 (&a)[N]) {
-    with_act_device(act, [&](auto kind) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (KEEP) {
-                F2 d;
-                act_both2<decltype(kind)::value>(g[i], a[i], d);
-                g[i] = mul2(a[i], u[i]);
-                u[i] = mul2(u[i], d);
-            } else {
-                g[i] = mul2(act_value2<decltype(kind)::value>(g[i]), u[i]);
-            }
-        }
-    });
 }
 
 // The kept values of a chunk of row m: three vectors of each 8 columns.

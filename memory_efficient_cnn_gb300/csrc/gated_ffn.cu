@@ -97,6 +97,8 @@ struct Problem {
         p.out = out; p.ldo = F;
         return p;
     }
+    // the forward pass that keeps nothing runs as one kernel
+    bool fused() const;
     TcPlan plan(const Product &p) const { return f32 ? plan_f32(p) : plan_tc(p); }
 };
 
@@ -114,23 +116,30 @@ struct SavedParts {
 const void *const kSome = reinterpret_cast<const void *>(16);  // a present operand, where only sizes matter
 void *const kSomeOut = reinterpret_cast<void *>(16);
 
+bool Problem::fused() const {
+    const double cost = f32 ? 0 : fused_cost(R, C, F);
+    return cost > 0 && cost < plan(gated(kSome, kSome, kSome, kSomeOut, nullptr)).cost + plan(down(kSome, kSome, kSomeOut)).cost;
+}
+
 struct ForwardParts {
+    bool one;  // the one kernel
     size_t h, h_lo, x, wg, wu, wd, part, bytes;
     ForwardParts(const Problem &q, bool saved) {
         Parts p(kStatusBytes);
+        one = !saved && !q.few() && q.R > 0 && q.fused();
         if (q.few()) {  // fp32: h as it is; else its rounding (in `saved` if there is one) and the remainder
             h = p.add(q.f32 ? (size_t)q.R * q.F * 4 : saved ? 0 : q.rows_f(q.R));
             h_lo = p.add(q.f32 ? 0 : q.rows_f(q.R));
             x = wg = wu = wd = part = bytes = p.end;
             return;
         }
-        h = h_lo = p.add(saved ? 0 : q.rows_f(q.R));
+        h = h_lo = p.add(saved || one ? 0 : q.rows_f(q.R));
         x = p.add(q.copies(q.C) ? q.rows_c(q.R) : 0);
         wg = p.add(q.copies(q.C) ? q.rows_c(q.F) : 0);
         wu = p.add(q.copies(q.C) ? q.rows_c(q.F) : 0);
         wd = p.add(q.copies(q.F) ? q.rows_f(q.C) : 0);
         part = p.end;
-        if (q.R > 0)
+        if (q.R > 0 && !one)
             p.add(std::max(q.plan(q.gated(kSome, kSome, kSome, kSomeOut, saved ? kSomeOut : nullptr)).part_bytes,
                            q.plan(q.down(kSome, kSome, kSomeOut)).part_bytes));
         bytes = p.end;
@@ -244,6 +253,12 @@ im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_
     w_up = seq.readable(w_up, q.F, q.C, parts.wu);
     w_down = seq.readable(w_down, q.C, q.F, parts.wd);
     seq.copy();
+    if (parts.one) {
+        const Fused f = {q.R, q.C, q.F, act, q.by_c(x, q.R, true), q.by_c(w_gate, q.F, true), q.by_c(w_up, q.F, true),
+                         q.by_f(w_down, q.C, true), y};
+        if (seq.e == cudaSuccess) seq.e = launch_fused(f, dtype == IM2WIN_BF16, static_cast<uint32_t *>(ws), st);
+        return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+    }
     seq.run(q.gated(x, w_gate, w_up, h, kept));
     seq.run(q.down(h, w_down, y));
     return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;

@@ -118,6 +118,16 @@ struct Few {
 bool is_few(int64_t R, int64_t C, int64_t F, int dtype);
 cudaError_t launch_few(const Few &f, int dtype, cudaStream_t st);
 
+// The forward pass of few channels (16-bit types) in one kernel, which keeps nothing:
+// an estimate of its time, comparable with TcPlan's, or zero where it does not apply.
+struct Fused {
+    int R, C, F, act;
+    Operand x, wg, wu, wd;  // pitches that are multiples of 8 elements
+    void *y;
+};
+double fused_cost(int64_t R, int64_t C, int64_t F);
+cudaError_t launch_fused(const Fused &f, bool bf16, uint32_t *status, cudaStream_t st);
+
 // Copies of dense matrices to a pitch that is a multiple of 8 elements: 16-bit types
 // as they are, fp32 in three bf16 planes.
 struct Repitch {
