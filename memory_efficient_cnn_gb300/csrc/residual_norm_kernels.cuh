@@ -373,19 +373,22 @@ struct Ahead {
     }
 };
 
-// Parameters of C elements in shared memory, as they are stored: a thread's part
-// of array i is one conflict-free access at a fixed address (the block's threads
-// fill it together; the caller's barrier follows). Types of 4 bytes, whose copies
+// Parameters of C elements in shared memory, those that are given one after the
+// other, as they are stored: a thread's part of one is a conflict-free access (the
+// block's threads fill them together; the caller's barrier follows). Types of 4 bytes, whose copies
 // would not fit beside the rows', read them through L1.
 template <typename R, int ARRAYS, int TPR>
 struct Params {
     static constexpr bool SHARED = sizeof(typename R::E) == 2;
-    static constexpr int BYTES = SHARED ? ARRAYS * TPR * (int)sizeof(typename R::Packed) : 0;
+    static constexpr int EACH = SHARED ? TPR * (int)sizeof(typename R::Packed) : 0, BYTES = ARRAYS * EACH;
     unsigned char *base;
     const void *const *from;
-    int C, t;
+    int C, t, place[ARRAYS];
     __device__ Params(void *smem, const void *const *from_, int C_, int t_)
         : base(static_cast<unsigned char *>(smem)), from(from_), C(C_), t(t_) {
+        int given = 0;
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i) place[i] = given, given += from[i] != nullptr;
         if (!SHARED || threadIdx.x >= TPR) return;
 #pragma unroll
         for (int i = 0; i < ARRAYS; ++i) {
@@ -397,7 +400,7 @@ struct Params {
         }
     }
     __device__ __forceinline__ typename R::P &at(int i, int j) {
-        return reinterpret_cast<typename R::P *>(base)[(i * R::VPT + j) * TPR + t];
+        return reinterpret_cast<typename R::P *>(base)[(place[i] * R::VPT + j) * TPR + t];
     }
     __device__ __forceinline__ void read(typename R::Packed &d, int i) {
         if (SHARED) {
@@ -506,7 +509,7 @@ __device__ __forceinline__ void norm_values(int kind, F2 (&v)[R::PAIRS], int C, 
 // bf16: 54 us, 5.0 TB/s; 200704 rows of 128 fp16 with two LAYER norms: 46 us, 4.5
 // TB/s, half of the issue slots taken (36 instructions a value).
 template <typename T, int V, int EPT, int TPR, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2)
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 3)
     norm_forward_rows(const __grid_constant__ NormArgs p, const __grid_constant__ FastDiv per_gate) {
     using R = Row<T, V, EPT, TPR>;
     constexpr int RPB = THREADS / TPR;
@@ -986,14 +989,19 @@ cudaError_t launch_rows(const NormArgs &p, cudaStream_t st) {
     constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR, EPT = 32 / (int)sizeof(T);
     using R = Row<T, V, EPT, TPR>;
     auto kernel = norm_forward_rows<T, V, EPT, TPR, THREADS>;
-    constexpr int smem = Ahead<R, 2, 3, THREADS>::BYTES + Params<R, PARAMS, TPR>::BYTES;
-    if (smem > 32 * 1024) {  // (48 KB with the static part need no leave)
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    using Pars = Params<R, PARAMS, TPR>;
+    constexpr int most = Ahead<R, 2, 3, THREADS>::BYTES + Pars::BYTES;
+    if (most > 32 * 1024) {  // (48 KB with the static part need no leave)
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
+    int smem = most - Pars::BYTES;
+    for (const void *given : {p.res_scale, p.w_post, p.b_post, p.w_pre, p.b_pre}) smem += given ? Pars::EACH : 0;
+    // three blocks an SM where their shared memory fits (226 KB with the static part)
+    const int per_sm = THREADS > 256 ? 1 : 3 * (smem + 2048) <= 226 * 1024 ? 3 : 2;
     const int64_t blocks = (p.R + RPB - 1) / RPB;
     const FastDiv per = make_fastdiv((uint32_t)std::min(p.per_gate, p.R));
-    kernel<<<(unsigned)std::min<int64_t>(blocks, SMS * (THREADS > 256 ? 1 : 2)), THREADS, smem, st>>>(p, per);
+    kernel<<<(unsigned)std::min<int64_t>(blocks, SMS * per_sm), THREADS, smem, st>>>(p, per);
     return cudaGetLastError();
 }
 
