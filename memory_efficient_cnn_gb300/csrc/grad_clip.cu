@@ -1,16 +1,22 @@
 // Global norm of a list of gradients and their clipping, in two launches for
 // each table of tensors: sums of squares, one partial for each block, and the
-// scaling, whose every block joins the partials in the same order.
+// scaling, whose every block joins the partials in the same order while its first
+// gradients are on their way.
 //
 // Bound by memory: two readings and one writing (lists that L2 holds: one of
-// each). 1.5 G values of 48 bf16 and fp32 tensors, 3 GB: 1425 us, 6.6 TB/s through
-// the three passes. 16-byte vectors, 8192 elements of one tensor a block at a time,
-// whose loads are all under way before the first is used. Squares and their sum in
-// a thread are fp32 (32 values), sums of threads and blocks fp64.
+// each). 1.5 G values of 48 bf16 and fp32 tensors, 3 GB: 1384 us, 6.5 TB/s through
+// the three passes; 3.2 M fp32 values of 53: 13 us. 16-byte vectors, 8192 elements of
+// one tensor a block at a time, whose loads are all under way before the first is
+// used; four blocks an SM, with registers for that (eight: 1425 us).
+//
+// Squares and their sum in a thread are fp32 (32 values), sums over chunks, threads
+// and blocks fp64, the last two by one warp of a block: the fp64 units are few (by every warp,
+// with the factor in fp64 too, the 3.2 M values took 25 us).
 #include <algorithm>
 #include <cmath>
 
 #include "elem.cuh"
+#include "tc_ptx.cuh"
 
 using namespace im2win;
 
@@ -18,7 +24,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int CHUNK = 8192;  // elements a block takes at a time, all of one tensor
-constexpr int PARTS = 1216;  // partial sums of a table (8 blocks on each of 152 SMs)
+constexpr int PARTS = 608;   // blocks and partial sums of a table at most (4 on each of 152 SMs)
 
 struct Entry {
     const void *in;
@@ -51,38 +57,43 @@ __device__ __forceinline__ int entry_of(const Table<CAP> &t, uint32_t chunk) {
 
 template <typename T>
 __device__ __forceinline__ float squares(const T *p, int n) {
+    using V = Vec16<T>;
     float a = 0.0f;
-    if (n == CHUNK && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-        using V = Vec16<T>;
+    int done = 0;
+    auto add = [&](const V &v) {
 #pragma unroll
-        for (int i = 0; i < CHUNK / (THREADS * V::N); ++i) {
-            const V v = reinterpret_cast<const V *>(p)[i * THREADS + threadIdx.x];
+        for (int j = 0; j < V::N; ++j) a = fmaf(to_f32(v.v[j]), to_f32(v.v[j]), a);
+    };
+    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        const V *from = reinterpret_cast<const V *>(p);
+        if (n == CHUNK) {  // (without conditions: with them this loop has two thirds of the rate)
+            V v[CHUNK / (THREADS * V::N)];
 #pragma unroll
-            for (int j = 0; j < V::N; ++j) a = fmaf(to_f32(v.v[j]), to_f32(v.v[j]), a);
+            for (int i = 0; i < CHUNK / (THREADS * V::N); ++i) v[i] = from[i * THREADS + threadIdx.x];
+#pragma unroll
+            for (int i = 0; i < CHUNK / (THREADS * V::N); ++i) add(v[i]);
+            return a;
         }
-    } else {
-        for (int i = threadIdx.x; i < n; i += THREADS) a = fmaf(to_f32(p[i]), to_f32(p[i]), a);
+        done = n / V::N * V::N;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n / V::N; i += THREADS) add(from[i]);
     }
+    for (int i = done + threadIdx.x; i < n; i += THREADS) a = fmaf(to_f32(p[i]), to_f32(p[i]), a);
     return a;
 }
 
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double s[THREADS / 32];
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double t = 0.0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) t += s[i];
-    __syncthreads();
-    return t;
+    return v;
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(THREADS) sum_squares(const __grid_constant__ Table<CAP> t, double *part) {
+__global__ void __launch_bounds__(THREADS, 4) sum_squares(const __grid_constant__ Table<CAP> t, double *part) {
+    tc::allow_dependents();
+    __shared__ double sums[THREADS];
     double a = 0.0;
-    for (uint32_t c = blockIdx.x; c < t.chunks; c += PARTS) {
+    for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const Entry &e = t.e[entry_of(t, c)];
         const int64_t at = (int64_t)(c - e.first) * CHUNK;
         const int n = (int)min((int64_t)CHUNK, e.size - at);
@@ -90,48 +101,102 @@ __global__ void __launch_bounds__(THREADS) sum_squares(const __grid_constant__ T
         else if (e.dtype == IM2WIN_F16) a += squares(static_cast<const f16_t *>(e.in) + at, n);
         else a += squares(static_cast<const bf16_t *>(e.in) + at, n);
     }
-    a = block_sum(a);
+    sums[threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+#pragma unroll
+    for (int i = 1; i < THREADS / 32; ++i) a += sums[i * 32 + threadIdx.x];
+    a = warp_sum(a);
     if (threadIdx.x == 0) part[blockIdx.x] = a;
 }
 
-template <typename T>
-__device__ __forceinline__ void scale(const T *in, T *out, int n, float f) {
-    if (n == CHUNK && ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
-        using V = Vec16<T>;
+// The norm and the factor of all gradients, from the partial sums of the launches before.
+struct Factor {
+    const double *part;
+    int64_t parts;
+    double max_norm, eps;
+    float *norm;
+    __device__ float get() const {
+        __shared__ float f;
+        tc::grid_dependency_wait();
+        if (threadIdx.x < 32) {
+            double a = 0.0;
+#pragma unroll 8
+            for (int64_t i = threadIdx.x; i < parts; i += 32) a += part[i];
+            a = warp_sum(a);
+            if (threadIdx.x == 0) {
+                float total = sqrtf((float)a);
+                if (!(a > 1e-30 && a < 1e38)) total = (float)sqrt(a);
+                if (norm && blockIdx.x == 0) *norm = total;
+                const float limit = (float)max_norm / (total + (float)eps);
+                f = limit >= 1.0f ? 1.0f : limit;  // NaN stays NaN
+            }
+        }
+        __syncthreads();
+        return f;
+    }
+};
+
+// FIRST: of a block's chunks, whose factor is asked for once its loads are under way.
+template <bool FIRST, typename T>
+__device__ __forceinline__ void scale(const T *in, T *out, int n, float &f, const Factor &factor) {
+    using V = Vec16<T>;
+    auto times = [&](V &v) {
+#pragma unroll
+        for (int j = 0; j < V::N; ++j) v.v[j] = from_f32<T>(to_f32(v.v[j]) * f);
+    };
+    const bool vectors = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    const V *from = reinterpret_cast<const V *>(in);
+    V *to = reinterpret_cast<V *>(out);
+    if (vectors && n == CHUNK) {
         V v[CHUNK / (THREADS * V::N)];
 #pragma unroll
-        for (int i = 0; i < CHUNK / (THREADS * V::N); ++i)
-            v[i] = reinterpret_cast<const V *>(in)[i * THREADS + threadIdx.x];
+        for (int i = 0; i < CHUNK / (THREADS * V::N); ++i) v[i] = from[i * THREADS + threadIdx.x];
+        if (FIRST) f = factor.get();
+        if (f == 1.0f && in == out) return;
 #pragma unroll
         for (int i = 0; i < CHUNK / (THREADS * V::N); ++i) {
-#pragma unroll
-            for (int j = 0; j < V::N; ++j) v[i].v[j] = from_f32<T>(to_f32(v[i].v[j]) * f);
-            reinterpret_cast<V *>(out)[i * THREADS + threadIdx.x] = v[i];
+            times(v[i]);
+            to[i * THREADS + threadIdx.x] = v[i];
         }
-    } else {
-        for (int i = threadIdx.x; i < n; i += THREADS) out[i] = from_f32<T>(to_f32(in[i]) * f);
+        return;
     }
+    if (FIRST) f = factor.get();
+    if (f == 1.0f && in == out) return;
+    const int done = vectors ? n / V::N * V::N : 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < done / V::N; i += THREADS) {
+        V v = from[i];
+        times(v);
+        to[i] = v;
+    }
+    for (int i = done + threadIdx.x; i < n; i += THREADS) out[i] = from_f32<T>(to_f32(in[i]) * f);
 }
 
-// `parts` partial sums of every table of the call.
+template <bool FIRST, int CAP>
+__device__ __forceinline__ void scale_chunk(const Table<CAP> &t, uint32_t c, float &f, const Factor &factor) {
+    const Entry &e = t.e[entry_of(t, c)];
+    if (!FIRST && f == 1.0f && e.out == e.in) return;
+    const int64_t at = (int64_t)(c - e.first) * CHUNK;
+    const int n = (int)min((int64_t)CHUNK, e.size - at);
+    if (e.dtype == IM2WIN_F32)
+        scale<FIRST>(static_cast<const float *>(e.in) + at, static_cast<float *>(e.out) + at, n, f, factor);
+    else if (e.dtype == IM2WIN_F16)
+        scale<FIRST>(static_cast<const f16_t *>(e.in) + at, static_cast<f16_t *>(e.out) + at, n, f, factor);
+    else
+        scale<FIRST>(static_cast<const bf16_t *>(e.in) + at, static_cast<bf16_t *>(e.out) + at, n, f, factor);
+}
+
 template <int CAP>
-__global__ void __launch_bounds__(THREADS)
-    clip(const __grid_constant__ Table<CAP> t, const double *part, int64_t parts, double max_norm, double eps, float *norm) {
-    double a = 0.0;
-    for (int64_t i = threadIdx.x; i < parts; i += THREADS) a += part[i];
-    const double total = sqrt(block_sum(a));
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
-    const double limit = max_norm / (total + eps);
-    const float f = limit >= 1.0 ? 1.0f : (float)limit;  // NaN stays NaN
-    for (uint32_t c = blockIdx.x; c < t.chunks; c += PARTS) {
-        const Entry &e = t.e[entry_of(t, c)];
-        if (e.out == nullptr || (f == 1.0f && e.out == e.in)) continue;
-        const int64_t at = (int64_t)(c - e.first) * CHUNK;
-        const int n = (int)min((int64_t)CHUNK, e.size - at);
-        if (e.dtype == IM2WIN_F32) scale(static_cast<const float *>(e.in) + at, static_cast<float *>(e.out) + at, n, f);
-        else if (e.dtype == IM2WIN_F16) scale(static_cast<const f16_t *>(e.in) + at, static_cast<f16_t *>(e.out) + at, n, f);
-        else scale(static_cast<const bf16_t *>(e.in) + at, static_cast<bf16_t *>(e.out) + at, n, f);
-    }
+__global__ void __launch_bounds__(THREADS, 4) clip(const __grid_constant__ Table<CAP> t, const Factor factor) {
+    float f = 1.0f;
+    uint32_t c = blockIdx.x;
+    if (c < t.chunks) scale_chunk<true>(t, c, f, factor);
+    else factor.get();
+    while ((c += gridDim.x) < t.chunks) scale_chunk<false>(t, c, f, factor);
+}
+__global__ void __launch_bounds__(THREADS) norm_alone(const Factor factor) {
+    factor.get();
 }
 
 int64_t tables(int64_t count) { return std::max<int64_t>(1, (count + LARGE - 1) / LARGE); }
@@ -156,21 +221,37 @@ bool fill(Table<CAP> &t, const void *const *grads, void *const *outs, const int6
     return true;
 }
 
+unsigned blocks_of(uint32_t chunks) { return std::max(1u, std::min<unsigned>(chunks, PARTS)); }
+
 template <int CAP>
 im2win_status run(const void *const *grads, void *const *outs, const int64_t *sizes, const int *dtypes, int64_t count,
                   double max_norm, double eps, float *norm, double *part, cudaStream_t st) {
     static thread_local Table<CAP> t;
     const int64_t n_tables = tables(count);
+    int64_t parts = 0;
     for (int64_t k = 0; k < n_tables; ++k) {
         if (!fill(t, grads, outs, sizes, dtypes, k * CAP, count)) return IM2WIN_ERR_UNSUPPORTED;
-        sum_squares<CAP><<<PARTS, THREADS, 0, st>>>(t, part + k * PARTS);
+        const unsigned blocks = blocks_of(t.chunks);
+        sum_squares<CAP><<<blocks, THREADS, 0, st>>>(t, part + parts);
         if (cudaGetLastError() != cudaSuccess) return IM2WIN_ERR_CUDA;
+        parts += blocks;
     }
+    // (the first of them begins while the last sums end; the others' inputs and outputs are other tensors)
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
     for (int64_t k = 0; k < n_tables; ++k) {
         if (n_tables > 1) fill(t, grads, outs, sizes, dtypes, k * CAP, count);
-        const unsigned grid = outs && t.chunks ? std::min<unsigned>(PARTS, t.chunks) : 1;
-        clip<CAP><<<grid, THREADS, 0, st>>>(t, part, n_tables * PARTS, max_norm, eps, k == 0 ? norm : nullptr);
-        if (cudaGetLastError() != cudaSuccess) return IM2WIN_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(outs ? blocks_of(t.chunks) : 1);
+        cfg.blockDim = dim3(THREADS);
+        cfg.stream = st;
+        cfg.attrs = &early;
+        cfg.numAttrs = 1;
+        const Factor factor = {part, parts, max_norm, eps, k == 0 ? norm : nullptr};
+        const cudaError_t e = !outs ? cudaLaunchKernelEx(&cfg, norm_alone, factor)
+                              : cudaLaunchKernelEx(&cfg, clip<CAP>, t, factor);
+        if (e != cudaSuccess) return IM2WIN_ERR_CUDA;
         if (!outs) break;
     }
     return IM2WIN_OK;
