@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
+from array import array
 
 import torch
 
@@ -329,45 +331,54 @@ def residual_norm_backward(dr, dn, x: torch.Tensor, y: torch.Tensor | None = Non
 
 
 # ---------------------------------------------------------------- gradient clipping
+# Lists go through map() and array: a list of hundreds costs more on the host than on the GPU.
+_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_pointer, _device_of, _contiguous = torch.Tensor.data_ptr, torch.Tensor.get_device, torch.Tensor.is_contiguous
+
+
+def _address(values):
+    return values.buffer_info()[0]
+
+
 def im2win_clip_grad_norm_size(sizes) -> int:
     out = ctypes.c_size_t(0)
-    arr = sizes if isinstance(sizes, ctypes.Array) else (ctypes.c_int64 * len(sizes))(*sizes)
-    _check("im2win_clip_grad_norm_size", lib().im2win_clip_grad_norm_size(arr, len(sizes), ctypes.byref(out)))
+    sizes = sizes if isinstance(sizes, array) else array("q", sizes)
+    _check("im2win_clip_grad_norm_size",
+           lib().im2win_clip_grad_norm_size(_address(sizes), len(sizes), ctypes.byref(out)))
     return out.value
 
 
 def _clip_check(fn, grads, outs, device: int):
     """The gradients' dtype codes after the checks of the lists."""
-    given = grads
+    given, dtypes = grads, list(map(_dtype_of, grads))
     if outs is not None and outs is not grads:
         if len(outs) != len(grads):
             raise ValueError(f"{fn}: {len(outs)} outputs for {len(grads)} gradients")
-        if [t.shape for t in outs] != [t.shape for t in grads] or [t.dtype for t in outs] != [t.dtype for t in grads]:
+        if list(map(_shape_of, outs)) != list(map(_shape_of, grads)) or list(map(_dtype_of, outs)) != dtypes:
             for i, (g, o) in enumerate(zip(grads, outs)):
                 _shape(fn, f"outs[{i}]", o, g.shape)
                 _same_dtype(fn, g, o)
         given = grads + outs
-    if device < 0 or not all([t.get_device() == device and t.is_contiguous() for t in given]):
+    if device < 0 or not all(map(_contiguous, given)) or any(map(device.__ne__, map(_device_of, given))):
         _cuda(*given)
         _same_device(fn, *given)
         raise ValueError(f"{fn}: every tensor must be on one device")
     try:
-        return (ctypes.c_int * len(grads))(*[_DTYPE[t.dtype] for t in grads])
+        return array("i", map(_DTYPE.__getitem__, dtypes))
     except KeyError:
         return [_dtype_code(t) for t in grads]  # raises
 
 
 def _counts(grads):
-    return (ctypes.c_int64 * len(grads))(*[t.numel() for t in grads])
+    return array("q", map(torch.Tensor.numel, grads))
 
 
 def _clip(fn, grads, outs, counts, codes, max_norm, eps, norm, ws):
-    k = len(grads)
-    pointers = ctypes.c_void_p * k
-    at = pointers(*[t.data_ptr() for t in grads])
-    to = None if outs is None else at if outs is grads else pointers(*[t.data_ptr() for t in outs])
-    _check(fn, lib().im2win_clip_grad_norm(at, to, counts, codes, k, max_norm, eps, norm.data_ptr(), ws.data_ptr(),
-                                           _bytes(ws), _stream(norm.get_device())))
+    at = array("Q", map(_pointer, grads))
+    to = None if outs is None else at if outs is grads else array("Q", map(_pointer, outs))
+    _check(fn, lib().im2win_clip_grad_norm(
+        _address(at), None if to is None else _address(to), _address(counts), _address(codes), len(grads), max_norm, eps,
+        norm.data_ptr(), ws.data_ptr(), _bytes(ws), _stream(norm.get_device())))
 
 
 def im2win_clip_grad_norm(grads, outs, max_norm: float, eps: float, norm, ws) -> None:
