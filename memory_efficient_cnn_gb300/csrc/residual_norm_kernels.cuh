@@ -505,9 +505,10 @@ __device__ __forceinline__ void norm_values(int kind, F2 (&v)[R::PAIRS], int C, 
 
 // One row a TPR threads; a block takes a run of rows, its row slots in turn.
 // Two rows read, two written: the parameters stay in shared memory as they are
-// stored, the next rows are on their way while one is worked on. 8192 rows of 4096
-// bf16: 54 us, 5.0 TB/s; 200704 rows of 128 fp16 with two LAYER norms: 46 us, 4.5
-// TB/s, half of the issue slots taken (36 instructions a value).
+// stored, the next rows are on their way while one is worked on. Three blocks an SM
+// where shared memory has room: 8192 rows of 4096 bf16 take 50 us, 5.4 TB/s (56 us in
+// two); 200704 rows of 128 fp16 with two LAYER norms 44 us, 4.6 TB/s, half of the issue
+// slots taken (36 instructions a value).
 template <typename T, int V, int EPT, int TPR, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 3)
     norm_forward_rows(const __grid_constant__ NormArgs p, const __grid_constant__ FastDiv per_gate) {
