@@ -351,8 +351,8 @@ im2win_status im2win_gated_ffn_size(int buffer, int64_t R, int64_t C, int64_t F,
  * Gated feed-forward block:
  *   g = x w_gate^T, u = x w_up^T, h = act(g) * u, y = h w_down^T,
  * x[R][C], w_gate[F][C], w_up[F][C], w_down[C][F], y[R][C]. The products run on
- * the tensor cores (fp32 as six bf16 products, as exact as an fp32 sum; few rows:
- * reading the weights once), with g and u in fp32. F16/BF16: h is rounded to the
+ * the tensor cores (fp32 as six bf16 products, as exact as an fp32 sum; few rows of
+ * fp32 on the CUDA cores), with g and u in fp32. F16/BF16: h is rounded to the
  * dtype between the two products (an |h| beyond the dtype's range becomes infinite
  * there). F32: a row with an infinity may give NaN where fp32 gives an infinity.
  * `saved` (NULL for inference) receives what im2win_gated_ffn_backward needs;

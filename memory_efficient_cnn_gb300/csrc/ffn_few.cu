@@ -11,7 +11,8 @@
 // remainder of that, two 16-bit numbers, at the cost of a second MMA a step: it
 // keeps 16 bits of bf16's 8 and 22 of fp16's 11.
 //
-// fp32: the same split on the CUDA cores, 4 weight rows a block.
+// fp32: the same split on the CUDA cores, 4 weight rows a block and up to 8 rows of x;
+// more rows take more blocks, which find the weights in L2.
 //
 // Measured with blocks of weights of 4096 x 10240, 252 MB in bf16: 43 us for one row
 // and 47 us for five, 5.9 and 5.4 TB/s; 58 us for sixteen. fp32, 4096 x 8192, 403 MB:
@@ -280,14 +281,16 @@ __device__ __forceinline__ int fold_lanes(float (&v)[SIZE], int lane) {
     }
 }
 
-// fp32: NR rows of b, 4 weight rows a block, vectors of V elements. From four rows
+// fp32: NR rows of b and 4 weight rows a block, vectors of V elements. From four rows
 // on two blocks an SM, of one step at a time (one block of two steps: 132 us instead
 // of 102 us for eight rows of 4096 x 8192); below, registers for two steps in flight.
 template <int NR, int V, bool GATED>
 __global__ void __launch_bounds__(THREADS, NR >= 4 ? 2 : 1) few_fma(const __grid_constant__ FewParams p) {
     constexpr int NW = GATED ? 2 : 1, ROWS = 4, SUMS = NW * ROWS * NR;
     __shared__ float red[WARPS][SUMS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n0 = blockIdx.x * ROWS;
+    // blocks of the same weights and other rows follow one another, so that L2 has the weights
+    const int groups = (p.R + NR - 1) / NR, m0 = blockIdx.x % groups * NR, n0 = blockIdx.x / groups * ROWS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     using P = Vec<float, V>;
     float acc[SUMS] = {};  // [NW][NR][ROWS]
     tc::grid_dependency_wait();
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(THREADS, NR >= 4 ? 2 : 1) few_fma(const __grid
                                                        (int64_t)min(n0 + r, p.N - 1) * p.K + k);
 #pragma unroll
         for (int m = 0; m < NR; ++m) {
-            const P x = *reinterpret_cast<const P *>(static_cast<const float *>(p.b) + (int64_t)min(m, p.R - 1) * p.ldb + k);
+            const P x = *reinterpret_cast<const P *>(static_cast<const float *>(p.b) + (int64_t)min(m0 + m, p.R - 1) * p.ldb + k);
 #pragma unroll
             for (int i = 0; i < NW; ++i)
 #pragma unroll
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, NR >= 4 ? 2 : 1) few_fma(const __grid
     }
     __syncthreads();
     if (threadIdx.x >= NR * ROWS) return;
-    const int m = threadIdx.x / ROWS, n = n0 + threadIdx.x % ROWS;
+    const int m = m0 + threadIdx.x / ROWS, n = n0 + threadIdx.x % ROWS;
     if (m >= p.R || n >= p.N) return;
     float v[NW] = {};
 #pragma unroll
@@ -393,7 +396,7 @@ cudaError_t launch_16(const FewParams &p, cudaStream_t st) {
 
 template <int NR, bool GATED>
 cudaError_t launch_fma(const FewParams &p, cudaStream_t st) {
-    const int blocks = (p.N + 3) / 4;
+    const int blocks = (p.N + 3) / 4 * ((p.R + NR - 1) / NR);
     return p.K % 4 == 0 ? launch(few_fma<NR, 4, GATED>, blocks, 0, st, p) : launch(few_fma<NR, 1, GATED>, blocks, 0, st, p);
 }
 
@@ -417,10 +420,12 @@ cudaError_t launch_any(const FewParams &p, int dtype, cudaStream_t st) {
 // 13 us against 19 us of the tensor-memory products; 4096 x 10240: 58 us against 57
 // us); up to 32 rows for small weights, where the products' partial sums count for
 // more than the second reading of b here (32 rows of 512 x 1536: 8 us against 14 us;
-// 2048 x 4096: 26 us against 28 us; 2048 x 8192: 46 us against 31 us). fp32: up to 8
-// rows (2048 x 4096: 35 us against 90 us).
+// 2048 x 4096: 26 us against 28 us; 2048 x 8192: 46 us against 31 us). fp32: up to 32
+// rows (2048 x 4096: 48 us against 90 us for 16 rows, 87 us against 92 us for 32), and
+// up to 128 where the work is small (64 rows of 256 x 640: 13 us against 25 us; of 384 x
+// 1001: 22 us against 29 us; of 1024 x 2816: 76 us against 43 us).
 bool is_few(int64_t R, int64_t C, int64_t F, int dtype) {
-    if (dtype == IM2WIN_F32) return R <= 8;
+    if (dtype == IM2WIN_F32) return R <= 32 || (R <= 128 && R * C * F <= (int64_t(1) << 24));
     return R <= 16 || (R <= 32 && C * F <= (int64_t(8) << 20));
 }
 

@@ -61,6 +61,13 @@ def test_large(dt, R, C, F):
     check(R, C, F, dt, "gelu", seed=7)
 
 
+@pytest.mark.parametrize("R,C,F", [(33, 520, 1000), (40, 1000, 700), (72, 1024, 520), (100, 600, 512), (32, 1100, 700),
+                                   (128, 360, 363)])
+def test_f32_rows_of_less_than_a_tile(R, C, F):
+    """Both sides of where the fp32 kernels of few rows end."""
+    check(R, C, F, "f32", "silu", seed=R)
+
+
 def test_leading_axes_and_out():
     x, wg, wu, wd, _ = (t.cuda() for t in make(2 * 3 * 5, 64, 128, "bf16"))
     want = mec.gated_ffn(x, wg, wu, wd)
