@@ -38,7 +38,7 @@ enum FusedSite : uint32_t {
 
 struct FusedParams {
     CUtensorMap x, w[2], wd;
-    int M, N, n_mma;     // rows, channels, channels rounded up to 16
+    int M, N, n_mma;     // rows, channels, columns of the product that makes them
     int KB, chunks, tiles;
     int bf16, act, vec;
     void *out;
@@ -288,7 +288,7 @@ double fused_cost(int64_t R, int64_t C, int64_t F) {
 
 cudaError_t launch_fused(const Fused &f, bool bf16, uint32_t *status, cudaStream_t st) {
     FusedParams p = {};
-    p.M = f.R; p.N = f.C; p.n_mma = (f.C + 15) / 16 * 16;
+    p.M = f.R; p.N = f.C; p.n_mma = fused_columns(f.C);
     p.KB = (f.C + BK - 1) / BK;
     p.chunks = (f.F + CHUNK_F - 1) / CHUNK_F;
     p.tiles = (f.R + TILE_M - 1) / TILE_M;

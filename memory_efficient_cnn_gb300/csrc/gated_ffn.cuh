@@ -126,6 +126,8 @@ struct Fused {
     void *y;
 };
 double fused_cost(int64_t R, int64_t C, int64_t F);
+// Columns of its second product: a pair's 256-row product takes multiples of 32.
+constexpr int fused_columns(int C) { return (C + 31) / 32 * 32; }
 cudaError_t launch_fused(const Fused &f, bool bf16, uint32_t *status, cudaStream_t st);
 
 // Copies of dense matrices to a pitch that is a multiple of 8 elements: 16-bit types
