@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
                 }
             }
         }
+        if (ok) ok = drain(empty, STAGES, s, phase, ctl, SITE_STAGE_EMPTY);
         if (!ok) let_end();
     } else if (warp == 1 && lane == 0) {
         // ---- MMAs

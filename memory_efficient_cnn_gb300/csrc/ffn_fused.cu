@@ -139,6 +139,18 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_fused(const __grid_constant__ 
             }
             if (++j == p.chunks) j = 0, ++tile;
         }
+        // every arrival that is on its way to this CTA: buffer s of two has had `uses` / 2 rounds (h_empty, on
+        // which this thread has not waited before, lags d_empty by less than a round: h was written after it)
+        auto drain2 = [&](uint32_t bar, int uses, uint32_t site) {
+            for (int s = 0; ok && s < 2; ++s) {
+                const int rounds = (uses + 1 - s) / 2;
+                if (rounds) ok = bar_wait(bar + 8 * s, (rounds - 1) & 1, ctl, site);
+            }
+        };
+        if (ok) ok = drain(g_empty, G_SLOTS, gs, g_phase, ctl, SITE_G_EMPTY);
+        drain2(x_empty, my_tiles, SITE_X_EMPTY);
+        drain2(d_empty, total, SITE_D_EMPTY);
+        drain2(h_empty, total, SITE_H_EMPTY);
         if (!ok) let_end();
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---- MMAs of g and u (a thread of their own: they must not wait for h of other chunks)
@@ -267,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_fused(const __grid_constant__ 
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_relaxed();
+    cluster_sync();  // (a release: the other CTA's arrivals here have been made)
     tc_fence_after();
     if (warp == 2) free_tmem<2>(tmem, TMEM_COLUMNS);
 }

@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                 if (++s == T::STAGES) s = 0, phase ^= 1;
             }
         }
+        if (ok) ok = drain(empty, T::STAGES, s, phase, ctl, SITE_STAGE_EMPTY);
         if (!ok) let_end();
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---- MMAs
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
     }
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_relaxed();
+    if (CG == 2) cluster_sync();  // (a release: the other CTA's arrivals here have been made)
     tc_fence_after();
     if (warp == 2) free_tmem<CG>(tmem, 2 * BN);
 }

@@ -33,16 +33,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same without ordering memory (a release would wait for the stores under way).
-__device__ __forceinline__ void cluster_sync_relaxed() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 // Address in the cluster's shared memory of `addr` in CTA `rank`.
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// An arrival that orders no memory: tensor memory that has been read (tcgen05.wait::ld and a
+// fence before it) is handed back so. The barrier at the kernel's end releases it to the other
+// CTA before that may exit.
 __device__ __forceinline__ void arrive_relaxed(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -261,6 +260,18 @@ enum Site : uint32_t { SITE_STAGE_FULL = 32, SITE_STAGE_EMPTY, SITE_ACC_FULL, SI
 __device__ __forceinline__ void let_end() {
     const uint64_t t0 = globaltimer();
     while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
+}
+
+// Waits until every slot of a ring of `slots` has been given back, the next one to be filled being
+// `s` in `phase`. The arrivals that give slots back come by themselves, from MMAs that the other
+// CTA of a pair may have issued: a CTA waits for all of them before it ends, so that none finds
+// its shared memory gone.
+__device__ __forceinline__ bool drain(uint32_t empty, int slots, int s, uint32_t phase, const Ctl &ctl, uint32_t site) {
+    for (int i = 0; i < slots; ++i) {
+        if (!bar_wait(empty + 8 * s, phase ^ 1, ctl, site)) return false;
+        if (++s == slots) s = 0, phase ^= 1;
+    }
+    return true;
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
