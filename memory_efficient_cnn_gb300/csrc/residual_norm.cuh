@@ -65,8 +65,7 @@ enum BackSum { BACK_RES, BACK_W_PRE, BACK_B_PRE, BACK_A, BACK_B, BACK_SUMS };
 constexpr int SMS = 152;  // blocks are cut for this many SMs, so that results depend on the shape alone
 constexpr int FUSED_THREADS = 512;
 
-// The fused pass holds rows of up to 4096 elements (8 a thread), or 8192 (16 a
-// thread, which leaves no shared memory for short groups).
+// The fused pass holds rows of up to 4096 elements (8 a thread), or 8192 (16 a thread).
 inline BackPlan plan_back(int64_t R, int64_t C, int64_t per_gate) {
     BackPlan b;
     if (R == 0 || C > 16 * FUSED_THREADS) return b;
@@ -77,12 +76,13 @@ inline BackPlan plan_back(int64_t R, int64_t C, int64_t per_gate) {
     const int64_t rpb = b.threads / b.tpr;
     b.groups = (R + per_gate - 1) / per_gate;
     b.blocks = (int)std::min<int64_t>(SMS, (R + rpb - 1) / rpb);
-    // rounds of a slot: long groups end with two joins, about a round's time each
+    // Rounds of a slot: long groups end with two joins, about a round's time each. Both forms read rows
+    // once; 4096 x 8192 bf16, RMS: 242 us with a gate a row in the short form and 2441 us in the long one,
+    // a gate for 8 rows 192 us and 518 us; for 16 rows the rule takes the long one's 345 us, for 64 216 us.
     const int64_t slots = b.blocks * rpb;
     const int64_t long_rounds = (R + slots - 1) / slots + 2 * (b.groups / b.blocks + 1) + b.groups / b.blocks;
     const int64_t short_rounds = (b.groups + slots - 1) / slots * (per_gate + 1);
     b.short_groups = short_rounds < long_rounds;
-    if (b.short_groups && b.ept == 16) return BackPlan();
     b.segments = b.short_groups ? 0 : b.groups + b.blocks;
     return b;
 }

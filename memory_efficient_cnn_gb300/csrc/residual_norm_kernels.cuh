@@ -612,27 +612,32 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 3)
 //                weighed A and B to its sums in shared memory.
 // Four rows read, two written. 8192 rows of 4096 bf16, RMS: 118 us; 200704 rows of 128
 // fp16, LAYER: 86 us; instructions bound both (70 a value, half of the issue slots). One
-// block an SM: five sums and a row's values take 123 registers of 128.
-template <typename R>
-constexpr int BACK_DEPTH = sizeof(typename R::Packed) <= 16 ? 3 : sizeof(typename R::Packed) <= 32 ? 2 : 1;
-template <typename R, int THREADS>
-using BackAhead = Ahead<R, 4, BACK_DEPTH<R>, THREADS>;
+// block an SM: five sums and a row's values take 123 registers of 128. Rows of 4097 to
+// 8192 elements have 16 a thread, and part of the sums in local memory: 4096 rows of
+// 8192 bf16, RMS, 159 us with one gate.
+// Rows on their way, the one at hand among them: as many as leave shared memory for the rest.
+template <typename R, bool SHORT>
+constexpr int BACK_DEPTH = sizeof(typename R::Packed) <= 16                                          ? 3
+                           : sizeof(typename R::Packed) <= 32 && !(SHORT && sizeof(typename R::E) == 2) ? 2
+                                                                                                       : 1;
+template <typename R, int THREADS, bool SHORT>
+using BackAhead = Ahead<R, 4, BACK_DEPTH<R, SHORT>, THREADS>;
 // Shared memory of the rows on their way, which also joins slots: THREADS * EPT floats.
-template <typename R, int THREADS>
-constexpr int BACK_ROWS_BYTES = BackAhead<R, THREADS>::BYTES > THREADS * R::PAIRS * 8 ? BackAhead<R, THREADS>::BYTES
-                                                                                  : THREADS * R::PAIRS * 8;
+template <typename R, int THREADS, bool SHORT>
+constexpr int BACK_ROWS_BYTES = BackAhead<R, THREADS, SHORT>::BYTES > THREADS * R::PAIRS * 8 ? BackAhead<R, THREADS, SHORT>::BYTES
+                                                                                         : THREADS * R::PAIRS * 8;
 
 template <typename T, int V, int EPT, int TPR, int THREADS, bool SHORT>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_backward_fused(const __grid_constant__ NormArgs p, const __grid_constant__ BackPlan plan, float *part, float *seg,
                         T *dgate) {
     using R = Row<T, V, EPT, TPR>;
-    using A = BackAhead<R, THREADS>;
-    constexpr int RPB = THREADS / TPR, DEPTH = BACK_DEPTH<R>;
+    using A = BackAhead<R, THREADS, SHORT>;
+    constexpr int RPB = THREADS / TPR, DEPTH = BACK_DEPTH<R, SHORT>;
     constexpr int W = TPR * EPT;  // columns a slot holds
     // rows on their way, between groups [RPB][W] to join slots; parameters; SHORT: A and B weighed, [2][RPB][W]
     extern __shared__ uint4 dyn[];
-    unsigned char *par_at = reinterpret_cast<unsigned char *>(dyn) + BACK_ROWS_BYTES<R, THREADS>;
+    unsigned char *par_at = reinterpret_cast<unsigned char *>(dyn) + BACK_ROWS_BYTES<R, THREADS, SHORT>;
     float *sums = reinterpret_cast<float *>(par_at + Params<R, PARAMS, TPR>::BYTES);
     __shared__ float buf[2][2][THREADS / 32];
     RowReduce<TPR, THREADS> red(buf);
@@ -950,9 +955,10 @@ template <typename T, int V, int EPT, int TPR, bool SHORT>
 cudaError_t launch_fused(const NormArgs &p, const BackPlan &plan, float *part, float *seg, T *dgate, cudaStream_t st) {
     constexpr int THREADS = FUSED_THREADS;
     using R = Row<T, V, EPT, TPR>;
-    const size_t smem = BACK_ROWS_BYTES<R, THREADS> + Params<R, PARAMS, TPR>::BYTES + (SHORT ? 2 * THREADS * EPT * 4 : 0);
+    constexpr int smem = BACK_ROWS_BYTES<R, THREADS, SHORT> + Params<R, PARAMS, TPR>::BYTES + (SHORT ? 2 * THREADS * EPT * 4 : 0);
+    static_assert(smem <= 226 * 1024, "a block's shared memory");
     auto kernel = norm_backward_fused<T, V, EPT, TPR, THREADS, SHORT>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kernel<<<plan.blocks, THREADS, smem, st>>>(p, plan, part, seg, dgate);
     return cudaGetLastError();
@@ -960,12 +966,13 @@ cudaError_t launch_fused(const NormArgs &p, const BackPlan &plan, float *part, f
 
 template <typename T, int V>
 cudaError_t launch_fused_tpr(const NormArgs &p, const BackPlan &plan, float *part, float *seg, T *dgate, cudaStream_t st) {
-    if (plan.ept == 16) return launch_fused<T, V, 16, 512, false>(p, plan, part, seg, dgate, st);
-    auto with = [&](auto tpr) {
-        constexpr int TPR = decltype(tpr)::value;
-        return plan.short_groups ? launch_fused<T, V, 8, TPR, true>(p, plan, part, seg, dgate, st)
-                                 : launch_fused<T, V, 8, TPR, false>(p, plan, part, seg, dgate, st);
+    auto as = [&](auto ept, auto tpr) {
+        constexpr int EPT = decltype(ept)::value, TPR = decltype(tpr)::value;
+        return plan.short_groups ? launch_fused<T, V, EPT, TPR, true>(p, plan, part, seg, dgate, st)
+                                 : launch_fused<T, V, EPT, TPR, false>(p, plan, part, seg, dgate, st);
     };
+    if (plan.ept == 16) return as(IntC<16>(), IntC<512>());
+    auto with = [&](auto tpr) { return as(IntC<8>(), tpr); };
     switch (plan.tpr) {
         case 8: return with(IntC<8>());
         case 16: return with(IntC<16>());

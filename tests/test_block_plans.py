@@ -30,3 +30,15 @@ def test_one_kernel_columns(plans):
             taken += 1
             assert n % 32 == 0 and 32 <= n <= 256 and n >= C, C
     assert taken == 113  # 16 to 128 channels
+
+
+def test_norm_backward_reads_once(plans):
+    """Rows of up to 8192 elements stay in registers whatever a gate's extent; short groups are taken whole."""
+    plans.norm_back_blocks.argtypes = [ctypes.c_int64] * 3 + [ctypes.POINTER(ctypes.c_int)]
+    short = ctypes.c_int()
+    for R in (1, 16, 600, 4096, 100000):
+        for C in (1, 64, 4096, 4097, 5000, 6000, 8191, 8192):
+            for per in (1, 2, 8, 64, 1000, R):
+                assert plans.norm_back_blocks(R, C, min(per, R), ctypes.byref(short)) > 0, (R, C, per)
+                if per == 1 and R > 1:
+                    assert short.value, (R, C)
