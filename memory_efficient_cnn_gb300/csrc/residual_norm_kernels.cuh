@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int64_t g = g0 + slot, first = g * p.per_gate;
             const int64_t last = g < plan.groups ? min(p.R, first + p.per_gate) : first;
             rows(g < plan.groups ? g : 0, first, last, 1, (int)p.per_gate, pg);
-            if (!p.y) continue;
+            if (!p.y || g >= plan.groups) continue;  // (a slot without a group has the first one's gate: nothing to weigh)
             typename R::Packed w, b;
             if (p.w_post) R::load(w, p.w_post, 0, C, t);
             if (p.b_post) R::load(b, p.b_post, 0, C, t);
@@ -864,7 +864,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 fold[RPB * W + 2 * e * TPR + t] += b0, fold[RPB * W + (2 * e + 1) * TPR + t] += b1;
                 acc[BACK_A][e] = acc[BACK_B][e] = f2(0.0f);
             }
-            if (dgate && g < plan.groups) R::store(dgate, g * C, C, t, d);
+            if (dgate) R::store(dgate, g * C, C, t, d);
         }
 #pragma unroll
         for (int e = 0; e < R::PAIRS; ++e) {

@@ -45,3 +45,13 @@ def test_same_bits_every_time(per):
         args = [t.cuda() for t in (dr, dn, x, y)]
         a, b = (mec.residual_norm_backward(*args, **p) for _ in range(2))
         assert all(a[k] is b[k] is None or torch.equal(a[k], b[k]) for k in a)
+
+
+def test_an_infinite_gate_stays_with_its_group():
+    """Slots without a group add nothing to the sums, whatever the first group's gate is."""
+    x, y, dr, _, p = make(10, 64, "f32", "layer", "none", per=1)
+    p["gate"][0, 3] = float("inf")
+    p = moved(p, lambda t: t.cuda())
+    g = mec.residual_norm_backward(dr.cuda(), None, x.cuda(), y.cuda(), **p)
+    assert float(g["db_post"][3]) == float("inf") * float(dr[0, 3].sign())
+    assert bool(g["dw_post"][3].isinf()) and bool(g["dgate"].isfinite().all())
