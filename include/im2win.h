@@ -437,7 +437,8 @@ im2win_status im2win_clip_grad_norm_size(const int64_t *sizes, int64_t count, si
  * element's alignment (views into a flat buffer), the other pointers 16 bytes
  * (norm: 4). A NaN among the gradients makes the norm and every output NaN, an
  * infinity makes the factor 0, as the formula gives. Squares are summed in
- * fp32 within at most 8192 elements and in fp64 across them.
+ * fp32 within at most 8192 elements and in fp64 across them; squares beyond fp32's
+ * range, of gradients that are within it, are summed scaled.
  */
 im2win_status im2win_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *sizes,
                                     const int *dtypes, int64_t count, double max_norm, double eps, float *norm,

@@ -55,31 +55,52 @@ __device__ __forceinline__ int entry_of(const Table<CAP> &t, uint32_t chunk) {
     return lo;
 }
 
+// A thread's sum of squares `a`, or, where they passed fp32's range (its subnormal numbers,
+// which the sums below 2^-100 may hold, or its largest), the same of the values times a power
+// of two: again(scale).
+template <typename Fn>
+__device__ __forceinline__ double in_range(float a, Fn again) {
+    if (a >= 0x1p-100f && a <= 3.402823466e38f) return a;
+    const bool large = !(a < 1.0f);  // (infinite, or NaN)
+    return (double)again(large ? 0x1p-100f : 0x1p100f) * (large ? 0x1p200 : 0x1p-200);
+}
+
 template <typename T>
-__device__ __forceinline__ float squares(const T *p, int n) {
+__device__ __forceinline__ double squares(const T *p, int n) {
     using V = Vec16<T>;
-    float a = 0.0f;
-    int done = 0;
-    auto add = [&](const V &v) {
+    auto add = [](float &a, const V &v, float scale) {
 #pragma unroll
-        for (int j = 0; j < V::N; ++j) a = fmaf(to_f32(v.v[j]), to_f32(v.v[j]), a);
-    };
-    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-        const V *from = reinterpret_cast<const V *>(p);
-        if (n == CHUNK) {  // (without conditions: with them this loop has two thirds of the rate)
-            V v[CHUNK / (THREADS * V::N)];
-#pragma unroll
-            for (int i = 0; i < CHUNK / (THREADS * V::N); ++i) v[i] = from[i * THREADS + threadIdx.x];
-#pragma unroll
-            for (int i = 0; i < CHUNK / (THREADS * V::N); ++i) add(v[i]);
-            return a;
+        for (int j = 0; j < V::N; ++j) {
+            const float x = to_f32(v.v[j]) * scale;
+            a = fmaf(x, x, a);
         }
-        done = n / V::N * V::N;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < n / V::N; i += THREADS) add(from[i]);
+    };
+    const bool vectors = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    const V *from = reinterpret_cast<const V *>(p);
+    if (vectors && n == CHUNK) {  // (without conditions: with them this loop has two thirds of the rate)
+        V v[CHUNK / (THREADS * V::N)];
+#pragma unroll
+        for (int i = 0; i < CHUNK / (THREADS * V::N); ++i) v[i] = from[i * THREADS + threadIdx.x];
+        auto sum = [&](float scale) {
+            float a = 0.0f;
+#pragma unroll
+            for (int i = 0; i < CHUNK / (THREADS * V::N); ++i) add(a, v[i], scale);
+            return a;
+        };
+        return in_range(sum(1.0f), sum);
     }
-    for (int i = done + threadIdx.x; i < n; i += THREADS) a = fmaf(to_f32(p[i]), to_f32(p[i]), a);
-    return a;
+    const int done = vectors ? n / V::N * V::N : 0;
+    auto sum = [&](float scale) {
+        float a = 0.0f;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < done / V::N; i += THREADS) add(a, from[i], scale);
+        for (int i = done + threadIdx.x; i < n; i += THREADS) {
+            const float x = to_f32(p[i]) * scale;
+            a = fmaf(x, x, a);
+        }
+        return a;
+    };
+    return in_range(sum(1.0f), sum);
 }
 
 __device__ __forceinline__ double warp_sum(double v) {

@@ -107,3 +107,37 @@ def test_beyond_32_bit_offsets():
     want = torch.tensor([0.4, 0.3, 1.2], dtype=torch.float64)
     got = torch.stack([g[0], g[-1], g[1 << 31]]).double().cpu()
     assert bool(((got - want).abs() <= want * 2.0 ** -7).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [5, 8192, 70001])
+@pytest.mark.parametrize("power", [-140, -100, -74, -55, 60, 66, 110])
+def test_squares_outside_of_fp32(dt, n, power):
+    """Gradients whose squares pass fp32's range below or above, alone and beside ordinary ones;
+    the norm itself is within the range."""
+    g = (make([n], ["f32"])[0] * 2.0 ** 10).double().mul(2.0 ** power / 2 ** 10).to(DT[dt])
+    for grads in ([g], [g, torch.full((9,), 3.0, dtype=DT[dt])]):
+        dev = [t.cuda() for t in grads]
+        norm = mec.grad_norm(dev)
+        want = true_norm(grads)
+        assert abs(float(norm) - want) <= NORM_TOL * want + 2.0 ** -149, (float(norm), want)
+        if want == 0:  # (bf16 ends at 2^-133)
+            continue
+        outs = [torch.empty_like(t) for t in dev]
+        limit = 0.25 * want
+        assert torch.equal(mec.clip_grad_norm(dev, limit, outs=outs, eps=0.0), norm)
+        factor = limit / want
+        for t, o in zip(grads, outs):
+            v = t.double() * factor
+            # a norm or a limit below fp32's normal numbers is a multiple of 2^-149
+            e = v.abs() * (U[t.dtype] + NORM_TOL + 4 * 2.0 ** -24 + 2.0 ** -147 / want) + TINY[t.dtype]
+            assert bool(((o.double().cpu() - v).abs() <= e).all())
+
+
+def test_infinities_among_squares_outside_of_fp32():
+    for big in (1e30, 1e-30):
+        g = torch.full((9000,), big, device="cuda")
+        for bad in (float("inf"), float("-inf"), float("nan")):
+            g[17] = bad
+            norm = float(mec.grad_norm([g]))
+            assert norm != norm if bad != bad else norm == float("inf")
