@@ -392,7 +392,6 @@ TcPlan plan_f32(const Product &d) { return plan_tiles(d, 1, BN, 0.95, d.epi == E
 
 cudaError_t launch_f32(const Product &d, uint32_t *status, bool first, void *part, cudaStream_t st) {
     const TcPlan pl = plan_f32(d);
-    if (pl.units == 0) return cudaErrorInvalidValue;
     F32Params p = {};
     p.M = d.M; p.N = d.N; p.KB = (d.K + BK - 1) / BK;
     const bool two = d.a1.p != nullptr;

@@ -437,12 +437,11 @@ TcPlan plan_tc(const Product &d) {
     // single CTA's shared-memory fill), outputs a little over half of it on the smaller tile.
     const double epi = d.epi == EPI_DGATED ? 4 : d.epi == EPI_GATED ? (d.kept ? 3 : 2.1) : 1.8;
     const TcPlan pair = plan_tiles(d, 2, 256, 0.345, epi), single = plan_tiles(d, 1, 128, 0.335, 0.55 * epi + 0.1);
-    return pair.units == 0 || (single.units != 0 && single.cost < pair.cost) ? single : pair;
+    return single.cost < pair.cost ? single : pair;
 }
 
 cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool first, void *part, cudaStream_t st) {
     const TcPlan pl = plan_tc(d);
-    if (pl.units == 0) return cudaErrorInvalidValue;
     TcParams p = {};
     p.M = d.M; p.N = d.N; p.KB = (d.K + BK - 1) / BK;
     const bool two = d.a1.p != nullptr;

@@ -382,10 +382,10 @@ inline TcPlan plan_tiles(const Product &d, int cg, int bn, double kb, double epi
     pl.tiles_m = (d.M + tm - 1) / tm;
     pl.tiles_n = (d.N + cols - 1) / cols;
     const int64_t tiles = (int64_t)z * pl.tiles_m * pl.tiles_n, total = tiles * KT;
-    if (tiles > 0x3fffffff || total > 0x3fffffffll) return pl;  // (streamed indexes stay in 32 bits)
     pl.units = (int)std::min<int64_t>(most, tiles);
     const int64_t waves = (tiles + pl.units - 1) / pl.units;
     pl.cost = 4 + KT * kb + epi + (double)(waves - 1) * std::max(KT * kb, epi);
+    if (total > 0x3fffffffll) return pl;  // (streamed indexes stay in 32 bits)
     TcPlan st = pl;
     st.streamed = true;
     st.units = (int)std::min<int64_t>(most, std::max<int64_t>(1, total / 4));  // 4 blocks at least

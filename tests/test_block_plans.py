@@ -6,6 +6,7 @@ import subprocess
 
 import pytest
 
+import memory_efficient_cnn_gb300 as mec
 from memory_efficient_cnn_gb300 import build as mbuild
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -30,6 +31,18 @@ def test_one_kernel_columns(plans):
             taken += 1
             assert n % 32 == 0 and 32 <= n <= 256 and n >= C, C
     assert taken == 113  # 16 to 128 channels
+
+
+@pytest.mark.parametrize("R,C,F", [(131072, 131072, 131072), (2 ** 31 - 1024, 512, 512), (512, 2 ** 31 - 1024, 512),
+                                   (512, 512, 2 ** 31 - 1024), (2 ** 20, 2 ** 20, 2 ** 20), (1, 1, 1)])
+def test_every_product_has_a_plan(plans, R, C, F):
+    """Whatever im2win_gated_ffn_size accepts can be launched: its products have tiles."""
+    streamed = ctypes.c_int()
+    for f32 in (0, 1):
+        mec.im2win_gated_ffn_size(mec.FFN_BACKWARD, R, C, F, mec.F32 if f32 else mec.BF16)
+        for M, N, K, kind, two in ((R, F, C, 1, 0), (R, C, F, 0, 0), (R, F, C, 2, 0), (R, C, F, 0, 1), (F, C, R, 0, 2),
+                                   (C, F, R, 0, 0)):
+            assert plans.ffn_product_units(f32, M, N, K, kind, two, ctypes.byref(streamed)) > 0, (f32, M, N, K, kind)
 
 
 def test_norm_backward_reads_once(plans):
