@@ -64,6 +64,16 @@ def _shape(fn, name, t, want):
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(want)}")
 
 
+def _unrecorded(fn, *ts):
+    """Refuses tensors whose gradients would silently go missing: nothing here is recorded
+    by autograd, the gradients are calls of their own."""
+    if torch.is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{fn}: a tensor requires grad, but autograd does not record this call; make it under "
+                                 "torch.no_grad() (its gradients are a call of their own) or detach the tensor")
+
+
 def _empty(nbytes, device):
     return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
@@ -160,6 +170,7 @@ def _ffn_buffer(buffer, dims, x):
 
 
 def _ffn_forward(fn, x, w_gate, w_up, w_down, act, ws, out, saved, train):
+    _unrecorded(fn, x, w_gate, w_up, w_down)
     dims = _ffn_shapes(fn, x, w_gate, w_up, w_down)
     given = ws is not None or out is not None or saved is not None
     if ws is None:
@@ -176,7 +187,8 @@ def _ffn_forward(fn, x, w_gate, w_up, w_down, act, ws, out, saved, train):
 
 def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, act: str = "silu",
               ws: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
-    """Gated feed-forward block over the last axis of x[..., C]."""
+    """Gated feed-forward block over the last axis of x[..., C]. Autograd does not record it:
+    tensors that require grad are refused outside of torch.no_grad()."""
     return _ffn_forward("gated_ffn", x, w_gate, w_up, w_down, act, ws, out, None, False)[0]
 
 
@@ -300,8 +312,10 @@ def residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post: str =
                   b_pre=None, eps: float = 1e-6):
     """(r, n) of r = res_scale * x + gate * post(y), n = pre(r) over the last
     axis; n is None where pre is "none". gate[i] belongs to rows_per_gate
-    consecutive rows (None: all rows). y None: r = res_scale * x."""
+    consecutive rows (None: all rows). y None: r = res_scale * x. Autograd does not
+    record it: tensors that require grad are refused outside of torch.no_grad()."""
     fn = "residual_norm"
+    _unrecorded(fn, x, y, gate, res_scale, w_post, b_post, w_pre, b_pre)
     dims = _norm_check(fn, x, y, gate, rows_per_gate, (), (res_scale, w_post, b_post, w_pre, b_pre))
     r = torch.empty_like(x)
     n = torch.empty_like(x) if pre != "none" else None

@@ -173,6 +173,29 @@ def test_clip_binding_refusals():
         mec.clip_grad_norm([g], 1.0)
 
 
+# ---------------------------------------------------------------- autograd
+@pytest.mark.parametrize("which", range(4))
+def test_ffn_refuses_what_autograd_would_lose(which):
+    ts = [torch.zeros(4, 8), torch.zeros(16, 8), torch.zeros(16, 8), torch.zeros(8, 16)]
+    ts[which].requires_grad_()
+    for call in (mec.gated_ffn, mec.gated_ffn_train):
+        with pytest.raises(ValueError, match="requires grad"):
+            call(*ts)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # as any tensor without a GPU
+            call(*ts)
+
+
+@pytest.mark.parametrize("name", ["x", "y", "gate", "res_scale", "w_post", "b_post", "w_pre", "b_pre"])
+def test_norm_refuses_what_autograd_would_lose(name):
+    ts = dict(x=torch.zeros(6, 8), y=torch.zeros(6, 8), gate=torch.zeros(1, 8),
+              **{k: torch.zeros(8) for k in ("res_scale", "w_post", "b_post", "w_pre", "b_pre")})
+    ts[name].requires_grad_()
+    with pytest.raises(ValueError, match="requires grad"):
+        mec.residual_norm(**ts, post="layer", pre="layer")
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        mec.residual_norm(**ts, post="layer", pre="layer")
+
+
 # ---------------------------------------------------------------- the references themselves
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "sigmoid", "relu"])
 def test_ffn_reference_gradients(act):
