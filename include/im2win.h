@@ -351,13 +351,18 @@ im2win_status im2win_gated_ffn_size(int buffer, int64_t R, int64_t C, int64_t F,
  * Gated feed-forward block:
  *   g = x w_gate^T, u = x w_up^T, h = act(g) * u, y = h w_down^T,
  * x[R][C], w_gate[F][C], w_up[F][C], w_down[C][F], y[R][C]. The products run on
- * the tensor cores (fp32 as six bf16 products, as exact as an fp32 sum; few rows of
- * fp32 on the CUDA cores), with g and u in fp32. F16/BF16: h is rounded to the
- * dtype between the two products (an |h| beyond the dtype's range becomes infinite
- * there). F32: a row with an infinity may give NaN where fp32 gives an infinity.
- * `saved` (NULL for inference) receives what im2win_gated_ffn_backward needs;
- * its contents are opaque. ws begins with the 256-byte status block that
- * im2win_device_status reads.
+ * the tensor cores (few rows of fp32 on the CUDA cores), with g and u in fp32.
+ * F16/BF16: h is rounded to the dtype between the two products (an |h| beyond the
+ * dtype's range becomes infinite there). Calls of few rows (up to 16, or 32 where C F
+ * is at most 2^23) keep the remainder of that rounding for y too: the same row's y may
+ * differ by the rounding of h from that of a call of more rows. F32: each product of
+ * two values is six of their bf16 parts, off by at most 2^-22 of itself, so that a sum
+ * errs about as an fp32 one; with an infinity in it a sum may give NaN where fp32
+ * gives an infinity (not for up to 32 rows).
+ * `saved` (NULL for inference) receives what im2win_gated_ffn_backward needs, the
+ * rounded h among it; its contents are opaque. ws begins with the 256-byte status
+ * block that im2win_device_status reads; a call that has nothing to launch (R = 0, or
+ * a backward call that is asked for nothing) leaves it as it was.
  */
 im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, void *y,
                                void *saved, void *ws, size_t ws_bytes, int64_t R, int64_t C, int64_t F, int act,
@@ -368,9 +373,11 @@ im2win_status im2win_gated_ffn(const void *x, const void *w_gate, const void *w_
  * the `saved` buffer of that forward call:
  *   dh = dy w_down, dg = dh * u * act'(g), du = dh * act(g),
  *   dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x, dw_down = dy^T h.
- * dg and du are rounded to the dtype between the products (act is checked, but its
- * values and slopes are in `saved`). dx, or the three dw
- * together, may be NULL and are then not computed. With R = 0 the dw are zero.
+ * dg and du are rounded to the dtype between the products: in F16 those below 3e-8
+ * vanish, those below 6e-5 lose bits and those above 65504 become infinite, as a loss
+ * scale that is too small or too large makes of any F16 gradient. act is checked, but
+ * its values and slopes are in `saved`. dw_down is made of the h in `saved`. dx, or the
+ * three dw together, may be NULL and are then not computed. With R = 0 the dw are zero.
  */
 im2win_status im2win_gated_ffn_backward(const void *dy, const void *x, const void *w_gate, const void *w_up,
                                         const void *w_down, const void *saved, void *dx, void *dw_gate, void *dw_up,
@@ -396,7 +403,8 @@ typedef enum {
  * n must be given exactly when pre is not IM2WIN_NORM_NONE; a w or b of an absent norm
  * is an error, and so is a call with neither r nor n. The outputs may be the inputs x or y
  * themselves (r = x updates the residual in place) but must not overlap them
- * otherwise. Needs no workspace. C is at most 2^20.
+ * otherwise. Needs no workspace. C is at most 2^20. A normed row's sum of squares has
+ * to stay within fp32 (a row with one value beyond 1.8e19 does not).
  */
 im2win_status im2win_residual_norm(const void *x, const void *y, const void *gate, int64_t rows_per_gate,
                                    const void *res_scale, int post, const void *w_post, const void *b_post, int pre,

@@ -1,7 +1,9 @@
 // fp32 products of the gated feed-forward on the tensor cores.
 //
 // An fp32 operand is three bf16 planes, a = h + m + l (split_f32), and
-//   a b = h h' + (h m' + m h' + m m' + h l' + l h') + O(2^-24 a b):
+//   a b = h h' + (h m' + m h' + m m' + h l' + l h') + (m l' + l m' + l l'),
+// the last bracket left out: |m| <= 2^-7 |a| and |l| <= 2^-16 |a|, so that it is at
+// most 2^-22 |a b|, and of either sign:
 // six bf16 products for one of fp32, a twelfth of the CUDA cores' time for the
 // same number of multiplications (8192 against 256 floating-point operations a
 // clock and SM, over six). The products themselves are exact; what has to be kept
