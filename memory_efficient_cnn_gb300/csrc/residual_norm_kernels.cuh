@@ -508,7 +508,7 @@ __device__ __forceinline__ void norm_values(int kind, F2 (&v)[R::PAIRS], int C, 
 // stored, the next rows are on their way while one is worked on. Three blocks an SM
 // where shared memory has room: 8192 rows of 4096 bf16 take 50 us, 5.4 TB/s (56 us in
 // two); 200704 rows of 128 fp16 with two LAYER norms 44 us, 4.6 TB/s, half of the issue
-// slots taken (36 instructions a value).
+// slots taken (38 instructions a value).
 template <typename T, int V, int EPT, int TPR, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 3)
     norm_forward_rows(const __grid_constant__ NormArgs p, const __grid_constant__ FastDiv per_gate) {
@@ -611,8 +611,8 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 3)
 //  short groups  a row slot takes whole groups, writes their dgate and adds the
 //                weighed A and B to its sums in shared memory.
 // Four rows read, two written. 8192 rows of 4096 bf16, RMS: 118 us; 200704 rows of 128
-// fp16, LAYER: 86 us; instructions bound both (70 a value, half of the issue slots). One
-// block an SM: five sums and a row's values take 123 registers of 128. Rows of 4097 to
+// fp16, LAYER: 86 us; instructions bound both (74 a value, half of the issue slots). One
+// block an SM: five sums and a row's values take 124 registers of 128. Rows of 4097 to
 // 8192 elements have 16 a thread, and part of the sums in local memory: 4096 rows of
 // 8192 bf16, RMS, 159 us with one gate.
 // Rows on their way, the one at hand among them: as many as leave shared memory for the rest.
