@@ -330,7 +330,8 @@ typedef enum {
     IM2WIN_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
     IM2WIN_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
     IM2WIN_ACT_RELU = 3,      /* max(g, 0); its derivative at 0 is 0 */
-    IM2WIN_ACT_SIGMOID = 4    /* 1 / (1 + exp(-g)) */
+    IM2WIN_ACT_SIGMOID = 4,   /* 1 / (1 + exp(-g)) */
+    IM2WIN_ACT_NONE = 5       /* g; of the group norm alone */
 } im2win_act;
 
 /* Which buffer of the gated feed-forward a size is asked for. */
@@ -451,6 +452,37 @@ im2win_status im2win_clip_grad_norm_size(const int64_t *sizes, int64_t count, si
 im2win_status im2win_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *sizes,
                                     const int *dtypes, int64_t count, double max_norm, double eps, float *norm,
                                     void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Group norm of channels-last maps with its activation
+ * ----------------------------------------------------
+ * x[N][P][C]: N images of P positions (H*W). The channels form G groups of C/G
+ * neighbours; with the mean and variance of the P * C/G elements of an image's group,
+ *   xh = (x - mean) / sqrt(var + eps),  z = xh w + b,  y = act(z).
+ * w[C] and b[C] may be NULL (1 and 0). G = C is the instance norm, G = 1 one group of
+ * all channels. Statistics and sums are fp32, made of means and squared deviations; an
+ * output is rounded once. N * P * C is at most 2^40, C at most 2^20, N * C at most
+ * 2^31, C a multiple of G (else IM2WIN_ERR_INVALID_ARG).
+ * stats[N][G][2] (fp32; NULL: not kept) receives each group's mean and 1/sqrt(var +
+ * eps) for the backward call. y may be x itself and must not overlap it otherwise.
+ * A NaN or infinity spoils its own image's group and no other.
+ */
+im2win_status im2win_group_norm_size(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, size_t *bytes);
+im2win_status im2win_group_norm(const void *x, const void *w, const void *b, void *y, void *stats, void *ws,
+                                size_t ws_bytes, int64_t N, int64_t P, int64_t C, int64_t G, int act, double eps,
+                                int dtype, void *stream);
+
+/*
+ * Gradients of im2win_group_norm at the same x, w, b and act, from dy and the `stats`
+ * of that call: dz = dy act'(z), db = sum dz, dw = sum dz xh over images and positions,
+ * dx = (w dz - mean(w dz) - xh mean(w dz xh)) / sqrt(var + eps), the means over the
+ * image's group. Each of dx, dw, db may be NULL (not computed); dw without w, or db
+ * without b, is an error. dx may be dy itself; no output may overlap an input otherwise.
+ * With N * P = 0 the sums are zero. The workspace is of the same size.
+ */
+im2win_status im2win_group_norm_backward(const void *dy, const void *x, const void *stats, const void *w, const void *b,
+                                         void *dx, void *dw, void *db, void *ws, size_t ws_bytes, int64_t N, int64_t P,
+                                         int64_t C, int64_t G, int act, int dtype, void *stream);
 
 #ifdef __cplusplus
 }

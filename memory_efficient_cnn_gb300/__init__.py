@@ -24,3 +24,6 @@ from .block import (  # noqa: F401,E402
     im2win_clip_grad_norm_size, im2win_gated_ffn, im2win_gated_ffn_backward, im2win_gated_ffn_size,
     im2win_residual_norm, im2win_residual_norm_backward, im2win_residual_norm_backward_size, residual_norm,
     residual_norm_backward)
+from .group_norm import (  # noqa: F401,E402
+    NORM_ACTS, group_norm, group_norm_backward, group_norm_train, im2win_group_norm, im2win_group_norm_backward,
+    im2win_group_norm_size)

@@ -1,0 +1,105 @@
+// Group norm: argument checks and buffers.
+#include <initializer_list>
+
+#include "group_norm.cuh"
+
+using namespace im2win;
+using namespace im2win::gnorm;
+
+namespace {
+
+im2win_status check_dims(int64_t N, int64_t P, int64_t C, int64_t G, int dtype) {
+    if (N < 0 || P < 0 || C < 1 || G < 1 || elem_size(dtype) == 0 || C % G != 0) return IM2WIN_ERR_INVALID_ARG;
+    const int64_t most = int64_t(1) << 31;
+    if (N >= most || P >= most || C > (int64_t(1) << 20) || N * P > (int64_t(1) << 40) / C || N * C > (int64_t(1) << 31))
+        return IM2WIN_ERR_UNSUPPORTED;
+    return IM2WIN_OK;
+}
+
+bool known_act(int act) {
+    return act == IM2WIN_ACT_NONE || with_act(act, [](auto) {});
+}
+
+GroupArgs make(int64_t N, int64_t P, int64_t C, int64_t G, int act, int dtype) {
+    GroupArgs a = {};
+    a.N = N, a.P = P, a.C = (int)C, a.G = (int)G, a.D = (int)(C / G), a.act = act;
+    cut(a, elem_size(dtype));
+    return a;
+}
+
+// The workspace: partial sums, the groups' sums (backward), the statistics (where the caller keeps none).
+struct Parts {
+    size_t part, sums, stats, bytes;
+    explicit Parts(const GroupArgs &a) {
+        part = 0;
+        sums = round_up((size_t)(2 * a.N * a.chunks) * a.C * 4, 256);
+        stats = sums + round_up((size_t)(a.N * a.G) * 8, 256);
+        bytes = stats + round_up((size_t)(a.N * a.G) * 8, 256);
+    }
+};
+
+void place(GroupArgs &a, void *ws, void *stats) {
+    const Parts parts(a);
+    unsigned char *base = static_cast<unsigned char *>(ws);
+    a.part = reinterpret_cast<float *>(base + parts.part);
+    a.sums = reinterpret_cast<float *>(base + parts.sums);
+    a.stats = static_cast<float *>(stats ? stats : base + parts.stats);
+}
+
+}  // namespace
+
+extern "C" {
+
+im2win_status im2win_group_norm_size(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, size_t *bytes) {
+    if (!bytes) return IM2WIN_ERR_INVALID_ARG;
+    const im2win_status s = check_dims(N, P, C, G, dtype);
+    if (s == IM2WIN_OK) *bytes = std::max<size_t>(256, Parts(make(N, P, C, G, 0, dtype)).bytes);
+    return s;
+}
+
+im2win_status im2win_group_norm(const void *x, const void *w, const void *b, void *y, void *stats, void *ws,
+                                size_t ws_bytes, int64_t N, int64_t P, int64_t C, int64_t G, int act, double eps,
+                                int dtype, void *stream) {
+    const im2win_status s = check_dims(N, P, C, G, dtype);
+    if (s != IM2WIN_OK) return s;
+    if (!known_act(act) || !(eps >= 0.0)) return IM2WIN_ERR_INVALID_ARG;
+    if (N * P == 0) return IM2WIN_OK;  // nothing to read or write
+    if (!x || !y) return IM2WIN_ERR_INVALID_ARG;
+    for (const void *p : {x, w, b, (const void *)y, (const void *)stats, (const void *)ws})
+        if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
+    GroupArgs a = make(N, P, C, G, act, dtype);
+    if (!ws || ws_bytes < Parts(a).bytes) return IM2WIN_ERR_WORKSPACE;
+    a.x = x, a.w = w, a.b = b, a.y = y, a.eps = (float)eps;
+    place(a, ws, stats);
+    cudaError_t e = cudaErrorInvalidValue;
+    with_dtype(dtype, [&](auto *t) { e = launch_forward<std::remove_pointer_t<decltype(t)>>(a, static_cast<cudaStream_t>(stream)); });
+    return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+}
+
+im2win_status im2win_group_norm_backward(const void *dy, const void *x, const void *stats, const void *w, const void *b,
+                                         void *dx, void *dw, void *db, void *ws, size_t ws_bytes, int64_t N, int64_t P,
+                                         int64_t C, int64_t G, int act, int dtype, void *stream) {
+    const im2win_status s = check_dims(N, P, C, G, dtype);
+    if (s != IM2WIN_OK) return s;
+    if (!known_act(act) || (dw && !w) || (db && !b)) return IM2WIN_ERR_INVALID_ARG;
+    if (N * P > 0 && (!dy || !x || !stats)) return IM2WIN_ERR_INVALID_ARG;
+    for (const void *p : {dy, x, stats, w, b, (const void *)dx, (const void *)dw, (const void *)db, (const void *)ws})
+        if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (N * P == 0) {  // sums over nothing
+        cudaError_t e = cudaSuccess;
+        for (void *p : {dw, db})
+            if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)C * elem_size(dtype), st);
+        return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+    }
+    if (!dx && !dw && !db) return IM2WIN_OK;
+    GroupArgs a = make(N, P, C, G, act, dtype);
+    if (!ws || ws_bytes < Parts(a).bytes) return IM2WIN_ERR_WORKSPACE;
+    a.x = x, a.dy = dy, a.w = w, a.b = b, a.dx = dx, a.dw = dw, a.db = db;
+    place(a, ws, const_cast<void *>(stats));
+    cudaError_t e = cudaErrorInvalidValue;
+    with_dtype(dtype, [&](auto *t) { e = launch_backward<std::remove_pointer_t<decltype(t)>>(a, st); });
+    return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,81 @@
+"""Refusals and sizes of the group norm, the router and the experts' feed-forward,
+answered on the host: no GPU is needed, and nothing is launched."""
+import ctypes
+
+import pytest
+import torch
+
+import memory_efficient_cnn_gb300 as mec
+from memory_efficient_cnn_gb300 import build as mbuild
+from memory_efficient_cnn_gb300._binding import (
+    BF16, ERR_INVALID_ARG, ERR_MISALIGNED, ERR_UNSUPPORTED, ERR_WORKSPACE, F16, F32, OK)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    mbuild.build()
+    return mec.lib()
+
+
+# ---------------------------------------------------------------- group norm
+def norm_call(x=4096, w=4096, b=4096, y=8192, stats=None, ws=16384, ws_bytes=1 << 40, N=2, P=9, C=8, G=2, act=5, eps=1e-5,
+              dtype=F16):
+    return mec.lib().im2win_group_norm(x, w, b, y, stats, ws, ws_bytes, N, P, C, G, act, eps, dtype, None)
+
+
+def test_group_norm_refusals():
+    for kw in (dict(x=None), dict(y=None), dict(act=6), dict(act=-1), dict(dtype=3), dict(N=-1), dict(P=-1), dict(C=0),
+               dict(G=0), dict(G=3), dict(G=16), dict(eps=-1.0), dict(eps=float("nan"))):
+        assert norm_call(**kw) == ERR_INVALID_ARG, kw
+    for kw in (dict(x=4098), dict(w=4104), dict(b=4100), dict(y=8200), dict(stats=8), dict(ws=16392)):
+        assert norm_call(**kw) == ERR_MISALIGNED, kw
+    for kw in (dict(C=1 << 21, G=1), dict(N=1 << 31), dict(P=1 << 31), dict(N=1 << 20, P=1 << 20), dict(N=1 << 12, C=1 << 20)):
+        assert norm_call(**kw) == ERR_UNSUPPORTED, kw
+    assert norm_call(ws=None) == ERR_WORKSPACE
+    assert norm_call(ws_bytes=mec.im2win_group_norm_size(2, 9, 8, 2, F16) - 1) == ERR_WORKSPACE
+    for kw in (dict(N=0), dict(P=0)):
+        assert norm_call(x=None, y=None, ws=None, ws_bytes=0, **kw) == OK
+    sz = ctypes.c_size_t()
+    assert mec.lib().im2win_group_norm_size(2, 9, 8, 2, F16, None) == ERR_INVALID_ARG
+    assert mec.lib().im2win_group_norm_size(2, 9, 8, 3, F16, ctypes.byref(sz)) == ERR_INVALID_ARG
+
+
+def test_group_norm_backward_refusals():
+    def call(dy=4096, x=4096, stats=4096, w=4096, b=4096, dx=8192, dw=8192, db=8192, ws=16384, ws_bytes=1 << 40, P=9, act=0):
+        return mec.lib().im2win_group_norm_backward(dy, x, stats, w, b, dx, dw, db, ws, ws_bytes, 2, P, 8, 2, act, F32, None)
+
+    for kw in (dict(dy=None), dict(x=None), dict(stats=None), dict(w=None), dict(b=None), dict(act=6)):
+        assert call(**kw) == ERR_INVALID_ARG, kw
+    for kw in (dict(dy=8), dict(dx=8200), dict(dw=8), dict(db=4), dict(ws=8)):
+        assert call(**kw) == ERR_MISALIGNED, kw
+    assert call(ws=None) == ERR_WORKSPACE and call(ws_bytes=0) == ERR_WORKSPACE
+    assert call(dx=None, dw=None, db=None, ws=None) == OK  # nothing asked for
+    assert call(P=0, dy=None, x=None, stats=None, dw=None, db=None, ws=None) == OK
+
+
+def test_group_norm_binding_refusals():
+    x, w = torch.zeros(2, 9, 8), torch.zeros(8)
+    stats = torch.zeros(2, 4, 2)
+    with pytest.raises(ValueError, match="do not form 3 groups"):
+        mec.group_norm(x, 3)
+    with pytest.raises(ValueError, match="do not form 0 groups"):
+        mec.group_norm(x, 0)
+    with pytest.raises(ValueError, match=r"\[N, ..., C\]"):
+        mec.group_norm(w, 2)
+    with pytest.raises(ValueError, match="w has shape"):
+        mec.group_norm(x, 2, torch.zeros(7))
+    with pytest.raises(ValueError, match="out has shape"):
+        mec.group_norm(x, 2, out=torch.zeros(2, 8, 8))
+    with pytest.raises(TypeError, match="one dtype"):
+        mec.group_norm(x, 2, w.half())
+    with pytest.raises(ValueError, match="out is x"):
+        mec.group_norm_train(x, 2, out=x)
+    with pytest.raises(ValueError, match="requires grad"):
+        mec.group_norm(x, 2, w.requires_grad_())
+    w = w.detach()
+    with pytest.raises(ValueError, match="dy has shape"):
+        mec.group_norm_backward(torch.zeros(2, 9, 16), x, stats)
+    with pytest.raises(ValueError, match=r"stats must be"):
+        mec.group_norm_backward(x, x, stats[0])
+    with pytest.raises(ValueError, match="CUDA"):
+        mec.group_norm(x, 2, w, w)
