@@ -484,6 +484,37 @@ im2win_status im2win_group_norm_backward(const void *dy, const void *x, const vo
                                          void *dx, void *dw, void *db, void *ws, size_t ws_bytes, int64_t N, int64_t P,
                                          int64_t C, int64_t G, int act, int dtype, void *stream);
 
+/*
+ * A block of experts
+ * ------------------
+ * T rows (positions of channels-last maps, or feature vectors) are each sent to k of E
+ * gated feed-forwards. The router chooses them from logits[T][E], and im2win_expert_ffn
+ * computes the sum of their weighted outputs.
+ */
+typedef enum {
+    IM2WIN_ROUTE_TOP = 0, /* weights: softmax over the row's k choices */
+    IM2WIN_ROUTE_ALL = 1  /* weights: the choices' shares of the softmax over all E */
+} im2win_route;
+
+/*
+ * experts[T][k]: the indexes of each row's k largest logits, the largest first, equal
+ * ones (also 0 and -0) by the lower index; weights[T][k] (dtype): their softmax weights,
+ * in fp32 until the rounding. A logit of -infinity marks an expert that the row may not
+ * take; where fewer than k are left, the other places have expert -1 and weight 0. A NaN
+ * ranks above all numbers and makes the row's weights NaN. E is at most 1024, k at most 32
+ * and at most E.
+ */
+im2win_status im2win_expert_route(const void *logits, void *weights, int32_t *experts, int64_t T, int64_t E, int64_t k,
+                                  int over, int dtype, void *stream);
+
+/*
+ * dlogits[T][E] from dweights[T][k] at the same logits and the experts chosen there (the
+ * choice itself has no gradient). Places whose expert is outside [0, E) take no part.
+ */
+im2win_status im2win_expert_route_backward(const void *dweights, const void *logits, const int32_t *experts,
+                                           void *dlogits, int64_t T, int64_t E, int64_t k, int over, int dtype,
+                                           void *stream);
+
 #ifdef __cplusplus
 }
 #endif

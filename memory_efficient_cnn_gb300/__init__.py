@@ -27,3 +27,5 @@ from .block import (  # noqa: F401,E402
 from .group_norm import (  # noqa: F401,E402
     NORM_ACTS, group_norm, group_norm_backward, group_norm_train, im2win_group_norm, im2win_group_norm_backward,
     im2win_group_norm_size)
+from .experts import (  # noqa: F401,E402
+    ROUTES, expert_route, expert_route_backward, im2win_expert_route, im2win_expert_route_backward)

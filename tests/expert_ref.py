@@ -75,3 +75,50 @@ def group_norm_all(x, G, w, b, act, eps, dtype, dy=None):
     if b is not None:
         out["db"] = rounded(dz.sum((0, 1)), edz.sum((0, 1)) + kc * dz.abs().sum((0, 1)), (C,))
     return out
+
+
+# ---------------------------------------------------------------- router
+def route(logits, k):
+    """Indexes of the k largest of each row of float64 logits, equal ones by the lower index, -1 where none may be taken."""
+    at = torch.argsort(logits, dim=-1, descending=True, stable=True)[..., :k]
+    return torch.where(logits.gather(-1, at) == -math.inf, -1, at)
+
+
+def route_all(logits, k, over, dtype, dweights=None, experts=None):
+    """logits [T, E] in float64. An exponential of a difference of logits errs by the rounding of that difference,
+    up to 2^-24 of |l| + |top|, and by its own few roundings; a sum of E of them by acc(E)."""
+    un, tiny = U[dtype], TINY[dtype]
+    T, E_ = logits.shape
+    if experts is None:
+        experts = route(logits, k)
+    took = (experts >= 0) & (experts < E_)
+    safe = experts.clamp(0, E_ - 1).long()
+    chosen = torch.where(took, logits.gather(-1, safe), torch.full((), -math.inf, dtype=torch.float64))
+    top = (logits if over == "all" else chosen).amax(-1, keepdim=True)
+    top = torch.where(top == -math.inf, torch.zeros_like(top), top)
+    p = torch.exp(logits - top)
+    e = torch.exp(chosen - top)
+    total = (p if over == "all" else e).sum(-1, keepdim=True)
+    total = torch.where(total == 0, torch.ones_like(total), total)
+    finite = torch.where(logits.isfinite(), logits, torch.zeros_like(logits))
+    rel = E * (finite.abs().amax(-1, keepdim=True) + top.abs()) + EXTRA
+    ks = acc(E_) + 2 * rel
+    w = e / total
+    ew = w * (rel + ks) + 2.0 ** -140
+    out = {"weights": (w, ew + un * (w + ew) + tiny)}
+    if dweights is None:
+        return experts, out
+    dw = torch.where(took, dweights, torch.zeros_like(dweights))
+    s = (w * dw).sum(-1, keepdim=True)
+    es = (ew * dw.abs()).sum(-1, keepdim=True) + ks * (w * dw).abs().sum(-1, keepdim=True)
+    z = lambda v: torch.zeros_like(logits).scatter_add(-1, safe, torch.where(took, v, torch.zeros_like(v)))  # noqa: E731
+    if over == "all":
+        q, add = p / total, z(dw)
+        v = q * (add - s)
+        ev = q * (rel + ks) * (add.abs() + s.abs()) + q * (es + 4 * E * (z(dw.abs()) + s.abs()))
+    else:
+        v = z(w * (dw - s))
+        ev = z(ew * (dw - s).abs() + w * (es + 4 * E * (dw.abs() + s.abs())))
+    ev = ev + 2.0 ** -120
+    out["dlogits"] = (v, ev + un * (v.abs() + ev) + tiny)
+    return experts, out

@@ -79,3 +79,37 @@ def test_group_norm_binding_refusals():
         mec.group_norm_backward(x, x, stats[0])
     with pytest.raises(ValueError, match="CUDA"):
         mec.group_norm(x, 2, w, w)
+
+
+# ---------------------------------------------------------------- router
+def test_route_refusals():
+    def call(logits=4096, weights=4096, experts=4096, T=3, E=8, k=2, over=0, dtype=BF16):
+        return mec.lib().im2win_expert_route(logits, weights, experts, T, E, k, over, dtype, None)
+
+    def back(dw=4096, logits=4096, experts=4096, dl=4096, T=3, E=8, k=2, over=0, dtype=BF16):
+        return mec.lib().im2win_expert_route_backward(dw, logits, experts, dl, T, E, k, over, dtype, None)
+
+    for fn, names in ((call, ("logits", "weights", "experts")), (back, ("dw", "logits", "experts", "dl"))):
+        for name in names:
+            assert fn(**{name: None}) == ERR_INVALID_ARG
+            assert fn(**{name: 4104}) == ERR_MISALIGNED
+        for kw in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(over=2), dict(over=-1), dict(dtype=4)):
+            assert fn(**kw) == ERR_INVALID_ARG, kw
+        for kw in (dict(E=1025), dict(E=64, k=33), dict(T=1 << 31)):
+            assert fn(**kw) == ERR_UNSUPPORTED, kw
+        assert fn(T=0, **{n: None for n in names}) == OK
+
+
+def test_route_binding_refusals():
+    logits, w, e = torch.zeros(4, 8), torch.zeros(4, 2), torch.zeros(4, 2, dtype=torch.int32)
+    for k in (0, 9):
+        with pytest.raises(ValueError, match="k must be between"):
+            mec.expert_route(logits, k)
+    with pytest.raises(ValueError, match="dweights has shape"):
+        mec.expert_route_backward(torch.zeros(3, 2), logits, e)
+    with pytest.raises(TypeError, match="one dtype"):
+        mec.expert_route_backward(w.half(), logits, e)
+    with pytest.raises(ValueError, match="requires grad"):
+        mec.expert_route(logits.clone().requires_grad_(), 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        mec.expert_route(logits, 2)
