@@ -515,6 +515,42 @@ im2win_status im2win_expert_route_backward(const void *dweights, const void *log
                                            void *dlogits, int64_t T, int64_t E, int64_t k, int over, int dtype,
                                            void *stream);
 
+/* Bytes of a buffer of the experts' feed-forward (host arithmetic only). T may be 0; E at most
+ * 1024, k at most 32 (it may pass E); T k + 64 E, E C and E F below 2^31 - 1024, and E C F and
+ * (T k + 64 E) times C or F at most 2^40 (else IM2WIN_ERR_UNSUPPORTED). */
+im2win_status im2win_expert_ffn_size(int buffer, int64_t T, int64_t k, int64_t E, int64_t C, int64_t F, int dtype,
+                                     size_t *bytes);
+
+/*
+ * Gated feed-forward by experts:
+ *   y[t] = sum over j < k of weights[t][j] ffn_e(x[t]),   e = experts[t][j],
+ *   ffn_e(v) = (act(v w_gate[e]^T) * (v w_up[e]^T)) w_down[e]^T,
+ * x[T][C], experts[T][k] (int32, on the device), weights[T][k] (dtype), w_gate[E][F][C],
+ * w_up[E][F][C], w_down[E][C][F], y[T][C]. A place whose expert is outside [0, E) takes no part
+ * (a position dropped where its expert is full), whatever its weight; a row with none left gets
+ * zeros; a row may name an expert twice. Only the experts that rows name are read.
+ * The products are those of im2win_gated_ffn, with its roundings (h, and in the backward pass
+ * dg and du); ffn_e(x[t]) is rounded to the dtype as well before it is weighted and summed in
+ * fp32. y must not overlap an input. `saved` (NULL for inference; FFN_SAVED) receives what the
+ * backward call needs; its contents are opaque. ws begins with the status block.
+ */
+im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const void *weights, const void *w_gate,
+                                const void *w_up, const void *w_down, void *y, void *saved, void *ws, size_t ws_bytes,
+                                int64_t T, int64_t k, int64_t E, int64_t C, int64_t F, int act, int dtype, void *stream);
+
+/*
+ * Gradients of im2win_expert_ffn at the same weights, from dy[T][C] and the `saved` buffer of that
+ * call (which holds the rows and their experts): dx[T][C], dweights[T][k], and dw_gate, dw_up,
+ * dw_down (zero for an expert without rows). Each of dx, dweights, or the three dw together, may be
+ * NULL and is then not computed. weights times dy, and each choice's share of dx, are rounded to the
+ * dtype; the sums over rows of an expert have a fixed order.
+ */
+im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, const void *w_gate, const void *w_up,
+                                         const void *w_down, const void *saved, void *dx, void *dweights,
+                                         void *dw_gate, void *dw_up, void *dw_down, void *ws, size_t ws_bytes,
+                                         int64_t T, int64_t k, int64_t E, int64_t C, int64_t F, int act, int dtype,
+                                         void *stream);
+
 #ifdef __cplusplus
 }
 #endif

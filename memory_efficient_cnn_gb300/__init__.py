@@ -28,4 +28,5 @@ from .group_norm import (  # noqa: F401,E402
     NORM_ACTS, group_norm, group_norm_backward, group_norm_train, im2win_group_norm, im2win_group_norm_backward,
     im2win_group_norm_size)
 from .experts import (  # noqa: F401,E402
-    ROUTES, expert_route, expert_route_backward, im2win_expert_route, im2win_expert_route_backward)
+    ROUTES, expert_ffn, expert_ffn_backward, expert_ffn_train, expert_route, expert_route_backward, im2win_expert_ffn,
+    im2win_expert_ffn_backward, im2win_expert_ffn_size, im2win_expert_route, im2win_expert_route_backward)

@@ -30,7 +30,8 @@ EXPORTS = ("im2win_workspace_size", "im2win_transform", "im2win_conv", "im2win_c
            "im2win_residual_norm", "im2win_residual_norm_backward_size", "im2win_residual_norm_backward",
            "im2win_clip_grad_norm_size", "im2win_clip_grad_norm",
            "im2win_group_norm_size", "im2win_group_norm", "im2win_group_norm_backward",
-           "im2win_expert_route", "im2win_expert_route_backward")
+           "im2win_expert_route", "im2win_expert_route_backward",
+           "im2win_expert_ffn_size", "im2win_expert_ffn", "im2win_expert_ffn_backward")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 KERNEL_F32, KERNEL_TAP, KERNEL_EXPAND = 0, 1, 2
 
@@ -101,6 +102,9 @@ def lib() -> ctypes.CDLL:
             L.im2win_group_norm_backward.argtypes = [vp] * 9 + [sz, i64, i64, i64, i64, ci, ci, vp]
             L.im2win_expert_route.argtypes = [vp, vp, vp, i64, i64, i64, ci, ci, vp]
             L.im2win_expert_route_backward.argtypes = [vp, vp, vp, vp, i64, i64, i64, ci, ci, vp]
+            L.im2win_expert_ffn_size.argtypes = [ci] + [i64] * 5 + [ci, ctypes.POINTER(sz)]
+            L.im2win_expert_ffn.argtypes = [vp] * 9 + [sz] + [i64] * 5 + [ci, ci, vp]
+            L.im2win_expert_ffn_backward.argtypes = [vp] * 12 + [sz] + [i64] * 5 + [ci, ci, vp]
             for f in EXPORTS:
                 if f != "im2win_status_string":
                     getattr(L, f).restype = ci

@@ -1,0 +1,293 @@
+// Gated feed-forward grouped by expert: argument checks, buffers and the sequence of launches.
+//
+//   plan, gather   rows to their experts: xs
+//   gated          h = act(xs w_gate_e^T) * (xs w_up_e^T)
+//   down           ys = h w_down_e^T
+//   combine        y = sum over a row's choices of weight * ys
+// backward
+//   gather         dys = weight * dy, dweights = dy . ys
+//   dgated         dh = dys w_down_e, made into dg, du
+//   dx             dxs = dg w_gate_e + du w_up_e, summed over a row's choices
+//   dw             dw_gate_e = dg^T xs, dw_up_e = du^T xs, dw_down_e = dys^T h over the expert's rows
+//
+// The products are the gated feed-forward's kernels with the rows in groups. Between the kernels xs, h,
+// ys, dys, dg, du and dxs are in the dtype (fp32: as three bf16 planes where they are operands):
+// in fp32 they would double the bytes of everything but the weights, and the products read 16 bits.
+#include <algorithm>
+#include <initializer_list>
+
+#include "expert_ffn.cuh"
+
+using namespace im2win;
+using namespace im2win::ffn;
+
+namespace {
+
+im2win_status check_dims(int64_t T, int64_t k, int64_t E, int64_t C, int64_t F, int dtype) {
+    if (T < 0 || k < 1 || E < 1 || C < 1 || F < 1 || elem_size(dtype) == 0) return IM2WIN_ERR_INVALID_ARG;
+    const int64_t most = 0x7fffffff - 1023, area = int64_t(1) << 40;
+    if (k > MAX_CHOICES || E > MAX_EXPERTS || T > most / k - 64 * E || C > most / E || F > most / E || C > area / F / E)
+        return IM2WIN_ERR_UNSUPPORTED;
+    const int64_t rows = grouped_rows(T * k, E);
+    return rows > area / C || rows > area / F ? IM2WIN_ERR_UNSUPPORTED : IM2WIN_OK;
+}
+
+bool known_act(int act) {
+    return with_act(act, [](auto) {});
+}
+
+// Byte offsets of the parts of a buffer, each on a 256-byte boundary.
+struct Parts {
+    size_t end;
+    explicit Parts(size_t begin) : end(begin) {}
+    size_t add(size_t bytes) {
+        const size_t at = end;
+        end += round_up(bytes, 256);
+        return at;
+    }
+};
+
+struct Problem {
+    int64_t T, rows, pairs;
+    int k, E, C, F, dtype, act;
+    bool f32;
+    int64_t Cp, Fp;  // pitches of grouped rows and of copied weights
+    Problem(int64_t T_, int64_t k_, int64_t E_, int64_t C_, int64_t F_, int act_, int dtype_)
+        : T(T_), rows(grouped_rows(T_ * k_, E_)), pairs(T_ * k_), k((int)k_), E((int)E_), C((int)C_), F((int)F_), dtype(dtype_),
+          act(act_), f32(dtype_ == IM2WIN_F32), Cp((C_ + 7) / 8 * 8), Fp((F_ + 7) / 8 * 8) {}
+
+    size_t operand(int64_t n, int64_t pitch) const { return (size_t)(n * pitch) * (f32 ? 6 : 2); }
+    size_t result() const { return (size_t)(rows * Cp) * (f32 ? 4 : 2); }  // ys, dxs
+    bool copies(int64_t cols) const { return f32 || cols % 8 != 0; }
+
+    Operand rows_c(const void *p, bool k_major) const { return {p, Cp, k_major, rows * Cp}; }
+    Operand rows_f(const void *p, bool k_major) const { return {p, Fp, k_major, rows * Fp}; }
+    // the experts' matrices; the planes of copies of fp32 ones lie behind all of them
+    Operand w_in(const void *p, bool k_major) const { return {p, Cp, k_major, (int64_t)E * F * Cp}; }
+    Operand w_out(const void *p, bool k_major) const { return {p, Fp, k_major, (int64_t)E * C * Fp}; }
+
+    Product product(int M, int N, int K, const int32_t *begin, const int32_t *count) const {
+        Product p;
+        p.M = M; p.N = N; p.K = K;
+        p.act = act;
+        p.groups = {begin, count, E};
+        p.rows = (double)pairs;
+        return p;
+    }
+};
+
+struct SavedParts {
+    size_t begin, count, slot, pair, xs, h, kept, ys, bytes;
+    // kept: what the backward pass alone needs
+    SavedParts(const Problem &q, size_t from, bool keep) {
+        Parts p(from);
+        begin = p.add((size_t)(q.E + 1) * 4);
+        count = p.add((size_t)q.E * 4);
+        slot = p.add((size_t)q.pairs * 4);
+        pair = p.add((size_t)q.rows * 4);
+        xs = p.add(q.operand(q.rows, q.Cp));
+        h = p.add(q.operand(q.rows, q.Fp));
+        kept = p.add(keep ? kept_bytes(q.rows, q.F, q.f32) : 0);
+        ys = p.add(q.result());
+        bytes = p.end;
+    }
+};
+
+// A forward call's workspace; without `saved`, its parts too.
+struct ForwardParts {
+    size_t hist, wg, wu, wd, own, bytes;
+    ForwardParts(const Problem &q, bool saved) {
+        Parts p(kStatusBytes);
+        const int64_t per = pairs_per_block(q.pairs), blocks = (q.pairs + per - 1) / per;
+        hist = p.add(blocks > 1 ? (size_t)blocks * q.E * 4 : 0);
+        wg = p.add(q.copies(q.C) ? q.operand((int64_t)q.E * q.F, q.Cp) : 0);
+        wu = p.add(q.copies(q.C) ? q.operand((int64_t)q.E * q.F, q.Cp) : 0);
+        wd = p.add(q.copies(q.F) ? q.operand((int64_t)q.E * q.C, q.Fp) : 0);
+        own = p.end;
+        bytes = saved ? own : SavedParts(q, own, false).bytes;
+    }
+};
+
+struct BackwardParts {
+    size_t dys, dg, du, dxs, wg, wu, wd, bytes;
+    explicit BackwardParts(const Problem &q) {
+        Parts p(kStatusBytes);
+        dys = p.add(q.operand(q.rows, q.Cp));
+        dg = p.add(q.operand(q.rows, q.Fp));
+        du = p.add(q.operand(q.rows, q.Fp));
+        dxs = p.add(q.result());
+        wg = p.add(q.copies(q.C) ? q.operand((int64_t)q.E * q.F, q.Cp) : 0);
+        wu = p.add(q.copies(q.C) ? q.operand((int64_t)q.E * q.F, q.Cp) : 0);
+        wd = p.add(q.copies(q.F) ? q.operand((int64_t)q.E * q.C, q.Fp) : 0);
+        bytes = p.end;
+    }
+};
+
+unsigned char *at(void *base, size_t off) { return static_cast<unsigned char *>(base) + off; }
+int32_t *ints(void *base, size_t off) { return reinterpret_cast<int32_t *>(at(base, off)); }
+
+Rows rows_of(const Problem &q, const SavedParts &s, void *saved) {
+    return {q.T, q.rows, q.k, q.E, q.C, q.Cp, {ints(saved, s.begin), ints(saved, s.count), ints(saved, s.slot), ints(saved, s.pair)}};
+}
+
+// The launches of one call, up to the first that fails.
+struct Sequence {
+    const Problem &q;
+    void *ws;
+    cudaStream_t st;
+    cudaError_t e = cudaSuccess;
+    Repitch copies[3];
+    int n_copies = 0;
+
+    const void *readable(const void *src, int rows, int cols, size_t to) {
+        if (!q.copies(cols)) return src;
+        copies[n_copies++] = {src, at(ws, to), rows, cols};
+        return at(ws, to);
+    }
+    template <typename Fn>
+    void step(Fn f) {
+        if (e == cudaSuccess) e = f();
+    }
+    void copy() {
+        if (n_copies) step([&] { return launch_repitch(copies, n_copies, q.f32, st); });
+    }
+    void run(const Product &p) {
+        uint32_t *status = static_cast<uint32_t *>(ws);
+        step([&] {
+            return q.f32 ? launch_f32(p, status, false, nullptr, st) : launch_tc(p, q.dtype == IM2WIN_BF16, status, false, nullptr, st);
+        });
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+im2win_status im2win_expert_ffn_size(int buffer, int64_t T, int64_t k, int64_t E, int64_t C, int64_t F, int dtype,
+                                     size_t *bytes) {
+    if (!bytes) return IM2WIN_ERR_INVALID_ARG;
+    const im2win_status s = check_dims(T, k, E, C, F, dtype);
+    if (s != IM2WIN_OK) return s;
+    const Problem q(T, k, E, C, F, 0, dtype);
+    switch (buffer) {
+        case IM2WIN_FFN_FORWARD: *bytes = ForwardParts(q, false).bytes; return IM2WIN_OK;
+        case IM2WIN_FFN_TRAIN: *bytes = ForwardParts(q, true).bytes; return IM2WIN_OK;
+        case IM2WIN_FFN_BACKWARD: *bytes = BackwardParts(q).bytes; return IM2WIN_OK;
+        case IM2WIN_FFN_SAVED: *bytes = SavedParts(q, 0, true).bytes; return IM2WIN_OK;
+        default: return IM2WIN_ERR_INVALID_ARG;
+    }
+}
+
+im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const void *weights, const void *w_gate,
+                                const void *w_up, const void *w_down, void *y, void *saved, void *ws, size_t ws_bytes,
+                                int64_t T, int64_t k, int64_t E, int64_t C, int64_t F, int act, int dtype, void *stream) {
+    const im2win_status s = check_dims(T, k, E, C, F, dtype);
+    if (s != IM2WIN_OK) return s;
+    if (!known_act(act)) return IM2WIN_ERR_INVALID_ARG;
+    if (T == 0) return IM2WIN_OK;  // no rows: nothing to read or write
+    if (!x || !experts || !weights || !w_gate || !w_up || !w_down || !y) return IM2WIN_ERR_INVALID_ARG;
+    for (const void *p : {x, (const void *)experts, weights, w_gate, w_up, w_down, (const void *)y, (const void *)saved,
+                          (const void *)ws})
+        if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
+    const Problem q(T, k, E, C, F, act, dtype);
+    const ForwardParts parts(q, saved != nullptr);
+    if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
+    const SavedParts own(q, saved ? 0 : parts.own, saved != nullptr);
+    void *keep = saved ? saved : ws;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Rows rows = rows_of(q, own, keep);
+    Sequence seq{q, ws, st};
+    seq.step([&] { return launch_plan(rows, experts, ints(ws, parts.hist), static_cast<uint32_t *>(ws), st); });
+    w_gate = seq.readable(w_gate, q.E * q.F, q.C, parts.wg);
+    w_up = seq.readable(w_up, q.E * q.F, q.C, parts.wu);
+    w_down = seq.readable(w_down, q.E * q.C, q.F, parts.wd);
+    seq.copy();
+    seq.step([&] { return launch_gather(rows, x, at(keep, own.xs), dtype, st); });
+
+    Product gated = q.product((int)q.rows, q.F, q.C, rows.plan.begin, rows.plan.count);
+    gated.a0 = q.rows_c(at(keep, own.xs), true);
+    gated.b0 = q.w_in(w_gate, true), gated.b1 = q.w_in(w_up, true);
+    gated.epi = EPI_GATED;
+    gated.out = at(keep, own.h), gated.ldo = q.Fp, gated.plane = q.rows * q.Fp;
+    gated.kept = saved ? at(keep, own.kept) : nullptr;
+    seq.run(gated);
+
+    Product down = q.product((int)q.rows, q.C, q.F, rows.plan.begin, rows.plan.count);
+    down.a0 = q.rows_f(at(keep, own.h), true), down.b0 = q.w_out(w_down, true);
+    down.out = at(keep, own.ys), down.ldo = q.Cp;
+    seq.run(down);
+    seq.step([&] { return launch_combine(rows, at(keep, own.ys), weights, y, dtype, st); });
+    return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+}
+
+im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, const void *w_gate, const void *w_up,
+                                         const void *w_down, const void *saved, void *dx, void *dweights,
+                                         void *dw_gate, void *dw_up, void *dw_down, void *ws, size_t ws_bytes,
+                                         int64_t T, int64_t k, int64_t E, int64_t C, int64_t F, int act, int dtype,
+                                         void *stream) {
+    const im2win_status s = check_dims(T, k, E, C, F, dtype);
+    if (s != IM2WIN_OK) return s;
+    if (!known_act(act)) return IM2WIN_ERR_INVALID_ARG;
+    const bool want_dw = dw_gate != nullptr;
+    if ((dw_up != nullptr) != want_dw || (dw_down != nullptr) != want_dw) return IM2WIN_ERR_INVALID_ARG;
+    if (T > 0 && (!dy || !weights || !w_gate || !w_up || !w_down || !saved)) return IM2WIN_ERR_INVALID_ARG;
+    for (const void *p : {dy, weights, w_gate, w_up, w_down, saved, (const void *)dx, (const void *)dweights,
+                          (const void *)dw_gate, (const void *)dw_up, (const void *)dw_down, (const void *)ws})
+        if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {  // sums over no rows
+        cudaError_t e = cudaSuccess;
+        for (void *w : {dw_gate, dw_up, dw_down})
+            if (w && e == cudaSuccess) e = cudaMemsetAsync(w, 0, (size_t)(E * C * F) * elem_size(dtype), st);
+        return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+    }
+    if (!dx && !dweights && !want_dw) return IM2WIN_OK;
+    const Problem q(T, k, E, C, F, act, dtype);
+    const BackwardParts parts(q);
+    if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
+    const SavedParts own(q, 0, true);
+    void *keep = const_cast<void *>(saved);
+    const Rows rows = rows_of(q, own, keep);
+    Sequence seq{q, ws, st};
+    void *dys = at(ws, parts.dys), *dg = at(ws, parts.dg), *du = at(ws, parts.du);
+    seq.step([&] {
+        return launch_gather_back(rows, dy, weights, at(keep, own.ys), dys, dweights, static_cast<uint32_t *>(ws), dtype, st);
+    });
+    if (dx || want_dw) {
+        w_down = seq.readable(w_down, q.E * q.C, q.F, parts.wd);
+        if (dx) {
+            w_gate = seq.readable(w_gate, q.E * q.F, q.C, parts.wg);
+            w_up = seq.readable(w_up, q.E * q.F, q.C, parts.wu);
+        }
+        seq.copy();
+        Product d = q.product((int)q.rows, q.F, q.C, rows.plan.begin, rows.plan.count);
+        d.a0 = q.rows_c(dys, true), d.b0 = q.w_out(w_down, false);
+        d.epi = EPI_DGATED;
+        d.out = dg, d.out2 = du, d.ldo = q.Fp, d.plane = q.rows * q.Fp;
+        d.kept = at(keep, own.kept);
+        seq.run(d);
+    }
+    if (dx) {
+        Product d = q.product((int)q.rows, q.C, q.F, rows.plan.begin, rows.plan.count);
+        d.a0 = q.rows_f(dg, true), d.b0 = q.w_in(w_gate, false);
+        d.a1 = q.rows_f(du, true), d.b1 = q.w_in(w_up, false);
+        d.out = at(ws, parts.dxs), d.ldo = q.Cp;
+        seq.run(d);
+        seq.step([&] { return launch_combine(rows, at(ws, parts.dxs), nullptr, dx, dtype, st); });
+    }
+    if (want_dw) {
+        Product in = q.product(q.F, q.C, (int)q.rows, rows.plan.begin, rows.plan.count);
+        in.a0 = q.rows_f(dg, false), in.a1 = q.rows_f(du, false);
+        in.b0 = in.b1 = q.rows_c(at(keep, own.xs), false);
+        in.batch = true;
+        in.out = dw_gate, in.out2 = dw_up, in.ldo = q.C;
+        seq.run(in);
+        Product out = q.product(q.C, q.F, (int)q.rows, rows.plan.begin, rows.plan.count);
+        out.a0 = q.rows_c(dys, false), out.b0 = q.rows_f(at(keep, own.h), false);
+        out.out = dw_down, out.ldo = q.F;
+        seq.run(out);
+    }
+    return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -46,6 +46,8 @@ struct F32Params {
     int64_t part_ld, part_step;
     int first;
     uint32_t *status;
+    Groups groups;
+    int table_at, rows_bound;
 };
 
 // 16 columns of a row of whole 16-byte vectors in fp32, `n` columns from here on (a multiple of 4).
@@ -120,11 +122,12 @@ __device__ __forceinline__ void gate4(int act, F2 *g, F2 *u, F2 *h) {
 }
 __device__ __forceinline__ ulonglong2 words(const F2 *v) { return make_ulonglong2(v[0].v, v[1].v); }
 
-// N (a multiple of 8) columns of row m from column n on, from their sums v (GATED: g, and u).
+// N (a multiple of 8) columns of row m (below m_end) from column n on, from their sums v (GATED: g,
+// and u); none: the row's outputs are zero.
 template <int EPI, int N>
-__device__ __forceinline__ void finish(const F32Params &p, F2 *v, F2 *u, int z, int m, int n) {
+__device__ __forceinline__ void finish(const F32Params &p, F2 *v, F2 *u, int m, int n, int m_end, bool none = false) {
     const int left = p.N - n;
-    if (m >= p.M || left <= 0) return;
+    if (m >= m_end || left <= 0) return;
     const int64_t at = (int64_t)m * p.ldo + n;
     if (EPI == EPI_STORE) return;  // (store_f32)
     float *kept_a = p.kept, *kept_b = p.kept + kept_count_f32(p.M, p.N);
@@ -153,12 +156,16 @@ __device__ __forceinline__ void finish(const F32Params &p, F2 *v, F2 *u, int z, 
                 first[2 * j] = first[2 * j + 1] = second[2 * j] = second[2 * j + 1] = f2(0.0f);
             }
         }
+        if (none) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) first[j] = second[j] = f2(0.0f);
+        }
         store_planes8(static_cast<uint16_t *>(p.out) + at + 8 * i, p.plane, first, left - 8 * i);
         if (EPI == EPI_DGATED) store_planes8(static_cast<uint16_t *>(p.out2) + at + 8 * i, p.plane, second, left - 8 * i);
     }
 }
 
-template <bool AK, bool BKM, int EPI>
+template <bool AK, bool BKM, int EPI, bool GROUPED>
 __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant__ F32Params p) {
     extern __shared__ unsigned char dyn[];
     __shared__ uint32_t tmem_slot;
@@ -192,7 +199,15 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
     const uint32_t tmem = tmem_slot;  // buffer i: the sums of h h' at 2 i BN, the others' BN further
     if (p.first && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
 
-    Walk walk(p, blockIdx.x, gridDim.x);
+    const GroupTable table = group_table(dyn + p.table_at, p.groups.E);
+    if (GROUPED) {  // (as in the 16-bit kernel)
+        if (warp == 3) fill_group_table(table, p.groups, p.rows_bound, ROWS, p.tiles_n, lane);
+        __syncthreads();
+    }
+    auto walk = [&] {
+        if constexpr (GROUPED) return GroupWalk<!AK>(p, table, ROWS, blockIdx.x, gridDim.x);
+        else return Walk(p, blockIdx.x, gridDim.x);
+    }();
     Work w;
     if (warp == 0 && lane == 0) {
         // ---- copies
@@ -201,9 +216,9 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
         bool ok = true;
         const uint32_t a_bytes = AK ? p.a_rows * BK * 2 : (p.a_rows + 63) / 64 * 64 * BK * 2;
         while (ok && walk.next(w)) {
-            const int m0 = w.tm * ROWS;
+            const int m0 = w.tm * ROWS + (GROUPED && AK ? w.row0 : 0);
             for (int kb = w.k0; ok && kb < w.k1; ++kb) {
-                const int seg = kb >= p.KB ? 1 : 0, k = (kb - seg * p.KB) * BK;
+                const int seg = kb >= p.KB ? 1 : 0, k = (kb - seg * p.KB) * BK + (GROUPED && !AK ? w.row0 : 0);
 #pragma unroll 1
                 for (int q = 0; q < PLANES; ++q) {
                     if (!(ok = bar_wait(empty + 8 * s, phase ^ 1, ctl, SITE_STAGE_EMPTY))) break;
@@ -217,7 +232,19 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
                     } else {
                         for (int i = 0; i < p.a_rows; i += 64) tma_2d<1>(sa + i * BK * 2, ma, m0 + i, k, bar);
                     }
-                    if (EPI == EPI_GATED) {  // gate rows, then up rows of the same hidden channels
+                    if (GROUPED && EPI == EPI_GATED) {
+                        tma_3d<1>(sb, &p.b[0][q], k, w.tn * (BN / 2), w.e, bar);
+                        tma_3d<1>(sb + B_BYTES / 2, &p.b[1][q], k, w.tn * (BN / 2), w.e, bar);
+                    } else if (GROUPED && AK) {
+                        if (BKM) {
+                            tma_3d<1>(sb, mb, k, w.tn * BN, w.e, bar);
+                        } else if (p.b_blocks) {
+                            tma_4d<1>(sb, mb, 0, k, w.tn * (BN / 64), w.e, bar);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < BN; i += 64) tma_3d<1>(sb + i * BK * 2, mb, w.tn * BN + i, k, w.e, bar);
+                        }
+                    } else if (EPI == EPI_GATED) {  // gate rows, then up rows of the same hidden channels
                         tma_2d<1>(sb, &p.b[0][q], k, w.tn * (BN / 2), bar);
                         tma_2d<1>(sb + B_BYTES / 2, &p.b[1][q], k, w.tn * (BN / 2), bar);
                     } else if (BKM) {
@@ -316,8 +343,10 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
                 }
             }
             if (!ok) break;
-            const int m = w.tm * ROWS + q * 32 + lane;
-            if (p.part) {
+            const int m = w.tm * ROWS + q * 32 + lane + (GROUPED && AK ? w.row0 : 0);
+            const int m_end = !GROUPED || !AK ? p.M : EPI == EPI_STORE ? w.row_end : w.pad_end;
+            const bool none = GROUPED && AK && m >= w.row_end;
+            if (!GROUPED && p.part) {
                 float *dst = p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
                 if (m < p.M) {
                     store_f32(dst + c0, sum[0], CHUNK);
@@ -325,18 +354,19 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
                 }
             } else if (EPI == EPI_STORE) {
                 float *out = static_cast<float *>(w.z ? p.out2 : p.out);
+                if (GROUPED && !AK) out += (int64_t)w.e * p.M * p.ldo;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int n = w.tn * BN + c0 + half * CHUNK;
                     if (n >= p.N) break;
-                    if (!p.vec) store_f32_staged(out + (int64_t)(m - lane) * p.ldo + n, p.ldo, sum[half], p.M - (m - lane), p.N - n, stage);
-                    else if (m < p.M) store_f32(out + (int64_t)m * p.ldo + n, sum[half], p.N - n);
+                    if (!p.vec) store_f32_staged(out + (int64_t)(m - lane) * p.ldo + n, p.ldo, sum[half], m_end - (m - lane), p.N - n, stage);
+                    else if (m < m_end) store_f32(out + (int64_t)m * p.ldo + n, sum[half], p.N - n);
                 }
             } else if (EPI == EPI_GATED) {
-                finish<EPI, CHUNK>(p, sum[0], sum[1], w.z, m, w.tn * (BN / 2) + c0);
+                finish<EPI, CHUNK>(p, sum[0], sum[1], m, w.tn * (BN / 2) + c0, m_end, none);
             } else {
-                finish<EPI, CHUNK>(p, sum[0], nullptr, w.z, m, w.tn * BN + c0);
-                finish<EPI, CHUNK>(p, sum[1], nullptr, w.z, m, w.tn * BN + c1);
+                finish<EPI, CHUNK>(p, sum[0], nullptr, m, w.tn * BN + c0, m_end, none);
+                finish<EPI, CHUNK>(p, sum[1], nullptr, m, w.tn * BN + c1, m_end, none);
             }
         }
     }
@@ -372,25 +402,39 @@ __global__ void __launch_bounds__(256) f32_join(const __grid_constant__ F32Param
             }
         }
     } else {
-        finish<EPI, 8>(p, v, u, z, m, n);
+        finish<EPI, 8>(p, v, u, m, n, p.M);
     }
 }
 
-template <bool AK, bool BKM, int EPI>
-cudaError_t launch_kind(const F32Params &p, const TcPlan &pl, cudaStream_t st) {
-    auto kernel = f32_product<AK, BKM, EPI>;
-    const int smem = EPI == EPI_STORE && !p.vec && !p.part ? SMEM_STAGED : SMEM;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_STAGED);
+template <bool AK, bool BKM, int EPI, bool GROUPED>
+cudaError_t launch_kind(F32Params &p, const TcPlan &pl, cudaStream_t st) {
+    auto kernel = f32_product<AK, BKM, EPI, GROUPED>;
+    p.table_at = EPI == EPI_STORE && !p.vec && !p.part ? SMEM_STAGED : SMEM;
+    const int smem = p.table_at + (GROUPED ? group_table_bytes(p.groups.E) : 0);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         SMEM_STAGED + (GROUPED ? group_table_bytes(MAX_EXPERTS) : 0));
     if (e != cudaSuccess) return e;
     e = launch_with(kernel, pl.units, THREADS, smem, 1, st, p);
     if (e != cudaSuccess || !p.part) return e;
     return launch_with(f32_join<EPI>, join_blocks(p), 256, 0, 1, st, p, pl.units);
 }
 
+template <bool GROUPED>
+cudaError_t launch_any(F32Params &p, const TcPlan &pl, const Product &d, cudaStream_t st) {
+    if (d.epi == EPI_GATED) return launch_kind<true, true, EPI_GATED, GROUPED>(p, pl, st);
+    if (d.epi == EPI_DGATED) return launch_kind<true, false, EPI_DGATED, GROUPED>(p, pl, st);
+    if (!d.a0.k_major) return launch_kind<false, false, EPI_STORE, GROUPED>(p, pl, st);
+    if (d.b0.k_major) return launch_kind<true, true, EPI_STORE, GROUPED>(p, pl, st);
+    return launch_kind<true, false, EPI_STORE, GROUPED>(p, pl, st);
+}
+
 }  // namespace
 
 // A K block is 24 MMAs of 64 clocks.
-TcPlan plan_f32(const Product &d) { return plan_tiles(d, 1, BN, 0.95, d.epi == EPI_STORE ? 1 : 3); }
+TcPlan plan_f32(const Product &d) {
+    const double epi = d.epi == EPI_STORE ? 1 : 3;
+    return d.groups.E ? plan_groups(d, 1, BN, 0.95, epi) : plan_tiles(d, 1, BN, 0.95, epi);
+}
 
 cudaError_t launch_f32(const Product &d, uint32_t *status, bool first, void *part, cudaStream_t st) {
     const TcPlan pl = plan_f32(d);
@@ -400,15 +444,19 @@ cudaError_t launch_f32(const Product &d, uint32_t *status, bool first, void *par
     p.segs = d.epi != EPI_GATED && two && !d.batch ? 2 : 1;
     p.batch = d.batch ? 2 : 1;
     p.tiles_m = pl.tiles_m; p.tiles_n = pl.tiles_n; p.tiles = p.batch * pl.tiles_m * pl.tiles_n;
+    p.groups = d.groups;
+    p.rows_bound = d.a0.k_major ? d.M : d.K;
+    const int stack = d.a0.k_major ? d.groups.E : 0;
+    if (d.groups.E && !d.a0.k_major) p.tiles *= d.groups.E;
     p.a_rows = std::min(ROWS, (d.M + 7) / 8 * 8);
     p.a_blocks = !d.a0.k_major && d.M % 64 == 0;
     p.b_blocks = !d.b0.k_major && d.N % 64 == 0;
     const int b_box = d.epi == EPI_GATED ? BN / 2 : BN;
     for (int q = 0; q < PLANES; ++q) {
         if (!encode(p.a[0][q], d.a0, q, d.M, d.K, p.a_rows, p.a_blocks) ||
-            !encode(p.b[0][q], d.b0, q, d.N, d.K, b_box, p.b_blocks) ||
+            !encode(p.b[0][q], d.b0, q, d.N, d.K, b_box, p.b_blocks, stack) ||
             (two && !encode(p.a[1][q], d.a1, q, d.M, d.K, p.a_rows, p.a_blocks)) ||
-            (d.b1.p && !encode(p.b[1][q], d.b1, q, d.N, d.K, b_box, p.b_blocks)))
+            (d.b1.p && !encode(p.b[1][q], d.b1, q, d.N, d.K, b_box, p.b_blocks, stack)))
             return cudaErrorInvalidValue;
     }
     p.act = d.act;
@@ -422,11 +470,7 @@ cudaError_t launch_f32(const Product &d, uint32_t *status, bool first, void *par
     }
     p.status = status;
     p.first = first;
-    if (d.epi == EPI_GATED) return launch_kind<true, true, EPI_GATED>(p, pl, st);
-    if (d.epi == EPI_DGATED) return launch_kind<true, false, EPI_DGATED>(p, pl, st);
-    if (!d.a0.k_major) return launch_kind<false, false, EPI_STORE>(p, pl, st);
-    if (d.b0.k_major) return launch_kind<true, true, EPI_STORE>(p, pl, st);
-    return launch_kind<true, false, EPI_STORE>(p, pl, st);
+    return d.groups.E ? launch_any<true>(p, pl, d, st) : launch_any<false>(p, pl, d, st);
 }
 
 }  // namespace ffn

@@ -58,6 +58,8 @@ struct TcParams {
     int64_t part_ld, part_step;  // row pitch and distance between contributions, in floats
     int first;                 // the call's first launch: clears the status
     uint32_t *status;
+    Groups groups;
+    int table_at, rows_bound;  // where the groups lie in shared memory; rows of the grouped buffers
 };
 
 // Eight kept values: their upper halves and the bytes after them.
@@ -99,10 +101,10 @@ __device__ __forceinline__ void keep_columns(unsigned char *at, const F2 *a, con
 struct KeptChunk {
     uint4 v[2][3];
 };
-__device__ __forceinline__ void fetch_kept(const TcParams &p, KeptChunk &k, int m, int n) {
+__device__ __forceinline__ void fetch_kept(const TcParams &p, KeptChunk &k, int m, int m_end, int n) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (m >= p.M || n + 8 * i >= p.N) continue;
+        if (m >= m_end || n + 8 * i >= p.N) continue;
         const unsigned char *at = p.kept + kept_block(m, n + 8 * i, p.N);
 #pragma unroll
         for (int j = 0; j < 3; ++j) k.v[i][j] = *reinterpret_cast<const uint4 *>(at + 512 * j);
@@ -110,19 +112,19 @@ __device__ __forceinline__ void fetch_kept(const TcParams &p, KeptChunk &k, int 
 }
 
 // Outputs of a chunk of rows m0 + lane from their accumulator values v (and u, or kept), columns
-// from n; every lane of the warp is here.
+// from n; every lane of the warp is here. Rows end at m_end.
 template <int EPI>
 __device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[PAIRS], F2 (&u)[PAIRS], const KeptChunk &k, int m0,
-                                             int n, uint16_t *out, uint32_t *stage) {
+                                             int n, int m_end, uint16_t *out, uint32_t *stage) {
     const int m = m0 + (threadIdx.x & 31);
     if (n >= p.N) return;
     const int64_t at = (int64_t)m * p.ldo + n;
     if (EPI == EPI_STORE) {
-        if (p.vec == 2) store_rows_staged(out + (int64_t)m0 * p.ldo + n, p.ldo, v, min(32, p.M - m0), p.N - n, p.bf16, stage);
-        else if (m < p.M) store_row(out + at, v, p.N - n, p.vec, p.bf16);
+        if (p.vec == 2) store_rows_staged(out + (int64_t)m0 * p.ldo + n, p.ldo, v, min(32, m_end - m0), p.N - n, p.bf16, stage);
+        else if (m < m_end) store_row(out + at, v, p.N - n, p.vec, p.bf16);
         return;
     }
-    if (m >= p.M) return;
+    if (m >= m_end) return;
     const int left = (int)(p.ldo - n);  // own buffers: whole vectors, whose last may pass N
     if (EPI == EPI_GATED) {
         F2 a[PAIRS];
@@ -152,7 +154,8 @@ __device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[PAIRS], 
     store_row(out + at, v, left, p.vec, p.bf16);
 }
 
-template <int CG, int BN, bool AK, bool BKM, int EPI>
+// GROUPED: rows of A by expert, each with its matrix of B (AK); or sums by expert of the rows (!AK).
+template <int CG, int BN, bool AK, bool BKM, int EPI, bool GROUPED>
 __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__ TcParams p) {
     using T = Tile<CG, BN>;
     extern __shared__ unsigned char dyn[];
@@ -201,10 +204,19 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
     const uint32_t tmem = tmem_slot;
     // (a wait of this launch gives up two seconds from now at the earliest, after this store)
     if (p.first && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
+    const GroupTable table = group_table(dyn + p.table_at, p.groups.E);
+    if (GROUPED) {
+        if (warp == 3) fill_group_table(table, p.groups, p.rows_bound, T::M, p.tiles_n, lane);
+        __syncthreads();
+    }
+    auto begin_walk = [&] {
+        if constexpr (GROUPED) return GroupWalk<!AK>(p, table, T::M, unit, units);
+        else return Walk(p, unit, units);
+    };
 
     if (warp == 0 && lane == 0) {
         // ---- copies
-        Walk walk(p, unit, units);
+        auto walk = begin_walk();
         Work w;
         int s = 0;
         uint32_t phase = 0;
@@ -213,13 +225,13 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
         const uint32_t a_bytes = AK ? p.a_rows * BK * 2 : (p.a_rows + 63) / 64 * 64 * BK * 2;
         const uint32_t bytes = CG * (a_bytes + T::B_BYTES);
         while (ok && walk.next(w)) {
-            const int m0 = w.tm * T::M + (int)rank * ROWS;
+            const int m0 = w.tm * T::M + (int)rank * ROWS + (GROUPED && AK ? w.row0 : 0);
             for (int kb = w.k0; kb < w.k1; ++kb) {
                 if (!(ok = bar_wait(empty + 8 * s, phase ^ 1, ctl, SITE_STAGE_EMPTY))) break;
                 const uint32_t sa = base + s * T::STAGE, sb = sa + T::A_BYTES;
                 const uint32_t bar = CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
                 if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
-                const int seg = kb >= p.KB ? 1 : 0, k = (kb - seg * p.KB) * BK;
+                const int seg = kb >= p.KB ? 1 : 0, k = (kb - seg * p.KB) * BK + (GROUPED && !AK ? w.row0 : 0);
                 const CUtensorMap *ma = &p.a[seg | w.z], *mb = &p.b[seg | w.z];
                 if (AK) {
                     tma_2d<CG>(sa, ma, k, m0, bar);
@@ -230,7 +242,10 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                 }
                 if (EPI == EPI_GATED) {  // gate rows, then up rows of the same hidden channels
                     const int n0 = w.tn * (BN / 2);
-                    if (CG == 2) {
+                    if (GROUPED) {
+                        tma_3d<CG>(sb, &p.b[CG == 2 ? rank : 0], k, n0, w.e, bar);
+                        if (CG == 1) tma_3d<CG>(sb + b_box * BK * 2, &p.b[1], k, n0, w.e, bar);
+                    } else if (CG == 2) {
                         tma_2d<CG>(sb, &p.b[rank], k, n0, bar);
                     } else {
                         tma_2d<CG>(sb, &p.b[0], k, n0, bar);
@@ -238,7 +253,16 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                     }
                 } else {
                     const int n0 = w.tn * BN + (int)rank * T::B_ROWS;
-                    if (BKM) {
+                    if (GROUPED && AK) {
+                        if (BKM) {
+                            tma_3d<CG>(sb, mb, k, n0, w.e, bar);
+                        } else if (p.b_blocks) {
+                            tma_4d<CG>(sb, mb, 0, k, n0 / 64, w.e, bar);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < T::B_ROWS; i += 64) tma_3d<CG>(sb + i * BK * 2, mb, n0 + i, k, w.e, bar);
+                        }
+                    } else if (BKM) {
                         tma_2d<CG>(sb, mb, k, n0, bar);
                     } else if (p.b_blocks) {
                         tma_3d<CG>(sb, mb, 0, k, n0 / 64, bar);
@@ -254,7 +278,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
         if (!ok) let_end();
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---- MMAs
-        Walk walk(p, unit, units);
+        auto walk = begin_walk();
         Work w;
         int s = 0, n_tile = 0;
         uint32_t phase = 0;
@@ -287,7 +311,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
         if (!ok) let_end();
     } else if (warp >= 4) {
         // ---- outputs: a warp for 32 rows and a share of the columns
-        Walk walk(p, unit, units);
+        auto walk = begin_walk();
         Work w;
         int n_tile = 0;
         const int q = warp & 3, share = (warp - 4) >> 2;
@@ -297,11 +321,13 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
         uint32_t *stage = reinterpret_cast<uint32_t *>(dyn + T::STAGES * T::STAGE + 1024) + (warp - 4) * STAGED_WORDS;
         while (walk.next(w)) {
             const int buf = n_tile & 1;
-            const int m = w.tm * T::M + (int)rank * ROWS + q * 32 + lane;
+            const int m = w.tm * T::M + (int)rank * ROWS + q * 32 + lane + (GROUPED && AK ? w.row0 : 0);
+            // (the padding of rows that will be summed over is stored too)
+            const int m_end = !GROUPED || !AK ? p.M : EPI == EPI_STORE ? w.row_end : w.pad_end;
             constexpr int SPAN = COLS / SHARES;  // output columns of the warp
             // what was kept of a chunk is on its way before the chunk's sums are looked at
             KeptChunk kept;
-            if (EPI == EPI_DGATED && !p.part) fetch_kept(p, kept, m, w.tn * COLS + share * SPAN);
+            if (EPI == EPI_DGATED && !p.part) fetch_kept(p, kept, m, m_end, w.tn * COLS + share * SPAN);
             if (!warp_bar_wait(acc_full + 8 * buf, (n_tile >> 1) & 1, ctl, SITE_ACC_FULL)) break;
             tc_fence_after();
             const uint32_t taddr = tmem + buf * BN + ((uint32_t)(q * 32) << 16);
@@ -330,6 +356,10 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                 }
             } else {
                 uint16_t *out = static_cast<uint16_t *>(w.z ? p.out2 : p.out);
+                if (GROUPED && !AK) out += (int64_t)w.e * p.M * p.ldo;
+                // nothing accumulates where an expert has no rows, and the padding's outputs are zero
+                // whatever the weights hold
+                const bool none = GROUPED && (AK ? EPI != EPI_STORE && m >= w.row_end : w.k1 == 0);
 #pragma unroll 1
                 for (int c = share * SPAN; c < (share + 1) * SPAN; c += CHUNK) {
                     uint32_t r[CHUNK], ru[CHUNK];
@@ -340,9 +370,14 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                     F2 v[PAIRS], u[PAIRS];
                     pairs_of(r, v);
                     if (EPI == EPI_GATED) pairs_of(ru, u);
-                    const KeptChunk now = kept;
-                    if (EPI == EPI_DGATED && c + CHUNK < (share + 1) * SPAN) fetch_kept(p, kept, m, w.tn * COLS + c + CHUNK);
-                    finish_chunk<EPI>(p, v, u, now, m - lane, w.tn * COLS + c, out, stage);
+                    if (GROUPED && none) {
+#pragma unroll
+                        for (int i = 0; i < PAIRS; ++i) v[i] = u[i] = f2(0.0f);
+                    }
+                    KeptChunk now = kept;
+                    if (GROUPED && none && EPI == EPI_DGATED) now = KeptChunk{};
+                    if (EPI == EPI_DGATED && c + CHUNK < (share + 1) * SPAN) fetch_kept(p, kept, m, m_end, w.tn * COLS + c + CHUNK);
+                    finish_chunk<EPI>(p, v, u, now, m - lane, w.tn * COLS + c, m_end, out, stage);
                 }
             }
             ++n_tile;
@@ -409,25 +444,27 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams 
     put(static_cast<uint16_t *>(z ? p.out2 : p.out) + at, v);
 }
 
-template <int CG, int BN, bool AK, bool BKM, int EPI>
-cudaError_t launch_shape(const TcParams &p, const TcPlan &pl, cudaStream_t st) {
+template <int CG, int BN, bool AK, bool BKM, int EPI, bool GROUPED>
+cudaError_t launch_shape(TcParams &p, const TcPlan &pl, cudaStream_t st) {
     using T = Tile<CG, BN>;
-    auto kernel = tc_product<CG, BN, AK, BKM, EPI>;
-    const int smem = EPI == EPI_STORE && p.vec == 2 && !p.part ? T::SMEM_STAGED : T::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_STAGED);
+    auto kernel = tc_product<CG, BN, AK, BKM, EPI, GROUPED>;
+    p.table_at = EPI == EPI_STORE && p.vec == 2 && !p.part ? T::SMEM_STAGED : T::SMEM;
+    const int smem = p.table_at + (GROUPED ? group_table_bytes(p.groups.E) : 0);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         T::SMEM_STAGED + (GROUPED ? group_table_bytes(MAX_EXPERTS) : 0));
     if (e != cudaSuccess) return e;
     e = launch_with(kernel, pl.units * CG, THREADS, smem, CG, st, p);
     if (e != cudaSuccess || !p.part) return e;
     return launch_with(tc_join<BN, EPI>, join_blocks(p), 256, 0, 1, st, p, T::M, pl.units);
 }
 
-template <int CG, int BN>
-cudaError_t launch_tile(const TcParams &p, const TcPlan &pl, const Product &d, cudaStream_t st) {
-    if (d.epi == EPI_GATED) return launch_shape<CG, BN, true, true, EPI_GATED>(p, pl, st);
-    if (d.epi == EPI_DGATED) return launch_shape<CG, BN, true, false, EPI_DGATED>(p, pl, st);
-    if (!d.a0.k_major) return launch_shape<CG, BN, false, false, EPI_STORE>(p, pl, st);
-    if (d.b0.k_major) return launch_shape<CG, BN, true, true, EPI_STORE>(p, pl, st);
-    return launch_shape<CG, BN, true, false, EPI_STORE>(p, pl, st);
+template <int CG, int BN, bool GROUPED>
+cudaError_t launch_tile(TcParams &p, const TcPlan &pl, const Product &d, cudaStream_t st) {
+    if (d.epi == EPI_GATED) return launch_shape<CG, BN, true, true, EPI_GATED, GROUPED>(p, pl, st);
+    if (d.epi == EPI_DGATED) return launch_shape<CG, BN, true, false, EPI_DGATED, GROUPED>(p, pl, st);
+    if (!d.a0.k_major) return launch_shape<CG, BN, false, false, EPI_STORE, GROUPED>(p, pl, st);
+    if (d.b0.k_major) return launch_shape<CG, BN, true, true, EPI_STORE, GROUPED>(p, pl, st);
+    return launch_shape<CG, BN, true, false, EPI_STORE, GROUPED>(p, pl, st);
 }
 
 }  // namespace
@@ -436,6 +473,10 @@ TcPlan plan_tc(const Product &d) {
     // A K block takes the same time in either shape (the pair's MMAs, four times as many; the
     // single CTA's shared-memory fill), outputs a little over half of it on the smaller tile.
     const double epi = d.epi == EPI_DGATED ? 4 : d.epi == EPI_GATED ? (d.kept ? 3 : 2.1) : 1.8;
+    if (d.groups.E) {
+        const TcPlan pair = plan_groups(d, 2, 256, 0.345, epi), single = plan_groups(d, 1, 128, 0.335, 0.55 * epi + 0.1);
+        return single.cost < pair.cost ? single : pair;
+    }
     const TcPlan pair = plan_tiles(d, 2, 256, 0.345, epi), single = plan_tiles(d, 1, 128, 0.335, 0.55 * epi + 0.1);
     return single.cost < pair.cost ? single : pair;
 }
@@ -447,15 +488,18 @@ cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool first,
     const bool two = d.a1.p != nullptr;
     p.segs = d.epi != EPI_GATED && two && !d.batch ? 2 : 1;
     p.batch = d.batch ? 2 : 1;
-    p.tiles_m = pl.tiles_m; p.tiles_n = pl.tiles_n; p.tiles = p.batch * pl.tiles_m * pl.tiles_n;
+    p.groups = d.groups;
+    p.rows_bound = d.a0.k_major ? d.M : d.K;
+    const int stack = d.a0.k_major ? d.groups.E : 0, matrices = d.groups.E && !d.a0.k_major ? d.groups.E : 1;
+    p.tiles_m = pl.tiles_m; p.tiles_n = pl.tiles_n; p.tiles = matrices * p.batch * pl.tiles_m * pl.tiles_n;
     p.a_rows = std::min(ROWS, (d.M + 7) / 8 * 8);
     const int b_box = d.epi == EPI_GATED && pl.cg == 1 ? pl.bn / 2 : pl.bn / pl.cg;
     p.a_blocks = !d.a0.k_major && d.M % 64 == 0;
     p.b_blocks = !d.b0.k_major && d.N % 64 == 0;
-    if (!encode(p.a[0], d.a0, 0, d.M, d.K, p.a_rows, p.a_blocks) || !encode(p.b[0], d.b0, 0, d.N, d.K, b_box, p.b_blocks))
+    if (!encode(p.a[0], d.a0, 0, d.M, d.K, p.a_rows, p.a_blocks) || !encode(p.b[0], d.b0, 0, d.N, d.K, b_box, p.b_blocks, stack))
         return cudaErrorInvalidValue;
     if (two && !encode(p.a[1], d.a1, 0, d.M, d.K, p.a_rows, p.a_blocks)) return cudaErrorInvalidValue;
-    if (d.b1.p && !encode(p.b[1], d.b1, 0, d.N, d.K, b_box, p.b_blocks)) return cudaErrorInvalidValue;
+    if (d.b1.p && !encode(p.b[1], d.b1, 0, d.N, d.K, b_box, p.b_blocks, stack)) return cudaErrorInvalidValue;
     p.bf16 = bf16; p.act = d.act;
     p.out = d.out; p.out2 = d.out2; p.kept = static_cast<unsigned char *>(d.kept); p.ldo = d.ldo;
     p.vec = d.ldo % 16 == 0 && aligned_to(d.out, 32) && aligned_to(d.out2, 32) ? 32 : d.ldo % 8 == 0 ? 16 : 2;
@@ -466,7 +510,8 @@ cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool first,
     }
     p.status = status;
     p.first = first;
-    return pl.cg == 2 ? launch_tile<2, 256>(p, pl, d, st) : launch_tile<1, 128>(p, pl, d, st);
+    if (d.groups.E) return pl.cg == 2 ? launch_tile<2, 256, true>(p, pl, d, st) : launch_tile<1, 128, true>(p, pl, d, st);
+    return pl.cg == 2 ? launch_tile<2, 256, false>(p, pl, d, st) : launch_tile<1, 128, false>(p, pl, d, st);
 }
 
 }  // namespace ffn

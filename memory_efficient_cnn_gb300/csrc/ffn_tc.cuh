@@ -76,6 +76,17 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
             : "memory");
 }
 template <int CG>
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int e, uint32_t bar) {
+    if (CG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+            "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(e), "r"(bar)
+            : "memory");
+    else
+        tma_load_4d(dst, map, x, y, z, e, bar);
+}
+template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     if (CG == 2)
         asm volatile(
@@ -120,6 +131,9 @@ struct Work {
     int z, tm, tn;  // batch, tile row, tile column
     int k0, k1;     // K blocks, over all segments
     int slot;       // streamed: the run's place among the tile's
+    // Grouped rows of A: the tile's expert, its first row, and the ends of its rows without and
+    // with the padding. Grouped sums: the expert, its first row, of which the K blocks count.
+    int e, row0, row_end, pad_end;
 };
 
 // The K blocks of a streamed launch are dealt to `units` CTA groups: unit i takes
@@ -169,6 +183,83 @@ struct Walk {
         const int rows = min(8, tiles_m - band * 8);
         w.tn = r / rows;
         w.tm = band * 8 + r - w.tn * rows;
+        return true;
+    }
+};
+
+// The groups as the roles of a CTA read them, in shared memory: the experts' first rows, their
+// counts, and, of rows of A, their first tiles and the number of all.
+struct GroupTable {
+    int *begin, *count, *first;
+};
+__host__ __device__ inline int group_table_bytes(int E) { return (3 * E + 1) * 4; }
+__device__ inline GroupTable group_table(void *smem, int E) {
+    int *p = static_cast<int *>(smem);
+    return {p, p + E, p + 2 * E};
+}
+// Filled by one warp. tile_m, tiles_n: rows of a tile, tiles of a row of them. (A backward call gets the
+// groups from a buffer of the caller's: whatever it holds, no row at or past `bound` is touched.)
+__device__ inline void fill_group_table(const GroupTable &t, const Groups &g, int bound, int tile_m, int tiles_n, int lane) {
+    int before = 0;  // tiles of the experts before this pass
+    for (int e0 = 0; e0 < g.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int begin = e < g.E ? min(max(g.begin[e], 0), bound) / GROUP_ROWS * GROUP_ROWS : 0;
+        const int count = e < g.E ? min(max(g.count[e], 0), bound - begin) : 0;
+        const int tiles = (count + tile_m - 1) / tile_m * tiles_n;
+        int sum = tiles;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (e < g.E) t.begin[e] = begin, t.count[e] = count, t.first[e] = before + sum - tiles;
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) t.first[g.E] = before;
+}
+
+// Walks a CTA group's work over experts: tile after tile of rows of A (each expert in bands as
+// above), or, SUMMED, the E * batch output matrices.
+template <bool SUMMED>
+struct GroupWalk {
+    GroupTable t;
+    int KB, KT, tiles_m, tiles_n, tile_m, E, units, at, end, e;
+    template <typename P>
+    __device__ GroupWalk(const P &p, const GroupTable &table, int tile_m_, int unit, int units_) : t(table) {
+        KB = p.KB, KT = p.KB * p.segs, tiles_m = p.tiles_m, tiles_n = p.tiles_n, tile_m = tile_m_, E = p.groups.E;
+        units = units_, at = unit, e = 0;
+        end = SUMMED ? p.tiles : t.first[E];
+    }
+    __device__ bool next(Work &w) {
+        if (at >= end) return false;
+        int r, rows_m;
+        w.z = w.slot = w.k0 = 0;
+        if (SUMMED) {
+            const int per = tiles_m * tiles_n, m = at / per;  // (the matrices of an expert follow one another)
+            r = at - m * per;
+            w.z = m / E;  // (all of the first product before those of the second)
+            w.e = m - w.z * E;
+            w.k1 = (t.count[w.e] + BK - 1) / BK;
+            rows_m = tiles_m;
+        } else {
+            int hi = E;  // first[e] <= at < first[hi]
+            while (hi - e > 1) {
+                const int mid = (e + hi) / 2;
+                if (t.first[mid] <= at) e = mid;
+                else hi = mid;
+            }
+            w.e = e;
+            r = at - t.first[e];
+            w.k1 = KT;
+            rows_m = (t.count[e] + tile_m - 1) / tile_m;
+        }
+        w.row0 = t.begin[w.e];
+        w.row_end = w.row0 + t.count[w.e];
+        w.pad_end = w.row0 + (t.count[w.e] + GROUP_ROWS - 1) / GROUP_ROWS * GROUP_ROWS;
+        const int band = r / (8 * tiles_n), in = r - band * 8 * tiles_n;
+        const int rows = min(8, rows_m - band * 8);
+        w.tn = in / rows;
+        w.tm = band * 8 + in - w.tn * rows;
+        at += units;
         return true;
     }
 };
@@ -288,18 +379,21 @@ inline PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
 
 // An operand of I output indexes and K steps, copied `rows` output indexes at a
 // time. K innermost: (K, I). Else: (I, K) in blocks of 64 output indexes, or, where
-// I is a number of whole blocks, (64, K, I / 64), which takes several in one copy.
-inline bool encode(CUtensorMap &map, const Operand &o, int plane, int I, int K, int rows, bool blocks) {
+// I is a number of whole blocks, (64, K, I / 64), which takes several in one copy. stack:
+// so many such matrices behind one another, as the outermost axis (0: one, without it).
+inline bool encode(CUtensorMap &map, const Operand &o, int plane, int I, int K, int rows, bool blocks, int stack = 0) {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
     if (!enc) return false;
     void *base = const_cast<uint16_t *>(static_cast<const uint16_t *>(o.p) + plane * o.plane);
     const cuuint64_t pitch = (cuuint64_t)o.ld * 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)(o.k_major ? K : blocks ? 64 : I), (cuuint64_t)(o.k_major ? I : K),
-                                (cuuint64_t)(blocks ? I / 64 : 1)};
-    const cuuint64_t strides[2] = {pitch, 128};
-    const cuuint32_t box[3] = {64u, o.k_major ? (cuuint32_t)rows : (cuuint32_t)BK, (cuuint32_t)(rows / 64)};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, blocks ? 3 : 2, base, dims, strides, box, estr,
+    cuuint64_t dims[4] = {(cuuint64_t)(o.k_major ? K : blocks ? 64 : I), (cuuint64_t)(o.k_major ? I : K),
+                          (cuuint64_t)(blocks ? I / 64 : 1), 1};
+    cuuint64_t strides[3] = {pitch, 128, 128};
+    cuuint32_t box[4] = {64u, o.k_major ? (cuuint32_t)rows : (cuuint32_t)BK, (cuuint32_t)(rows / 64), 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const cuuint32_t rank = blocks ? 3 : 2;
+    if (stack) dims[rank] = (cuuint64_t)stack, strides[rank - 1] = pitch * (cuuint64_t)(o.k_major ? I : K), box[rank] = 1u;
+    return enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, stack ? rank + 1 : rank, base, dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -398,6 +492,26 @@ inline TcPlan plan_tiles(const Product &d, int cg, int bn, double kb, double epi
     const double moved = (double)(tiles + st.units) * std::min(tm, d.M) * bn * 8;
     st.cost = 4 + (double)((total + st.units - 1) / st.units) * kb + bn / 128.0 + 4 + moved / 6e6;
     return st.cost < pl.cost ? st : pl;
+}
+
+// The plan of a grouped product: plain tiles of 128 * cg rows and bn columns. The experts' shares are
+// not known here; each expert's last tile of rows is taken to be half full.
+inline TcPlan plan_groups(const Product &d, int cg, int bn, double kb, double epi) {
+    const bool summed = !d.a0.k_major;
+    const int E = d.groups.E, tm = ROWS * cg, cols = d.epi == EPI_GATED ? bn / 2 : bn, z = d.batch ? 2 : 1;
+    TcPlan pl;
+    pl.cg = cg, pl.bn = bn;
+    pl.tiles_m = (d.M + tm - 1) / tm;
+    pl.tiles_n = (d.N + cols - 1) / cols;
+    const double KT = summed ? d.rows / E / BK + 0.5 : (double)((d.K + BK - 1) / BK * (d.epi != EPI_GATED && d.a1.p ? 2 : 1));
+    const double tiles = summed ? (double)z * E * pl.tiles_m * pl.tiles_n
+                                : std::max(1.0, std::min(d.rows / tm + 0.5 * E, d.rows)) * pl.tiles_n;
+    // (a bound, for rows of A: every expert's last tile may hold one row)
+    const double most = summed ? tiles : std::min<double>((double)((int64_t)d.M / tm + E), d.M) * pl.tiles_n;
+    pl.units = (int)std::min<double>(SMS / cg, most);
+    const double waves = std::max(1.0, tiles / (SMS / cg));
+    pl.cost = 4 + KT * kb + epi + (waves - 1) * std::max(KT * kb, epi);
+    return pl;
 }
 
 }  // namespace

@@ -74,6 +74,16 @@ __device__ __forceinline__ void split_f32(float v, uint16_t &h, uint16_t &m, uin
     l = __bfloat16_as_ushort(__float2bfloat16_rn(rest - __bfloat162float(mid)));
 }
 
+// Rows grouped by expert: those of expert e are begin[e] to begin[e] + count[e], begin[e] a
+// multiple of GROUP_ROWS and the rows up to the next multiple of it padding: zero wherever
+// they are summed over. On the device; E = 0: no groups.
+constexpr int GROUP_ROWS = 64;
+constexpr int MAX_EXPERTS = 1024;
+struct Groups {
+    const int32_t *begin = nullptr, *count = nullptr;
+    int E = 0;
+};
+
 // D[M][N] = A0 B0^T (+ A1 B1^T); EPI_GATED: g = A0 B0^T, u = A0 B1^T; batch: out =
 // A0 B0^T and out2 = A1 B1^T.
 struct Product {
@@ -86,6 +96,11 @@ struct Product {
     void *kept = nullptr;  // written (EPI_GATED, may be null) or read (EPI_DGATED)
     int64_t ldo = 0;       // row pitch of out and out2 in elements
     int64_t plane = 0;     // fp32, GATED and DGATED: elements from one plane of out and out2 to the next
+    // With groups, the rows of A (A k_major; M: a bound of them) meet their expert's matrix of
+    // the E that lie behind one another in B; or, the rows being summed over (K: a bound of
+    // them), out and out2 are E matrices behind one another, each the sum of its expert's rows.
+    Groups groups;
+    double rows = 0;       // with groups: the rows that there may be besides the padding
 };
 
 // Tensor cores: fp16/bf16; operands 16-byte aligned with pitches that are multiples

@@ -7,10 +7,15 @@ and nothing is computed here.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
+
 import torch
 
 from ._binding import _check, _cuda, _dtype_code, _same_device, lib
-from .block import _alike, _code, _same_dtype, _shape, _stream, _unrecorded
+from .block import (
+    ACTS, FFN_BACKWARD, FFN_FORWARD, FFN_SAVED, FFN_TRAIN, _alike, _bytes, _code, _empty, _ptr, _same_dtype, _shape, _stream,
+    _unrecorded)
 
 ROUTES = {"top": 0, "all": 1}
 
@@ -90,3 +95,135 @@ def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts:
     dlogits = torch.empty_like(logits)
     im2win_expert_route_backward(dweights, logits, experts, dlogits, over)
     return dlogits
+
+
+# ---------------------------------------------------------------- feed-forward
+@functools.lru_cache(maxsize=4096)
+def im2win_expert_ffn_size(buffer: int, T, k, E, C, F, dtype: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("im2win_expert_ffn_size", lib().im2win_expert_ffn_size(buffer, T, k, E, C, F, dtype, ctypes.byref(out)))
+    return out.value
+
+
+def _ffn_dims(fn, x, weights, w_gate, w_up, w_down):
+    """(T, k, E, C, F) after the shape, type and device checks; x is [..., C] and weights
+    [..., k] with the same leading axes."""
+    if x.dim() < 1 or weights.dim() < 1 or w_gate.dim() != 3:
+        raise ValueError(f"{fn}: x must be [..., C], weights [..., k] and w_gate [E, F, C]")
+    C, k = x.shape[-1], weights.shape[-1]
+    E, F = w_gate.shape[:2]
+    if not (C >= 1 and F >= 1 and E >= 1 and k >= 1 and weights.shape[:-1] == x.shape[:-1]
+            and w_gate.shape == w_up.shape == (E, F, C) and w_down.shape == (E, C, F)
+            and _alike(x.dtype, x.get_device(), x, weights, w_gate, w_up, w_down)):
+        _shape(fn, "weights", weights, (*x.shape[:-1], k))
+        _shape(fn, "w_gate", w_gate, (E, F, C))
+        _shape(fn, "w_up", w_up, (E, F, C))
+        _shape(fn, "w_down", w_down, (E, C, F))
+        if C < 1 or F < 1 or E < 1 or k < 1:
+            raise ValueError(f"{fn}: C, F, the experts and a row's choices must be at least 1")
+        _same(fn, x, weights, w_gate, w_up, w_down)
+    return x.numel() // C, k, E, C, F
+
+
+def _buffer(fn, name, t, x, kind, dims):
+    """A buffer of the call: the caller's, checked, or a new one."""
+    size = im2win_expert_ffn_size(kind, *dims, _dtype_code(x))
+    if t is None:
+        return _empty(size, x.device)
+    _same_device(fn, x, t)
+    _cuda(t)
+    if _bytes(t) < size:
+        raise ValueError(f"{fn}: {name} is too small")
+    return t
+
+
+def _ffn(fn, dims, x, experts, weights, w_gate, w_up, w_down, y, saved, ws, act):
+    _check(fn, lib().im2win_expert_ffn(
+        x.data_ptr(), experts.data_ptr(), weights.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+        y.data_ptr(), _ptr(saved), ws.data_ptr(), _bytes(ws), *dims, _code(ACTS, act, "act"), _dtype_code(x),
+        _stream(x.get_device())))
+
+
+def im2win_expert_ffn(x, experts, weights, w_gate, w_up, w_down, y, saved, ws, act: str = "silu") -> None:
+    """y = the sum of the chosen experts' weighted outputs; saved None: inference."""
+    fn = "im2win_expert_ffn"
+    dims = _ffn_dims(fn, x, weights, w_gate, w_up, w_down)
+    _experts(fn, experts, x, weights.shape)
+    _shape(fn, "y", y, x.shape)
+    _same(fn, x, y)
+    if saved is not None:
+        _buffer(fn, "saved", saved, x, FFN_SAVED, dims)
+    _same_device(fn, x, ws)
+    _cuda(ws)
+    _ffn(fn, dims, x, experts, weights, w_gate, w_up, w_down, y, saved, ws, act)
+
+
+def _ffn_backward(fn, dims, dy, weights, w_gate, w_up, w_down, saved, grads, ws, act):
+    _check(fn, lib().im2win_expert_ffn_backward(
+        dy.data_ptr(), weights.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), saved.data_ptr(),
+        *[_ptr(t) for t in grads], ws.data_ptr(), _bytes(ws), *dims, _code(ACTS, act, "act"), _dtype_code(dy),
+        _stream(dy.get_device())))
+
+
+def im2win_expert_ffn_backward(dy, weights, w_gate, w_up, w_down, saved, dx, dweights, dw_gate, dw_up, dw_down, ws,
+                               act: str = "silu") -> None:
+    """Gradients of im2win_expert_ffn; dx, dweights, or the three dw, may be None."""
+    fn = "im2win_expert_ffn_backward"
+    dims = _ffn_dims(fn, dy, weights, w_gate, w_up, w_down)
+    _buffer(fn, "saved", saved, dy, FFN_SAVED, dims)
+    grads = (dx, dweights, dw_gate, dw_up, dw_down)
+    for name, t, like in zip(("dx", "dweights", "dw_gate", "dw_up", "dw_down"), grads, (dy, weights, w_gate, w_up, w_down)):
+        if t is not None:
+            _shape(fn, name, t, like.shape)
+            _same(fn, dy, t)
+    _same_device(fn, dy, ws)
+    _cuda(ws)
+    _ffn_backward(fn, dims, dy, weights, w_gate, w_up, w_down, saved, grads, ws, act)
+
+
+def _forward(fn, x, experts, weights, w_gate, w_up, w_down, act, ws, out, saved, train):
+    _unrecorded(fn, x, weights, w_gate, w_up, w_down)
+    dims = _ffn_dims(fn, x, weights, w_gate, w_up, w_down)
+    _experts(fn, experts, x, weights.shape)
+    ws = _buffer(fn, "ws", ws, x, FFN_TRAIN if train else FFN_FORWARD, dims)
+    if train:
+        saved = _buffer(fn, "saved", saved, x, FFN_SAVED, dims)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _shape(fn, "out", out, x.shape)
+        _same(fn, x, out)
+    _ffn(fn, dims, x, experts, weights, w_gate, w_up, w_down, out, saved, ws, act)
+    return out, saved
+
+
+def expert_ffn(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+               w_down: torch.Tensor, act: str = "silu", ws: torch.Tensor | None = None,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gated feed-forward of x[..., C] by experts: the sum over a row's choices, experts[..., k] (int32) and
+    weights[..., k] as expert_route() gives them, of weight * gated_ffn(row) with that expert's w_gate[E, F, C],
+    w_up[E, F, C] and w_down[E, C, F]. A choice outside of the experts (-1) takes no part. Autograd does not
+    record it: tensors that require grad are refused outside of torch.no_grad()."""
+    return _forward("expert_ffn", x, experts, weights, w_gate, w_up, w_down, act, ws, out, None, False)[0]
+
+
+def expert_ffn_train(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, w_gate: torch.Tensor,
+                     w_up: torch.Tensor, w_down: torch.Tensor, act: str = "silu", ws: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, saved: torch.Tensor | None = None):
+    """expert_ffn() and the buffer its expert_ffn_backward() needs: (y, saved)."""
+    return _forward("expert_ffn_train", x, experts, weights, w_gate, w_up, w_down, act, ws, out, saved, True)
+
+
+def expert_ffn_backward(dy: torch.Tensor, weights: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                        w_down: torch.Tensor, saved: torch.Tensor, act: str = "silu", ws: torch.Tensor | None = None,
+                        need_dx: bool = True, need_dweights: bool = True, need_dw: bool = True):
+    """(dx, dweights, dw_gate, dw_up, dw_down) of expert_ffn_train() at the same weights; None for
+    what is not needed. x and the experts are in `saved`."""
+    fn = "expert_ffn_backward"
+    dims = _ffn_dims(fn, dy, weights, w_gate, w_up, w_down)
+    _buffer(fn, "saved", saved, dy, FFN_SAVED, dims)
+    ws = _buffer(fn, "ws", ws, dy, FFN_BACKWARD, dims)
+    grads = [torch.empty_like(t) if need else None for t, need in (
+        (dy, need_dx), (weights, need_dweights), (w_gate, need_dw), (w_up, need_dw), (w_down, need_dw))]
+    _ffn_backward(fn, dims, dy, weights, w_gate, w_up, w_down, saved, grads, ws, act)
+    return tuple(grads)

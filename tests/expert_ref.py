@@ -122,3 +122,84 @@ def route_all(logits, k, over, dtype, dweights=None, experts=None):
     ev = ev + 2.0 ** -120
     out["dlogits"] = (v, ev + un * (v.abs() + ev) + tiny)
     return experts, out
+
+
+# ---------------------------------------------------------------- experts' feed-forward
+def expert_ffn(x, experts, weights, wg, wu, wd, act):
+    y = torch.zeros_like(x)
+    for e in range(wg.shape[0]):
+        t, j = (experts == e).nonzero(as_tuple=True)
+        h = act_pair(act, x[t] @ wg[e].T)[0] * (x[t] @ wu[e].T)
+        y.index_add_(0, t, weights[t, j].unsqueeze(-1) * (h @ wd[e].T))
+    return y
+
+
+def experts_all(x, experts, weights, wg, wu, wd, act, dtype, dy=None):
+    """x [T, C], experts and weights [T, k], the matrices [E, ...], all but experts in float64. As
+    block_ref.ffn_all for each expert's rows, with the roundings of the choices' outputs, of
+    weights * dy and of the choices' shares of dx besides."""
+    un, tiny = U[dtype], TINY[dtype]
+    T, C = x.shape
+    E_, F, k = wg.shape[0], wg.shape[1], experts.shape[1]
+
+    def product(p, ep, q, K):
+        """p q^T, its error from p's and the sum's."""
+        return p @ q.T, (0 if ep is None else ep @ q.abs().T) + acc(K) * (p.abs() @ q.abs().T)
+
+    def both(p, ep, q, eq, K):
+        v, e = product(p, ep, q, K)
+        return v, e + (0 if eq is None else (p.abs() + (0 if ep is None else ep)) @ eq.T)
+
+    def rounded(v, e):
+        return v, e + un * (v.abs() + e) + tiny
+
+    y, ey, my = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x)
+    out = {}
+    if dy is not None:
+        dx, edx, mdx = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x)
+        dwt, edwt = torch.zeros_like(weights), torch.zeros_like(weights)
+        dws = {n: [] for n in ("dw_gate", "dw_up", "dw_down")}
+    for e in range(E_):
+        t, j = (experts == e).nonzero(as_tuple=True)
+        xe, w = x[t], weights[t, j].unsqueeze(-1)
+        (g, eg), (u, eu) = product(xe, None, wg[e], C), product(xe, None, wu[e], C)
+        a, d = act_pair(act, g)
+        ea = 1.2 * eg + EXTRA * (a.abs() + d.abs() * g.abs())
+        h = a * u
+        h, eh = rounded(h, ea * u.abs() + a.abs() * eu + ea * eu + EXTRA * h.abs())
+        ys, eys = rounded(*product(h, eh, wd[e], F))
+        y.index_add_(0, t, w * ys)
+        ey.index_add_(0, t, w.abs() * eys)
+        my.index_add_(0, t, (w * ys).abs())
+        if dy is None:
+            continue
+        dye = dy[t]
+        dwt[t, j] = (dye * ys).sum(-1)
+        edwt[t, j] = (dye.abs() * eys).sum(-1) + acc(C) * (dye * ys).abs().sum(-1)
+        dys, edys = rounded(w * dye, E * (w * dye).abs())
+        dh, edh = product(dys, edys, wd[e].T, C)
+        ed = 1.2 * eg + EXTRA * (d.abs() + 1)
+        if act == "relu":
+            ed = (g.abs() <= eg).to(g.dtype)
+        dg, du = dh * u * d, dh * a
+        edg = edh * (u * d).abs() + (dh.abs() + edh) * (eu * (d.abs() + ed) + u.abs() * ed) + EXTRA * dg.abs()
+        edu = edh * a.abs() + (dh.abs() + edh) * ea + EXTRA * du.abs()
+        dg, edg = rounded(dg, edg)
+        du, edu = rounded(du, edu)
+        v1, e1 = product(dg, edg, wg[e].T, 2 * F)
+        v2, e2 = product(du, edu, wu[e].T, 2 * F)
+        dxs, edxs = rounded(v1 + v2, e1 + e2)
+        dx.index_add_(0, t, dxs)
+        edx.index_add_(0, t, edxs)
+        mdx.index_add_(0, t, dxs.abs())
+        rows = max(1, t.numel())
+        dws["dw_gate"].append(rounded(*both(dg.T, edg.T, xe.T, None, rows)))
+        dws["dw_up"].append(rounded(*both(du.T, edu.T, xe.T, None, rows)))
+        dws["dw_down"].append(rounded(*both(dys.T, edys.T, h.T, eh.T, rows)))
+    out["y"] = rounded(y, ey + k * E * my)
+    if dy is not None:
+        out["dx"] = rounded(dx, edx + k * E * mdx)
+        out["dweights"] = rounded(dwt, edwt)
+        for n, pairs in dws.items():
+            out[n] = tuple(torch.stack([p[i] for p in pairs]) for i in range(2))
+    return out

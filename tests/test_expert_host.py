@@ -113,3 +113,73 @@ def test_route_binding_refusals():
         mec.expert_route(logits.clone().requires_grad_(), 2)
     with pytest.raises(ValueError, match="CUDA"):
         mec.expert_route(logits, 2)
+
+
+# ---------------------------------------------------------------- experts' feed-forward
+def test_expert_ffn_sizes():
+    for dt in (0, 1, 2):
+        for T, k, E, C, F in ((0, 1, 1, 8, 8), (1, 2, 8, 512, 2048), (777, 2, 24, 1000, 1366), (5, 32, 3, 7, 9)):
+            sizes = [mec.im2win_expert_ffn_size(b, T, k, E, C, F, dt) for b in range(4)]
+            assert all(s % 256 == 0 and s >= 256 for s in sizes)
+    sz = ctypes.c_size_t()
+    q = mec.lib().im2win_expert_ffn_size
+    for bad in ((0, -1, 1, 1, 8, 8, 0), (0, 1, 0, 1, 8, 8, 0), (0, 1, 1, 0, 8, 8, 0), (0, 1, 1, 1, 0, 8, 0), (0, 1, 1, 1, 8, 0, 0),
+                (4, 1, 1, 1, 8, 8, 0), (0, 1, 1, 1, 8, 8, 3)):
+        assert q(*bad, ctypes.byref(sz)) == ERR_INVALID_ARG
+    assert q(0, 1, 1, 1, 8, 8, 0, None) == ERR_INVALID_ARG
+    for big in ((0, 1, 33, 40, 8, 8, 0), (0, 1, 1, 1025, 8, 8, 0), (0, 1 << 31, 1, 1, 8, 8, 0), (0, 1 << 30, 2, 1, 8, 8, 0),
+                (0, 1, 1, 1024, 1 << 21, 8, 0), (0, 1, 1, 1024, 8, 1 << 21, 0), (0, 1, 1, 1024, 1 << 16, 1 << 16, 0),
+                (0, 1 << 24, 1, 1, 1 << 17, 8, 0)):
+        assert q(*big, ctypes.byref(sz)) == ERR_UNSUPPORTED, big
+
+
+def test_expert_ffn_refusals():
+    def call(x=4096, experts=4096, weights=4096, wg=8192, wu=8192, wd=8192, y=4096, saved=None, ws=16384, ws_bytes=1 << 40, T=3,
+             k=2, E=4, C=8, F=8, act=0, dtype=F16):
+        return mec.lib().im2win_expert_ffn(x, experts, weights, wg, wu, wd, y, saved, ws, ws_bytes, T, k, E, C, F, act, dtype, None)
+
+    for kw in (dict(x=None), dict(experts=None), dict(weights=None), dict(wg=None), dict(wu=None), dict(wd=None), dict(y=None),
+               dict(act=5), dict(act=-1), dict(dtype=3), dict(T=-1), dict(k=0), dict(E=0), dict(C=0), dict(F=0)):
+        assert call(**kw) == ERR_INVALID_ARG, kw
+    for name in ("x", "experts", "weights", "wg", "wu", "wd", "y", "saved", "ws"):
+        assert call(**{name: 4104}) == ERR_MISALIGNED, name
+    assert call(ws=None) == ERR_WORKSPACE
+    assert call(ws_bytes=mec.im2win_expert_ffn_size(mec.FFN_FORWARD, 3, 2, 4, 8, 8, F16) - 1) == ERR_WORKSPACE
+    assert call(E=1025) == ERR_UNSUPPORTED and call(k=33) == ERR_UNSUPPORTED
+    assert call(T=0, x=None, y=None, ws=None) == OK
+
+    def back(dy=4096, weights=4096, w=8192, saved=8192, dx=4096, dweights=4096, dw=(4096,) * 3, ws=16384, ws_bytes=1 << 40, T=3,
+             act=0):
+        return mec.lib().im2win_expert_ffn_backward(dy, weights, w, w, w, saved, dx, dweights, *dw, ws, ws_bytes, T, 2, 4, 8, 8, act,
+                                                    F32, None)
+
+    for kw in (dict(dy=None), dict(weights=None), dict(w=None), dict(saved=None), dict(act=5), dict(dw=(4096, None, 4096)),
+               dict(dw=(None, 4096, 4096))):
+        assert back(**kw) == ERR_INVALID_ARG, kw
+    for kw in (dict(dy=8), dict(weights=4), dict(w=8), dict(saved=8), dict(dx=8), dict(dweights=8), dict(dw=(8,) * 3), dict(ws=8)):
+        assert back(**kw) == ERR_MISALIGNED, kw
+    assert back(ws=None) == ERR_WORKSPACE and back(ws_bytes=16) == ERR_WORKSPACE
+    assert back(dx=None, dweights=None, dw=(None,) * 3, ws=None) == OK
+
+
+def test_expert_ffn_binding_refusals():
+    x, e, p = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    w, d = torch.zeros(3, 16, 8), torch.zeros(3, 8, 16)
+    with pytest.raises(ValueError, match="w_up has shape"):
+        mec.expert_ffn(x, e, p, w, w[:2], d)
+    with pytest.raises(ValueError, match="w_down has shape"):
+        mec.expert_ffn(x, e, p, w, w, w)
+    with pytest.raises(ValueError, match="weights has shape"):
+        mec.expert_ffn(x, e, p[:3], w, w, d)
+    with pytest.raises(ValueError, match=r"w_gate \[E, F, C\]"):
+        mec.expert_ffn(x, e, p, w[0], w[0], d[0])
+    with pytest.raises(TypeError, match="one dtype"):
+        mec.expert_ffn(x, e, p.half(), w, w, d)
+    with pytest.raises(ValueError, match="CUDA"):
+        mec.expert_ffn(x, e, p, w, w, d)
+    with pytest.raises(ValueError, match="requires grad"):
+        mec.expert_ffn(x, e, p, w, w, d.clone().requires_grad_())
+    with pytest.raises(TypeError, match="int32"):
+        mec.experts._experts("f", e.long(), x, (4, 2))
+    with pytest.raises(ValueError, match="experts has shape"):
+        mec.experts._experts("f", e[:3], x, (4, 2))
