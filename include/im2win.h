@@ -530,8 +530,7 @@ im2win_status im2win_expert_ffn_size(int buffer, int64_t T, int64_t k, int64_t E
  * (a position dropped where its expert is full), whatever its weight; a row with none left gets
  * zeros; a row may name an expert twice. Only the experts that rows name are read.
  * The products are those of im2win_gated_ffn, with its roundings (h, and in the backward pass
- * dg and du); ffn_e(x[t]) is rounded to the dtype as well before it is weighted and summed in
- * fp32. y must not overlap an input. `saved` (NULL for inference; FFN_SAVED) receives what the
+ * dg, du and weights h); ffn_e(x[t]) is weighted and summed in fp32. y must not overlap an input. `saved` (NULL for inference; FFN_SAVED) receives what the
  * backward call needs; its contents are opaque. ws begins with the status block.
  */
 im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const void *weights, const void *w_gate,
@@ -542,8 +541,7 @@ im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const voi
  * Gradients of im2win_expert_ffn at the same weights, from dy[T][C] and the `saved` buffer of that
  * call (which holds the rows and their experts): dx[T][C], dweights[T][k], and dw_gate, dw_up,
  * dw_down (zero for an expert without rows). Each of dx, dweights, or the three dw together, may be
- * NULL and is then not computed. weights times dy, and each choice's share of dx, are rounded to the
- * dtype; the sums over rows of an expert have a fixed order.
+ * NULL and is then not computed. Sums have a fixed order.
  */
 im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, const void *w_gate, const void *w_up,
                                          const void *w_down, const void *saved, void *dx, void *dweights,

@@ -1,18 +1,20 @@
 // Gated feed-forward grouped by expert: argument checks, buffers and the sequence of launches.
 //
 //   plan, gather   rows to their experts: xs
-//   gated          h = act(xs w_gate_e^T) * (xs w_up_e^T)
+//   gated          h = act(xs w_gate_e^T) * (xs w_up_e^T); training: hw = weight * h
 //   down           ys = h w_down_e^T
 //   combine        y = sum over a row's choices of weight * ys
 // backward
-//   gather         dys = weight * dy, dweights = dy . ys
-//   dgated         dh = dys w_down_e, made into dg, du
+//   gather         dy to the experts: dys; dweights = dy . ys
+//   dgated         dh = weight * (dys w_down_e), made into dg, du
 //   dx             dxs = dg w_gate_e + du w_up_e, summed over a row's choices
-//   dw             dw_gate_e = dg^T xs, dw_up_e = du^T xs, dw_down_e = dys^T h over the expert's rows
+//   dw             dw_gate_e = dg^T xs, dw_up_e = du^T xs, dw_down_e = dys^T hw over the expert's rows
 //
-// The products are the gated feed-forward's kernels with the rows in groups. Between the kernels xs, h,
-// ys, dys, dg, du and dxs are in the dtype (fp32: as three bf16 planes where they are operands):
-// in fp32 they would double the bytes of everything but the weights, and the products read 16 bits.
+// The products are the gated feed-forward's kernels with the rows in groups. h, hw, dg and du are
+// operands and rounded to the dtype, as there; ys and dxs stay in fp32 until a row's sum, and the
+// weights are applied in fp32 before the rounding of hw, dg and du, so that no other rounding
+// comes between the inputs and the outputs (16-bit ys, weight * dy and dxs made y 1.2 and dx
+// 1.4 times as far off).
 #include <algorithm>
 #include <initializer_list>
 
@@ -57,7 +59,7 @@ struct Problem {
           act(act_), f32(dtype_ == IM2WIN_F32), Cp((C_ + 7) / 8 * 8), Fp((F_ + 7) / 8 * 8) {}
 
     size_t operand(int64_t n, int64_t pitch) const { return (size_t)(n * pitch) * (f32 ? 6 : 2); }
-    size_t result() const { return (size_t)(rows * Cp) * (f32 ? 4 : 2); }  // ys, dxs
+    size_t result() const { return (size_t)(rows * Cp) * 4; }  // ys, dxs
     bool copies(int64_t cols) const { return f32 || cols % 8 != 0; }
 
     Operand rows_c(const void *p, bool k_major) const { return {p, Cp, k_major, rows * Cp}; }
@@ -77,16 +79,18 @@ struct Problem {
 };
 
 struct SavedParts {
-    size_t begin, count, slot, pair, xs, h, kept, ys, bytes;
-    // kept: what the backward pass alone needs
+    size_t begin, count, slot, pair, scale, xs, h, hw, kept, ys, bytes;
+    // keep: what the backward pass alone needs
     SavedParts(const Problem &q, size_t from, bool keep) {
         Parts p(from);
         begin = p.add((size_t)(q.E + 1) * 4);
         count = p.add((size_t)q.E * 4);
         slot = p.add((size_t)q.pairs * 4);
         pair = p.add((size_t)q.rows * 4);
+        scale = p.add(keep ? (size_t)q.rows * 4 : 0);
         xs = p.add(q.operand(q.rows, q.Cp));
         h = p.add(q.operand(q.rows, q.Fp));
+        hw = p.add(keep ? q.operand(q.rows, q.Fp) : 0);
         kept = p.add(keep ? kept_bytes(q.rows, q.F, q.f32) : 0);
         ys = p.add(q.result());
         bytes = p.end;
@@ -109,10 +113,11 @@ struct ForwardParts {
 };
 
 struct BackwardParts {
-    size_t dys, dg, du, dxs, wg, wu, wd, bytes;
+    size_t dys, scale, dg, du, dxs, wg, wu, wd, bytes;
     explicit BackwardParts(const Problem &q) {
         Parts p(kStatusBytes);
         dys = p.add(q.operand(q.rows, q.Cp));
+        scale = p.add((size_t)q.rows * 4);
         dg = p.add(q.operand(q.rows, q.Fp));
         du = p.add(q.operand(q.rows, q.Fp));
         dxs = p.add(q.result());
@@ -125,6 +130,7 @@ struct BackwardParts {
 
 unsigned char *at(void *base, size_t off) { return static_cast<unsigned char *>(base) + off; }
 int32_t *ints(void *base, size_t off) { return reinterpret_cast<int32_t *>(at(base, off)); }
+float *floats(void *base, size_t off) { return reinterpret_cast<float *>(at(base, off)); }
 
 Rows rows_of(const Problem &q, const SavedParts &s, void *saved) {
     return {q.T, q.rows, q.k, q.E, q.C, q.Cp, {ints(saved, s.begin), ints(saved, s.count), ints(saved, s.slot), ints(saved, s.pair)}};
@@ -202,21 +208,21 @@ im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const voi
     w_up = seq.readable(w_up, q.E * q.F, q.C, parts.wu);
     w_down = seq.readable(w_down, q.E * q.C, q.F, parts.wd);
     seq.copy();
-    seq.step([&] { return launch_gather(rows, x, at(keep, own.xs), dtype, st); });
+    seq.step([&] { return launch_gather(rows, x, weights, at(keep, own.xs), saved ? floats(keep, own.scale) : nullptr, dtype, st); });
 
     Product gated = q.product((int)q.rows, q.F, q.C, rows.plan.begin, rows.plan.count);
     gated.a0 = q.rows_c(at(keep, own.xs), true);
     gated.b0 = q.w_in(w_gate, true), gated.b1 = q.w_in(w_up, true);
     gated.epi = EPI_GATED;
     gated.out = at(keep, own.h), gated.ldo = q.Fp, gated.plane = q.rows * q.Fp;
-    gated.kept = saved ? at(keep, own.kept) : nullptr;
+    if (saved) gated.kept = at(keep, own.kept), gated.scale = floats(keep, own.scale), gated.out2 = at(keep, own.hw);
     seq.run(gated);
 
     Product down = q.product((int)q.rows, q.C, q.F, rows.plan.begin, rows.plan.count);
     down.a0 = q.rows_f(at(keep, own.h), true), down.b0 = q.w_out(w_down, true);
     down.out = at(keep, own.ys), down.ldo = q.Cp;
     seq.run(down);
-    seq.step([&] { return launch_combine(rows, at(keep, own.ys), weights, y, dtype, st); });
+    seq.step([&] { return launch_combine(rows, floats(keep, own.ys), weights, y, dtype, st); });
     return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
 }
 
@@ -251,7 +257,8 @@ im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, co
     Sequence seq{q, ws, st};
     void *dys = at(ws, parts.dys), *dg = at(ws, parts.dg), *du = at(ws, parts.du);
     seq.step([&] {
-        return launch_gather_back(rows, dy, weights, at(keep, own.ys), dys, dweights, static_cast<uint32_t *>(ws), dtype, st);
+        return launch_gather_back(rows, dy, weights, floats(keep, own.ys), dys, floats(ws, parts.scale), dweights,
+                                  static_cast<uint32_t *>(ws), dtype, st);
     });
     if (dx || want_dw) {
         w_down = seq.readable(w_down, q.E * q.C, q.F, parts.wd);
@@ -264,7 +271,7 @@ im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, co
         d.a0 = q.rows_c(dys, true), d.b0 = q.w_out(w_down, false);
         d.epi = EPI_DGATED;
         d.out = dg, d.out2 = du, d.ldo = q.Fp, d.plane = q.rows * q.Fp;
-        d.kept = at(keep, own.kept);
+        d.kept = at(keep, own.kept), d.scale = floats(ws, parts.scale);
         seq.run(d);
     }
     if (dx) {
@@ -273,7 +280,7 @@ im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, co
         d.a1 = q.rows_f(du, true), d.b1 = q.w_in(w_up, false);
         d.out = at(ws, parts.dxs), d.ldo = q.Cp;
         seq.run(d);
-        seq.step([&] { return launch_combine(rows, at(ws, parts.dxs), nullptr, dx, dtype, st); });
+        seq.step([&] { return launch_combine(rows, floats(ws, parts.dxs), nullptr, dx, dtype, st); });
     }
     if (want_dw) {
         Product in = q.product(q.F, q.C, (int)q.rows, rows.plan.begin, rows.plan.count);
@@ -283,7 +290,7 @@ im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, co
         in.out = dw_gate, in.out2 = dw_up, in.ldo = q.C;
         seq.run(in);
         Product out = q.product(q.C, q.F, (int)q.rows, rows.plan.begin, rows.plan.count);
-        out.a0 = q.rows_c(dys, false), out.b0 = q.rows_f(at(keep, own.h), false);
+        out.a0 = q.rows_c(dys, false), out.b0 = q.rows_f(at(keep, own.hw), false);
         out.out = dw_down, out.ldo = q.F;
         seq.run(out);
     }

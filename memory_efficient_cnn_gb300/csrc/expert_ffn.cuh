@@ -38,14 +38,16 @@ struct Rows {
 
 // The plan; clears the status. hist: an int for each expert and block, where there are several blocks.
 cudaError_t launch_plan(const Rows &r, const int32_t *experts, int32_t *hist, uint32_t *status, cudaStream_t st);
-// grouped[row] = x[pair / k], zero in the padding; fp32: in three bf16 planes.
-cudaError_t launch_gather(const Rows &r, const void *x, void *grouped, int dtype, cudaStream_t st);
-// grouped[row] = weights[pair] * dy[pair / k], zero in the padding; dweights[pair] (where not null)
-// = dy[pair / k] . y[row], or zero without a row. Clears the status.
-cudaError_t launch_gather_back(const Rows &r, const void *dy, const void *weights, const void *y, void *grouped,
-                               void *dweights, uint32_t *status, int dtype, cudaStream_t st);
-// out[t] = sum over the row's choices of weights (null: 1) * grouped[slot], in their order.
-cudaError_t launch_combine(const Rows &r, const void *grouped, const void *weights, void *out, int dtype, cudaStream_t st);
+// grouped[row] = x[pair / k], zero in the padding; fp32: in three bf16 planes. scale[row] (where not
+// null) = weights[pair].
+cudaError_t launch_gather(const Rows &r, const void *x, const void *weights, void *grouped, float *scale, int dtype,
+                          cudaStream_t st);
+// The same of dy; dweights[pair] (where not null) = dy[pair / k] . ys[row], or zero without a row.
+// Clears the status.
+cudaError_t launch_gather_back(const Rows &r, const void *dy, const void *weights, const float *ys, void *grouped,
+                               float *scale, void *dweights, uint32_t *status, int dtype, cudaStream_t st);
+// out[t] = sum over the row's choices of weights (null: 1) * ys[slot], in their order.
+cudaError_t launch_combine(const Rows &r, const float *ys, const void *weights, void *out, int dtype, cudaStream_t st);
 
 }  // namespace ffn
 }  // namespace im2win

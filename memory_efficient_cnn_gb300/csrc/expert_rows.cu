@@ -165,13 +165,15 @@ __device__ __forceinline__ int64_t pair_of(const Rows &r, int64_t row) {
 
 // A warp for 256 columns of a row.
 template <typename T, bool V>
-__global__ void __launch_bounds__(THREADS) expert_gather(const __grid_constant__ Rows r, const T *x, void *grouped, int parts) {
+__global__ void __launch_bounds__(THREADS) expert_gather(const __grid_constant__ Rows r, const T *x, const T *weights,
+                                                         void *grouped, float *scale, int parts) {
     tc::allow_dependents();
     tc::grid_dependency_wait();
     const int64_t id = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5), row = id / parts;
     const int c = ((int)(id - row * parts) * 32 + (threadIdx.x & 31)) * 8;
     const int64_t q = pair_of(r, row);
     if (q < -1 || c >= r.Cp) return;
+    if (scale && c == 0) scale[row] = q >= 0 ? to_f32(weights[q]) : 0.0f;
     float v[8] = {};
     if (q >= 0) load8<T, V>(x + q / r.k * r.C + c, r.C - c, v);
     store_operand<T>(grouped, r, row, c, v);
@@ -180,7 +182,8 @@ __global__ void __launch_bounds__(THREADS) expert_gather(const __grid_constant__
 // A warp a row.
 template <typename T, bool V>
 __global__ void __launch_bounds__(THREADS) expert_gather_back(const __grid_constant__ Rows r, const T *dy, const T *weights,
-                                                              const T *y, void *grouped, T *dweights, uint32_t *status) {
+                                                              const float *ys, void *grouped, float *scale, T *dweights,
+                                                              uint32_t *status) {
     tc::grid_dependency_wait();
     tc::allow_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) status[0] = 0;
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(THREADS) expert_gather_back(const __grid_const
     if (dweights && id < r.T * r.k && r.plan.slot[id] < 0) dweights[id] = from_f32<T>(0.0f);
     const int64_t row = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5), q = pair_of(r, row);
     if (q < -1) return;
-    const float w = q >= 0 ? to_f32(weights[q]) : 0.0f;
+    if ((threadIdx.x & 31) == 0) scale[row] = q >= 0 ? to_f32(weights[q]) : 0.0f;
     const T *from = dy + (q >= 0 ? q / r.k * r.C : 0);
     float dot = 0.0f;
     for (int c = (threadIdx.x & 31) * 8; c < r.Cp; c += 256) {
@@ -197,12 +200,10 @@ __global__ void __launch_bounds__(THREADS) expert_gather_back(const __grid_const
             load8<T, V>(from + c, r.C - c, d);
             if (dweights) {
                 float o[8];
-                load8<T, V>(y + row * r.Cp + c, r.C - c, o);
+                load8<float, true>(ys + row * r.Cp + c, 8, o);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dot = fmaf(d[i], o[i], dot);
+                for (int i = 0; i < 8; ++i) dot = c + i < r.C ? fmaf(d[i], o[i], dot) : dot;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] *= w;
         }
         store_operand<T>(grouped, r, row, c, d);
     }
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(THREADS) expert_gather_back(const __grid_const
 
 // A warp for 256 columns of an output row.
 template <typename T, bool V>
-__global__ void __launch_bounds__(THREADS) expert_combine(const __grid_constant__ Rows r, const T *grouped, const T *weights,
+__global__ void __launch_bounds__(THREADS) expert_combine(const __grid_constant__ Rows r, const float *ys, const T *weights,
                                                           T *out, int parts) {
     tc::allow_dependents();
     tc::grid_dependency_wait();
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(THREADS) expert_combine(const __grid_constant_
         const int64_t slot = r.plan.slot[t * r.k + j];
         if (slot < 0 || slot >= r.rows) continue;
         float v[8];
-        load8<T, true>(grouped + slot * r.Cp + c, 8, v);
+        load8<float, true>(ys + slot * r.Cp + c, 8, v);
         const float w = weights ? to_f32(weights[t * r.k + j]) : 1.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
@@ -272,30 +273,31 @@ cudaError_t launch_plan(const Rows &r, const int32_t *experts, int32_t *hist, ui
                   r.plan, status);
 }
 
-cudaError_t launch_gather(const Rows &r, const void *x, void *grouped, int dtype, cudaStream_t st) {
+cudaError_t launch_gather(const Rows &r, const void *x, const void *weights, void *grouped, float *scale, int dtype,
+                          cudaStream_t st) {
     const int parts = (int)((r.Cp + 255) / 256);
     return with_rows(dtype, r.C, [&](auto *t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         return launch(expert_gather<T, decltype(v)::value>, (r.rows * parts + WARPS - 1) / WARPS, st, r, static_cast<const T *>(x),
-                      grouped, parts);
+                      static_cast<const T *>(weights), grouped, scale, parts);
     });
 }
 
-cudaError_t launch_gather_back(const Rows &r, const void *dy, const void *weights, const void *y, void *grouped,
-                               void *dweights, uint32_t *status, int dtype, cudaStream_t st) {
+cudaError_t launch_gather_back(const Rows &r, const void *dy, const void *weights, const float *ys, void *grouped,
+                               float *scale, void *dweights, uint32_t *status, int dtype, cudaStream_t st) {
     return with_rows(dtype, r.C, [&](auto *t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         return launch(expert_gather_back<T, decltype(v)::value>, (r.rows + WARPS - 1) / WARPS, st, r, static_cast<const T *>(dy),
-                      static_cast<const T *>(weights), static_cast<const T *>(y), grouped, static_cast<T *>(dweights), status);
+                      static_cast<const T *>(weights), ys, grouped, scale, static_cast<T *>(dweights), status);
     });
 }
 
-cudaError_t launch_combine(const Rows &r, const void *grouped, const void *weights, void *out, int dtype, cudaStream_t st) {
+cudaError_t launch_combine(const Rows &r, const float *ys, const void *weights, void *out, int dtype, cudaStream_t st) {
     const int parts = (r.C + 255) / 256;
     return with_rows(dtype, r.C, [&](auto *t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         return launch(expert_combine<T, decltype(v)::value>, (r.T * parts + WARPS - 1) / WARPS, st, r,
-                      static_cast<const T *>(grouped), static_cast<const T *>(weights), static_cast<T *>(out), parts);
+                      ys, static_cast<const T *>(weights), static_cast<T *>(out), parts);
     });
 }
 

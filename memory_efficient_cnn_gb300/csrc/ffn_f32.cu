@@ -47,6 +47,7 @@ struct F32Params {
     int first;
     uint32_t *status;
     Groups groups;
+    const float *scale;
     int table_at, rows_bound;
 };
 
@@ -125,7 +126,8 @@ __device__ __forceinline__ ulonglong2 words(const F2 *v) { return make_ulonglong
 // N (a multiple of 8) columns of row m (below m_end) from column n on, from their sums v (GATED: g,
 // and u); none: the row's outputs are zero.
 template <int EPI, int N>
-__device__ __forceinline__ void finish(const F32Params &p, F2 *v, F2 *u, int m, int n, int m_end, bool none = false) {
+__device__ __forceinline__ void finish(const F32Params &p, F2 *v, F2 *u, int m, int n, int m_end, bool none = false,
+                                       float scale = 1.0f) {
     const int left = p.N - n;
     if (m >= m_end || left <= 0) return;
     const int64_t at = (int64_t)m * p.ldo + n;
@@ -147,7 +149,9 @@ __device__ __forceinline__ void finish(const F32Params &p, F2 *v, F2 *u, int m, 
                     *reinterpret_cast<ulonglong2 *>(kept_a + k) = words(x);
                     *reinterpret_cast<ulonglong2 *>(kept_b + k) = words(y);
                 }
+                if (p.scale) second[2 * j] = mul2(first[2 * j], f2(scale)), second[2 * j + 1] = mul2(first[2 * j + 1], f2(scale));
             } else if (in) {
+                x[0] = mul2(x[0], f2(scale)), x[1] = mul2(x[1], f2(scale));
                 const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(kept_a + k);
                 const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(kept_b + k);
                 first[2 * j] = mul2(x[0], F2{b.x}), first[2 * j + 1] = mul2(x[1], F2{b.y});
@@ -161,7 +165,7 @@ __device__ __forceinline__ void finish(const F32Params &p, F2 *v, F2 *u, int m, 
             for (int j = 0; j < 4; ++j) first[j] = second[j] = f2(0.0f);
         }
         store_planes8(static_cast<uint16_t *>(p.out) + at + 8 * i, p.plane, first, left - 8 * i);
-        if (EPI == EPI_DGATED) store_planes8(static_cast<uint16_t *>(p.out2) + at + 8 * i, p.plane, second, left - 8 * i);
+        if (EPI == EPI_DGATED || p.scale) store_planes8(static_cast<uint16_t *>(p.out2) + at + 8 * i, p.plane, second, left - 8 * i);
     }
 }
 
@@ -346,6 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
             const int m = w.tm * ROWS + q * 32 + lane + (GROUPED && AK ? w.row0 : 0);
             const int m_end = !GROUPED || !AK ? p.M : EPI == EPI_STORE ? w.row_end : w.pad_end;
             const bool none = GROUPED && AK && m >= w.row_end;
+            const float scale = !GROUPED ? 1.0f : EPI != EPI_STORE && p.scale && !none ? p.scale[m] : 0.0f;
             if (!GROUPED && p.part) {
                 float *dst = p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
                 if (m < p.M) {
@@ -363,10 +368,10 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
                     else if (m < m_end) store_f32(out + (int64_t)m * p.ldo + n, sum[half], p.N - n);
                 }
             } else if (EPI == EPI_GATED) {
-                finish<EPI, CHUNK>(p, sum[0], sum[1], m, w.tn * (BN / 2) + c0, m_end, none);
+                finish<EPI, CHUNK>(p, sum[0], sum[1], m, w.tn * (BN / 2) + c0, m_end, none, scale);
             } else {
-                finish<EPI, CHUNK>(p, sum[0], nullptr, m, w.tn * BN + c0, m_end, none);
-                finish<EPI, CHUNK>(p, sum[1], nullptr, m, w.tn * BN + c1, m_end, none);
+                finish<EPI, CHUNK>(p, sum[0], nullptr, m, w.tn * BN + c0, m_end, none, scale);
+                finish<EPI, CHUNK>(p, sum[1], nullptr, m, w.tn * BN + c1, m_end, none, scale);
             }
         }
     }
@@ -445,6 +450,7 @@ cudaError_t launch_f32(const Product &d, uint32_t *status, bool first, void *par
     p.batch = d.batch ? 2 : 1;
     p.tiles_m = pl.tiles_m; p.tiles_n = pl.tiles_n; p.tiles = p.batch * pl.tiles_m * pl.tiles_n;
     p.groups = d.groups;
+    p.scale = d.scale;
     p.rows_bound = d.a0.k_major ? d.M : d.K;
     const int stack = d.a0.k_major ? d.groups.E : 0;
     if (d.groups.E && !d.a0.k_major) p.tiles *= d.groups.E;

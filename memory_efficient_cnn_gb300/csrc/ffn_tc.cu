@@ -59,6 +59,7 @@ struct TcParams {
     int first;                 // the call's first launch: clears the status
     uint32_t *status;
     Groups groups;
+    const float *scale;
     int table_at, rows_bound;  // where the groups lie in shared memory; rows of the grouped buffers
 };
 
@@ -112,13 +113,21 @@ __device__ __forceinline__ void fetch_kept(const TcParams &p, KeptChunk &k, int 
 }
 
 // Outputs of a chunk of rows m0 + lane from their accumulator values v (and u, or kept), columns
-// from n; every lane of the warp is here. Rows end at m_end.
-template <int EPI>
+// from n; every lane of the warp is here. Rows end at m_end. WIDE: outputs in fp32. scale: the row's.
+template <int EPI, bool WIDE>
 __device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[PAIRS], F2 (&u)[PAIRS], const KeptChunk &k, int m0,
-                                             int n, int m_end, uint16_t *out, uint32_t *stage) {
+                                             int n, int m_end, uint16_t *out, uint32_t *stage, float scale) {
     const int m = m0 + (threadIdx.x & 31);
     if (n >= p.N) return;
     const int64_t at = (int64_t)m * p.ldo + n;
+    if (WIDE) {
+        ulonglong2 *to = reinterpret_cast<ulonglong2 *>(static_cast<float *>(p.out) + at);
+        if (m >= m_end) return;
+#pragma unroll
+        for (int i = 0; i < PAIRS / 2; ++i)
+            if (4 * i < p.ldo - n) to[i] = make_ulonglong2(v[2 * i].v, v[2 * i + 1].v);
+        return;
+    }
     if (EPI == EPI_STORE) {
         if (p.vec == 2) store_rows_staged(out + (int64_t)m0 * p.ldo + n, p.ldo, v, min(32, m_end - m0), p.N - n, p.bf16, stage);
         else if (m < m_end) store_row(out + at, v, p.N - n, p.vec, p.bf16);
@@ -133,6 +142,11 @@ __device__ __forceinline__ void finish_chunk(const TcParams &p, F2 (&v)[PAIRS], 
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (8 * i < left) keep_columns(p.kept + kept_block(m, n + 8 * i, p.N), a + 4 * i, u + 4 * i);
+            if (p.scale) {
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) a[i] = mul2(v[i], f2(scale));
+                store_row(static_cast<uint16_t *>(p.out2) + at, a, left, p.vec, p.bf16);
+            }
         } else {
             gate_values<PAIRS, false>(p.act, v, u, a);
         }
@@ -359,6 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                 if (GROUPED && !AK) out += (int64_t)w.e * p.M * p.ldo;
                 // nothing accumulates where an expert has no rows, and the padding's outputs are zero
                 // whatever the weights hold
+                const float scale = GROUPED && EPI != EPI_STORE && p.scale && m < w.row_end ? p.scale[m] : 0.0f;
                 const bool none = GROUPED && (AK ? EPI != EPI_STORE && m >= w.row_end : w.k1 == 0);
 #pragma unroll 1
                 for (int c = share * SPAN; c < (share + 1) * SPAN; c += CHUNK) {
@@ -377,7 +392,12 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                     KeptChunk now = kept;
                     if (GROUPED && none && EPI == EPI_DGATED) now = KeptChunk{};
                     if (EPI == EPI_DGATED && c + CHUNK < (share + 1) * SPAN) fetch_kept(p, kept, m, m_end, w.tn * COLS + c + CHUNK);
-                    finish_chunk<EPI>(p, v, u, now, m - lane, w.tn * COLS + c, m_end, out, stage);
+                    if (GROUPED && EPI == EPI_DGATED) {
+#pragma unroll
+                        for (int i = 0; i < PAIRS; ++i) v[i] = mul2(v[i], f2(scale));
+                    }
+                    finish_chunk<EPI, GROUPED && AK && EPI == EPI_STORE>(p, v, u, now, m - lane, w.tn * COLS + c, m_end, out,
+                                                                         stage, scale);
                 }
             }
             ++n_tile;
@@ -489,6 +509,7 @@ cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool first,
     p.segs = d.epi != EPI_GATED && two && !d.batch ? 2 : 1;
     p.batch = d.batch ? 2 : 1;
     p.groups = d.groups;
+    p.scale = d.scale;
     p.rows_bound = d.a0.k_major ? d.M : d.K;
     const int stack = d.a0.k_major ? d.groups.E : 0, matrices = d.groups.E && !d.a0.k_major ? d.groups.E : 1;
     p.tiles_m = pl.tiles_m; p.tiles_n = pl.tiles_n; p.tiles = matrices * p.batch * pl.tiles_m * pl.tiles_n;

@@ -99,7 +99,10 @@ struct Product {
     // With groups, the rows of A (A k_major; M: a bound of them) meet their expert's matrix of
     // the E that lie behind one another in B; or, the rows being summed over (K: a bound of
     // them), out and out2 are E matrices behind one another, each the sum of its expert's rows.
+    // Grouped STORE of rows writes fp32. scale: a factor for each row: GATED with `kept` writes out2 =
+    // h * scale besides, DGATED scales dh.
     Groups groups;
+    const float *scale = nullptr;
     double rows = 0;       // with groups: the rows that there may be besides the padding
 };
 

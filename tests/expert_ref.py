@@ -136,8 +136,8 @@ def expert_ffn(x, experts, weights, wg, wu, wd, act):
 
 def experts_all(x, experts, weights, wg, wu, wd, act, dtype, dy=None):
     """x [T, C], experts and weights [T, k], the matrices [E, ...], all but experts in float64. As
-    block_ref.ffn_all for each expert's rows, with the roundings of the choices' outputs, of
-    weights * dy and of the choices' shares of dx besides."""
+    block_ref.ffn_all for each expert's rows, with the weights applied in fp32 and the rounding of
+    weights * h, dw_down's operand."""
     un, tiny = U[dtype], TINY[dtype]
     T, C = x.shape
     E_, F, k = wg.shape[0], wg.shape[1], experts.shape[1]
@@ -166,8 +166,9 @@ def experts_all(x, experts, weights, wg, wu, wd, act, dtype, dy=None):
         a, d = act_pair(act, g)
         ea = 1.2 * eg + EXTRA * (a.abs() + d.abs() * g.abs())
         h = a * u
-        h, eh = rounded(h, ea * u.abs() + a.abs() * eu + ea * eu + EXTRA * h.abs())
-        ys, eys = rounded(*product(h, eh, wd[e], F))
+        exact_h, eh = h, ea * u.abs() + a.abs() * eu + ea * eu + EXTRA * h.abs()
+        h, eh = rounded(h, eh)
+        ys, eys = product(h, eh, wd[e], F)
         y.index_add_(0, t, w * ys)
         ey.index_add_(0, t, w.abs() * eys)
         my.index_add_(0, t, (w * ys).abs())
@@ -176,8 +177,9 @@ def experts_all(x, experts, weights, wg, wu, wd, act, dtype, dy=None):
         dye = dy[t]
         dwt[t, j] = (dye * ys).sum(-1)
         edwt[t, j] = (dye.abs() * eys).sum(-1) + acc(C) * (dye * ys).abs().sum(-1)
-        dys, edys = rounded(w * dye, E * (w * dye).abs())
-        dh, edh = product(dys, edys, wd[e].T, C)
+        dh, edh = product(dye, None, wd[e].T, C)
+        dh, edh = w * dh, w.abs() * edh + E * (w * dh).abs()
+        hw, ehw = rounded(w * exact_h, w.abs() * (eh + E * exact_h.abs()))
         ed = 1.2 * eg + EXTRA * (d.abs() + 1)
         if act == "relu":
             ed = (g.abs() <= eg).to(g.dtype)
@@ -188,14 +190,14 @@ def experts_all(x, experts, weights, wg, wu, wd, act, dtype, dy=None):
         du, edu = rounded(du, edu)
         v1, e1 = product(dg, edg, wg[e].T, 2 * F)
         v2, e2 = product(du, edu, wu[e].T, 2 * F)
-        dxs, edxs = rounded(v1 + v2, e1 + e2)
+        dxs, edxs = v1 + v2, e1 + e2
         dx.index_add_(0, t, dxs)
         edx.index_add_(0, t, edxs)
         mdx.index_add_(0, t, dxs.abs())
         rows = max(1, t.numel())
         dws["dw_gate"].append(rounded(*both(dg.T, edg.T, xe.T, None, rows)))
         dws["dw_up"].append(rounded(*both(du.T, edu.T, xe.T, None, rows)))
-        dws["dw_down"].append(rounded(*both(dys.T, edys.T, h.T, eh.T, rows)))
+        dws["dw_down"].append(rounded(*both(dye.T, None, hw.T, ehw.T, rows)))
     out["y"] = rounded(y, ey + k * E * my)
     if dy is not None:
         out["dx"] = rounded(dx, edx + k * E * mdx)
