@@ -20,10 +20,11 @@ bool known_act(int act) {
     return act == IM2WIN_ACT_NONE || with_act(act, [](auto) {});
 }
 
-GroupArgs make(int64_t N, int64_t P, int64_t C, int64_t G, int act, int dtype) {
+// maps: tensors that a pass keeps on the chip, if it can (forward 1, backward 2).
+GroupArgs make(int64_t N, int64_t P, int64_t C, int64_t G, int act, int dtype, int maps) {
     GroupArgs a = {};
     a.N = N, a.P = P, a.C = (int)C, a.G = (int)G, a.D = (int)(C / G), a.act = act;
-    cut(a, elem_size(dtype));
+    if (!cut_resident(a, elem_size(dtype), maps)) cut(a, elem_size(dtype));
     return a;
 }
 
@@ -53,7 +54,8 @@ extern "C" {
 im2win_status im2win_group_norm_size(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, size_t *bytes) {
     if (!bytes) return IM2WIN_ERR_INVALID_ARG;
     const im2win_status s = check_dims(N, P, C, G, dtype);
-    if (s == IM2WIN_OK) *bytes = std::max<size_t>(256, Parts(make(N, P, C, G, 0, dtype)).bytes);
+    if (s == IM2WIN_OK)
+        *bytes = std::max<size_t>({256, Parts(make(N, P, C, G, 0, dtype, 1)).bytes, Parts(make(N, P, C, G, 0, dtype, 2)).bytes});
     return s;
 }
 
@@ -67,7 +69,7 @@ im2win_status im2win_group_norm(const void *x, const void *w, const void *b, voi
     if (!x || !y) return IM2WIN_ERR_INVALID_ARG;
     for (const void *p : {x, w, b, (const void *)y, (const void *)stats, (const void *)ws})
         if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
-    GroupArgs a = make(N, P, C, G, act, dtype);
+    GroupArgs a = make(N, P, C, G, act, dtype, 1);
     if (!ws || ws_bytes < Parts(a).bytes) return IM2WIN_ERR_WORKSPACE;
     a.x = x, a.w = w, a.b = b, a.y = y, a.eps = (float)eps;
     place(a, ws, stats);
@@ -93,7 +95,7 @@ im2win_status im2win_group_norm_backward(const void *dy, const void *x, const vo
         return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
     }
     if (!dx && !dw && !db) return IM2WIN_OK;
-    GroupArgs a = make(N, P, C, G, act, dtype);
+    GroupArgs a = make(N, P, C, G, act, dtype, 2);
     if (!ws || ws_bytes < Parts(a).bytes) return IM2WIN_ERR_WORKSPACE;
     a.x = x, a.dy = dy, a.w = w, a.b = b, a.dx = dx, a.dw = dw, a.db = db;
     place(a, ws, const_cast<void *>(stats));

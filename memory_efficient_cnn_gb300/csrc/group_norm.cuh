@@ -23,23 +23,69 @@ struct GroupArgs {
     // `chunks` of `len` positions an image
     int cols, slabs, rows, chunks;
     int64_t len;
+    // resident: a cluster of `chunks` CTAs keeps the `slab` channels of an image on the chip
+    bool resident;
+    int slab, tile, smem;  // bytes: the tiles, and all
 };
 
 constexpr int THREADS = 256;
-constexpr int BATCH = 8;  // positions a thread has in flight
+constexpr int64_t RESIDENT_BYTES = 16 << 20;
+constexpr size_t MAX_SMEM = 227 << 10;
+constexpr int FEW = 4;  // positions a thread has at least, if there are as many
 
 // Elements of a vector: 16 bytes where the channels allow, else pairs, else one.
 inline int vector_of(int64_t C, int size) { return C % (16 / size) == 0 ? 16 / size : C % 2 == 0 ? 2 : 1; }
 
-// Fills in the cut: eight blocks an SM, if the positions last. A constant number of SMs,
+// The shared memory of a resident CTA besides its tile: a value for each element of a vector and
+// thread (`sums` of them), their sums by channel and by group.
+inline size_t resident_extra(int slab, int D, int vector, int sums) {
+    return (size_t)sums * 4 * (THREADS * vector + std::max(THREADS, slab) + slab / D + 4);
+}
+
+// Whether an image's channels can stay on the chip between their sums and their outputs, and the
+// cut if so: a slab of whole groups by all positions, over a cluster of up to eight CTAs, `maps`
+// tensors of it (backward: x and dy). Slabs of 128 bytes of a position where they fit (shorter ones read
+// parts of DRAM bursts), tiles of up to 48 KB, so that an SM has several CTAs in different phases;
+// larger tiles only where the image does not fit otherwise.
+inline bool cut_resident(GroupArgs &a, int size, int maps) {
+    if (a.N * a.P * a.C * size * maps > RESIDENT_BYTES) return false;
+    const int v = vector_of(a.C, size);
+    int unit = a.D;
+    while (unit % v) unit += a.D;
+    for (const int64_t most : {48 << 10, 96 << 10, 190 << 10})
+        for (const int bytes : {128, 64, 32}) {
+            const int slab = std::min<int>(a.C, std::max(1, bytes / (unit * size)) * unit);
+            if (slab / v > THREADS) return false;
+            const int rows = THREADS / (slab / v);
+            auto tile = [&](int s) {
+                const int64_t len = (a.P + s - 1) / s;
+                return (len + rows - 1) / rows * THREADS * v * size * maps;
+            };
+            int s = 1;
+            while (s < 8 && tile(s) > most) s *= 2;
+            const size_t extra = resident_extra(slab, a.D, v, 2);
+            if (tile(s) > most || tile(s) + extra > MAX_SMEM) continue;
+            const int slabs = (a.C + slab - 1) / slab;
+            // spread over the SMs while each thread has two positions
+            while (s < 8 && a.N * slabs * s < 304 && a.P >= (int64_t)rows * 4 * s) s *= 2;
+            a.resident = true;
+            a.slab = slab, a.slabs = slabs, a.chunks = s;
+            a.len = (a.P + s - 1) / s;
+            a.tile = (int)tile(s), a.smem = (int)(tile(s) + extra);
+            return true;
+        }
+    return false;
+}
+
+// Fills in the cut: six blocks an SM (two rounds of the forward, three of the backward kernels), if the positions last. A constant number of SMs,
 // so that results depend on the shape alone.
 inline void cut(GroupArgs &a, int size) {
     const int vecs = a.C / vector_of(a.C, size);
     a.cols = std::min(vecs, THREADS);
     a.slabs = (vecs + a.cols - 1) / a.cols;
     a.rows = THREADS / a.cols;
-    const int64_t most = (a.P + (int64_t)a.rows * BATCH - 1) / ((int64_t)a.rows * BATCH);
-    const int64_t want = std::max<int64_t>(1, 152 * 8 / std::max<int64_t>(1, a.N * a.slabs));
+    const int64_t most = (a.P + (int64_t)a.rows * FEW - 1) / ((int64_t)a.rows * FEW);
+    const int64_t want = std::max<int64_t>(1, 152 * 6 / std::max<int64_t>(1, a.N * a.slabs));
     const int64_t chunks = std::max<int64_t>(1, std::min(most, want));
     a.len = std::max<int64_t>(1, (a.P + chunks - 1) / chunks);
     a.chunks = (int)std::max<int64_t>(1, (a.P + a.len - 1) / a.len);

@@ -93,11 +93,25 @@ __device__ __forceinline__ void with_norm_act(int act, Fn f) {
     if (act == IM2WIN_ACT_NONE) f(IntC<IM2WIN_ACT_NONE>());
     else with_act_device(act, f);
 }
+// 1 / (1 + 2^a), two values with one reciprocal: 1/p and 1/q are q and p over pq. Half the
+// instructions of the slowest unit: with a reciprocal each, silu over 51 million values took
+// 25 us of the reading and writing pass's 31 us. (a is bounded so that pq stays finite; a NaN becomes a
+// number here, which its neighbour needs: callers multiply by the value itself.)
+__device__ __forceinline__ F2 logistic2(F2 a) {
+    const F2 e = add2(exp2_2(each2(a, [](float v) { return fminf(v, 63.0f); })), f2(1.0f));
+    float p, q, inv;
+    split(e, p, q);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(p * q));
+    return f2(inv * q, inv * p);
+}
 // act(z); fp32 by the functions themselves, 16-bit types by the approximations made for them.
 template <typename T, int ACT>
 __device__ __forceinline__ F2 act_of(F2 z) {
     if constexpr (ACT == IM2WIN_ACT_NONE) return z;
     else if constexpr (sizeof(T) == 4) return each2(z, [](float v) { return act_value<ACT>(v); });
+    else if constexpr (ACT == IM2WIN_ACT_SILU) return mul2(z, logistic2(mul2(z, f2(-1.4426950408889634f))));
+    else if constexpr (ACT == IM2WIN_ACT_GELU_TANH)  // -log2(e) 2 sqrt(2 / pi) (z + 0.044715 z^3)
+        return mul2(z, logistic2(mul2(z, fma2(mul2(z, z), f2(-0.10294324f), f2(-2.3022082f)))));
     else return act_value2<ACT>(z);
 }
 // act'(z)
@@ -111,6 +125,14 @@ __device__ __forceinline__ F2 slope_of(F2 z) {
             act_both<ACT>(v, a, d);
             return d;
         });
+    } else if constexpr (ACT == IM2WIN_ACT_SILU) {  // p + z p (1 - p)
+        const F2 p = logistic2(mul2(z, f2(-1.4426950408889634f)));
+        return fma2(mul2(z, p), fma2(p, f2(-1.0f), f2(1.0f)), p);
+    } else if constexpr (ACT == IM2WIN_ACT_GELU_TANH) {  // p + z p (1 - p) a'(z); (the square is bounded: 0 times it stays 0)
+        const F2 sq = each2(mul2(z, z), [](float v) { return v > 1e38f ? 1e38f : v; });
+        const F2 p = logistic2(mul2(z, fma2(sq, f2(-0.10294324f), f2(-2.3022082f))));
+        const F2 s = mul2(mul2(z, p), fma2(p, f2(-1.0f), f2(1.0f)));
+        return fma2(s, fma2(sq, f2(0.21406859f), f2(1.5957691f)), p);
     } else {
         F2 a, d;
         act_both2<ACT>(z, a, d);
@@ -119,123 +141,221 @@ __device__ __forceinline__ F2 slope_of(F2 z) {
 }
 __device__ __forceinline__ F2 neg2(F2 a) { return mul2(a, f2(-1.0f)); }
 
-// What a thread of the position passes works on.
+// What a thread of the position passes works on: `count` positions, `step` elements apart.
 template <typename T, int V>
 struct Place {
     using Word = typename Group<T, V>::Word;
-    int64_t n, p0, p1, base;  // image, positions of the block, element (n, 0, channel)
-    int chunk, slab, row, col, c;  // c: first channel of the thread's vector
+    int64_t n, first, step;  // image, first element
+    int chunk, row, col, c, positions, count;  // c: first channel of the thread's vector; positions: of the block
     bool in;
-    __device__ explicit Place(const GroupArgs &a) {
-        int64_t id = blockIdx.x;
+    // last: in the opposite order, so that a second pass begins with what the first one has left in L2
+    __device__ Place(const GroupArgs &a, bool last = false) {
+        int64_t id = last ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
         chunk = (int)(id % a.chunks);
         id /= a.chunks;
-        slab = (int)(id % a.slabs);
+        const int slab = (int)(id % a.slabs);
         n = id / a.slabs;
-        row = threadIdx.x / a.cols, col = threadIdx.x % a.cols;
+        row = threadIdx.x / a.cols, col = threadIdx.x - row * a.cols;
         c = (slab * a.cols + col) * V;
         in = row < a.rows && c < a.C;
-        p0 = chunk * a.len, p1 = min(a.P, p0 + a.len);
-        base = n * a.P * a.C + c;
+        const int64_t p0 = chunk * a.len;
+        positions = (int)(min(a.P, p0 + a.len) - p0);
+        count = in ? count_of(a, row) : 0;
+        first = (n * a.P + p0 + row) * a.C + c;
+        step = (int64_t)a.rows * a.C;
     }
-    __device__ const Word *at(const void *x, const GroupArgs &a, int64_t p) const {
-        return reinterpret_cast<const Word *>(static_cast<const T *>(x) + base + p * a.C);
-    }
-    __device__ Word *at(void *x, const GroupArgs &a, int64_t p) const {
-        return reinterpret_cast<Word *>(static_cast<T *>(x) + base + p * a.C);
-    }
+    __device__ int count_of(const GroupArgs &a, int r) const { return r < positions ? (positions - r + a.rows - 1) / a.rows : 0; }
+    __device__ const T *at(const void *x) const { return static_cast<const T *>(x) + first; }
+    __device__ T *at(void *x) const { return static_cast<T *>(x) + first; }
 };
+// A copy of this thread's, on its way to shared memory.
+template <typename Word>
+__device__ __forceinline__ void copy_ahead(Word *to, const void *from) {
+    if constexpr (sizeof(Word) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
+    else if constexpr (sizeof(Word) >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(to)), "l"(from), "n"(sizeof(Word)) : "memory");
+    else
+        *to = *static_cast<const Word *>(from);
+}
 
-// The thread's channels' parameters and statistics.
+// The vectors of a thread's positions, of MAPS tensors, through its own slots of shared memory: DEPTH - 1
+// positions are under way while one is worked on, without registers for them (with the next vectors in
+// registers the backward kernels had 16 warps an SM and read at half of the memory's rate).
+template <int MAPS>
+constexpr int RING_DEPTH = 8 / MAPS;
+template <typename T, int V>
+constexpr int RING_BYTES = 8 * THREADS * V * (int)sizeof(T);
+template <typename T, int V, int MAPS, typename Fn>
+__device__ __forceinline__ void each_vector(const Place<T, V> &at, const T *const (&src)[MAPS], void *ring, Fn f) {
+    using Word = typename Group<T, V>::Word;
+    constexpr int DEPTH = RING_DEPTH<MAPS>;
+    Word *slots = static_cast<Word *>(ring) + threadIdx.x;
+    const T *from[MAPS];
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) from[m] = src[m];
+    int ahead = 0, put = 0, get = 0;
+    auto start = [&] {
+        if (ahead < at.count) {
+#pragma unroll
+            for (int m = 0; m < MAPS; ++m) {
+                copy_ahead(slots + (put * MAPS + m) * THREADS, from[m]);
+                from[m] += at.step;
+            }
+        }
+        ++ahead;
+        if (++put == DEPTH) put = 0;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < DEPTH - 1; ++i) start();
+#pragma unroll 1
+    for (int k = 0; k < at.count; ++k) {
+        start();
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        Word w[MAPS];
+#pragma unroll
+        for (int m = 0; m < MAPS; ++m) w[m] = slots[(get * MAPS + m) * THREADS];
+        if (++get == DEPTH) get = 0;
+        f(k, w);
+    }
+}
+
+// What makes z of the thread's channels: z = (x - mean) scale + b, scale = w / deviation.
 template <typename T, int V>
 struct Channels {
     static constexpr int PAIRS = Group<T, V>::PAIRS;
-    F2 mean[PAIRS], inv[PAIRS], w[PAIRS], b[PAIRS];
+    F2 minus_mean[PAIRS], scale[PAIRS], b[PAIRS];
     __device__ Channels(const GroupArgs &a, int64_t n, int c) {
+        each(a, n, c, [&](int i, const float2 (&s)[2], const float (&w)[2], const float (&bias)[2]) {
+            minus_mean[i] = f2(-s[0].x, -s[1].x);
+            scale[i] = f2(s[0].y * w[0], s[1].y * w[1]);
+            b[i] = f2(bias[0], bias[1]);
+        });
+    }
+    __device__ F2 z(int i, F2 deviation) const { return fma2(deviation, scale[i], b[i]); }
+    // f(pair, its channels' mean and inverse deviation, w, b)
+    template <typename Fn>
+    static __device__ void each(const GroupArgs &a, int64_t n, int c, Fn f) {
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
-            float v[4][2] = {};
+            float2 s[2] = {};
+            float w[2] = {}, b[2] = {};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 if (2 * i + j >= V) continue;
                 const int ch = c + 2 * i + j;
-                const float2 s = reinterpret_cast<const float2 *>(a.stats)[n * a.G + ch / a.D];
-                v[0][j] = s.x, v[1][j] = s.y;
-                v[2][j] = a.w ? to_f32(static_cast<const T *>(a.w)[ch]) : 1.0f;
-                v[3][j] = a.b ? to_f32(static_cast<const T *>(a.b)[ch]) : 0.0f;
+                s[j] = reinterpret_cast<const float2 *>(a.stats)[n * a.G + ch / a.D];
+                w[j] = a.w ? to_f32(static_cast<const T *>(a.w)[ch]) : 1.0f;
+                b[j] = a.b ? to_f32(static_cast<const T *>(a.b)[ch]) : 0.0f;
             }
-            mean[i] = f2(v[0][0], v[0][1]), inv[i] = f2(v[1][0], v[1][1]);
-            w[i] = f2(v[2][0], v[2][1]), b[i] = f2(v[3][0], v[3][1]);
+            f(i, s, w, b);
         }
     }
-    __device__ F2 hat(int i, F2 x) const { return mul2(add2(x, neg2(mean[i])), inv[i]); }
 };
 
-// Means and sums of squared deviations of a chunk's positions, for each channel.
+// dz of a vector and its deviations from the mean.
+template <typename T, int V, int ACT>
+__device__ __forceinline__ void gradients(const Channels<T, V> &ch, const typename Group<T, V>::Word &wx,
+                                          const typename Group<T, V>::Word &wd, F2 (&dev)[Group<T, V>::PAIRS],
+                                          F2 (&dz)[Group<T, V>::PAIRS]) {
+    to_pairs<T, V>(wx, dev);
+    to_pairs<T, V>(wd, dz);
+#pragma unroll
+    for (int i = 0; i < Group<T, V>::PAIRS; ++i) {
+        dev[i] = add2(dev[i], ch.minus_mean[i]);
+        dz[i] = mul2(dz[i], slope_of<T, ACT>(ch.z(i, dev[i])));
+    }
+}
+// dx of them: i w dz - i (m1 + hat m2), with the group's means m1 of w dz and m2 of w dz hat.
 template <typename T, int V>
-__global__ void __launch_bounds__(THREADS) gn_moments(const __grid_constant__ GroupArgs a) {
-    constexpr int PAIRS = Group<T, V>::PAIRS;
+struct Back {
+    static constexpr int PAIRS = Group<T, V>::PAIRS;
+    F2 base[PAIRS], slope[PAIRS];  // - i m1, - i^2 m2
+    // of(group): its -m1 and -m2; c: the first channel, g: a group's channels' start
+    template <typename Fn>
+    __device__ Back(const GroupArgs &a, int64_t n, int c, Fn of) {
+        Channels<T, V>::each(a, n, c, [&](int i, const float2 (&s)[2], const float (&)[2], const float (&)[2]) {
+            float2 m[2] = {};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (2 * i + j < V) m[j] = of((c + 2 * i + j) / a.D);
+            base[i] = f2(m[0].x * s[0].y, m[1].x * s[1].y);
+            slope[i] = f2(m[0].y * s[0].y * s[0].y, m[1].y * s[1].y * s[1].y);
+        });
+    }
+    __device__ F2 dx(const Channels<T, V> &ch, int i, F2 dev, F2 dz) const {
+        return fma2(dev, slope[i], fma2(dz, ch.scale[i], base[i]));
+    }
+};
+
+// A thread's channels' two sums, row `row` of the partial ones.
+template <int V, int PAIRS>
+__device__ __forceinline__ void store_channels(const GroupArgs &a, int64_t row, int c, const F2 (&v)[PAIRS], const F2 (&u)[PAIRS]) {
+    float *m = a.part + row * a.C + c, *q = m + a.N * a.chunks * a.C;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+        float lo, hi, lo2, hi2;
+        split(v[i], lo, hi);
+        split(u[i], lo2, hi2);
+        m[2 * i] = lo, q[2 * i] = lo2;
+        if (V > 1) m[2 * i + 1] = hi, q[2 * i + 1] = hi2;
+    }
+}
+
+// Means and sums of squared deviations of a chunk's positions, for each channel. A thread sums deviations from the
+// mean of its first positions; what the sum of squares loses to a pivot that is d from its mean is 2^-24 n d^2 of its n
+// values, of which an outlier among the FIRST makes at most n / FIRST^2 of its own square.
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS, 4) gn_moments(const __grid_constant__ GroupArgs a) {
+    constexpr int PAIRS = Group<T, V>::PAIRS, FIRST = 4;
     using Word = typename Group<T, V>::Word;
-    __shared__ F2 red[2 * PAIRS][THREADS];
+    __shared__ alignas(16) unsigned char ring[std::max(RING_BYTES<T, V>, 2 * PAIRS * THREADS * 8)];
+    __shared__ float counts[THREADS];
+    F2(*red)[THREADS] = reinterpret_cast<F2(*)[THREADS]>(ring);
     const Place<T, V> at(a);
     tc::allow_dependents();
     tc::grid_dependency_wait();
-    F2 mean[PAIRS], m2[PAIRS];
+    F2 mean[PAIRS], m2[PAIRS], pivot[PAIRS];
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) mean[i] = m2[i] = f2(0.0f);
-    float count = 0.0f;
-    // joins another set of values' moments to the thread's
-    auto join = [&](float n, auto other) {
-        const float total = count + n, share = n / total, scale = count * share;
+    for (int i = 0; i < PAIRS; ++i) mean[i] = m2[i] = pivot[i] = f2(0.0f);
+    if (at.count > 0) {
+#pragma unroll
+        for (int j = 0; j < FIRST; ++j) {
+            if (j >= at.count) continue;
+            F2 v[PAIRS];
+            to_pairs<T, V>(*reinterpret_cast<const Word *>(at.at(a.x) + j * at.step), v);
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) pivot[i] = add2(pivot[i], v[i]);
+        }
+        const F2 share = f2(-1.0f / (float)min(FIRST, at.count));  // (the negative pivot)
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) pivot[i] = mul2(pivot[i], share);
+    }
+    const T *const src[1] = {at.at(a.x)};
+    each_vector<T, V, 1>(at, src, ring, [&](int, const Word (&w)[1]) {
+        F2 v[PAIRS];
+        to_pairs<T, V>(w[0], v);
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
-            F2 om, o2;
-            other(i, om, o2);
-            const F2 d = add2(om, neg2(mean[i]));
-            mean[i] = fma2(d, f2(share), mean[i]);
-            m2[i] = fma2(mul2(d, d), f2(scale), add2(m2[i], o2));
+            const F2 d = add2(v[i], pivot[i]);
+            mean[i] = add2(mean[i], d);
+            m2[i] = fma2(d, d, m2[i]);
         }
-        count = total;
-    };
-    if (at.in) {
-        for (int64_t p = at.p0 + at.row; p < at.p1; p += (int64_t)a.rows * BATCH) {
-            Word word[BATCH];
-            int n = 0;
+    });
+    __syncthreads();  // (the ring becomes `red`)
+    float count = (float)at.count;
+    if (at.count > 0) {
+        const F2 share = f2(1.0f / count);
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j)
-                if (p + (int64_t)j * a.rows < at.p1) word[j] = *at.at(a.x, a, p + (int64_t)j * a.rows), n = j + 1;
-            F2 sum[PAIRS], sq[PAIRS];
-#pragma unroll
-            for (int i = 0; i < PAIRS; ++i) sum[i] = sq[i] = f2(0.0f);
-#pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                if (j >= n) continue;
-                F2 v[PAIRS];
-                to_pairs<T, V>(word[j], v);
-#pragma unroll
-                for (int i = 0; i < PAIRS; ++i) sum[i] = add2(sum[i], v[i]);
-            }
-            const float inv = 1.0f / n;
-#pragma unroll
-            for (int i = 0; i < PAIRS; ++i) sum[i] = mul2(sum[i], f2(inv));
-#pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                if (j >= n) continue;
-                F2 v[PAIRS];
-                to_pairs<T, V>(word[j], v);
-#pragma unroll
-                for (int i = 0; i < PAIRS; ++i) {
-                    const F2 d = add2(v[i], neg2(sum[i]));
-                    sq[i] = fma2(d, d, sq[i]);
-                }
-            }
-            join((float)n, [&](int i, F2 &om, F2 &o2) { om = sum[i], o2 = sq[i]; });
+        for (int i = 0; i < PAIRS; ++i) {
+            const F2 d = mul2(mean[i], share);
+            m2[i] = each2(fma2(mul2(d, mean[i]), f2(-1.0f), m2[i]), [](float v) { return v < 0.0f ? 0.0f : v; });
+            mean[i] = add2(d, neg2(pivot[i]));
         }
     }
     // over the block's rows, in halves
-    auto count_of = [&](int row) { return row >= at.p1 - at.p0 ? 0.0f : (float)((at.p1 - at.p0 - row + a.rows - 1) / a.rows); };
-    __shared__ float counts[THREADS];
-    if (at.col == 0 && at.row < a.rows) counts[at.row] = count_of(at.row);
+    if (at.col == 0 && at.row < a.rows) counts[at.row] = (float)at.count_of(a, at.row);
     for (int n = a.rows; n > 1;) {
         const int h = (n + 1) / 2;
         if (at.in && at.row >= h && at.row < n) {
@@ -246,24 +366,21 @@ __global__ void __launch_bounds__(THREADS) gn_moments(const __grid_constant__ Gr
         const float other = at.row < n - h ? counts[at.row + h] : 0.0f;
         if (at.in && other > 0.0f) {
             const int t = threadIdx.x + h * a.cols;
-            join(other, [&](int i, F2 &om, F2 &o2) { om = red[2 * i][t], o2 = red[2 * i + 1][t]; });
+            const float total = count + other, share = other / total, scale = count * share;
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                const F2 d = add2(red[2 * i][t], neg2(mean[i]));
+                mean[i] = fma2(d, f2(share), mean[i]);
+                m2[i] = fma2(mul2(d, d), f2(scale), add2(m2[i], red[2 * i + 1][t]));
+            }
+            count = total;
         }
         __syncthreads();
         if (at.col == 0 && at.row < n - h) counts[at.row] += other;
         n = h;
         __syncthreads();
     }
-    if (at.in && at.row == 0) {
-        float *m = a.part + (at.n * a.chunks + at.chunk) * a.C + at.c, *q = m + a.N * a.chunks * a.C;
-#pragma unroll
-        for (int i = 0; i < PAIRS; ++i) {
-            float lo, hi, lo2, hi2;
-            split(mean[i], lo, hi);
-            split(m2[i], lo2, hi2);
-            m[2 * i] = lo, q[2 * i] = lo2;
-            if (V > 1) m[2 * i + 1] = hi, q[2 * i + 1] = hi2;
-        }
-    }
+    if (at.in && at.row == 0) store_channels<V>(a, at.n * a.chunks + at.chunk, at.c, mean, m2);
 }
 
 // Sum over SPAN threads (a warp, or the block), the same for each and in a fixed order.
@@ -294,57 +411,54 @@ __global__ void __launch_bounds__(THREADS) gn_stats(const __grid_constant__ Grou
     const float *m = a.part + n * a.chunks * a.C + c0;
     // chunk k holds count(k) positions
     auto count = [&](int k) { return (float)(min(a.P, (k + 1) * a.len) - k * a.len); };
-    float sum = 0.0f;
-    for (int i = threadIdx.x % SPAN; i < items; i += SPAN) {
-        const int k = i / a.D;
-        sum = fmaf(m[(int64_t)k * a.C + i - k * a.D], count(k), sum);
-    }
-    const float total = (float)a.P * a.D, mean = span_sum<SPAN>(sum, s) / total;
-    float sq = 0.0f;
+    // deviations of the chunks' means from the first one
+    const float pivot = m[0];
+    float sum = 0.0f, sq = 0.0f;
+#pragma unroll 4
     for (int i = threadIdx.x % SPAN; i < items; i += SPAN) {
         const int k = i / a.D;
         const int64_t at = (int64_t)k * a.C + i - k * a.D;
-        const float d = m[at] - mean;
-        sq += fmaf(d * d, count(k), m[half + at]);
+        const float d = m[at] - pivot, nd = d * count(k);
+        sum += nd;
+        sq += fmaf(nd, d, m[half + at]);
     }
-    sq = span_sum<SPAN>(sq, s);
-    if (threadIdx.x % SPAN == 0) reinterpret_cast<float2 *>(a.stats)[id] = make_float2(mean, 1.0f / sqrtf(sq / total + a.eps));
+    const float total = (float)a.P * a.D;
+    sum = span_sum<SPAN>(sum, s);
+    sq = span_sum<SPAN>(sq, s) - sum / total * sum;
+    if (threadIdx.x % SPAN == 0)
+        reinterpret_cast<float2 *>(a.stats)[id] = make_float2(pivot + sum / total, 1.0f / sqrtf((sq < 0.0f ? 0.0f : sq) / total + a.eps));
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(THREADS) gn_apply(const __grid_constant__ GroupArgs a) {
+__global__ void __launch_bounds__(THREADS, 4) gn_apply(const __grid_constant__ GroupArgs a) {
     constexpr int PAIRS = Group<T, V>::PAIRS;
     using Word = typename Group<T, V>::Word;
-    const Place<T, V> at(a);
+    __shared__ alignas(16) unsigned char ring[RING_BYTES<T, V>];
+    const Place<T, V> at(a, true);
     tc::allow_dependents();
     tc::grid_dependency_wait();
     if (!at.in) return;
     const Channels<T, V> ch(a, at.n, at.c);
+    const T *const src[1] = {at.at(a.x)};
+    T *y = at.at(a.y);
     with_norm_act(a.act, [&](auto kind) {
-        for (int64_t p = at.p0 + at.row; p < at.p1; p += a.rows * 4) {
-            Word word[4];
+        each_vector<T, V, 1>(at, src, ring, [&](int k, const Word (&w)[1]) {
+            F2 v[PAIRS];
+            to_pairs<T, V>(w[0], v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (p + j * a.rows < at.p1) word[j] = *at.at(a.x, a, p + j * a.rows);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (p + j * a.rows >= at.p1) continue;
-                F2 v[PAIRS];
-                to_pairs<T, V>(word[j], v);
-#pragma unroll
-                for (int i = 0; i < PAIRS; ++i) v[i] = act_of<T, decltype(kind)::value>(fma2(ch.hat(i, v[i]), ch.w[i], ch.b[i]));
-                *at.at(a.y, a, p + j * a.rows) = from_pairs<T, V>(v);
-            }
-        }
+            for (int i = 0; i < PAIRS; ++i) v[i] = act_of<T, decltype(kind)::value>(ch.z(i, add2(v[i], ch.minus_mean[i])));
+            __stcs(reinterpret_cast<Word *>(y + k * at.step), from_pairs<T, V>(v));
+        });
     });
 }
 
 // Sums of dz and dz xh over a chunk's positions, for each channel.
 template <typename T, int V>
-__global__ void __launch_bounds__(THREADS) gn_back_sums(const __grid_constant__ GroupArgs a) {
-    constexpr int PAIRS = Group<T, V>::PAIRS, FEW = BATCH / 2;
+__global__ void __launch_bounds__(THREADS, 3) gn_back_sums(const __grid_constant__ GroupArgs a) {
+    constexpr int PAIRS = Group<T, V>::PAIRS;
     using Word = typename Group<T, V>::Word;
-    __shared__ F2 red[2 * PAIRS][THREADS];
+    __shared__ alignas(16) unsigned char ring[std::max(RING_BYTES<T, V>, 2 * PAIRS * THREADS * 8)];
+    F2(*red)[THREADS] = reinterpret_cast<F2(*)[THREADS]>(ring);
     const Place<T, V> at(a);
     tc::allow_dependents();
     tc::grid_dependency_wait();
@@ -353,29 +467,23 @@ __global__ void __launch_bounds__(THREADS) gn_back_sums(const __grid_constant__ 
     for (int i = 0; i < PAIRS; ++i) s0[i] = s1[i] = f2(0.0f);
     if (at.in) {
         const Channels<T, V> ch(a, at.n, at.c);
+        const T *const src[2] = {at.at(a.x), at.at(a.dy)};
         with_norm_act(a.act, [&](auto kind) {
-            for (int64_t p = at.p0 + at.row; p < at.p1; p += a.rows * FEW) {
-                Word wx[FEW], wd[FEW];
+            each_vector<T, V, 2>(at, src, ring, [&](int, const Word (&w)[2]) {
+                F2 dev[PAIRS], dz[PAIRS];
+                gradients<T, V, decltype(kind)::value>(ch, w[0], w[1], dev, dz);
 #pragma unroll
-                for (int j = 0; j < FEW; ++j)
-                    if (p + j * a.rows < at.p1) wx[j] = *at.at(a.x, a, p + j * a.rows), wd[j] = *at.at(a.dy, a, p + j * a.rows);
-#pragma unroll
-                for (int j = 0; j < FEW; ++j) {
-                    if (p + j * a.rows >= at.p1) continue;
-                    F2 x[PAIRS], d[PAIRS];
-                    to_pairs<T, V>(wx[j], x);
-                    to_pairs<T, V>(wd[j], d);
-#pragma unroll
-                    for (int i = 0; i < PAIRS; ++i) {
-                        const F2 hat = ch.hat(i, x[i]);
-                        const F2 dz = mul2(d[i], slope_of<T, decltype(kind)::value>(fma2(hat, ch.w[i], ch.b[i])));
-                        s0[i] = add2(s0[i], dz);
-                        s1[i] = fma2(dz, hat, s1[i]);
-                    }
+                for (int i = 0; i < PAIRS; ++i) {
+                    s0[i] = add2(s0[i], dz[i]);
+                    s1[i] = fma2(dz[i], dev[i], s1[i]);
                 }
-            }
+            });
+        });
+        Channels<T, V>::each(a, at.n, at.c, [&](int i, const float2 (&s)[2], const float (&)[2], const float (&)[2]) {
+            s1[i] = mul2(s1[i], f2(s[0].y, s[1].y));  // deviations to normed values
         });
     }
+    __syncthreads();  // (the ring becomes `red`)
     for (int n = a.rows; n > 1;) {
         const int h = (n + 1) / 2;
         if (at.in && at.row >= h && at.row < n) {
@@ -391,17 +499,7 @@ __global__ void __launch_bounds__(THREADS) gn_back_sums(const __grid_constant__ 
         __syncthreads();
         n = h;
     }
-    if (at.in && at.row == 0) {
-        float *m = a.part + (at.n * a.chunks + at.chunk) * a.C + at.c, *q = m + a.N * a.chunks * a.C;
-#pragma unroll
-        for (int i = 0; i < PAIRS; ++i) {
-            float lo, hi, lo2, hi2;
-            split(s0[i], lo, hi);
-            split(s1[i], lo2, hi2);
-            m[2 * i] = lo, q[2 * i] = lo2;
-            if (V > 1) m[2 * i + 1] = hi, q[2 * i + 1] = hi2;
-        }
-    }
+    if (at.in && at.row == 0) store_channels<V>(a, at.n * a.chunks + at.chunk, at.c, s0, s1);
 }
 
 // A group's means of w dz and w dz xh; SPAN threads a group.
@@ -428,62 +526,15 @@ __global__ void __launch_bounds__(THREADS) gn_back_means(const __grid_constant__
     if (threadIdx.x % SPAN == 0) reinterpret_cast<float2 *>(a.sums)[id] = make_float2(s0 / total, s1 / total);
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(THREADS) gn_back_apply(const __grid_constant__ GroupArgs a) {
-    constexpr int PAIRS = Group<T, V>::PAIRS, FEW = BATCH / 2;
-    using Word = typename Group<T, V>::Word;
-    const Place<T, V> at(a);
-    tc::allow_dependents();
-    tc::grid_dependency_wait();
-    if (!at.in) return;
-    const Channels<T, V> ch(a, at.n, at.c);
-    F2 m1[PAIRS], m2[PAIRS];
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-        float v[2][2] = {};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (2 * i + j >= V) continue;
-            const float2 s = reinterpret_cast<const float2 *>(a.sums)[at.n * a.G + (at.c + 2 * i + j) / a.D];
-            v[0][j] = -s.x, v[1][j] = -s.y;
-        }
-        m1[i] = f2(v[0][0], v[0][1]), m2[i] = f2(v[1][0], v[1][1]);
-    }
-    with_norm_act(a.act, [&](auto kind) {
-        for (int64_t p = at.p0 + at.row; p < at.p1; p += a.rows * FEW) {
-            Word wx[FEW], wd[FEW];
-#pragma unroll
-            for (int j = 0; j < FEW; ++j)
-                if (p + j * a.rows < at.p1) wx[j] = *at.at(a.x, a, p + j * a.rows), wd[j] = *at.at(a.dy, a, p + j * a.rows);
-#pragma unroll
-            for (int j = 0; j < FEW; ++j) {
-                if (p + j * a.rows >= at.p1) continue;
-                F2 x[PAIRS], d[PAIRS];
-                to_pairs<T, V>(wx[j], x);
-                to_pairs<T, V>(wd[j], d);
-#pragma unroll
-                for (int i = 0; i < PAIRS; ++i) {
-                    const F2 hat = ch.hat(i, x[i]);
-                    const F2 dz = mul2(d[i], slope_of<T, decltype(kind)::value>(fma2(hat, ch.w[i], ch.b[i])));
-                    d[i] = mul2(fma2(hat, m2[i], fma2(dz, ch.w[i], m1[i])), ch.inv[i]);
-                }
-                *at.at(a.dx, a, p + j * a.rows) = from_pairs<T, V>(d);
-            }
-        }
-    });
-}
-
 // dw and db: the channels' sums over images and chunks; 32 channels by 8 runs of rows a block.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) gn_back_params(const __grid_constant__ GroupArgs a) {
+__device__ void sum_params(const GroupArgs &a, int block) {
     __shared__ float red[2][8][33];
-    tc::allow_dependents();
-    tc::grid_dependency_wait();
-    const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = block * 32 + lane;
     const int64_t rows = a.N * a.chunks, half = rows * a.C;
     float s0 = 0.0f, s1 = 0.0f;
     if (c < a.C) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t r = run; r < rows; r += 8) s0 += a.part[r * a.C + c], s1 += a.part[half + r * a.C + c];
     }
     red[0][run][lane] = s0, red[1][run][lane] = s1;
@@ -495,19 +546,348 @@ __global__ void __launch_bounds__(THREADS) gn_back_params(const __grid_constant_
     for (int i = 0; i < 8; ++i) t += red[run][i][lane];
     if (out) out[c] = from_f32<T>(t);
 }
+template <typename T>
+__global__ void __launch_bounds__(THREADS) gn_back_params(const __grid_constant__ GroupArgs a) {
+    tc::allow_dependents();
+    tc::grid_dependency_wait();
+    sum_params<T>(a, blockIdx.x);
+}
 
-template <typename K>
-cudaError_t launch(K kernel, int64_t blocks, cudaStream_t st, const GroupArgs &a) {
+// dx; the first `param_blocks` blocks make dw and db meanwhile.
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS, 3) gn_back_apply(const __grid_constant__ GroupArgs a, int param_blocks) {
+    constexpr int PAIRS = Group<T, V>::PAIRS;
+    using Word = typename Group<T, V>::Word;
+    __shared__ alignas(16) unsigned char ring[RING_BYTES<T, V>];
+    tc::allow_dependents();
+    tc::grid_dependency_wait();
+    if ((int)blockIdx.x < param_blocks) {
+        sum_params<T>(a, blockIdx.x);
+        return;
+    }
+    const Place<T, V> at(a, true);
+    if (!at.in) return;
+    const Channels<T, V> ch(a, at.n, at.c);
+    const Back<T, V> back(a, at.n, at.c, [&](int g) {
+        const float2 s = reinterpret_cast<const float2 *>(a.sums)[at.n * a.G + g];
+        return make_float2(-s.x, -s.y);
+    });
+    T *dx = at.at(a.dx);
+    const T *const src[2] = {at.at(a.x), at.at(a.dy)};
+    with_norm_act(a.act, [&](auto kind) {
+        each_vector<T, V, 2>(at, src, ring, [&](int k, const Word (&w)[2]) {
+            F2 dev[PAIRS], dz[PAIRS];
+            gradients<T, V, decltype(kind)::value>(ch, w[0], w[1], dev, dz);
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) dz[i] = back.dx(ch, i, dev[i], dz[i]);
+            __stcs(reinterpret_cast<Word *>(dx + k * at.step), from_pairs<T, V>(dz));
+        });
+    });
+}
+
+// ---- resident: an image's slab of channels stays in shared memory between the passes over it
+
+// What a CTA of a cluster works on: positions p0 to p1 of image n, channels c0 to c0 + sc. A thread keeps to
+// one vector of channels and takes every rows-th position; its i-th vector lies at tile[i * THREADS + tid].
+template <typename T, int V>
+struct Seat {
+    using Word = typename Group<T, V>::Word;
+    int64_t n, p0, p1, base;
+    int rank, c0, sc, cols, rows, row, col, c;
+    bool in;
+    __device__ explicit Seat(const GroupArgs &a) {
+        rank = blockIdx.x % a.chunks;
+        const int64_t id = blockIdx.x / a.chunks;
+        n = id / a.slabs;
+        c0 = (int)(id - n * a.slabs) * a.slab;
+        sc = min(a.slab, a.C - c0);
+        cols = sc / V, rows = THREADS / cols;
+        row = threadIdx.x / cols, col = threadIdx.x - row * cols;
+        in = row < rows;
+        c = c0 + col * V;
+        p0 = min(a.P, rank * a.len), p1 = min(a.P, p0 + a.len);
+        base = n * a.P * a.C + c;
+    }
+    // the thread's vectors of x on their way to the tile
+    __device__ void fetch(const GroupArgs &a, const void *x, Word *tile) const {
+        if (!in) return;
+        const T *from = static_cast<const T *>(x) + base + (p0 + row) * a.C;
+        const int64_t step = (int64_t)rows * a.C;
+        Word *to = tile + threadIdx.x;
+        for (int64_t p = p0 + row; p < p1; p += rows, from += step, to += THREADS) copy_ahead(to, from);
+    }
+    // f(i-th vector's pairs, position) for each of the thread's vectors
+    template <typename Fn>
+    __device__ void each(Fn f) const {
+        if (!in) return;
+        int at = threadIdx.x;
+        for (int64_t p = p0 + row; p < p1; p += rows, at += THREADS) f(at, p);
+    }
+};
+__device__ __forceinline__ void wait_fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Scratch of the sums over a CTA.
+struct Sums {
+    float *each, *channel, *group;  // [SUMS][THREADS * V], [SUMS][segments * sc], [SUMS][groups]
+    int segments;
+};
+// The sums of SUMS values over the CTA's positions, by channel (in `segments` parts) and, `weight` times them,
+// by group. Every thread calls this; the results may be read after it.
+template <typename T, int V, int SUMS, typename Fn>
+__device__ __forceinline__ void sum_groups(const GroupArgs &a, const Seat<T, V> &at, Sums &s,
+                                           const F2 (&v)[SUMS][Group<T, V>::PAIRS], Fn weight) {
+    constexpr int EACH = THREADS * V;
+    const int wide = max(THREADS, at.sc), groups = at.sc / a.D;
+    if (at.in) {
+#pragma unroll
+        for (int q = 0; q < SUMS; ++q)
+#pragma unroll
+            for (int i = 0; i < Group<T, V>::PAIRS; ++i) {
+                float lo, hi;
+                split(v[q][i], lo, hi);
+                s.each[q * EACH + threadIdx.x * V + 2 * i] = lo;
+                if (V > 1) s.each[q * EACH + threadIdx.x * V + 2 * i + 1] = hi;
+            }
+    }
+    __syncthreads();
+    s.segments = max(1, THREADS / at.sc);
+    const int per = (at.rows + s.segments - 1) / s.segments;
+    for (int id = threadIdx.x; id < s.segments * at.sc; id += THREADS) {
+        const int seg = id / at.sc, c = id - seg * at.sc;
+        float sum[SUMS] = {};
+        for (int r = seg * per; r < min(at.rows, (seg + 1) * per); ++r)
+#pragma unroll
+            for (int q = 0; q < SUMS; ++q) sum[q] += s.each[q * EACH + r * at.sc + c];
+#pragma unroll
+        for (int q = 0; q < SUMS; ++q) s.channel[q * wide + id] = sum[q];
+    }
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int g = warp; g < groups; g += THREADS / 32) {
+        float sum[SUMS] = {};
+        for (int j = lane; j < s.segments * a.D; j += 32) {
+            const int seg = j / a.D, c = g * a.D + j - seg * a.D;
+            const float w = weight(c);
+#pragma unroll
+            for (int q = 0; q < SUMS; ++q) sum[q] = fmaf(w, s.channel[q * wide + seg * at.sc + c], sum[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < SUMS; ++q) {
+            sum[q] = span_sum<32>(sum[q], nullptr);
+            if (lane == 0) s.group[q * groups + g] = sum[q];
+        }
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ float peer_read(const float *p, int rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The parts of a resident CTA's shared memory behind its tiles.
+template <typename T, int V, int SUMS>
+__device__ __forceinline__ Sums scratch(const GroupArgs &a, int sc, unsigned char *at) {
+    float *p = reinterpret_cast<float *>(at);
+    return {p, p + SUMS * THREADS * V, p + SUMS * (THREADS * V + max(THREADS, sc)), 0};
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ GroupArgs a) {
+    constexpr int PAIRS = Group<T, V>::PAIRS;
+    using Word = typename Group<T, V>::Word;
+    extern __shared__ uint4 dyn[];
+    const Seat<T, V> at(a);
+    Word *tile = reinterpret_cast<Word *>(dyn);
+    Sums s = scratch<T, V, 2>(a, at.sc, reinterpret_cast<unsigned char *>(dyn) + a.tile);
+    tc::allow_dependents();
+    tc::grid_dependency_wait();
+    at.fetch(a, a.x, tile);
+    F2 w[PAIRS], b[PAIRS];
+    int group[V];  // of the thread's channels, in the slab
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+        float v[2][2] = {};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (2 * i + j >= V) continue;
+            const int ch = min(at.c + 2 * i + j, a.C - 1);
+            group[2 * i + j] = min(at.col * V + 2 * i + j, at.sc - 1) / a.D;
+            v[0][j] = a.w ? to_f32(static_cast<const T *>(a.w)[ch]) : 1.0f;
+            v[1][j] = a.b ? to_f32(static_cast<const T *>(a.b)[ch]) : 0.0f;
+        }
+        w[i] = f2(v[0][0], v[0][1]), b[i] = f2(v[1][0], v[1][1]);
+    }
+    auto of_groups = [&](const float *of, F2 (&v)[PAIRS]) {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) v[i] = f2(of[group[2 * i]], V > 1 ? of[group[V > 1 ? 2 * i + 1 : 0]] : 0.0f);
+    };
+    wait_fetched();
+    const int groups = at.sc / a.D;
+    F2 sum[1][PAIRS], mean[PAIRS], inv[PAIRS];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) sum[0][i] = f2(0.0f);
+    at.each([&](int j, int64_t) {
+        F2 v[PAIRS];
+        to_pairs<T, V>(tile[j], v);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) sum[0][i] = add2(sum[0][i], v[i]);
+    });
+    sum_groups<T, V, 1>(a, at, s, sum, [](int) { return 1.0f; });
+    // the CTA's own mean, and the squared deviations from it
+    float *means = s.group + groups, *m2 = s.group;
+    const float count = (float)(at.p1 - at.p0) * a.D;
+    for (int g = threadIdx.x; g < groups; g += THREADS) means[g] = count > 0.0f ? s.group[g] / count : 0.0f;
+    __syncthreads();
+    of_groups(means, mean);
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) sum[0][i] = f2(0.0f);
+    at.each([&](int j, int64_t) {
+        F2 v[PAIRS];
+        to_pairs<T, V>(tile[j], v);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            const F2 d = add2(v[i], neg2(mean[i]));
+            sum[0][i] = fma2(d, d, sum[0][i]);
+        }
+    });
+    sum_groups<T, V, 1>(a, at, s, sum, [](int) { return 1.0f; });
+    // the cluster's; results go where no other CTA reads
+    if (a.chunks > 1) cluster_barrier();
+    float *result = s.channel;  // [2][groups]
+    for (int g = threadIdx.x; g < groups; g += THREADS) {
+        float m = means[g], q = m2[g];
+        if (a.chunks > 1) {
+            float total = 0.0f;
+            m = 0.0f, q = 0.0f;
+            for (int r = 0; r < a.chunks; ++r) total += peer_read(means + g, r) * (float)(min(a.P, (r + 1) * a.len) - min(a.P, r * a.len));
+            m = total / (float)a.P;
+            for (int r = 0; r < a.chunks; ++r) {
+                const float d = peer_read(means + g, r) - m;
+                q += fmaf(d * d, (float)(min(a.P, (r + 1) * a.len) - min(a.P, r * a.len)) * a.D, peer_read(m2 + g, r));
+            }
+        }
+        const float i = 1.0f / sqrtf(q / ((float)a.P * a.D) + a.eps);
+        result[g] = m, result[groups + g] = i;
+        if (a.stats && at.rank == 0) reinterpret_cast<float2 *>(a.stats)[at.n * a.G + at.c0 / a.D + g] = make_float2(m, i);
+    }
+    // (the others' scratch is read no more after this: they may go on, or end)
+    if (a.chunks > 1) cluster_barrier();
+    else __syncthreads();
+    of_groups(result, mean);
+    of_groups(result + groups, inv);
+    with_norm_act(a.act, [&](auto kind) {
+        at.each([&](int j, int64_t p) {
+            F2 v[PAIRS];
+            to_pairs<T, V>(tile[j], v);
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i)
+                v[i] = act_of<T, decltype(kind)::value>(fma2(mul2(add2(v[i], neg2(mean[i])), inv[i]), w[i], b[i]));
+            *reinterpret_cast<Word *>(static_cast<T *>(a.y) + at.base + p * a.C) = from_pairs<T, V>(v);
+        });
+    });
+}
+
+// Backward: x and dy in shared memory; the channels' sums go to `part` for dw and db.
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS) gn_back_resident(const __grid_constant__ GroupArgs a) {
+    constexpr int PAIRS = Group<T, V>::PAIRS;
+    using Word = typename Group<T, V>::Word;
+    extern __shared__ uint4 dyn[];
+    const Seat<T, V> at(a);
+    Word *xs = reinterpret_cast<Word *>(dyn);
+    Word *ds = reinterpret_cast<Word *>(reinterpret_cast<unsigned char *>(dyn) + a.tile / 2);
+    Sums s = scratch<T, V, 2>(a, at.sc, reinterpret_cast<unsigned char *>(dyn) + a.tile);
+    tc::allow_dependents();
+    tc::grid_dependency_wait();
+    at.fetch(a, a.x, xs);
+    at.fetch(a, a.dy, ds);
+    const Channels<T, V> ch(a, at.n, at.in ? at.c : at.c0);
+    wait_fetched();
+    F2 sum[2][PAIRS];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) sum[0][i] = sum[1][i] = f2(0.0f);
+    with_norm_act(a.act, [&](auto kind) {
+        at.each([&](int j, int64_t) {
+            F2 dev[PAIRS], dz[PAIRS];
+            gradients<T, V, decltype(kind)::value>(ch, xs[j], ds[j], dev, dz);
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                sum[0][i] = add2(sum[0][i], dz[i]);
+                sum[1][i] = fma2(dz[i], dev[i], sum[1][i]);
+            }
+        });
+    });
+    Channels<T, V>::each(a, at.n, at.in ? at.c : at.c0, [&](int i, const float2 (&t)[2], const float (&)[2], const float (&)[2]) {
+        sum[1][i] = mul2(sum[1][i], f2(t[0].y, t[1].y));  // deviations to normed values
+    });
+    sum_groups<T, V, 2>(a, at, s, sum, [&](int c) { return a.w ? to_f32(static_cast<const T *>(a.w)[at.c0 + c]) : 1.0f; });
+    const int groups = at.sc / a.D, wide = max(THREADS, at.sc);
+    if (a.dw || a.db) {
+        const int64_t row = (at.n * a.chunks + at.rank) * a.C + at.c0, half = a.N * a.chunks * a.C;
+        for (int c = threadIdx.x; c < at.sc; c += THREADS) {
+            float t[2] = {};
+            for (int seg = 0; seg < s.segments; ++seg) t[0] += s.channel[seg * at.sc + c], t[1] += s.channel[wide + seg * at.sc + c];
+            a.part[row + c] = t[0], a.part[half + row + c] = t[1];
+        }
+    }
+    if (!a.dx) return;  // (of every CTA alike)
+    if (a.chunks > 1) cluster_barrier();
+    else __syncthreads();
+    float *result = s.each;  // [2][groups]
+    for (int g = threadIdx.x; g < groups; g += THREADS) {
+        float t[2] = {};
+        for (int r = 0; r < a.chunks; ++r)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) t[q] += a.chunks > 1 ? peer_read(s.group + q * groups + g, r) : s.group[q * groups + g];
+        const float total = (float)a.P * a.D;
+        result[g] = -t[0] / total, result[groups + g] = -t[1] / total;
+    }
+    if (a.chunks > 1) cluster_barrier();
+    else __syncthreads();
+    const int g0 = at.c0 / a.D;
+    const Back<T, V> back(a, at.n, at.in ? at.c : at.c0, [&](int g) { return make_float2(result[g - g0], result[groups + g - g0]); });
+    with_norm_act(a.act, [&](auto kind) {
+        at.each([&](int j, int64_t p) {
+            F2 dev[PAIRS], dz[PAIRS];
+            gradients<T, V, decltype(kind)::value>(ch, xs[j], ds[j], dev, dz);
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) dz[i] = back.dx(ch, i, dev[i], dz[i]);
+            *reinterpret_cast<Word *>(static_cast<T *>(a.dx) + at.base + p * a.C) = from_pairs<T, V>(dz);
+        });
+    });
+}
+
+template <typename K, typename... A>
+cudaError_t launch_with(K kernel, int64_t blocks, cudaStream_t st, int smem, int cluster, const A &...args) {
+    if (smem) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = smem;
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(THREADS);
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename K>
+cudaError_t launch(K kernel, int64_t blocks, cudaStream_t st, const GroupArgs &a, int smem = 0, int cluster = 1) {
+    return launch_with(kernel, blocks, st, smem, cluster, a);
 }
 
 // A block a group where a warp would take more than 32 loads of each sum.
@@ -530,6 +910,7 @@ cudaError_t launch_forward(const GroupArgs &a, cudaStream_t st) {
     const int64_t blocks = a.N * a.slabs * a.chunks;
     return with_vector<T>(a, [&](auto v) {
         constexpr int V = decltype(v)::value;
+        if (a.resident) return launch(gn_resident<T, V>, blocks, st, a, a.smem, a.chunks);
         cudaError_t e = launch(gn_moments<T, V>, blocks, st, a);
         if (e == cudaSuccess) e = by_block(a) ? launch(gn_stats<THREADS>, group_blocks(a), st, a) : launch(gn_stats<32>, group_blocks(a), st, a);
         return e == cudaSuccess ? launch(gn_apply<T, V>, blocks, st, a) : e;
@@ -541,11 +922,12 @@ cudaError_t launch_backward(const GroupArgs &a, cudaStream_t st) {
     const int64_t blocks = a.N * a.slabs * a.chunks;
     return with_vector<T>(a, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        cudaError_t e = launch(gn_back_sums<T, V>, blocks, st, a);
-        if (a.dx) {
+        cudaError_t e = a.resident ? launch(gn_back_resident<T, V>, blocks, st, a, a.smem, a.chunks) : launch(gn_back_sums<T, V>, blocks, st, a);
+        if (a.dx && !a.resident) {
             if (e == cudaSuccess)
                 e = by_block(a) ? launch(gn_back_means<T, THREADS>, group_blocks(a), st, a) : launch(gn_back_means<T, 32>, group_blocks(a), st, a);
-            if (e == cudaSuccess) e = launch(gn_back_apply<T, V>, blocks, st, a);
+            const int params = a.dw || a.db ? (a.C + 31) / 32 : 0;
+            return e == cudaSuccess ? launch_with(gn_back_apply<T, V>, blocks + params, st, 0, 1, a, params) : e;
         }
         if (e == cudaSuccess && (a.dw || a.db)) e = launch(gn_back_params<T>, (a.C + 31) / 32, st, a);
         return e;
