@@ -58,6 +58,8 @@ struct Problem {
         : T(T_), rows(grouped_rows(T_ * k_, E_)), pairs(T_ * k_), k((int)k_), E((int)E_), C((int)C_), F((int)F_), dtype(dtype_),
           act(act_), f32(dtype_ == IM2WIN_F32), Cp((C_ + 7) / 8 * 8), Fp((F_ + 7) / 8 * 8) {}
 
+    // inference of few pairs has kernels of its own
+    bool few() const { return pairs <= FEW_PAIRS; }
     size_t operand(int64_t n, int64_t pitch) const { return (size_t)(n * pitch) * (f32 ? 6 : 2); }
     size_t result() const { return (size_t)(rows * Cp) * 4; }  // ys, dxs
     bool copies(int64_t cols) const { return f32 || cols % 8 != 0; }
@@ -99,9 +101,15 @@ struct SavedParts {
 
 // A forward call's workspace; without `saved`, its parts too.
 struct ForwardParts {
-    size_t hist, wg, wu, wd, own, bytes;
+    size_t hist, wg, wu, wd, own, h, h_lo, bytes;
     ForwardParts(const Problem &q, bool saved) {
         Parts p(kStatusBytes);
+        h = p.add(q.few() && !saved ? (size_t)q.pairs * (q.f32 ? q.F * (size_t)4 : q.Fp * (size_t)2) : 0);
+        h_lo = p.add(q.few() && !saved && !q.f32 ? (size_t)q.pairs * q.Fp * 2 : 0);
+        if (q.few() && !saved) {
+            hist = wg = wu = wd = own = bytes = p.end;
+            return;
+        }
         const int64_t per = pairs_per_block(q.pairs), blocks = (q.pairs + per - 1) / per;
         hist = p.add(blocks > 1 ? (size_t)blocks * q.E * 4 : 0);
         wg = p.add(q.copies(q.C) ? q.operand((int64_t)q.E * q.F, q.Cp) : 0);
@@ -198,9 +206,14 @@ im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const voi
     const Problem q(T, k, E, C, F, act, dtype);
     const ForwardParts parts(q, saved != nullptr);
     if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (q.few() && !saved) {
+        const ExpertFew f = {(int)T, q.k, q.E, q.C, q.F, act, x, weights, w_gate, w_up, w_down, experts, y, at(ws, parts.h),
+                             at(ws, parts.h_lo), q.f32 ? (int64_t)q.F : q.Fp, static_cast<uint32_t *>(ws)};
+        return launch_expert_few(f, dtype, st) == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
+    }
     const SavedParts own(q, saved ? 0 : parts.own, saved != nullptr);
     void *keep = saved ? saved : ws;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Rows rows = rows_of(q, own, keep);
     Sequence seq{q, ws, st};
     seq.step([&] { return launch_plan(rows, experts, ints(ws, parts.hist), static_cast<uint32_t *>(ws), st); });

@@ -49,5 +49,18 @@ cudaError_t launch_gather_back(const Rows &r, const void *dy, const void *weight
 // out[t] = sum over the row's choices of weights (null: 1) * ys[slot], in their order.
 cudaError_t launch_combine(const Rows &r, const float *ys, const void *weights, void *out, int dtype, cudaStream_t st);
 
+// Inference of few rows: up to FEW_PAIRS pairs. h and its remainder h_lo (16-bit types) have T k rows of
+// ldh elements, a multiple of 8 there.
+constexpr int FEW_PAIRS = 64;
+struct ExpertFew {
+    int T, k, E, C, F, act;
+    const void *x, *weights, *w_gate, *w_up, *w_down;
+    const int32_t *experts;
+    void *y, *h, *h_lo;
+    int64_t ldh;
+    uint32_t *status;
+};
+cudaError_t launch_expert_few(const ExpertFew &f, int dtype, cudaStream_t st);
+
 }  // namespace ffn
 }  // namespace im2win

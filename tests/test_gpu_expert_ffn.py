@@ -23,7 +23,7 @@ def make(T, k, E, C, F, dt, seed=0, choose="uneven"):
         experts = torch.randint(-2, E + 2, (T, k), generator=g)
     else:
         experts = (torch.rand(T, E, generator=g) * (1.0 + torch.arange(E) % 3)).topk(min(k, E), -1)[1]
-        experts = torch.cat([experts, experts[:, :k - experts.shape[1]]], -1)
+        experts = experts.repeat(1, -(-k // experts.shape[1]))[:, :k]
     weights = torch.softmax(torch.randn(T, k, generator=g), -1).to(DT[dt])
     return (n(T, C), experts.to(torch.int32), weights, n(E, F, C, std=C ** -0.5), n(E, F, C, std=C ** -0.5),
             n(E, C, F, std=F ** -0.5), n(T, C, std=0.5))
@@ -72,6 +72,28 @@ def test_large(dt, T, k, E, C, F):
 @pytest.mark.parametrize("E", [300, 1024])
 def test_many_experts(E):
     check(500, 3, E, 24, 40, "bf16", seed=E)
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("choose", ["uneven", "one", "any"])
+@pytest.mark.parametrize("T,k,E,C,F", [(1, 2, 8, 512, 1024), (32, 2, 6, 520, 264), (16, 4, 3, 1000, 366), (64, 1, 20, 64, 200),
+                                       (2, 32, 9, 48, 33), (5, 3, 40, 1030, 514), (13, 5, 4, 72, 4100)])
+def test_few_rows(dt, choose, T, k, E, C, F):
+    """Inference of up to 64 pairs, which has kernels of its own, and 65 beside it."""
+    x, experts, weights, wg, wu, wd, _ = make(T, k, E, C, F, dt, T + F, choose)
+    want = ref.experts_all(x.double(), experts, weights.double(), wg.double(), wu.double(), wd.double(), "gelu", DT[dt])
+    y = mec.expert_ffn(*(t.cuda() for t in (x, experts, weights, wg, wu, wd)), act="gelu")
+    block_ref.check(dict(y=y), want, f"{dt} {choose} {(T, k, E, C, F)}")
+
+
+def test_few_rows_touch_their_experts_alone():
+    """The other experts' weights are not read into the result, whatever they hold."""
+    for dt in DT:
+        x, experts, weights, wg, wu, wd, _ = (t.cuda() for t in make(3, 2, 8, 264, 136, dt))
+        want = mec.expert_ffn(x, experts, weights, wg, wu, wd)
+        for e in set(range(8)) - set(experts.flatten().tolist()):
+            wg[e] = wu[e] = wd[e] = float("nan")
+        assert torch.equal(mec.expert_ffn(x, experts, weights, wg, wu, wd), want)
 
 
 def test_no_choice_left():
