@@ -465,9 +465,11 @@ im2win_status im2win_clip_grad_norm(const void *const *grads, void *const *outs,
  * 2^31, C a multiple of G (else IM2WIN_ERR_INVALID_ARG).
  * stats[N][G][2] (fp32; NULL: not kept) receives each group's mean and 1/sqrt(var +
  * eps) for the backward call. y may be x itself and must not overlap it otherwise.
- * A NaN or infinity spoils its own image's group and no other.
+ * A NaN or infinity spoils its own image's group and no other. im2win_group_norm_size gives
+ * the workspace of a forward (backward = 0) or backward call, host arithmetic only; it may be
+ * zero, and ws then NULL.
  */
-im2win_status im2win_group_norm_size(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, size_t *bytes);
+im2win_status im2win_group_norm_size(int backward, int64_t N, int64_t P, int64_t C, int64_t G, int dtype, size_t *bytes);
 im2win_status im2win_group_norm(const void *x, const void *w, const void *b, void *y, void *stats, void *ws,
                                 size_t ws_bytes, int64_t N, int64_t P, int64_t C, int64_t G, int act, double eps,
                                 int dtype, void *stream);
@@ -478,7 +480,7 @@ im2win_status im2win_group_norm(const void *x, const void *w, const void *b, voi
  * dx = (w dz - mean(w dz) - xh mean(w dz xh)) / sqrt(var + eps), the means over the
  * image's group. Each of dx, dw, db may be NULL (not computed); dw without w, or db
  * without b, is an error. dx may be dy itself; no output may overlap an input otherwise.
- * With N * P = 0 the sums are zero. The workspace is of the same size.
+ * With N * P = 0 the sums are zero.
  */
 im2win_status im2win_group_norm_backward(const void *dy, const void *x, const void *stats, const void *w, const void *b,
                                          void *dx, void *dw, void *db, void *ws, size_t ws_bytes, int64_t N, int64_t P,

@@ -97,7 +97,7 @@ def lib() -> ctypes.CDLL:
             L.im2win_residual_norm_backward.argtypes = [vp, vp] + block + [vp] * 9 + [sz, i64, i64, ci, vp]
             L.im2win_clip_grad_norm_size.argtypes = [vp, i64, ctypes.POINTER(sz)]
             L.im2win_clip_grad_norm.argtypes = [vp, vp, vp, vp, i64, f64, f64, vp, vp, sz, vp]
-            L.im2win_group_norm_size.argtypes = [i64, i64, i64, i64, ci, ctypes.POINTER(sz)]
+            L.im2win_group_norm_size.argtypes = [ci, i64, i64, i64, i64, ci, ctypes.POINTER(sz)]
             L.im2win_group_norm.argtypes = [vp] * 6 + [sz, i64, i64, i64, i64, ci, f64, ci, vp]
             L.im2win_group_norm_backward.argtypes = [vp] * 9 + [sz, i64, i64, i64, i64, ci, ci, vp]
             L.im2win_expert_route.argtypes = [vp, vp, vp, i64, i64, i64, ci, ci, vp]

@@ -2,6 +2,7 @@
 // conversion to and from fp32, 16-byte vectors, and the activations.
 #pragma once
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -53,6 +54,21 @@ inline bool with_dtype(int dtype, Fn f) {
         case IM2WIN_BF16: f((bf16_t *)nullptr); return true;
         default: return false;
     }
+}
+
+// Lets a kernel have up to `bytes` (always the same for it) of dynamic shared memory. Once for each
+// device: asking takes longer than a launch.
+template <auto Kernel>
+inline cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

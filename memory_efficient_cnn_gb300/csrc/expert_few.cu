@@ -316,12 +316,10 @@ __global__ void __launch_bounds__(THREADS, 2) expert_few_fma(const __grid_consta
     if constexpr (!GATED) write_outputs<float, COLS>(p, o, t.tile);
 }
 
-template <typename K>
-cudaError_t launch(K kernel, int64_t blocks, size_t smem, int cluster, cudaStream_t st, const ExpertFewParams &p) {
-    if (smem) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+template <auto Kernel>
+cudaError_t launch(int64_t blocks, size_t smem, int cluster, cudaStream_t st, const ExpertFewParams &p) {
+    const cudaError_t e = smem ? allow_smem<Kernel>((int)smem) : cudaSuccess;
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(THREADS);
@@ -335,7 +333,7 @@ cudaError_t launch(K kernel, int64_t blocks, size_t smem, int cluster, cudaStrea
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, Kernel, p);
 }
 
 template <bool GATED>
@@ -352,14 +350,14 @@ cudaError_t launch_few(ExpertFewParams &p, int dtype, cudaStream_t st) {
         blocks = (int64_t)p.tiles * p.shares;
     }
     if (f32) {
-        return p.K % 4 == 0 ? launch(expert_few_fma<4, GATED>, blocks, 0, p.shares, st, p)
-                            : launch(expert_few_fma<1, GATED>, blocks, 0, p.shares, st, p);
+        return p.K % 4 == 0 ? launch<expert_few_fma<4, GATED>>(blocks, 0, p.shares, st, p)
+                            : launch<expert_few_fma<1, GATED>>(blocks, 0, p.shares, st, p);
     }
     auto go = [&](auto v, auto vb) {
         constexpr int V = decltype(v)::value, VB = decltype(vb)::value;
         const size_t smem = (V == 8 ? Ring<RING_VECS<1, GATED>>::BYTES : 0) + WARPS * (GATED ? 2 : 1) * 16 * GROUP * 4;
-        return bf16 ? launch(expert_few_mma<true, V, VB, GATED>, blocks, smem, p.shares, st, p)
-                    : launch(expert_few_mma<false, V, VB, GATED>, blocks, smem, p.shares, st, p);
+        return bf16 ? launch<expert_few_mma<true, V, VB, GATED>>(blocks, smem, p.shares, st, p)
+                    : launch<expert_few_mma<false, V, VB, GATED>>(blocks, smem, p.shares, st, p);
     };
     // x has the weights' row length; h has rows of whole vectors
     if (p.K % 8 == 0) return go(IntC<8>(), IntC<8>());

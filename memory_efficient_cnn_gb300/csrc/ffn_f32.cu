@@ -413,11 +413,10 @@ __global__ void __launch_bounds__(256) f32_join(const __grid_constant__ F32Param
 
 template <bool AK, bool BKM, int EPI, bool GROUPED>
 cudaError_t launch_kind(F32Params &p, const TcPlan &pl, cudaStream_t st) {
-    auto kernel = f32_product<AK, BKM, EPI, GROUPED>;
+    constexpr auto kernel = f32_product<AK, BKM, EPI, GROUPED>;
     p.table_at = EPI == EPI_STORE && !p.vec && !p.part ? SMEM_STAGED : SMEM;
     const int smem = p.table_at + (GROUPED ? group_table_bytes(p.groups.E) : 0);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SMEM_STAGED + (GROUPED ? group_table_bytes(MAX_EXPERTS) : 0));
+    cudaError_t e = allow_smem<kernel>(SMEM_STAGED + (GROUPED ? group_table_bytes(MAX_EXPERTS) : 0));
     if (e != cudaSuccess) return e;
     e = launch_with(kernel, pl.units, THREADS, smem, 1, st, p);
     if (e != cudaSuccess || !p.part) return e;

@@ -467,11 +467,10 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams 
 template <int CG, int BN, bool AK, bool BKM, int EPI, bool GROUPED>
 cudaError_t launch_shape(TcParams &p, const TcPlan &pl, cudaStream_t st) {
     using T = Tile<CG, BN>;
-    auto kernel = tc_product<CG, BN, AK, BKM, EPI, GROUPED>;
+    constexpr auto kernel = tc_product<CG, BN, AK, BKM, EPI, GROUPED>;
     p.table_at = EPI == EPI_STORE && p.vec == 2 && !p.part ? T::SMEM_STAGED : T::SMEM;
     const int smem = p.table_at + (GROUPED ? group_table_bytes(p.groups.E) : 0);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         T::SMEM_STAGED + (GROUPED ? group_table_bytes(MAX_EXPERTS) : 0));
+    cudaError_t e = allow_smem<kernel>(T::SMEM_STAGED + (GROUPED ? group_table_bytes(MAX_EXPERTS) : 0));
     if (e != cudaSuccess) return e;
     e = launch_with(kernel, pl.units * CG, THREADS, smem, CG, st, p);
     if (e != cudaSuccess || !p.part) return e;

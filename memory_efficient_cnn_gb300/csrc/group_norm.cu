@@ -28,34 +28,32 @@ GroupArgs make(int64_t N, int64_t P, int64_t C, int64_t G, int act, int dtype, i
     return a;
 }
 
-// The workspace: partial sums, the groups' sums (backward), the statistics (where the caller keeps none).
+// The workspace: partial sums, and the groups' sums (backward) or their statistics (forward, where the
+// caller keeps none). A forward call whose maps stay on the chip needs none.
 struct Parts {
-    size_t part, sums, stats, bytes;
-    explicit Parts(const GroupArgs &a) {
+    size_t part, sums, bytes;
+    Parts(const GroupArgs &a, bool backward) {
         part = 0;
-        sums = round_up((size_t)(2 * a.N * a.chunks) * a.C * 4, 256);
-        stats = sums + round_up((size_t)(a.N * a.G) * 8, 256);
-        bytes = stats + round_up((size_t)(a.N * a.G) * 8, 256);
+        sums = a.resident && !backward ? 0 : round_up((size_t)(2 * a.N * a.chunks) * a.C * 4, 256);
+        bytes = sums + (a.resident ? 0 : round_up((size_t)(a.N * a.G) * 8, 256));
     }
 };
 
-void place(GroupArgs &a, void *ws, void *stats) {
-    const Parts parts(a);
+void place(GroupArgs &a, const Parts &parts, void *ws, void *stats) {
     unsigned char *base = static_cast<unsigned char *>(ws);
     a.part = reinterpret_cast<float *>(base + parts.part);
     a.sums = reinterpret_cast<float *>(base + parts.sums);
-    a.stats = static_cast<float *>(stats ? stats : base + parts.stats);
+    a.stats = static_cast<float *>(stats || a.resident ? stats : base + parts.sums);
 }
 
 }  // namespace
 
 extern "C" {
 
-im2win_status im2win_group_norm_size(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, size_t *bytes) {
+im2win_status im2win_group_norm_size(int backward, int64_t N, int64_t P, int64_t C, int64_t G, int dtype, size_t *bytes) {
     if (!bytes) return IM2WIN_ERR_INVALID_ARG;
     const im2win_status s = check_dims(N, P, C, G, dtype);
-    if (s == IM2WIN_OK)
-        *bytes = std::max<size_t>({256, Parts(make(N, P, C, G, 0, dtype, 1)).bytes, Parts(make(N, P, C, G, 0, dtype, 2)).bytes});
+    if (s == IM2WIN_OK) *bytes = N * P == 0 ? 0 : Parts(make(N, P, C, G, 0, dtype, backward ? 2 : 1), backward != 0).bytes;
     return s;
 }
 
@@ -70,9 +68,10 @@ im2win_status im2win_group_norm(const void *x, const void *w, const void *b, voi
     for (const void *p : {x, w, b, (const void *)y, (const void *)stats, (const void *)ws})
         if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
     GroupArgs a = make(N, P, C, G, act, dtype, 1);
-    if (!ws || ws_bytes < Parts(a).bytes) return IM2WIN_ERR_WORKSPACE;
+    const Parts parts(a, false);
+    if (ws_bytes < parts.bytes || (!ws && parts.bytes)) return IM2WIN_ERR_WORKSPACE;
     a.x = x, a.w = w, a.b = b, a.y = y, a.eps = (float)eps;
-    place(a, ws, stats);
+    place(a, parts, ws, stats);
     cudaError_t e = cudaErrorInvalidValue;
     with_dtype(dtype, [&](auto *t) { e = launch_forward<std::remove_pointer_t<decltype(t)>>(a, static_cast<cudaStream_t>(stream)); });
     return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
@@ -96,9 +95,10 @@ im2win_status im2win_group_norm_backward(const void *dy, const void *x, const vo
     }
     if (!dx && !dw && !db) return IM2WIN_OK;
     GroupArgs a = make(N, P, C, G, act, dtype, 2);
-    if (!ws || ws_bytes < Parts(a).bytes) return IM2WIN_ERR_WORKSPACE;
+    const Parts parts(a, true);
+    if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
     a.x = x, a.dy = dy, a.w = w, a.b = b, a.dx = dx, a.dw = dw, a.db = db;
-    place(a, ws, const_cast<void *>(stats));
+    place(a, parts, ws, const_cast<void *>(stats));
     cudaError_t e = cudaErrorInvalidValue;
     with_dtype(dtype, [&](auto *t) { e = launch_backward<std::remove_pointer_t<decltype(t)>>(a, st); });
     return e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;

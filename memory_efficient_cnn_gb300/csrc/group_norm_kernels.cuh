@@ -865,10 +865,6 @@ __global__ void __launch_bounds__(THREADS) gn_back_resident(const __grid_constan
 
 template <typename K, typename... A>
 cudaError_t launch_with(K kernel, int64_t blocks, cudaStream_t st, int smem, int cluster, const A &...args) {
-    if (smem) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.dynamicSmemBytes = smem;
     cfg.gridDim = dim3((unsigned)blocks);
@@ -910,7 +906,10 @@ cudaError_t launch_forward(const GroupArgs &a, cudaStream_t st) {
     const int64_t blocks = a.N * a.slabs * a.chunks;
     return with_vector<T>(a, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        if (a.resident) return launch(gn_resident<T, V>, blocks, st, a, a.smem, a.chunks);
+        if (a.resident) {
+            const cudaError_t e = allow_smem<gn_resident<T, V>>(MAX_SMEM);
+            return e == cudaSuccess ? launch(gn_resident<T, V>, blocks, st, a, a.smem, a.chunks) : e;
+        }
         cudaError_t e = launch(gn_moments<T, V>, blocks, st, a);
         if (e == cudaSuccess) e = by_block(a) ? launch(gn_stats<THREADS>, group_blocks(a), st, a) : launch(gn_stats<32>, group_blocks(a), st, a);
         return e == cudaSuccess ? launch(gn_apply<T, V>, blocks, st, a) : e;
@@ -922,7 +921,9 @@ cudaError_t launch_backward(const GroupArgs &a, cudaStream_t st) {
     const int64_t blocks = a.N * a.slabs * a.chunks;
     return with_vector<T>(a, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        cudaError_t e = a.resident ? launch(gn_back_resident<T, V>, blocks, st, a, a.smem, a.chunks) : launch(gn_back_sums<T, V>, blocks, st, a);
+        cudaError_t e = a.resident ? allow_smem<gn_back_resident<T, V>>(MAX_SMEM) : cudaSuccess;
+        if (e == cudaSuccess)
+            e = a.resident ? launch(gn_back_resident<T, V>, blocks, st, a, a.smem, a.chunks) : launch(gn_back_sums<T, V>, blocks, st, a);
         if (a.dx && !a.resident) {
             if (e == cudaSuccess)
                 e = by_block(a) ? launch(gn_back_means<T, THREADS>, group_blocks(a), st, a) : launch(gn_back_means<T, 32>, group_blocks(a), st, a);

@@ -22,11 +22,11 @@ ROUTES = {"top": 0, "all": 1}
 
 def _experts(fn, experts, like, shape):
     """Checks an index tensor of a call on like's device."""
-    if tuple(experts.shape) != tuple(shape):
+    if experts.shape != shape:
         _shape(fn, "experts", experts, shape)
-    if experts.dtype != torch.int32:
+    if experts.dtype is not torch.int32:
         raise TypeError(f"{fn}: experts must be int32, got {experts.dtype}")
-    if not _alike(torch.int32, like.get_device(), experts):
+    if experts.get_device() != like.get_device() or not experts.is_contiguous() or not experts.is_cuda:
         _same_device(fn, like, experts)
         _cuda(experts)
 
@@ -56,8 +56,18 @@ def im2win_expert_route(logits, weights, experts, over: str = "top") -> None:
     _shape(fn, "weights", weights, (*logits.shape[:-1], k))
     _same(fn, logits, weights)
     _experts(fn, experts, logits, weights.shape)
+    _route(fn, dims, logits, weights, experts, over)
+
+
+def _route(fn, dims, logits, weights, experts, over):
     _check(fn, lib().im2win_expert_route(logits.data_ptr(), weights.data_ptr(), experts.data_ptr(), *dims,
                                          _code(ROUTES, over, "over"), _dtype_code(logits), _stream(logits.get_device())))
+
+
+def _route_backward(fn, dims, dweights, logits, experts, dlogits, over):
+    _check(fn, lib().im2win_expert_route_backward(
+        dweights.data_ptr(), logits.data_ptr(), experts.data_ptr(), dlogits.data_ptr(), *dims, _code(ROUTES, over, "over"),
+        _dtype_code(logits), _stream(logits.get_device())))
 
 
 def im2win_expert_route_backward(dweights, logits, experts, dlogits, over: str = "top") -> None:
@@ -69,9 +79,7 @@ def im2win_expert_route_backward(dweights, logits, experts, dlogits, over: str =
     _shape(fn, "dlogits", dlogits, logits.shape)
     _same(fn, logits, dweights, dlogits)
     _experts(fn, experts, logits, dweights.shape)
-    _check(fn, lib().im2win_expert_route_backward(
-        dweights.data_ptr(), logits.data_ptr(), experts.data_ptr(), dlogits.data_ptr(), *dims, _code(ROUTES, over, "over"),
-        _dtype_code(logits), _stream(logits.get_device())))
+    _route_backward(fn, dims, dweights, logits, experts, dlogits, over)
 
 
 def expert_route(logits: torch.Tensor, k: int, over: str = "top"):
@@ -82,18 +90,27 @@ def expert_route(logits: torch.Tensor, k: int, over: str = "top"):
     torch.no_grad()."""
     fn = "expert_route"
     _unrecorded(fn, logits)
-    _route_dims(fn, logits, k)
-    shape = (*logits.shape[:-1], k)
-    weights = torch.empty(shape, dtype=logits.dtype, device=logits.device)
-    experts = torch.empty(shape, dtype=torch.int32, device=logits.device)
-    im2win_expert_route(logits, weights, experts, over)
+    dims = _route_dims(fn, logits, k)
+    if logits.get_device() < 0 or not logits.is_contiguous():
+        _cuda(logits)
+    shape, device = (*logits.shape[:-1], k), logits.device
+    weights = torch.empty(shape, dtype=logits.dtype, device=device)
+    experts = torch.empty(shape, dtype=torch.int32, device=device)
+    _route(fn, dims, logits, weights, experts, over)
     return weights, experts
 
 
 def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, over: str = "top"):
     """dlogits of expert_route() at the same logits and over, and the experts it chose."""
+    fn = "expert_route_backward"
+    k = dweights.shape[-1] if dweights.dim() else 0
+    dims = _route_dims(fn, logits, k)
+    if dweights.shape != (*logits.shape[:-1], k):
+        _shape(fn, "dweights", dweights, (*logits.shape[:-1], k))
+    _same(fn, logits, dweights)
+    _experts(fn, experts, logits, dweights.shape)
     dlogits = torch.empty_like(logits)
-    im2win_expert_route_backward(dweights, logits, experts, dlogits, over)
+    _route_backward(fn, dims, dweights, logits, experts, dlogits, over)
     return dlogits
 
 

@@ -31,13 +31,16 @@ def test_group_norm_refusals():
         assert norm_call(**kw) == ERR_MISALIGNED, kw
     for kw in (dict(C=1 << 21, G=1), dict(N=1 << 31), dict(P=1 << 31), dict(N=1 << 20, P=1 << 20), dict(N=1 << 12, C=1 << 20)):
         assert norm_call(**kw) == ERR_UNSUPPORTED, kw
-    assert norm_call(ws=None) == ERR_WORKSPACE
-    assert norm_call(ws_bytes=mec.im2win_group_norm_size(2, 9, 8, 2, F16) - 1) == ERR_WORKSPACE
+    # maps that stay on the chip need no workspace, large ones do
+    assert mec.im2win_group_norm_size(False, 2, 9, 8, 2, F16) == 0 < mec.im2win_group_norm_size(True, 2, 9, 8, 2, F16)
+    large = dict(N=64, P=3136, C=128)
+    assert norm_call(ws=None, **large) == ERR_WORKSPACE
+    assert norm_call(ws_bytes=mec.im2win_group_norm_size(False, 64, 3136, 128, 2, F16) - 1, **large) == ERR_WORKSPACE
     for kw in (dict(N=0), dict(P=0)):
         assert norm_call(x=None, y=None, ws=None, ws_bytes=0, **kw) == OK
     sz = ctypes.c_size_t()
-    assert mec.lib().im2win_group_norm_size(2, 9, 8, 2, F16, None) == ERR_INVALID_ARG
-    assert mec.lib().im2win_group_norm_size(2, 9, 8, 3, F16, ctypes.byref(sz)) == ERR_INVALID_ARG
+    assert mec.lib().im2win_group_norm_size(0, 2, 9, 8, 2, F16, None) == ERR_INVALID_ARG
+    assert mec.lib().im2win_group_norm_size(0, 2, 9, 8, 3, F16, ctypes.byref(sz)) == ERR_INVALID_ARG
 
 
 def test_group_norm_backward_refusals():
