@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 
 import torch
 
@@ -39,23 +40,32 @@ def _same(fn, x, *ts):
 
 
 # ---------------------------------------------------------------- router
-def _route_dims(fn, logits, k):
-    if logits.dim() < 1 or logits.shape[-1] < 1:
-        raise ValueError(f"{fn}: logits must be [..., E]")
-    E = logits.shape[-1]
+@functools.lru_cache(maxsize=4096)
+def _route_plan(shape, k):
+    """((T, E, k), the choices' shape) of logits' shape; ValueError where they do not fit."""
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError("logits must be [..., E]")
+    E = shape[-1]
     if not 1 <= k <= E:
-        raise ValueError(f"{fn}: k must be between 1 and {E}, the number of experts; got {k}")
-    return logits.numel() // E, E, k
+        raise ValueError(f"k must be between 1 and {E}, the number of experts; got {k}")
+    return (math.prod(shape[:-1]), E, k), (*shape[:-1], k)
+
+
+def _route_dims(fn, logits, k):
+    try:
+        return _route_plan(logits.shape, k)
+    except ValueError as e:
+        raise ValueError(f"{fn}: {e}") from None
 
 
 def im2win_expert_route(logits, weights, experts, over: str = "top") -> None:
     """experts = the indexes of the k largest logits of each row, weights = their softmax weights."""
     fn = "im2win_expert_route"
     k = weights.shape[-1] if weights.dim() else 0
-    dims = _route_dims(fn, logits, k)
-    _shape(fn, "weights", weights, (*logits.shape[:-1], k))
+    dims, shape = _route_dims(fn, logits, k)
+    _shape(fn, "weights", weights, shape)
     _same(fn, logits, weights)
-    _experts(fn, experts, logits, weights.shape)
+    _experts(fn, experts, logits, shape)
     _route(fn, dims, logits, weights, experts, over)
 
 
@@ -74,11 +84,11 @@ def im2win_expert_route_backward(dweights, logits, experts, dlogits, over: str =
     """dlogits from dweights at the same logits and the experts chosen there."""
     fn = "im2win_expert_route_backward"
     k = dweights.shape[-1] if dweights.dim() else 0
-    dims = _route_dims(fn, logits, k)
-    _shape(fn, "dweights", dweights, (*logits.shape[:-1], k))
+    dims, shape = _route_dims(fn, logits, k)
+    _shape(fn, "dweights", dweights, shape)
     _shape(fn, "dlogits", dlogits, logits.shape)
     _same(fn, logits, dweights, dlogits)
-    _experts(fn, experts, logits, dweights.shape)
+    _experts(fn, experts, logits, shape)
     _route_backward(fn, dims, dweights, logits, experts, dlogits, over)
 
 
@@ -89,13 +99,13 @@ def expert_route(logits: torch.Tensor, k: int, over: str = "top"):
     and weight 0. Autograd does not record it: tensors that require grad are refused outside of
     torch.no_grad()."""
     fn = "expert_route"
-    _unrecorded(fn, logits)
-    dims = _route_dims(fn, logits, k)
+    if logits.requires_grad:
+        _unrecorded(fn, logits)
+    dims, shape = _route_dims(fn, logits, k)
     if logits.get_device() < 0 or not logits.is_contiguous():
         _cuda(logits)
-    shape, device = (*logits.shape[:-1], k), logits.device
-    weights = torch.empty(shape, dtype=logits.dtype, device=device)
-    experts = torch.empty(shape, dtype=torch.int32, device=device)
+    weights = torch.empty(shape, dtype=logits.dtype, device=logits.device)
+    experts = torch.empty_like(weights, dtype=torch.int32)
     _route(fn, dims, logits, weights, experts, over)
     return weights, experts
 
@@ -104,11 +114,11 @@ def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts:
     """dlogits of expert_route() at the same logits and over, and the experts it chose."""
     fn = "expert_route_backward"
     k = dweights.shape[-1] if dweights.dim() else 0
-    dims = _route_dims(fn, logits, k)
-    if dweights.shape != (*logits.shape[:-1], k):
-        _shape(fn, "dweights", dweights, (*logits.shape[:-1], k))
+    dims, shape = _route_dims(fn, logits, k)
+    if dweights.shape != shape:
+        _shape(fn, "dweights", dweights, shape)
     _same(fn, logits, dweights)
-    _experts(fn, experts, logits, dweights.shape)
+    _experts(fn, experts, logits, shape)
     dlogits = torch.empty_like(logits)
     _route_backward(fn, dims, dweights, logits, experts, dlogits, over)
     return dlogits
