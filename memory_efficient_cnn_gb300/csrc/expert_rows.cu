@@ -31,18 +31,32 @@ __global__ void __launch_bounds__(THREADS) expert_count(const int32_t *experts, 
     for (int e = threadIdx.x; e < E; e += THREADS) hist[(int64_t)blockIdx.x * E + e] = sum[e];
 }
 
-__global__ void __launch_bounds__(THREADS) expert_place(const int32_t *experts, const int32_t *hist, int64_t pairs, int per,
-                                                        int E, PairPlan plan, uint32_t *status) {
-    __shared__ int32_t total[MAX_EXPERTS], next[MAX_EXPERTS];  // an expert's pairs, and its next row in this block
-    __shared__ uint8_t in_warp[WARPS][MAX_EXPERTS];
+constexpr int PLACE_THREADS = 1024, PLACE_WARPS = PLACE_THREADS / 32;
+
+// Each warp takes a run of the block's pairs: it counts them by expert, and when the counts of the blocks and
+// warps before it are known, gives them their rows in their order.
+__global__ void __launch_bounds__(PLACE_THREADS) expert_place(const int32_t *experts, const int32_t *hist, int64_t pairs,
+                                                              int per, int E, PairPlan plan, uint32_t *status) {
+    extern __shared__ int32_t next[];  // [PLACE_WARPS][E]: counts, then the warp's next rows
+    __shared__ int32_t total[MAX_EXPERTS], first[MAX_EXPERTS];
     // (not before the wait: the products that follow take tensor memory as soon as they start)
     tc::grid_dependency_wait();
     tc::allow_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
-    const int64_t begin = (int64_t)b * per, end = min(pairs, begin + per);
+    const int run = (per + PLACE_WARPS - 1) / PLACE_WARPS;
+    const int64_t block_end = min(pairs, (int64_t)(b + 1) * per), begin = min(block_end, (int64_t)b * per + (int64_t)warp * run),
+                  end = min(block_end, begin + run);
+    int32_t *mine = next + warp * E;
     if (b == 0 && threadIdx.x == 0) status[0] = 0;
-    for (int e = threadIdx.x; e < E; e += THREADS) {
-        int32_t sum = 0, before = 0;
+    for (int e = lane; e < E; e += 32) mine[e] = 0;
+    __syncwarp();
+    for (int64_t q = begin + lane; q < end; q += 32) {
+        const int32_t e = experts[q];
+        if ((uint32_t)e < (uint32_t)E) atomicAdd(&mine[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += PLACE_THREADS) {
+        int32_t before = 0, sum = 0;  // the expert's pairs in the blocks before, and in all
         if (hist) {
             for (int i = 0; i < (int)gridDim.x; ++i) {
                 const int32_t v = hist[(int64_t)i * E + e];
@@ -50,18 +64,15 @@ __global__ void __launch_bounds__(THREADS) expert_place(const int32_t *experts, 
                 sum += v;
             }
         }
-        total[e] = sum, next[e] = before;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) in_warp[w][e] = 0;
+#pragma unroll 8
+        for (int w = 0; w < PLACE_WARPS; ++w) {
+            const int32_t v = next[w * E + e];
+            next[w * E + e] = before;
+            before += v;
+        }
+        total[e] = hist ? sum : before;
     }
     __syncthreads();
-    if (!hist) {
-        for (int64_t q = begin + threadIdx.x; q < end; q += THREADS) {
-            const int32_t e = experts[q];
-            if ((uint32_t)e < (uint32_t)E) atomicAdd(&total[e], 1);
-        }
-        __syncthreads();
-    }
     if (warp == 0) {
         int rows = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
@@ -72,41 +83,35 @@ __global__ void __launch_bounds__(THREADS) expert_place(const int32_t *experts, 
                 const int v = __shfl_up_sync(ALL, sum, o);
                 if (lane >= o) sum += v;
             }
-            if (e < E) {
-                const int first = rows + sum - padded;
-                next[e] += first;
-                if (b == 0) {
-                    plan.begin[e] = first, plan.count[e] = total[e];
-                    for (int i = total[e]; i < padded; ++i) plan.pair[first + i] = -1;
-                }
-            }
+            if (e < E) first[e] = rows + sum - padded;
             rows += __shfl_sync(ALL, sum, 31);
         }
         if (b == 0 && lane == 0) plan.begin[E] = rows;
     }
     __syncthreads();
-    for (int64_t q0 = begin; q0 < end; q0 += THREADS) {
-        const int64_t q = q0 + threadIdx.x;
+    if (b == 0) {
+        for (int e = warp; e < E; e += PLACE_WARPS) {
+            if (lane == 0) plan.begin[e] = first[e], plan.count[e] = total[e];
+            const int padded = (total[e] + GROUP_ROWS - 1) / GROUP_ROWS * GROUP_ROWS;
+            for (int i = total[e] + lane; i < padded; i += 32) plan.pair[first[e] + i] = -1;
+        }
+    }
+    for (int64_t q0 = begin; q0 < end; q0 += 32) {
+        const int64_t q = q0 + lane;
         int32_t e = q < end ? experts[q] : -1;
         if ((uint32_t)e >= (uint32_t)E) e = -1;
         const unsigned same = __match_any_sync(ALL, e);
         const int rank = __popc(same & ((1u << lane) - 1u));
-        if (rank == 0 && e >= 0) in_warp[warp][e] = (uint8_t)__popc(same);
-        __syncthreads();
         if (e >= 0) {
-            int row = next[e] + rank;
-            for (int w = 0; w < warp; ++w) row += in_warp[w][e];
+            const int row = first[e] + mine[e] + rank;
             plan.slot[q] = row;
             plan.pair[row] = (int32_t)q;
         } else if (q < end) {
             plan.slot[q] = -1;
         }
-        __syncthreads();
-        if (rank == 0 && e >= 0) {
-            atomicAdd(&next[e], __popc(same));
-            in_warp[warp][e] = 0;
-        }
-        __syncthreads();
+        __syncwarp();
+        if (rank == 0 && e >= 0) mine[e] += __popc(same);
+        __syncwarp();
     }
 }
 
@@ -237,10 +242,11 @@ __global__ void __launch_bounds__(THREADS) expert_combine(const __grid_constant_
 }
 
 template <typename K, typename... A>
-cudaError_t launch(K kernel, int64_t blocks, cudaStream_t st, A... args) {
+cudaError_t launch_sized(K kernel, int64_t blocks, int threads, int smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -248,6 +254,11 @@ cudaError_t launch(K kernel, int64_t blocks, cudaStream_t st, A... args) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, int64_t blocks, cudaStream_t st, A... args) {
+    return launch_sized(kernel, blocks, THREADS, 0, st, args...);
 }
 
 // Calls f with null pointers of the type, and whether rows of C are whole vectors.
@@ -269,8 +280,11 @@ cudaError_t launch_plan(const Rows &r, const int32_t *experts, int32_t *hist, ui
     cudaError_t e = cudaSuccess;
     if (blocks > 1) e = launch(expert_count, blocks, st, experts, hist, pairs, per, r.E);
     if (e != cudaSuccess) return e;
-    return launch(expert_place, blocks, st, experts, static_cast<const int32_t *>(blocks > 1 ? hist : nullptr), pairs, per, r.E,
-                  r.plan, status);
+    const int smem = PLACE_WARPS * r.E * 4;
+    e = allow_smem<expert_place>(PLACE_WARPS * MAX_EXPERTS * 4);
+    if (e != cudaSuccess) return e;
+    return launch_sized(expert_place, blocks, PLACE_THREADS, smem, st, experts,
+                        static_cast<const int32_t *>(blocks > 1 ? hist : nullptr), pairs, per, r.E, r.plan, status);
 }
 
 cudaError_t launch_gather(const Rows &r, const void *x, const void *weights, void *grouped, float *scale, int dtype,

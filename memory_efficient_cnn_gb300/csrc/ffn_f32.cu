@@ -218,9 +218,11 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
         int s = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t a_bytes = AK ? p.a_rows * BK * 2 : (p.a_rows + 63) / 64 * 64 * BK * 2;
+        uint32_t a_bytes = AK ? p.a_rows * BK * 2 : (p.a_rows + 63) / 64 * 64 * BK * 2;
         while (ok && walk.next(w)) {
             const int m0 = w.tm * ROWS + (GROUPED && AK ? w.row0 : 0);
+            const int a_copies = GROUPED && AK ? min(max((w.pad_end - m0) / 64, 0), 2) : 0;  // (as in the 16-bit kernel)
+            if (GROUPED && AK) a_bytes = a_copies * 64 * BK * 2;
             for (int kb = w.k0; ok && kb < w.k1; ++kb) {
                 const int seg = kb >= p.KB ? 1 : 0, k = (kb - seg * p.KB) * BK + (GROUPED && !AK ? w.row0 : 0);
 #pragma unroll 1
@@ -229,7 +231,9 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
                     const uint32_t sa = base + s * STAGE, sb = sa + A_BYTES, bar = full + 8 * s;
                     mbar_arrive_expect_tx(bar, a_bytes + B_BYTES);
                     const CUtensorMap *ma = &p.a[seg | w.z][q], *mb = &p.b[seg | w.z][q];
-                    if (AK) {
+                    if (GROUPED && AK) {
+                        for (int i = 0; i < a_copies; ++i) tma_2d<1>(sa + i * 64 * BK * 2, ma, k, m0 + i * 64, bar);
+                    } else if (AK) {
                         tma_2d<1>(sa, ma, k, m0, bar);
                     } else if (p.a_blocks) {
                         tma_3d<1>(sa, ma, 0, k, m0 / 64, bar);
@@ -454,6 +458,7 @@ cudaError_t launch_f32(const Product &d, uint32_t *status, bool first, void *par
     const int stack = d.a0.k_major ? d.groups.E : 0;
     if (d.groups.E && !d.a0.k_major) p.tiles *= d.groups.E;
     p.a_rows = std::min(ROWS, (d.M + 7) / 8 * 8);
+    if (stack) p.a_rows = 64;  // (of one copy)
     p.a_blocks = !d.a0.k_major && d.M % 64 == 0;
     p.b_blocks = !d.b0.k_major && d.N % 64 == 0;
     const int b_box = d.epi == EPI_GATED ? BN / 2 : BN;

@@ -34,7 +34,7 @@ struct Tile {
     static constexpr int B_ROWS = BN / CG;  // rows of B a CTA stages
     static constexpr int A_BYTES = ROWS * BK * 2, B_BYTES = B_ROWS * BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = STAGE <= 24 * 1024 ? 8 : 6;
     static constexpr int SMEM = STAGE * STAGES + 1024;  // + alignment
     // staged outputs besides, where they are needed (with them L1 has 28 KB instead of 60, and
     // the epilogue that reads kept values takes 39 us instead of 34)
@@ -237,9 +237,15 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
         bool ok = true;
         constexpr int b_box = EPI == EPI_GATED && CG == 1 ? BN / 2 : T::B_ROWS;
         const uint32_t a_bytes = AK ? p.a_rows * BK * 2 : (p.a_rows + 63) / 64 * 64 * BK * 2;
-        const uint32_t bytes = CG * (a_bytes + T::B_BYTES);
+        uint32_t bytes = CG * (a_bytes + T::B_BYTES);
         while (ok && walk.next(w)) {
             const int m0 = w.tm * T::M + (int)rank * ROWS + (GROUPED && AK ? w.row0 : 0);
+            // grouped rows: copies of 64, as many as the expert's rows (and their padding) take of the tile
+            const int a_copies = GROUPED && AK ? min(max((w.pad_end - m0) / 64, 0), 2) : 0;
+            if (GROUPED && AK) {
+                const int all = CG == 2 ? min(max((w.pad_end - w.tm * T::M - w.row0) / 64, 0), 4) : a_copies;
+                bytes = CG * T::B_BYTES + all * 64 * BK * 2;
+            }
             for (int kb = w.k0; kb < w.k1; ++kb) {
                 if (!(ok = bar_wait(empty + 8 * s, phase ^ 1, ctl, SITE_STAGE_EMPTY))) break;
                 const uint32_t sa = base + s * T::STAGE, sb = sa + T::A_BYTES;
@@ -247,7 +253,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                 if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
                 const int seg = kb >= p.KB ? 1 : 0, k = (kb - seg * p.KB) * BK + (GROUPED && !AK ? w.row0 : 0);
                 const CUtensorMap *ma = &p.a[seg | w.z], *mb = &p.b[seg | w.z];
-                if (AK) {
+                if (GROUPED && AK) {
+                    for (int i = 0; i < a_copies; ++i) tma_2d<CG>(sa + i * 64 * BK * 2, ma, k, m0 + i * 64, bar);
+                } else if (AK) {
                     tma_2d<CG>(sa, ma, k, m0, bar);
                 } else if (p.a_blocks) {
                     tma_3d<CG>(sa, ma, 0, k, m0 / 64, bar);
@@ -486,6 +494,13 @@ cudaError_t launch_tile(TcParams &p, const TcPlan &pl, const Product &d, cudaStr
     return launch_shape<CG, BN, true, false, EPI_STORE, GROUPED>(p, pl, st);
 }
 
+cudaError_t launch_narrow(TcParams &p, const TcPlan &pl, const Product &d, cudaStream_t st) {
+    if (d.epi == EPI_GATED) return launch_shape<2, 128, true, true, EPI_GATED, true>(p, pl, st);
+    if (d.epi == EPI_DGATED) return launch_shape<2, 128, true, false, EPI_DGATED, true>(p, pl, st);
+    if (d.b0.k_major) return launch_shape<2, 128, true, true, EPI_STORE, true>(p, pl, st);
+    return launch_shape<2, 128, true, false, EPI_STORE, true>(p, pl, st);
+}
+
 }  // namespace
 
 TcPlan plan_tc(const Product &d) {
@@ -493,8 +508,12 @@ TcPlan plan_tc(const Product &d) {
     // single CTA's shared-memory fill), outputs a little over half of it on the smaller tile.
     const double epi = d.epi == EPI_DGATED ? 4 : d.epi == EPI_GATED ? (d.kept ? 3 : 2.1) : 1.8;
     if (d.groups.E) {
-        const TcPlan pair = plan_groups(d, 2, 256, 0.345, epi), single = plan_groups(d, 1, 128, 0.335, 0.55 * epi + 0.1);
-        return single.cost < pair.cost ? single : pair;
+        TcPlan best = plan_groups(d, 2, 256, 0.345, epi);
+        const TcPlan single = plan_groups(d, 1, 128, 0.335, 0.55 * epi + 0.1);
+        if (single.cost < best.cost) best = single;
+        // narrower tiles for rows of A alone, whose experts may be read by few rows each
+        const TcPlan narrow = plan_groups(d, 2, 128, 0.26, 0.55 * epi + 0.1);
+        return d.a0.k_major && narrow.cost < best.cost ? narrow : best;
     }
     const TcPlan pair = plan_tiles(d, 2, 256, 0.345, epi), single = plan_tiles(d, 1, 128, 0.335, 0.55 * epi + 0.1);
     return single.cost < pair.cost ? single : pair;
@@ -516,6 +535,7 @@ cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool first,
     const int b_box = d.epi == EPI_GATED && pl.cg == 1 ? pl.bn / 2 : pl.bn / pl.cg;
     p.a_blocks = !d.a0.k_major && d.M % 64 == 0;
     p.b_blocks = !d.b0.k_major && d.N % 64 == 0;
+    if (stack) p.a_rows = 64;  // (of one copy)
     if (!encode(p.a[0], d.a0, 0, d.M, d.K, p.a_rows, p.a_blocks) || !encode(p.b[0], d.b0, 0, d.N, d.K, b_box, p.b_blocks, stack))
         return cudaErrorInvalidValue;
     if (two && !encode(p.a[1], d.a1, 0, d.M, d.K, p.a_rows, p.a_blocks)) return cudaErrorInvalidValue;
@@ -530,7 +550,10 @@ cudaError_t launch_tc(const Product &d, bool bf16, uint32_t *status, bool first,
     }
     p.status = status;
     p.first = first;
-    if (d.groups.E) return pl.cg == 2 ? launch_tile<2, 256, true>(p, pl, d, st) : launch_tile<1, 128, true>(p, pl, d, st);
+    if (d.groups.E) {
+        if (pl.cg == 1) return launch_tile<1, 128, true>(p, pl, d, st);
+        return pl.bn == 256 ? launch_tile<2, 256, true>(p, pl, d, st) : launch_narrow(p, pl, d, st);
+    }
     return pl.cg == 2 ? launch_tile<2, 256, false>(p, pl, d, st) : launch_tile<1, 128, false>(p, pl, d, st);
 }
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -495,21 +496,31 @@ inline TcPlan plan_tiles(const Product &d, int cg, int bn, double kb, double epi
 }
 
 // The plan of a grouped product: plain tiles of 128 * cg rows and bn columns. The experts' shares are
-// not known here; each expert's last tile of rows is taken to be half full.
+// not known here; they are taken to be even, with the last tile of rows half full. kb and epi
+// as in plan_tiles; while few rows share an expert's weights, a K block takes no less than its part of
+// reading them at 6 TB/s.
 inline TcPlan plan_groups(const Product &d, int cg, int bn, double kb, double epi) {
     const bool summed = !d.a0.k_major;
-    const int E = d.groups.E, tm = ROWS * cg, cols = d.epi == EPI_GATED ? bn / 2 : bn, z = d.batch ? 2 : 1;
+    const int tm = ROWS * cg, cols = d.epi == EPI_GATED ? bn / 2 : bn, z = d.batch ? 2 : 1, most = SMS / cg;
     TcPlan pl;
     pl.cg = cg, pl.bn = bn;
     pl.tiles_m = (d.M + tm - 1) / tm;
     pl.tiles_n = (d.N + cols - 1) / cols;
-    const double KT = summed ? d.rows / E / BK + 0.5 : (double)((d.K + BK - 1) / BK * (d.epi != EPI_GATED && d.a1.p ? 2 : 1));
-    const double tiles = summed ? (double)z * E * pl.tiles_m * pl.tiles_n
-                                : std::max(1.0, std::min(d.rows / tm + 0.5 * E, d.rows)) * pl.tiles_n;
-    // (a bound, for rows of A: every expert's last tile may hold one row)
-    const double most = summed ? tiles : std::min<double>((double)((int64_t)d.M / tm + E), d.M) * pl.tiles_n;
-    pl.units = (int)std::min<double>(SMS / cg, most);
-    const double waves = std::max(1.0, tiles / (SMS / cg));
+    const double E = std::min<double>(d.groups.E, d.rows);  // experts with rows
+    double KT, tiles;
+    if (summed) {
+        KT = d.rows / d.groups.E / BK + 0.5;
+        tiles = (double)z * d.groups.E * pl.tiles_m * pl.tiles_n;
+        pl.units = (int)std::min<double>(most, tiles);
+    } else {
+        const double tiles_m = std::max(1.0, d.rows / E / tm + 0.5);  // of an expert
+        KT = (double)((d.K + BK - 1) / BK * (d.epi != EPI_GATED && d.a1.p ? 2 : 1));
+        tiles = std::ceil(E * tiles_m) * pl.tiles_n;
+        kb = std::max(kb, bn * BK * 2.0 * most / tiles_m / 6e6);
+        // (a bound: every expert's last tile may hold one row)
+        pl.units = (int)std::min<double>(most, std::min<double>((double)((int64_t)d.M / tm + d.groups.E), d.M) * pl.tiles_n);
+    }
+    const double waves = std::ceil(std::max(1.0, tiles / most));
     pl.cost = 4 + KT * kb + epi + (waves - 1) * std::max(KT * kb, epi);
     return pl;
 }
