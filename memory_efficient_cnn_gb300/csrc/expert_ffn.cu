@@ -70,15 +70,65 @@ struct Problem {
     Operand w_in(const void *p, bool k_major) const { return {p, Cp, k_major, (int64_t)E * F * Cp}; }
     Operand w_out(const void *p, bool k_major) const { return {p, Fp, k_major, (int64_t)E * C * Fp}; }
 
-    Product product(int M, int N, int K, const int32_t *begin, const int32_t *count) const {
+    Product product(int M, int N, int K) const {
         Product p;
         p.M = M; p.N = N; p.K = K;
         p.act = act;
-        p.groups = {begin, count, E};
+        p.groups.E = E;
         p.rows = (double)pairs;
         return p;
     }
+    Product gated(const void *xs, const void *wg, const void *wu, void *h, void *hw, void *kept) const {
+        Product p = product((int)rows, F, C);
+        p.a0 = rows_c(xs, true);
+        p.b0 = w_in(wg, true), p.b1 = w_in(wu, true);
+        p.epi = EPI_GATED;
+        p.out = h, p.out2 = hw, p.ldo = Fp, p.plane = rows * Fp, p.kept = kept;
+        return p;
+    }
+    Product down(const void *h, const void *wd, void *ys) const {
+        Product p = product((int)rows, C, F);
+        p.a0 = rows_f(h, true), p.b0 = w_out(wd, true);
+        p.out = ys, p.ldo = Cp;
+        return p;
+    }
+    Product dgated(const void *dys, const void *wd, void *kept, void *dg, void *du) const {
+        Product p = product((int)rows, F, C);
+        p.a0 = rows_c(dys, true), p.b0 = w_out(wd, false);
+        p.epi = EPI_DGATED;
+        p.out = dg, p.out2 = du, p.ldo = Fp, p.plane = rows * Fp, p.kept = kept;
+        return p;
+    }
+    Product dx(const void *dg, const void *du, const void *wg, const void *wu, void *dxs) const {
+        Product p = product((int)rows, C, F);
+        p.a0 = rows_f(dg, true), p.b0 = w_in(wg, false);
+        p.a1 = rows_f(du, true), p.b1 = w_in(wu, false);
+        p.out = dxs, p.ldo = Cp;
+        return p;
+    }
+    Product dw_in(const void *dg, const void *du, const void *xs, void *dwg, void *dwu) const {
+        Product p = product(F, C, (int)rows);
+        p.a0 = rows_f(dg, false), p.a1 = rows_f(du, false);
+        p.b0 = p.b1 = rows_c(xs, false);
+        p.batch = true;
+        p.out = dwg, p.out2 = dwu, p.ldo = C;
+        return p;
+    }
+    Product dw_down(const void *dys, const void *hw, void *out) const {
+        Product p = product(C, F, (int)rows);
+        p.a0 = rows_c(dys, false), p.b0 = rows_f(hw, false);
+        p.out = out, p.ldo = F;
+        return p;
+    }
+    size_t part_bytes(std::initializer_list<Product> list) const {
+        size_t most = 0;
+        for (const Product &p : list) most = std::max(most, (f32 ? plan_f32(p) : plan_tc(p)).part_bytes);
+        return most;
+    }
 };
+
+const void *const kSome = reinterpret_cast<const void *>(16);  // a present operand, where only sizes matter
+void *const kSomeOut = reinterpret_cast<void *>(16);
 
 struct SavedParts {
     size_t begin, count, slot, pair, scale, xs, h, hw, kept, ys, bytes;
@@ -101,13 +151,13 @@ struct SavedParts {
 
 // A forward call's workspace; without `saved`, its parts too.
 struct ForwardParts {
-    size_t hist, wg, wu, wd, own, h, h_lo, bytes;
+    size_t hist, wg, wu, wd, part, own, h, h_lo, bytes;
     ForwardParts(const Problem &q, bool saved) {
         Parts p(kStatusBytes);
         h = p.add(q.few() && !saved ? (size_t)q.pairs * (q.f32 ? q.F * (size_t)4 : q.Fp * (size_t)2) : 0);
         h_lo = p.add(q.few() && !saved && !q.f32 ? (size_t)q.pairs * q.Fp * 2 : 0);
         if (q.few() && !saved) {
-            hist = wg = wu = wd = own = bytes = p.end;
+            hist = wg = wu = wd = part = own = bytes = p.end;
             return;
         }
         const int64_t per = pairs_per_block(q.pairs), blocks = (q.pairs + per - 1) / per;
@@ -115,13 +165,15 @@ struct ForwardParts {
         wg = p.add(q.copies(q.C) ? q.operand((int64_t)q.E * q.F, q.Cp) : 0);
         wu = p.add(q.copies(q.C) ? q.operand((int64_t)q.E * q.F, q.Cp) : 0);
         wd = p.add(q.copies(q.F) ? q.operand((int64_t)q.E * q.C, q.Fp) : 0);
+        part = p.add(q.pairs == 0 ? 0 : q.part_bytes({q.gated(kSome, kSome, kSome, kSomeOut, nullptr, saved ? kSomeOut : nullptr),
+                                                      q.down(kSome, kSome, kSomeOut)}));
         own = p.end;
         bytes = saved ? own : SavedParts(q, own, false).bytes;
     }
 };
 
 struct BackwardParts {
-    size_t dys, scale, dg, du, dxs, wg, wu, wd, bytes;
+    size_t dys, scale, dg, du, dxs, wg, wu, wd, part, bytes;
     explicit BackwardParts(const Problem &q) {
         Parts p(kStatusBytes);
         dys = p.add(q.operand(q.rows, q.Cp));
@@ -132,6 +184,10 @@ struct BackwardParts {
         wg = p.add(q.copies(q.C) ? q.operand((int64_t)q.E * q.F, q.Cp) : 0);
         wu = p.add(q.copies(q.C) ? q.operand((int64_t)q.E * q.F, q.Cp) : 0);
         wd = p.add(q.copies(q.F) ? q.operand((int64_t)q.E * q.C, q.Fp) : 0);
+        part = p.add(q.pairs == 0 ? 0 : q.part_bytes({q.dgated(kSome, kSome, kSomeOut, kSomeOut, kSomeOut),
+                                                      q.dx(kSome, kSome, kSome, kSome, kSomeOut),
+                                                      q.dw_in(kSome, kSome, kSome, kSomeOut, kSomeOut),
+                                                      q.dw_down(kSome, kSome, kSomeOut)}));
         bytes = p.end;
     }
 };
@@ -147,7 +203,9 @@ Rows rows_of(const Problem &q, const SavedParts &s, void *saved) {
 // The launches of one call, up to the first that fails.
 struct Sequence {
     const Problem &q;
+    const Rows &rows;
     void *ws;
+    void *part;
     cudaStream_t st;
     cudaError_t e = cudaSuccess;
     Repitch copies[3];
@@ -165,10 +223,13 @@ struct Sequence {
     void copy() {
         if (n_copies) step([&] { return launch_repitch(copies, n_copies, q.f32, st); });
     }
-    void run(const Product &p) {
+    // scale: the rows' factors, where not null
+    void run(Product p, const float *scale = nullptr) {
         uint32_t *status = static_cast<uint32_t *>(ws);
+        p.groups.begin = rows.plan.begin, p.groups.count = rows.plan.count;
+        p.scale = scale;
         step([&] {
-            return q.f32 ? launch_f32(p, status, false, nullptr, st) : launch_tc(p, q.dtype == IM2WIN_BF16, status, false, nullptr, st);
+            return q.f32 ? launch_f32(p, status, false, part, st) : launch_tc(p, q.dtype == IM2WIN_BF16, status, false, part, st);
         });
     }
 };
@@ -215,7 +276,7 @@ im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const voi
     const SavedParts own(q, saved ? 0 : parts.own, saved != nullptr);
     void *keep = saved ? saved : ws;
     const Rows rows = rows_of(q, own, keep);
-    Sequence seq{q, ws, st};
+    Sequence seq{q, rows, ws, at(ws, parts.part), st};
     seq.step([&] { return launch_plan(rows, experts, ints(ws, parts.hist), static_cast<uint32_t *>(ws), st); });
     w_gate = seq.readable(w_gate, q.E * q.F, q.C, parts.wg);
     w_up = seq.readable(w_up, q.E * q.F, q.C, parts.wu);
@@ -223,18 +284,10 @@ im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const voi
     seq.copy();
     seq.step([&] { return launch_gather(rows, x, weights, at(keep, own.xs), saved ? floats(keep, own.scale) : nullptr, dtype, st); });
 
-    Product gated = q.product((int)q.rows, q.F, q.C, rows.plan.begin, rows.plan.count);
-    gated.a0 = q.rows_c(at(keep, own.xs), true);
-    gated.b0 = q.w_in(w_gate, true), gated.b1 = q.w_in(w_up, true);
-    gated.epi = EPI_GATED;
-    gated.out = at(keep, own.h), gated.ldo = q.Fp, gated.plane = q.rows * q.Fp;
-    if (saved) gated.kept = at(keep, own.kept), gated.scale = floats(keep, own.scale), gated.out2 = at(keep, own.hw);
-    seq.run(gated);
-
-    Product down = q.product((int)q.rows, q.C, q.F, rows.plan.begin, rows.plan.count);
-    down.a0 = q.rows_f(at(keep, own.h), true), down.b0 = q.w_out(w_down, true);
-    down.out = at(keep, own.ys), down.ldo = q.Cp;
-    seq.run(down);
+    seq.run(q.gated(at(keep, own.xs), w_gate, w_up, at(keep, own.h), saved ? at(keep, own.hw) : nullptr,
+                    saved ? at(keep, own.kept) : nullptr),
+            saved ? floats(keep, own.scale) : nullptr);
+    seq.run(q.down(at(keep, own.h), w_down, at(keep, own.ys)));
     seq.step([&] { return launch_combine(rows, floats(keep, own.ys), weights, y, dtype, st); });
     return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
 }
@@ -267,7 +320,7 @@ im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, co
     const SavedParts own(q, 0, true);
     void *keep = const_cast<void *>(saved);
     const Rows rows = rows_of(q, own, keep);
-    Sequence seq{q, ws, st};
+    Sequence seq{q, rows, ws, at(ws, parts.part), st};
     void *dys = at(ws, parts.dys), *dg = at(ws, parts.dg), *du = at(ws, parts.du);
     seq.step([&] {
         return launch_gather_back(rows, dy, weights, floats(keep, own.ys), dys, floats(ws, parts.scale), dweights,
@@ -280,32 +333,15 @@ im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, co
             w_up = seq.readable(w_up, q.E * q.F, q.C, parts.wu);
         }
         seq.copy();
-        Product d = q.product((int)q.rows, q.F, q.C, rows.plan.begin, rows.plan.count);
-        d.a0 = q.rows_c(dys, true), d.b0 = q.w_out(w_down, false);
-        d.epi = EPI_DGATED;
-        d.out = dg, d.out2 = du, d.ldo = q.Fp, d.plane = q.rows * q.Fp;
-        d.kept = at(keep, own.kept), d.scale = floats(ws, parts.scale);
-        seq.run(d);
+        seq.run(q.dgated(dys, w_down, at(keep, own.kept), dg, du), floats(ws, parts.scale));
     }
     if (dx) {
-        Product d = q.product((int)q.rows, q.C, q.F, rows.plan.begin, rows.plan.count);
-        d.a0 = q.rows_f(dg, true), d.b0 = q.w_in(w_gate, false);
-        d.a1 = q.rows_f(du, true), d.b1 = q.w_in(w_up, false);
-        d.out = at(ws, parts.dxs), d.ldo = q.Cp;
-        seq.run(d);
+        seq.run(q.dx(dg, du, w_gate, w_up, at(ws, parts.dxs)));
         seq.step([&] { return launch_combine(rows, floats(ws, parts.dxs), nullptr, dx, dtype, st); });
     }
     if (want_dw) {
-        Product in = q.product(q.F, q.C, (int)q.rows, rows.plan.begin, rows.plan.count);
-        in.a0 = q.rows_f(dg, false), in.a1 = q.rows_f(du, false);
-        in.b0 = in.b1 = q.rows_c(at(keep, own.xs), false);
-        in.batch = true;
-        in.out = dw_gate, in.out2 = dw_up, in.ldo = q.C;
-        seq.run(in);
-        Product out = q.product(q.C, q.F, (int)q.rows, rows.plan.begin, rows.plan.count);
-        out.a0 = q.rows_c(dys, false), out.b0 = q.rows_f(at(keep, own.hw), false);
-        out.out = dw_down, out.ldo = q.F;
-        seq.run(out);
+        seq.run(q.dw_in(dg, du, at(keep, own.xs), dw_gate, dw_up));
+        seq.run(q.dw_down(dys, at(keep, own.hw), dw_down));
     }
     return seq.e == cudaSuccess ? IM2WIN_OK : IM2WIN_ERR_CUDA;
 }

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
 
     const GroupTable table = group_table(dyn + p.table_at, p.groups.E);
     if (GROUPED) {  // (as in the 16-bit kernel)
-        if (warp == 3) fill_group_table(table, p.groups, p.rows_bound, ROWS, p.tiles_n, lane);
+        if (warp == 3) fill_group_table<!AK>(table, p, ROWS, lane);
         __syncthreads();
     }
     auto walk = [&] {
@@ -355,9 +355,10 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
             const int m_end = !GROUPED || !AK ? p.M : EPI == EPI_STORE ? w.row_end : w.pad_end;
             const bool none = GROUPED && AK && m >= w.row_end;
             const float scale = !GROUPED ? 1.0f : EPI != EPI_STORE && p.scale && !none ? p.scale[m] : 0.0f;
-            if (!GROUPED && p.part) {
-                float *dst = p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
-                if (m < p.M) {
+            if (GROUPED ? p.part && !w.whole : p.part != nullptr) {
+                float *dst = GROUPED ? p.part + ((int64_t)(2 * blockIdx.x + w.slot) * ROWS + q * 32 + lane) * BN
+                                     : p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
+                if (m < m_end) {
                     store_f32(dst + c0, sum[0], CHUNK);
                     store_f32(dst + c1, sum[1], CHUNK);
                 }
@@ -385,6 +386,21 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
     if (warp == 2) free_tmem<1>(tmem, 4 * BN);
 }
 
+// Eight columns of a row, `left` of them there.
+__device__ __forceinline__ void store_octet(const F32Params &p, float *out, const F2 (&v)[4], int left) {
+    if (p.vec && left >= 8) {
+        reinterpret_cast<ulonglong2 *>(out)[0] = words(v);
+        reinterpret_cast<ulonglong2 *>(out)[1] = words(v + 2);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float a, b;
+            split(v[i / 2], a, b);
+            if (i < left) out[i] = i & 1 ? b : a;
+        }
+    }
+}
+
 // Adds the partial tiles of a streamed launch: one thread for eight output columns.
 template <int EPI>
 __global__ void __launch_bounds__(256) f32_join(const __grid_constant__ F32Params p, int units) {
@@ -397,34 +413,58 @@ __global__ void __launch_bounds__(256) f32_join(const __grid_constant__ F32Param
     F2 v[4], u[4];
     add_partials<EPI == EPI_GATED, BN>(src, p.part_step, count, v, u);
     if (EPI == EPI_STORE) {
-        float *out = static_cast<float *>(z ? p.out2 : p.out) + (int64_t)m * p.ldo + n;
-        const int left = p.N - n;
-        if (p.vec && left >= 8) {
-            reinterpret_cast<ulonglong2 *>(out)[0] = words(v);
-            reinterpret_cast<ulonglong2 *>(out)[1] = words(v + 2);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float a, b;
-                split(v[i / 2], a, b);
-                if (i < left) out[i] = i & 1 ? b : a;
-            }
-        }
+        store_octet(p, static_cast<float *>(z ? p.out2 : p.out) + (int64_t)m * p.ldo + n, v, p.N - n);
     } else {
         finish<EPI, 8>(p, v, u, m, n, p.M);
+    }
+}
+
+// The same for a streamed launch over experts.
+template <bool AK, int EPI>
+__global__ void __launch_bounds__(256) f32_group_join(const __grid_constant__ F32Params p, int units) {
+    constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;
+    extern __shared__ unsigned char dyn[];
+    allow_dependents();
+    grid_dependency_wait();
+    const GroupTable table = group_table(dyn, p.groups.E);
+    if (threadIdx.x < 32) fill_group_table<!AK>(table, p, ROWS, threadIdx.x);
+    __syncthreads();
+    if (!AK) zero_empty<float>(table, p.groups.E, p.out, p.batch == 2 ? p.out2 : nullptr, (int64_t)p.M * p.ldo);
+    Work w;
+    int unit, last;
+    if (!group_join_source(GroupSpace<!AK>(p, table, ROWS), units, w, unit, last)) return;
+    const int m_end = !AK ? p.M : EPI == EPI_STORE ? w.row_end : w.pad_end;
+    for (int id = blockIdx.x % JOIN_SHARES * 256 + threadIdx.x; id < ROWS * COLS / 8; id += JOIN_SHARES * 256) {
+        const int row = id / (COLS / 8), col = id % (COLS / 8) * 8;
+        const int m = w.tm * ROWS + row + (AK ? w.row0 : 0), n = w.tn * COLS + col;
+        if (m >= m_end || n >= p.N) continue;
+        F2 v[4], u[4];
+        add_parts<EPI == EPI_GATED>(p.part, ROWS, BN, row, col, unit, last, v, u);
+        const bool none = AK && m >= w.row_end;
+        if (EPI == EPI_STORE) {
+            float *out = static_cast<float *>(w.z ? p.out2 : p.out) + (AK ? 0 : (int64_t)w.e * p.M * p.ldo);
+            store_octet(p, out + (int64_t)m * p.ldo + n, v, p.N - n);
+        } else {
+            finish<EPI, 8>(p, v, u, m, n, m_end, none, p.scale && !none ? p.scale[m] : 0.0f);
+        }
     }
 }
 
 template <bool AK, bool BKM, int EPI, bool GROUPED>
 cudaError_t launch_kind(F32Params &p, const TcPlan &pl, cudaStream_t st) {
     constexpr auto kernel = f32_product<AK, BKM, EPI, GROUPED>;
-    p.table_at = EPI == EPI_STORE && !p.vec && !p.part ? SMEM_STAGED : SMEM;
+    // (a streamed launch over experts finishes whole tiles itself)
+    p.table_at = EPI == EPI_STORE && !p.vec && (GROUPED || !p.part) ? SMEM_STAGED : SMEM;
     const int smem = p.table_at + (GROUPED ? group_table_bytes(p.groups.E) : 0);
     cudaError_t e = allow_smem<kernel>(SMEM_STAGED + (GROUPED ? group_table_bytes(MAX_EXPERTS) : 0));
     if (e != cudaSuccess) return e;
     e = launch_with(kernel, pl.units, THREADS, smem, 1, st, p);
     if (e != cudaSuccess || !p.part) return e;
-    return launch_with(f32_join<EPI>, join_blocks(p), 256, 0, 1, st, p, pl.units);
+    if constexpr (GROUPED) {
+        return launch_with(f32_group_join<AK, EPI>, group_join_blocks(pl.units, !AK), 256, group_table_bytes(p.groups.E), 1, st, p, pl.units);
+    } else {
+        return launch_with(f32_join<EPI>, join_blocks(p), 256, 0, 1, st, p, pl.units);
+    }
 }
 
 template <bool GROUPED>

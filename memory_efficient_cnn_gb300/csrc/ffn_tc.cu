@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
     if (p.first && blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
     const GroupTable table = group_table(dyn + p.table_at, p.groups.E);
     if (GROUPED) {
-        if (warp == 3) fill_group_table(table, p.groups, p.rows_bound, T::M, p.tiles_n, lane);
+        if (warp == 3) fill_group_table<!AK>(table, p, T::M, lane);
         __syncthreads();
     }
     auto begin_walk = [&] {
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
             constexpr int SPAN = COLS / SHARES;  // output columns of the warp
             // what was kept of a chunk is on its way before the chunk's sums are looked at
             KeptChunk kept;
-            if (EPI == EPI_DGATED && !p.part) fetch_kept(p, kept, m, m_end, w.tn * COLS + share * SPAN);
+            if (EPI == EPI_DGATED && (GROUPED ? w.whole : !p.part)) fetch_kept(p, kept, m, m_end, w.tn * COLS + share * SPAN);
             if (!warp_bar_wait(acc_full + 8 * buf, (n_tile >> 1) & 1, ctl, SITE_ACC_FULL)) break;
             tc_fence_after();
             const uint32_t taddr = tmem + buf * BN + ((uint32_t)(q * 32) << 16);
@@ -361,16 +361,17 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                 __syncwarp();
                 if (lane == 0) arrive_relaxed(empty_bar0 + 8 * buf);
             };
-            if (p.part) {
+            if (GROUPED ? p.part && !w.whole : p.part != nullptr) {
                 constexpr int PART_SPAN = BN / SHARES;
-                float *dst = p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
+                float *dst = GROUPED ? p.part + ((int64_t)(2 * unit + w.slot) * T::M + (int)rank * ROWS + q * 32 + lane) * BN
+                                     : p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
 #pragma unroll 1
                 for (int c = share * PART_SPAN; c < (share + 1) * PART_SPAN; c += CHUNK) {
                     uint32_t r[CHUNK];
                     load_chunk(taddr + c, r);
                     tmem_wait_ld();
                     if (c + CHUNK == (share + 1) * PART_SPAN) release();
-                    if (m < p.M) {
+                    if (m < m_end) {
 #pragma unroll
                         for (int i = 0; i < CHUNK / 4; ++i)
                             reinterpret_cast<uint4 *>(dst + c)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
@@ -418,18 +419,10 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
     if (warp == 2) free_tmem<CG>(tmem, 2 * BN);
 }
 
-// Adds the partial tiles of a streamed launch and finishes the outputs: one
-// thread for eight consecutive output columns.
-template <int BN, int EPI>
-__global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams p, int tile_m, int units) {
-    allow_dependents();
-    grid_dependency_wait();
-    constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;
-    int z, m, n, count;
-    const float *src;
-    if (!join_source<COLS, BN>(p, tile_m, units, z, m, n, count, src)) return;
-    F2 v[4], u[4];
-    add_partials<EPI == EPI_GATED, BN>(src, p.part_step, count, v, u);
+// Eight output columns of row m from their sums v (GATED: g, and u); none: whatever was kept, they are zero.
+template <int EPI>
+__device__ __forceinline__ void finish_octet(const TcParams &p, F2 (&v)[4], F2 (&u)[4], int m, int n, void *out, float scale,
+                                             bool none = false) {
     const int left = min(8, p.N - n);
     const int64_t at = (int64_t)m * p.ldo + n;
     auto put = [&](uint16_t *dst, const F2(&r)[4]) {
@@ -453,12 +446,18 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams 
         if (p.kept) {
             gate_values<4, true>(p.act, v, u, a);
             keep_columns(p.kept + kept_block(m, n, p.N), a, u);
+            if (p.scale) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = mul2(v[i], f2(scale));
+                put(static_cast<uint16_t *>(p.out2) + at, a);
+            }
         } else {
             gate_values<4, false>(p.act, v, u, a);
         }
     } else if (EPI == EPI_DGATED) {
         const uint4 *from = reinterpret_cast<const uint4 *>(p.kept + kept_block(m, n, p.N));
-        const uint4 ha = from[0], hb = from[32], lo = from[64];
+        const uint4 nothing = make_uint4(0, 0, 0, 0);
+        const uint4 ha = none ? nothing : from[0], hb = none ? nothing : from[32], lo = none ? nothing : from[64];
         F2 a[4], b[4];
         kept8(a, ha, lo.x, lo.y);
         kept8(b, hb, lo.z, lo.w);
@@ -469,20 +468,79 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams 
         }
         put(static_cast<uint16_t *>(p.out2) + at, a);
     }
-    put(static_cast<uint16_t *>(z ? p.out2 : p.out) + at, v);
+    put(static_cast<uint16_t *>(out) + at, v);
+}
+
+// Adds the partial tiles of a streamed launch and finishes the outputs: one
+// thread for eight consecutive output columns.
+template <int BN, int EPI>
+__global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcParams p, int tile_m, int units) {
+    allow_dependents();
+    grid_dependency_wait();
+    constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;
+    int z, m, n, count;
+    const float *src;
+    if (!join_source<COLS, BN>(p, tile_m, units, z, m, n, count, src)) return;
+    F2 v[4], u[4];
+    add_partials<EPI == EPI_GATED, BN>(src, p.part_step, count, v, u);
+    finish_octet<EPI>(p, v, u, m, n, z ? p.out2 : p.out, 0.0f);
+}
+
+// The same for a streamed launch over experts.
+template <int CG, int BN, bool AK, int EPI>
+__global__ void __launch_bounds__(256) tc_group_join(const __grid_constant__ TcParams p, int units) {
+    using T = Tile<CG, BN>;
+    constexpr int COLS = EPI == EPI_GATED ? BN / 2 : BN;
+    extern __shared__ unsigned char dyn[];
+    allow_dependents();
+    grid_dependency_wait();
+    const GroupTable table = group_table(dyn, p.groups.E);
+    if (threadIdx.x < 32) fill_group_table<!AK>(table, p, T::M, threadIdx.x);
+    __syncthreads();
+    if (!AK) zero_empty<uint16_t>(table, p.groups.E, p.out, p.batch == 2 ? p.out2 : nullptr, (int64_t)p.M * p.ldo);
+    Work w;
+    int unit, last;
+    if (!group_join_source(GroupSpace<!AK>(p, table, T::M), units, w, unit, last)) return;
+    const int m_end = !AK ? p.M : EPI == EPI_STORE ? w.row_end : w.pad_end;
+    for (int id = blockIdx.x % JOIN_SHARES * 256 + threadIdx.x; id < T::M * COLS / 8; id += JOIN_SHARES * 256) {
+        const int row = id / (COLS / 8), col = id % (COLS / 8) * 8;
+        const int m = w.tm * T::M + row + (AK ? w.row0 : 0), n = w.tn * COLS + col;
+        if (m >= m_end || n >= p.N) continue;
+        F2 v[4], u[4];
+        add_parts<EPI == EPI_GATED>(p.part, T::M, BN, row, col, unit, last, v, u);
+        if (AK && EPI == EPI_STORE) {
+            ulonglong2 *to = reinterpret_cast<ulonglong2 *>(static_cast<float *>(p.out) + (int64_t)m * p.ldo + n);
+            to[0] = make_ulonglong2(v[0].v, v[1].v), to[1] = make_ulonglong2(v[2].v, v[3].v);
+            continue;
+        }
+        const bool none = AK && m >= w.row_end;
+        const float scale = AK && p.scale && !none ? p.scale[m] : 0.0f;
+        if (none || EPI == EPI_DGATED) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = none ? f2(0.0f) : mul2(v[i], f2(scale)), u[i] = none ? f2(0.0f) : u[i];
+        }
+        void *out = w.z ? p.out2 : p.out;
+        if (!AK) out = static_cast<uint16_t *>(out) + (int64_t)w.e * p.M * p.ldo;
+        finish_octet<EPI>(p, v, u, m, n, out, scale, none);
+    }
 }
 
 template <int CG, int BN, bool AK, bool BKM, int EPI, bool GROUPED>
 cudaError_t launch_shape(TcParams &p, const TcPlan &pl, cudaStream_t st) {
     using T = Tile<CG, BN>;
     constexpr auto kernel = tc_product<CG, BN, AK, BKM, EPI, GROUPED>;
-    p.table_at = EPI == EPI_STORE && p.vec == 2 && !p.part ? T::SMEM_STAGED : T::SMEM;
+    // (a streamed launch over experts finishes whole tiles itself)
+    p.table_at = EPI == EPI_STORE && p.vec == 2 && (GROUPED || !p.part) ? T::SMEM_STAGED : T::SMEM;
     const int smem = p.table_at + (GROUPED ? group_table_bytes(p.groups.E) : 0);
     cudaError_t e = allow_smem<kernel>(T::SMEM_STAGED + (GROUPED ? group_table_bytes(MAX_EXPERTS) : 0));
     if (e != cudaSuccess) return e;
     e = launch_with(kernel, pl.units * CG, THREADS, smem, CG, st, p);
     if (e != cudaSuccess || !p.part) return e;
-    return launch_with(tc_join<BN, EPI>, join_blocks(p), 256, 0, 1, st, p, T::M, pl.units);
+    if constexpr (GROUPED) {
+        return launch_with(tc_group_join<CG, BN, AK, EPI>, group_join_blocks(pl.units, !AK), 256, group_table_bytes(p.groups.E), 1, st, p, pl.units);
+    } else {
+        return launch_with(tc_join<BN, EPI>, join_blocks(p), 256, 0, 1, st, p, T::M, pl.units);
+    }
 }
 
 template <int CG, int BN, bool GROUPED>
@@ -511,9 +569,11 @@ TcPlan plan_tc(const Product &d) {
         TcPlan best = plan_groups(d, 2, 256, 0.345, epi);
         const TcPlan single = plan_groups(d, 1, 128, 0.335, 0.55 * epi + 0.1);
         if (single.cost < best.cost) best = single;
-        // narrower tiles for rows of A alone, whose experts may be read by few rows each
+        // Narrower tiles where about one tile of rows reads an expert: the weights are most of what is copied, and
+        // the waves come out more even. (With many tiles the rows are copied twice as often: 46 us instead of 40 us
+        // for 25088 rows of 2 x 1024 by 256 columns.)
         const TcPlan narrow = plan_groups(d, 2, 128, 0.26, 0.55 * epi + 0.1);
-        return d.a0.k_major && narrow.cost < best.cost ? narrow : best;
+        return d.a0.k_major && d.rows <= 256.0 * d.groups.E && narrow.cost < best.cost ? narrow : best;
     }
     const TcPlan pair = plan_tiles(d, 2, 256, 0.345, epi), single = plan_tiles(d, 1, 128, 0.335, 0.55 * epi + 0.1);
     return single.cost < pair.cost ? single : pair;

@@ -135,6 +135,7 @@ struct Work {
     // Grouped rows of A: the tile's expert, its first row, and the ends of its rows without and
     // with the padding. Grouped sums: the expert, its first row, of which the K blocks count.
     int e, row0, row_end, pad_end;
+    bool whole;  // grouped: the run is all of its tile
 };
 
 // The K blocks of a streamed launch are dealt to `units` CTA groups: unit i takes
@@ -188,8 +189,8 @@ struct Walk {
     }
 };
 
-// The groups as the roles of a CTA read them, in shared memory: the experts' first rows, their
-// counts, and, of rows of A, their first tiles and the number of all.
+// The groups as the roles of a CTA read them, in shared memory: the experts' first rows, their counts, and
+// where their work begins: of rows of A in tiles, of sums in K blocks of all tiles of a matrix.
 struct GroupTable {
     int *begin, *count, *first;
 };
@@ -198,72 +199,194 @@ __device__ inline GroupTable group_table(void *smem, int E) {
     int *p = static_cast<int *>(smem);
     return {p, p + E, p + 2 * E};
 }
-// Filled by one warp. tile_m, tiles_n: rows of a tile, tiles of a row of them. (A backward call gets the
-// groups from a buffer of the caller's: whatever it holds, no row at or past `bound` is touched.)
-__device__ inline void fill_group_table(const GroupTable &t, const Groups &g, int bound, int tile_m, int tiles_n, int lane) {
-    int before = 0;  // tiles of the experts before this pass
+// Filled by one warp. (A backward call gets the groups from a buffer of the caller's: whatever it
+// holds, no row at or past rows_bound is touched.)
+template <bool SUMMED, typename P>
+__device__ inline void fill_group_table(const GroupTable &t, const P &p, int tile_m, int lane) {
+    const Groups &g = p.groups;
+    int before = 0;
     for (int e0 = 0; e0 < g.E; e0 += 32) {
         const int e = e0 + lane;
-        const int begin = e < g.E ? min(max(g.begin[e], 0), bound) / GROUP_ROWS * GROUP_ROWS : 0;
-        const int count = e < g.E ? min(max(g.count[e], 0), bound - begin) : 0;
-        const int tiles = (count + tile_m - 1) / tile_m * tiles_n;
-        int sum = tiles;
+        const int begin = e < g.E ? min(max(g.begin[e], 0), p.rows_bound) / GROUP_ROWS * GROUP_ROWS : 0;
+        const int count = e < g.E ? min(max(g.count[e], 0), p.rows_bound - begin) : 0;
+        const int work = SUMMED ? (count + BK - 1) / BK * p.tiles_m * p.tiles_n : (count + tile_m - 1) / tile_m * p.tiles_n;
+        int sum = work;
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += v;
         }
-        if (e < g.E) t.begin[e] = begin, t.count[e] = count, t.first[e] = before + sum - tiles;
+        if (e < g.E) t.begin[e] = begin, t.count[e] = count, t.first[e] = before + sum - work;
         before += __shfl_sync(0xffffffffu, sum, 31);
     }
     if (lane == 0) t.first[g.E] = before;
 }
 
-// Walks a CTA group's work over experts: tile after tile of rows of A (each expert in bands as
-// above), or, SUMMED, the E * batch output matrices.
+// The K blocks of a grouped launch in one order: tile after tile of an expert (in bands as above), expert
+// after expert; SUMMED: first all of out, then all of out2.
 template <bool SUMMED>
-struct GroupWalk {
+struct GroupSpace {
     GroupTable t;
-    int KB, KT, tiles_m, tiles_n, tile_m, E, units, at, end, e;
+    int KT, tiles_m, tiles_n, tile_m, E, batch;
     template <typename P>
-    __device__ GroupWalk(const P &p, const GroupTable &table, int tile_m_, int unit, int units_) : t(table) {
-        KB = p.KB, KT = p.KB * p.segs, tiles_m = p.tiles_m, tiles_n = p.tiles_n, tile_m = tile_m_, E = p.groups.E;
-        units = units_, at = unit, e = 0;
-        end = SUMMED ? p.tiles : t.first[E];
-    }
-    __device__ bool next(Work &w) {
-        if (at >= end) return false;
-        int r, rows_m;
-        w.z = w.slot = w.k0 = 0;
-        if (SUMMED) {
-            const int per = tiles_m * tiles_n, m = at / per;  // (the matrices of an expert follow one another)
-            r = at - m * per;
-            w.z = m / E;  // (all of the first product before those of the second)
-            w.e = m - w.z * E;
-            w.k1 = (t.count[w.e] + BK - 1) / BK;
-            rows_m = tiles_m;
-        } else {
-            int hi = E;  // first[e] <= at < first[hi]
-            while (hi - e > 1) {
-                const int mid = (e + hi) / 2;
-                if (t.first[mid] <= at) e = mid;
-                else hi = mid;
-            }
-            w.e = e;
-            r = at - t.first[e];
-            w.k1 = KT;
-            rows_m = (t.count[e] + tile_m - 1) / tile_m;
-        }
+    __device__ GroupSpace(const P &p, const GroupTable &table, int tile_m_)
+        : t(table), KT(p.KB * p.segs), tiles_m(p.tiles_m), tiles_n(p.tiles_n), tile_m(tile_m_), E(p.groups.E), batch(p.batch) {}
+    __device__ int64_t total() const { return (int64_t)t.first[E] * (SUMMED ? batch : KT); }
+    // CTA groups that a streamed launch deals its blocks to: four blocks each at least
+    __device__ int takers(int units) const { return (int)max((int64_t)1, min((int64_t)units, total() / 4)); }
+    // the r-th tile of expert w.e
+    __device__ void place(Work &w, int r) const {
+        const int count = t.count[w.e], rows_m = SUMMED ? tiles_m : (count + tile_m - 1) / tile_m;
         w.row0 = t.begin[w.e];
-        w.row_end = w.row0 + t.count[w.e];
-        w.pad_end = w.row0 + (t.count[w.e] + GROUP_ROWS - 1) / GROUP_ROWS * GROUP_ROWS;
+        w.row_end = w.row0 + count;
+        w.pad_end = w.row0 + (count + GROUP_ROWS - 1) / GROUP_ROWS * GROUP_ROWS;
         const int band = r / (8 * tiles_n), in = r - band * 8 * tiles_n;
         const int rows = min(8, rows_m - band * 8);
         w.tn = in / rows;
         w.tm = band * 8 + in - w.tn * rows;
+    }
+    __device__ int expert_of(int64_t at) const {  // first[e] <= at < first[e + 1]
+        int e = 0, hi = E;
+        while (hi - e > 1) {
+            const int mid = (e + hi) / 2;
+            if (t.first[mid] <= at) e = mid;
+            else hi = mid;
+        }
+        return e;
+    }
+    // The tile with block `at` (below total()): w but for its K blocks; returns the block's place in it, of `len`.
+    __device__ int locate(int64_t at, Work &w, int &len) const {
+        int r, k;
+        if (SUMMED) {
+            w.z = at >= t.first[E] ? 1 : 0;
+            const int in = (int)(at - (int64_t)w.z * t.first[E]);
+            w.e = expert_of(in);
+            len = (t.count[w.e] + BK - 1) / BK;
+            r = (in - t.first[w.e]) / len;
+            k = in - t.first[w.e] - r * len;
+        } else {
+            const int tile = (int)(at / KT);
+            w.z = 0;
+            w.e = expert_of(tile);
+            len = KT;
+            r = tile - t.first[w.e];
+            k = (int)(at - (int64_t)tile * KT);
+        }
+        place(w, r);
+        return k;
+    }
+};
+
+// Walks a CTA group's work over experts: every units-th tile, or a share of the K blocks (streamed). A run
+// that is part of its tile goes to the unit's first buffer of partial sums where it begins inside, and can
+// only be the unit's first then, else to its second.
+template <bool SUMMED>
+struct GroupWalk {
+    GroupSpace<SUMMED> space;
+    int units;
+    bool streamed;
+    int64_t at, end;
+    template <typename P>
+    __device__ GroupWalk(const P &p, const GroupTable &table, int tile_m, int unit, int units_) : space(p, table, tile_m), units(units_) {
+        streamed = p.part != nullptr;
+        if (streamed) {
+            const int64_t total = space.total();
+            const int takers = space.takers(units);
+            at = unit < takers ? stream_begin(total, takers, unit) : total;
+            end = unit < takers ? stream_begin(total, takers, unit + 1) : total;
+        } else {
+            at = unit;
+            end = SUMMED ? p.tiles : table.first[space.E];
+        }
+    }
+    __device__ bool next(Work &w) {
+        if (at >= end) return false;
+        int len;
+        if (streamed) {
+            w.k0 = space.locate(at, w, len);
+            w.k1 = (int)min((int64_t)len, w.k0 + end - at);
+            w.slot = w.k0 == 0;
+            w.whole = w.k0 == 0 && w.k1 == len;
+            at += w.k1 - w.k0;
+            return true;
+        }
+        w.k0 = w.slot = 0;
+        w.whole = true;
+        if (SUMMED) {  // (experts without rows too: their outputs are zero)
+            const int per = space.tiles_m * space.tiles_n, m = (int)at / per;
+            w.z = m / space.E;
+            w.e = m - w.z * space.E;
+            w.k1 = (space.t.count[w.e] + BK - 1) / BK;
+            space.place(w, (int)at - m * per);
+        } else {
+            space.locate(at * space.KT, w, len);
+            w.k1 = len;
+        }
         at += units;
         return true;
     }
 };
+
+// ---- joining the partial tiles of a streamed grouped launch: JOIN_SHARES blocks for each border between
+// two units. The tile that a border cuts is joined at its first border. (A block for every 256 octets of
+// output columns took 13 us where these take 5.)
+constexpr int JOIN_SHARES = 8;
+inline int group_join_blocks(int units, bool summed) { return (units - 1) * JOIN_SHARES + (summed ? 64 : 0); }
+// The block's tile w and the units whose parts it adds: `unit`'s second buffer, then the first ones of those up
+// to `last`. False: nothing to do.
+template <bool SUMMED>
+__device__ __forceinline__ bool group_join_source(const GroupSpace<SUMMED> &space, int units, Work &w, int &unit, int &last) {
+    const int i = blockIdx.x / JOIN_SHARES + 1;
+    const int takers = space.takers(units);
+    if (i >= takers || i >= units) return false;
+    const int64_t total = space.total(), at = stream_begin(total, takers, i);
+    int len;
+    const int k = space.locate(at, w, len);
+    const int64_t start = at - k;
+    if (k == 0 || start < stream_begin(total, takers, i - 1)) return false;
+    unit = i - 1, last = i;
+    while (last + 1 < takers && stream_begin(total, takers, last + 1) < start + len) ++last;
+    return true;
+}
+// Their sums (TWO: of g and u, half a tile's columns apart).
+template <bool TWO>
+__device__ __forceinline__ void add_parts(const float *part, int tile_m, int bn, int row, int col, int unit, int last, F2 (&v)[4],
+                                          F2 (&u)[4]) {
+    const int64_t tile = (int64_t)tile_m * bn;
+    const float *from = part + (int64_t)row * bn + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = u[i] = f2(0.0f);
+    auto add = [](F2(&sum)[4], const float *p) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 a = reinterpret_cast<const float4 *>(p)[i];
+            sum[2 * i] = add2(sum[2 * i], f2(a.x, a.y)), sum[2 * i + 1] = add2(sum[2 * i + 1], f2(a.z, a.w));
+        }
+    };
+    for (int j = unit; j <= last; ++j) {
+        const float *p = from + (2 * j + (j == unit ? 1 : 0)) * tile;
+        add(v, p);
+        if (TWO) add(u, p + bn / 2);
+    }
+}
+// Zeros for the matrices of experts without rows, by the launch's last 64 blocks.
+template <typename T>
+__device__ __forceinline__ void zero_empty(const GroupTable &t, int E, void *out, void *out2, int64_t elements) {
+    const int block = blockIdx.x - (gridDim.x - 64);
+    if (block < 0) return;
+    for (int e = 0; e < E; ++e) {
+        if (t.count[e] > 0) continue;
+        for (void *base : {out, out2}) {
+            if (!base) continue;
+            T *p = static_cast<T *>(base) + e * elements;
+            if (elements * sizeof(T) % 16 == 0) {
+                for (int64_t i = block * 256 + threadIdx.x; i < elements * (int64_t)sizeof(T) / 16; i += 64 * 256)
+                    reinterpret_cast<uint4 *>(p)[i] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int64_t i = block * 256 + threadIdx.x; i < elements; i += 64 * 256) p[i] = T(0);
+            }
+        }
+    }
+}
 
 constexpr int CHUNK = 16;  // accumulator columns a warp turns into outputs at a time
 constexpr int PAIRS = CHUNK / 2;
@@ -495,10 +618,11 @@ inline TcPlan plan_tiles(const Product &d, int cg, int bn, double kb, double epi
     return st.cost < pl.cost ? st : pl;
 }
 
-// The plan of a grouped product: plain tiles of 128 * cg rows and bn columns. The experts' shares are
-// not known here; they are taken to be even, with the last tile of rows half full. kb and epi
-// as in plan_tiles; while few rows share an expert's weights, a K block takes no less than its part of
-// reading them at 6 TB/s.
+// The plan of a grouped product: tiles of 128 * cg rows and bn columns, whole or their K blocks dealt out
+// evenly (streamed). The experts' shares are not known here; they are taken to be even, with the
+// last tile of rows half full, and the largest expert to have 1.6 times its share of a sum. kb and epi as
+// in plan_tiles; while few rows share an expert's weights, a K block takes no less than its part of
+// reading them at 6 TB/s. Partial tiles, of which a unit has two at most, stay in L2.
 inline TcPlan plan_groups(const Product &d, int cg, int bn, double kb, double epi) {
     const bool summed = !d.a0.k_major;
     const int tm = ROWS * cg, cols = d.epi == EPI_GATED ? bn / 2 : bn, z = d.batch ? 2 : 1, most = SMS / cg;
@@ -507,21 +631,36 @@ inline TcPlan plan_groups(const Product &d, int cg, int bn, double kb, double ep
     pl.tiles_m = (d.M + tm - 1) / tm;
     pl.tiles_n = (d.N + cols - 1) / cols;
     const double E = std::min<double>(d.groups.E, d.rows);  // experts with rows
-    double KT, tiles;
+    double KT, tiles, largest, bound, read = 0;
     if (summed) {
-        KT = d.rows / d.groups.E / BK + 0.5;
-        tiles = (double)z * d.groups.E * pl.tiles_m * pl.tiles_n;
-        pl.units = (int)std::min<double>(most, tiles);
+        KT = d.rows / E / BK + 0.5;
+        tiles = (double)z * E * pl.tiles_m * pl.tiles_n;
+        // (both operands' rows are read in pieces of 256 bytes, at 3 TB/s as measured)
+        read = KT * tiles * ((double)tm / pl.tiles_n + (double)bn / pl.tiles_m) * BK * 2 / 3e6;
+        largest = 1.6 * KT;
+        bound = (double)z * d.groups.E * pl.tiles_m * pl.tiles_n;
     } else {
         const double tiles_m = std::max(1.0, d.rows / E / tm + 0.5);  // of an expert
-        KT = (double)((d.K + BK - 1) / BK * (d.epi != EPI_GATED && d.a1.p ? 2 : 1));
+        KT = largest = (double)((d.K + BK - 1) / BK * (d.epi != EPI_GATED && d.a1.p ? 2 : 1));
         tiles = std::ceil(E * tiles_m) * pl.tiles_n;
-        kb = std::max(kb, bn * BK * 2.0 * most / tiles_m / 6e6);
-        // (a bound: every expert's last tile may hold one row)
-        pl.units = (int)std::min<double>(most, std::min<double>((double)((int64_t)d.M / tm + d.groups.E), d.M) * pl.tiles_n);
+        kb = std::max(kb, bn / tiles_m * BK * 2 * most / 6e6);
+        // (every expert's last tile may hold one row)
+        bound = std::min<double>((double)((int64_t)d.M / tm + d.groups.E), d.M) * pl.tiles_n;
     }
+    pl.units = (int)std::min<double>(most, bound);
     const double waves = std::ceil(std::max(1.0, tiles / most));
-    pl.cost = 4 + KT * kb + epi + (waves - 1) * std::max(KT * kb, epi);
+    pl.cost = 4 + std::max(read, largest * kb + epi + (waves - 1) * std::max(KT * kb, epi));
+    // Work counts stay in 32 bits. With more tiles streaming does not pay: whole tiles next to one another find
+    // their operands in L2 (16384 rows by 2048 columns: 683 us streamed, 420 us plain; 64 tiles of 49 blocks on 76
+    // pairs: 49 us and 40 us; 45 tiles of 32 blocks on 152 CTAs in fp32: 30 us and 45 us).
+    if (bound * (KT + 1) * 4 > 1e9 || 2 * tiles > most) return pl;
+    const double part = (double)most * tm * bn * 4, blocks = tiles * KT;
+    const double cost = 4 + std::max(std::max(read, std::max(4.0, blocks / most) * kb), tiles / most * epi) + epi + 4 + 3 * part / 10e6;
+    if (cost >= pl.cost) return pl;
+    pl.streamed = true;
+    pl.cost = cost;
+    pl.units = most;
+    pl.part_bytes = (size_t)(2 * most) * tm * bn * 4;
     return pl;
 }
 

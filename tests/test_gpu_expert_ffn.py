@@ -69,6 +69,14 @@ def test_large(dt, T, k, E, C, F):
     check(T, k, E, C, F, dt, "gelu", seed=3)
 
 
+@pytest.mark.parametrize("choose", ["uneven", "one", "any"])
+@pytest.mark.parametrize("dt,T,k,E,C,F", [("bf16", 70, 2, 3, 2000, 1607), ("f16", 9000, 1, 5, 72, 104), ("bf16", 4100, 2, 2, 33, 40),
+                                          ("f32", 150, 2, 3, 700, 1101), ("f32", 4000, 1, 4, 40, 65), ("f16", 66, 1, 1, 2304, 136)])
+def test_long_sums_over_few_tiles(choose, dt, T, k, E, C, F):
+    """Sums whose K blocks are dealt out over more CTAs than there are tiles, with experts that get none."""
+    check(T, k, E, C, F, dt, seed=T, choose=choose)
+
+
 @pytest.mark.parametrize("E", [300, 1024])
 def test_many_experts(E):
     check(500, 3, E, 24, 40, "bf16", seed=E)
