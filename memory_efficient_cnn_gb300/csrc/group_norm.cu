@@ -24,7 +24,7 @@ bool known_act(int act) {
 GroupArgs make(int64_t N, int64_t P, int64_t C, int64_t G, int act, int dtype, int maps) {
     GroupArgs a = {};
     a.N = N, a.P = P, a.C = (int)C, a.G = (int)G, a.D = (int)(C / G), a.act = act;
-    if (!cut_resident(a, elem_size(dtype), maps)) cut(a, elem_size(dtype));
+    if (!cut_resident(a, elem_size(dtype), maps)) cut(a, elem_size(dtype), maps);
     return a;
 }
 

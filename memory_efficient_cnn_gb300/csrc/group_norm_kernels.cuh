@@ -96,7 +96,8 @@ __device__ __forceinline__ void with_norm_act(int act, Fn f) {
 // 1 / (1 + 2^a), two values with one reciprocal: 1/p and 1/q are q and p over pq. Half the
 // instructions of the slowest unit: with a reciprocal each, silu over 51 million values took
 // 25 us of the reading and writing pass's 31 us. (a is bounded so that pq stays finite; a NaN becomes a
-// number here, which its neighbour needs: callers multiply by the value itself.)
+// number here, which its neighbour needs: callers multiply by the value
+// itself. Where a is bounded silu is z 2^-63, nothing next to z's rounding.)
 __device__ __forceinline__ F2 logistic2(F2 a) {
     const F2 e = add2(exp2_2(each2(a, [](float v) { return fminf(v, 63.0f); })), f2(1.0f));
     float p, q, inv;
@@ -186,8 +187,9 @@ template <int MAPS>
 constexpr int RING_DEPTH = 8 / MAPS;
 template <typename T, int V>
 constexpr int RING_BYTES = 8 * THREADS * V * (int)sizeof(T);
-template <typename T, int V, int MAPS, typename Fn>
-__device__ __forceinline__ void each_vector(const Place<T, V> &at, const T *const (&src)[MAPS], void *ring, Fn f) {
+// begin(slots) is called with the first DEPTH - 1 positions under way, f(position, vectors) for each of them.
+template <typename T, int V, int MAPS, typename Begin, typename Fn>
+__device__ __forceinline__ void each_vector(const Place<T, V> &at, const T *const (&src)[MAPS], void *ring, Begin begin, Fn f) {
     using Word = typename Group<T, V>::Word;
     constexpr int DEPTH = RING_DEPTH<MAPS>;
     Word *slots = static_cast<Word *>(ring) + threadIdx.x;
@@ -209,6 +211,7 @@ __device__ __forceinline__ void each_vector(const Place<T, V> &at, const T *cons
     };
 #pragma unroll
     for (int i = 0; i < DEPTH - 1; ++i) start();
+    begin(slots);
 #pragma unroll 1
     for (int k = 0; k < at.count; ++k) {
         start();
@@ -219,6 +222,10 @@ __device__ __forceinline__ void each_vector(const Place<T, V> &at, const T *cons
         if (++get == DEPTH) get = 0;
         f(k, w);
     }
+}
+template <typename T, int V, int MAPS, typename Fn>
+__device__ __forceinline__ void each_vector(const Place<T, V> &at, const T *const (&src)[MAPS], void *ring, Fn f) {
+    each_vector<T, V, MAPS>(at, src, ring, [](auto *) {}, f);
 }
 
 // What makes z of the thread's channels: z = (x - mean) scale + b, scale = w / deviation.
@@ -319,21 +326,22 @@ __global__ void __launch_bounds__(THREADS, 4) gn_moments(const __grid_constant__
     F2 mean[PAIRS], m2[PAIRS], pivot[PAIRS];
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) mean[i] = m2[i] = pivot[i] = f2(0.0f);
-    if (at.count > 0) {
+    const T *const src[1] = {at.at(a.x)};
+    auto take_pivot = [&](const Word *slots) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(RING_DEPTH<1> - 1 - FIRST) : "memory");
+        const F2 share = f2(-1.0f / (float)max(1, min(FIRST, at.count)));  // (the negative pivot)
 #pragma unroll
         for (int j = 0; j < FIRST; ++j) {
             if (j >= at.count) continue;
             F2 v[PAIRS];
-            to_pairs<T, V>(*reinterpret_cast<const Word *>(at.at(a.x) + j * at.step), v);
+            to_pairs<T, V>(slots[j * THREADS], v);
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) pivot[i] = add2(pivot[i], v[i]);
         }
-        const F2 share = f2(-1.0f / (float)min(FIRST, at.count));  // (the negative pivot)
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) pivot[i] = mul2(pivot[i], share);
-    }
-    const T *const src[1] = {at.at(a.x)};
-    each_vector<T, V, 1>(at, src, ring, [&](int, const Word (&w)[1]) {
+    };
+    each_vector<T, V, 1>(at, src, ring, take_pivot, [&](int, const Word (&w)[1]) {
         F2 v[PAIRS];
         to_pairs<T, V>(w[0], v);
 #pragma unroll
@@ -886,8 +894,8 @@ cudaError_t launch(K kernel, int64_t blocks, cudaStream_t st, const GroupArgs &a
     return launch_with(kernel, blocks, st, smem, cluster, a);
 }
 
-// A block a group where a warp would take more than 32 loads of each sum.
-inline bool by_block(const GroupArgs &a) { return (int64_t)a.D * a.chunks > 1024; }
+// A block a group where a warp would take more than 8 loads of each sum.
+inline bool by_block(const GroupArgs &a) { return (int64_t)a.D * a.chunks > 256; }
 inline int64_t group_blocks(const GroupArgs &a) { return by_block(a) ? a.N * a.G : (a.N * a.G + 7) / 8; }
 
 template <typename T, typename Fn>
