@@ -491,7 +491,8 @@ im2win_status im2win_group_norm_backward(const void *dy, const void *x, const vo
  * ------------------
  * T rows (positions of channels-last maps, or feature vectors) are each sent to k of E
  * gated feed-forwards. The router chooses them from logits[T][E], and im2win_expert_ffn
- * computes the sum of their weighted outputs.
+ * computes the sum of their weighted outputs. experts, weights and dweights need only their
+ * element's alignment (rows of a longer list), the other pointers 16 bytes.
  */
 typedef enum {
     IM2WIN_ROUTE_TOP = 0, /* weights: softmax over the row's k choices */

@@ -261,9 +261,9 @@ im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const voi
     if (!known_act(act)) return IM2WIN_ERR_INVALID_ARG;
     if (T == 0) return IM2WIN_OK;  // no rows: nothing to read or write
     if (!x || !experts || !weights || !w_gate || !w_up || !w_down || !y) return IM2WIN_ERR_INVALID_ARG;
-    for (const void *p : {x, (const void *)experts, weights, w_gate, w_up, w_down, (const void *)y, (const void *)saved,
-                          (const void *)ws})
+    for (const void *p : {x, w_gate, w_up, w_down, (const void *)y, (const void *)saved, (const void *)ws})
         if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
+    if (!aligned_to(experts, 4) || !aligned_to(weights, elem_size(dtype))) return IM2WIN_ERR_MISALIGNED;
     const Problem q(T, k, E, C, F, act, dtype);
     const ForwardParts parts(q, saved != nullptr);
     if (!ws || ws_bytes < parts.bytes) return IM2WIN_ERR_WORKSPACE;
@@ -303,9 +303,10 @@ im2win_status im2win_expert_ffn_backward(const void *dy, const void *weights, co
     const bool want_dw = dw_gate != nullptr;
     if ((dw_up != nullptr) != want_dw || (dw_down != nullptr) != want_dw) return IM2WIN_ERR_INVALID_ARG;
     if (T > 0 && (!dy || !weights || !w_gate || !w_up || !w_down || !saved)) return IM2WIN_ERR_INVALID_ARG;
-    for (const void *p : {dy, weights, w_gate, w_up, w_down, saved, (const void *)dx, (const void *)dweights,
-                          (const void *)dw_gate, (const void *)dw_up, (const void *)dw_down, (const void *)ws})
+    for (const void *p : {dy, w_gate, w_up, w_down, saved, (const void *)dx, (const void *)dw_gate, (const void *)dw_up,
+                          (const void *)dw_down, (const void *)ws})
         if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
+    if (!aligned_to(weights, elem_size(dtype)) || !aligned_to(dweights, elem_size(dtype))) return IM2WIN_ERR_MISALIGNED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) {  // sums over no rows
         cudaError_t e = cudaSuccess;

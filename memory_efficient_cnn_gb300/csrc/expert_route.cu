@@ -6,7 +6,6 @@
 // the lanes' own largest, then the lowest lane that has it, which is the lowest index. The
 // kernel reads the logits once and is bound by that for many rows, by its launch for few.
 #include <algorithm>
-#include <initializer_list>
 
 #include "elem.cuh"
 #include "tc_ptx.cuh"
@@ -269,8 +268,7 @@ im2win_status im2win_expert_route(const void *logits, void *weights, int32_t *ex
     const im2win_status s = check(T, E, k, over, dtype);
     if (s != IM2WIN_OK || T == 0) return s;
     if (!logits || !weights || !experts) return IM2WIN_ERR_INVALID_ARG;
-    for (const void *p : {logits, (const void *)weights, (const void *)experts})
-        if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
+    if (!aligned_to(logits, 16) || !aligned_to(weights, elem_size(dtype)) || !aligned_to(experts, 4)) return IM2WIN_ERR_MISALIGNED;
     RouteArgs a = {};
     a.logits = logits, a.weights = weights, a.experts = experts;
     a.T = T, a.E = (int)E, a.k = (int)k, a.over = over;
@@ -283,8 +281,8 @@ im2win_status im2win_expert_route_backward(const void *dweights, const void *log
     const im2win_status s = check(T, E, k, over, dtype);
     if (s != IM2WIN_OK || T == 0) return s;
     if (!dweights || !logits || !experts || !dlogits) return IM2WIN_ERR_INVALID_ARG;
-    for (const void *p : {dweights, logits, (const void *)experts, (const void *)dlogits})
-        if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
+    if (!aligned_to(logits, 16) || !aligned_to(dlogits, 16) || !aligned_to(dweights, elem_size(dtype)) || !aligned_to(experts, 4))
+        return IM2WIN_ERR_MISALIGNED;
     RouteArgs a = {};
     a.dweights = dweights, a.logits = logits, a.experts = const_cast<int32_t *>(experts), a.dlogits = dlogits;
     a.T = T, a.E = (int)E, a.k = (int)k, a.over = over;

@@ -95,7 +95,9 @@ def test_route_refusals():
     for fn, names in ((call, ("logits", "weights", "experts")), (back, ("dw", "logits", "experts", "dl"))):
         for name in names:
             assert fn(**{name: None}) == ERR_INVALID_ARG
-            assert fn(**{name: 4104}) == ERR_MISALIGNED
+            assert fn(**{name: 4097}) == ERR_MISALIGNED  # (lists of choices need their element's alignment alone)
+            if name in ("logits", "dl"):
+                assert fn(**{name: 4104}) == ERR_MISALIGNED
         for kw in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(over=2), dict(over=-1), dict(dtype=4)):
             assert fn(**kw) == ERR_INVALID_ARG, kw
         for kw in (dict(E=1025), dict(E=64, k=33), dict(T=1 << 31)):
@@ -144,8 +146,9 @@ def test_expert_ffn_refusals():
     for kw in (dict(x=None), dict(experts=None), dict(weights=None), dict(wg=None), dict(wu=None), dict(wd=None), dict(y=None),
                dict(act=5), dict(act=-1), dict(dtype=3), dict(T=-1), dict(k=0), dict(E=0), dict(C=0), dict(F=0)):
         assert call(**kw) == ERR_INVALID_ARG, kw
-    for name in ("x", "experts", "weights", "wg", "wu", "wd", "y", "saved", "ws"):
+    for name in ("x", "wg", "wu", "wd", "y", "saved", "ws"):
         assert call(**{name: 4104}) == ERR_MISALIGNED, name
+    assert call(experts=4098) == ERR_MISALIGNED and call(weights=4097) == ERR_MISALIGNED
     assert call(ws=None) == ERR_WORKSPACE
     assert call(ws_bytes=mec.im2win_expert_ffn_size(mec.FFN_FORWARD, 3, 2, 4, 8, 8, F16) - 1) == ERR_WORKSPACE
     assert call(E=1025) == ERR_UNSUPPORTED and call(k=33) == ERR_UNSUPPORTED
@@ -159,7 +162,7 @@ def test_expert_ffn_refusals():
     for kw in (dict(dy=None), dict(weights=None), dict(w=None), dict(saved=None), dict(act=5), dict(dw=(4096, None, 4096)),
                dict(dw=(None, 4096, 4096))):
         assert back(**kw) == ERR_INVALID_ARG, kw
-    for kw in (dict(dy=8), dict(weights=4), dict(w=8), dict(saved=8), dict(dx=8), dict(dweights=8), dict(dw=(8,) * 3), dict(ws=8)):
+    for kw in (dict(dy=8), dict(weights=2), dict(w=8), dict(saved=8), dict(dx=8), dict(dweights=2), dict(dw=(8,) * 3), dict(ws=8)):
         assert back(**kw) == ERR_MISALIGNED, kw
     assert back(ws=None) == ERR_WORKSPACE and back(ws_bytes=16) == ERR_WORKSPACE
     assert back(dx=None, dweights=None, dw=(None,) * 3, ws=None) == OK
