@@ -58,8 +58,15 @@ struct Problem {
         : T(T_), rows(grouped_rows(T_ * k_, E_)), pairs(T_ * k_), k((int)k_), E((int)E_), C((int)C_), F((int)F_), dtype(dtype_),
           act(act_), f32(dtype_ == IM2WIN_F32), Cp((C_ + 7) / 8 * 8), Fp((F_ + 7) / 8 * 8) {}
 
-    // inference of few pairs has kernels of its own
-    bool few() const { return pairs <= FEW_PAIRS; }
+    // Inference of few pairs has kernels of its own. fp32, and widths whose experts' matrices would all be copied
+    // to a pitch, up to 64 pairs (16 rows of 4 choices of 64 experts of 1000 x 1366: 97 us and 133 us; fp32, 4 rows
+    // of 2 of 8 of 2048 x 4096: 122 us and 503 us). Else up to 8 pairs (4 rows of 2 of 8 of 2048 x 4096: 69 us
+    // and 76 us), and up to 32 of smaller experts (16 rows of 2 of 8 of 1024 x 2048: 40 us and 46 us; of 2048 x
+    // 4096: 111 us and 92 us; 32 rows of 1024 x 2048: 52 us and 46 us).
+    bool few() const {
+        if (f32 || copies(C) || copies(F)) return pairs <= FEW_PAIRS;
+        return pairs <= 8 || (pairs <= 32 && (pairs < E ? pairs : E) * C * F <= (int64_t(1) << 25));
+    }
     size_t operand(int64_t n, int64_t pitch) const { return (size_t)(n * pitch) * (f32 ? 6 : 2); }
     size_t result() const { return (size_t)(rows * Cp) * 4; }  // ys, dxs
     bool copies(int64_t cols) const { return f32 || cols % 8 != 0; }

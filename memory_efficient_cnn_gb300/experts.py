@@ -15,7 +15,7 @@ import torch
 
 from ._binding import _check, _cuda, _dtype_code, _same_device, lib
 from .block import (
-    ACTS, FFN_BACKWARD, FFN_FORWARD, FFN_SAVED, FFN_TRAIN, _alike, _bytes, _code, _empty, _ptr, _same_dtype, _shape, _stream,
+    ACTS, FFN_BACKWARD, FFN_FORWARD, FFN_SAVED, FFN_TRAIN, _alike, _bytes, _code, _ptr, _same_dtype, _shape, _stream,
     _unrecorded)
 
 ROUTES = {"top": 0, "all": 1}
@@ -132,31 +132,39 @@ def im2win_expert_ffn_size(buffer: int, T, k, E, C, F, dtype: int) -> int:
     return out.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _ffn_plan(x, weights, w_gate, w_up, w_down):
+    """(T, k, E, C, F) of the tensors' shapes; ValueError where they do not fit."""
+    if len(x) < 1 or len(weights) < 1 or len(w_gate) != 3:
+        raise ValueError("x must be [..., C], weights [..., k] and w_gate [E, F, C]")
+    C, k = x[-1], weights[-1]
+    E, F = w_gate[:2]
+    for name, shape, want in (("weights", weights, (*x[:-1], k)), ("w_gate", w_gate, (E, F, C)), ("w_up", w_up, (E, F, C)),
+                              ("w_down", w_down, (E, C, F))):
+        if shape != want:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected {want}")
+    if C < 1 or F < 1 or E < 1 or k < 1:
+        raise ValueError("C, F, the experts and a row's choices must be at least 1")
+    return math.prod(x[:-1]), k, E, C, F
+
+
 def _ffn_dims(fn, x, weights, w_gate, w_up, w_down):
     """(T, k, E, C, F) after the shape, type and device checks; x is [..., C] and weights
     [..., k] with the same leading axes."""
-    if x.dim() < 1 or weights.dim() < 1 or w_gate.dim() != 3:
-        raise ValueError(f"{fn}: x must be [..., C], weights [..., k] and w_gate [E, F, C]")
-    C, k = x.shape[-1], weights.shape[-1]
-    E, F = w_gate.shape[:2]
-    if not (C >= 1 and F >= 1 and E >= 1 and k >= 1 and weights.shape[:-1] == x.shape[:-1]
-            and w_gate.shape == w_up.shape == (E, F, C) and w_down.shape == (E, C, F)
-            and _alike(x.dtype, x.get_device(), x, weights, w_gate, w_up, w_down)):
-        _shape(fn, "weights", weights, (*x.shape[:-1], k))
-        _shape(fn, "w_gate", w_gate, (E, F, C))
-        _shape(fn, "w_up", w_up, (E, F, C))
-        _shape(fn, "w_down", w_down, (E, C, F))
-        if C < 1 or F < 1 or E < 1 or k < 1:
-            raise ValueError(f"{fn}: C, F, the experts and a row's choices must be at least 1")
+    try:
+        dims = _ffn_plan(x.shape, weights.shape, w_gate.shape, w_up.shape, w_down.shape)
+    except ValueError as e:
+        raise ValueError(f"{fn}: {e}") from None
+    if not _alike(x.dtype, x.get_device(), x, weights, w_gate, w_up, w_down):
         _same(fn, x, weights, w_gate, w_up, w_down)
-    return x.numel() // C, k, E, C, F
+    return dims
 
 
 def _buffer(fn, name, t, x, kind, dims):
     """A buffer of the call: the caller's, checked, or a new one."""
     size = im2win_expert_ffn_size(kind, *dims, _dtype_code(x))
     if t is None:
-        return _empty(size, x.device)
+        return torch.empty(size, dtype=torch.uint8, device=x.device)
     _same_device(fn, x, t)
     _cuda(t)
     if _bytes(t) < size:

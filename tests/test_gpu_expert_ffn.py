@@ -84,10 +84,10 @@ def test_many_experts(E):
 
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("choose", ["uneven", "one", "any"])
-@pytest.mark.parametrize("T,k,E,C,F", [(1, 2, 8, 512, 1024), (32, 2, 6, 520, 264), (16, 4, 3, 1000, 366), (64, 1, 20, 64, 200),
+@pytest.mark.parametrize("T,k,E,C,F", [(1, 2, 8, 512, 1024), (32, 2, 6, 520, 264), (16, 4, 3, 1000, 366), (64, 1, 20, 64, 200), (16, 2, 6, 520, 264), (8, 1, 3, 2048, 4096),
                                        (2, 32, 9, 48, 33), (5, 3, 40, 1030, 514), (13, 5, 4, 72, 4100)])
 def test_few_rows(dt, choose, T, k, E, C, F):
-    """Inference of up to 64 pairs, which has kernels of its own, and 65 beside it."""
+    """Inference of up to 8, 32 or 64 pairs, which has kernels of its own, and of 65."""
     x, experts, weights, wg, wu, wd, _ = make(T, k, E, C, F, dt, T + F, choose)
     want = ref.experts_all(x.double(), experts, weights.double(), wg.double(), wu.double(), wd.double(), "gelu", DT[dt])
     y = mec.expert_ffn(*(t.cuda() for t in (x, experts, weights, wg, wu, wd)), act="gelu")
