@@ -30,6 +30,7 @@ struct GroupArgs {
 
 constexpr int THREADS = 256;
 constexpr int64_t RESIDENT_BYTES = 16 << 20;
+constexpr int MOST_SHARES = 8;  // CTAs of a cluster
 constexpr size_t MAX_SMEM = 227 << 10;
 constexpr int FEW = 4;  // positions a thread has at least, if there are as many
 
@@ -62,12 +63,12 @@ inline bool cut_resident(GroupArgs &a, int size, int maps) {
                 return (len + rows - 1) / rows * THREADS * v * size * maps;
             };
             int s = 1;
-            while (s < 8 && tile(s) > most) s *= 2;
+            while (s < MOST_SHARES && tile(s) > most) s *= 2;
             const size_t extra = resident_extra(slab, a.D, v, 2);
             if (tile(s) > most || tile(s) + extra > MAX_SMEM) continue;
             const int slabs = (a.C + slab - 1) / slab;
             // spread over the SMs while each thread has two positions
-            while (s < 8 && a.N * slabs * s < 304 && a.P >= (int64_t)rows * 4 * s) s *= 2;
+            while (s < MOST_SHARES && a.N * slabs * s < 304 && a.P >= (int64_t)rows * 4 * s) s *= 2;
             a.resident = true;
             a.slab = slab, a.slabs = slabs, a.chunks = s;
             a.len = (a.P + s - 1) / s;

@@ -239,7 +239,9 @@ template <typename T, int V>
 struct Channels {
     static constexpr int PAIRS = Group<T, V>::PAIRS;
     F2 minus_mean[PAIRS], scale[PAIRS], b[PAIRS];
-    __device__ Channels(const GroupArgs &a, int64_t n, int c) {
+    __device__ Channels() {}
+    __device__ Channels(const GroupArgs &a, int64_t n, int c) { load(a, n, c); }
+    __device__ void load(const GroupArgs &a, int64_t n, int c) {
         each(a, n, c, [&](int i, const float2 (&s)[2], const float (&w)[2], const float (&bias)[2]) {
             minus_mean[i] = f2(-s[0].x, -s[1].x);
             scale[i] = f2(s[0].y * w[0], s[1].y * w[1]);
@@ -285,9 +287,9 @@ template <typename T, int V>
 struct Back {
     static constexpr int PAIRS = Group<T, V>::PAIRS;
     F2 base[PAIRS], slope[PAIRS];  // - i m1, - i^2 m2
-    // of(group): its -m1 and -m2; c: the first channel, g: a group's channels' start
+    // of(group): its -m1 and -m2; c: the first channel
     template <typename Fn>
-    __device__ Back(const GroupArgs &a, int64_t n, int c, Fn of) {
+    __device__ void load(const GroupArgs &a, int64_t n, int c, Fn of) {
         Channels<T, V>::each(a, n, c, [&](int i, const float2 (&s)[2], const float (&)[2], const float (&)[2]) {
             float2 m[2] = {};
 #pragma unroll
@@ -327,8 +329,9 @@ __global__ void __launch_bounds__(THREADS, 4) gn_moments(const __grid_constant__
     __shared__ float counts[THREADS];
     F2(*red)[THREADS] = reinterpret_cast<F2(*)[THREADS]>(ring);
     const Place<T, V> at(a);
-    tc::allow_dependents();
+    // (in this order: the last launch of a call reads its inputs ahead of its own wait)
     tc::grid_dependency_wait();
+    tc::allow_dependents();
     F2 mean[PAIRS], m2[PAIRS], pivot[PAIRS];
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) mean[i] = m2[i] = pivot[i] = f2(0.0f);
@@ -450,13 +453,16 @@ __global__ void __launch_bounds__(THREADS, 4) gn_apply(const __grid_constant__ G
     __shared__ alignas(16) unsigned char ring[RING_BYTES<T, V>];
     const Place<T, V> at(a, true);
     tc::allow_dependents();
-    tc::grid_dependency_wait();
-    if (!at.in) return;
-    const Channels<T, V> ch(a, at.n, at.c);
     const T *const src[1] = {at.at(a.x)};
     T *y = at.at(a.y);
+    Channels<T, V> ch;
+    // x on its way before the statistics are there
+    auto begin = [&](const Word *) {
+        tc::grid_dependency_wait();
+        if (at.in) ch.load(a, at.n, at.c);
+    };
     with_norm_act(a.act, [&](auto kind) {
-        each_vector<T, V, 1>(at, src, ring, [&](int k, const Word (&w)[1]) {
+        each_vector<T, V, 1>(at, src, ring, begin, [&](int k, const Word (&w)[1]) {
             F2 v[PAIRS];
             to_pairs<T, V>(w[0], v);
 #pragma unroll
@@ -474,8 +480,9 @@ __global__ void __launch_bounds__(THREADS, 3) gn_back_sums(const __grid_constant
     __shared__ alignas(16) unsigned char ring[std::max(RING_BYTES<T, V>, 2 * PAIRS * THREADS * 8)];
     F2(*red)[THREADS] = reinterpret_cast<F2(*)[THREADS]>(ring);
     const Place<T, V> at(a);
-    tc::allow_dependents();
+    // (in this order: the last launch of a call reads its inputs ahead of its own wait)
     tc::grid_dependency_wait();
+    tc::allow_dependents();
     F2 s0[PAIRS], s1[PAIRS];
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) s0[i] = s1[i] = f2(0.0f);
@@ -574,22 +581,27 @@ __global__ void __launch_bounds__(THREADS, 3) gn_back_apply(const __grid_constan
     using Word = typename Group<T, V>::Word;
     __shared__ alignas(16) unsigned char ring[RING_BYTES<T, V>];
     tc::allow_dependents();
-    tc::grid_dependency_wait();
     if ((int)blockIdx.x < param_blocks) {
+        tc::grid_dependency_wait();
         sum_params<T>(a, blockIdx.x);
         return;
     }
     const Place<T, V> at(a, true);
-    if (!at.in) return;
-    const Channels<T, V> ch(a, at.n, at.c);
-    const Back<T, V> back(a, at.n, at.c, [&](int g) {
-        const float2 s = reinterpret_cast<const float2 *>(a.sums)[at.n * a.G + g];
-        return make_float2(-s.x, -s.y);
-    });
+    Channels<T, V> ch;
+    Back<T, V> back;
+    auto begin = [&](const Word *) {  // (as above)
+        tc::grid_dependency_wait();
+        if (!at.in) return;
+        ch.load(a, at.n, at.c);
+        back.load(a, at.n, at.c, [&](int g) {
+            const float2 s = reinterpret_cast<const float2 *>(a.sums)[at.n * a.G + g];
+            return make_float2(-s.x, -s.y);
+        });
+    };
     T *dx = at.at(a.dx);
     const T *const src[2] = {at.at(a.x), at.at(a.dy)};
     with_norm_act(a.act, [&](auto kind) {
-        each_vector<T, V, 2>(at, src, ring, [&](int k, const Word (&w)[2]) {
+        each_vector<T, V, 2>(at, src, ring, begin, [&](int k, const Word (&w)[2]) {
             F2 dev[PAIRS], dz[PAIRS];
             gradients<T, V, decltype(kind)::value>(ch, w[0], w[1], dev, dz);
 #pragma unroll
@@ -697,7 +709,7 @@ __device__ __forceinline__ float peer_read(const float *p, int rank) {
     uint32_t at;
     float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
     return v;
 }
 __device__ __forceinline__ void cluster_barrier() {
@@ -777,14 +789,20 @@ __global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ G
     for (int g = threadIdx.x; g < groups; g += THREADS) {
         float m = means[g], q = m2[g];
         if (a.chunks > 1) {
-            float total = 0.0f;
-            m = 0.0f, q = 0.0f;
-            for (int r = 0; r < a.chunks; ++r) total += peer_read(means + g, r) * (float)(min(a.P, (r + 1) * a.len) - min(a.P, r * a.len));
-            m = total / (float)a.P;
-            for (int r = 0; r < a.chunks; ++r) {
-                const float d = peer_read(means + g, r) - m;
-                q += fmaf(d * d, (float)(min(a.P, (r + 1) * a.len) - min(a.P, r * a.len)) * a.D, peer_read(m2 + g, r));
+            // (all on their way before the first is used)
+            float mr[MOST_SHARES], qr[MOST_SHARES], nr[MOST_SHARES], total = 0.0f;
+#pragma unroll
+            for (int r = 0; r < MOST_SHARES; ++r) {
+                mr[r] = r < a.chunks ? peer_read(means + g, r) : 0.0f;
+                qr[r] = r < a.chunks ? peer_read(m2 + g, r) : 0.0f;
+                nr[r] = (float)(min(a.P, (r + 1) * a.len) - min(a.P, r * a.len));
             }
+#pragma unroll
+            for (int r = 0; r < MOST_SHARES; ++r) total = fmaf(mr[r], nr[r], total);
+            m = total / (float)a.P;
+            q = 0.0f;
+#pragma unroll
+            for (int r = 0; r < MOST_SHARES; ++r) q += fmaf((mr[r] - m) * (mr[r] - m), nr[r] * a.D, qr[r]);
         }
         const float i = 1.0f / sqrtf(q / ((float)a.P * a.D) + a.eps);
         result[g] = m, result[groups + g] = i;
@@ -855,17 +873,25 @@ __global__ void __launch_bounds__(THREADS) gn_back_resident(const __grid_constan
     else __syncthreads();
     float *result = s.each;  // [2][groups]
     for (int g = threadIdx.x; g < groups; g += THREADS) {
-        float t[2] = {};
-        for (int r = 0; r < a.chunks; ++r)
+        float t[2] = {s.group[g], s.group[groups + g]};
+        if (a.chunks > 1) {
+            float part[2][MOST_SHARES];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) t[q] += a.chunks > 1 ? peer_read(s.group + q * groups + g, r) : s.group[q * groups + g];
+            for (int r = 0; r < MOST_SHARES; ++r)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) part[q][r] = r < a.chunks ? peer_read(s.group + q * groups + g, r) : 0.0f;
+            t[0] = t[1] = 0.0f;
+#pragma unroll
+            for (int r = 0; r < MOST_SHARES; ++r) t[0] += part[0][r], t[1] += part[1][r];
+        }
         const float total = (float)a.P * a.D;
         result[g] = -t[0] / total, result[groups + g] = -t[1] / total;
     }
     if (a.chunks > 1) cluster_barrier();
     else __syncthreads();
     const int g0 = at.c0 / a.D;
-    const Back<T, V> back(a, at.n, at.in ? at.c : at.c0, [&](int g) { return make_float2(result[g - g0], result[groups + g - g0]); });
+    Back<T, V> back;
+    back.load(a, at.n, at.in ? at.c : at.c0, [&](int g) { return make_float2(result[g - g0], result[groups + g - g0]); });
     with_norm_act(a.act, [&](auto kind) {
         at.each([&](int j, int64_t p) {
             F2 dev[PAIRS], dz[PAIRS];

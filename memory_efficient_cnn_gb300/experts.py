@@ -41,19 +41,19 @@ def _same(fn, x, *ts):
 
 # ---------------------------------------------------------------- router
 @functools.lru_cache(maxsize=4096)
-def _route_plan(shape, k):
-    """((T, E, k), the choices' shape) of logits' shape; ValueError where they do not fit."""
+def _route_plan(shape, k, over):
+    """(T, E, the code of over, the choices' shape) of logits' shape; ValueError where they do not fit."""
     if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("logits must be [..., E]")
     E = shape[-1]
     if not 1 <= k <= E:
         raise ValueError(f"k must be between 1 and {E}, the number of experts; got {k}")
-    return (math.prod(shape[:-1]), E, k), (*shape[:-1], k)
+    return math.prod(shape[:-1]), E, _code(ROUTES, over, "over"), (*shape[:-1], k)
 
 
-def _route_dims(fn, logits, k):
+def _route_dims(fn, logits, k, over):
     try:
-        return _route_plan(logits.shape, k)
+        return _route_plan(logits.shape, k, over)
     except ValueError as e:
         raise ValueError(f"{fn}: {e}") from None
 
@@ -62,34 +62,39 @@ def im2win_expert_route(logits, weights, experts, over: str = "top") -> None:
     """experts = the indexes of the k largest logits of each row, weights = their softmax weights."""
     fn = "im2win_expert_route"
     k = weights.shape[-1] if weights.dim() else 0
-    dims, shape = _route_dims(fn, logits, k)
+    T, E, code, shape = _route_dims(fn, logits, k, over)
     _shape(fn, "weights", weights, shape)
     _same(fn, logits, weights)
     _experts(fn, experts, logits, shape)
-    _route(fn, dims, logits, weights, experts, over)
-
-
-def _route(fn, dims, logits, weights, experts, over):
-    _check(fn, lib().im2win_expert_route(logits.data_ptr(), weights.data_ptr(), experts.data_ptr(), *dims,
-                                         _code(ROUTES, over, "over"), _dtype_code(logits), _stream(logits.get_device())))
-
-
-def _route_backward(fn, dims, dweights, logits, experts, dlogits, over):
-    _check(fn, lib().im2win_expert_route_backward(
-        dweights.data_ptr(), logits.data_ptr(), experts.data_ptr(), dlogits.data_ptr(), *dims, _code(ROUTES, over, "over"),
-        _dtype_code(logits), _stream(logits.get_device())))
+    _route(fn, T, E, k, code, logits, weights, experts)
 
 
 def im2win_expert_route_backward(dweights, logits, experts, dlogits, over: str = "top") -> None:
     """dlogits from dweights at the same logits and the experts chosen there."""
     fn = "im2win_expert_route_backward"
-    k = dweights.shape[-1] if dweights.dim() else 0
-    dims, shape = _route_dims(fn, logits, k)
-    _shape(fn, "dweights", dweights, shape)
     _shape(fn, "dlogits", dlogits, logits.shape)
-    _same(fn, logits, dweights, dlogits)
+    _same(fn, logits, dlogits)
+    _route_backward(fn, dweights, logits, experts, dlogits, over)
+
+
+def _route(fn, T, E, k, code, logits, weights, experts):
+    _check(fn, lib().im2win_expert_route(logits.data_ptr(), weights.data_ptr(), experts.data_ptr(), T, E, k, code,
+                                         _dtype_code(logits), _stream(logits.get_device())))
+
+
+def _route_backward(fn, dweights, logits, experts, dlogits, over):
+    k = dweights.shape[-1] if dweights.dim() else 0
+    T, E, code, shape = _route_dims(fn, logits, k, over)
+    if dweights.shape != shape:
+        _shape(fn, "dweights", dweights, shape)
+    _same(fn, logits, dweights)
     _experts(fn, experts, logits, shape)
-    _route_backward(fn, dims, dweights, logits, experts, dlogits, over)
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _check(fn, lib().im2win_expert_route_backward(
+        dweights.data_ptr(), logits.data_ptr(), experts.data_ptr(), dlogits.data_ptr(), T, E, k, code, _dtype_code(logits),
+        _stream(logits.get_device())))
+    return dlogits
 
 
 def expert_route(logits: torch.Tensor, k: int, over: str = "top"):
@@ -101,27 +106,18 @@ def expert_route(logits: torch.Tensor, k: int, over: str = "top"):
     fn = "expert_route"
     if logits.requires_grad:
         _unrecorded(fn, logits)
-    dims, shape = _route_dims(fn, logits, k)
-    if logits.get_device() < 0 or not logits.is_contiguous():
+    T, E, code, shape = _route_dims(fn, logits, k, over)
+    if not (logits.is_cuda and logits.is_contiguous()):
         _cuda(logits)
     weights = torch.empty(shape, dtype=logits.dtype, device=logits.device)
     experts = torch.empty_like(weights, dtype=torch.int32)
-    _route(fn, dims, logits, weights, experts, over)
+    _route(fn, T, E, k, code, logits, weights, experts)
     return weights, experts
 
 
 def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, over: str = "top"):
     """dlogits of expert_route() at the same logits and over, and the experts it chose."""
-    fn = "expert_route_backward"
-    k = dweights.shape[-1] if dweights.dim() else 0
-    dims, shape = _route_dims(fn, logits, k)
-    if dweights.shape != shape:
-        _shape(fn, "dweights", dweights, shape)
-    _same(fn, logits, dweights)
-    _experts(fn, experts, logits, shape)
-    dlogits = torch.empty_like(logits)
-    _route_backward(fn, dims, dweights, logits, experts, dlogits, over)
-    return dlogits
+    return _route_backward("expert_route_backward", dweights, logits, experts, None, over)
 
 
 # ---------------------------------------------------------------- feed-forward
