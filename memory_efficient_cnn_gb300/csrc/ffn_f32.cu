@@ -356,9 +356,15 @@ __global__ void __launch_bounds__(THREADS, 1) f32_product(const __grid_constant_
             const bool none = GROUPED && AK && m >= w.row_end;
             const float scale = !GROUPED ? 1.0f : EPI != EPI_STORE && p.scale && !none ? p.scale[m] : 0.0f;
             if (GROUPED ? p.part && !w.whole : p.part != nullptr) {
-                float *dst = GROUPED ? p.part + ((int64_t)(2 * blockIdx.x + w.slot) * ROWS + q * 32 + lane) * BN
+                float *dst = GROUPED ? p.part + (int64_t)(2 * blockIdx.x + w.slot) * ROWS * BN + part_index(q * 32 + lane, 0, BN)
                                      : p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
-                if (m < m_end) {
+                if (GROUPED && m < m_end) {
+#pragma unroll
+                    for (int i = 0; i < PAIRS / 2; ++i) {
+                        *reinterpret_cast<ulonglong2 *>(dst + (c0 + 4 * i) * 32) = words(sum[0] + 2 * i);
+                        *reinterpret_cast<ulonglong2 *>(dst + (c1 + 4 * i) * 32) = words(sum[1] + 2 * i);
+                    }
+                } else if (m < m_end) {
                     store_f32(dst + c0, sum[0], CHUNK);
                     store_f32(dst + c1, sum[1], CHUNK);
                 }
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(256) f32_group_join(const __grid_constant__ F3
     if (!group_join_source(GroupSpace<!AK>(p, table, ROWS), units, w, unit, last)) return;
     const int m_end = !AK ? p.M : EPI == EPI_STORE ? w.row_end : w.pad_end;
     for (int id = blockIdx.x % JOIN_SHARES * 256 + threadIdx.x; id < ROWS * COLS / 8; id += JOIN_SHARES * 256) {
-        const int row = id / (COLS / 8), col = id % (COLS / 8) * 8;
+        const int row = id % ROWS, col = id / ROWS * 8;
         const int m = w.tm * ROWS + row + (AK ? w.row0 : 0), n = w.tn * COLS + col;
         if (m >= m_end || n >= p.N) continue;
         F2 v[4], u[4];

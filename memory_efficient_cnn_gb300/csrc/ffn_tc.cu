@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
             };
             if (GROUPED ? p.part && !w.whole : p.part != nullptr) {
                 constexpr int PART_SPAN = BN / SHARES;
-                float *dst = GROUPED ? p.part + ((int64_t)(2 * unit + w.slot) * T::M + (int)rank * ROWS + q * 32 + lane) * BN
+                float *dst = GROUPED ? p.part + (int64_t)(2 * unit + w.slot) * T::M * BN + part_index((int)rank * ROWS + q * 32 + lane, 0, BN)
                                      : p.part + w.slot * p.part_step + ((int64_t)w.z * p.M + m) * p.part_ld + (int64_t)w.tn * BN;
 #pragma unroll 1
                 for (int c = share * PART_SPAN; c < (share + 1) * PART_SPAN; c += CHUNK) {
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_product(const __grid_constant__
                     if (m < m_end) {
 #pragma unroll
                         for (int i = 0; i < CHUNK / 4; ++i)
-                            reinterpret_cast<uint4 *>(dst + c)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                            reinterpret_cast<uint4 *>(GROUPED ? dst + c * 32 : dst + c)[GROUPED ? 32 * i : i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
                     }
                 }
             } else {
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(256) tc_group_join(const __grid_constant__ TcP
     if (!group_join_source(GroupSpace<!AK>(p, table, T::M), units, w, unit, last)) return;
     const int m_end = !AK ? p.M : EPI == EPI_STORE ? w.row_end : w.pad_end;
     for (int id = blockIdx.x % JOIN_SHARES * 256 + threadIdx.x; id < T::M * COLS / 8; id += JOIN_SHARES * 256) {
-        const int row = id / (COLS / 8), col = id % (COLS / 8) * 8;
+        const int row = id % T::M, col = id / T::M * 8;
         const int m = w.tm * T::M + row + (AK ? w.row0 : 0), n = w.tn * COLS + col;
         if (m >= m_end || n >= p.N) continue;
         F2 v[4], u[4];

@@ -328,7 +328,7 @@ struct GroupWalk {
 
 // ---- joining the partial tiles of a streamed grouped launch: JOIN_SHARES blocks for each border between
 // two units. The tile that a border cuts is joined at its first border. (A block for every 256 octets of
-// output columns took 13 us where these take 5.)
+// output columns took 13 us where these take 9.)
 constexpr int JOIN_SHARES = 8;
 inline int group_join_blocks(int units, bool summed) { return (units - 1) * JOIN_SHARES + (summed ? 64 : 0); }
 // The block's tile w and the units whose parts it adds: `unit`'s second buffer, then the first ones of those up
@@ -347,25 +347,28 @@ __device__ __forceinline__ bool group_join_source(const GroupSpace<SUMMED> &spac
     while (last + 1 < takers && stream_begin(total, takers, last + 1) < start + len) ++last;
     return true;
 }
+// Partial tiles lie in blocks of 32 rows by 4 columns, 16 bytes a row, so that the warp that writes 32 rows of one moves
+// 512 contiguous bytes, and the one that reads them.
+__device__ __forceinline__ int part_index(int row, int col, int bn) { return (row / 32 * (bn / 4) + col / 4) * 128 + row % 32 * 4; }
 // Their sums (TWO: of g and u, half a tile's columns apart).
 template <bool TWO>
 __device__ __forceinline__ void add_parts(const float *part, int tile_m, int bn, int row, int col, int unit, int last, F2 (&v)[4],
                                           F2 (&u)[4]) {
     const int64_t tile = (int64_t)tile_m * bn;
-    const float *from = part + (int64_t)row * bn + col;
+    const float *from = part + part_index(row, col, bn);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = u[i] = f2(0.0f);
     auto add = [](F2(&sum)[4], const float *p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float4 a = reinterpret_cast<const float4 *>(p)[i];
+            const float4 a = reinterpret_cast<const float4 *>(p)[32 * i];
             sum[2 * i] = add2(sum[2 * i], f2(a.x, a.y)), sum[2 * i + 1] = add2(sum[2 * i + 1], f2(a.z, a.w));
         }
     };
     for (int j = unit; j <= last; ++j) {
         const float *p = from + (2 * j + (j == unit ? 1 : 0)) * tile;
         add(v, p);
-        if (TWO) add(u, p + bn / 2);
+        if (TWO) add(u, p + bn / 8 * 128);
     }
 }
 // Zeros for the matrices of experts without rows, by the launch's last 64 blocks.
@@ -635,8 +638,7 @@ inline TcPlan plan_groups(const Product &d, int cg, int bn, double kb, double ep
     if (summed) {
         KT = d.rows / E / BK + 0.5;
         tiles = (double)z * E * pl.tiles_m * pl.tiles_n;
-        // (both operands' rows are read in pieces of 256 bytes, at 3 TB/s as measured)
-        read = KT * tiles * ((double)tm / pl.tiles_n + (double)bn / pl.tiles_m) * BK * 2 / 3e6;
+        read = KT * tiles * ((double)tm / pl.tiles_n + (double)bn / pl.tiles_m) * BK * 2 / 5e6;
         largest = 1.6 * KT;
         bound = (double)z * d.groups.E * pl.tiles_m * pl.tiles_n;
     } else {
@@ -651,11 +653,11 @@ inline TcPlan plan_groups(const Product &d, int cg, int bn, double kb, double ep
     const double waves = std::ceil(std::max(1.0, tiles / most));
     pl.cost = 4 + std::max(read, largest * kb + epi + (waves - 1) * std::max(KT * kb, epi));
     // Work counts stay in 32 bits. With more tiles streaming does not pay: whole tiles next to one another find
-    // their operands in L2 (16384 rows by 2048 columns: 683 us streamed, 420 us plain; 64 tiles of 49 blocks on 76
-    // pairs: 49 us and 40 us; 45 tiles of 32 blocks on 152 CTAs in fp32: 30 us and 45 us).
-    if (bound * (KT + 1) * 4 > 1e9 || 2 * tiles > most) return pl;
+    // their operands in L2 (16384 rows by 2048 columns: 683 us streamed, 420 us plain; 45 tiles of 32 blocks on 152
+    // CTAs in fp32: 30 us and 45 us).
+    if (bound * (KT + 1) * 4 > 1e9 || tiles > most) return pl;
     const double part = (double)most * tm * bn * 4, blocks = tiles * KT;
-    const double cost = 4 + std::max(std::max(read, std::max(4.0, blocks / most) * kb), tiles / most * epi) + epi + 4 + 3 * part / 10e6;
+    const double cost = 4 + std::max(std::max(read, std::max(4.0, blocks / most) * kb), tiles / most * epi) + epi + 4 + 1.5 * part / 10e6;
     if (cost >= pl.cost) return pl;
     pl.streamed = true;
     pl.cost = cost;

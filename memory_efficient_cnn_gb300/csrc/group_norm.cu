@@ -24,18 +24,21 @@ bool known_act(int act) {
 GroupArgs make(int64_t N, int64_t P, int64_t C, int64_t G, int act, int dtype, int maps) {
     GroupArgs a = {};
     a.N = N, a.P = P, a.C = (int)C, a.G = (int)G, a.D = (int)(C / G), a.act = act;
+    if (cut_rows(a, elem_size(dtype))) return a;
     if (!cut_resident(a, elem_size(dtype), maps)) cut(a, elem_size(dtype), maps);
+    a.part_rows = N * a.chunks;
     return a;
 }
 
 // The workspace: partial sums, and the groups' sums (backward) or their statistics (forward, where the
-// caller keeps none). A forward call whose maps stay on the chip needs none.
+// caller keeps none). A forward call that reads its maps once needs none.
 struct Parts {
     size_t part, sums, bytes;
     Parts(const GroupArgs &a, bool backward) {
         part = 0;
-        sums = a.resident && !backward ? 0 : round_up((size_t)(2 * a.N * a.chunks) * a.C * 4, 256);
-        bytes = sums + (a.resident ? 0 : round_up((size_t)(a.N * a.G) * 8, 256));
+        const bool once = a.resident || a.lanes;  // read once, in one launch
+        sums = once && !backward ? 0 : round_up((size_t)(2 * a.part_rows) * a.C * 4, 256);
+        bytes = sums + (once ? 0 : round_up((size_t)(a.N * a.G) * 8, 256));
     }
 };
 
@@ -43,7 +46,7 @@ void place(GroupArgs &a, const Parts &parts, void *ws, void *stats) {
     unsigned char *base = static_cast<unsigned char *>(ws);
     a.part = reinterpret_cast<float *>(base + parts.part);
     a.sums = reinterpret_cast<float *>(base + parts.sums);
-    a.stats = static_cast<float *>(stats || a.resident ? stats : base + parts.sums);
+    a.stats = static_cast<float *>(stats || a.resident || a.lanes ? stats : base + parts.sums);
 }
 
 }  // namespace

@@ -26,6 +26,8 @@ struct GroupArgs {
     // resident: a cluster of `chunks` CTAs keeps the `slab` channels of an image on the chip
     bool resident;
     int slab, tile, smem;  // bytes: the tiles, and all
+    int64_t part_rows;     // rows of the partial sums
+    int lanes;             // one position an image: lanes of a group (0: not so), `cols` of them a block and row
 };
 
 constexpr int THREADS = 256;
@@ -78,6 +80,24 @@ inline bool cut_resident(GroupArgs &a, int size, int maps) {
     return false;
 }
 
+// One position an image: a row's group belongs to up to 32 lanes with up to four vectors each. False where it is longer
+// than that, or there are more positions.
+inline bool cut_rows(GroupArgs &a, int size) {
+    if (a.P != 1) return false;
+    const int vecs = a.D / vector_of(a.D, size);
+    int lanes = 1;
+    while (lanes < 32 && lanes < vecs) lanes *= 2;
+    if (vecs > 4 * lanes) return false;
+    const int64_t slots = (int64_t)a.G * lanes;
+    a.lanes = lanes;
+    a.cols = (int)std::min<int64_t>(slots, THREADS);
+    a.slabs = (int)((slots + a.cols - 1) / a.cols);
+    a.rows = THREADS / a.cols;
+    a.chunks = (int)std::max<int64_t>(1, std::min<int64_t>((a.N + a.rows - 1) / a.rows, 152 * 6 / a.slabs));
+    a.part_rows = a.chunks;
+    return true;
+}
+
 // Fills in the cut: as few chunks of positions as fill whole rounds of the blocks that the SMs hold at a time (four
 // forward, three backward) to 93%, or else the best of up to four rounds. 64 images of 56 x 56 in 9 chunks are one
 // round forward, where 14 left half of the second one empty.
@@ -88,9 +108,11 @@ inline void cut(GroupArgs &a, int size, int maps) {
     a.rows = THREADS / a.cols;
     const int64_t longest = std::max<int64_t>(1, (a.P + (int64_t)a.rows * FEW - 1) / ((int64_t)a.rows * FEW));
     const int64_t round = 152 * (maps == 1 ? 4 : 3), one = std::max<int64_t>(1, a.N * a.slabs);
-    int64_t chunks = 1;
+    // (up to the first round they only fill it further)
+    const int64_t first = std::max<int64_t>(1, std::min(longest, round * 93 / 100 / one));
+    int64_t chunks = first;
     double best = 0;
-    for (int64_t c = 1; c <= longest && (c - 1) * one < 4 * round; ++c) {
+    for (int64_t c = first; c <= longest && (c - 1) * one < 4 * round; ++c) {
         const int64_t blocks = c * one, rounds = (blocks + round - 1) / round;
         const double full = (double)blocks / (double)(rounds * round);
         if (full > best) best = full, chunks = c;

@@ -307,7 +307,7 @@ struct Back {
 // A thread's channels' two sums, row `row` of the partial ones.
 template <int V, int PAIRS>
 __device__ __forceinline__ void store_channels(const GroupArgs &a, int64_t row, int c, const F2 (&v)[PAIRS], const F2 (&u)[PAIRS]) {
-    float *m = a.part + row * a.C + c, *q = m + a.N * a.chunks * a.C;
+    float *m = a.part + row * a.C + c, *q = m + a.part_rows * a.C;
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
         float lo, hi, lo2, hi2;
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(THREADS) gn_stats(const __grid_constant__ Grou
     tc::grid_dependency_wait();
     const int64_t id = (int64_t)blockIdx.x * (THREADS / SPAN) + threadIdx.x / SPAN;
     if (id >= a.N * a.G) return;
-    const int64_t n = id / a.G, half = a.N * a.chunks * a.C;
+    const int64_t n = id / a.G, half = a.part_rows * a.C;
     const int c0 = (int)(id % a.G) * a.D, items = a.D * a.chunks;
     const float *m = a.part + n * a.chunks * a.C + c0;
     // chunk k holds count(k) positions
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(THREADS) gn_back_means(const __grid_constant__
     tc::grid_dependency_wait();
     const int64_t id = (int64_t)blockIdx.x * (THREADS / SPAN) + threadIdx.x / SPAN;
     if (id >= a.N * a.G) return;
-    const int64_t n = id / a.G, half = a.N * a.chunks * a.C;
+    const int64_t n = id / a.G, half = a.part_rows * a.C;
     const int c0 = (int)(id % a.G) * a.D, items = a.D * a.chunks;
     const float *m = a.part + n * a.chunks * a.C + c0;
     float s0 = 0.0f, s1 = 0.0f;
@@ -552,7 +552,7 @@ template <typename T>
 __device__ void sum_params(const GroupArgs &a, int block) {
     __shared__ float red[2][8][33];
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = block * 32 + lane;
-    const int64_t rows = a.N * a.chunks, half = rows * a.C;
+    const int64_t rows = a.part_rows, half = rows * a.C;
     float s0 = 0.0f, s1 = 0.0f;
     if (c < a.C) {
 #pragma unroll 8
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(THREADS) gn_back_resident(const __grid_constan
     sum_groups<T, V, 2>(a, at, s, sum, [&](int c) { return a.w ? to_f32(static_cast<const T *>(a.w)[at.c0 + c]) : 1.0f; });
     const int groups = at.sc / a.D, wide = max(THREADS, at.sc);
     if (a.dw || a.db) {
-        const int64_t row = (at.n * a.chunks + at.rank) * a.C + at.c0, half = a.N * a.chunks * a.C;
+        const int64_t row = (at.n * a.chunks + at.rank) * a.C + at.c0, half = a.part_rows * a.C;
         for (int c = threadIdx.x; c < at.sc; c += THREADS) {
             float t[2] = {};
             for (int seg = 0; seg < s.segments; ++seg) t[0] += s.channel[seg * at.sc + c], t[1] += s.channel[wide + seg * at.sc + c];
@@ -903,6 +903,170 @@ __global__ void __launch_bounds__(THREADS) gn_back_resident(const __grid_constan
     });
 }
 
+// ---- one position an image: a group is D neighbouring elements of a row, in the registers of a.lanes lanes
+
+// A thread's group and vectors: the m-th one begins at element d(m) of the group where it is there.
+template <typename T, int V, int M>
+struct RowSeat {
+    using Word = typename Group<T, V>::Word;
+    int row, lane, g, vecs, lanes;
+    int64_t n, step;
+    bool in;
+    __device__ explicit RowSeat(const GroupArgs &a) {
+        const int slab = blockIdx.x % a.slabs, slot = threadIdx.x % a.cols + slab * a.cols;
+        row = threadIdx.x / a.cols;
+        lanes = a.lanes, lane = slot % lanes, g = slot / lanes, vecs = a.D / V;
+        in = row < a.rows && g < a.G;
+        n = (int64_t)(blockIdx.x / a.slabs) * a.rows + row;
+        step = (int64_t)a.chunks * a.rows;
+    }
+    __device__ bool has(int m) const { return lane + m * lanes < vecs; }
+    __device__ int channel(const GroupArgs &a, int m) const { return g * a.D + (lane + m * lanes) * V; }
+    __device__ float sum(float v) const {
+        for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+};
+// The sum of a pair's elements (V = 1: there is one).
+template <int V>
+__device__ __forceinline__ float pair_sum(F2 v) {
+    float lo, hi;
+    split(v, lo, hi);
+    return V > 1 ? lo + hi : lo;
+}
+// Parameters of a vector's channels.
+template <typename T, int V>
+__device__ __forceinline__ void params_of(const void *p, int c, float absent, F2 (&v)[Group<T, V>::PAIRS]) {
+    if (p) {
+        to_pairs<T, V>(*reinterpret_cast<const typename Group<T, V>::Word *>(static_cast<const T *>(p) + c), v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Group<T, V>::PAIRS; ++i) v[i] = f2(absent);
+    }
+}
+
+template <typename T, int V, int M>
+__global__ void __launch_bounds__(THREADS) gn_rows(const __grid_constant__ GroupArgs a) {
+    constexpr int PAIRS = Group<T, V>::PAIRS;
+    using Word = typename Group<T, V>::Word;
+    const RowSeat<T, V, M> at(a);
+    tc::grid_dependency_wait();
+    tc::allow_dependents();
+    const float share = 1.0f / (float)a.D;
+    with_norm_act(a.act, [&](auto kind) {
+        for (int64_t n = at.n; n - at.row < a.N; n += at.step) {  // (as often for every row of the block: lanes exchange)
+            const bool there = at.in && n < a.N;
+            F2 v[M][PAIRS];
+            float s = 0.0f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) v[m][i] = f2(0.0f);
+                if (there && at.has(m)) to_pairs<T, V>(*reinterpret_cast<const Word *>(static_cast<const T *>(a.x) + n * a.C + at.channel(a, m)), v[m]);
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) s += pair_sum<V>(v[m][i]);
+            }
+            const float mean = at.sum(s) * share;
+            s = 0.0f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                if (!at.has(m)) continue;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    v[m][i] = add2(v[m][i], f2(-mean));
+                    s += pair_sum<V>(mul2(v[m][i], v[m][i]));
+                }
+            }
+            const float inv = 1.0f / sqrtf(at.sum(s) * share + a.eps);
+            if (!there) continue;
+            if (a.stats && at.lane == 0) reinterpret_cast<float2 *>(a.stats)[n * a.G + at.g] = make_float2(mean, inv);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                if (!at.has(m)) continue;
+                const int c = at.channel(a, m);
+                F2 w[PAIRS], b[PAIRS];
+                params_of<T, V>(a.w, c, 1.0f, w);
+                params_of<T, V>(a.b, c, 0.0f, b);
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i)
+                    v[m][i] = act_of<T, decltype(kind)::value>(fma2(v[m][i], mul2(w[i], f2(inv)), b[i]));
+                *reinterpret_cast<Word *>(static_cast<T *>(a.y) + n * a.C + c) = from_pairs<T, V>(v[m]);
+            }
+        }
+    });
+}
+
+template <typename T, int V, int M>
+__global__ void __launch_bounds__(THREADS) gn_back_rows(const __grid_constant__ GroupArgs a) {
+    constexpr int PAIRS = Group<T, V>::PAIRS;
+    using Word = typename Group<T, V>::Word;
+    __shared__ F2 red[2 * PAIRS][THREADS];
+    const RowSeat<T, V, M> at(a);
+    tc::grid_dependency_wait();
+    tc::allow_dependents();
+    const float share = 1.0f / (float)a.D;
+    F2 s0[M][PAIRS], s1[M][PAIRS];  // of the thread's channels over its rows: dz, dz hat
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) s0[m][i] = s1[m][i] = f2(0.0f);
+    with_norm_act(a.act, [&](auto kind) {
+        for (int64_t n = at.n; n - at.row < a.N; n += at.step) {
+            const bool there = at.in && n < a.N;
+            float2 st = make_float2(0.0f, 0.0f);
+            if (there) st = reinterpret_cast<const float2 *>(a.stats)[n * a.G + at.g];
+            F2 hat[M][PAIRS], e[M][PAIRS];  // e: w dz
+            float t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                if (!there || !at.has(m)) continue;
+                const int c = at.channel(a, m);
+                F2 w[PAIRS], b[PAIRS];
+                params_of<T, V>(a.w, c, 1.0f, w);
+                params_of<T, V>(a.b, c, 0.0f, b);
+                to_pairs<T, V>(*reinterpret_cast<const Word *>(static_cast<const T *>(a.x) + n * a.C + c), hat[m]);
+                to_pairs<T, V>(*reinterpret_cast<const Word *>(static_cast<const T *>(a.dy) + n * a.C + c), e[m]);
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    hat[m][i] = mul2(add2(hat[m][i], f2(-st.x)), f2(st.y));
+                    const F2 dz = mul2(e[m][i], slope_of<T, decltype(kind)::value>(fma2(hat[m][i], w[i], b[i])));
+                    s0[m][i] = add2(s0[m][i], dz);
+                    s1[m][i] = fma2(dz, hat[m][i], s1[m][i]);
+                    e[m][i] = mul2(dz, w[i]);
+                    t0 += pair_sum<V>(e[m][i]);
+                    t1 += pair_sum<V>(mul2(e[m][i], hat[m][i]));
+                }
+            }
+            if (!a.dx) continue;  // (of every thread alike)
+            const F2 m1 = f2(-at.sum(t0) * share), m2 = f2(-at.sum(t1) * share);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                if (!there || !at.has(m)) continue;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) e[m][i] = mul2(fma2(hat[m][i], m2, add2(e[m][i], m1)), f2(st.y));
+                *reinterpret_cast<Word *>(static_cast<T *>(a.dx) + n * a.C + at.channel(a, m)) = from_pairs<T, V>(e[m]);
+            }
+        }
+    });
+    if (!a.dw && !a.db) return;
+    // over the block's rows, one after the other
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) red[2 * i][threadIdx.x] = s0[m][i], red[2 * i + 1][threadIdx.x] = s1[m][i];
+        __syncthreads();
+        if (at.row > 0 || !at.in || !at.has(m)) continue;
+        for (int r = 1; r < a.rows; ++r)
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                s0[m][i] = add2(s0[m][i], red[2 * i][threadIdx.x + r * a.cols]);
+                s1[m][i] = add2(s1[m][i], red[2 * i + 1][threadIdx.x + r * a.cols]);
+            }
+        store_channels<V>(a, blockIdx.x / a.slabs, at.channel(a, m), s0[m], s1[m]);
+    }
+}
+
 template <typename K, typename... A>
 cudaError_t launch_with(K kernel, int64_t blocks, cudaStream_t st, int smem, int cluster, const A &...args) {
     cudaLaunchConfig_t cfg = {};
@@ -939,10 +1103,22 @@ cudaError_t with_vector(const GroupArgs &a, Fn f) {
     }
 }
 
+// Calls f with the vector of a group's elements and a thread's number of them.
+template <typename T, typename Fn>
+cudaError_t with_row_vectors(const GroupArgs &a, Fn f) {
+    const int v = vector_of(a.D, sizeof(T)), m = (a.D / v + a.lanes - 1) / a.lanes;
+    auto go = [&](auto vec) { return m == 1 ? f(vec, IntC<1>()) : m == 2 ? f(vec, IntC<2>()) : f(vec, IntC<4>()); };
+    return v == 1 ? go(IntC<1>()) : v == 2 ? go(IntC<2>()) : go(IntC<16 / (int)sizeof(T)>());
+}
+
 }  // namespace
 
 template <typename T>
 cudaError_t launch_forward(const GroupArgs &a, cudaStream_t st) {
+    if (a.lanes)
+        return with_row_vectors<T>(a, [&](auto v, auto m) {
+            return launch(gn_rows<T, decltype(v)::value, decltype(m)::value>, a.slabs * a.chunks, st, a);
+        });
     const int64_t blocks = a.N * a.slabs * a.chunks;
     return with_vector<T>(a, [&](auto v) {
         constexpr int V = decltype(v)::value;
@@ -958,6 +1134,13 @@ cudaError_t launch_forward(const GroupArgs &a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_backward(const GroupArgs &a, cudaStream_t st) {
+    if (a.lanes) {
+        cudaError_t e = with_row_vectors<T>(a, [&](auto v, auto m) {
+            return launch(gn_back_rows<T, decltype(v)::value, decltype(m)::value>, a.slabs * a.chunks, st, a);
+        });
+        if (e == cudaSuccess && (a.dw || a.db)) e = launch(gn_back_params<T>, (a.C + 31) / 32, st, a);
+        return e;
+    }
     const int64_t blocks = a.N * a.slabs * a.chunks;
     return with_vector<T>(a, [&](auto v) {
         constexpr int V = decltype(v)::value;

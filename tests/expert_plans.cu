@@ -26,10 +26,16 @@ int group_product_units(int f32, int summed, int M, int N, int K, int E, int64_t
 
 int64_t expert_grouped_rows(int64_t pairs, int64_t E) { return im2win::ffn::grouped_rows(pairs, E); }
 
-// The group norm's cut: out = resident, chunks, positions a chunk, channels a slab, bytes of the tiles, of all shared memory, vector.
+// The group norm's cut: out = resident, chunks, positions a chunk, channels a slab, bytes of the tiles, of all shared memory,
+// vector, slabs; or, for one position an image, 2, blocks of rows, rows and lanes of a block, lanes of a group, 0, vector, slabs.
 void group_norm_cut(int64_t N, int64_t P, int C, int G, int size, int maps, int64_t *out) {
     im2win::gnorm::GroupArgs a = {};
     a.N = N, a.P = P, a.C = C, a.G = G, a.D = C / G;
+    if (im2win::gnorm::cut_rows(a, size)) {
+        const int64_t r[] = {2, a.chunks, a.rows, a.cols, a.lanes, 0, im2win::gnorm::vector_of(a.D, size), a.slabs};
+        for (int i = 0; i < 8; ++i) out[i] = r[i];
+        return;
+    }
     if (!im2win::gnorm::cut_resident(a, size, maps)) im2win::gnorm::cut(a, size, maps);
     const int v = im2win::gnorm::vector_of(C, size);
     const int64_t r[] = {a.resident, a.chunks, a.len, a.resident ? a.slab : a.cols * v, a.tile, a.smem, v, a.slabs};

@@ -60,6 +60,14 @@ def test_large(N, P, C, G, dt):
 
 
 @pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("N,C,G", [(1, 1, 1), (3, 8, 8), (1000, 64, 8), (77, 96, 4), (5000, 30, 6), (300, 512, 2), (64, 1024, 1),
+                                   (40, 4096, 4), (33, 4100, 2), (9, 2049, 3), (2100, 2048, 32), (20, 510, 1), (7, 12288, 3)])
+def test_one_position(dt, N, C, G):
+    """Groups of single rows, of one element to more than the lanes of a warp hold."""
+    check(N, 1, C, G, dt, "gelu", seed=N + C)
+
+
+@pytest.mark.parametrize("dt", DT)
 def test_without_parameters(dt):
     check(2, 50, 40, 5, dt, affine=False)
     x, w, b, dy = dev(*make(2, 50, 40, dt))
@@ -86,7 +94,7 @@ def test_far_mean(P):
     block_ref.check(dict(y=mec.group_norm(x.cuda(), 4)), want)
 
 
-@pytest.mark.parametrize("P", [9, 4000])
+@pytest.mark.parametrize("P", [1, 9, 4000])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_spoiled_values_stay_in_their_group(P, bad):
     x, w, b, dy = dev(*make(3, P, 24, "bf16"))
