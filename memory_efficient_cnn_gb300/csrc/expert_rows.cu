@@ -4,7 +4,7 @@
 // Nothing here depends on the order of blocks: a pair's place is the number of its expert's
 // pairs before it, and sums run over a row's choices in their order. The plan of 25088 pairs takes 7 us, of 1554
 // 5 us (one block: a chain of barriers and dependent loads); gathering and summing run at the memory's rate (16384
-// pairs of 2048 channels: 27 us, 42 us with the products dy . ys, 27 us).
+// pairs of 2048 channels: 19 us, 38 us with the products dy . ys, 27 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(PLACE_THREADS) expert_place(const int32_t *exp
     for (int e = threadIdx.x; e < E; e += PLACE_THREADS) {
         int32_t before = 0, sum = 0;  // the expert's pairs in the blocks before, and in all
         if (hist) {
+#pragma unroll 8
             for (int i = 0; i < (int)gridDim.x; ++i) {
                 const int32_t v = hist[(int64_t)i * E + e];
                 before += i < b ? v : 0;
@@ -170,20 +171,28 @@ __device__ __forceinline__ int64_t pair_of(const Rows &r, int64_t row) {
     return q < 0 || q >= r.T * r.k ? -1 : q;
 }
 
-// A warp for 256 columns of a row.
-template <typename T, bool V>
+// A warp for 256 * GATHER columns of a row: looking up where the row comes from takes longer than copying 256, but
+// registers for 1024 of which most are not there cost more (2048 columns: 24 us and 31 us; 256: 15 us and 12 us).
+template <typename T, bool V, int GATHER>
 __global__ void __launch_bounds__(THREADS) expert_gather(const __grid_constant__ Rows r, const T *x, const T *weights,
                                                          void *grouped, float *scale, int parts) {
     tc::allow_dependents();
     tc::grid_dependency_wait();
     const int64_t id = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5), row = id / parts;
-    const int c = ((int)(id - row * parts) * 32 + (threadIdx.x & 31)) * 8;
+    const int c0 = ((int)(id - row * parts) * GATHER * 32 + (threadIdx.x & 31)) * 8;
     const int64_t q = pair_of(r, row);
-    if (q < -1 || c >= r.Cp) return;
-    if (scale && c == 0) scale[row] = q >= 0 ? to_f32(weights[q]) : 0.0f;
-    float v[8] = {};
-    if (q >= 0) load8<T, V>(x + q / r.k * r.C + c, r.C - c, v);
-    store_operand<T>(grouped, r, row, c, v);
+    if (q < -1) return;
+    if (scale && c0 == 0) scale[row] = q >= 0 ? to_f32(weights[q]) : 0.0f;
+    const T *from = x + (q >= 0 ? q / r.k * r.C : 0);
+    float v[GATHER][8] = {};
+#pragma unroll
+    for (int i = 0; i < GATHER; ++i) {
+        const int c = c0 + i * 256;
+        if (q >= 0 && c < r.Cp) load8<T, V>(from + c, r.C - c, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < GATHER; ++i)
+        if (c0 + i * 256 < r.Cp) store_operand<T>(grouped, r, row, c0 + i * 256, v[i]);
 }
 
 // A warp a row.
@@ -291,11 +300,12 @@ cudaError_t launch_plan(const Rows &r, const int32_t *experts, int32_t *hist, ui
 
 cudaError_t launch_gather(const Rows &r, const void *x, const void *weights, void *grouped, float *scale, int dtype,
                           cudaStream_t st) {
-    const int parts = (int)((r.Cp + 255) / 256);
+    const int columns = r.Cp <= 512 ? 256 : 1024, parts = (int)((r.Cp + columns - 1) / columns);
     return with_rows(dtype, r.C, [&](auto *t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
-        return launch(expert_gather<T, decltype(v)::value>, (r.rows * parts + WARPS - 1) / WARPS, st, r, static_cast<const T *>(x),
-                      static_cast<const T *>(weights), grouped, scale, parts);
+        constexpr bool V = decltype(v)::value;
+        return launch(columns == 256 ? expert_gather<T, V, 1> : expert_gather<T, V, 4>, (r.rows * parts + WARPS - 1) / WARPS, st, r,
+                      static_cast<const T *>(x), static_cast<const T *>(weights), grouped, scale, parts);
     });
 }
 
