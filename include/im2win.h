@@ -531,14 +531,17 @@ im2win_status im2win_expert_ffn_size(int buffer, int64_t T, int64_t k, int64_t E
  * x[T][C], experts[T][k] (int32, on the device), weights[T][k] (dtype), w_gate[E][F][C],
  * w_up[E][F][C], w_down[E][C][F], y[T][C]. A place whose expert is outside [0, E) takes no part
  * (a position dropped where its expert is full), whatever its weight; a row with none left gets
- * zeros; a row may name an expert twice. Only the experts that rows name are read.
+ * zeros; a row may name an expert twice. Nothing of an expert that no row names reaches a
+ * result; its matrices are read only to copy all of them (F32, or C or F no multiple of 8, but
+ * for few pairs, below).
  * The products are those of im2win_gated_ffn, with its roundings (h, and in the backward pass
- * dg, du and weights h); ffn_e(x[t]) is weighted and summed in fp32. Calls without `saved` of
+ * dg, du and weights * h); ffn_e(x[t]) is weighted and summed in fp32. Calls without `saved` of
  * few pairs (T k up to 64 in F32 and where C or F is no multiple of 8; else up to 8, or 32 where
  * min(E, T k) C F is at most 2^25) keep the remainder of h's rounding too: the same row's y may
- * differ by that rounding from a call of more rows, or from training. What F32 says of infinities
- * holds here from 65 pairs on, and in training. y must not overlap an input. `saved` (NULL for inference; FFN_SAVED) receives what the
- * backward call needs; its contents are opaque. ws begins with the status block.
+ * differ by that rounding from a call of more rows, or from training. What im2win_gated_ffn says of
+ * infinities in F32 holds here from 65 pairs on, and in training.
+ * y must not overlap an input. `saved` (NULL for inference; FFN_SAVED) receives what the backward
+ * call needs; its contents are opaque. ws begins with the status block.
  */
 im2win_status im2win_expert_ffn(const void *x, const int32_t *experts, const void *weights, const void *w_gate,
                                 const void *w_up, const void *w_down, void *y, void *saved, void *ws, size_t ws_bytes,
