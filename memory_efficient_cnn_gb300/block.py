@@ -28,6 +28,14 @@ def _code(table, name, what):
         raise ValueError(f"{what} must be one of {', '.join(table)}; got {name!r}") from None
 
 
+def _count(fn, what, n) -> int:
+    """A whole number as an int: True is 1, numpy's integers are taken, 8.0 is refused."""
+    try:
+        return int(operator.index(n))
+    except TypeError:
+        raise TypeError(f"{fn}: {what} must be a whole number, got {n!r}") from None
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 

@@ -15,8 +15,8 @@ import torch
 
 from ._binding import _check, _cuda, _dtype_code, _same_device, lib
 from .block import (
-    ACTS, FFN_BACKWARD, FFN_FORWARD, FFN_SAVED, FFN_TRAIN, _alike, _bytes, _code, _ptr, _same_dtype, _shape, _stream,
-    _unrecorded)
+    ACTS, FFN_BACKWARD, FFN_FORWARD, FFN_SAVED, FFN_TRAIN, _alike, _bytes, _code, _count, _ptr, _same_dtype, _shape,
+    _stream, _unrecorded)
 
 ROUTES = {"top": 0, "all": 1}
 
@@ -40,7 +40,8 @@ def _same(fn, x, *ts):
 
 
 # ---------------------------------------------------------------- router
-@functools.lru_cache(maxsize=4096)
+# (2.0 hashes as 2, and an answer holds what it was asked with: callers pass ints alone)
+@functools.lru_cache(maxsize=4096, typed=True)
 def _route_plan(shape, k, over):
     """(T, E, the code of over, the choices' shape) of logits' shape; ValueError where they do not fit."""
     if len(shape) < 1 or shape[-1] < 1:
@@ -52,6 +53,8 @@ def _route_plan(shape, k, over):
 
 
 def _route_dims(fn, logits, k, over):
+    if type(k) is not int:
+        k = _count(fn, "k", k)
     try:
         return _route_plan(logits.shape, k, over)
     except ValueError as e:

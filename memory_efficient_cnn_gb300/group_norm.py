@@ -13,7 +13,7 @@ import math
 import torch
 
 from ._binding import _check, _cuda, _dtype_code, _same_device, lib
-from .block import ACTS, _bytes, _code, _ptr, _same_dtype, _shape, _stream, _unrecorded
+from .block import ACTS, _bytes, _code, _count, _ptr, _same_dtype, _shape, _stream, _unrecorded
 
 NORM_ACTS = {**ACTS, "none": 5}
 
@@ -26,7 +26,8 @@ def im2win_group_norm_size(backward: bool, N, P, C, G, dtype: int) -> int:
 
 
 # Shapes are looked up, not worked out again: a small call costs less on the GPU than on the host.
-@functools.lru_cache(maxsize=4096)
+# (8.0 and True hash as 8 and 1, and an answer holds what it was asked with: callers pass ints alone)
+@functools.lru_cache(maxsize=4096, typed=True)
 def _plan(shape, groups):
     """((N, P, C, G), (C,)) of x's shape; ValueError where x or the groups do not fit."""
     if len(shape) < 2 or shape[-1] < 1:
@@ -40,6 +41,8 @@ def _plan(shape, groups):
 def _dims(fn, x, groups, params, maps):
     """(N, P, C, G) after the checks of a call's tensors; maps are (name, tensor or
     None) of x's shape, params those of its channels."""
+    if type(groups) is not int:
+        groups = _count(fn, "groups", groups)
     try:
         dims, channels = _plan(x.shape, groups)
     except ValueError as e:
@@ -121,7 +124,7 @@ def _normed(fn, x, groups, w, b, act, eps, ws, out, train):
     _unrecorded(fn, x, w, b)
     dims = _dims(fn, x, groups, (("w", w), ("b", b)), (("out", out),))
     y = torch.empty_like(x) if out is None else out
-    stats = torch.empty((dims[0], groups, 2), dtype=torch.float32, device=x.device) if train else None
+    stats = torch.empty((dims[0], dims[3], 2), dtype=torch.float32, device=x.device) if train else None
     _forward(fn, dims, x, w, b, y, stats, ws, act, eps)
     return y, stats
 
