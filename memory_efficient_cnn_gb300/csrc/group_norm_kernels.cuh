@@ -415,7 +415,10 @@ __device__ __forceinline__ float span_sum(float v, float *s) {
     return t;
 }
 
-// A group's chunks and channels become its mean and inverse deviation; SPAN threads a group.
+// A group's chunks and channels become its mean and inverse deviation; SPAN threads a group. Twice over them: the
+// deviations are those from the group's own mean, and their sum is what the first pass's rounding left of it. (From a
+// pivot, sum of squares less square of the sum: a first chunk a hundred deviations away took 2e-3 of the variance
+// of 36000 items.)
 template <int SPAN>
 __global__ void __launch_bounds__(THREADS) gn_stats(const __grid_constant__ GroupArgs a) {
     __shared__ float s[THREADS / 32];
@@ -426,24 +429,52 @@ __global__ void __launch_bounds__(THREADS) gn_stats(const __grid_constant__ Grou
     const int64_t n = id / a.G, half = a.part_rows * a.C;
     const int c0 = (int)(id % a.G) * a.D, items = a.D * a.chunks;
     const float *m = a.part + n * a.chunks * a.C + c0;
-    // chunk k holds count(k) positions
-    auto count = [&](int k) { return (float)(min(a.P, (k + 1) * a.len) - k * a.len); };
-    // deviations of the chunks' means from the first one
-    const float pivot = m[0];
-    float sum = 0.0f, sq = 0.0f;
-#pragma unroll 4
-    for (int i = threadIdx.x % SPAN; i < items; i += SPAN) {
+    const float total = (float)a.P * a.D, share = 1.0f / total;
+    // an item's place, and its number of positions
+    auto item = [&](int i, int64_t &at) {
         const int k = i / a.D;
-        const int64_t at = (int64_t)k * a.C + i - k * a.D;
-        const float d = m[at] - pivot, nd = d * count(k);
-        sum += nd;
-        sq += fmaf(nd, d, m[half + at]);
+        at = (int64_t)k * a.C + i - k * a.D;
+        return (float)(min(a.P, (k + 1) * a.len) - k * a.len);
+    };
+    // a thread's first items stay in registers (all of a warp's groups)
+    constexpr int KEEP = 8;
+    const int t = threadIdx.x % SPAN;
+    float means[KEEP], squares[KEEP], counts[KEEP];
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+        means[j] = squares[j] = counts[j] = 0.0f;
+        if (t + j * SPAN >= items) continue;
+        int64_t at;
+        counts[j] = item(t + j * SPAN, at);
+        means[j] = m[at], squares[j] = m[half + at];
     }
-    const float total = (float)a.P * a.D;
+    float mean = 0.0f, sum = 0.0f, sq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) mean = fmaf(means[j], counts[j] * share, mean);
+#pragma unroll 4
+    for (int i = t + KEEP * SPAN; i < items; i += SPAN) {
+        int64_t at;
+        const float count = item(i, at);
+        mean = fmaf(m[at], count * share, mean);
+    }
+    mean = span_sum<SPAN>(mean, s);
+    auto add = [&](float d, float count, float square) {
+        sum = fmaf(d, count, sum);
+        sq += fmaf(d * count, d, square);
+    };
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j)
+        if (t + j * SPAN < items) add(means[j] - mean, counts[j], squares[j]);
+#pragma unroll 4
+    for (int i = t + KEEP * SPAN; i < items; i += SPAN) {
+        int64_t at;
+        const float count = item(i, at);
+        add(m[at] - mean, count, m[half + at]);
+    }
     sum = span_sum<SPAN>(sum, s);
-    sq = span_sum<SPAN>(sq, s) - sum / total * sum;
+    sq = span_sum<SPAN>(sq, s) - sum * share * sum;
     if (threadIdx.x % SPAN == 0)
-        reinterpret_cast<float2 *>(a.stats)[id] = make_float2(pivot + sum / total, 1.0f / sqrtf((sq < 0.0f ? 0.0f : sq) / total + a.eps));
+        reinterpret_cast<float2 *>(a.stats)[id] = make_float2(mean + sum * share, 1.0f / sqrtf((sq < 0.0f ? 0.0f : sq) * share + a.eps));
 }
 
 template <typename T, int V>
