@@ -786,24 +786,24 @@ __global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ G
     };
     wait_fetched();
     const int groups = at.sc / a.D;
-    F2 sum[1][PAIRS], mean[PAIRS], inv[PAIRS];
+    F2 total[1][PAIRS], sum[2][PAIRS], mean[PAIRS], inv[PAIRS];
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) sum[0][i] = f2(0.0f);
+    for (int i = 0; i < PAIRS; ++i) total[0][i] = sum[0][i] = sum[1][i] = f2(0.0f);
     at.each([&](int j, int64_t) {
         F2 v[PAIRS];
         to_pairs<T, V>(tile[j], v);
 #pragma unroll
-        for (int i = 0; i < PAIRS; ++i) sum[0][i] = add2(sum[0][i], v[i]);
+        for (int i = 0; i < PAIRS; ++i) total[0][i] = add2(total[0][i], v[i]);
     });
-    sum_groups<T, V, 1>(a, at, s, sum, [](int) { return 1.0f; });
-    // the CTA's own mean, and the squared deviations from it
+    sum_groups<T, V, 1>(a, at, s, total, [](int) { return 1.0f; });
+    // the CTA's own mean, the squared deviations from it, and their sum: what the first sum's rounding left of the mean
+    // (of values around 4000 deviations that was 1e-3 of one)
     float *means = s.group + groups, *m2 = s.group;
-    const float count = (float)(at.p1 - at.p0) * a.D;
-    for (int g = threadIdx.x; g < groups; g += THREADS) means[g] = count > 0.0f ? s.group[g] / count : 0.0f;
+    const float count = (float)(at.p1 - at.p0) * a.D, part = count > 0.0f ? 1.0f / count : 0.0f;
+    float own = 0.0f;  // of group threadIdx.x (a slab has 64 at most)
+    if (threadIdx.x < groups) means[threadIdx.x] = own = s.group[threadIdx.x] * part;
     __syncthreads();
     of_groups(means, mean);
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) sum[0][i] = f2(0.0f);
     at.each([&](int j, int64_t) {
         F2 v[PAIRS];
         to_pairs<T, V>(tile[j], v);
@@ -811,9 +811,15 @@ __global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ G
         for (int i = 0; i < PAIRS; ++i) {
             const F2 d = add2(v[i], neg2(mean[i]));
             sum[0][i] = fma2(d, d, sum[0][i]);
+            sum[1][i] = add2(sum[1][i], d);
         }
     });
-    sum_groups<T, V, 1>(a, at, s, sum, [](int) { return 1.0f; });
+    sum_groups<T, V, 2>(a, at, s, sum, [](int) { return 1.0f; });
+    if (threadIdx.x < groups) {
+        const float left = means[threadIdx.x], q = m2[threadIdx.x] - left * part * left;
+        means[threadIdx.x] = own + left * part;
+        m2[threadIdx.x] = q < 0.0f ? 0.0f : q;
+    }
     // the cluster's; results go where no other CTA reads
     if (a.chunks > 1) cluster_barrier();
     float *result = s.channel;  // [2][groups]
@@ -821,6 +827,7 @@ __global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ G
         float m = means[g], q = m2[g];
         if (a.chunks > 1) {
             // (all on their way before the first is used)
+            // (the first CTA has positions wherever there are any)
             float mr[MOST_SHARES], qr[MOST_SHARES], nr[MOST_SHARES], total = 0.0f;
 #pragma unroll
             for (int r = 0; r < MOST_SHARES; ++r) {
@@ -829,11 +836,11 @@ __global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ G
                 nr[r] = (float)(min(a.P, (r + 1) * a.len) - min(a.P, r * a.len));
             }
 #pragma unroll
-            for (int r = 0; r < MOST_SHARES; ++r) total = fmaf(mr[r], nr[r], total);
-            m = total / (float)a.P;
+            for (int r = 0; r < MOST_SHARES; ++r) total = nr[r] > 0.0f ? fmaf(mr[r] - mr[0], nr[r], total) : total;
+            m = mr[0] + total / (float)a.P;
             q = 0.0f;
 #pragma unroll
-            for (int r = 0; r < MOST_SHARES; ++r) q += fmaf((mr[r] - m) * (mr[r] - m), nr[r] * a.D, qr[r]);
+            for (int r = 0; r < MOST_SHARES; ++r) q += nr[r] > 0.0f ? fmaf((mr[r] - m) * (mr[r] - m), nr[r] * a.D, qr[r]) : 0.0f;
         }
         const float i = 1.0f / sqrtf(q / ((float)a.P * a.D) + a.eps);
         result[g] = m, result[groups + g] = i;
@@ -1009,24 +1016,36 @@ __global__ void __launch_bounds__(THREADS) gn_rows(const __grid_constant__ Group
 #pragma unroll
             for (int m = 0; m < M; ++m) word[m] = next[m];
             if (AHEAD) fetch_row(a, at, a.x, n + at.step, next);
+            // fp32: the sum of distances to the group's first value, so that a far mean costs its own rounding alone
+            // (and the first one of at most 1024 is 32 deviations from it at most). 16-bit values of a mean so far
+            // hold fewer digits than it costs, and 3% of the time.
             F2 v[M][PAIRS];
-            float s = 0.0f;
+            float s = 0.0f, pivot = 0.0f;
 #pragma unroll
             for (int m = 0; m < M; ++m) {
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) v[m][i] = f2(0.0f);
                 if (there && at.has(m)) to_pairs<T, V>(word[m], v[m]);
+                if (sizeof(T) == 4 && m == 0) {
+                    float unused;
+                    split(v[0][0], pivot, unused);
+                    pivot = __shfl_sync(0xffffffffu, pivot, threadIdx.x & 31 & ~(at.lanes - 1));
+                }
+                if (sizeof(T) == 4 && !at.has(m)) continue;
 #pragma unroll
-                for (int i = 0; i < PAIRS; ++i) s += pair_sum<V>(v[m][i]);
+                for (int i = 0; i < PAIRS; ++i) {
+                    if (sizeof(T) == 4) v[m][i] = add2(v[m][i], f2(-pivot));
+                    s += pair_sum<V>(v[m][i]);
+                }
             }
-            const float mean = at.sum(s) * share;
+            const float off = at.sum(s) * share, mean = pivot + off;
             s = 0.0f;
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 if (!at.has(m)) continue;
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) {
-                    v[m][i] = add2(v[m][i], f2(-mean));
+                    v[m][i] = add2(v[m][i], f2(-off));
                     s += pair_sum<V>(mul2(v[m][i], v[m][i]));
                 }
             }

@@ -11,7 +11,7 @@ from block_ref import E, EXTRA, TINY, U, acc
 from expert_ref import act_of
 
 
-def group_norm(x, G, w, b, act, eps, dtype, dy=None, run=256, run_params=512):
+def group_norm(x, G, w, b, act, eps, dtype, dy=None, run=256, run_params=512, roundings=2):
     """{output: (value, bound)} of x [N, P, C] in float64, also of the statistics that the forward call keeps."""
     un, tiny = U[dtype], TINY[dtype]
     N, P, C = x.shape
@@ -22,8 +22,8 @@ def group_norm(x, G, w, b, act, eps, dtype, dy=None, run=256, run_params=512):
     dev = v - mean
     var = (dev * dev).mean((1, 3), keepdim=True)
     inv = 1 / torch.sqrt(var + eps)
-    # the means of parts, each rounded and then averaged, and the result's own rounding
-    em = ks * dev.abs().mean((1, 3), keepdim=True) + 2 * E * mean.abs()
+    # the means of parts, each rounded and then averaged, and the result's own rounding; 1: there is one part
+    em = ks * dev.abs().mean((1, 3), keepdim=True) + roundings * E * mean.abs()
     ed = em + 2 * E * dev.abs()
     ei = ks / 2 + 8 * E + (em * inv) ** 2
     hat = dev * inv
