@@ -27,18 +27,20 @@ GroupArgs make(int64_t N, int64_t P, int64_t C, int64_t G, int act, int dtype, i
     if (cut_rows(a, elem_size(dtype))) return a;
     if (!cut_resident(a, elem_size(dtype), maps)) cut(a, elem_size(dtype), maps);
     a.part_rows = N * a.chunks;
+    a.folds = folds_of(a.part_rows);
     return a;
 }
 
 // The workspace: partial sums, and the groups' sums (backward) or their statistics (forward, where the
-// caller keeps none). A forward call that reads its maps once needs none.
+// caller keeps none); backward, runs of the partial sums. A forward call that reads its maps once needs none.
 struct Parts {
-    size_t part, sums, bytes;
+    size_t part, sums, folded, bytes;
     Parts(const GroupArgs &a, bool backward) {
         part = 0;
         const bool once = a.resident || a.lanes;  // read once, in one launch
         sums = once && !backward ? 0 : round_up((size_t)(2 * a.part_rows) * a.C * 4, 256);
-        bytes = sums + (once ? 0 : round_up((size_t)(a.N * a.G) * 8, 256));
+        folded = sums + (once ? 0 : round_up((size_t)(a.N * a.G) * 8, 256));
+        bytes = folded + (backward ? round_up((size_t)2 * a.folds * a.C * 4, 256) : 0);
     }
 };
 
@@ -46,6 +48,7 @@ void place(GroupArgs &a, const Parts &parts, void *ws, void *stats) {
     unsigned char *base = static_cast<unsigned char *>(ws);
     a.part = reinterpret_cast<float *>(base + parts.part);
     a.sums = reinterpret_cast<float *>(base + parts.sums);
+    a.folded = reinterpret_cast<float *>(base + parts.folded);
     a.stats = static_cast<float *>(stats || a.resident || a.lanes ? stats : base + parts.sums);
 }
 

@@ -578,31 +578,47 @@ __global__ void __launch_bounds__(THREADS) gn_back_means(const __grid_constant__
     if (threadIdx.x % SPAN == 0) reinterpret_cast<float2 *>(a.sums)[id] = make_float2(s0 / total, s1 / total);
 }
 
-// dw and db: the channels' sums over images and chunks; 32 channels by 8 runs of rows a block.
-template <typename T>
-__device__ void sum_params(const GroupArgs &a, int block) {
+// The sums of rows `begin` to `end` of both halves of `part` (each of `rows` rows), for 32 channels: put(half, channel, sum).
+template <typename Fn>
+__device__ __forceinline__ void sum_rows(const GroupArgs &a, const float *part, int64_t rows, int64_t begin, int64_t end, int block, Fn put) {
     __shared__ float red[2][8][33];
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = block * 32 + lane;
-    const int64_t rows = a.part_rows, half = rows * a.C;
+    const int64_t half = rows * a.C;
     float s0 = 0.0f, s1 = 0.0f;
     if (c < a.C) {
 #pragma unroll 8
-        for (int64_t r = run; r < rows; r += 8) s0 += a.part[r * a.C + c], s1 += a.part[half + r * a.C + c];
+        for (int64_t r = begin + run; r < end; r += 8) s0 += part[r * a.C + c], s1 += part[half + r * a.C + c];
     }
     red[0][run][lane] = s0, red[1][run][lane] = s1;
     __syncthreads();
     if (run >= 2 || c >= a.C) return;
-    T *out = static_cast<T *>(run ? a.dw : a.db);
     float t = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) t += red[run][i][lane];
-    if (out) out[c] = from_f32<T>(t);
+    put(run, c, t);
+}
+// dw and db: the channels' sums over images and chunks, or over the runs of those.
+template <typename T>
+__device__ __forceinline__ void sum_params(const GroupArgs &a, int block) {
+    const int64_t rows = a.folds ? a.folds : a.part_rows;
+    sum_rows(a, a.folds ? a.folded : a.part, rows, 0, rows, block, [&](int half, int c, float sum) {
+        T *out = static_cast<T *>(half ? a.dw : a.db);
+        if (out) out[c] = from_f32<T>(sum);
+    });
 }
 template <typename T>
 __global__ void __launch_bounds__(THREADS) gn_back_params(const __grid_constant__ GroupArgs a) {
     tc::allow_dependents();
     tc::grid_dependency_wait();
     sum_params<T>(a, blockIdx.x);
+}
+// The partial sums in a.folds runs of rows, a block for a run's 32 channels.
+__global__ void __launch_bounds__(THREADS) gn_back_fold(const __grid_constant__ GroupArgs a) {
+    tc::allow_dependents();
+    tc::grid_dependency_wait();
+    const int64_t f = blockIdx.x % a.folds, per = (a.part_rows + a.folds - 1) / a.folds;
+    sum_rows(a, a.part, a.part_rows, f * per, min(a.part_rows, (f + 1) * per), blockIdx.x / a.folds,
+             [&](int half, int c, float sum) { a.folded[(half * (int64_t)a.folds + f) * a.C + c] = sum; });
 }
 
 // dx; the first `param_blocks` blocks make dw and db meanwhile.
@@ -1219,12 +1235,16 @@ cudaError_t launch_forward(const GroupArgs &a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_backward(const GroupArgs &a, cudaStream_t st) {
+    const int params = a.dw || a.db ? (a.C + 31) / 32 : 0;
+    auto sum = [&](cudaError_t e) {
+        if (e == cudaSuccess && params && a.folds) e = launch(gn_back_fold, (int64_t)params * a.folds, st, a);
+        return e == cudaSuccess && params ? launch(gn_back_params<T>, params, st, a) : e;
+    };
     if (a.lanes) {
         cudaError_t e = with_row_vectors<T>(a, [&](auto v, auto m) {
             return launch(gn_back_rows<T, decltype(v)::value, decltype(m)::value>, a.slabs * a.chunks, st, a);
         });
-        if (e == cudaSuccess && (a.dw || a.db)) e = launch(gn_back_params<T>, (a.C + 31) / 32, st, a);
-        return e;
+        return sum(e);
     }
     const int64_t blocks = a.N * a.slabs * a.chunks;
     return with_vector<T>(a, [&](auto v) {
@@ -1235,11 +1255,12 @@ cudaError_t launch_backward(const GroupArgs &a, cudaStream_t st) {
         if (a.dx && !a.resident) {
             if (e == cudaSuccess)
                 e = by_block(a) ? launch(gn_back_means<T, THREADS>, group_blocks(a), st, a) : launch(gn_back_means<T, 32>, group_blocks(a), st, a);
-            const int params = a.dw || a.db ? (a.C + 31) / 32 : 0;
-            return e == cudaSuccess ? launch_with(gn_back_apply<T, V>, blocks + params, st, 0, 1, a, params) : e;
+            // dw and db beside dx, unless they are summed in runs first
+            const int beside = a.folds ? 0 : params;
+            if (e == cudaSuccess) e = launch_with(gn_back_apply<T, V>, blocks + beside, st, 0, 1, a, beside);
+            return beside ? e : sum(e);
         }
-        if (e == cudaSuccess && (a.dw || a.db)) e = launch(gn_back_params<T>, (a.C + 31) / 32, st, a);
-        return e;
+        return sum(e);
     });
 }
 
