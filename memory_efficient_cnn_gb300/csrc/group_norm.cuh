@@ -128,7 +128,7 @@ inline void cut(GroupArgs &a, int size, int maps) {
 // Runs that the rows of partial sums of dw and db are summed in first. Up to 2048 rows a block of 32 channels adds up
 // itself, 256 in a row; images of few positions can make millions, and then neither a run nor its block has more than
 // about the square root of them (32768 x 4 x 32 in 16 bits: backward 1278 us without runs, 682 us with them; a million
-// images of 2 x 8: 9e-4 and 2e-6 off in a sum of equal terms).
+// images of 2 x 8: 9e-4 and 1.4e-7 off in a sum of equal terms).
 inline int folds_of(int64_t rows) { return rows <= 2048 ? 0 : (int)std::ceil(std::sqrt((double)rows)); }
 
 template <typename T>

@@ -400,12 +400,12 @@ __global__ void __launch_bounds__(THREADS, 4) gn_moments(const __grid_constant__
     if (at.in && at.row == 0) store_channels<V>(a, at.n * a.chunks + at.chunk, at.c, mean, m2);
 }
 
-// Sum over SPAN threads (a warp, or the block), the same for each and in a fixed order.
+// Sum over SPAN threads (part of a warp, a warp, or the block), the same for each and in a fixed order.
 template <int SPAN>
 __device__ __forceinline__ float span_sum(float v, float *s) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (SPAN == 32) return v;
+    for (int o = (SPAN < 32 ? SPAN : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (SPAN <= 32) return v;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
     float t = 0.0f;
@@ -424,8 +424,8 @@ __global__ void __launch_bounds__(THREADS) gn_stats(const __grid_constant__ Grou
     __shared__ float s[THREADS / 32];
     tc::allow_dependents();
     tc::grid_dependency_wait();
-    const int64_t id = (int64_t)blockIdx.x * (THREADS / SPAN) + threadIdx.x / SPAN;
-    if (id >= a.N * a.G) return;
+    const int64_t wanted = (int64_t)blockIdx.x * (THREADS / SPAN) + threadIdx.x / SPAN;
+    const int64_t id = min(wanted, a.N * a.G - 1);  // (every lane takes part in the exchanges)
     const int64_t n = id / a.G, half = a.part_rows * a.C;
     const int c0 = (int)(id % a.G) * a.D, items = a.D * a.chunks;
     const float *m = a.part + n * a.chunks * a.C + c0;
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(THREADS) gn_stats(const __grid_constant__ Grou
         at = (int64_t)k * a.C + i - k * a.D;
         return (float)(min(a.P, (k + 1) * a.len) - k * a.len);
     };
-    // a thread's first items stay in registers (all of a warp's groups)
+    // a thread's first items stay in registers (all of a group, but for a block's)
     constexpr int KEEP = 8;
     const int t = threadIdx.x % SPAN;
     float means[KEEP], squares[KEEP], counts[KEEP];
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(THREADS) gn_stats(const __grid_constant__ Grou
     }
     sum = span_sum<SPAN>(sum, s);
     sq = span_sum<SPAN>(sq, s) - sum * share * sum;
-    if (threadIdx.x % SPAN == 0)
+    if (t == 0 && wanted == id)
         reinterpret_cast<float2 *>(a.stats)[id] = make_float2(mean + sum * share, 1.0f / sqrtf((sq < 0.0f ? 0.0f : sq) * share + a.eps));
 }
 
@@ -770,8 +770,9 @@ __device__ __forceinline__ Sums scratch(const GroupArgs &a, int sc, unsigned cha
     return {p, p + SUMS * THREADS * V, p + SUMS * (THREADS * V + max(THREADS, sc)), 0};
 }
 
+// (four CTAs an SM of fewer elements, three of eight: small images are as fast as many fit)
 template <typename T, int V>
-__global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ GroupArgs a) {
+__global__ void __launch_bounds__(THREADS, V == 8 ? 3 : 4) gn_resident(const __grid_constant__ GroupArgs a) {
     constexpr int PAIRS = Group<T, V>::PAIRS;
     using Word = typename Group<T, V>::Word;
     extern __shared__ uint4 dyn[];
@@ -802,9 +803,10 @@ __global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ G
     };
     wait_fetched();
     const int groups = at.sc / a.D;
-    F2 total[1][PAIRS], sum[2][PAIRS], mean[PAIRS], inv[PAIRS];
+    constexpr int SUMS = sizeof(T) == 4 ? 2 : 1;
+    F2 total[1][PAIRS], sum[SUMS][PAIRS], mean[PAIRS], inv[PAIRS];
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) total[0][i] = sum[0][i] = sum[1][i] = f2(0.0f);
+    for (int i = 0; i < PAIRS; ++i) total[0][i] = sum[0][i] = sum[SUMS - 1][i] = f2(0.0f);
     at.each([&](int j, int64_t) {
         F2 v[PAIRS];
         to_pairs<T, V>(tile[j], v);
@@ -812,8 +814,9 @@ __global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ G
         for (int i = 0; i < PAIRS; ++i) total[0][i] = add2(total[0][i], v[i]);
     });
     sum_groups<T, V, 1>(a, at, s, total, [](int) { return 1.0f; });
-    // the CTA's own mean, the squared deviations from it, and their sum: what the first sum's rounding left of the mean
-    // (of values around 4000 deviations that was 1e-3 of one)
+    // the CTA's own mean and the squared deviations from it; fp32, also their sum: what the first sum's rounding left of the
+    // mean. (16-bit values of a mean so far away that this counts hold fewer digits themselves, and it takes
+    // 32768 images of 4 x 32 from 410 to 590 us.)
     float *means = s.group + groups, *m2 = s.group;
     const float count = (float)(at.p1 - at.p0) * a.D, part = count > 0.0f ? 1.0f / count : 0.0f;
     float own = 0.0f;  // of group threadIdx.x (a slab has 64 at most)
@@ -827,11 +830,11 @@ __global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ G
         for (int i = 0; i < PAIRS; ++i) {
             const F2 d = add2(v[i], neg2(mean[i]));
             sum[0][i] = fma2(d, d, sum[0][i]);
-            sum[1][i] = add2(sum[1][i], d);
+            if (SUMS == 2) sum[SUMS - 1][i] = add2(sum[SUMS - 1][i], d);
         }
     });
-    sum_groups<T, V, 2>(a, at, s, sum, [](int) { return 1.0f; });
-    if (threadIdx.x < groups) {
+    sum_groups<T, V, SUMS>(a, at, s, sum, [](int) { return 1.0f; });
+    if (SUMS == 2 && threadIdx.x < groups) {
         const float left = means[threadIdx.x], q = m2[threadIdx.x] - left * part * left;
         means[threadIdx.x] = own + left * part;
         m2[threadIdx.x] = q < 0.0f ? 0.0f : q;
@@ -852,11 +855,11 @@ __global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ G
                 nr[r] = (float)(min(a.P, (r + 1) * a.len) - min(a.P, r * a.len));
             }
 #pragma unroll
-            for (int r = 0; r < MOST_SHARES; ++r) total = nr[r] > 0.0f ? fmaf(mr[r] - mr[0], nr[r], total) : total;
+            for (int r = 0; r < MOST_SHARES; ++r) total = fmaf(mr[r] - mr[0], nr[r], total);
             m = mr[0] + total / (float)a.P;
             q = 0.0f;
 #pragma unroll
-            for (int r = 0; r < MOST_SHARES; ++r) q += nr[r] > 0.0f ? fmaf((mr[r] - m) * (mr[r] - m), nr[r] * a.D, qr[r]) : 0.0f;
+            for (int r = 0; r < MOST_SHARES; ++r) q += fmaf((mr[r] - m) * (mr[r] - m), nr[r] * a.D, qr[r]);
         }
         const float i = 1.0f / sqrtf(q / ((float)a.P * a.D) + a.eps);
         result[g] = m, result[groups + g] = i;
@@ -1228,7 +1231,11 @@ cudaError_t launch_forward(const GroupArgs &a, cudaStream_t st) {
             return e == cudaSuccess ? launch(gn_resident<T, V>, blocks, st, a, a.smem, a.chunks) : e;
         }
         cudaError_t e = launch(gn_moments<T, V>, blocks, st, a);
-        if (e == cudaSuccess) e = by_block(a) ? launch(gn_stats<THREADS>, group_blocks(a), st, a) : launch(gn_stats<32>, group_blocks(a), st, a);
+        // (eight lanes for 64 items: 200704 images of 4 x 64 in eight groups take 1880 us, 2350 us with 32)
+        if (e == cudaSuccess)
+            e = by_block(a)                 ? launch(gn_stats<THREADS>, a.N * a.G, st, a)
+                : a.D * a.chunks > 64       ? launch(gn_stats<32>, (a.N * a.G + 7) / 8, st, a)
+                                            : launch(gn_stats<8>, (a.N * a.G + 31) / 32, st, a);
         return e == cudaSuccess ? launch(gn_apply<T, V>, blocks, st, a) : e;
     });
 }
@@ -1236,10 +1243,7 @@ cudaError_t launch_forward(const GroupArgs &a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_backward(const GroupArgs &a, cudaStream_t st) {
     const int params = a.dw || a.db ? (a.C + 31) / 32 : 0;
-    auto sum = [&](cudaError_t e) {
-        if (e == cudaSuccess && params && a.folds) e = launch(gn_back_fold, (int64_t)params * a.folds, st, a);
-        return e == cudaSuccess && params ? launch(gn_back_params<T>, params, st, a) : e;
-    };
+    auto sum = [&](cudaError_t e) { return e == cudaSuccess && params ? launch(gn_back_params<T>, params, st, a) : e; };
     if (a.lanes) {
         cudaError_t e = with_row_vectors<T>(a, [&](auto v, auto m) {
             return launch(gn_back_rows<T, decltype(v)::value, decltype(m)::value>, a.slabs * a.chunks, st, a);
@@ -1252,11 +1256,12 @@ cudaError_t launch_backward(const GroupArgs &a, cudaStream_t st) {
         cudaError_t e = a.resident ? allow_smem<gn_back_resident<T, V>>(MAX_SMEM) : cudaSuccess;
         if (e == cudaSuccess)
             e = a.resident ? launch(gn_back_resident<T, V>, blocks, st, a, a.smem, a.chunks) : launch(gn_back_sums<T, V>, blocks, st, a);
+        if (e == cudaSuccess && params && a.folds) e = launch(gn_back_fold, (int64_t)params * a.folds, st, a);
         if (a.dx && !a.resident) {
             if (e == cudaSuccess)
                 e = by_block(a) ? launch(gn_back_means<T, THREADS>, group_blocks(a), st, a) : launch(gn_back_means<T, 32>, group_blocks(a), st, a);
-            // dw and db beside dx, unless they are summed in runs first
-            const int beside = a.folds ? 0 : params;
+            // dw and db beside dx, if the grid holds both
+            const int beside = blocks + params <= 0x7fffffff ? params : 0;
             if (e == cudaSuccess) e = launch_with(gn_back_apply<T, V>, blocks + beside, st, 0, 1, a, beside);
             return beside ? e : sum(e);
         }
