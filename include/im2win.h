@@ -464,7 +464,8 @@ im2win_status im2win_clip_grad_norm(const void *const *grads, void *const *outs,
  * output is rounded once. N * P * C is at most 2^40, C at most 2^20, N * C at most
  * 2^31, C a multiple of G (else IM2WIN_ERR_INVALID_ARG).
  * stats[N][G][2] (fp32; NULL: not kept) receives each group's mean and 1/sqrt(var +
- * eps) for the backward call. y may be x itself and must not overlap it otherwise.
+ * eps) for the backward call. Pointers are 16-byte aligned; the stats that a backward call
+ * reads need 8 bytes (those of some images of a batch). y may be x itself and must not overlap it otherwise.
  * A NaN or infinity spoils its own image's group and no other. im2win_group_norm_size gives
  * the workspace of a forward (backward = 0) or backward call, host arithmetic only; it may be
  * zero, and ws then NULL.

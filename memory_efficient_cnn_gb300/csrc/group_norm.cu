@@ -90,8 +90,9 @@ im2win_status im2win_group_norm_backward(const void *dy, const void *x, const vo
     if (s != IM2WIN_OK) return s;
     if (!known_act(act) || (dw && !w) || (db && !b)) return IM2WIN_ERR_INVALID_ARG;
     if (N * P > 0 && (!dy || !x || !stats)) return IM2WIN_ERR_INVALID_ARG;
-    for (const void *p : {dy, x, stats, w, b, (const void *)dx, (const void *)dw, (const void *)db, (const void *)ws})
+    for (const void *p : {dy, x, w, b, (const void *)dx, (const void *)dw, (const void *)db, (const void *)ws})
         if (!aligned_to(p, 16)) return IM2WIN_ERR_MISALIGNED;
+    if (!aligned_to(stats, 8)) return IM2WIN_ERR_MISALIGNED;  // (read in pairs: some images' part of a batch's)
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (N * P == 0) {  // sums over nothing
         cudaError_t e = cudaSuccess;

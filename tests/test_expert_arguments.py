@@ -1,5 +1,6 @@
-"""Counts that callers pass to the group norm and the router: what is no whole number is refused, and a
-refused call leaves the next right one of the same shape as it was. On the host; nothing is launched."""
+"""Arguments of the group norm and the router that are no plain ones: counts that are no whole numbers are refused, and a
+refused call leaves the next right one of the same shape as it was; statistics of a part of a batch. On the host;
+nothing is launched."""
 import importlib
 
 import numpy as np
@@ -7,7 +8,8 @@ import pytest
 import torch
 
 import memory_efficient_cnn_gb300 as mec
-from memory_efficient_cnn_gb300 import experts
+from memory_efficient_cnn_gb300 import build as mbuild, experts
+from memory_efficient_cnn_gb300._binding import ERR_MISALIGNED, ERR_WORKSPACE
 
 norm = importlib.import_module("memory_efficient_cnn_gb300.group_norm")  # (the name is the function's in the package)
 
@@ -52,3 +54,13 @@ def test_answers_by_shape_do_not_mix_types():
     assert all_ints(norm._plan(torch.Size([3, 7, 32]), 4)[0])
     experts._route_plan(torch.Size([3, 9]), 3.0, "all")
     assert all_ints(experts._route_plan(torch.Size([3, 9]), 3, "all"))
+
+
+def test_statistics_of_a_part_of_a_batch_may_begin_on_8_bytes():
+    mbuild.build()
+
+    def call(stats, ws=None):
+        return mec.lib().im2win_group_norm_backward(4096, 4096, stats, 4096, 4096, 8192, 8192, 8192, ws, 0, 2, 9, 8, 2, 0, mec.F32, None)
+
+    assert call(4104) == call(4096) == ERR_WORKSPACE  # (what is looked at next)
+    assert call(4100) == call(4097) == ERR_MISALIGNED
