@@ -520,7 +520,7 @@ im2win_status im2win_expert_route_backward(const void *dweights, const void *log
                                            void *stream);
 
 /* Bytes of a buffer of the experts' feed-forward (host arithmetic only). T may be 0; E at most
- * 1024, k at most 32 (it may pass E); T k + 64 E, E C and E F below 2^31 - 1024, and E C F and
+ * 1024, k at most 32 (it may pass E); T k + 64 E, E C and E F up to 2^31 - 1024, and E C F and
  * (T k + 64 E) times C or F at most 2^40 (else IM2WIN_ERR_UNSUPPORTED). */
 im2win_status im2win_expert_ffn_size(int buffer, int64_t T, int64_t k, int64_t E, int64_t C, int64_t F, int dtype,
                                      size_t *bytes);

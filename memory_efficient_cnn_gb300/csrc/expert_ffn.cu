@@ -28,7 +28,7 @@ namespace {
 im2win_status check_dims(int64_t T, int64_t k, int64_t E, int64_t C, int64_t F, int dtype) {
     if (T < 0 || k < 1 || E < 1 || C < 1 || F < 1 || elem_size(dtype) == 0) return IM2WIN_ERR_INVALID_ARG;
     const int64_t most = 0x7fffffff - 1023, area = int64_t(1) << 40;
-    if (k > MAX_CHOICES || E > MAX_EXPERTS || T > most / k - 64 * E || C > most / E || F > most / E || C > area / F / E)
+    if (k > MAX_CHOICES || E > MAX_EXPERTS || T > (most - 64 * E) / k || C > most / E || F > most / E || C > area / F / E)
         return IM2WIN_ERR_UNSUPPORTED;
     const int64_t rows = grouped_rows(T * k, E);
     return rows > area / C || rows > area / F ? IM2WIN_ERR_UNSUPPORTED : IM2WIN_OK;
