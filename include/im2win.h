@@ -513,7 +513,11 @@ im2win_status im2win_expert_route(const void *logits, void *weights, int32_t *ex
 
 /*
  * dlogits[T][E] from dweights[T][k] at the same logits and the experts chosen there (the
- * choice itself has no gradient). Places whose expert is outside [0, E) take no part.
+ * choice itself has no gradient). Places whose expert is outside [0, E) take no part: over TOP, the
+ * softmax is formed again over the others. A caller who drops places after the routing (an expert that
+ * is full) gives the list that the router made here, not the shortened one: the weights of the places
+ * that are left were made with the dropped ones beside them. dweights is zero at a dropped place, as
+ * im2win_expert_ffn_backward with the shortened list gives it.
  */
 im2win_status im2win_expert_route_backward(const void *dweights, const void *logits, const int32_t *experts,
                                            void *dlogits, int64_t T, int64_t E, int64_t k, int over, int dtype,

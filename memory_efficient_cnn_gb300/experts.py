@@ -119,7 +119,9 @@ def expert_route(logits: torch.Tensor, k: int, over: str = "top"):
 
 
 def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, over: str = "top"):
-    """dlogits of expert_route() at the same logits and over, and the experts it chose."""
+    """dlogits of expert_route() at the same logits and over, and the experts it chose: its own list, also where
+    places were dropped (-1) from a copy of it before expert_ffn(), whose dweights are zero there. A list with
+    -1 in place of a chosen expert would make the other places' softmax over "top" another one."""
     return _route_backward("expert_route_backward", dweights, logits, experts, None, over)
 
 
