@@ -415,6 +415,19 @@ __device__ __forceinline__ float span_sum(float v, float *s) {
     return t;
 }
 
+// The sums of two values at once.
+template <int SPAN>
+__device__ __forceinline__ float2 span_sums(float2 v, float2 *s) {
+    v = make_float2(span_sum<SPAN < 32 ? SPAN : 32>(v.x, nullptr), span_sum<SPAN < 32 ? SPAN : 32>(v.y, nullptr));
+    if (SPAN <= 32) return v;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < SPAN / 32; ++i) v.x += s[i].x, v.y += s[i].y;
+    return v;
+}
+
 // A group's chunks and channels become its mean and inverse deviation; SPAN threads a group. Twice over them: the
 // deviations are those from the group's own mean, and their sum is what the first pass's rounding left of it. (From a
 // pivot, sum of squares less square of the sum: a first chunk a hundred deviations away took 2e-3 of the variance
@@ -422,6 +435,7 @@ __device__ __forceinline__ float span_sum(float v, float *s) {
 template <int SPAN>
 __global__ void __launch_bounds__(THREADS) gn_stats(const __grid_constant__ GroupArgs a) {
     __shared__ float s[THREADS / 32];
+    __shared__ float2 s2[THREADS / 32];
     tc::allow_dependents();
     tc::grid_dependency_wait();
     const int64_t wanted = (int64_t)blockIdx.x * (THREADS / SPAN) + threadIdx.x / SPAN;
@@ -471,8 +485,8 @@ __global__ void __launch_bounds__(THREADS) gn_stats(const __grid_constant__ Grou
         const float count = item(i, at);
         add(m[at] - mean, count, m[half + at]);
     }
-    sum = span_sum<SPAN>(sum, s);
-    sq = span_sum<SPAN>(sq, s) - sum * share * sum;
+    const float2 both = span_sums<SPAN>(make_float2(sum, sq), s2);
+    sum = both.x, sq = both.y - sum * share * sum;
     if (t == 0 && wanted == id)
         reinterpret_cast<float2 *>(a.stats)[id] = make_float2(mean + sum * share, 1.0f / sqrtf((sq < 0.0f ? 0.0f : sq) * share + a.eps));
 }
@@ -770,9 +784,8 @@ __device__ __forceinline__ Sums scratch(const GroupArgs &a, int sc, unsigned cha
     return {p, p + SUMS * THREADS * V, p + SUMS * (THREADS * V + max(THREADS, sc)), 0};
 }
 
-// (four CTAs an SM of fewer elements, three of eight: small images are as fast as many fit)
 template <typename T, int V>
-__global__ void __launch_bounds__(THREADS, V == 8 ? 3 : 4) gn_resident(const __grid_constant__ GroupArgs a) {
+__global__ void __launch_bounds__(THREADS) gn_resident(const __grid_constant__ GroupArgs a) {
     constexpr int PAIRS = Group<T, V>::PAIRS;
     using Word = typename Group<T, V>::Word;
     extern __shared__ uint4 dyn[];
@@ -818,9 +831,9 @@ __global__ void __launch_bounds__(THREADS, V == 8 ? 3 : 4) gn_resident(const __g
     // mean. (16-bit values of a mean so far away that this counts hold fewer digits themselves, and it takes
     // 32768 images of 4 x 32 from 410 to 590 us.)
     float *means = s.group + groups, *m2 = s.group;
-    const float count = (float)(at.p1 - at.p0) * a.D, part = count > 0.0f ? 1.0f / count : 0.0f;
+    const float count = (float)(at.p1 - at.p0) * a.D;
     float own = 0.0f;  // of group threadIdx.x (a slab has 64 at most)
-    if (threadIdx.x < groups) means[threadIdx.x] = own = s.group[threadIdx.x] * part;
+    if (threadIdx.x < groups) means[threadIdx.x] = own = count > 0.0f ? s.group[threadIdx.x] / count : 0.0f;
     __syncthreads();
     of_groups(means, mean);
     at.each([&](int j, int64_t) {
@@ -835,8 +848,8 @@ __global__ void __launch_bounds__(THREADS, V == 8 ? 3 : 4) gn_resident(const __g
     });
     sum_groups<T, V, SUMS>(a, at, s, sum, [](int) { return 1.0f; });
     if (SUMS == 2 && threadIdx.x < groups) {
-        const float left = means[threadIdx.x], q = m2[threadIdx.x] - left * part * left;
-        means[threadIdx.x] = own + left * part;
+        const float left = means[threadIdx.x], off = count > 0.0f ? left / count : 0.0f, q = m2[threadIdx.x] - off * left;
+        means[threadIdx.x] = own + off;
         m2[threadIdx.x] = q < 0.0f ? 0.0f : q;
     }
     // the cluster's; results go where no other CTA reads
@@ -845,14 +858,14 @@ __global__ void __launch_bounds__(THREADS, V == 8 ? 3 : 4) gn_resident(const __g
     for (int g = threadIdx.x; g < groups; g += THREADS) {
         float m = means[g], q = m2[g];
         if (a.chunks > 1) {
-            // (all on their way before the first is used)
-            // (the first CTA has positions wherever there are any)
+            // (all on their way before the first is used; the first CTA has positions wherever there are any)
+            const int len = (int)a.len, left = (int)a.P;  // (below 2^24: the maps are)
             float mr[MOST_SHARES], qr[MOST_SHARES], nr[MOST_SHARES], total = 0.0f;
 #pragma unroll
             for (int r = 0; r < MOST_SHARES; ++r) {
                 mr[r] = r < a.chunks ? peer_read(means + g, r) : 0.0f;
                 qr[r] = r < a.chunks ? peer_read(m2 + g, r) : 0.0f;
-                nr[r] = (float)(min(a.P, (r + 1) * a.len) - min(a.P, r * a.len));
+                nr[r] = (float)max(0, min(len, left - r * len));
             }
 #pragma unroll
             for (int r = 0; r < MOST_SHARES; ++r) total = fmaf(mr[r] - mr[0], nr[r], total);
