@@ -10,7 +10,7 @@
 // join by n1 n2 / (n1 + n2) (m1 - m2)^2 (Chan, Golub, LeVeque), without the cancellation
 // of a sum of squares.
 //
-// Maps of up to 16 MB stay on the chip (one launch: 1 x 7 x 7 x 512 in 4 us, 13 x 31 x 37 x 90 of fp32 in 12 us forward
+// Maps of up to 16 MB stay on the chip (one launch: 1 x 7 x 7 x 512 in 5 us, 13 x 31 x 37 x 90 of fp32 in 13 us forward
 // and 16 us backward); larger ones are read twice. 64 x 56 x 56 x 128 of 16 bits: 12 us for the moments (51 MB, 4.2 TB/s),
 // 3 for the statistics, 13 for the outputs; backward 23 for the sums (103 MB), 3 for the means, 24 for dx. Between a
 // launch's first loads and its last sum over a block's rows 3 to 5 us go by that no other block fills; besides, half of
@@ -974,8 +974,8 @@ __global__ void __launch_bounds__(THREADS) gn_back_resident(const __grid_constan
 }
 
 // ---- one position an image: a group is D neighbouring elements of a row, in the registers of a.lanes lanes; the next
-// row's are on their way. 200704 rows of 512 channels in 8 groups, bf16 and silu: 112 us forward, 187 us backward (3.7
-// and 3.3 TB/s), bound by instructions and the lanes' exchanges.
+// row's are on their way. 200704 rows of 512 channels in 8 groups, bf16 and silu: 108 us forward, 181 us backward (3.8
+// and 3.4 TB/s), bound by instructions and the lanes' exchanges (79 and 68% of the issue slots).
 
 // A thread's group and vectors: the m-th one begins at element d(m) of the group where it is there.
 template <typename T, int V, int M>
