@@ -461,8 +461,9 @@ im2win_status im2win_clip_grad_norm(const void *const *grads, void *const *outs,
  *   xh = (x - mean) / sqrt(var + eps),  z = xh w + b,  y = act(z).
  * w[C] and b[C] may be NULL (1 and 0). G = C is the instance norm, G = 1 one group of
  * all channels. Statistics and sums are fp32, made of means and squared deviations; an
- * output is rounded once. N * P * C is at most 2^40, C at most 2^20, N * C at most
- * 2^31, C a multiple of G (else IM2WIN_ERR_INVALID_ARG).
+ * output is rounded once. C is a multiple of G (else IM2WIN_ERR_INVALID_ARG); N * P * C is
+ * at most 2^40, C at most 2^20, N * C at most 2^31, N and P below 2^31 (else
+ * IM2WIN_ERR_UNSUPPORTED).
  * stats[N][G][2] (fp32; NULL: not kept) receives each group's mean and 1/sqrt(var +
  * eps) for the backward call. Pointers are 16-byte aligned; the stats that a backward call
  * reads need 8 bytes (those of some images of a batch). y may be x itself and must not overlap it otherwise.
@@ -505,8 +506,9 @@ typedef enum {
  * ones (also 0 and -0) by the lower index; weights[T][k] (dtype): their softmax weights,
  * in fp32 until the rounding. A logit of -infinity marks an expert that the row may not
  * take; where fewer than k are left, the other places have expert -1 and weight 0. A NaN
- * ranks above all numbers and makes the row's weights NaN. E is at most 1024, k at most 32
- * and at most E.
+ * ranks above all numbers and makes the row's weights NaN. k is at most E (else
+ * IM2WIN_ERR_INVALID_ARG); E is at most 1024, k at most 32, T below 2^31 (else
+ * IM2WIN_ERR_UNSUPPORTED).
  */
 im2win_status im2win_expert_route(const void *logits, void *weights, int32_t *experts, int64_t T, int64_t E, int64_t k,
                                   int over, int dtype, void *stream);
