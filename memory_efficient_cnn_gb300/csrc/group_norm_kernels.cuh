@@ -1049,8 +1049,8 @@ __global__ void __launch_bounds__(THREADS) gn_rows(const __grid_constant__ Group
             for (int m = 0; m < M; ++m) word[m] = next[m];
             if (AHEAD) fetch_row(a, at, a.x, n + at.step, next);
             // fp32: the sum of distances to the group's first value, so that a far mean costs its own rounding alone
-            // (and the first one of at most 1024 is 32 deviations from it at most). 16-bit values of a mean so far
-            // hold fewer digits than it costs, and 3% of the time.
+            // (and the first one of at most 1024 is 32 deviations from it at most). 16-bit values with a mean so far away hold
+            // fewer digits than it costs; for them it took 116 us instead of 111 us.
             F2 v[M][PAIRS];
             float s = 0.0f, pivot = 0.0f;
 #pragma unroll
